@@ -119,7 +119,7 @@ def _lens(c, seed):
 
 def _counts(c):
     """Rows a ragged case brings for each request, 0 .. 2 * per and `per` on average."""
-    return np.round((np.arange(c["B"]) * 0.7548776662 % 1.0) * 2 * c["per"]).astype(np.int32)
+    return np.round((np.arange(1, c["B"] + 1) * 0.7548776662 % 1.0) * 2 * c["per"]).astype(np.int32)
 
 
 def _parents(rng, B, n):
