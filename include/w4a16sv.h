@@ -319,6 +319,152 @@ w4a16_status w4a16_linear_noalloc(const void* x, int M, int64_t K, const void* q
                                   const void* scales_packed, int64_t N, void* out, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache (the tutorial page, section 8.7: a serving
+ * stack's KV cache over accepted and rejected tokens; the format is this
+ * library's choice). A request's committed tokens fill blocks of 64. A full
+ * block sits in a page in 8 bits: value = code * scale, one fp32 power-of-two
+ * scale for the block's keys of a head and one for its values. The block
+ * being filled stays in bf16 in a tail page, so every token is rounded once,
+ * from bf16, when its block is complete, and the cache does not depend on
+ * how the tokens were split into steps. A draft's own keys and values never
+ * enter the cache: attention reads them where the projection left them, and
+ * kv8_append takes the kept ones.
+ *
+ *   k, v            device 8-bit codes [layers][pages][Hkv][64][D], D = 128
+ *   k_scale, v_scale  device fp32 [layers][pages][Hkv]
+ *   k_tail, v_tail  device bf16 [layers][tail_pages][Hkv][64][D]
+ *   fmt             0: e4m3 (largest code 448), 1: e5m2 (largest used 57344)
+ *   lens[b]         committed tokens of request b
+ *   block_table     device int32 [B][max_blocks]: the pages of the full
+ *                   blocks 0 .. lens[b] / 64 - 1 (other entries unread)
+ *   tails[b]        the tail page of request b: rows 0 .. lens[b] % 64 - 1 hold
+ *                   its newest tokens. Tail pages go in pairs 2i, 2i + 1: a
+ *                   step that completes a block moves to the pair's other
+ *                   page, so no step overwrites what it reads (one that was
+ *                   given up can be run again).
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * Block tables, slot maps and the free list of one step, built on the GPU
+ * from the requests' lengths (the step stays capturable in a CUDA graph: the
+ * host reads nothing back).
+ *
+ * Which rows a request keeps:
+ *   draft mode  (accepted_node != NULL): row b * n + j is node j of request b;
+ *               the nodes on the root path of accepted_node[b] are kept, root
+ *               first (tree_parents NULL: the chain); rows = B * n, n 1 .. 64
+ *   ragged mode (row_start != NULL): rows row_start[b] .. row_start[b+1] - 1
+ *               are all kept (row_start[B + 1], 0 first, <= rows at the end)
+ * Each kept row i of request b goes to position lens[b] + i. The blocks
+ * lens[b] / 64 .. (lens[b] + kept) / 64 - 1 become full and get pages from
+ * the free list, request by request. A request whose pages are not there
+ * (counted with those asked for before it) keeps nothing in this step:
+ * new_lens[b] = lens[b]. release[b] != 0 (release may be NULL): the request
+ * has ended; it keeps nothing, new_lens[b] = 0 and its pages go to the end of
+ * the free list (for later steps).
+ *
+ *   free_ring   device int32 [ring_cap], a ring of free page ids; queue[0] =
+ *               its head, queue[1] = free pages, queue[2] is not read.
+ *               Pages are taken at the head and returned behind the last.
+ *   block_table, free_ring  updated in place: only entries of blocks that
+ *               become full, and ring places behind the last free page
+ *   new_lens, new_tails  [B]; new_start [B + 1]: kept rows before request b
+ *   new_queue   [3]: head, free pages, pages asked for and not there
+ *   src_rows    [rows]: the source row of each kept row, in order; -1 behind
+ *   slots       [rows]: where it goes: page * 64 + offset in a block that this
+ *               step completes, -1 - r for row r of the tail page; INT32_MIN
+ *               behind the last
+ * No output may overlap an input. The same call again, on the same inputs,
+ * gives the same results. B <= 4096, ring_cap <= 2^25, B * max_blocks < 2^31.
+ * Bad input (a length outside the table, falling row_start, a bad node or
+ * parent, a page id outside [0, 2^25), a full ring, a queue outside the ring)
+ * sets W4A16_ERR_DEVICE_INPUT in the device error word; the request then
+ * keeps nothing (a bad node or parent: its root alone; a falling row_start:
+ * any of the rows; a bad page: the
+ * block's slots are INT32_MIN), and nothing is written out of bounds.
+ * ---------------------------------------------------------------------- */
+w4a16_status kv_block_plan(const int32_t* lens, const int32_t* tails, const int32_t* row_start,
+                           const int32_t* tree_parents, const int32_t* accepted_node, const int32_t* release, int B,
+                           int n, int rows, int max_blocks, int ring_cap, int32_t* block_table, int32_t* free_ring,
+                           const int32_t* queue, int32_t* new_lens, int32_t* new_tails, int32_t* new_start,
+                           int32_t* new_queue, int32_t* src_rows, int32_t* slots, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The kept rows of a step into the cache, every layer in one call. A block
+ * that the step completes is written to its page: scale = the smallest power
+ * of two, 2^-100 at least, that brings the block's largest finite magnitude
+ * to the largest code or below (1 for an all-zero block), code = value /
+ * scale rounded to nearest even (infinities and larger values to the largest
+ * code, NaN to NaN). The rows of the block still being filled go to the tail
+ * page in bf16.
+ *   k_new, v_new  device bf16 [layers][rows][Hkv][D]: `row_stride` elements
+ *                 from row to row and `layer_stride` from layer to layer
+ *                 (multiples of 8), heads D apart; 16-byte aligned
+ *   tails         the tail pages before the step (kv_block_plan's input);
+ *                 new_tails, new_start, src_rows, slots: kv_block_plan's outputs
+ * Slots or rows that fit no such plan, or ids outside the cache, set
+ * W4A16_ERR_DEVICE_INPUT and are skipped.
+ * ---------------------------------------------------------------------- */
+w4a16_status kv8_append(const void* k_new, const void* v_new, int64_t row_stride, int64_t layer_stride,
+                        const int32_t* tails, const int32_t* new_tails, const int32_t* new_start,
+                        const int32_t* src_rows, const int32_t* slots, int B, int rows, int Hkv, int D, int layers,
+                        int pages, int tail_pages, int fmt, void* k, void* v, float* k_scale, float* v_scale,
+                        void* k_tail, void* v_tail, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Tree-masked verify attention over the 8-bit cache, one layer: the same
+ * function as tree_attention (mask, heads, scale, limits on n), with the
+ * committed prefix in pages and the tail page, and the tree's own keys and
+ * values read from k_new, v_new.
+ *   q             device bf16 [B][n][H][D], out likewise (16-byte aligned);
+ *   k_new, v_new  device bf16 [B][n][Hkv][D]; heads D apart, tokens q_stride,
+ *                 kv_stride elements apart (multiples of 8, so that the three
+ *                 can be slices of one fused projection); out is dense
+ *   lens          device int32 [B], 0 <= lens[b] <= max_len
+ *   max_len       an upper bound of lens[] known to the caller;
+ *                 max_len / 64 <= max_blocks
+ *   workspace     kv8_tree_attention_workspace_bytes() bytes (256-byte
+ *                 aligned; may be NULL when that is 0); no initialisation
+ * Arithmetic: scores and sums in fp32 (the 8-bit keys enter the tensor cores
+ * as they are; q as the sum of two 8-bit terms, exact down to 2^-14 of the
+ * row's largest element), the softmax weights rounded to fp16 for the 8-bit
+ * values and to bf16 for the tail's and the tree's own, out to bf16.
+ * A length outside [0, max_len], a bad parent, or a page or tail id outside
+ * the cache sets W4A16_ERR_DEVICE_INPUT (length clamped; the node attends to
+ * itself and the prefix; a bad page reads as zeros). Launch rules as for
+ * w4a16_linear.
+ * ---------------------------------------------------------------------- */
+size_t kv8_tree_attention_workspace_bytes(int B, int n, int H, int Hkv, int D, int max_len);
+w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                                int64_t kv_stride, const void* k, const void* v, const float* k_scale,
+                                const float* v_scale, const void* k_tail, const void* v_tail,
+                                const int32_t* block_table, const int32_t* lens, const int32_t* tails,
+                                const int32_t* tree_parents, int B, int n, int H, int Hkv, int D, int max_blocks,
+                                int pages, int tail_pages, int max_len, int fmt, float scale, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, entropy and the most probable tokens of
+ * logit rows (what a serving step reports beside the tokens it emits).
+ *   logits     device [R][V], fp32 (bf16 = 0) or bf16 (bf16 = 1), dense
+ *   ids        device int32 [R][m] (may be NULL with m = 0); -1: no token
+ *   logp       fp32 [R][m]: ln softmax(logits[r])[ids[r][i]], 0 for id -1
+ *   entropy    fp32 [R] (nats; may be NULL): -sum p ln p
+ *   top_ids, top_logp  int32 / fp32 [R][top]: the `top` largest logits in
+ *              falling order, ties to the lower index, a NaN above all
+ *              others; top 0 .. 64, <= V (may be NULL with top = 0)
+ *   workspace  token_logprobs_workspace_bytes() bytes (256-byte aligned)
+ * Masked tokens (-inf logits) have probability 0; a row with a NaN or +inf,
+ * or with -inf alone, has NaN log probabilities and entropy. An id outside
+ * [-1, V) sets W4A16_ERR_DEVICE_INPUT and gives NaN. R 1 .. 2^20, V 1 .. 2^20,
+ * m 0 .. 64. Launch rules as for w4a16_linear.
+ * ---------------------------------------------------------------------- */
+size_t token_logprobs_workspace_bytes(int R, int V, int top);
+w4a16_status token_logprobs(const void* logits, int bf16, const int32_t* ids, int R, int V, int m, int top,
+                            float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Device status: synchronises `stream`, reads and clears the device error
  * word of the current device. W4A16_OK, W4A16_ERR_DEVICE_TIMEOUT,
  * W4A16_ERR_DEVICE_INPUT or W4A16_ERR_CUDA.

@@ -52,6 +52,13 @@ SIGNATURES = {
     "tree_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
                               _vp, _vp, _sz, _vp]),
     "kv_compact": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
+    "kv_block_plan": (_i32, [_vp] * 6 + [_i32] * 5 + [_vp] * 10),
+    "kv8_append": (_i32, [_vp, _vp, _i64, _i64] + [_vp] * 5 + [_i32] * 8 + [_vp] * 7),
+    "kv8_tree_attention_workspace_bytes": (_sz, [_i32] * 6),
+    "kv8_tree_attention": (_i32, [_vp, _vp, _vp, _i64, _i64] + [_vp] * 10 + [_i32] * 10 +
+                           [ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "token_logprobs_workspace_bytes": (_sz, [_i32] * 3),
+    "token_logprobs": (_i32, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "w4a16_linear_noalloc_scratch_bytes": (_sz, []),
     "w4a16_linear_noalloc": (_i32, [_vp, _i32, _i64, _vp, _vp, _i64, _vp, _vp]),
 }

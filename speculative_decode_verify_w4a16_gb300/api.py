@@ -320,3 +320,271 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
 def check_device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error status."""
     return int(lib().w4a16_check_device_status(_stream(stream)))
+
+
+# ------------------------------------------------------ paged 8-bit cache
+
+KV_BLOCK = 64  # tokens per block (a page, a scale)
+_KV8_FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+@dataclass
+class KV8Cache:
+    """Keys and values of full 64-token blocks in 8 bits, code * scale with a
+    scale per (block, head), and the blocks being filled in bf16 tail pages
+    (in pairs; see the header). The leading dimension is the layer."""
+    k: torch.Tensor        # float8_e4m3fn or float8_e5m2 [layers, pages, Hkv, 64, D]
+    v: torch.Tensor
+    k_scale: torch.Tensor  # fp32 [layers, pages, Hkv]
+    v_scale: torch.Tensor
+    k_tail: torch.Tensor   # bf16 [layers, tail_pages, Hkv, 64, D]
+    v_tail: torch.Tensor
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size()
+                   for t in (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail))
+
+
+@dataclass
+class BlockPlan:
+    """What kv_block_plan leaves for kv8_append and for the next step."""
+    new_lens: torch.Tensor   # int32 [B]
+    new_tails: torch.Tensor  # int32 [B]
+    new_start: torch.Tensor  # int32 [B + 1]: kept rows before each request
+    queue: torch.Tensor      # int32 [3]: ring head, free pages, pages missing
+    src_rows: torch.Tensor   # int32 [rows]: source row of each kept row, -1 behind
+    slots: torch.Tensor      # int32 [rows]: its place (page * 64 + offset, or -1 - tail row)
+
+
+def kv8_cache(layers: int, pages: int, B: int, Hkv: int, D: int = 128, dtype: torch.dtype = torch.float8_e4m3fn,
+              device=None) -> KV8Cache:
+    """An empty cache of `pages` pages, with a pair of tail pages for each of B requests."""
+    if dtype not in _KV8_FORMATS:
+        raise ValueError("dtype must be torch.float8_e4m3fn or torch.float8_e5m2")
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    codes = [torch.zeros((layers, pages, Hkv, KV_BLOCK, D), dtype=torch.uint8, device=dev).view(dtype)
+             for _ in range(2)]
+    scales = [torch.ones((layers, pages, Hkv), dtype=torch.float32, device=dev) for _ in range(2)]
+    tails = [torch.zeros((layers, 2 * B, Hkv, KV_BLOCK, D), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    return KV8Cache(*codes, *scales, *tails)
+
+
+def _need_cache(c: KV8Cache):
+    layers, pages, Hkv, block, D = c.k.shape
+    if c.k.dtype not in _KV8_FORMATS:
+        raise ValueError("the cache's codes must be torch.float8_e4m3fn or torch.float8_e5m2")
+    if block != KV_BLOCK:
+        raise ValueError(f"a page holds {KV_BLOCK} tokens, the cache has {block}")
+    _need(c.k, "cache.k", c.k.dtype)
+    _need(c.v, "cache.v", c.k.dtype, c.k.shape)
+    _need(c.k_scale, "cache.k_scale", torch.float32, (layers, pages, Hkv))
+    _need(c.v_scale, "cache.v_scale", torch.float32, (layers, pages, Hkv))
+    tail_pages = c.k_tail.shape[1]
+    _need(c.k_tail, "cache.k_tail", torch.bfloat16, (layers, tail_pages, Hkv, KV_BLOCK, D))
+    _need(c.v_tail, "cache.v_tail", torch.bfloat16, (layers, tail_pages, Hkv, KV_BLOCK, D))
+    return layers, pages, tail_pages, Hkv, D
+
+
+def _need_rows(t: torch.Tensor, name: str, shape) -> int:
+    """A bf16 tensor [..., heads, D] whose heads are dense and whose tokens are
+    evenly apart (a slice of a fused projection); returns that stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    tokens, (H, D) = t.shape[-3], t.shape[-2:]
+    stride = t.stride(-3) if tokens > 1 else (t.stride(-4) if t.dim() > 3 and t.shape[-4] > 1 else H * D)
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if stride < H * D or stride % 8 != 0:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and not overlap")
+    return stride
+
+
+def kv_block_plan(lens: torch.Tensor, tails: torch.Tensor, block_table: torch.Tensor, free_ring: torch.Tensor,
+                  queue: torch.Tensor, *, row_start: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+                  accepted_node: Optional[torch.Tensor] = None, n: Optional[int] = None,
+                  tree_parents: Optional[torch.Tensor] = None, release: Optional[torch.Tensor] = None,
+                  plan: Optional[BlockPlan] = None, stream=None) -> BlockPlan:
+    """Block tables, slot maps and free list of one step, on the GPU. Either
+    ragged rows (row_start int32 [B + 1], rows = row_start[B] or more) or a
+    draft's accepted path (accepted_node int32 [B], n nodes a request,
+    tree_parents int32 [B, n] or None for the chain). block_table int32
+    [B, max_blocks] and free_ring int32 [cap] are updated in place; lens,
+    tails and queue are not (the plan holds their next values)."""
+    _need(lens, "lens", torch.int32)
+    B = lens.numel()
+    _need(lens, "lens", torch.int32, (B,))
+    _need(tails, "tails", torch.int32, (B,))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
+    _need(free_ring, "free_ring", torch.int32, (free_ring.numel(),))
+    _need(queue, "queue", torch.int32, (3,))
+    if (row_start is None) == (accepted_node is None):
+        raise ValueError("give row_start (ragged rows) or accepted_node (a draft's accepted path)")
+    if row_start is not None:
+        _need(row_start, "row_start", torch.int32, (B + 1,))
+        if rows is None:
+            raise ValueError("rows (an upper bound of row_start[B]) is required with row_start")
+        if tree_parents is not None:
+            raise ValueError("tree_parents goes with accepted_node")
+        rows, n = int(rows), 0
+    else:
+        _need(accepted_node, "accepted_node", torch.int32, (B,))
+        if tree_parents is not None:
+            n = tree_parents.shape[-1] if n is None else n
+            _need(tree_parents, "tree_parents", torch.int32, (B, n))
+        if n is None:
+            raise ValueError("n is required for a sequence draft")
+        rows = B * int(n)
+    if release is not None:
+        _need(release, "release", torch.int32, (B,))
+    if plan is None:
+        sizes = (B, B, B + 1, 3, max(rows, 1), max(rows, 1))
+        plan = BlockPlan(*(torch.empty(s, dtype=torch.int32, device=lens.device) for s in sizes))
+    _need(plan.new_lens, "plan.new_lens", torch.int32, (B,))
+    _need(plan.new_tails, "plan.new_tails", torch.int32, (B,))
+    _need(plan.new_start, "plan.new_start", torch.int32, (B + 1,))
+    _need(plan.queue, "plan.queue", torch.int32, (3,))
+    for t, name in ((plan.src_rows, "plan.src_rows"), (plan.slots, "plan.slots")):
+        _need(t, name, torch.int32)
+        if t.numel() < rows:
+            raise ValueError(f"{name} must hold {rows} rows, has {t.numel()}")
+    check(lib().kv_block_plan(_ptr(lens), _ptr(tails), _ptr(row_start), _ptr(tree_parents), _ptr(accepted_node),
+                              _ptr(release), B, int(n), rows, block_table.shape[1], free_ring.numel(),
+                              _ptr(block_table), _ptr(free_ring), _ptr(queue), _ptr(plan.new_lens),
+                              _ptr(plan.new_tails), _ptr(plan.new_start), _ptr(plan.queue), _ptr(plan.src_rows),
+                              _ptr(plan.slots), _stream(stream)), "kv_block_plan")
+    return plan
+
+
+def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails: torch.Tensor, plan: BlockPlan,
+               stream=None) -> None:
+    """The step's kept rows into the cache, every layer at once. k_new, v_new
+    bf16 [layers, rows, Hkv, D] (rows evenly apart, heads dense; [rows, Hkv, D]
+    for one layer); tails: the tail pages before the step."""
+    layers, pages, tail_pages, Hkv, D = _need_cache(cache)
+    if k_new.dim() == 3:
+        k_new, v_new = k_new.unsqueeze(0), v_new.unsqueeze(0)
+    rows = k_new.shape[1]
+    stride = _need_rows(k_new, "k_new", (layers, rows, Hkv, D))
+    if _need_rows(v_new, "v_new", (layers, rows, Hkv, D)) != stride:
+        raise ValueError("k_new and v_new must have the same strides")
+    layer_stride = k_new.stride(0) if layers > 1 else 0
+    if layers > 1 and v_new.stride(0) != layer_stride:
+        raise ValueError("k_new and v_new must have the same strides")
+    B = tails.numel()
+    _need(tails, "tails", torch.int32, (B,))
+    _need(plan.new_tails, "plan.new_tails", torch.int32, (B,))
+    _need(plan.new_start, "plan.new_start", torch.int32, (B + 1,))
+    for t, name in ((plan.src_rows, "plan.src_rows"), (plan.slots, "plan.slots")):
+        _need(t, name, torch.int32)
+        if t.numel() < rows:
+            raise ValueError(f"{name} must hold {rows} rows, has {t.numel()}")
+    check(lib().kv8_append(_ptr(k_new), _ptr(v_new), stride, layer_stride, _ptr(tails), _ptr(plan.new_tails),
+                           _ptr(plan.new_start), _ptr(plan.src_rows), _ptr(plan.slots), B, rows, Hkv, D, layers,
+                           pages, tail_pages, _KV8_FORMATS[cache.k.dtype], _ptr(cache.k), _ptr(cache.v),
+                           _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(cache.k_tail), _ptr(cache.v_tail),
+                           _stream(stream)), "kv8_append")
+
+
+def kv8_tree_attention_workspace_bytes(B: int, n: int, H: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(lib().kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, max_len))
+
+
+def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: KV8Cache, layer: int,
+                       block_table: torch.Tensor, lens: torch.Tensor, tails: torch.Tensor,
+                       tree_parents: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                       scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tree-masked verify attention over the 8-bit cache of one layer. q bf16
+    [B, n, H, D] and the tree's own k_new, v_new bf16 [B, n, Hkv, D] may be
+    slices of one fused projection (heads dense, tokens evenly apart); lens,
+    tails int32 [B]; block_table int32 [B, max_blocks]; max_len: an upper bound
+    of lens (default: what the table holds). Returns bf16 [B, n, H, D]."""
+    layers, pages, tail_pages, Hkv, D = _need_cache(cache)
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} is not one of the cache's {layers}")
+    if q.dim() != 4:
+        raise ValueError(f"q must have 4 dimensions, got {tuple(q.shape)}")
+    B, n, H = q.shape[:3]
+    strides = []
+    for t, name, heads in ((q, "q", H), (k_new, "k_new", Hkv), (v_new, "v_new", Hkv)):
+        s = _need_rows(t, name, (B, n, heads, D))
+        if B > 1 and n > 1 and t.stride(0) != n * s:
+            raise ValueError(f"{name}: the tokens of all requests must be evenly apart")
+        strides.append(s)
+    if B * n > 1 and strides[1] != strides[2]:
+        raise ValueError("k_new and v_new must have the same strides")
+    _need(lens, "lens", torch.int32, (B,))
+    _need(tails, "tails", torch.int32, (B,))
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
+    if tree_parents is not None:
+        _need(tree_parents, "tree_parents", torch.int32, (B, n))
+    max_blocks = block_table.shape[1]
+    max_len = max_blocks * KV_BLOCK + KV_BLOCK - 1 if max_len is None else int(max_len)
+    scale = D ** -0.5 if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((B, n, H, D), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (B, n, H, D))
+    nbytes = kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, max_len)
+    if ws is None and nbytes > 0:
+        ws = workspace(nbytes, q.device, "attention")
+    codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
+    tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
+    check(lib().kv8_tree_attention(
+        _ptr(q), _ptr(k_new), _ptr(v_new), strides[0], strides[1], _ptr(cache.k) + codes, _ptr(cache.v) + codes,
+        _ptr(cache.k_scale) + heads, _ptr(cache.v_scale) + heads, _ptr(cache.k_tail) + tail, _ptr(cache.v_tail) + tail,
+        _ptr(block_table), _ptr(lens), _ptr(tails), _ptr(tree_parents), B, n, H, Hkv, D, max_blocks, pages, tail_pages,
+        max_len, _KV8_FORMATS[cache.k.dtype], scale, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
+        _stream(stream)), "kv8_tree_attention")
+    return out
+
+
+# ------------------------------------------------------ log probabilities
+
+@dataclass
+class TokenLogprobs:
+    logp: torch.Tensor      # fp32 [R, m] (or [R]): of the given tokens
+    entropy: torch.Tensor   # fp32 [R]
+    top_ids: torch.Tensor   # int32 [R, top]
+    top_logp: torch.Tensor  # fp32 [R, top]
+
+
+def token_logprobs_workspace_bytes(R: int, V: int, top: int) -> int:
+    return int(lib().token_logprobs_workspace_bytes(R, V, top))
+
+
+def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top: int = 0, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> TokenLogprobs:
+    """Log probabilities of given tokens under logit rows (fp32 or bf16 [R, V];
+    ids int32 [R, m] or [R], -1 for none), each row's entropy, and its `top`
+    most probable tokens (ties to the lower index)."""
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be {torch.float32} or {torch.bfloat16}, got {logits.dtype}")
+    _need(logits, "logits", logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must have shape (R, V), got {tuple(logits.shape)}")
+    R, V = logits.shape
+    _need(ids, "ids", torch.int32)
+    if ids.dim() not in (1, 2) or ids.shape[0] != R:
+        raise ValueError(f"ids must have shape ({R}, m) or ({R},), got {tuple(ids.shape)}")
+    m, dev = (ids.shape[1] if ids.dim() == 2 else 1), logits.device
+    out = TokenLogprobs(torch.empty(ids.shape, dtype=torch.float32, device=dev),
+                        torch.empty(R, dtype=torch.float32, device=dev),
+                        torch.empty((R, top), dtype=torch.int32, device=dev),
+                        torch.empty((R, top), dtype=torch.float32, device=dev))
+    if ws is None:
+        ws = workspace(token_logprobs_workspace_bytes(R, V, top), dev, "logprobs")
+    check(lib().token_logprobs(_ptr(logits), int(logits.dtype == torch.bfloat16), _ptr(ids), R, V, m, top,
+                               _ptr(out.logp), _ptr(out.entropy), _ptr(out.top_ids), _ptr(out.top_logp), _ptr(ws),
+                               ws.numel(), _stream(stream)), "token_logprobs")
+    return out

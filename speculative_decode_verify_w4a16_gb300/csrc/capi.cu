@@ -332,6 +332,165 @@ w4a16_status spec_accept_prestat(const float* p_logits, const float* p_stats, co
              : W4A16_ERR_CUDA;
 }
 
+// ------------------------------------------------- paged 8-bit cache
+w4a16_status kv_block_plan(const int32_t* lens, const int32_t* tails, const int32_t* row_start,
+                           const int32_t* tree_parents, const int32_t* accepted_node, const int32_t* release, int B,
+                           int n, int rows, int max_blocks, int ring_cap, int32_t* block_table, int32_t* free_ring,
+                           const int32_t* queue, int32_t* new_lens, int32_t* new_tails, int32_t* new_start,
+                           int32_t* new_queue, int32_t* src_rows, int32_t* slots, void* stream) {
+  if (!lens || !tails || !block_table || !free_ring || !queue || !new_lens || !new_tails || !new_start || !new_queue)
+    return W4A16_ERR_INVALID_ARG;
+  if ((row_start != nullptr) == (accepted_node != nullptr) || (tree_parents && !accepted_node))
+    return W4A16_ERR_INVALID_ARG;  // one of the two modes
+  if (B < 1 || rows < 0 || max_blocks < 1 || ring_cap < 1 || (rows > 0 && (!src_rows || !slots)))
+    return W4A16_ERR_INVALID_ARG;
+  if (accepted_node && (n < 1 || (int64_t)B * n != rows)) return W4A16_ERR_INVALID_ARG;
+  if (B > kPlanMaxB || (accepted_node && n > 64) || ring_cap > (1 << 25) || (int64_t)B * max_blocks > INT32_MAX ||
+      max_blocks > (INT32_MAX - 63) / 64)
+    return W4A16_ERR_UNSUPPORTED;
+  const void* all[] = {lens,  tails,    row_start, tree_parents, accepted_node, release,  block_table, free_ring,
+                       queue, new_lens, new_tails, new_start,    new_queue,     src_rows, slots};
+  for (const void* a : all)
+    if (!aligned(a, 4)) return W4A16_ERR_INVALID_ARG;
+  if (new_lens == lens || new_tails == tails || new_queue == queue) return W4A16_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  return launch_block_plan(lens, tails, row_start, tree_parents, accepted_node, release, B, n, rows, max_blocks,
+                           ring_cap, block_table, free_ring, queue, new_lens, new_tails, new_start, new_queue,
+                           src_rows, slots, dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? W4A16_OK
+             : W4A16_ERR_CUDA;
+}
+
+// pages and heads of a cache: every index in 64-token rows fits int32
+static bool kv8_cache_ok(int Hkv, int pages, int tail_pages) {
+  return Hkv >= 1 && Hkv <= 65535 && pages >= 1 && pages <= (1 << 25) && tail_pages >= 1 &&
+         (int64_t)pages * Hkv <= INT32_MAX && (int64_t)tail_pages * Hkv <= INT32_MAX;
+}
+
+w4a16_status kv8_append(const void* k_new, const void* v_new, int64_t row_stride, int64_t layer_stride,
+                        const int32_t* tails, const int32_t* new_tails, const int32_t* new_start,
+                        const int32_t* src_rows, const int32_t* slots, int B, int rows, int Hkv, int D, int layers,
+                        int pages, int tail_pages, int fmt, void* k, void* v, float* k_scale, float* v_scale,
+                        void* k_tail, void* v_tail, void* stream) {
+  if (!k_new || !v_new || !tails || !new_tails || !new_start || !src_rows || !slots || !k || !v || !k_scale ||
+      !v_scale || !k_tail || !v_tail)
+    return W4A16_ERR_INVALID_ARG;
+  if (B < 1 || rows < 1 || layers < 1 || !kv8_cache_ok(Hkv, pages, tail_pages) || fmt < 0 || fmt > 1 ||
+      row_stride < (int64_t)Hkv * D || row_stride % 8 != 0 || layer_stride < 0 || layer_stride % 8 != 0)
+    return W4A16_ERR_INVALID_ARG;
+  if (D != 128 || B > kPlanMaxB || rows > (1 << 28) || (int64_t)layers * Hkv > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+  const void* wide[] = {k_new, v_new, k, v, k_tail, v_tail};
+  for (const void* a : wide)
+    if (!aligned(a, 16)) return W4A16_ERR_INVALID_ARG;
+  const void* words[] = {tails, new_tails, new_start, src_rows, slots, k_scale, v_scale};
+  for (const void* a : words)
+    if (!aligned(a, 4)) return W4A16_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  return launch_kv8_append(k_new, v_new, row_stride, layer_stride, tails, new_tails, new_start, src_rows, slots, B,
+                           rows, Hkv, layers, pages, tail_pages, fmt, k, v, k_scale, v_scale, k_tail, v_tail,
+                           dev.num_sms, dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? W4A16_OK
+             : W4A16_ERR_CUDA;
+}
+
+static bool kv8_attn_shape_ok(int B, int n, int H, int Hkv, int max_len) {
+  return B >= 1 && B <= 65535 && n >= 1 && H >= 1 && Hkv >= 1 && Hkv <= 65535 && H % Hkv == 0 && max_len >= 0 &&
+         (int64_t)B * n * H <= INT32_MAX && (int64_t)B * Hkv <= INT32_MAX;
+}
+
+size_t kv8_tree_attention_workspace_bytes(int B, int n, int H, int Hkv, int D, int max_len) {
+  if (!kv8_attn_shape_ok(B, n, H, Hkv, max_len) || D != 128 || n > 64) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return 0;
+  return kv8_attention_ws(B, n, H, Hkv, max_len, dev.num_sms);
+}
+
+w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                                int64_t kv_stride, const void* k, const void* v, const float* k_scale,
+                                const float* v_scale, const void* k_tail, const void* v_tail,
+                                const int32_t* block_table, const int32_t* lens, const int32_t* tails,
+                                const int32_t* tree_parents, int B, int n, int H, int Hkv, int D, int max_blocks,
+                                int pages, int tail_pages, int max_len, int fmt, float scale, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_new || !v_new || !k || !v || !k_scale || !v_scale || !k_tail || !v_tail || !block_table || !lens ||
+      !tails || !out)
+    return W4A16_ERR_INVALID_ARG;
+  if (!kv8_attn_shape_ok(B, n, H, Hkv, max_len) || !kv8_cache_ok(Hkv, pages, tail_pages) || fmt < 0 || fmt > 1 ||
+      max_blocks < 1 || max_len / 64 > max_blocks || (int64_t)B * max_blocks > INT32_MAX || q_stride < (int64_t)H * D ||
+      q_stride % 8 != 0 || kv_stride < (int64_t)Hkv * D || kv_stride % 8 != 0 || !(scale > 0.0f) || !(scale < INFINITY))
+    return W4A16_ERR_INVALID_ARG;
+  if (D != 128 || n > 64 || kv_stride > (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
+  const void* wide[] = {q, k_new, v_new, k, v, k_tail, v_tail, out};
+  for (const void* a : wide)
+    if (!aligned(a, 16)) return W4A16_ERR_INVALID_ARG;
+  const void* words[] = {k_scale, v_scale, block_table, lens, tails, tree_parents};
+  for (const void* a : words)
+    if (!aligned(a, 4)) return W4A16_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  const size_t need = kv8_attention_ws(B, n, H, Hkv, max_len, dev.num_sms);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  Kv8AttnParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.q_stride = q_stride;
+  p.kv_stride = kv_stride;
+  p.k = static_cast<const uint8_t*>(k);
+  p.v = static_cast<const uint8_t*>(v);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_tail = static_cast<const __nv_bfloat16*>(k_tail);
+  p.v_tail = static_cast<const __nv_bfloat16*>(v_tail);
+  p.table = block_table;
+  p.lens = lens;
+  p.tails = tails;
+  p.parents = tree_parents;
+  p.B = B;
+  p.n = n;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.max_blocks = max_blocks;
+  p.pages = pages;
+  p.tail_pages = tail_pages;
+  p.max_len = max_len;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = dev.err;
+  return launch_kv8_attention(p, fmt, workspace, dev.num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? W4A16_OK
+             : W4A16_ERR_CUDA;
+}
+
+// ------------------------------------------------- log probabilities
+static bool logprobs_shape_ok(int R, int V, int m, int top) {
+  return R >= 1 && R <= (1 << 20) && V >= 1 && V <= (1 << 20) && m >= 0 && m <= 64 && top >= 0 && top <= 64 &&
+         top <= V && (int64_t)R * ((V + 7 + 1023) / 1024) <= (int64_t)8 * INT32_MAX;
+}
+
+size_t token_logprobs_workspace_bytes(int R, int V, int top) {
+  return logprobs_shape_ok(R, V, 0, top) ? token_logprobs_ws(R, V) : 0;
+}
+
+w4a16_status token_logprobs(const void* logits, int bf16, const int32_t* ids, int R, int V, int m, int top,
+                            float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!logits || !logprobs_shape_ok(R, V, m, top) || bf16 < 0 || bf16 > 1) return W4A16_ERR_INVALID_ARG;
+  if ((m > 0 && (!ids || !logp)) || (top > 0 && (!top_ids || !top_logp))) return W4A16_ERR_INVALID_ARG;
+  if (!aligned(logits, bf16 ? 2 : 4) || !aligned(ids, 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(top_ids, 4) || !aligned(top_logp, 4))
+    return W4A16_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < token_logprobs_ws(R, V)) return W4A16_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  return launch_token_logprobs(logits, bf16 != 0, ids, R, V, m, top, logp, entropy, top_ids, top_logp, workspace,
+                               dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? W4A16_OK
+             : W4A16_ERR_CUDA;
+}
+
 w4a16_status w4a16_check_device_status(void* stream) {
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;

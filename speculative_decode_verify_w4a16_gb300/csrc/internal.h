@@ -1,6 +1,7 @@
 // Internal host-side interface between the C-ABI layer and the kernel files.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -128,6 +129,42 @@ cudaError_t launch_tree_attention(const void* q, const void* k_cache, const void
 cudaError_t launch_kv_compact(void* k_cache, void* v_cache, const int32_t* lens, const int32_t* parents,
                               const int32_t* node, int B, int n, int Hkv, int D, int Lcap, int layers,
                               int32_t* new_lens, unsigned* err, cudaStream_t stream);
+
+// ---- paged 8-bit cache: block plan, append, attention
+size_t block_plan_smem(int B, bool draft);
+constexpr int kPlanMaxB = 4096;
+cudaError_t launch_block_plan(const int32_t* lens, const int32_t* tails, const int32_t* row_start,
+                              const int32_t* parents, const int32_t* node, const int32_t* release, int B, int n,
+                              int rows, int max_blocks, int ring_cap, int32_t* table, int32_t* ring,
+                              const int32_t* queue, int32_t* new_lens, int32_t* new_tails, int32_t* new_start,
+                              int32_t* new_queue, int32_t* src_rows, int32_t* slots, unsigned* err,
+                              cudaStream_t stream);
+cudaError_t launch_kv8_append(const void* k_new, const void* v_new, int64_t row_stride, int64_t layer_stride,
+                              const int32_t* tails, const int32_t* new_tails, const int32_t* new_start,
+                              const int32_t* src_rows, const int32_t* slots, int B, int rows, int Hkv, int layers,
+                              int pages, int tail_pages, int fmt, void* k, void* v, float* k_scale, float* v_scale,
+                              void* k_tail, void* v_tail, int num_sms, unsigned* err, cudaStream_t stream);
+struct Kv8AttnParams {
+  const __nv_bfloat16* q;  // [B][n][H][D], tokens q_stride apart
+  const __nv_bfloat16 *k_new, *v_new;  // [B][n][Hkv][D], tokens kv_stride apart
+  int64_t q_stride, kv_stride;
+  const uint8_t *k, *v;  // [pages][Hkv][64][D]
+  const float *k_scale, *v_scale;
+  const __nv_bfloat16 *k_tail, *v_tail;  // [tail_pages][Hkv][64][D]
+  const int32_t *table, *lens, *tails, *parents;
+  int B, n, H, Hkv, max_blocks, pages, tail_pages, max_len;
+  float scale_log2;  // softmax scale * log2(e)
+  __nv_bfloat16* out;  // [B][n][H][D]
+  unsigned* err;
+};
+size_t kv8_attention_ws(int B, int n, int H, int Hkv, int max_len, int num_sms);
+cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspace, int num_sms, cudaStream_t stream);
+
+// ---- log probabilities of logit rows
+size_t token_logprobs_ws(int R, int V);
+cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* ids, int R, int V, int m, int top,
+                                  float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
+                                  unsigned* err, cudaStream_t stream);
 
 // ---- accept
 struct AcceptPlan {
