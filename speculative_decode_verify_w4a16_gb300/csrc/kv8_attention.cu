@@ -1,120 +1,1038 @@
 // Tree-masked verify attention over the paged 8-bit cache (contract in
-// w4a16sv.h): the first, plain form. A warp takes one query row (request,
-// node, head) and walks over its keys: the request's full blocks, its tail
-// rows, the tree's own rows on the node's root path; lane l holds columns
-// 4 l .. 4 l + 3. Everything in fp32.
+// w4a16sv.h).
+//
+// The query rows of a KV head are its G = H / Hkv query heads at every tree
+// node, row R = node * G + head-in-group, in row blocks of up to NP = 64 rows.
+// The keys are the M side of both products, 128 of them a tile:
+//   S^T [key][row]  = K [key][d] . Q^T         (M = 128 keys, N = rows)
+//   O^T [d][row]   += V^T [d][key] . P^T       (M = 128 columns, N = rows)
+// so that the few rows of a draft fill the N side exactly and the work of the
+// softmax is rows x keys, not 128 x keys. The 8-bit keys go from HBM through
+// TMA straight into the tensor cores (kind::f8f6f4): q is the sum of two e4m3
+// terms, q 2^e = q1 + q2 / 32 with e such that the row's largest magnitude is
+// in [128, 256), which together hold bf16's 8 bits exactly for elements down
+// to 2^-14 of that maximum (absolute error 2^-23 of it below); the terms are
+// separate N columns (S = S1 + S2 / 32), so that K is read from shared memory
+// once. The 8-bit values are widened to fp16, exactly, on their way (shared
+// memory to shared memory), because the softmax weights need more than e4m3
+// holds: P is rounded to fp16 (half a step 2^-11).
+//
+// A page's scales are powers of two per 64 keys: the keys' multiplies the
+// scores; the values' is added to the exponent. P = 2^(s + log2 sv - m) is
+// what multiplies the code, and the normaliser adds P / sv, in fp32.
+//
+// Online softmax: m is a reference per row, 7 below the maximum of s + log2 sv
+// when it was last raised; it is raised again only when a weight would pass
+// 2^15 (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is
+// 2^-21 of the largest). One vote per tile over the four warps finds that;
+// the maximum itself, and the rescaling of O^T in TMEM, are computed only then
+// (the first tile, and seldom after it).
+//
+// The last tile of bf16 rows, the tail page's (rows 0 .. 63 of the tile) and
+// the tree's own (64 .. 127), comes first in a request's tiles, with bf16
+// operands (kind::f16) and the mask: tail row r for r < lens % 64, node j for
+// the rows of j and its descendants. Rows that hold nothing are zeroed in
+// shared memory, and so are values that are not finite in a node (a node does
+// not see its siblings, and 0 * NaN is NaN); they are added at the end to the
+// rows that do see the node.
+//
+// Work: every (request, KV head, row block) unit has 1 + ceil(full blocks / 2)
+// tiles. The tiles of all units are laid end to end and cut into one run per
+// SM; a CTA walks over its run, which may end one unit and start others. A
+// unit inside one run is finished there; one that was cut leaves (m, l, O^T)
+// per run, and kv8_attention_combine_kernel merges them.
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
-#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace w4a16 {
 
 constexpr int kKaD = 128;
-constexpr int kKaWarps = 4;
+constexpr int kKaTile = 128;      // keys per tile
+constexpr float kKaRoom = 7.0f;   // log2 of the largest weight when m is set
+constexpr float kKaLimit = 15.0f;  // ... and where m is raised
+constexpr float kKaNone = -1e30f;  // m before any key
 
-template <int FMT>
-__device__ __forceinline__ float4 ka_decode(uint32_t w) {
-  constexpr __nv_fp8_interpretation_t t = FMT == 0 ? __NV_E4M3 : __NV_E5M2;
-  const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), t));
-  const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), t));
-  const float2 x = __half22float2(a), y = __half22float2(b);
-  return make_float4(x.x, x.y, y.x, y.y);
-}
-__device__ __forceinline__ float4 ka_bf16(uint2 w) {
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
-}
-
-struct KaRow {  // the online softmax of one query row
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  __device__ void add(float4 q, float4 k, float4 v) {
-    float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s), c = mn == -INFINITY ? 1.0f : exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * c + w;
-    o.x = o.x * c + w * v.x;
-    o.y = o.y * c + w * v.y;
-    o.z = o.z * c + w * v.z;
-    o.w = o.w * c + w * v.w;
-  }
+struct KaWork {  // the cut of the tiles into runs
+  int row_blocks, np, ctas, min_tiles;
+  float* part_o;      // [2 ctas][np][D]
+  float2* part_ml;    // [2 ctas][np]
+  int64_t* pre;       // [B + 1]: tiles of one unit of the requests before b
 };
 
-template <int FMT>
-__global__ void __launch_bounds__(32 * kKaWarps) kv8_attention_plain_kernel(const Kv8AttnParams p) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kKaWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.B * p.n * p.H) return;
-  const int h = (int)(row % p.H), j = (int)(row / p.H % p.n), b = (int)(row / p.H / p.n);
-  const int kvh = h / (p.H / p.Hkv);
-  int len = p.lens[b];
-  if (len < 0 || len > p.max_len) {
-    if (lane == 0) report_error(p.err, kErrInput);
-    len = len < 0 ? 0 : p.max_len;
+__device__ __forceinline__ float ka_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t ka_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t ka_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// named barrier over one softmax warpgroup, and the same with a vote
+__device__ __forceinline__ void ka_bar(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool ka_bar_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, %2, 128, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return r != 0;
+}
+// float <-> an unsigned that rises with it (NaN never raises a maximum)
+__device__ __forceinline__ unsigned ka_key(float x) {
+  const unsigned b = __float_as_uint(x);
+  return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float ka_unkey(unsigned k) {
+  return k == 0u ? -INFINITY : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+// Lane 0 waits (bounded), every lane gets the outcome; the first tests do not
+// suspend (these hand-offs are short). Once a wait has run out (ok false) the
+// later ones return at once: the warps that meet at named barriers then walk
+// through the rest of their work, on garbage and in bounds, instead of
+// leaving the others waiting.
+__device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, unsigned* err, bool still = true) {
+  if (!still) return false;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) {
+    int k = 0;
+    while (k < 64 && !mbar_try_wait(bar, parity)) ++k;
+    if (k == 64) ok = mbar_wait(bar, parity, err) ? 1 : 0;
   }
-  float4 q = ka_bf16(*reinterpret_cast<const uint2*>(p.q + ((int64_t)b * p.n + j) * p.q_stride + h * kKaD + 4 * lane));
-  q.x *= p.scale_log2;
-  q.y *= p.scale_log2;
-  q.z *= p.scale_log2;
-  q.w *= p.scale_log2;
-  KaRow st;
-  for (int blk = 0; blk < len / 64; ++blk) {
-    const int page = p.table[(int64_t)b * p.max_blocks + blk];
-    const bool ok = page >= 0 && page < p.pages;
-    if (!ok && lane == 0) report_error(p.err, kErrInput);
-    const int64_t at = ok ? (int64_t)page * p.Hkv + kvh : 0;
-    const float sk = ok ? p.k_scale[at] : 0.0f, sv = ok ? p.v_scale[at] : 0.0f;
-    for (int r = 0; r < 64; ++r) {
-      float4 k = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = k;
-      if (ok) {
-        k = ka_decode<FMT>(*reinterpret_cast<const uint32_t*>(p.k + (at * 64 + r) * kKaD + 4 * lane));
-        v = ka_decode<FMT>(*reinterpret_cast<const uint32_t*>(p.v + (at * 64 + r) * kKaD + 4 * lane));
-      }
-      st.add(q, make_float4(k.x * sk, k.y * sk, k.z * sk, k.w * sk),
-             make_float4(v.x * sv, v.y * sv, v.z * sv, v.w * sv));
-    }
-  }
-  const int tail = p.tails[b];
-  if (len % 64 > 0 && (tail < 0 || tail >= p.tail_pages)) {
-    if (lane == 0) report_error(p.err, kErrInput);
-  } else {
-    for (int r = 0; r < len % 64; ++r) {
-      const int64_t at = (((int64_t)tail * p.Hkv + kvh) * 64 + r) * kKaD + 4 * lane;
-      st.add(q, ka_bf16(*reinterpret_cast<const uint2*>(p.k_tail + at)),
-             ka_bf16(*reinterpret_cast<const uint2*>(p.v_tail + at)));
-    }
-  }
-  for (int a = j; a >= 0;) {
-    const int64_t at = ((int64_t)b * p.n + a) * p.kv_stride + kvh * kKaD + 4 * lane;
-    st.add(q, ka_bf16(*reinterpret_cast<const uint2*>(p.k_new + at)),
-           ka_bf16(*reinterpret_cast<const uint2*>(p.v_new + at)));
-    const int up = p.parents ? p.parents[(int64_t)b * p.n + a] : a - 1;
-    if (a == 0 ? up != -1 : (up < 0 || up >= a)) {
-      if (lane == 0) report_error(p.err, kErrInput);
-      break;
-    }
-    a = up;
-  }
-  const float inv = 1.0f / st.l;
-  __nv_bfloat16* out = p.out + row * kKaD + 4 * lane;
-  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(st.o.x * inv, st.o.y * inv);
-  *reinterpret_cast<__nv_bfloat162*>(out + 2) = __floats2bfloat162_rn(st.o.z * inv, st.o.w * inv);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
 }
 
-size_t kv8_attention_ws(int, int, int, int, int, int) { return 0; }
+__device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
+  const int l = p.lens[b];
+  return l < 0 ? 0 : l > p.max_len ? p.max_len : l;
+}
+__device__ __forceinline__ int ka_tiles(int len) { return 1 + (len / 64 + 1) / 2; }
 
-cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void*, int, cudaStream_t stream) {
+// One part of a run: tiles lo .. hi - 1 of the nt tiles of unit u of request b
+struct KaSeg {
+  int b, u, lo, hi, nt, len;
+};
+struct KaIter {
+  int64_t left;
+  int b, u, tile, units;
+  int len, nt;
+};
+__device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSeg& s) {
+  if (it.left <= 0 || it.b >= p.B) return false;
+  const int take = (int)min((int64_t)(it.nt - it.tile), it.left);
+  s = KaSeg{it.b, it.u, it.tile, it.tile + take, it.nt, it.len};
+  it.left -= take;
+  it.tile = 0;
+  if (++it.u == it.units) {
+    it.u = 0;
+    ++it.b;
+    if (it.left > 0 && it.b < p.B) {
+      it.len = ka_len(p, it.b);
+      it.nt = ka_tiles(it.len);
+    }
+  }
+  return true;
+}
+
+// run c of C: tiles [c T / C, (c + 1) T / C); as many runs as leave min_tiles
+// tiles each
+__device__ __forceinline__ int64_t ka_runs(int64_t T, int ctas, int min_tiles) {
+  const int64_t r = T / min_tiles;
+  return r < 1 ? 1 : r > ctas ? ctas : r;
+}
+__device__ __forceinline__ int64_t ka_run_begin(int64_t T, int64_t C, int64_t c) { return c * T / C; }
+
+template <int NP>
+struct KaCfg {
+  static constexpr int kGroups = NP > 32 ? 2 : 1;  // softmax warpgroups, NP / kGroups rows each
+  static constexpr int kRows = NP / kGroups;
+  static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
+  static constexpr int kThreads = 32 * (kConv0 + 4);
+  // stages of 128 keys (16 KB): the values leave theirs as soon as they are
+  // widened, so theirs is the ring to shorten
+  static constexpr int kStages = NP > 16 ? 3 : 4, kVStages = NP > 48 ? 2 : kStages;
+  static constexpr int kTileBytes = kKaTile * 128;
+  static constexpr int kPBytes = NP * 256;
+  static constexpr int kKOff = 0;
+  static constexpr int kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kWOff = kVOff + kVStages * kTileBytes;  // two buffers of 16-bit values
+  static constexpr int kQ8Off = kWOff + 2 * 2 * kTileBytes;   // 2 NP rows of 128 bytes
+  static constexpr int kQ16Off = kQ8Off + 2 * NP * 128;       // 2 halves of NP rows of 128 bytes
+  static constexpr int kPOff = kQ16Off + 2 * NP * 128;
+  static constexpr int kMaskOff = kPOff + 2 * kPBytes;        // u64 [NP]
+  static constexpr int kGmOff = kMaskOff + NP * 8;            // float2 [NP]: score factor, m
+  static constexpr int kFacOff = kGmOff + NP * 8;             // float [NP]
+  static constexpr int kMaxOff = kFacOff + NP * 4;            // u32 [4][NP], and the sums of the end
+  static constexpr int kRowOff = kMaxOff + NP * 16;           // int [NP]
+  static constexpr int kBarOff = kRowOff + NP * 4;
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11;
+  static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
+  // TMEM columns: scores (two terms) of two tiles, then O^T
+  static constexpr uint32_t kOCol = 4 * NP;
+  static constexpr uint32_t kCols = 5 * NP <= 128 ? 128 : 5 * NP <= 256 ? 256 : 512;
+  static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
+  static_assert(NP % 16 == 0 && kRows % 8 == 0, "row block");
+};
+
+struct KaMaps {
+  CUtensorMap k, v, k_tail, v_tail, k_new, v_new;
+};
+
+template <int NP, int FMT>
+__global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
+    kv8_attention_kernel(const __grid_constant__ KaMaps maps, const Kv8AttnParams p, const KaWork wk) {
+  using C = KaCfg<NP>;
+  constexpr int S = C::kStages, SV = C::kVStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* mask_s = reinterpret_cast<uint64_t*>(smem + C::kMaskOff);
+  float2* gm_s = reinterpret_cast<float2*>(smem + C::kGmOff);
+  float* fac_s = reinterpret_cast<float*>(smem + C::kFacOff);
+  unsigned* max_s = reinterpret_cast<unsigned*>(smem + C::kMaxOff);
+  int* row_s = reinterpret_cast<int*>(smem + C::kRowOff);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* k_free = k_full + S;
+  uint64_t* v_full = k_free + S;
+  uint64_t* v_free = v_full + SV;
+  uint64_t* w_full = v_free + SV;  // [2] 16-bit values ready
+  uint64_t* s_full = w_full + 2;   // [2]
+  uint64_t* p_full = s_full + 2;   // [2]
+  uint64_t* pv_done = p_full + 2;  // [2]
+  uint64_t* q_ready = pv_done + 2;
+  uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
+  uint64_t* mma_fin = x_full + 1;
+  __shared__ uint32_t tmem_s;
+  __shared__ int64_t scan_s[32];
+  __shared__ int64_t s_pre;
+  __shared__ int s_b;
+  __shared__ int par_s[64];
+  __shared__ unsigned long long bad_s[4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  grid_launch_dependents();
+  grid_dependency_wait();
+  // ---- this CTA's run: sums of the requests' tiles
+  const int units = p.Hkv * wk.row_blocks;
+  int64_t mine = 0;
+  for (int b = tid; b < p.B; b += C::kThreads) {
+    mine += ka_tiles(ka_len(p, b));
+    if (blockIdx.x == 0) {
+      const int l = p.lens[b];
+      if (l < 0 || l > p.max_len) report_error(p.err, kErrInput);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  if (lane == 0) scan_s[warp] = mine;
+  __syncthreads();
+  int64_t T = 0;
+  for (int w = 0; w < C::kThreads / 32; ++w) T += scan_s[w];
+  T *= units;
+  const int64_t runs = ka_runs(T, wk.ctas, wk.min_tiles);
+  const int64_t f0 = ka_run_begin(T, runs, blockIdx.x), f1 = ka_run_begin(T, runs, (int64_t)blockIdx.x + 1);
+  if (blockIdx.x >= runs) return;
+  {
+    const int64_t target = f0 / units;  // pre[b] <= target < pre[b + 1]
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
+      const int b = b0 + tid, n = b < p.B ? ka_tiles(ka_len(p, b)) : 0;
+      int x = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan_s[warp] = x;
+      __syncthreads();
+      int64_t at = before + x - n;
+      for (int w = 0; w < C::kThreads / 32; ++w) {
+        if (w < warp) at += scan_s[w];
+        before += scan_s[w];
+      }
+      if (b < p.B) {
+        if (target >= at && target < at + n) {
+          s_b = b;
+          s_pre = at;
+        }
+        if (blockIdx.x == 0) {  // for the merging of cut units
+          wk.pre[b] = at;
+          if (b == p.B - 1) wk.pre[p.B] = at + n;
+        }
+      }
+      if (before > target && blockIdx.x != 0) break;
+    }
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_free[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_free[s], 4);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&w_full[k], 4);
+      mbar_init(&s_full[k], 1);
+      mbar_init(&p_full[k], 4 * C::kGroups);
+      mbar_init(&pv_done[k], 1);
+    }
+    mbar_init(q_ready, 4 * C::kGroups);
+    mbar_init(x_full, 1);
+    mbar_init(mma_fin, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(&tmem_s, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  KaIter it;
+  {
+    it.left = f1 - f0;
+    it.units = units;
+    it.b = s_b;
+    it.len = ka_len(p, it.b);
+    it.nt = ka_tiles(it.len);
+    const int64_t rel = f0 - (int64_t)units * s_pre;
+    it.u = (int)(rel / it.nt);
+    it.tile = (int)(rel % it.nt);
+  }
+  KaSeg sg;
+  int issued = 0;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    // K stages are used in order; a bf16 tile takes two neighbours (32 KB), and
+    // passes over the last stage, which has none. Every use of a stage, a
+    // passed one too, completes a phase of its full and its free barrier.
+    // (A bf16 tile's values go straight to a 16-bit buffer: the widening warps
+    // ask for them.)
+    int kc = 0, vc = 0;  // uses of the K and V stages
+    int k_more = 0;      // a use of K whose tile was given up
+    bool ok = true;
+    auto k_wait = [&](int use) {
+      return use < S || mbar_wait(&k_free[use % S], (uint32_t)(use / S - 1) & 1u, p.err);
+    };
+    while (ok && ka_next(p, it, sg)) {
+      const int kvh = sg.u / wk.row_blocks;
+      if (sg.lo == 0) {
+        const int t = sg.len & 63;
+        const bool pass = kc % S == S - 1;
+        if (lane == 0) {
+          if (pass && (ok = k_wait(kc))) mbar_arrive(&k_full[S - 1]);
+          const int use = kc + (pass ? 1 : 0), s = use % S;
+          ok = ok && k_wait(use) && k_wait(use + 1);
+          if (ok) {
+            const int tail = p.tails[sg.b];
+            const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
+            if (t > 0 && !tok) report_error(p.err, kErrInput);
+            uint8_t* kd = smem + C::kKOff + s * C::kTileBytes;
+            mbar_arrive(&k_full[s + 1]);
+            mbar_arrive_expect_tx(&k_full[s], (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
+            for (int h = 0; h < 2; ++h) {
+              if (tok) tma_load_3d(kd + h * C::kTileBytes, &maps.k_tail, 64 * h, 0, tail * p.Hkv + kvh, &k_full[s]);
+              tma_load_4d(kd + h * C::kTileBytes + 8192, &maps.k_new, 64 * h, kvh, 0, sg.b, &k_full[s]);
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (ok) kc += pass ? 3 : 2;
+      }
+      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1; the page
+      // ids of 16 tiles at a time in the lanes
+      const int full = sg.len / 64;
+      const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
+      const int i0 = max(sg.lo, 1);
+      int page = 0;
+      for (int i = i0; ok && i < sg.hi; ++i) {
+        const int k = (i - i0) & 15;
+        if (k == 0) {
+          const int blk = 2 * (i - 1) + lane;
+          page = blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
+          if (page != -2 && (page < 0 || page >= p.pages)) {
+            report_error(p.err, kErrInput);
+            page = -2;
+          }
+        }
+        const int pa = __shfl_sync(0xffffffffu, page, 2 * k), pb = __shfl_sync(0xffffffffu, page, 2 * k + 1);
+        if (lane == 0) {
+          // a page that is not there: past the tensor's end, filled with zeros
+          const int none = p.pages * p.Hkv;
+          const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
+          const int ks = kc % S, vs = vc % SV;
+          ok = k_wait(kc);
+          if (ok) {
+            uint8_t* kd = smem + C::kKOff + ks * C::kTileBytes;
+            mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+            tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
+            tma_load_3d(kd + 8192, &maps.k, 0, 0, zb, &k_full[ks]);
+            k_more = 1;
+            if (vc >= SV) ok = mbar_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
+          }
+          if (ok) {
+            uint8_t* vd = smem + C::kVOff + vs * C::kTileBytes;
+            mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+            tma_load_3d(vd, &maps.v, 0, 0, za, &v_full[vs]);
+            tma_load_3d(vd + 8192, &maps.v, 0, 0, zb, &v_full[vs]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (ok) {
+          ++kc;
+          ++vc;
+          k_more = 0;
+        }
+      }
+    }
+    // every copy has landed before the CTA exits (it has, unless a wait ran
+    // out somewhere): the last use of each stage
+    if (lane == 0) {
+      const int ke = kc + k_more;
+      for (int u = ke > S ? ke - S : 0; u < ke; ++u) mbar_wait(&k_full[u % S], (uint32_t)(u / S) & 1u, p.err);
+      for (int u = vc > SV ? vc - SV : 0; u < vc; ++u) mbar_wait(&v_full[u % SV], (uint32_t)(u / SV) & 1u, p.err);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA
+    constexpr uint32_t id_s8 = umma_idesc(2 * NP, (uint32_t)FMT, 0u, 0u, 0u);
+    constexpr uint32_t id_s16 = umma_idesc(NP, 1u, 1u, 0u, 0u);
+    constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 1u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
+    const uint32_t kb = smem_u32(smem + C::kKOff), wb = smem_u32(smem + C::kWOff), pb = smem_u32(smem + C::kPOff);
+    const uint32_t q8 = smem_u32(smem + C::kQ8Off), q16 = smem_u32(smem + C::kQ16Off);
+    int kc = 0, tc = 0, seg = 0;  // K stages, tiles, segments so far
+    bool ok = true;
+    while (ok && ka_next(p, it, sg)) {
+      ok = ka_wait(q_ready, (uint32_t)seg & 1u, p.err);
+      tc_fence_after();
+      const int n = sg.hi - sg.lo, t0 = tc;
+      // S of tile i (its scores' buffer was read before P of tile i - 2 was
+      // ready, which P V (i - 2) waited for)
+      auto issue_s = [&](int i) {
+        const uint32_t d = tmem + (uint32_t)((t0 + i) & 1) * 2u * NP;
+        const bool first = i == 0 && sg.lo == 0;
+        if (first && kc % S == S - 1) {  // the stage that the producer passed over
+          if (!ka_wait(&k_full[S - 1], (uint32_t)(kc / S) & 1u, p.err)) return false;
+          umma_commit_warp(&k_free[S - 1]);
+          issued = 1;
+          ++kc;
+        }
+        const int s = kc % S;
+        if (!ka_wait(&k_full[s], (uint32_t)(kc / S) & 1u, p.err)) return false;
+        if (first && !ka_wait(&k_full[s + 1], (uint32_t)((kc + 1) / S) & 1u, p.err)) return false;
+        tc_fence_after();
+        const uint32_t a = kb + (uint32_t)s * C::kTileBytes;
+        if (first) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ss_warp(d, umma_desc_sw128_kmajor(a + (uint32_t)((k >> 2) * C::kTileBytes + 32 * (k & 3))),
+                              umma_desc_sw128_kmajor(q16 + (uint32_t)((k >> 2) * NP * 128 + 32 * (k & 3))), id_s16,
+                              k > 0 ? 1u : 0u);
+          umma_commit_warp(&k_free[s]);
+          umma_commit_warp(&k_free[s + 1]);
+          kc += 2;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8_ss_warp(d, umma_desc_sw128_kmajor(a + 32u * (uint32_t)k),
+                            umma_desc_sw128_kmajor(q8 + 32u * (uint32_t)k), id_s8, k > 0 ? 1u : 0u);
+          umma_commit_warp(&k_free[s]);
+          ++kc;
+        }
+        umma_commit_warp(&s_full[(t0 + i) & 1]);
+        issued = 1;
+        return true;
+      };
+      for (int i = 0; ok && i < 2 && i < n; ++i) ok = issue_s(i);
+      for (int i = 0; ok && i < n; ++i) {
+        const int w = (t0 + i) & 1;
+        const uint32_t ph = (uint32_t)((t0 + i) >> 1) & 1u;
+        if (!ka_wait(&w_full[w], ph, p.err) || !ka_wait(&p_full[w], ph, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t id = i == 0 && sg.lo == 0 ? id_o16 : id_o8;
+        // V^T: 128-byte rows of 64 columns a key, the other 64 columns a half
+        // on; P^T: chunks of 8 rows, 16 bytes a key. 16 keys an MMA.
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_bf16_ss_warp(tmem + C::kOCol,
+                            umma_desc_sw128_mnmajor(wb + (uint32_t)(w * 2 * C::kTileBytes + 2048 * k),
+                                                    (uint32_t)C::kTileBytes, 1024u),
+                            umma_desc_flat_mnmajor(pb + (uint32_t)(w * C::kPBytes + 256 * k), 128u, 2048u), id,
+                            (i > 0 || k > 0) ? 1u : 0u);
+        umma_commit_warp(&pv_done[w]);
+        if (i + 2 < n) ok = issue_s(i + 2);
+      }
+      tc += n;
+      ++seg;
+    }
+    if (issued) umma_commit_warp(mma_fin);
+  } else if (warp >= C::kConv0) {
+    // -------------------------------------------- values to 16-bit, in place
+    // of the tile's order: a thread takes 16 codes (one 16-byte chunk c) of
+    // rows r, r + 16, ..: their 16 fp16 fill two chunks of a half-row. The
+    // chunks of the two halves are stored in opposite order, so that a
+    // quarter-warp's stores fall into different banks.
+    const int ct = tid - 32 * C::kConv0;
+    const int c = ct & 7, r0 = ct >> 3;
+    int vc = 0, tc = 0, xc = 0, seg = 0;
+    bool ok = true;
+    while (ka_next(p, it, sg)) {
+      for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
+        uint8_t* w = smem + C::kWOff + (tc & 1) * 2 * C::kTileBytes;
+        // P V (tc - 2) has left the buffer
+        if (tc >= 2) ok = ka_wait(&pv_done[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
+        if (i == 0) {
+          const int t = sg.len & 63, tail = p.tails[sg.b];
+          const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
+          if (ct == 0) bad_s[seg & 3] = 0ull;
+          asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+          if (ct == 0 && ok) {  // (all four warps are past the last such tile)
+            const int kvh = sg.u / wk.row_blocks;
+            mbar_arrive_expect_tx(x_full, (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
+            for (int h = 0; h < 2; ++h) {
+              if (tok) tma_load_3d(w + h * C::kTileBytes, &maps.v_tail, 64 * h, 0, tail * p.Hkv + kvh, x_full);
+              tma_load_4d(w + h * C::kTileBytes + 8192, &maps.v_new, 64 * h, kvh, 0, sg.b, x_full);
+            }
+          }
+          __syncwarp();
+          ok = ka_wait(x_full, (uint32_t)xc & 1u, p.err, ok);
+          ++xc;
+          // thread = row of the tile: its 256 bytes, both halves
+          const bool node = ct >= 64;
+          const bool there = node ? ct - 64 < p.n : tok && ct < t;
+          uint4* row[2] = {reinterpret_cast<uint4*>(w + ct * 128),
+                           reinterpret_cast<uint4*>(w + C::kTileBytes + ct * 128)};
+          bool bad = false;
+#pragma unroll 1
+          for (int k = 0; k < 16; ++k) {
+            uint4* at = row[k >> 3] + ((k + ct) & 7);
+            if (!there) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else if (node) {
+              uint4 x = *at;
+              uint32_t* e = &x.x;
+              bool any = false;
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                if ((e[m] & 0x7F80u) == 0x7F80u) {
+                  e[m] &= 0xFFFF0000u;
+                  any = true;
+                }
+                if ((e[m] & 0x7F800000u) == 0x7F800000u) {
+                  e[m] &= 0xFFFFu;
+                  any = true;
+                }
+              }
+              if (any) *at = x;
+              bad |= any;
+            }
+          }
+          if (bad) atomicOr(&bad_s[seg & 3], 1ull << (ct - 64));
+        } else {
+          const int s = vc % SV;
+          ok = ka_wait(&v_full[s], (uint32_t)(vc / SV) & 1u, p.err, ok);
+          ++vc;
+          const uint8_t* v = smem + C::kVOff + s * C::kTileBytes;
+          uint4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = r0 + 16 * k;
+            x[k] = *reinterpret_cast<const uint4*>(v + r * 128 + ((c ^ (r & 7)) << 4));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = r0 + 16 * k;
+            const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              if constexpr (FMT == 0) {
+                const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[m] & 0xFFFFu), __NV_E4M3);
+                const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[m] >> 16), __NV_E4M3);
+                o[2 * m] = (uint32_t)a.x | ((uint32_t)a.y << 16);
+                o[2 * m + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
+              } else {  // e5m2 is the upper byte of fp16
+                o[2 * m] = __byte_perm(in[m], 0u, 0x1404);
+                o[2 * m + 1] = __byte_perm(in[m], 0u, 0x3424);
+              }
+            }
+            uint8_t* dst = w + (c >> 2) * C::kTileBytes + r * 128;
+            const int c0 = (c & 3) * 2, sw = r & 7;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            const int f = c >> 2;  // the second half stores its upper chunk first
+            *reinterpret_cast<uint4*>(dst + (((c0 + f) ^ sw) << 4)) = f ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + (((c0 + (f ^ 1)) ^ sw) << 4)) = f ? lo : hi;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_free[s]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_full[tc & 1]);
+      }
+      ++seg;
+    }
+  } else if (warp >= C::kSoft0) {
+    // ------------------------------------------------------------ softmax
+    constexpr int Q = C::kRows;
+    const int wg = (warp - C::kSoft0) >> 2, qd = warp & 3;
+    const int key = qd * 32 + lane;  // the thread's key of a tile (TMEM lane)
+    const int st = tid - 32 * C::kSoft0 - 128 * wg;  // thread of the warpgroup
+    const int qa = wg * Q;                           // its first row
+    const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
+    const int bar = 1 + wg;
+    int tc = 0, seg = 0;
+    bool ok = true;
+    while (ka_next(p, it, sg)) {
+      const int kvh = sg.u / wk.row_blocks, rb = sg.u % wk.row_blocks;
+      const int G = p.H / p.Hkv, rows = p.n * G;
+      // ---- Q: 16 lanes a row, 8 columns each, into the two e4m3 terms and bf16
+      {
+        const int d = (st & 15) * 8;
+        uint4 v[Q / 8];
+#pragma unroll
+        for (int k = 0; k < Q / 8; ++k) {
+          const int R = rb * NP + qa + 8 * k + (st >> 4);
+          const int j = R / G, g = R - j * G;
+          v[k] = R < rows ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)sg.b * p.n + j) * p.q_stride +
+                                                            (kvh * G + g) * kKaD + d)
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (sg.lo == 0 && p.parents) {
+          // the parents (bad ones reported and cut off), for the masks; both
+          // warpgroups write the same
+          for (int j = st; j < p.n; j += 128) {
+            int up = p.parents[(int64_t)sg.b * p.n + j];
+            if (j == 0 ? up != -1 : (up < 0 || up >= j)) {
+              report_error(p.err, kErrInput);
+              up = -1;
+            }
+            par_s[j] = up;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < Q / 8; ++k) {
+          const int r = qa + 8 * k + (st >> 4);
+          const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          unsigned m = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
+            m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const int ex = min(134 - (int)(m >> 7), 120);  // |q| 2^ex in [128, 256)
+          const float up = __uint_as_float((unsigned)(127 + ex) << 23);
+          uint32_t t1[2], t2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t a = 0, b = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t u = in[2 * e + h];
+              float x0 = __uint_as_float(u << 16) * up, x1 = __uint_as_float(u & 0xFFFF0000u) * up;
+              if (!(fabsf(x0) < INFINITY)) x0 = NAN;
+              if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+              const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+              const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
+              const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
+                                                           __NV_SATFINITE, __NV_E4M3);
+              a |= c1 << (16 * h);
+              b |= c2 << (16 * h);
+            }
+            t1[e] = a;
+            t2[e] = b;
+          }
+          const int sw = r & 7;
+          uint8_t* q8 = smem + C::kQ8Off + r * 128 + ((((d >> 4) ^ sw) << 4) | (d & 8));
+          *reinterpret_cast<uint2*>(q8) = make_uint2(t1[0], t1[1]);
+          *reinterpret_cast<uint2*>(q8 + NP * 128) = make_uint2(t2[0], t2[1]);
+          *reinterpret_cast<uint4*>(smem + C::kQ16Off + (d >> 6) * NP * 128 + r * 128 + ((((d >> 3) & 7) ^ sw) << 4)) =
+              v[k];
+          if ((st & 15) == 0)
+            gm_s[r] = make_float2(__uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2, kKaNone);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+        ka_bar(bar);
+        if (st < Q) {
+          const int r = qa + st, R = rb * NP + r, j = R / G, g = R - j * G;
+          row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + g : -1;
+          uint64_t m = 0;
+          if (sg.lo == 0 && R < rows) {
+            if (p.parents)
+              for (int k = j; k >= 0; k = par_s[k]) m |= 1ull << k;
+            else
+              m = j == 63 ? ~0ull : (1ull << (j + 1)) - 1ull;
+          }
+          mask_s[r] = m;
+        }
+        ka_bar(bar);
+      }
+      float l[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) l[q] = 0.0f;
+      // ---- scales of this warp's block of each tile, 32 tiles at a time, the
+      // next ones asked for ahead
+      const int half = qd >> 1, full = sg.len / 64, i1 = max(sg.lo, 1);
+      const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
+      auto page_of = [&](int base) {
+        const int i = base + lane, blk = 2 * (i - 1) + half;
+        if (i >= sg.hi || blk >= full) return -2;
+        const int pg = tab[blk];
+        return pg < 0 || pg >= p.pages ? -1 : pg;
+      };
+      auto scale_of = [&](int pg, float& sk, float& sv) {
+        sk = pg >= 0 ? p.k_scale[(int64_t)pg * p.Hkv + kvh] : 0.0f;
+        sv = pg >= 0 ? p.v_scale[(int64_t)pg * p.Hkv + kvh] : 1.0f;
+      };
+      int pg = page_of(i1), pg_next = -2;
+      float sk_l, sv_l, sk_n = 0.0f, sv_n = 1.0f;
+      scale_of(pg, sk_l, sv_l);
+      for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
+        const int buf = tc & 1;
+        const bool bf = i == 0;
+        float sk = 1.0f, sv = 1.0f;
+        bool gone = false;  // this warp's block does not exist
+        if (!bf) {
+          const int k = (i - i1) & 31;
+          if (k == 0 && i > i1) {
+            pg = pg_next;
+            sk_l = sk_n;
+            sv_l = sv_n;
+          }
+          if (k == 8) pg_next = page_of(i - k + 32);
+          if (k == 20) scale_of(pg_next, sk_n, sv_n);
+          sk = __shfl_sync(0xffffffffu, sk_l, k);
+          sv = __shfl_sync(0xffffffffu, sv_l, k);
+          gone = __shfl_sync(0xffffffffu, pg, k) == -2;
+        }
+        const float lsv = bf ? 0.0f : log2f(sv), isv = 1.0f / sv;
+        ok = ka_wait(&s_full[buf], (uint32_t)(tc >> 1) & 1u, p.err, ok);
+        tc_fence_after();
+        // ---- a = s + log2 sv
+        float a[Q];
+        const uint32_t sc = trow + (uint32_t)buf * 2u * NP + (uint32_t)qa;
+#pragma unroll
+        for (int q0 = 0; q0 < Q; q0 += 8) {
+          uint32_t u1[8], u2[8];
+          tmem_ld_32x32b<8>(sc + q0, u1);
+          if (!bf) tmem_ld_32x32b<8>(sc + NP + q0, u2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float g = gm_s[qa + q0 + q].x;
+            if (bf)
+              a[q0 + q] = __uint_as_float(u1[q]) * p.scale_log2;
+            else
+              a[q0 + q] = fmaf(fmaf(__uint_as_float(u2[q]), 0.03125f, __uint_as_float(u1[q])), g * sk, lsv);
+          }
+        }
+        if (bf) {
+          const int tail = p.tails[sg.b];
+          const bool mine = key < (sg.len & 63) && tail >= 0 && tail < p.tail_pages;
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const bool see = key < 64 ? mine : (mask_s[qa + q] >> (key - 64)) & 1ull;
+            if (!see) a[q] = -INFINITY;
+          }
+        } else if (gone) {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) a[q] = -INFINITY;
+        }
+        // ---- does a weight pass the limit?
+        float over = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) over = fmaxf(over, a[q] - gm_s[qa + q].y);
+        if (ka_bar_any(bar, over > kKaLimit)) {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const unsigned m = __reduce_max_sync(0xffffffffu, ka_key(a[q]));
+            if (lane == 0) max_s[qd * NP + qa + q] = m;
+          }
+          ka_bar(bar);
+          if (st < Q) {
+            const int r = qa + st;
+            const float mx = ka_unkey(max(max(max_s[r], max_s[NP + r]), max(max_s[2 * NP + r], max_s[3 * NP + r])));
+            const float m = gm_s[r].y;
+            float f = 1.0f;
+            if (mx - m > kKaLimit) {
+              const float mn = mx - kKaRoom;
+              f = ka_ex2(m - mn);
+              gm_s[r].y = mn;
+            }
+            fac_s[r] = f;
+          }
+          ka_bar(bar);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) l[q] *= fac_s[qa + q];
+          if (i > sg.lo) {
+            // O^T holds the sums up to tile i - 1
+            ok = ka_wait(&pv_done[buf ^ 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+            tc_fence_after();
+#pragma unroll 1
+            for (int q0 = 0; q0 < Q; q0 += 8) {
+              uint32_t o[8];
+              tmem_ld_32x32b<8>(trow + C::kOCol + (uint32_t)(qa + q0), o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac_s[qa + q0 + q]);
+              tmem_st_32x32b_x8(trow + C::kOCol + (uint32_t)(qa + q0), o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // ---- P, into the buffer that P V (i - 2) has left
+        if (tc >= 2) ok = ka_wait(&pv_done[buf], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
+        uint8_t* pd = smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16;
+#pragma unroll
+        for (int q0 = 0; q0 < Q; q0 += 8) {
+          float e[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            e[q] = ka_ex2(a[q0 + q] - gm_s[qa + q0 + q].y);
+            l[q0 + q] = fmaf(e[q], isv, l[q0 + q]);
+          }
+          *reinterpret_cast<uint4*>(pd + (q0 >> 3) * 2048) =
+              bf ? make_uint4(ka_bf162(e[0], e[1]), ka_bf162(e[2], e[3]), ka_bf162(e[4], e[5]), ka_bf162(e[6], e[7]))
+                 : make_uint4(ka_half2(e[0], e[1]), ka_half2(e[2], e[3]), ka_half2(e[4], e[5]), ka_half2(e[6], e[7]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      // ---- the end of the unit's part: the rows' sums over the keys (through
+      // the P buffers, which no MMA reads any more), then O^T
+      ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+      tc_fence_after();
+      // (each warpgroup's own chunks of them: the other one may be ahead)
+      auto sum = [&](int q) {
+        return reinterpret_cast<float*>(smem + C::kPOff + (q >= Q / 2 ? C::kPBytes : 0) + (qa >> 3) * 2048) +
+               (q % (Q / 2)) * 128;
+      };
+#pragma unroll
+      for (int q = 0; q < Q; ++q) sum(q)[key] = l[q];
+      ka_bar(bar);
+      {
+        float* part = reinterpret_cast<float*>(max_s);
+        const int q = st & 31, k0 = (st >> 5) * 32;
+        if (q < Q) {
+          float t = 0.0f;
+          for (int k = 0; k < 32; ++k) t += sum(q)[k0 + ((k + q) & 31)];
+          part[(st >> 5) * NP + qa + q] = t;
+        }
+        ka_bar(bar);
+        if (st < Q) {
+          const int r = qa + st;
+          fac_s[r] = (part[r] + part[NP + r]) + (part[2 * NP + r] + part[3 * NP + r]);
+        }
+        ka_bar(bar);
+      }
+      const bool whole = sg.lo == 0 && sg.hi == sg.nt;
+      // a cut unit's part: a run's first part in its first slot, else the second
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (seg == 0 ? 0 : 1);
+      const unsigned long long bad = sg.lo == 0 ? bad_s[seg & 3] : 0ull;
+      if (!whole && st < Q) wk.part_ml[slot * NP + qa + st] = make_float2(gm_s[qa + st].y, fac_s[qa + st]);
+#pragma unroll 1
+      for (int q0 = 0; q0 < Q; q0 += 8) {
+        uint32_t o[8];
+        tmem_ld_32x32b<8>(trow + C::kOCol + (uint32_t)(qa + q0), o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = qa + q0 + q;
+          float x = __uint_as_float(o[q]);
+          if (bad & mask_s[r]) {  // values that are not finite, of nodes this row sees
+            for (unsigned long long m = bad & mask_s[r]; m; m &= m - 1) {
+              const int j = __ffsll((long long)m) - 1;
+              const float v = __bfloat162float(p.v_new[((int64_t)sg.b * p.n + j) * p.kv_stride + kvh * kKaD + key]);
+              if (!(fabsf(v) < INFINITY)) x += v;
+            }
+          }
+          if (whole) {
+            if (row_s[r] >= 0) p.out[(int64_t)row_s[r] * kKaD + key] = __float2bfloat16_rn(x / fac_s[r]);
+          } else {
+            wk.part_o[(slot * NP + r) * kKaD + key] = x;
+          }
+        }
+      }
+      tc_fence_before();
+      ka_bar(bar);  // the small arrays are free for the next part
+      ++seg;
+    }
+  }
+
+  // ---------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1 && lane == 0 && issued) mbar_wait(mma_fin, 0u, p.err);  // no MMA in flight when TMEM is freed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
+}
+
+// One warp per query row: the parts of a unit that was cut over several runs,
+// merged and stored as bf16 (lane k: columns 4 k .. 4 k + 3). A unit inside
+// one run was finished there.
+__global__ void __launch_bounds__(256) kv8_attention_combine_kernel(const Kv8AttnParams p, const KaWork wk) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int G = p.H / p.Hkv, rows = p.n * G, units = p.Hkv * wk.row_blocks;
+  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (id >= (int64_t)p.B * p.Hkv * rows) return;
+  const int b = (int)(id / ((int64_t)p.Hkv * rows)), rest = (int)(id - (int64_t)b * p.Hkv * rows);
+  const int kvh = rest / rows, R = rest - kvh * rows;
+  const int rb = R / wk.np, r = R - rb * wk.np;
+  const int64_t T = __ldcg(&wk.pre[p.B]) * units;
+  const int64_t runs = ka_runs(T, wk.ctas, wk.min_tiles);
+  const int64_t first = __ldcg(&wk.pre[b]), nt = __ldcg(&wk.pre[b + 1]) - first;
+  const int64_t u0 = first * units + ((int64_t)kvh * wk.row_blocks + rb) * nt, u1 = u0 + nt;
+  // the run that holds tile f: run c begins at c T / runs
+  auto owner = [&](int64_t f) {
+    int64_t c = f * runs / T;
+    while (ka_run_begin(T, runs, c + 1) <= f) ++c;
+    while (ka_run_begin(T, runs, c) > f) --c;
+    return c;
+  };
+  const int64_t c0 = owner(u0), c1 = owner(u1 - 1);
+  if (c0 == c1) return;
+  // the parts: the first one is its run's first part only if the run begins with it
+  const int64_t s0 = 2 * c0 + (ka_run_begin(T, runs, c0) == u0 ? 0 : 1);
+  float M = -INFINITY;
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float m = __ldcg(&wk.part_ml[(c == c0 ? s0 : 2 * c) * wk.np + r]).x;
+    M = m > M ? m : M;
+  }
+  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t c = c0; c <= c1; ++c) {
+    const int64_t at = (c == c0 ? s0 : 2 * c) * wk.np + r;
+    const float2 ml = __ldcg(&wk.part_ml[at]);
+    const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);
+    l = fmaf(w, ml.y, l);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(wk.part_o + at * kKaD) + lane);
+    o[0] = fmaf(w, v.x, o[0]);
+    o[1] = fmaf(w, v.y, o[1]);
+    o[2] = fmaf(w, v.z, o[2]);
+    o[3] = fmaf(w, v.w, o[3]);
+  }
+  const int j = R / G, g = R - j * G;
+  const float inv = 1.0f / l;
+  __nv_bfloat16* dst = p.out + (((int64_t)b * p.n + j) * p.H + kvh * G + g) * kKaD + 4 * lane;
+  *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+  *reinterpret_cast<__nv_bfloat162*>(dst + 2) = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
+}
+
+// ------------------------------------------------------------------ host
+struct KaPlan {
+  int np, row_blocks, ctas;
+  size_t o_bytes, ml_bytes, total;
+};
+static KaPlan ka_plan(int B, int n, int H, int Hkv, int num_sms) {
+  KaPlan k;
+  const int rows = n * (H / Hkv);
+  // row blocks of at most 64 rows, all of the same size up to a multiple of 16
+  k.row_blocks = (rows + 63) / 64;
+  k.np = ((rows + k.row_blocks - 1) / k.row_blocks + 15) / 16 * 16;
+  k.ctas = num_sms > 0 ? num_sms : 1;
+  k.o_bytes = (size_t)2 * k.ctas * k.np * kKaD * 4;
+  k.ml_bytes = (size_t)2 * k.ctas * k.np * 8;
+  k.total = k.o_bytes + k.ml_bytes + ((size_t)B + 1) * 8;
+  return k;
+}
+
+size_t kv8_attention_ws(int B, int n, int H, int Hkv, int, int num_sms) { return ka_plan(B, n, H, Hkv, num_sms).total; }
+
+template <int NP, int FMT>
+static cudaError_t launch_ka(const KaMaps& maps, const Kv8AttnParams& p, const KaWork& wk, cudaStream_t stream) {
+  constexpr int smem = KaCfg<NP>::kTotal;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv8_attention_kernel<NP, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_attention_kernel<NP, FMT>, dim3((unsigned)wk.ctas), dim3(KaCfg<NP>::kThreads), (size_t)smem,
+                    stream, maps, p, wk);
+}
+
+cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspace, int num_sms, cudaStream_t stream) {
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+  if (!encode) return cudaErrorNotSupported;
+  const KaPlan k = ka_plan(p.B, p.n, p.H, p.Hkv, num_sms);
+  KaMaps maps;
+  const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
+  auto map = [&](CUtensorMap* m, CUtensorMapDataType t, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box) {
+    return encode(m, t, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  bool ok = true;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)kKaD, 64, (cuuint64_t)p.pages * p.Hkv}, st[2] = {kKaD, kKaD * 64};
+    const cuuint32_t box[3] = {(cuuint32_t)kKaD, 64u, 1u};
+    ok = map(&maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.k, dims, st, box) &&
+         map(&maps.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.v, dims, st, box);
+  }
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)kKaD, 64, (cuuint64_t)p.tail_pages * p.Hkv}, st[2] = {kKaD * 2, kKaD * 128};
+    const cuuint32_t box[3] = {64u, 64u, 1u};
+    ok = ok && map(&maps.k_tail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.k_tail, dims, st, box) &&
+         map(&maps.v_tail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p.v_tail, dims, st, box);
+  }
+  {
+    const cuuint64_t dims[4] = {(cuuint64_t)kKaD, (cuuint64_t)p.Hkv, (cuuint64_t)p.n, (cuuint64_t)p.B};
+    const cuuint64_t st[3] = {kKaD * 2, (cuuint64_t)p.kv_stride * 2, (cuuint64_t)p.kv_stride * 2 * p.n};
+    const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)p.n, 1u};
+    ok = ok && map(&maps.k_new, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.k_new, dims, st, box) &&
+         map(&maps.v_new, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.v_new, dims, st, box);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  KaWork wk;
+  wk.row_blocks = k.row_blocks;
+  wk.np = k.np;
+  wk.ctas = k.ctas;
+  wk.min_tiles = 2;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  wk.part_o = reinterpret_cast<float*>(ws);
+  wk.part_ml = reinterpret_cast<float2*>(ws + k.o_bytes);
+  wk.pre = reinterpret_cast<int64_t*>(ws + k.o_bytes + k.ml_bytes);
+  cudaError_t e;
+  switch (k.np) {
+    case 16: e = fmt ? launch_ka<16, 1>(maps, p, wk, stream) : launch_ka<16, 0>(maps, p, wk, stream); break;
+    case 32: e = fmt ? launch_ka<32, 1>(maps, p, wk, stream) : launch_ka<32, 0>(maps, p, wk, stream); break;
+    case 48: e = fmt ? launch_ka<48, 1>(maps, p, wk, stream) : launch_ka<48, 0>(maps, p, wk, stream); break;
+    default: e = fmt ? launch_ka<64, 1>(maps, p, wk, stream) : launch_ka<64, 0>(maps, p, wk, stream); break;
+  }
+  if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.B * p.n * p.H;
-  const dim3 grid((unsigned)((rows + kKaWarps - 1) / kKaWarps)), block(32 * kKaWarps);
-  return fmt == 0 ? launch_pdl(kv8_attention_plain_kernel<0>, grid, block, 0, stream, p)
-                  : launch_pdl(kv8_attention_plain_kernel<1>, grid, block, 0, stream, p);
+  return launch_pdl(kv8_attention_combine_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p, wk);
 }
 
 }  // namespace w4a16

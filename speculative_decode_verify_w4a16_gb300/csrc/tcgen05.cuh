@@ -49,6 +49,30 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// The same with NC = 8 or 16 repetitions into r[0 .. NC), and stored.
+template <int NC>
+__device__ __forceinline__ void tmem_ld_32x32b(uint32_t taddr, uint32_t* r) {
+  static_assert(NC == 8 || NC == 16, "repetitions");
+  if constexpr (NC == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 32 lanes x 32 bits, 32 repetitions: thread i reads lane (base + i),
 // columns col .. col + 31 into r[0..31]; no wait.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -119,6 +143,26 @@ __device__ __forceinline__ uint64_t umma_desc_sw128_mnmajor(uint32_t addr, uint3
   return d;
 }
 
+// Instruction descriptor in general: D fp32, M = 128 (cta_group::1), N = n.
+// fa, fb: the operands' formats (kind::f16: 0 fp16, 1 bf16; kind::f8f6f4: 0
+// e4m3, 1 e5m2); ta, tb: 1 for an MN-major operand.
+__host__ __device__ constexpr uint32_t umma_idesc(uint32_t n, uint32_t fa, uint32_t fb, uint32_t ta, uint32_t tb) {
+  return (1u << 4) | (fa << 7) | (fb << 10) | (ta << 15) | (tb << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor: MN-major operand of 16-bit elements without
+// swizzle. Core matrices of 8 K rows x 8 consecutive N (or M) elements (16
+// bytes a row, 128 bytes in all, contiguous); the next 8 K rows `kstep` bytes
+// on, the next 8 N elements `nstep` bytes on.
+__device__ __forceinline__ uint64_t umma_desc_flat_mnmajor(uint32_t addr, uint32_t kstep, uint32_t nstep) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);         // start address
+  d |= (uint64_t)((kstep >> 4) & 0x3FFFu) << 16;  // leading byte offset: next 8 K rows
+  d |= (uint64_t)((nstep >> 4) & 0x3FFFu) << 32;  // stride byte offset: next 8 N elements
+  d |= (uint64_t)1u << 46;                         // descriptor version (sm_100)
+  return d;                                        // layout 0: no swizzle
+}
+
 // Warp-wide forms: all 32 lanes execute the call with the same operands and
 // the lane that elect.sync picks (the same one every time in a converged
 // warp) issues. Issued this way from a loop the whole warp runs, a 128 x 64
@@ -146,6 +190,17 @@ __device__ __forceinline__ void umma_bf16_ss_warp(uint32_t d_tmem, uint64_t a_de
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same for 8-bit operands (kind::f8f6f4: 32 elements of K an instruction).
+__device__ __forceinline__ void umma_f8_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
@@ -159,6 +214,24 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
       "[%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 3-D and 4-D loads (coordinates innermost first).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            int32_t w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -55,9 +55,9 @@ def _plan_case(B, hi, rng, spare_pages, max_blocks):
     return lens, tails, table, ring, np.array([head, spare_pages, 0], np.int32)
 
 
-def _check_plan(case, kept, rows, release, **kw):
+def _check_plan(case, kept, total, release, **kw):
     lens, tails, table, ring, queue = case
-    want_table, want_ring, want = ref.plan(lens, tails, table, ring, queue, rows, kept, release)
+    want_table, want_ring, want = ref.plan(lens, tails, table, ring, queue, total, kept, release)
     t, r = _i32(table), _i32(ring)
     args = (_i32(lens), _i32(tails), t, r, _i32(queue))
     for _ in range(2):  # the same call again gives the same

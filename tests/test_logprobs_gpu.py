@@ -23,7 +23,8 @@ def _built():
 
 def _reference(x, ids, top):
     x = x.double().cpu()
-    lp = x - torch.logsumexp(x, 1, keepdim=True)
+    z = x - x.amax(1, keepdim=True)  # first: logits as low as -3e38 would swallow the sum's logarithm
+    lp = z - z.exp().sum(1, keepdim=True).log()
     ent = -torch.special.xlogy(lp.exp(), lp.exp()).sum(1)
     pick = torch.where(ids >= 0, lp.gather(1, ids.clamp(min=0).long()), 0.0)
     order = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :top]
