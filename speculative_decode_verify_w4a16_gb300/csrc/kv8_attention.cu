@@ -22,11 +22,15 @@
 // what multiplies the code, and the normaliser adds P / sv, in fp32.
 //
 // Online softmax: m is a reference per row, 7 below the maximum of s + log2 sv
-// when it was last raised; it is raised again only when a weight would pass
-// 2^15 (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is
-// 2^-21 of the largest). One vote per tile over the four warps finds that;
-// the maximum itself, and the rescaling of O^T in TMEM, are computed only then
-// (the first tile, and seldom after it).
+// when it was last set; it is raised again only when a weight would pass 2^15
+// (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is 2^-21
+// of the largest). One vote per tile over the four warps finds that; the
+// maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
+// the first tile of a part, and seldom after it).
+//
+// Code that runs once per part (the query rows, the first maximum, the end) is
+// kept short, in rolled loops: a CTA meets it with cold instruction caches, and
+// straight-line code then costs some 300 cycles per eight instructions.
 //
 // The last tile of bf16 rows, the tail page's (rows 0 .. 63 of the tile) and
 // the tree's own (64 .. 127), comes first in a request's tiles, with bf16
@@ -54,9 +58,8 @@ namespace w4a16 {
 
 constexpr int kKaD = 128;
 constexpr int kKaTile = 128;      // keys per tile
-constexpr float kKaRoom = 7.0f;   // log2 of the largest weight when m is set
+constexpr float kKaRoom = 7.0f;    // log2 of the largest weight when m is set
 constexpr float kKaLimit = 15.0f;  // ... and where m is raised
-constexpr float kKaNone = -1e30f;  // m before any key
 
 struct KaWork {  // the cut of the tiles into runs
   int row_blocks, np, ctas, min_tiles;
@@ -92,30 +95,50 @@ __device__ __forceinline__ bool ka_bar_any(int id, bool p) {
       : "memory");
   return r != 0;
 }
-// float <-> an unsigned that rises with it (NaN never raises a maximum)
-__device__ __forceinline__ unsigned ka_key(float x) {
-  const unsigned b = __float_as_uint(x);
-  return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+// two fp32 lanes in one 64-bit register, for the paired fp32 instructions
+__device__ __forceinline__ uint64_t ka_2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
 }
-__device__ __forceinline__ float ka_unkey(unsigned k) {
-  return k == 0u ? -INFINITY : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+__device__ __forceinline__ void ka_un2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-// Lane 0 waits (bounded), every lane gets the outcome; the first tests do not
-// suspend (these hand-offs are short). Once a wait has run out (ok false) the
-// later ones return at once: the warps that meet at named barriers then walk
-// through the rest of their work, on garbage and in bounds, instead of
-// leaving the others waiting.
+__device__ __forceinline__ uint64_t ka_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t ka_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t ka_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float ka_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __noinline__ bool ka_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
+  return mbar_wait(bar, parity, err);
+}
+// Bounded wait by a whole warp, or by one thread: every lane tests the same
+// barrier. The first tests do not ask the hardware to suspend (these hand-offs
+// are short, and a suspended thread wakes up late). Once a wait has run out
+// (still false) the later ones return at once: the warps that meet at named
+// barriers then walk through the rest of their work, on garbage and in bounds,
+// instead of leaving the others waiting.
 __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, unsigned* err, bool still = true) {
   if (!still) return false;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) {
-    int k = 0;
-    while (k < 64 && !mbar_try_wait(bar, parity)) ++k;
-    if (k == 64) ok = mbar_wait(bar, parity, err) ? 1 : 0;
-  }
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
+#pragma unroll 1
+  for (int k = 0; k < 64; ++k)
+    if (mbar_try_wait(bar, parity)) return true;
+  return ka_wait_long(bar, parity, err);
 }
 
 __device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
@@ -150,13 +173,22 @@ __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSe
   return true;
 }
 
-// run c of C: tiles [c T / C, (c + 1) T / C); as many runs as leave min_tiles
-// tiles each
+// as many runs of the T tiles as leave min_tiles tiles each; run c of them
+// begins at c (T / runs) + min(c, T % runs)
 __device__ __forceinline__ int64_t ka_runs(int64_t T, int ctas, int min_tiles) {
   const int64_t r = T / min_tiles;
   return r < 1 ? 1 : r > ctas ? ctas : r;
 }
-__device__ __forceinline__ int64_t ka_run_begin(int64_t T, int64_t C, int64_t c) { return c * T / C; }
+struct KaCut {
+  int64_t runs, per, rest;
+  __device__ __forceinline__ KaCut(int64_t T, int ctas, int min_tiles)
+      : runs(ka_runs(T, ctas, min_tiles)), per(T / runs), rest(T - per * runs) {}
+  __device__ __forceinline__ int64_t begin(int64_t c) const { return c * per + (c < rest ? c : rest); }
+  __device__ __forceinline__ int64_t owner(int64_t f) const {  // the run that holds tile f
+    const int64_t big = rest * (per + 1);
+    return f < big ? f / (per + 1) : rest + (f - big) / per;
+  }
+};
 
 template <int NP>
 struct KaCfg {
@@ -175,11 +207,11 @@ struct KaCfg {
   static constexpr int kQ8Off = kWOff + 2 * 2 * kTileBytes;   // 2 NP rows of 128 bytes
   static constexpr int kQ16Off = kQ8Off + 2 * NP * 128;       // 2 halves of NP rows of 128 bytes
   static constexpr int kPOff = kQ16Off + 2 * NP * 128;
-  static constexpr int kMaskOff = kPOff + 2 * kPBytes;        // u64 [NP]
-  static constexpr int kGmOff = kMaskOff + NP * 8;            // float2 [NP]: score factor, m
-  static constexpr int kFacOff = kGmOff + NP * 8;             // float [NP]
-  static constexpr int kMaxOff = kFacOff + NP * 4;            // u32 [4][NP], and the sums of the end
-  static constexpr int kRowOff = kMaxOff + NP * 16;           // int [NP]
+  static constexpr int kMaskOff = kPOff + 2 * kPBytes;        // u64 [NP]: nodes a row sees
+  static constexpr int kGmOff = kMaskOff + NP * 8;            // float4 [NP / 2]: g, g, -m, -m of two rows
+  static constexpr int kFacOff = kGmOff + NP * 8;             // float [2][NP]
+  static constexpr int kPartOff = kFacOff + NP * 8;           // float [4][NP]
+  static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
   static constexpr int kBarOff = kRowOff + NP * 4;
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
@@ -189,6 +221,30 @@ struct KaCfg {
   static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
   static_assert(NP % 16 == 0 && kRows % 8 == 0, "row block");
 };
+
+// Values that are not finite, of nodes that a row sees, added to O^T (in TMEM):
+// they were taken out of the products so as not to reach the other rows.
+template <int Q>
+__device__ __noinline__ void ka_add_bad(const Kv8AttnParams& p, int b, int kvh, unsigned long long bad,
+                                        const uint64_t* mask, uint32_t col, int d) {
+#pragma unroll 1
+  for (int q0 = 0; q0 < Q; q0 += 8) {
+    uint32_t o[8];
+    tmem_ld_32x32b<8>(col + (uint32_t)q0, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+#pragma unroll 1
+      for (unsigned long long m = bad & mask[q0 + q]; m; m &= m - 1) {
+        const int j = __ffsll((long long)m) - 1;
+        const float v = __bfloat162float(p.v_new[((int64_t)b * p.n + j) * p.kv_stride + kvh * kKaD + d]);
+        if (!(fabsf(v) < INFINITY)) o[q] = __float_as_uint(__uint_as_float(o[q]) + v);
+      }
+    }
+    tmem_st_32x32b_x8(col + (uint32_t)q0, o);
+  }
+  tmem_wait_st();
+}
 
 struct KaMaps {
   CUtensorMap k, v, k_tail, v_tail, k_new, v_new;
@@ -202,9 +258,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* mask_s = reinterpret_cast<uint64_t*>(smem + C::kMaskOff);
-  float2* gm_s = reinterpret_cast<float2*>(smem + C::kGmOff);
+  float* gm_s = reinterpret_cast<float*>(smem + C::kGmOff);  // row r: g at 4 (r / 2) + r % 2, -m two on
   float* fac_s = reinterpret_cast<float*>(smem + C::kFacOff);
-  unsigned* max_s = reinterpret_cast<unsigned*>(smem + C::kMaxOff);
+  float* part_s = reinterpret_cast<float*>(smem + C::kPartOff);
   int* row_s = reinterpret_cast<int*>(smem + C::kRowOff);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* k_free = k_full + S;
@@ -226,32 +282,65 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   grid_launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_free[s], 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_free[s], 4);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&w_full[k], 4);
+      mbar_init(&s_full[k], 1);
+      mbar_init(&p_full[k], 4 * C::kGroups);
+      mbar_init(&pv_done[k], 1);
+    }
+    mbar_init(q_ready, 4 * C::kGroups);
+    mbar_init(x_full, 1);
+    mbar_init(mma_fin, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(&tmem_s, C::kCols);
+    tmem_relinquish();
+  }
+  if (warp == 3 && lane < 6) tma_prefetch_map(&maps.k + lane);
   grid_dependency_wait();
   // ---- this CTA's run: sums of the requests' tiles
   const int units = p.Hkv * wk.row_blocks;
-  int64_t mine = 0;
-  for (int b = tid; b < p.B; b += C::kThreads) {
-    mine += ka_tiles(ka_len(p, b));
-    if (blockIdx.x == 0) {
-      const int l = p.lens[b];
-      if (l < 0 || l > p.max_len) report_error(p.err, kErrInput);
-    }
+  int n0 = 0;  // request tid's
+  if (tid < p.B) {
+    n0 = ka_tiles(ka_len(p, tid));
+    if (blockIdx.x == 0 && (unsigned)p.lens[tid] > (unsigned)p.max_len) report_error(p.err, kErrInput);
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) scan_s[warp] = mine;
-  __syncthreads();
   int64_t T = 0;
-  for (int w = 0; w < C::kThreads / 32; ++w) T += scan_s[w];
-  T *= units;
-  const int64_t runs = ka_runs(T, wk.ctas, wk.min_tiles);
-  const int64_t f0 = ka_run_begin(T, runs, blockIdx.x), f1 = ka_run_begin(T, runs, (int64_t)blockIdx.x + 1);
-  if (blockIdx.x >= runs) return;
+  auto total = [&](int64_t x) {  // over the CTA
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    __syncthreads();
+    if (lane == 0) scan_s[warp] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) x += scan_s[w];
+    return x;
+  };
+  {
+    int64_t mine = n0;
+    for (int b = tid + C::kThreads; b < p.B; b += C::kThreads) {
+      mine += ka_tiles(ka_len(p, b));
+      if (blockIdx.x == 0 && (unsigned)p.lens[b] > (unsigned)p.max_len) report_error(p.err, kErrInput);
+    }
+    T = total(mine) * units;
+  }
+  const KaCut cut(T, wk.ctas, wk.min_tiles);
+  const int64_t f0 = cut.begin(blockIdx.x), f1 = cut.begin((int64_t)blockIdx.x + 1);
   {
     const int64_t target = f0 / units;  // pre[b] <= target < pre[b + 1]
     int64_t before = 0;
     for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
-      const int b = b0 + tid, n = b < p.B ? ka_tiles(ka_len(p, b)) : 0;
+      const int b = b0 + tid, n = b0 == 0 ? n0 : b < p.B ? ka_tiles(ka_len(p, b)) : 0;
       int x = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -279,44 +368,21 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       if (before > target && blockIdx.x != 0) break;
     }
   }
-  if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_free[s], 1);
-    }
-    for (int s = 0; s < SV; ++s) {
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_free[s], 4);
-    }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&w_full[k], 4);
-      mbar_init(&s_full[k], 1);
-      mbar_init(&p_full[k], 4 * C::kGroups);
-      mbar_init(&pv_done[k], 1);
-    }
-    mbar_init(q_ready, 4 * C::kGroups);
-    mbar_init(x_full, 1);
-    mbar_init(mma_fin, 1);
-    fence_mbarrier_init();
-  }
-  if (warp == 2) {
-    tmem_alloc(&tmem_s, C::kCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
+  // (a CTA past the last run walks over nothing)
   KaIter it;
   {
-    it.left = f1 - f0;
+    it.left = blockIdx.x < cut.runs ? f1 - f0 : 0;
     it.units = units;
-    it.b = s_b;
+    it.b = it.left > 0 ? s_b : 0;
     it.len = ka_len(p, it.b);
     it.nt = ka_tiles(it.len);
-    const int64_t rel = f0 - (int64_t)units * s_pre;
+    const int64_t rel = it.left > 0 ? f0 - (int64_t)units * s_pre : 0;
     it.u = (int)(rel / it.nt);
-    it.tile = (int)(rel % it.nt);
+    it.tile = (int)(rel - (int64_t)it.u * it.nt);
   }
   KaSeg sg;
   int issued = 0;
@@ -332,7 +398,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     int k_more = 0;      // a use of K whose tile was given up
     bool ok = true;
     auto k_wait = [&](int use) {
-      return use < S || mbar_wait(&k_free[use % S], (uint32_t)(use / S - 1) & 1u, p.err);
+      return use < S || ka_wait(&k_free[use % S], (uint32_t)(use / S - 1) & 1u, p.err);
     };
     while (ok && ka_next(p, it, sg)) {
       const int kvh = sg.u / wk.row_blocks;
@@ -388,7 +454,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
             tma_load_3d(kd + 8192, &maps.k, 0, 0, zb, &k_full[ks]);
             k_more = 1;
-            if (vc >= SV) ok = mbar_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
+            if (vc >= SV) ok = ka_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
           }
           if (ok) {
             uint8_t* vd = smem + C::kVOff + vs * C::kTileBytes;
@@ -555,15 +621,17 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           ok = ka_wait(&v_full[s], (uint32_t)(vc / SV) & 1u, p.err, ok);
           ++vc;
           const uint8_t* v = smem + C::kVOff + s * C::kTileBytes;
-          uint4 x[8];
+          uint4 x[4];
+#pragma unroll 1
+          for (int k0 = 0; k0 < 128; k0 += 64) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 16 * k;
+          for (int k = 0; k < 4; ++k) {
+            const int r = k0 + r0 + 16 * k;
             x[k] = *reinterpret_cast<const uint4*>(v + r * 128 + ((c ^ (r & 7)) << 4));
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 16 * k;
+          for (int k = 0; k < 4; ++k) {
+            const int r = k0 + r0 + 16 * k;
             const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             uint32_t o[8];
 #pragma unroll
@@ -585,6 +653,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             *reinterpret_cast<uint4*>(dst + (((c0 + f) ^ sw) << 4)) = f ? hi : lo;
             *reinterpret_cast<uint4*>(dst + (((c0 + (f ^ 1)) ^ sw) << 4)) = f ? lo : hi;
           }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_free[s]);
         }
@@ -603,101 +672,108 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     const int qa = wg * Q;                           // its first row
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
     const int bar = 1 + wg;
+    const int G = p.H / p.Hkv, rows = p.n * G;
+    // a [Q][128] array of the warpgroup over its own chunks of the P buffers
+    // (when no MMA reads them; the other warpgroup may be ahead)
+    auto own = [&](int q) {
+      return reinterpret_cast<float*>(smem + C::kPOff + (q >= Q / 2 ? C::kPBytes : 0) + (qa >> 3) * 2048) +
+             (q % (Q / 2)) * 128;
+    };
     int tc = 0, seg = 0;
     bool ok = true;
     while (ka_next(p, it, sg)) {
       const int kvh = sg.u / wk.row_blocks, rb = sg.u % wk.row_blocks;
-      const int G = p.H / p.Hkv, rows = p.n * G;
-      // ---- Q: 16 lanes a row, 8 columns each, into the two e4m3 terms and bf16
+      // ---- Q: four lanes a row, 32 columns each. x = q 2^ex, |x| < 256, as
+      // bf16 and as two e4m3 terms
       {
-        const int d = (st & 15) * 8;
-        uint4 v[Q / 8];
+        const int r = qa + (st >> 2), R = rb * NP + r, j = R / G, g = R - j * G;
+        const bool have = (st >> 2) < Q && R < rows;
+        uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < Q / 8; ++k) {
-          const int R = rb * NP + qa + 8 * k + (st >> 4);
-          const int j = R / G, g = R - j * G;
-          v[k] = R < rows ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)sg.b * p.n + j) * p.q_stride +
-                                                            (kvh * G + g) * kKaD + d)
-                          : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (sg.lo == 0 && p.parents) {
+        for (int k = 0; k < 4; ++k)
+          v[k] = have ? *(reinterpret_cast<const uint4*>(p.q + ((int64_t)sg.b * p.n + j) * p.q_stride +
+                                                         (kvh * G + g) * kKaD) + 4 * (st & 3) + k)
+                      : make_uint4(0u, 0u, 0u, 0u);
+        if (sg.lo == 0 && p.parents && st < p.n) {
           // the parents (bad ones reported and cut off), for the masks; both
           // warpgroups write the same
-          for (int j = st; j < p.n; j += 128) {
-            int up = p.parents[(int64_t)sg.b * p.n + j];
-            if (j == 0 ? up != -1 : (up < 0 || up >= j)) {
-              report_error(p.err, kErrInput);
-              up = -1;
-            }
-            par_s[j] = up;
+          int up = p.parents[(int64_t)sg.b * p.n + st];
+          if (st == 0 ? up != -1 : (up < 0 || up >= st)) {
+            report_error(p.err, kErrInput);
+            up = -1;
           }
+          par_s[st] = up;
         }
+        unsigned m = 0;
 #pragma unroll
-        for (int k = 0; k < Q / 8; ++k) {
-          const int r = qa + 8 * k + (st >> 4);
+        for (int k = 0; k < 4; ++k) {
           const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          unsigned m = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
             m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
           }
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int ex = min(134 - (int)(m >> 7), 120);  // |q| 2^ex in [128, 256)
+        const float up = __uint_as_float((unsigned)(127 + ex) << 23);
+        const int sw = r & 7;
+        uint8_t* q8 = smem + C::kQ8Off + r * 128;
+        uint8_t* q16 = smem + C::kQ16Off + ((st & 2) ? NP * 128 : 0) + r * 128;
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const int ex = min(134 - (int)(m >> 7), 120);  // |q| 2^ex in [128, 256)
-          const float up = __uint_as_float((unsigned)(127 + ex) << 23);
-          uint32_t t1[2], t2[2];
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t t1[2] = {0u, 0u}, t2[2] = {0u, 0u}, w[4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t a = 0, b = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t u = in[2 * e + h];
-              float x0 = __uint_as_float(u << 16) * up, x1 = __uint_as_float(u & 0xFFFF0000u) * up;
-              if (!(fabsf(x0) < INFINITY)) x0 = NAN;
-              if (!(fabsf(x1) < INFINITY)) x1 = NAN;
-              const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-              const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
-              const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
-                                                           __NV_SATFINITE, __NV_E4M3);
-              a |= c1 << (16 * h);
-              b |= c2 << (16 * h);
-            }
-            t1[e] = a;
-            t2[e] = b;
+          for (int e = 0; e < 4; ++e) {
+            float x0 = __uint_as_float(in[e] << 16) * up, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * up;
+            if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // e4m3 has no infinity; the row is NaN either way
+            if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+            w[e] = ka_bf162(x0, x1);
+            const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+            const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
+            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            t1[e >> 1] |= c1 << (16 * (e & 1));
+            t2[e >> 1] |= c2 << (16 * (e & 1));
           }
-          const int sw = r & 7;
-          uint8_t* q8 = smem + C::kQ8Off + r * 128 + ((((d >> 4) ^ sw) << 4) | (d & 8));
-          *reinterpret_cast<uint2*>(q8) = make_uint2(t1[0], t1[1]);
-          *reinterpret_cast<uint2*>(q8 + NP * 128) = make_uint2(t2[0], t2[1]);
-          *reinterpret_cast<uint4*>(smem + C::kQ16Off + (d >> 6) * NP * 128 + r * 128 + ((((d >> 3) & 7) ^ sw) << 4)) =
-              v[k];
-          if ((st & 15) == 0)
-            gm_s[r] = make_float2(__uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2, kKaNone);
+          if ((st >> 2) < Q) {
+            const int at = (((2 * (st & 3) + (k >> 1)) ^ sw) << 4) | ((k & 1) << 3);
+            *reinterpret_cast<uint2*>(q8 + at) = make_uint2(t1[0], t1[1]);
+            *reinterpret_cast<uint2*>(q8 + NP * 128 + at) = make_uint2(t2[0], t2[1]);
+            *reinterpret_cast<uint4*>(q16 + (((4 * (st & 1) + k) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        ka_bar(bar);
-        if (st < Q) {
-          const int r = qa + st, R = rb * NP + r, j = R / G, g = R - j * G;
+        if ((st & 3) == 0 && (st >> 2) < Q) {
+          gm_s[4 * (r >> 1) + (r & 1)] = __uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2;
+          gm_s[4 * (r >> 1) + 2 + (r & 1)] = 0.0f;
           row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + g : -1;
-          uint64_t m = 0;
-          if (sg.lo == 0 && R < rows) {
-            if (p.parents)
-              for (int k = j; k >= 0; k = par_s[k]) m |= 1ull << k;
-            else
-              m = j == 63 ? ~0ull : (1ull << (j + 1)) - 1ull;
-          }
-          mask_s[r] = m;
         }
         ka_bar(bar);
+        if (sg.lo == 0) {
+          if (st < Q) {
+            const int R2 = rb * NP + qa + st, j2 = R2 / G;
+            uint64_t mk = 0;
+            if (R2 < rows) {
+              if (p.parents)
+                for (int k = j2; k >= 0; k = par_s[k]) mk |= 1ull << k;
+              else
+                mk = j2 == 63 ? ~0ull : (1ull << (j2 + 1)) - 1ull;
+            }
+            mask_s[qa + st] = mk;
+          }
+          ka_bar(bar);
+        }
       }
-      float l[Q];
+      uint64_t l[Q / 2];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) l[q] = 0.0f;
-      // ---- scales of this warp's block of each tile, 32 tiles at a time, the
-      // next ones asked for ahead
+      for (int q = 0; q < Q / 2; ++q) l[q] = 0ull;
+      // ---- scales of this warp's block of each tile, 32 tiles at a time (a
+      // lane a tile), the next ones asked for ahead
       const int half = qd >> 1, full = sg.len / 64, i1 = max(sg.lo, 1);
       const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
       auto page_of = [&](int base) {
@@ -706,94 +782,113 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         const int pg = tab[blk];
         return pg < 0 || pg >= p.pages ? -1 : pg;
       };
-      auto scale_of = [&](int pg, float& sk, float& sv) {
-        sk = pg >= 0 ? p.k_scale[(int64_t)pg * p.Hkv + kvh] : 0.0f;
-        sv = pg >= 0 ? p.v_scale[(int64_t)pg * p.Hkv + kvh] : 1.0f;
-      };
-      int pg = page_of(i1), pg_next = -2;
-      float sk_l, sv_l, sk_n = 0.0f, sv_n = 1.0f;
-      scale_of(pg, sk_l, sv_l);
+      int pg = page_of(i1), pg_n = -2;
+      float sk_l = 0.0f, sv_l = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
+      if (pg >= 0) {
+        sk_l = p.k_scale[(int64_t)pg * p.Hkv + kvh];
+        sv_l = p.v_scale[(int64_t)pg * p.Hkv + kvh];
+      }
+      float lsv_l = log2f(sv_l), isv_l = 1.0f / sv_l;
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
         const int buf = tc & 1;
         const bool bf = i == 0;
-        float sk = 1.0f, sv = 1.0f;
-        bool gone = false;  // this warp's block does not exist
+        float sk = 1.0f, lsv = 0.0f, isv = 1.0f;
+        uint32_t see = ~0u;  // rows for which the thread's key counts
         if (!bf) {
           const int k = (i - i1) & 31;
           if (k == 0 && i > i1) {
-            pg = pg_next;
+            pg = pg_n;
             sk_l = sk_n;
-            sv_l = sv_n;
+            lsv_l = log2f(sv_n);
+            isv_l = 1.0f / sv_n;
           }
-          if (k == 8) pg_next = page_of(i - k + 32);
-          if (k == 20) scale_of(pg_next, sk_n, sv_n);
+          if (k == 8) pg_n = page_of(i + 24);
+          if (k == 20) {
+            sk_n = pg_n >= 0 ? p.k_scale[(int64_t)pg_n * p.Hkv + kvh] : 0.0f;
+            sv_n = pg_n >= 0 ? p.v_scale[(int64_t)pg_n * p.Hkv + kvh] : 1.0f;
+          }
           sk = __shfl_sync(0xffffffffu, sk_l, k);
-          sv = __shfl_sync(0xffffffffu, sv_l, k);
-          gone = __shfl_sync(0xffffffffu, pg, k) == -2;
+          lsv = __shfl_sync(0xffffffffu, lsv_l, k);
+          isv = __shfl_sync(0xffffffffu, isv_l, k);
+          if (__shfl_sync(0xffffffffu, pg, k) == -2) see = 0u;  // no such block
+        } else if (key < 64) {
+          const int tail = p.tails[sg.b];
+          if (key >= (sg.len & 63) || tail < 0 || tail >= p.tail_pages) see = 0u;
+        } else {
+          see = 0u;
+#pragma unroll 1
+          for (int q = 0; q < Q; ++q) see |= (uint32_t)((mask_s[qa + q] >> (key - 64)) & 1ull) << q;
         }
-        const float lsv = bf ? 0.0f : log2f(sv), isv = 1.0f / sv;
         ok = ka_wait(&s_full[buf], (uint32_t)(tc >> 1) & 1u, p.err, ok);
         tc_fence_after();
-        // ---- a = s + log2 sv
-        float a[Q];
+        // ---- t = s + log2 sv - m, two rows an instruction
+        float t[Q];
         const uint32_t sc = trow + (uint32_t)buf * 2u * NP + (uint32_t)qa;
+        const uint64_t sk2 = ka_2(sk, sk), lsv2 = ka_2(lsv, lsv), c32 = ka_2(0.03125f, 0.03125f);
+        const float4* gm = reinterpret_cast<const float4*>(gm_s) + (qa >> 1);
 #pragma unroll
         for (int q0 = 0; q0 < Q; q0 += 8) {
           uint32_t u1[8], u2[8];
           tmem_ld_32x32b<8>(sc + q0, u1);
-          if (!bf) tmem_ld_32x32b<8>(sc + NP + q0, u2);
+          tmem_ld_32x32b<8>(sc + NP + q0, u2);
           tmem_wait_ld();
+          if (bf) {  // one term
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float g = gm_s[qa + q0 + q].x;
-            if (bf)
-              a[q0 + q] = __uint_as_float(u1[q]) * p.scale_log2;
-            else
-              a[q0 + q] = fmaf(fmaf(__uint_as_float(u2[q]), 0.03125f, __uint_as_float(u1[q])), g * sk, lsv);
+            for (int q = 0; q < 8; ++q) u2[q] = 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < 8; q += 2) {
+            const float4 w = gm[(q0 + q) >> 1];
+            const uint64_t x = ka_fma2(ka_2(__uint_as_float(u2[q]), __uint_as_float(u2[q + 1])), c32,
+                                       ka_2(__uint_as_float(u1[q]), __uint_as_float(u1[q + 1])));
+            ka_un2(ka_fma2(x, ka_mul2(ka_2(w.x, w.y), sk2), ka_add2(ka_2(w.z, w.w), lsv2)), t[q0 + q], t[q0 + q + 1]);
           }
         }
-        if (bf) {
-          const int tail = p.tails[sg.b];
-          const bool mine = key < (sg.len & 63) && tail >= 0 && tail < p.tail_pages;
+        if (__any_sync(0xffffffffu, see != ~0u)) {
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const bool see = key < 64 ? mine : (mask_s[qa + q] >> (key - 64)) & 1ull;
-            if (!see) a[q] = -INFINITY;
-          }
-        } else if (gone) {
-#pragma unroll
-          for (int q = 0; q < Q; ++q) a[q] = -INFINITY;
+          for (int q = 0; q < Q; ++q)
+            if (!((see >> q) & 1u)) t[q] = -INFINITY;
         }
-        // ---- does a weight pass the limit?
-        float over = -INFINITY;
+        // ---- is m to be set, or does a weight pass the limit?
+        bool raise = i == sg.lo;
+        if (!raise) {
+          float over = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) over = fmaxf(over, a[q] - gm_s[qa + q].y);
-        if (ka_bar_any(bar, over > kKaLimit)) {
+          for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
+          raise = ka_bar_any(bar, over > kKaLimit);
+        }
+        if (raise) {
+          // P V (i - 1) has left O^T and the P buffers (at a part's first tile
+          // the end of the last part has seen to that)
+          if (i > sg.lo) ok = ka_wait(&pv_done[buf ^ 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+          tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const unsigned m = __reduce_max_sync(0xffffffffu, ka_key(a[q]));
-            if (lane == 0) max_s[qd * NP + qa + q] = m;
+          for (int q = 0; q < Q; ++q) own(q)[key] = t[q];
+          ka_bar(bar);
+          if (lane < Q) {
+            float mx = -INFINITY;
+            const float* x = own(lane);
+#pragma unroll 4
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[32 * (st >> 5) + ((k + lane) & 31)]);
+            part_s[(st >> 5) * NP + qa + lane] = mx;
           }
           ka_bar(bar);
           if (st < Q) {
             const int r = qa + st;
-            const float mx = ka_unkey(max(max(max_s[r], max_s[NP + r]), max(max_s[2 * NP + r], max_s[3 * NP + r])));
-            const float m = gm_s[r].y;
-            float f = 1.0f;
-            if (mx - m > kKaLimit) {
-              const float mn = mx - kKaRoom;
-              f = ka_ex2(m - mn);
-              gm_s[r].y = mn;
-            }
-            fac_s[r] = f;
+            const float mx = fmaxf(fmaxf(part_s[r], part_s[NP + r]), fmaxf(part_s[2 * NP + r], part_s[3 * NP + r]));
+            float d = 0.0f;
+            if (i == sg.lo ? mx > -INFINITY : mx > kKaLimit) d = mx - kKaRoom;
+            gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
+            fac_s[r] = ka_ex2(-d);
+            fac_s[NP + r] = d;
           }
           ka_bar(bar);
 #pragma unroll
-          for (int q = 0; q < Q; ++q) l[q] *= fac_s[qa + q];
+          for (int q = 0; q < Q; ++q) t[q] -= fac_s[NP + qa + q];
           if (i > sg.lo) {
-            // O^T holds the sums up to tile i - 1
-            ok = ka_wait(&pv_done[buf ^ 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
-            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < Q / 2; ++q)
+              l[q] = ka_mul2(l[q], *reinterpret_cast<const uint64_t*>(fac_s + qa + 2 * q));
 #pragma unroll 1
             for (int q0 = 0; q0 < Q; q0 += 8) {
               uint32_t o[8];
@@ -809,76 +904,66 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         // ---- P, into the buffer that P V (i - 2) has left
         if (tc >= 2) ok = ka_wait(&pv_done[buf], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
         uint8_t* pd = smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16;
+        const uint64_t isv2 = ka_2(isv, isv);
 #pragma unroll
         for (int q0 = 0; q0 < Q; q0 += 8) {
-          float e[8];
+          uint32_t w[4];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            e[q] = ka_ex2(a[q0 + q] - gm_s[qa + q0 + q].y);
-            l[q0 + q] = fmaf(e[q], isv, l[q0 + q]);
+          for (int q = 0; q < 4; ++q) {
+            const float e0 = ka_ex2(t[q0 + 2 * q]), e1 = ka_ex2(t[q0 + 2 * q + 1]);
+            l[q0 / 2 + q] = ka_fma2(ka_2(e0, e1), isv2, l[q0 / 2 + q]);
+            w[q] = bf ? ka_bf162(e0, e1) : ka_half2(e0, e1);
           }
-          *reinterpret_cast<uint4*>(pd + (q0 >> 3) * 2048) =
-              bf ? make_uint4(ka_bf162(e[0], e[1]), ka_bf162(e[2], e[3]), ka_bf162(e[4], e[5]), ka_bf162(e[6], e[7]))
-                 : make_uint4(ka_half2(e[0], e[1]), ka_half2(e[2], e[3]), ka_half2(e[4], e[5]), ka_half2(e[6], e[7]));
+          *reinterpret_cast<uint4*>(pd + (q0 >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // ---- the end of the unit's part: the rows' sums over the keys (through
-      // the P buffers, which no MMA reads any more), then O^T
+      // ---- the end of the unit's part: the rows' sums over the keys, then O^T
       ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
       tc_fence_after();
-      // (each warpgroup's own chunks of them: the other one may be ahead)
-      auto sum = [&](int q) {
-        return reinterpret_cast<float*>(smem + C::kPOff + (q >= Q / 2 ? C::kPBytes : 0) + (qa >> 3) * 2048) +
-               (q % (Q / 2)) * 128;
-      };
 #pragma unroll
-      for (int q = 0; q < Q; ++q) sum(q)[key] = l[q];
+      for (int q = 0; q < Q; q += 2) ka_un2(l[q / 2], own(q)[key], own(q + 1)[key]);
       ka_bar(bar);
-      {
-        float* part = reinterpret_cast<float*>(max_s);
-        const int q = st & 31, k0 = (st >> 5) * 32;
-        if (q < Q) {
-          float t = 0.0f;
-          for (int k = 0; k < 32; ++k) t += sum(q)[k0 + ((k + q) & 31)];
-          part[(st >> 5) * NP + qa + q] = t;
-        }
-        ka_bar(bar);
-        if (st < Q) {
-          const int r = qa + st;
-          fac_s[r] = (part[r] + part[NP + r]) + (part[2 * NP + r] + part[3 * NP + r]);
-        }
-        ka_bar(bar);
+      if (lane < Q) {
+        float x = 0.0f;
+        const float* y = own(lane);
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) x += y[32 * (st >> 5) + ((k + lane) & 31)];
+        part_s[(st >> 5) * NP + qa + lane] = x;
       }
+      ka_bar(bar);
       const bool whole = sg.lo == 0 && sg.hi == sg.nt;
       // a cut unit's part: a run's first part in its first slot, else the second
       const int64_t slot = 2 * (int64_t)blockIdx.x + (seg == 0 ? 0 : 1);
+      if (st < Q) {
+        const int r = qa + st;
+        const float x = (part_s[r] + part_s[NP + r]) + (part_s[2 * NP + r] + part_s[3 * NP + r]);
+        if (whole)
+          fac_s[r] = 1.0f / x;
+        else
+          wk.part_ml[slot * NP + r] = make_float2(-gm_s[4 * (r >> 1) + 2 + (r & 1)], x);
+      }
+      ka_bar(bar);
       const unsigned long long bad = sg.lo == 0 ? bad_s[seg & 3] : 0ull;
-      if (!whole && st < Q) wk.part_ml[slot * NP + qa + st] = make_float2(gm_s[qa + st].y, fac_s[qa + st]);
+      if (bad) ka_add_bad<Q>(p, sg.b, kvh, bad, mask_s + qa, trow + C::kOCol + (uint32_t)qa, key);
 #pragma unroll 1
       for (int q0 = 0; q0 < Q; q0 += 8) {
         uint32_t o[8];
         tmem_ld_32x32b<8>(trow + C::kOCol + (uint32_t)(qa + q0), o);
         tmem_wait_ld();
+        const int r = qa + q0;
+        if (whole) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int r = qa + q0 + q;
-          float x = __uint_as_float(o[q]);
-          if (bad & mask_s[r]) {  // values that are not finite, of nodes this row sees
-            for (unsigned long long m = bad & mask_s[r]; m; m &= m - 1) {
-              const int j = __ffsll((long long)m) - 1;
-              const float v = __bfloat162float(p.v_new[((int64_t)sg.b * p.n + j) * p.kv_stride + kvh * kKaD + key]);
-              if (!(fabsf(v) < INFINITY)) x += v;
-            }
-          }
-          if (whole) {
-            if (row_s[r] >= 0) p.out[(int64_t)row_s[r] * kKaD + key] = __float2bfloat16_rn(x / fac_s[r]);
-          } else {
-            wk.part_o[(slot * NP + r) * kKaD + key] = x;
-          }
+          for (int q = 0; q < 8; ++q)
+            if (row_s[r + q] >= 0)
+              p.out[(int64_t)row_s[r + q] * kKaD + key] = __float2bfloat16_rn(__uint_as_float(o[q]) * fac_s[r + q]);
+        } else {
+          float* dst = wk.part_o + (slot * NP + r) * kKaD + key;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q * kKaD] = __uint_as_float(o[q]);
         }
       }
       tc_fence_before();
@@ -913,20 +998,13 @@ __global__ void __launch_bounds__(256) kv8_attention_combine_kernel(const Kv8Att
   const int kvh = rest / rows, R = rest - kvh * rows;
   const int rb = R / wk.np, r = R - rb * wk.np;
   const int64_t T = __ldcg(&wk.pre[p.B]) * units;
-  const int64_t runs = ka_runs(T, wk.ctas, wk.min_tiles);
+  const KaCut cut(T, wk.ctas, wk.min_tiles);
   const int64_t first = __ldcg(&wk.pre[b]), nt = __ldcg(&wk.pre[b + 1]) - first;
   const int64_t u0 = first * units + ((int64_t)kvh * wk.row_blocks + rb) * nt, u1 = u0 + nt;
-  // the run that holds tile f: run c begins at c T / runs
-  auto owner = [&](int64_t f) {
-    int64_t c = f * runs / T;
-    while (ka_run_begin(T, runs, c + 1) <= f) ++c;
-    while (ka_run_begin(T, runs, c) > f) --c;
-    return c;
-  };
-  const int64_t c0 = owner(u0), c1 = owner(u1 - 1);
+  const int64_t c0 = cut.owner(u0), c1 = cut.owner(u1 - 1);
   if (c0 == c1) return;
   // the parts: the first one is its run's first part only if the run begins with it
-  const int64_t s0 = 2 * c0 + (ka_run_begin(T, runs, c0) == u0 ? 0 : 1);
+  const int64_t s0 = 2 * c0 + (cut.begin(c0) == u0 ? 0 : 1);
   float M = -INFINITY;
   for (int64_t c = c0; c <= c1; ++c) {
     const float m = __ldcg(&wk.part_ml[(c == c0 ? s0 : 2 * c) * wk.np + r]).x;
