@@ -13,9 +13,13 @@
 // in [128, 256), which together hold bf16's 8 bits exactly for elements down
 // to 2^-14 of that maximum (absolute error 2^-23 of it below); the terms are
 // separate N columns (S = S1 + S2 / 32), so that K is read from shared memory
-// once. The 8-bit values are widened to fp16, exactly, on their way (shared
-// memory to shared memory), because the softmax weights need more than e4m3
-// holds: P is rounded to fp16 (half a step 2^-11).
+// once. The 8-bit values are widened to fp16, exactly, on their way: four warps
+// read them transposed (ldmatrix on 8-bit elements) and store V^T in TMEM as
+// the A operand, because the softmax weights need more than e4m3 holds (P is
+// rounded to fp16, half a step 2^-11). Through TMEM, not through shared
+// memory: a tile's 32 KB of fp16 written there and read again by the MMAs took
+// most of the shared-memory bandwidth, and an MMA with A in TMEM takes 27
+// cycles instead of 48 (N = 48).
 //
 // A page's scales are powers of two per 64 keys: the keys' multiplies the
 // scores; the values' is added to the exponent. P = 2^(s + log2 sv - m) is
@@ -196,15 +200,14 @@ struct KaCfg {
   static constexpr int kRows = NP / kGroups;
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kThreads = 32 * (kConv0 + 4);
-  // stages of 128 keys (16 KB): the values leave theirs as soon as they are
-  // widened, so theirs is the ring to shorten
-  static constexpr int kStages = NP > 16 ? 3 : 4, kVStages = NP > 48 ? 2 : kStages;
+  // stages of 128 keys (16 KB), as many as fit
+  static constexpr int kStages = NP > 32 ? 4 : NP > 16 ? 5 : 6, kVStages = NP > 48 ? 3 : NP > 16 ? 4 : 5;
   static constexpr int kTileBytes = kKaTile * 128;
   static constexpr int kPBytes = NP * 256;
   static constexpr int kKOff = 0;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kWOff = kVOff + kVStages * kTileBytes;  // two buffers of 16-bit values
-  static constexpr int kQ8Off = kWOff + 2 * 2 * kTileBytes;   // 2 NP rows of 128 bytes
+  static constexpr int kXOff = kVOff + kVStages * kTileBytes;  // a bf16 tile's values: halves of 64 columns
+  static constexpr int kQ8Off = kXOff + 2 * kTileBytes;       // 2 NP rows of 128 bytes
   static constexpr int kQ16Off = kQ8Off + 2 * NP * 128;       // 2 halves of NP rows of 128 bytes
   static constexpr int kPOff = kQ16Off + 2 * NP * 128;
   static constexpr int kMaskOff = kPOff + 2 * kPBytes;        // u64 [NP]: nodes a row sees
@@ -215,9 +218,10 @@ struct KaCfg {
   static constexpr int kBarOff = kRowOff + NP * 4;
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
-  // TMEM columns: scores (two terms) of two tiles, then O^T
-  static constexpr uint32_t kOCol = 4 * NP;
-  static constexpr uint32_t kCols = 5 * NP <= 128 ? 128 : 5 * NP <= 256 ? 256 : 512;
+  // TMEM columns: scores (two terms) of two tiles, O^T, then V^T of two tiles
+  // (fp16 pairs along the keys: 64 columns)
+  static constexpr uint32_t kOCol = 4 * NP, kVCol = 5 * NP;
+  static constexpr uint32_t kCols = 5 * NP + 128 <= 256 ? 256 : 512;
   static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
   static_assert(NP % 16 == 0 && kRows % 8 == 0, "row block");
 };
@@ -392,8 +396,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     // K stages are used in order; a bf16 tile takes two neighbours (32 KB), and
     // passes over the last stage, which has none. Every use of a stage, a
     // passed one too, completes a phase of its full and its free barrier.
-    // (A bf16 tile's values go straight to a 16-bit buffer: the widening warps
-    // ask for them.)
+    // (A bf16 tile's values have a buffer of their own: the widening warps ask
+    // for them.)
     int kc = 0, vc = 0;  // uses of the K and V stages
     int k_more = 0;      // a use of K whose tile was given up
     bool ok = true;
@@ -482,8 +486,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     // --------------------------------------------------------------- MMA
     constexpr uint32_t id_s8 = umma_idesc(2 * NP, (uint32_t)FMT, 0u, 0u, 0u);
     constexpr uint32_t id_s16 = umma_idesc(NP, 1u, 1u, 0u, 0u);
-    constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 1u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
-    const uint32_t kb = smem_u32(smem + C::kKOff), wb = smem_u32(smem + C::kWOff), pb = smem_u32(smem + C::kPOff);
+    constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 0u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
+    const uint32_t kb = smem_u32(smem + C::kKOff), xb = smem_u32(smem + C::kXOff), pb = smem_u32(smem + C::kPOff);
     const uint32_t q8 = smem_u32(smem + C::kQ8Off), q16 = smem_u32(smem + C::kQ16Off);
     int kc = 0, tc = 0, seg = 0;  // K stages, tiles, segments so far
     bool ok = true;
@@ -537,16 +541,23 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t id = i == 0 && sg.lo == 0 ? id_o16 : id_o8;
-        // V^T: 128-byte rows of 64 columns a key, the other 64 columns a half
-        // on; P^T: chunks of 8 rows, 16 bytes a key. 16 keys an MMA.
+        // P^T: chunks of 8 rows, 16 bytes a key. 16 keys an MMA. V^T from TMEM,
+        // or a bf16 tile's from shared memory: 128-byte rows of 64 columns a
+        // key, the other 64 columns a half on
+        const uint32_t bp = pb + (uint32_t)(w * C::kPBytes);
+        if (i == 0 && sg.lo == 0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_ss_warp(tmem + C::kOCol,
-                            umma_desc_sw128_mnmajor(wb + (uint32_t)(w * 2 * C::kTileBytes + 2048 * k),
-                                                    (uint32_t)C::kTileBytes, 1024u),
-                            umma_desc_flat_mnmajor(pb + (uint32_t)(w * C::kPBytes + 256 * k), 128u, 2048u), id,
-                            (i > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ss_warp(tmem + C::kOCol,
+                              umma_desc_sw128_mnmajor(xb + 2048u * (uint32_t)k, (uint32_t)C::kTileBytes, 1024u),
+                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o16, k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ts_warp(tmem + C::kOCol, tmem + C::kVCol + 64u * (uint32_t)w + 8u * (uint32_t)k,
+                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o8,
+                              (i > 0 || k > 0) ? 1u : 0u);
+        }
         umma_commit_warp(&pv_done[w]);
         if (i + 2 < n) ok = issue_s(i + 2);
       }
@@ -555,23 +566,24 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     }
     if (issued) umma_commit_warp(mma_fin);
   } else if (warp >= C::kConv0) {
-    // -------------------------------------------- values to 16-bit, in place
-    // of the tile's order: a thread takes 16 codes (one 16-byte chunk c) of
-    // rows r, r + 16, ..: their 16 fp16 fill two chunks of a half-row. The
-    // chunks of the two halves are stored in opposite order, so that a
-    // quarter-warp's stores fall into different banks.
-    const int ct = tid - 32 * C::kConv0;
-    const int c = ct & 7, r0 = ct >> 3;
-    int vc = 0, tc = 0, xc = 0, seg = 0;
+    // ------------------------------------------------- values to fp16 in TMEM
+    // Warp qd owns the TMEM lanes (columns d of the values) 32 qd .. + 31. A
+    // 16 x 16 ldmatrix of 8-bit elements, transposed, gives a lane the codes of
+    // keys 4 (l % 4) .. + 3 at d = l / 4 and l / 4 + 8: widened, the fragment of
+    // a 16x256b TMEM store of 16 lanes d and 8 columns (16 keys).
+    const int ct = tid - 32 * C::kConv0, qd = warp & 3;
+    int vc = 0, tc = 0, xc = 0, seg = 0, last = -2;  // last: the latest bf16 tile
     bool ok = true;
     while (ka_next(p, it, sg)) {
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
-        uint8_t* w = smem + C::kWOff + (tc & 1) * 2 * C::kTileBytes;
-        // P V (tc - 2) has left the buffer
+        // P V (tc - 2) has left the TMEM buffer
         if (tc >= 2) ok = ka_wait(&pv_done[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
         if (i == 0) {
           const int t = sg.len & 63, tail = p.tails[sg.b];
           const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
+          uint8_t* w = smem + C::kXOff;
+          if (last == tc - 1) ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+          last = tc;
           if (ct == 0) bad_s[seg & 3] = 0ull;
           asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
           if (ct == 0 && ok) {  // (all four warps are past the last such tile)
@@ -616,48 +628,46 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             }
           }
           if (bad) atomicOr(&bad_s[seg & 3], 1ull << (ct - 64));
+          fence_proxy_async_smem();
         } else {
           const int s = vc % SV;
           ok = ka_wait(&v_full[s], (uint32_t)(vc / SV) & 1u, p.err, ok);
           ++vc;
-          const uint8_t* v = smem + C::kVOff + s * C::kTileBytes;
-          uint4 x[4];
-#pragma unroll 1
-          for (int k0 = 0; k0 < 128; k0 += 64) {
+          const uint32_t v = smem_u32(smem + C::kVOff + s * C::kTileBytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = k0 + r0 + 16 * k;
-            x[k] = *reinterpret_cast<const uint4*>(v + r * 128 + ((c ^ (r & 7)) << 4));
-          }
+          for (int dh = 0; dh < 2; ++dh) {
+            uint32_t x[16];  // 16 columns d of 128 keys
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = k0 + r0 + 16 * k;
-            const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              if constexpr (FMT == 0) {
-                const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[m] & 0xFFFFu), __NV_E4M3);
-                const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[m] >> 16), __NV_E4M3);
-                o[2 * m] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-                o[2 * m + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
-              } else {  // e5m2 is the upper byte of fp16
-                o[2 * m] = __byte_perm(in[m], 0u, 0x1404);
-                o[2 * m + 1] = __byte_perm(in[m], 0u, 0x3424);
-              }
+            for (int k = 0; k < 4; ++k) {
+              const int r = 32 * k + lane;
+              ldmatrix_b8_trans_x2(v + (uint32_t)(r * 128 + (((2 * qd + dh) ^ (r & 7)) << 4)), x + 4 * k);
             }
-            uint8_t* dst = w + (c >> 2) * C::kTileBytes + r * 128;
-            const int c0 = (c & 3) * 2, sw = r & 7;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            const int f = c >> 2;  // the second half stores its upper chunk first
-            *reinterpret_cast<uint4*>(dst + (((c0 + f) ^ sw) << 4)) = f ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + (((c0 + (f ^ 1)) ^ sw) << 4)) = f ? lo : hi;
-          }
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) {
+              uint32_t o[16];
+#pragma unroll
+              for (int m = 0; m < 8; ++m) {
+                const uint32_t in = x[8 * kh + m];
+                if constexpr (FMT == 0) {
+                  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in & 0xFFFFu), __NV_E4M3);
+                  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in >> 16), __NV_E4M3);
+                  o[2 * m] = (uint32_t)a.x | ((uint32_t)a.y << 16);
+                  o[2 * m + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
+                } else {  // e5m2 is the upper byte of fp16
+                  o[2 * m] = __byte_perm(in, 0u, 0x1404);
+                  o[2 * m + 1] = __byte_perm(in, 0u, 0x3424);
+                }
+              }
+              tmem_st_16x256b_x4(tmem + ((uint32_t)(32 * qd + 16 * dh) << 16) + C::kVCol +
+                                     64u * (uint32_t)(tc & 1) + 32u * (uint32_t)kh,
+                                 o);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_free[s]);
+          tmem_wait_st();
+          tc_fence_before();
         }
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_full[tc & 1]);
       }

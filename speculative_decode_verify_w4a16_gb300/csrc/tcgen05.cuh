@@ -98,6 +98,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// Two 16 x 16 matrices of 8-bit elements from shared memory, transposed: lane
+// i < 16 gives the address of row i (16 bytes) of the first, lane 16 + i of the
+// second. r[0]: rows 4 (l % 4) .. + 3 of the first at column l / 4, r[1] at
+// column l / 4 + 8; r[2], r[3] of the second.
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // ------------------------------------------------------------------ UMMA
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major,
 // M = 128 (cta_group::1), N = n (multiple of 16, 16..256).
