@@ -424,7 +424,8 @@ w4a16_status kv8_append(const void* k_new, const void* v_new, int64_t row_stride
  *   max_len       an upper bound of lens[] known to the caller;
  *                 max_len / 64 <= max_blocks
  *   workspace     kv8_tree_attention_workspace_bytes() bytes (256-byte
- *                 aligned; may be NULL when that is 0); no initialisation
+ *                 aligned), zero before its first use; every call leaves the
+ *                 counters at its start zero
  * Arithmetic: scores and sums in fp32 (the 8-bit keys enter the tensor cores
  * as they are; q as the sum of two 8-bit terms, exact down to 2^-14 of the
  * row's largest element), the softmax weights rounded to fp16 for the 8-bit

@@ -15,8 +15,9 @@ GROUP = 128
 
 
 def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -24,6 +25,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
+    if (t.dtype == dtype and t.is_contiguous() and (shape is None or t.shape == shape) and t.is_cuda
+            and t.get_device() == torch._C._cuda_getDevice()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
@@ -537,7 +541,7 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     _need(out, "out", torch.bfloat16, (B, n, H, D))
     nbytes = kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, max_len)
     if ws is None and nbytes > 0:
-        ws = workspace(nbytes, q.device, "attention")
+        ws = workspace(nbytes, q.device, "kv8_attention")  # apart from those that need no zeros
     codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
     tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
     check(lib().kv8_tree_attention(

@@ -404,7 +404,7 @@ size_t kv8_tree_attention_workspace_bytes(int B, int n, int H, int Hkv, int D, i
   if (!kv8_attn_shape_ok(B, n, H, Hkv, max_len) || D != 128 || n > 64) return 0;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return 0;
-  return kv8_attention_ws(B, n, H, Hkv, max_len, dev.num_sms);
+  return kv8_attention_ws(n, H, Hkv, dev.num_sms);
 }
 
 w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
@@ -421,7 +421,8 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
       max_blocks < 1 || max_len / 64 > max_blocks || (int64_t)B * max_blocks > INT32_MAX || q_stride < (int64_t)H * D ||
       q_stride % 8 != 0 || kv_stride < (int64_t)Hkv * D || kv_stride % 8 != 0 || !(scale > 0.0f) || !(scale < INFINITY))
     return W4A16_ERR_INVALID_ARG;
-  if (D != 128 || n > 64 || kv_stride > (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
+  if (D != 128 || n > 64 || kv_stride > (int64_t(1) << 31) || !kv8_attention_fits(B, n, H, Hkv, max_len))
+    return W4A16_ERR_UNSUPPORTED;
   const void* wide[] = {q, k_new, v_new, k, v, k_tail, v_tail, out};
   for (const void* a : wide)
     if (!aligned(a, 16)) return W4A16_ERR_INVALID_ARG;
@@ -430,7 +431,7 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
     if (!aligned(a, 4)) return W4A16_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
-  const size_t need = kv8_attention_ws(B, n, H, Hkv, max_len, dev.num_sms);
+  const size_t need = kv8_attention_ws(n, H, Hkv, dev.num_sms);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   Kv8AttnParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);

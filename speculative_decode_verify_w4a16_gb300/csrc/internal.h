@@ -157,7 +157,8 @@ struct Kv8AttnParams {
   __nv_bfloat16* out;  // [B][n][H][D]
   unsigned* err;
 };
-size_t kv8_attention_ws(int B, int n, int H, int Hkv, int max_len, int num_sms);
+size_t kv8_attention_ws(int n, int H, int Hkv, int num_sms);
+bool kv8_attention_fits(int B, int n, int H, int Hkv, int max_len);
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspace, int num_sms, cudaStream_t stream);
 
 // ---- log probabilities of logit rows

@@ -48,7 +48,7 @@
 // tiles. The tiles of all units are laid end to end and cut into one run per
 // SM; a CTA walks over its run, which may end one unit and start others. A
 // unit inside one run is finished there; one that was cut leaves (m, l, O^T)
-// per run, and kv8_attention_combine_kernel merges them.
+// per run, and the CTA that finishes last of them (a counter) merges them.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -67,9 +67,9 @@ constexpr float kKaLimit = 15.0f;  // ... and where m is raised
 
 struct KaWork {  // the cut of the tiles into runs
   int row_blocks, np, ctas, min_tiles;
-  float* part_o;      // [2 ctas][np][D]
-  float2* part_ml;    // [2 ctas][np]
-  int64_t* pre;       // [B + 1]: tiles of one unit of the requests before b
+  int* done;        // [ctas]: finished parts of the cut unit that begins in a run; zero at rest
+  float2* part_ml;  // [2 ctas][np]
+  float* part_o;    // [2 ctas][np][D]
 };
 
 __device__ __forceinline__ float ka_ex2(float x) {
@@ -84,6 +84,15 @@ __device__ __forceinline__ uint32_t ka_half2(float lo, float hi) {
 __device__ __forceinline__ uint32_t ka_bf162(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// four e4m3 codes widened to fp16 (exact)
+__device__ __forceinline__ void ka_widen(uint32_t in, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(in));
 }
 // named barrier over one softmax warpgroup, and the same with a vote
 __device__ __forceinline__ void ka_bar(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -151,20 +160,23 @@ __device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
 }
 __device__ __forceinline__ int ka_tiles(int len) { return 1 + (len / 64 + 1) / 2; }
 
-// One part of a run: tiles lo .. hi - 1 of the nt tiles of unit u of request b
+// One part of a run: tiles lo .. hi - 1 of the nt tiles of unit u of request
+// b; tile lo is tile at of all
 struct KaSeg {
   int b, u, lo, hi, nt, len;
+  unsigned at;
 };
 struct KaIter {
-  int64_t left;
+  unsigned at, left;
   int b, u, tile, units;
   int len, nt;
 };
 __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSeg& s) {
-  if (it.left <= 0 || it.b >= p.B) return false;
-  const int take = (int)min((int64_t)(it.nt - it.tile), it.left);
-  s = KaSeg{it.b, it.u, it.tile, it.tile + take, it.nt, it.len};
+  if (it.left == 0 || it.b >= p.B) return false;
+  const unsigned take = min((unsigned)(it.nt - it.tile), it.left);
+  s = KaSeg{it.b, it.u, it.tile, it.tile + (int)take, it.nt, it.len, it.at};
   it.left -= take;
+  it.at += take;
   it.tile = 0;
   if (++it.u == it.units) {
     it.u = 0;
@@ -177,31 +189,50 @@ __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSe
   return true;
 }
 
-// as many runs of the T tiles as leave min_tiles tiles each; run c of them
-// begins at c (T / runs) + min(c, T % runs)
-__device__ __forceinline__ int64_t ka_runs(int64_t T, int ctas, int min_tiles) {
-  const int64_t r = T / min_tiles;
-  return r < 1 ? 1 : r > ctas ? ctas : r;
-}
+// As many runs of the T tiles as leave min_tiles tiles each; run c of them
+// begins at c (T / runs) + min(c, T % runs). (T < 2^31: the host checks.)
 struct KaCut {
-  int64_t runs, per, rest;
-  __device__ __forceinline__ KaCut(int64_t T, int ctas, int min_tiles)
-      : runs(ka_runs(T, ctas, min_tiles)), per(T / runs), rest(T - per * runs) {}
-  __device__ __forceinline__ int64_t begin(int64_t c) const { return c * per + (c < rest ? c : rest); }
-  __device__ __forceinline__ int64_t owner(int64_t f) const {  // the run that holds tile f
-    const int64_t big = rest * (per + 1);
-    return f < big ? f / (per + 1) : rest + (f - big) / per;
+  unsigned runs, per, rest;
+  __device__ __forceinline__ KaCut(unsigned T, unsigned ctas, unsigned min_tiles) {
+    runs = T / min_tiles;
+    runs = runs < 1u ? 1u : runs > ctas ? ctas : runs;
+    per = T / runs;
+    rest = T - per * runs;
+  }
+  __device__ __forceinline__ unsigned begin(unsigned c) const { return c * per + min(c, rest); }
+  __device__ __forceinline__ unsigned owner(unsigned f) const {  // the run that holds tile f
+    const unsigned big = rest * (per + 1u);
+    return f < big ? f / (per + 1u) : rest + (f - big) / per;
   }
 };
 
+// Sixteen rows, a value each in every lane: reduced over the warp by halving
+// the rows at each exchange; lanes 2 i and 2 i + 1 return row ka_row(lane).
+template <bool MAX>
+__device__ __forceinline__ float ka_reduce16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int h = 8, m = 16; h >= 1; h >>= 1, m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float keep = up ? v[i + h] : v[i], got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + h], m);
+      v[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return MAX ? fmaxf(v[0], got) : v[0] + got;
+}
+__device__ __forceinline__ int ka_row(int lane) {
+  return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+}
+
 template <int NP>
 struct KaCfg {
-  static constexpr int kGroups = NP > 32 ? 2 : 1;  // softmax warpgroups, NP / kGroups rows each
-  static constexpr int kRows = NP / kGroups;
+  static constexpr int kRows = 16, kGroups = NP / kRows;  // softmax warpgroups, 16 rows each
   static constexpr int kSoft0 = 4, kConv0 = 4 + 4 * kGroups;
   static constexpr int kThreads = 32 * (kConv0 + 4);
   // stages of 128 keys (16 KB), as many as fit
-  static constexpr int kStages = NP > 32 ? 4 : NP > 16 ? 5 : 6, kVStages = NP > 48 ? 3 : NP > 16 ? 4 : 5;
+  static constexpr int kStages = NP > 32 ? 4 : 5, kVStages = NP > 48 ? 3 : NP > 16 ? 4 : 5;
   static constexpr int kTileBytes = kKaTile * 128;
   static constexpr int kPBytes = NP * 256;
   static constexpr int kKOff = 0;
@@ -210,10 +241,10 @@ struct KaCfg {
   static constexpr int kQ8Off = kXOff + 2 * kTileBytes;       // 2 NP rows of 128 bytes
   static constexpr int kQ16Off = kQ8Off + 2 * NP * 128;       // 2 halves of NP rows of 128 bytes
   static constexpr int kPOff = kQ16Off + 2 * NP * 128;
-  static constexpr int kMaskOff = kPOff + 2 * kPBytes;        // u64 [NP]: nodes a row sees
+  static constexpr int kZeroOff = kPOff + 2 * kPBytes;        // 1 KB of zeros (8 rows of 128 bytes)
+  static constexpr int kMaskOff = kZeroOff + 1024;            // u64 [NP]: nodes a row sees
   static constexpr int kGmOff = kMaskOff + NP * 8;            // float4 [NP / 2]: g, g, -m, -m of two rows
-  static constexpr int kFacOff = kGmOff + NP * 8;             // float [2][NP]
-  static constexpr int kPartOff = kFacOff + NP * 8;           // float [4][NP]
+  static constexpr int kPartOff = kGmOff + NP * 8;            // float [4][NP]
   static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
   static constexpr int kBarOff = kRowOff + NP * 4;
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11;
@@ -223,7 +254,7 @@ struct KaCfg {
   static constexpr uint32_t kOCol = 4 * NP, kVCol = 5 * NP;
   static constexpr uint32_t kCols = 5 * NP + 128 <= 256 ? 256 : 512;
   static_assert(kTotal + 1024 <= 227 * 1024, "shared memory");
-  static_assert(NP % 16 == 0 && kRows % 8 == 0, "row block");
+  static_assert(NP % 16 == 0 && NP <= 64, "row block");
 };
 
 // Values that are not finite, of nodes that a row sees, added to O^T (in TMEM):
@@ -250,6 +281,47 @@ __device__ __noinline__ void ka_add_bad(const Kv8AttnParams& p, int b, int kvh, 
   tmem_wait_st();
 }
 
+// barrier over all softmax warpgroups
+template <int GROUPS>
+__device__ __forceinline__ void ka_bar_all() {
+  asm volatile("barrier.cta.sync 9, %0;" ::"n"(128 * GROUPS) : "memory");
+}
+
+// The parts of a cut unit merged: the first in slot s0, that of run c0 + k in
+// slot 2 (c0 + k). A thread takes column d of its warpgroup's 16 rows; lane l
+// holds the maxima and sums of row l % 16.
+template <int NP>
+__device__ __noinline__ void ka_merge(const Kv8AttnParams& p, const KaWork& wk, unsigned s0, unsigned c0,
+                                      unsigned parts, int qa, int d, int lane, const int* row) {
+  const int r = qa + (lane & 15);
+  float M = -INFINITY;
+#pragma unroll 4
+  for (unsigned k = 0; k < parts; ++k)
+    M = fmaxf(M, __ldcg(&wk.part_ml[(k ? 2u * (c0 + k) : s0) * NP + r]).x);
+  float l = 0.0f, o[16];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) o[q] = 0.0f;
+#pragma unroll 1
+  for (unsigned k = 0; k < parts; ++k) {
+    const unsigned slot = k ? 2u * (c0 + k) : s0;
+    const float* src = wk.part_o + ((size_t)slot * NP + qa) * kKaD + d;
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) x[q] = __ldcg(src + q * kKaD);
+    const float2 ml = __ldcg(&wk.part_ml[slot * NP + r]);
+    const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);
+    l = fmaf(w, ml.y, l);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) o[q] = fmaf(__shfl_sync(0xffffffffu, w, q), x[q], o[q]);
+  }
+  const float inv = 1.0f / l;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float x = o[q] * __shfl_sync(0xffffffffu, inv, q);
+    if (row[qa + q] >= 0) p.out[(int64_t)row[qa + q] * kKaD + d] = __float2bfloat16_rn(x);
+  }
+}
+
 struct KaMaps {
   CUtensorMap k, v, k_tail, v_tail, k_new, v_new;
 };
@@ -263,7 +335,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* mask_s = reinterpret_cast<uint64_t*>(smem + C::kMaskOff);
   float* gm_s = reinterpret_cast<float*>(smem + C::kGmOff);  // row r: g at 4 (r / 2) + r % 2, -m two on
-  float* fac_s = reinterpret_cast<float*>(smem + C::kFacOff);
   float* part_s = reinterpret_cast<float*>(smem + C::kPartOff);
   int* row_s = reinterpret_cast<int*>(smem + C::kRowOff);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
@@ -278,9 +349,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
   uint64_t* mma_fin = x_full + 1;
   __shared__ uint32_t tmem_s;
-  __shared__ int64_t scan_s[32];
-  __shared__ int64_t s_pre;
-  __shared__ int s_b;
+  __shared__ unsigned scan_s[32];
+  __shared__ unsigned s_pre;
+  __shared__ int s_b, s_last;
   __shared__ int par_s[64];
   __shared__ unsigned long long bad_s[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -310,7 +381,11 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     tmem_alloc(&tmem_s, C::kCols);
     tmem_relinquish();
   }
-  if (warp == 3 && lane < 6) tma_prefetch_map(&maps.k + lane);
+  if (warp == 3) {
+    if (lane < 6) tma_prefetch_map(&maps.k + lane);
+    for (int k = lane; k < 64; k += 32) reinterpret_cast<uint4*>(smem + C::kZeroOff)[k] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   grid_dependency_wait();
   // ---- this CTA's run: sums of the requests' tiles
   const int units = p.Hkv * wk.row_blocks;
@@ -319,57 +394,44 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     n0 = ka_tiles(ka_len(p, tid));
     if (blockIdx.x == 0 && (unsigned)p.lens[tid] > (unsigned)p.max_len) report_error(p.err, kErrInput);
   }
-  int64_t T = 0;
-  auto total = [&](int64_t x) {  // over the CTA
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    __syncthreads();
-    if (lane == 0) scan_s[warp] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) x += scan_s[w];
-    return x;
-  };
+  unsigned T;
   {
-    int64_t mine = n0;
+    unsigned x = (unsigned)n0;
+#pragma unroll 1
     for (int b = tid + C::kThreads; b < p.B; b += C::kThreads) {
-      mine += ka_tiles(ka_len(p, b));
+      x += (unsigned)ka_tiles(ka_len(p, b));
       if (blockIdx.x == 0 && (unsigned)p.lens[b] > (unsigned)p.max_len) report_error(p.err, kErrInput);
     }
-    T = total(mine) * units;
+    x = __reduce_add_sync(0xffffffffu, x);
+    if (lane == 0) scan_s[warp] = x;
+    __syncthreads();
+    x = lane < C::kThreads / 32 ? scan_s[lane] : 0u;
+    T = __reduce_add_sync(0xffffffffu, x) * (unsigned)units;
   }
-  const KaCut cut(T, wk.ctas, wk.min_tiles);
-  const int64_t f0 = cut.begin(blockIdx.x), f1 = cut.begin((int64_t)blockIdx.x + 1);
+  const KaCut runs(T, (unsigned)wk.ctas, (unsigned)wk.min_tiles);
+  const unsigned f0 = runs.begin(blockIdx.x), f1 = runs.begin(blockIdx.x + 1u);
   {
-    const int64_t target = f0 / units;  // pre[b] <= target < pre[b + 1]
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
+    const unsigned target = f0 / (unsigned)units;  // tiles of one unit of the requests before b <= target
+    unsigned before = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B && before <= target; b0 += C::kThreads) {
       const int b = b0 + tid, n = b0 == 0 ? n0 : b < p.B ? ka_tiles(ka_len(p, b)) : 0;
-      int x = n;
+      unsigned x = (unsigned)n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
       }
       __syncthreads();
       if (lane == 31) scan_s[warp] = x;
       __syncthreads();
-      int64_t at = before + x - n;
-      for (int w = 0; w < C::kThreads / 32; ++w) {
-        if (w < warp) at += scan_s[w];
-        before += scan_s[w];
+      const unsigned w = lane < C::kThreads / 32 ? scan_s[lane] : 0u;
+      const unsigned at = before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + x - (unsigned)n;
+      before += __reduce_add_sync(0xffffffffu, w);
+      if (b < p.B && target >= at && target < at + (unsigned)n) {
+        s_b = b;
+        s_pre = at;
       }
-      if (b < p.B) {
-        if (target >= at && target < at + n) {
-          s_b = b;
-          s_pre = at;
-        }
-        if (blockIdx.x == 0) {  // for the merging of cut units
-          wk.pre[b] = at;
-          if (b == p.B - 1) wk.pre[p.B] = at + n;
-        }
-      }
-      if (before > target && blockIdx.x != 0) break;
     }
   }
   tc_fence_before();
@@ -379,14 +441,15 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   // (a CTA past the last run walks over nothing)
   KaIter it;
   {
-    it.left = blockIdx.x < cut.runs ? f1 - f0 : 0;
+    it.at = f0;
+    it.left = blockIdx.x < runs.runs ? f1 - f0 : 0u;
     it.units = units;
     it.b = it.left > 0 ? s_b : 0;
     it.len = ka_len(p, it.b);
     it.nt = ka_tiles(it.len);
-    const int64_t rel = it.left > 0 ? f0 - (int64_t)units * s_pre : 0;
-    it.u = (int)(rel / it.nt);
-    it.tile = (int)(rel - (int64_t)it.u * it.nt);
+    const unsigned rel = it.left > 0 ? f0 - (unsigned)units * s_pre : 0u;
+    it.u = (int)(rel / (unsigned)it.nt);
+    it.tile = (int)rel - it.u * it.nt;
   }
   KaSeg sg;
   int issued = 0;
@@ -489,7 +552,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 0u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
     const uint32_t kb = smem_u32(smem + C::kKOff), xb = smem_u32(smem + C::kXOff), pb = smem_u32(smem + C::kPOff);
     const uint32_t q8 = smem_u32(smem + C::kQ8Off), q16 = smem_u32(smem + C::kQ16Off);
-    int kc = 0, tc = 0, seg = 0;  // K stages, tiles, segments so far
+    const uint64_t zero = umma_desc_sw128_kmajor(smem_u32(smem + C::kZeroOff)) & ~((uint64_t)0x3FFFu << 32);
+    int kc = 0, tc = 0, seg = 0;  // K stages, tiles, parts so far
     bool ok = true;
     while (ok && ka_next(p, it, sg)) {
       ok = ka_wait(q_ready, (uint32_t)seg & 1u, p.err);
@@ -517,6 +581,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             umma_bf16_ss_warp(d, umma_desc_sw128_kmajor(a + (uint32_t)((k >> 2) * C::kTileBytes + 32 * (k & 3))),
                               umma_desc_sw128_kmajor(q16 + (uint32_t)((k >> 2) * NP * 128 + 32 * (k & 3))), id_s16,
                               k > 0 ? 1u : 0u);
+          // the second term's columns: zeros (one 8-row group of zeros stands
+          // for all of both operands: stride 0)
+          umma_bf16_ss_warp(d + NP, zero, zero, id_s16, 0u);
           umma_commit_warp(&k_free[s]);
           umma_commit_warp(&k_free[s + 1]);
           kc += 2;
@@ -585,7 +652,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           if (last == tc - 1) ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
           last = tc;
           if (ct == 0) bad_s[seg & 3] = 0ull;
-          asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+          asm volatile("barrier.cta.sync 8, 128;" ::: "memory");  // (ids 1 .. 4 and 9: the softmax)
           if (ct == 0 && ok) {  // (all four warps are past the last such tile)
             const int kvh = sg.u / wk.row_blocks;
             mbar_arrive_expect_tx(x_full, (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
@@ -649,10 +716,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
               for (int m = 0; m < 8; ++m) {
                 const uint32_t in = x[8 * kh + m];
                 if constexpr (FMT == 0) {
-                  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in & 0xFFFFu), __NV_E4M3);
-                  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in >> 16), __NV_E4M3);
-                  o[2 * m] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-                  o[2 * m + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
+                  ka_widen(in, o[2 * m], o[2 * m + 1]);
                 } else {  // e5m2 is the upper byte of fp16
                   o[2 * m] = __byte_perm(in, 0u, 0x1404);
                   o[2 * m + 1] = __byte_perm(in, 0u, 0x3424);
@@ -683,30 +747,31 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
     const int bar = 1 + wg;
     const int G = p.H / p.Hkv, rows = p.n * G;
-    // a [Q][128] array of the warpgroup over its own chunks of the P buffers
-    // (when no MMA reads them; the other warpgroup may be ahead)
-    auto own = [&](int q) {
-      return reinterpret_cast<float*>(smem + C::kPOff + (q >= Q / 2 ? C::kPBytes : 0) + (qa >> 3) * 2048) +
-             (q % (Q / 2)) * 128;
+    const float4* gm = reinterpret_cast<const float4*>(gm_s) + (qa >> 1);
+    // the query row of a part that the thread loads: eight lanes a row, 16
+    // columns each
+    auto load_q = [&](const KaSeg& g, uint4 (&v)[2]) {
+      const int kvh = g.u / wk.row_blocks, R = (g.u - kvh * wk.row_blocks) * NP + qa + (st >> 3), j = R / G;
+      v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (R < rows) {
+        const uint4* at = reinterpret_cast<const uint4*>(p.q + ((int64_t)g.b * p.n + j) * p.q_stride +
+                                                         (kvh * G + R - j * G) * kKaD) + 2 * (st & 7);
+        v[0] = at[0];
+        v[1] = at[1];
+      }
     };
     int tc = 0, seg = 0;
     bool ok = true;
-    while (ka_next(p, it, sg)) {
-      const int kvh = sg.u / wk.row_blocks, rb = sg.u % wk.row_blocks;
-      // ---- Q: four lanes a row, 32 columns each. x = q 2^ex, |x| < 256, as
-      // bf16 and as two e4m3 terms
+    uint4 v[2];
+    bool more = ka_next(p, it, sg);
+    if (more) load_q(sg, v);
+    while (more) {
+      const int kvh = sg.u / wk.row_blocks, rb = sg.u - kvh * wk.row_blocks;
+      // ---- Q: x = q 2^ex, |x| < 256, as bf16 and as two e4m3 terms
       {
-        const int r = qa + (st >> 2), R = rb * NP + r, j = R / G, g = R - j * G;
-        const bool have = (st >> 2) < Q && R < rows;
-        uint4 v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = have ? *(reinterpret_cast<const uint4*>(p.q + ((int64_t)sg.b * p.n + j) * p.q_stride +
-                                                         (kvh * G + g) * kKaD) + 4 * (st & 3) + k)
-                      : make_uint4(0u, 0u, 0u, 0u);
         if (sg.lo == 0 && p.parents && st < p.n) {
-          // the parents (bad ones reported and cut off), for the masks; both
-          // warpgroups write the same
+          // the parents (bad ones reported and cut off), for the masks; every
+          // warpgroup writes the same
           int up = p.parents[(int64_t)sg.b * p.n + st];
           if (st == 0 ? up != -1 : (up < 0 || up >= st)) {
             report_error(p.err, kErrInput);
@@ -714,65 +779,58 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           }
           par_s[st] = up;
         }
+        const int r = qa + (st >> 3), c = st & 7, sw = r & 7;
+        const uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
         unsigned m = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
-            m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-          }
+        for (int e = 0; e < 8; ++e) {
+          const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
+          m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
         }
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int ex = min(134 - (int)(m >> 7), 120);  // |q| 2^ex in [128, 256)
         const float up = __uint_as_float((unsigned)(127 + ex) << 23);
-        const int sw = r & 7;
-        uint8_t* q8 = smem + C::kQ8Off + r * 128;
-        uint8_t* q16 = smem + C::kQ16Off + ((st & 2) ? NP * 128 : 0) + r * 128;
+        uint32_t t1[4], t2[4], w[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          uint32_t t1[2] = {0u, 0u}, t2[2] = {0u, 0u}, w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x0 = __uint_as_float(in[e] << 16) * up, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * up;
-            if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // e4m3 has no infinity; the row is NaN either way
-            if (!(fabsf(x1) < INFINITY)) x1 = NAN;
-            w[e] = ka_bf162(x0, x1);
-            const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-            const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
-            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            t1[e >> 1] |= c1 << (16 * (e & 1));
-            t2[e >> 1] |= c2 << (16 * (e & 1));
-          }
-          if ((st >> 2) < Q) {
-            const int at = (((2 * (st & 3) + (k >> 1)) ^ sw) << 4) | ((k & 1) << 3);
-            *reinterpret_cast<uint2*>(q8 + at) = make_uint2(t1[0], t1[1]);
-            *reinterpret_cast<uint2*>(q8 + NP * 128 + at) = make_uint2(t2[0], t2[1]);
-            *reinterpret_cast<uint4*>(q16 + (((4 * (st & 1) + k) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int e = 0; e < 8; ++e) {
+          float x0 = __uint_as_float(in[e] << 16) * up, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * up;
+          if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // e4m3 has no infinity; the row is NaN either way
+          if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+          w[e] = ka_bf162(x0, x1);
+          const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+          const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
+          const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
+                                                       __NV_SATFINITE, __NV_E4M3);
+          t1[e >> 1] = (e & 1) ? t1[e >> 1] | (c1 << 16) : c1;
+          t2[e >> 1] = (e & 1) ? t2[e >> 1] | (c2 << 16) : c2;
         }
+        uint8_t* q8 = smem + C::kQ8Off + r * 128 + ((c ^ sw) << 4);
+        uint8_t* q16 = smem + C::kQ16Off + (c >> 2) * NP * 128 + r * 128;
+        *reinterpret_cast<uint4*>(q8) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        *reinterpret_cast<uint4*>(q8 + NP * 128) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        *reinterpret_cast<uint4*>(q16 + (((2 * (c & 3)) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(q16 + (((2 * (c & 3) + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
-        if ((st & 3) == 0 && (st >> 2) < Q) {
+        if (c == 0) {
+          const int R = rb * NP + r, j = R / G;
           gm_s[4 * (r >> 1) + (r & 1)] = __uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2;
           gm_s[4 * (r >> 1) + 2 + (r & 1)] = 0.0f;
-          row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + g : -1;
+          row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + R - j * G : -1;
         }
         ka_bar(bar);
         if (sg.lo == 0) {
           if (st < Q) {
-            const int R2 = rb * NP + qa + st, j2 = R2 / G;
+            const int R = rb * NP + qa + st, j = R / G;
             uint64_t mk = 0;
-            if (R2 < rows) {
+            if (R < rows) {
               if (p.parents)
-                for (int k = j2; k >= 0; k = par_s[k]) mk |= 1ull << k;
+#pragma unroll 1
+                for (int k = j; k >= 0; k = par_s[k]) mk |= 1ull << k;
               else
-                mk = j2 == 63 ? ~0ull : (1ull << (j2 + 1)) - 1ull;
+                mk = j == 63 ? ~0ull : (1ull << (j + 1)) - 1ull;
             }
             mask_s[qa + st] = mk;
           }
@@ -792,21 +850,21 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         const int pg = tab[blk];
         return pg < 0 || pg >= p.pages ? -1 : pg;
       };
-      int pg = page_of(i1), pg_n = -2;
-      float sk_l = 0.0f, sv_l = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
-      if (pg >= 0) {
-        sk_l = p.k_scale[(int64_t)pg * p.Hkv + kvh];
-        sv_l = p.v_scale[(int64_t)pg * p.Hkv + kvh];
+      int pg = 0, pg_n = page_of(i1);
+      float sk_l = 0.0f, lsv_l = 0.0f, isv_l = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
+      if (pg_n >= 0) {
+        sk_n = p.k_scale[(int64_t)pg_n * p.Hkv + kvh];
+        sv_n = p.v_scale[(int64_t)pg_n * p.Hkv + kvh];
       }
-      float lsv_l = log2f(sv_l), isv_l = 1.0f / sv_l;
+#pragma unroll 1
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
         const int buf = tc & 1;
         const bool bf = i == 0;
         float sk = 1.0f, lsv = 0.0f, isv = 1.0f;
-        uint32_t see = ~0u;  // rows for which the thread's key counts
+        uint32_t see = 0xFFFFu;  // rows for which the thread's key counts
         if (!bf) {
           const int k = (i - i1) & 31;
-          if (k == 0 && i > i1) {
+          if (k == 0) {
             pg = pg_n;
             sk_l = sk_n;
             lsv_l = log2f(sv_n);
@@ -835,17 +893,12 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         float t[Q];
         const uint32_t sc = trow + (uint32_t)buf * 2u * NP + (uint32_t)qa;
         const uint64_t sk2 = ka_2(sk, sk), lsv2 = ka_2(lsv, lsv), c32 = ka_2(0.03125f, 0.03125f);
-        const float4* gm = reinterpret_cast<const float4*>(gm_s) + (qa >> 1);
 #pragma unroll
         for (int q0 = 0; q0 < Q; q0 += 8) {
           uint32_t u1[8], u2[8];
           tmem_ld_32x32b<8>(sc + q0, u1);
           tmem_ld_32x32b<8>(sc + NP + q0, u2);
           tmem_wait_ld();
-          if (bf) {  // one term
-#pragma unroll
-            for (int q = 0; q < 8; ++q) u2[q] = 0u;
-          }
 #pragma unroll
           for (int q = 0; q < 8; q += 2) {
             const float4 w = gm[(q0 + q) >> 1];
@@ -854,7 +907,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             ka_un2(ka_fma2(x, ka_mul2(ka_2(w.x, w.y), sk2), ka_add2(ka_2(w.z, w.w), lsv2)), t[q0 + q], t[q0 + q + 1]);
           }
         }
-        if (__any_sync(0xffffffffu, see != ~0u)) {
+        if (__any_sync(0xffffffffu, see != 0xFFFFu)) {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
             if (!((see >> q) & 1u)) t[q] = -INFINITY;
@@ -868,95 +921,94 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           raise = ka_bar_any(bar, over > kKaLimit);
         }
         if (raise) {
-          // P V (i - 1) has left O^T and the P buffers (at a part's first tile
-          // the end of the last part has seen to that)
-          if (i > sg.lo) ok = ka_wait(&pv_done[buf ^ 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
-          tc_fence_after();
+          {
+            float x[Q];
 #pragma unroll
-          for (int q = 0; q < Q; ++q) own(q)[key] = t[q];
-          ka_bar(bar);
-          if (lane < Q) {
-            float mx = -INFINITY;
-            const float* x = own(lane);
-#pragma unroll 4
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[32 * (st >> 5) + ((k + lane) & 31)]);
-            part_s[(st >> 5) * NP + qa + lane] = mx;
+            for (int q = 0; q < Q; ++q) x[q] = t[q];
+            const float mx = ka_reduce16<true>(x, lane);
+            if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = mx;
           }
           ka_bar(bar);
-          if (st < Q) {
-            const int r = qa + st;
-            const float mx = fmaxf(fmaxf(part_s[r], part_s[NP + r]), fmaxf(part_s[2 * NP + r], part_s[3 * NP + r]));
-            float d = 0.0f;
-            if (i == sg.lo ? mx > -INFINITY : mx > kKaLimit) d = mx - kKaRoom;
-            gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
-            fac_s[r] = ka_ex2(-d);
-            fac_s[NP + r] = d;
-          }
-          ka_bar(bar);
+          const int r = qa + (lane & 15);  // a lane's row from here on
+          const float mx = fmaxf(fmaxf(part_s[r], part_s[NP + r]), fmaxf(part_s[2 * NP + r], part_s[3 * NP + r]));
+          float d = 0.0f;
+          if (i == sg.lo ? mx > -INFINITY : mx > kKaLimit) d = mx - kKaRoom;
+          const float f = ka_ex2(-d);
+          if (qd == 0 && lane < 16) gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
 #pragma unroll
-          for (int q = 0; q < Q; ++q) t[q] -= fac_s[NP + qa + q];
+          for (int q = 0; q < Q; ++q) t[q] -= __shfl_sync(0xffffffffu, d, q);
           if (i > sg.lo) {
 #pragma unroll
-            for (int q = 0; q < Q / 2; ++q)
-              l[q] = ka_mul2(l[q], *reinterpret_cast<const uint64_t*>(fac_s + qa + 2 * q));
+            for (int q = 0; q < Q; q += 2)
+              l[q / 2] = ka_mul2(l[q / 2], ka_2(__shfl_sync(0xffffffffu, f, q), __shfl_sync(0xffffffffu, f, q + 1)));
+            // O^T holds the sums up to tile i - 1
+            ok = ka_wait(&pv_done[buf ^ 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+            tc_fence_after();
 #pragma unroll 1
             for (int q0 = 0; q0 < Q; q0 += 8) {
               uint32_t o[8];
               tmem_ld_32x32b<8>(trow + C::kOCol + (uint32_t)(qa + q0), o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * fac_s[qa + q0 + q]);
+              for (int q = 0; q < 8; ++q)
+                o[q] = __float_as_uint(__uint_as_float(o[q]) * __shfl_sync(0xffffffffu, f, q0 + q));
               tmem_st_32x32b_x8(trow + C::kOCol + (uint32_t)(qa + q0), o);
             }
             tmem_wait_st();
           }
+          ka_bar(bar);  // the new m, and part_s read
         }
         // ---- P, into the buffer that P V (i - 2) has left
         if (tc >= 2) ok = ka_wait(&pv_done[buf], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
-        uint8_t* pd = smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16;
+        uint4* pd = reinterpret_cast<uint4*>(smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16);
         const uint64_t isv2 = ka_2(isv, isv);
 #pragma unroll
-        for (int q0 = 0; q0 < Q; q0 += 8) {
-          uint32_t w[4];
+        for (int q = 0; q < Q; q += 2) {
+          t[q] = ka_ex2(t[q]);
+          t[q + 1] = ka_ex2(t[q + 1]);
+          l[q / 2] = ka_fma2(ka_2(t[q], t[q + 1]), isv2, l[q / 2]);
+        }
+        if (bf) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float e0 = ka_ex2(t[q0 + 2 * q]), e1 = ka_ex2(t[q0 + 2 * q + 1]);
-            l[q0 / 2 + q] = ka_fma2(ka_2(e0, e1), isv2, l[q0 / 2 + q]);
-            w[q] = bf ? ka_bf162(e0, e1) : ka_half2(e0, e1);
-          }
-          *reinterpret_cast<uint4*>(pd + (q0 >> 3) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int q = 0; q < Q; q += 8)
+            pd[q * 16] = make_uint4(ka_bf162(t[q], t[q + 1]), ka_bf162(t[q + 2], t[q + 3]), ka_bf162(t[q + 4], t[q + 5]),
+                                    ka_bf162(t[q + 6], t[q + 7]));
+        } else {
+#pragma unroll
+          for (int q = 0; q < Q; q += 8)
+            pd[q * 16] = make_uint4(ka_half2(t[q], t[q + 1]), ka_half2(t[q + 2], t[q + 3]), ka_half2(t[q + 4], t[q + 5]),
+                                    ka_half2(t[q + 6], t[q + 7]));
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // ---- the end of the unit's part: the rows' sums over the keys, then O^T
-      ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
-      tc_fence_after();
+      // ---- the end of the unit's part: the rows' sums over the keys, then
+      // O^T. The next part's query rows are asked for first.
+      KaSeg nx;
+      more = ka_next(p, it, nx);
+      if (more) load_q(nx, v);
+      {
+        float x[Q];
 #pragma unroll
-      for (int q = 0; q < Q; q += 2) ka_un2(l[q / 2], own(q)[key], own(q + 1)[key]);
-      ka_bar(bar);
-      if (lane < Q) {
-        float x = 0.0f;
-        const float* y = own(lane);
-#pragma unroll 4
-        for (int k = 0; k < 32; ++k) x += y[32 * (st >> 5) + ((k + lane) & 31)];
-        part_s[(st >> 5) * NP + qa + lane] = x;
+        for (int q = 0; q < Q; q += 2) ka_un2(l[q / 2], x[q], x[q + 1]);
+        const float y = ka_reduce16<false>(x, lane);
+        if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = y;
       }
       ka_bar(bar);
+      float inv;  // of a lane's row
       const bool whole = sg.lo == 0 && sg.hi == sg.nt;
       // a cut unit's part: a run's first part in its first slot, else the second
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (seg == 0 ? 0 : 1);
-      if (st < Q) {
-        const int r = qa + st;
-        const float x = (part_s[r] + part_s[NP + r]) + (part_s[2 * NP + r] + part_s[3 * NP + r]);
-        if (whole)
-          fac_s[r] = 1.0f / x;
-        else
-          wk.part_ml[slot * NP + r] = make_float2(-gm_s[4 * (r >> 1) + 2 + (r & 1)], x);
+      const unsigned slot = 2u * blockIdx.x + (seg == 0 ? 0u : 1u);
+      {
+        const int r = qa + (lane & 15);
+        const float y = (part_s[r] + part_s[NP + r]) + (part_s[2 * NP + r] + part_s[3 * NP + r]);
+        inv = 1.0f / y;
+        if (!whole && st < Q) wk.part_ml[slot * NP + r] = make_float2(-gm_s[4 * (r >> 1) + 2 + (r & 1)], y);
       }
-      ka_bar(bar);
+      ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
+      tc_fence_after();
       const unsigned long long bad = sg.lo == 0 ? bad_s[seg & 3] : 0ull;
       if (bad) ka_add_bad<Q>(p, sg.b, kvh, bad, mask_s + qa, trow + C::kOCol + (uint32_t)qa, key);
 #pragma unroll 1
@@ -967,17 +1019,35 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         const int r = qa + q0;
         if (whole) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (row_s[r + q] >= 0)
-              p.out[(int64_t)row_s[r + q] * kKaD + key] = __float2bfloat16_rn(__uint_as_float(o[q]) * fac_s[r + q]);
+          for (int q = 0; q < 8; ++q) {
+            const float x = __uint_as_float(o[q]) * __shfl_sync(0xffffffffu, inv, q0 + q);
+            if (row_s[r + q] >= 0) p.out[(int64_t)row_s[r + q] * kKaD + key] = __float2bfloat16_rn(x);
+          }
         } else {
-          float* dst = wk.part_o + (slot * NP + r) * kKaD + key;
+          float* dst = wk.part_o + ((size_t)slot * NP + r) * kKaD + key;
 #pragma unroll
           for (int q = 0; q < 8; ++q) dst[q * kKaD] = __uint_as_float(o[q]);
         }
       }
+      if (!whole) {
+        // ---- the last of the unit's CTAs merges the parts
+        const unsigned u0 = sg.at - (unsigned)sg.lo;  // the unit's first tile
+        const unsigned c0 = runs.owner(u0), parts = runs.owner(u0 + (unsigned)sg.nt - 1u) - c0 + 1u;
+        __threadfence();
+        ka_bar_all<C::kGroups>();
+        if (warp == C::kSoft0 && lane == 0) {
+          s_last = atomic_add_acq_rel(&wk.done[c0], 1) == (int)parts - 1;
+          if (s_last) wk.done[c0] = 0;
+        }
+        ka_bar_all<C::kGroups>();
+        // the first part is its run's first only if the run begins with it
+        if (s_last)
+          ka_merge<NP>(p, wk, 2u * c0 + (runs.begin(c0) == u0 ? 0u : 1u), c0, parts, qa, key, lane, row_s);
+        ka_bar_all<C::kGroups>();
+      }
       tc_fence_before();
       ka_bar(bar);  // the small arrays are free for the next part
+      sg = nx;
       ++seg;
     }
   }
@@ -994,70 +1064,31 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   }
 }
 
-// One warp per query row: the parts of a unit that was cut over several runs,
-// merged and stored as bf16 (lane k: columns 4 k .. 4 k + 3). A unit inside
-// one run was finished there.
-__global__ void __launch_bounds__(256) kv8_attention_combine_kernel(const Kv8AttnParams p, const KaWork wk) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int G = p.H / p.Hkv, rows = p.n * G, units = p.Hkv * wk.row_blocks;
-  const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (id >= (int64_t)p.B * p.Hkv * rows) return;
-  const int b = (int)(id / ((int64_t)p.Hkv * rows)), rest = (int)(id - (int64_t)b * p.Hkv * rows);
-  const int kvh = rest / rows, R = rest - kvh * rows;
-  const int rb = R / wk.np, r = R - rb * wk.np;
-  const int64_t T = __ldcg(&wk.pre[p.B]) * units;
-  const KaCut cut(T, wk.ctas, wk.min_tiles);
-  const int64_t first = __ldcg(&wk.pre[b]), nt = __ldcg(&wk.pre[b + 1]) - first;
-  const int64_t u0 = first * units + ((int64_t)kvh * wk.row_blocks + rb) * nt, u1 = u0 + nt;
-  const int64_t c0 = cut.owner(u0), c1 = cut.owner(u1 - 1);
-  if (c0 == c1) return;
-  // the parts: the first one is its run's first part only if the run begins with it
-  const int64_t s0 = 2 * c0 + (cut.begin(c0) == u0 ? 0 : 1);
-  float M = -INFINITY;
-  for (int64_t c = c0; c <= c1; ++c) {
-    const float m = __ldcg(&wk.part_ml[(c == c0 ? s0 : 2 * c) * wk.np + r]).x;
-    M = m > M ? m : M;
-  }
-  float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t c = c0; c <= c1; ++c) {
-    const int64_t at = (c == c0 ? s0 : 2 * c) * wk.np + r;
-    const float2 ml = __ldcg(&wk.part_ml[at]);
-    const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);
-    l = fmaf(w, ml.y, l);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(wk.part_o + at * kKaD) + lane);
-    o[0] = fmaf(w, v.x, o[0]);
-    o[1] = fmaf(w, v.y, o[1]);
-    o[2] = fmaf(w, v.z, o[2]);
-    o[3] = fmaf(w, v.w, o[3]);
-  }
-  const int j = R / G, g = R - j * G;
-  const float inv = 1.0f / l;
-  __nv_bfloat16* dst = p.out + (((int64_t)b * p.n + j) * p.H + kvh * G + g) * kKaD + 4 * lane;
-  *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
-  *reinterpret_cast<__nv_bfloat162*>(dst + 2) = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-}
-
 // ------------------------------------------------------------------ host
 struct KaPlan {
   int np, row_blocks, ctas;
-  size_t o_bytes, ml_bytes, total;
+  size_t done_bytes, ml_bytes, total;
 };
-static KaPlan ka_plan(int B, int n, int H, int Hkv, int num_sms) {
+static KaPlan ka_plan(int n, int H, int Hkv, int num_sms) {
   KaPlan k;
   const int rows = n * (H / Hkv);
   // row blocks of at most 64 rows, all of the same size up to a multiple of 16
   k.row_blocks = (rows + 63) / 64;
   k.np = ((rows + k.row_blocks - 1) / k.row_blocks + 15) / 16 * 16;
   k.ctas = num_sms > 0 ? num_sms : 1;
-  k.o_bytes = (size_t)2 * k.ctas * k.np * kKaD * 4;
+  k.done_bytes = ((size_t)k.ctas * 4 + 255) / 256 * 256;
   k.ml_bytes = (size_t)2 * k.ctas * k.np * 8;
-  k.total = k.o_bytes + k.ml_bytes + ((size_t)B + 1) * 8;
+  k.total = k.done_bytes + k.ml_bytes + (size_t)2 * k.ctas * k.np * kKaD * 4;
   return k;
 }
 
-size_t kv8_attention_ws(int B, int n, int H, int Hkv, int, int num_sms) { return ka_plan(B, n, H, Hkv, num_sms).total; }
+size_t kv8_attention_ws(int n, int H, int Hkv, int num_sms) { return ka_plan(n, H, Hkv, num_sms).total; }
+
+// an upper bound of the tiles of all units
+bool kv8_attention_fits(int B, int n, int H, int Hkv, int max_len) {
+  const int64_t rb = ((int64_t)n * (H / Hkv) + 63) / 64;
+  return (double)B * Hkv * rb * ((double)max_len / 128.0 + 2.0) < 2147483648.0;
+}
 
 template <int NP, int FMT>
 static cudaError_t launch_ka(const KaMaps& maps, const Kv8AttnParams& p, const KaWork& wk, cudaStream_t stream) {
@@ -1072,7 +1103,7 @@ static cudaError_t launch_ka(const KaMaps& maps, const Kv8AttnParams& p, const K
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspace, int num_sms, cudaStream_t stream) {
   auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
   if (!encode) return cudaErrorNotSupported;
-  const KaPlan k = ka_plan(p.B, p.n, p.H, p.Hkv, num_sms);
+  const KaPlan k = ka_plan(p.n, p.H, p.Hkv, num_sms);
   KaMaps maps;
   const cuuint32_t es[4] = {1u, 1u, 1u, 1u};
   auto map = [&](CUtensorMap* m, CUtensorMapDataType t, int rank, const void* base, const cuuint64_t* dims,
@@ -1108,19 +1139,15 @@ cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspac
   wk.ctas = k.ctas;
   wk.min_tiles = 2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  wk.part_o = reinterpret_cast<float*>(ws);
-  wk.part_ml = reinterpret_cast<float2*>(ws + k.o_bytes);
-  wk.pre = reinterpret_cast<int64_t*>(ws + k.o_bytes + k.ml_bytes);
-  cudaError_t e;
+  wk.done = reinterpret_cast<int*>(ws);
+  wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
+  wk.part_o = reinterpret_cast<float*>(ws + k.done_bytes + k.ml_bytes);
   switch (k.np) {
-    case 16: e = fmt ? launch_ka<16, 1>(maps, p, wk, stream) : launch_ka<16, 0>(maps, p, wk, stream); break;
-    case 32: e = fmt ? launch_ka<32, 1>(maps, p, wk, stream) : launch_ka<32, 0>(maps, p, wk, stream); break;
-    case 48: e = fmt ? launch_ka<48, 1>(maps, p, wk, stream) : launch_ka<48, 0>(maps, p, wk, stream); break;
-    default: e = fmt ? launch_ka<64, 1>(maps, p, wk, stream) : launch_ka<64, 0>(maps, p, wk, stream); break;
+    case 16: return fmt ? launch_ka<16, 1>(maps, p, wk, stream) : launch_ka<16, 0>(maps, p, wk, stream);
+    case 32: return fmt ? launch_ka<32, 1>(maps, p, wk, stream) : launch_ka<32, 0>(maps, p, wk, stream);
+    case 48: return fmt ? launch_ka<48, 1>(maps, p, wk, stream) : launch_ka<48, 0>(maps, p, wk, stream);
+    default: return fmt ? launch_ka<64, 1>(maps, p, wk, stream) : launch_ka<64, 0>(maps, p, wk, stream);
   }
-  if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)p.B * p.n * p.H;
-  return launch_pdl(kv8_attention_combine_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p, wk);
 }
 
 }  // namespace w4a16

@@ -470,7 +470,7 @@ def test_attention_is_the_same_each_time_and_on_another_stream():
     run = lambda **kw: sv.kv8_tree_attention(*dq, c, 0, table, lens, tails, max_len=3000, **kw)
     first = run().cpu()
     s = torch.cuda.Stream()
-    ws = torch.empty(sv.kv8_tree_attention_workspace_bytes(B, n, H, Hkv, 128, 3000) + 256, dtype=torch.uint8, device=dev())
+    ws = torch.zeros(sv.kv8_tree_attention_workspace_bytes(B, n, H, Hkv, 128, 3000) + 256, dtype=torch.uint8, device=dev())
     s.wait_stream(torch.cuda.current_stream())
     for _ in range(3):
         assert torch.equal(run().cpu(), first)
@@ -503,7 +503,7 @@ def test_a_step_replayed_from_a_graph():
     k, v = (torch.zeros(B, n, Hkv, D, dtype=torch.bfloat16, device=dev()) for _ in range(2))
     node, out = _i32(np.zeros(B)), torch.empty_like(q)
     plan = sv.kv_block_plan(lens, tails, table, ring, queue, accepted_node=node, n=n)
-    ws = torch.empty(sv.kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, 250) + 256, dtype=torch.uint8, device=dev())
+    ws = torch.zeros(sv.kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, 250) + 256, dtype=torch.uint8, device=dev())
 
     def step():
         sv.kv8_tree_attention(q, k, v, cache, 0, table, lens, tails, max_len=250, out=out, ws=ws)
