@@ -247,7 +247,7 @@ struct KaCfg {
   static constexpr int kPartOff = kGmOff + NP * 8;            // float [4][NP]
   static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
   static constexpr int kBarOff = kRowOff + NP * 4;
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 11;
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
   // TMEM columns: scores (two terms) of two tiles, O^T, then V^T of two tiles
   // (fp16 pairs along the keys: 64 columns)
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint64_t* pv_done = p_full + 2;  // [2]
   uint64_t* q_ready = pv_done + 2;
   uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
-  uint64_t* mma_fin = x_full + 1;
+  uint64_t* s_free = x_full + 1;   // [2] scores read
+  uint64_t* mma_fin = s_free + 2;  // [2]
   __shared__ uint32_t tmem_s;
   __shared__ unsigned scan_s[32];
   __shared__ unsigned s_pre;
@@ -371,10 +372,11 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       mbar_init(&s_full[k], 1);
       mbar_init(&p_full[k], 4 * C::kGroups);
       mbar_init(&pv_done[k], 1);
+      mbar_init(&s_free[k], 4 * C::kGroups);
+      mbar_init(&mma_fin[k], 1);
     }
     mbar_init(q_ready, 4 * C::kGroups);
     mbar_init(x_full, 1);
-    mbar_init(mma_fin, 1);
     fence_mbarrier_init();
   }
   if (warp == 2) {
@@ -546,36 +548,71 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       for (int u = vc > SV ? vc - SV : 0; u < vc; ++u) mbar_wait(&v_full[u % SV], (uint32_t)(u / SV) & 1u, p.err);
     }
   } else if (warp == 1) {
-    // --------------------------------------------------------------- MMA
+    // ------------------------------------------------------------ O^T MMAs
+    constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 0u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
+    const uint32_t xb = smem_u32(smem + C::kXOff), pb = smem_u32(smem + C::kPOff);
+    int tc = 0;  // tiles so far
+    bool ok = true;
+    while (ok && ka_next(p, it, sg)) {
+#pragma unroll 1
+      for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
+        const int w = tc & 1;
+        const uint32_t ph = (uint32_t)(tc >> 1) & 1u;
+        ok = ka_wait(&w_full[w], ph, p.err) && ka_wait(&p_full[w], ph, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        // P^T: chunks of 8 rows, 16 bytes a key. 16 keys an MMA. V^T from TMEM,
+        // or a bf16 tile's from shared memory: 128-byte rows of 64 columns a
+        // key, the other 64 columns a half on
+        const uint32_t bp = pb + (uint32_t)(w * C::kPBytes);
+        if (i == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ss_warp(tmem + C::kOCol,
+                              umma_desc_sw128_mnmajor(xb + 2048u * (uint32_t)k, (uint32_t)C::kTileBytes, 1024u),
+                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o16, k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_bf16_ts_warp(tmem + C::kOCol, tmem + C::kVCol + 64u * (uint32_t)w + 8u * (uint32_t)k,
+                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o8,
+                              (i > sg.lo || k > 0) ? 1u : 0u);
+        }
+        umma_commit_warp(&pv_done[w]);
+        issued = 1;
+      }
+    }
+    if (issued) umma_commit_warp(&mma_fin[0]);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ S^T MMAs
+    // (a warp of its own: a tile's scores go out as soon as the scores two
+    // tiles before have been read, whatever P V waits for)
     constexpr uint32_t id_s8 = umma_idesc(2 * NP, (uint32_t)FMT, 0u, 0u, 0u);
     constexpr uint32_t id_s16 = umma_idesc(NP, 1u, 1u, 0u, 0u);
-    constexpr uint32_t id_o8 = umma_idesc(NP, 0u, 0u, 0u, 1u), id_o16 = umma_idesc(NP, 1u, 1u, 1u, 1u);
-    const uint32_t kb = smem_u32(smem + C::kKOff), xb = smem_u32(smem + C::kXOff), pb = smem_u32(smem + C::kPOff);
+    const uint32_t kb = smem_u32(smem + C::kKOff);
     const uint32_t q8 = smem_u32(smem + C::kQ8Off), q16 = smem_u32(smem + C::kQ16Off);
     const uint64_t zero = umma_desc_sw128_kmajor(smem_u32(smem + C::kZeroOff)) & ~((uint64_t)0x3FFFu << 32);
     int kc = 0, tc = 0, seg = 0;  // K stages, tiles, parts so far
     bool ok = true;
     while (ok && ka_next(p, it, sg)) {
       ok = ka_wait(q_ready, (uint32_t)seg & 1u, p.err);
-      tc_fence_after();
-      const int n = sg.hi - sg.lo, t0 = tc;
-      // S of tile i (its scores' buffer was read before P of tile i - 2 was
-      // ready, which P V (i - 2) waited for)
-      auto issue_s = [&](int i) {
-        const uint32_t d = tmem + (uint32_t)((t0 + i) & 1) * 2u * NP;
-        const bool first = i == 0 && sg.lo == 0;
-        if (first && kc % S == S - 1) {  // the stage that the producer passed over
-          if (!ka_wait(&k_full[S - 1], (uint32_t)(kc / S) & 1u, p.err)) return false;
+#pragma unroll 1
+      for (int i = sg.lo; ok && i < sg.hi; ++i, ++tc) {
+        const uint32_t d = tmem + (uint32_t)(tc & 1) * 2u * NP;
+        if (tc >= 2) ok = ka_wait(&s_free[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err);
+        if (i == 0 && kc % S == S - 1) {  // the stage that the producer passed over
+          ok = ka_wait(&k_full[S - 1], (uint32_t)(kc / S) & 1u, p.err, ok);
           umma_commit_warp(&k_free[S - 1]);
-          issued = 1;
           ++kc;
         }
         const int s = kc % S;
-        if (!ka_wait(&k_full[s], (uint32_t)(kc / S) & 1u, p.err)) return false;
-        if (first && !ka_wait(&k_full[s + 1], (uint32_t)((kc + 1) / S) & 1u, p.err)) return false;
+        ok = ka_wait(&k_full[s], (uint32_t)(kc / S) & 1u, p.err, ok);
+        if (i == 0) ok = ka_wait(&k_full[s + 1], (uint32_t)((kc + 1) / S) & 1u, p.err, ok);
+        issued = 1;
+        if (!ok) break;
         tc_fence_after();
         const uint32_t a = kb + (uint32_t)s * C::kTileBytes;
-        if (first) {
+        if (i == 0) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             umma_bf16_ss_warp(d, umma_desc_sw128_kmajor(a + (uint32_t)((k >> 2) * C::kTileBytes + 32 * (k & 3))),
@@ -595,43 +632,11 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           umma_commit_warp(&k_free[s]);
           ++kc;
         }
-        umma_commit_warp(&s_full[(t0 + i) & 1]);
-        issued = 1;
-        return true;
-      };
-      for (int i = 0; ok && i < 2 && i < n; ++i) ok = issue_s(i);
-      for (int i = 0; ok && i < n; ++i) {
-        const int w = (t0 + i) & 1;
-        const uint32_t ph = (uint32_t)((t0 + i) >> 1) & 1u;
-        if (!ka_wait(&w_full[w], ph, p.err) || !ka_wait(&p_full[w], ph, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        // P^T: chunks of 8 rows, 16 bytes a key. 16 keys an MMA. V^T from TMEM,
-        // or a bf16 tile's from shared memory: 128-byte rows of 64 columns a
-        // key, the other 64 columns a half on
-        const uint32_t bp = pb + (uint32_t)(w * C::kPBytes);
-        if (i == 0 && sg.lo == 0) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_ss_warp(tmem + C::kOCol,
-                              umma_desc_sw128_mnmajor(xb + 2048u * (uint32_t)k, (uint32_t)C::kTileBytes, 1024u),
-                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o16, k > 0 ? 1u : 0u);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16_ts_warp(tmem + C::kOCol, tmem + C::kVCol + 64u * (uint32_t)w + 8u * (uint32_t)k,
-                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o8,
-                              (i > 0 || k > 0) ? 1u : 0u);
-        }
-        umma_commit_warp(&pv_done[w]);
-        if (i + 2 < n) ok = issue_s(i + 2);
+        umma_commit_warp(&s_full[tc & 1]);
       }
-      tc += n;
       ++seg;
     }
-    if (issued) umma_commit_warp(mma_fin);
+    if (issued) umma_commit_warp(&mma_fin[1]);
   } else if (warp >= C::kConv0) {
     // ------------------------------------------------- values to fp16 in TMEM
     // Warp qd owns the TMEM lanes (columns d of the values) 32 qd .. + 31. A
@@ -907,6 +912,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             ka_un2(ka_fma2(x, ka_mul2(ka_2(w.x, w.y), sk2), ka_add2(ka_2(w.z, w.w), lsv2)), t[q0 + q], t[q0 + q + 1]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[buf]);
         if (__any_sync(0xffffffffu, see != 0xFFFFu)) {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
@@ -1055,7 +1063,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   // ---------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && lane == 0 && issued) mbar_wait(mma_fin, 0u, p.err);  // no MMA in flight when TMEM is freed
+  // no MMA in flight when TMEM is freed
+  if ((warp == 1 || warp == 3) && lane == 0 && issued) mbar_wait(&mma_fin[warp >> 1], 0u, p.err);
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
