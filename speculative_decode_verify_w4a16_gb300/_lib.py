@@ -82,6 +82,9 @@ def _load(path: str):
 def lib():
     """The loaded library (built in-tree by __graft_entry__.build())."""
     global _lib
+    L = _lib
+    if L is not None:
+        return L
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -5,6 +5,7 @@ CUDA stream; every step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -13,20 +14,23 @@ from ._lib import W4A16Error, check, lib
 
 GROUP = 128
 
+_device = torch._C._cuda_getDevice  # the current device's index
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
-    if (t.dtype == dtype and t.is_contiguous() and (shape is None or t.shape == shape) and t.is_cuda
-            and t.get_device() == torch._C._cuda_getDevice()):
+    if (t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.get_device() == _device()
+            and (shape is None or t.shape == shape)):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -48,10 +52,11 @@ _ws_cache: dict = {}
 def workspace(nbytes: int, device: Optional[torch.device] = None, key: str = "default") -> torch.Tensor:
     """A zero-filled scratch buffer of at least nbytes on `device`, cached per
     (device, key). The kernels leave it zeroed after every call."""
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    k = (dev.index if dev.index is not None else torch.cuda.current_device(), key)
+    index = None if device is None else (device if isinstance(device, torch.device) else torch.device(device)).index
+    k = (_device() if index is None else index, key)
     buf = _ws_cache.get(k)
     if buf is None or buf.numel() < nbytes:
+        dev = torch.device("cuda", k[0])
         buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
         _ws_cache[k] = buf
     return buf
@@ -375,35 +380,42 @@ def kv8_cache(layers: int, pages: int, B: int, Hkv: int, D: int = 128, dtype: to
 
 
 def _need_cache(c: KV8Cache):
-    layers, pages, Hkv, block, D = c.k.shape
-    if c.k.dtype not in _KV8_FORMATS:
+    k = c.k
+    shape = k.shape
+    layers, pages, Hkv, block, D = shape
+    dtype = k.dtype
+    if dtype not in _KV8_FORMATS:
         raise ValueError("the cache's codes must be torch.float8_e4m3fn or torch.float8_e5m2")
     if block != KV_BLOCK:
         raise ValueError(f"a page holds {KV_BLOCK} tokens, the cache has {block}")
-    _need(c.k, "cache.k", c.k.dtype)
-    _need(c.v, "cache.v", c.k.dtype, c.k.shape)
-    _need(c.k_scale, "cache.k_scale", torch.float32, (layers, pages, Hkv))
-    _need(c.v_scale, "cache.v_scale", torch.float32, (layers, pages, Hkv))
+    _need(k, "cache.k", dtype)
+    _need(c.v, "cache.v", dtype, shape)
+    _need(c.k_scale, "cache.k_scale", torch.float32, shape[:3])
+    _need(c.v_scale, "cache.v_scale", torch.float32, shape[:3])
     tail_pages = c.k_tail.shape[1]
-    _need(c.k_tail, "cache.k_tail", torch.bfloat16, (layers, tail_pages, Hkv, KV_BLOCK, D))
-    _need(c.v_tail, "cache.v_tail", torch.bfloat16, (layers, tail_pages, Hkv, KV_BLOCK, D))
+    tail = (layers, tail_pages, Hkv, KV_BLOCK, D)
+    _need(c.k_tail, "cache.k_tail", torch.bfloat16, tail)
+    _need(c.v_tail, "cache.v_tail", torch.bfloat16, tail)
     return layers, pages, tail_pages, Hkv, D
 
 
 def _need_rows(t: torch.Tensor, name: str, shape) -> int:
-    """A bf16 tensor [..., heads, D] whose heads are dense and whose tokens are
-    evenly apart (a slice of a fused projection); returns that stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    """A bf16 tensor [.., tokens, heads, D] whose heads are dense and whose
+    tokens are evenly apart, over all leading dimensions but a layer's (a
+    slice of a fused projection); returns the tokens' stride."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or t.get_device() != _device():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != _device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
+        if t.dtype is not torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    tokens, (H, D) = t.shape[-3], t.shape[-2:]
-    stride = t.stride(-3) if tokens > 1 else (t.stride(-4) if t.dim() > 3 and t.shape[-4] > 1 else H * D)
-    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+    outer, tokens, H, D = shape
+    so, stride, sh, sd = t.stride()
+    if tokens == 1:
+        stride = so if outer > 1 else H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     if stride < H * D or stride % 8 != 0:
         raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart and not overlap")
@@ -421,51 +433,59 @@ def kv_block_plan(lens: torch.Tensor, tails: torch.Tensor, block_table: torch.Te
     tree_parents int32 [B, n] or None for the chain). block_table int32
     [B, max_blocks] and free_ring int32 [cap] are updated in place; lens,
     tails and queue are not (the plan holds their next values)."""
-    _need(lens, "lens", torch.int32)
-    B = lens.numel()
-    _need(lens, "lens", torch.int32, (B,))
-    _need(tails, "tails", torch.int32, (B,))
-    _need(block_table, "block_table", torch.int32)
+    i32 = torch.int32
+    B = lens.shape[0] if lens.dim() == 1 else lens.numel()
+    vec = (B,)
+    _need(lens, "lens", i32, vec)
+    _need(tails, "tails", i32, vec)
+    _need(block_table, "block_table", i32)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
-    _need(free_ring, "free_ring", torch.int32, (free_ring.numel(),))
-    _need(queue, "queue", torch.int32, (3,))
+    cap = free_ring.numel()
+    _need(free_ring, "free_ring", i32, (cap,))
+    _need(queue, "queue", i32, (3,))
     if (row_start is None) == (accepted_node is None):
         raise ValueError("give row_start (ragged rows) or accepted_node (a draft's accepted path)")
     if row_start is not None:
-        _need(row_start, "row_start", torch.int32, (B + 1,))
+        _need(row_start, "row_start", i32, (B + 1,))
         if rows is None:
             raise ValueError("rows (an upper bound of row_start[B]) is required with row_start")
         if tree_parents is not None:
             raise ValueError("tree_parents goes with accepted_node")
         rows, n = int(rows), 0
     else:
-        _need(accepted_node, "accepted_node", torch.int32, (B,))
+        _need(accepted_node, "accepted_node", i32, vec)
         if tree_parents is not None:
             n = tree_parents.shape[-1] if n is None else n
-            _need(tree_parents, "tree_parents", torch.int32, (B, n))
+            _need(tree_parents, "tree_parents", i32, (B, n))
         if n is None:
             raise ValueError("n is required for a sequence draft")
-        rows = B * int(n)
+        n = int(n)
+        rows = B * n
     if release is not None:
-        _need(release, "release", torch.int32, (B,))
+        _need(release, "release", i32, vec)
     if plan is None:
         sizes = (B, B, B + 1, 3, max(rows, 1), max(rows, 1))
-        plan = BlockPlan(*(torch.empty(s, dtype=torch.int32, device=lens.device) for s in sizes))
-    _need(plan.new_lens, "plan.new_lens", torch.int32, (B,))
-    _need(plan.new_tails, "plan.new_tails", torch.int32, (B,))
-    _need(plan.new_start, "plan.new_start", torch.int32, (B + 1,))
-    _need(plan.queue, "plan.queue", torch.int32, (3,))
+        plan = BlockPlan(*(torch.empty(s, dtype=i32, device=lens.device) for s in sizes))
+    _need(plan.new_lens, "plan.new_lens", i32, vec)
+    _need(plan.new_tails, "plan.new_tails", i32, vec)
+    _need(plan.new_start, "plan.new_start", i32, (B + 1,))
+    _need(plan.queue, "plan.queue", i32, (3,))
+    _need_plan_rows(plan, rows)
+    check(lib().kv_block_plan(lens.data_ptr(), tails.data_ptr(), _ptr(row_start), _ptr(tree_parents),
+                              _ptr(accepted_node), _ptr(release), B, n, rows, block_table.shape[1], cap,
+                              block_table.data_ptr(), free_ring.data_ptr(), queue.data_ptr(),
+                              plan.new_lens.data_ptr(), plan.new_tails.data_ptr(), plan.new_start.data_ptr(),
+                              plan.queue.data_ptr(), plan.src_rows.data_ptr(), plan.slots.data_ptr(),
+                              _stream(stream)), "kv_block_plan")
+    return plan
+
+
+def _need_plan_rows(plan: BlockPlan, rows: int):
     for t, name in ((plan.src_rows, "plan.src_rows"), (plan.slots, "plan.slots")):
         _need(t, name, torch.int32)
         if t.numel() < rows:
             raise ValueError(f"{name} must hold {rows} rows, has {t.numel()}")
-    check(lib().kv_block_plan(_ptr(lens), _ptr(tails), _ptr(row_start), _ptr(tree_parents), _ptr(accepted_node),
-                              _ptr(release), B, int(n), rows, block_table.shape[1], free_ring.numel(),
-                              _ptr(block_table), _ptr(free_ring), _ptr(queue), _ptr(plan.new_lens),
-                              _ptr(plan.new_tails), _ptr(plan.new_start), _ptr(plan.queue), _ptr(plan.src_rows),
-                              _ptr(plan.slots), _stream(stream)), "kv_block_plan")
-    return plan
 
 
 def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails: torch.Tensor, plan: BlockPlan,
@@ -477,25 +497,33 @@ def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails:
     if k_new.dim() == 3:
         k_new, v_new = k_new.unsqueeze(0), v_new.unsqueeze(0)
     rows = k_new.shape[1]
-    stride = _need_rows(k_new, "k_new", (layers, rows, Hkv, D))
-    if _need_rows(v_new, "v_new", (layers, rows, Hkv, D)) != stride:
+    shape = (layers, rows, Hkv, D)
+    stride = _need_rows(k_new, "k_new", shape)
+    _need_rows(v_new, "v_new", shape)
+    if layers * rows > 1 and k_new.stride() != v_new.stride():
         raise ValueError("k_new and v_new must have the same strides")
     layer_stride = k_new.stride(0) if layers > 1 else 0
-    if layers > 1 and v_new.stride(0) != layer_stride:
-        raise ValueError("k_new and v_new must have the same strides")
     B = tails.numel()
     _need(tails, "tails", torch.int32, (B,))
     _need(plan.new_tails, "plan.new_tails", torch.int32, (B,))
     _need(plan.new_start, "plan.new_start", torch.int32, (B + 1,))
-    for t, name in ((plan.src_rows, "plan.src_rows"), (plan.slots, "plan.slots")):
-        _need(t, name, torch.int32)
-        if t.numel() < rows:
-            raise ValueError(f"{name} must hold {rows} rows, has {t.numel()}")
-    check(lib().kv8_append(_ptr(k_new), _ptr(v_new), stride, layer_stride, _ptr(tails), _ptr(plan.new_tails),
-                           _ptr(plan.new_start), _ptr(plan.src_rows), _ptr(plan.slots), B, rows, Hkv, D, layers,
-                           pages, tail_pages, _KV8_FORMATS[cache.k.dtype], _ptr(cache.k), _ptr(cache.v),
-                           _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(cache.k_tail), _ptr(cache.v_tail),
-                           _stream(stream)), "kv8_append")
+    _need_plan_rows(plan, rows)
+    check(lib().kv8_append(k_new.data_ptr(), v_new.data_ptr(), stride, layer_stride, tails.data_ptr(),
+                           plan.new_tails.data_ptr(), plan.new_start.data_ptr(), plan.src_rows.data_ptr(),
+                           plan.slots.data_ptr(), B, rows, Hkv, D, layers, pages, tail_pages,
+                           _KV8_FORMATS[cache.k.dtype], cache.k.data_ptr(), cache.v.data_ptr(),
+                           cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.k_tail.data_ptr(),
+                           cache.v_tail.data_ptr(), _stream(stream)), "kv8_append")
+
+
+@lru_cache(maxsize=256)
+def _attention_ws(device: int, B: int, n: int, H: int, Hkv: int, D: int, max_len: int) -> int:
+    return kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, max_len)
+
+
+@lru_cache(maxsize=256)
+def _logprobs_ws(R: int, V: int, top: int) -> int:
+    return token_logprobs_workspace_bytes(R, V, top)
 
 
 def kv8_tree_attention_workspace_bytes(B: int, n: int, H: int, Hkv: int, D: int, max_len: int) -> int:
@@ -517,14 +545,16 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
         raise ValueError(f"layer {layer} is not one of the cache's {layers}")
     if q.dim() != 4:
         raise ValueError(f"q must have 4 dimensions, got {tuple(q.shape)}")
-    B, n, H = q.shape[:3]
-    strides = []
-    for t, name, heads in ((q, "q", H), (k_new, "k_new", Hkv), (v_new, "v_new", Hkv)):
-        s = _need_rows(t, name, (B, n, heads, D))
-        if B > 1 and n > 1 and t.stride(0) != n * s:
-            raise ValueError(f"{name}: the tokens of all requests must be evenly apart")
-        strides.append(s)
-    if B * n > 1 and strides[1] != strides[2]:
+    B, n, H, _ = q.shape
+    q_stride = _need_rows(q, "q", (B, n, H, D))
+    new = (B, n, Hkv, D)
+    kv_stride = _need_rows(k_new, "k_new", new)
+    v_stride = _need_rows(v_new, "v_new", new)
+    if B > 1 and n > 1:
+        for t, name, s in ((q, "q", q_stride), (k_new, "k_new", kv_stride), (v_new, "v_new", v_stride)):
+            if t.stride(0) != n * s:
+                raise ValueError(f"{name}: the tokens of all requests must be evenly apart")
+    if B * n > 1 and kv_stride != v_stride:
         raise ValueError("k_new and v_new must have the same strides")
     _need(lens, "lens", torch.int32, (B,))
     _need(tails, "tails", torch.int32, (B,))
@@ -538,18 +568,20 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     scale = D ** -0.5 if scale is None else float(scale)
     if out is None:
         out = torch.empty((B, n, H, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, n, H, D))
-    nbytes = kv8_tree_attention_workspace_bytes(B, n, H, Hkv, D, max_len)
-    if ws is None and nbytes > 0:
-        ws = workspace(nbytes, q.device, "kv8_attention")  # apart from those that need no zeros
+    else:
+        _need(out, "out", torch.bfloat16, (B, n, H, D))
+    if ws is None:
+        ws = workspace(_attention_ws(q.get_device(), B, n, H, Hkv, D, max_len), q.device,
+                       "kv8_attention")  # apart from those that need no zeros
     codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
     tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
     check(lib().kv8_tree_attention(
-        _ptr(q), _ptr(k_new), _ptr(v_new), strides[0], strides[1], _ptr(cache.k) + codes, _ptr(cache.v) + codes,
-        _ptr(cache.k_scale) + heads, _ptr(cache.v_scale) + heads, _ptr(cache.k_tail) + tail, _ptr(cache.v_tail) + tail,
-        _ptr(block_table), _ptr(lens), _ptr(tails), _ptr(tree_parents), B, n, H, Hkv, D, max_blocks, pages, tail_pages,
-        max_len, _KV8_FORMATS[cache.k.dtype], scale, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(),
-        _stream(stream)), "kv8_tree_attention")
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_stride, kv_stride, cache.k.data_ptr() + codes,
+        cache.v.data_ptr() + codes, cache.k_scale.data_ptr() + heads, cache.v_scale.data_ptr() + heads,
+        cache.k_tail.data_ptr() + tail, cache.v_tail.data_ptr() + tail, block_table.data_ptr(), lens.data_ptr(),
+        tails.data_ptr(), _ptr(tree_parents), B, n, H, Hkv, D, max_blocks, pages, tail_pages, max_len,
+        _KV8_FORMATS[cache.k.dtype], scale, out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+        "kv8_tree_attention")
     return out
 
 
@@ -582,13 +614,14 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top: int = 0, ws: Op
     if ids.dim() not in (1, 2) or ids.shape[0] != R:
         raise ValueError(f"ids must have shape ({R}, m) or ({R},), got {tuple(ids.shape)}")
     m, dev = (ids.shape[1] if ids.dim() == 2 else 1), logits.device
-    out = TokenLogprobs(torch.empty(ids.shape, dtype=torch.float32, device=dev),
-                        torch.empty(R, dtype=torch.float32, device=dev),
+    f32 = torch.float32
+    out = TokenLogprobs(torch.empty(ids.shape, dtype=f32, device=dev), torch.empty(R, dtype=f32, device=dev),
                         torch.empty((R, top), dtype=torch.int32, device=dev),
-                        torch.empty((R, top), dtype=torch.float32, device=dev))
+                        torch.empty((R, top), dtype=f32, device=dev))
     if ws is None:
-        ws = workspace(token_logprobs_workspace_bytes(R, V, top), dev, "logprobs")
-    check(lib().token_logprobs(_ptr(logits), int(logits.dtype == torch.bfloat16), _ptr(ids), R, V, m, top,
-                               _ptr(out.logp), _ptr(out.entropy), _ptr(out.top_ids), _ptr(out.top_logp), _ptr(ws),
-                               ws.numel(), _stream(stream)), "token_logprobs")
+        ws = workspace(_logprobs_ws(R, V, top), dev, "logprobs")
+    check(lib().token_logprobs(logits.data_ptr(), int(logits.dtype is torch.bfloat16), ids.data_ptr(), R, V, m, top,
+                               out.logp.data_ptr(), out.entropy.data_ptr(), out.top_ids.data_ptr(),
+                               out.top_logp.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+          "token_logprobs")
     return out
