@@ -468,7 +468,7 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
 // ------------------------------------------------- log probabilities
 static bool logprobs_shape_ok(int R, int V, int m, int top) {
   return R >= 1 && R <= (1 << 20) && V >= 1 && V <= (1 << 20) && m >= 0 && m <= 64 && top >= 0 && top <= 64 &&
-         top <= V && (int64_t)R * ((V + 7 + 1023) / 1024) <= (int64_t)8 * INT32_MAX;
+         top <= V && (int64_t)R * ((V + 7 + 1023) / 1024) < (int64_t(1) << 30);
 }
 
 size_t token_logprobs_workspace_bytes(int R, int V, int top) {
@@ -487,7 +487,7 @@ w4a16_status token_logprobs(const void* logits, int bf16, const int32_t* ids, in
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
   return launch_token_logprobs(logits, bf16 != 0, ids, R, V, m, top, logp, entropy, top_ids, top_logp, workspace,
-                               dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                               dev.num_sms, dev.err, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? W4A16_OK
              : W4A16_ERR_CUDA;
 }

@@ -165,7 +165,7 @@ cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspac
 size_t token_logprobs_ws(int R, int V);
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* ids, int R, int V, int m, int top,
                                   float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
-                                  unsigned* err, cudaStream_t stream);
+                                  int num_sms, unsigned* err, cudaStream_t stream);
 
 // ---- accept
 struct AcceptPlan {

@@ -68,7 +68,7 @@ __device__ __forceinline__ unsigned kv8_mag(uint32_t w) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 4) kv8_append_kernel(const AppendParams p) {
   __shared__ int s_src[64];
   __shared__ unsigned s_max[2][kAppThreads / 32];
   grid_launch_dependents();
@@ -130,15 +130,27 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const AppendPar
   if (!page_piece) {
     // ---- copy: rows r0 .. r1 - 1, 16 words of 16 bytes each, keys and values
     const int per = (r1 - r0) * 32, total = (lh1 - lh0) * per;
-    for (int w = tid; w < total; w += kAppThreads) {
-      const int lh = lh0 + w / per, rest = w % per;
-      const int r = r0 + (rest >> 5), c = rest & 31;  // c: 0 .. 15 keys, 16 .. 31 values
-      const int layer = lh / p.Hkv, h = lh % p.Hkv;
-      const __nv_bfloat16* src = (c < 16 ? p.k_new : p.v_new) + layer * p.layer_stride +
-                                 (int64_t)s_src[r] * p.row_stride + h * kAppD + (c & 15) * 8;
-      const int64_t at = ((((int64_t)layer * p.tail_pages + tail_new) * p.Hkv + h) * 64 + r) * kAppD + (c & 15) * 8;
-      if (in_bounds(p.err, at + 7, (int64_t)p.layers * p.tail_pages * p.Hkv * 64 * kAppD))
-        *reinterpret_cast<uint4*>((c < 16 ? p.k_tail : p.v_tail) + at) = *reinterpret_cast<const uint4*>(src);
+    constexpr int kBatch = 4;  // words a thread holds: their loads are in flight together
+    for (int w0 = tid; w0 < total; w0 += kBatch * kAppThreads) {
+      uint4 x[kBatch];
+      int64_t to[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int w = w0 + k * kAppThreads;
+        if (w < total) {
+          const int lh = lh0 + w / per, rest = w % per;
+          const int r = r0 + (rest >> 5), c = rest & 31;  // c: 0 .. 15 keys, 16 .. 31 values
+          const int layer = lh / p.Hkv, h = lh % p.Hkv;
+          x[k] = __ldg(reinterpret_cast<const uint4*>((c < 16 ? p.k_new : p.v_new) + layer * p.layer_stride +
+                                                      (int64_t)s_src[r] * p.row_stride + h * kAppD + (c & 15) * 8));
+          to[k] = ((((int64_t)layer * p.tail_pages + tail_new) * p.Hkv + h) * 64 + r) * kAppD + (c & 15) * 8;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (w0 + k * kAppThreads < total &&
+            in_bounds(p.err, to[k] + 7, (int64_t)p.layers * p.tail_pages * p.Hkv * 64 * kAppD))
+          *reinterpret_cast<uint4*>((((w0 + k * kAppThreads) & 31) < 16 ? p.k_tail : p.v_tail) + to[k]) = x[k];
     }
     return;
   }
@@ -152,7 +164,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const AppendPar
   const int page = s0 >> 6;
   int buf = 0;
   for (int lh = lh0; lh < lh1; ++lh, buf ^= 1) {
-    const int layer = lh / p.Hkv, h = lh % p.Hkv;
+    const int layer = lh / p.Hkv, h = lh - layer * p.Hkv;
     const __nv_bfloat16* a = src_new + layer * p.layer_stride + h * kAppD + c;
     const __nv_bfloat16* o = src_tail + (((int64_t)layer * p.tail_pages + tail_old) * p.Hkv + h) * 64 * kAppD + c;
     uint4 x[8];

@@ -52,11 +52,9 @@ __device__ void plan_scan(int* a, int B, int* scratch) {
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int o = x - sum, total = 0;
-  for (int w = 0; w < nw; ++w) {
-    o += w < warp ? scratch[w] : 0;
-    total += scratch[w];
-  }
+  const int w = lane < nw ? scratch[lane] : 0;
+  const int total = __reduce_add_sync(0xffffffffu, w);
+  int o = x - sum + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
   for (int i = i0; i < i1; ++i) {
     const int c = a[i];
     a[i] = o;
@@ -77,6 +75,12 @@ __device__ __forceinline__ int plan_find(const int* a, int B, int x) {
       hi = mid - 1;
   }
   return lo;
+}
+
+// place a, 0 <= a <= cap, behind place head of the ring
+__device__ __forceinline__ int plan_ring(int head, int a, int cap) {
+  const int i = head + a;
+  return i >= cap ? i - cap : i;
 }
 
 __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanParams p) {
@@ -203,21 +207,21 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
   const int room = p.ring_cap - count;  // ring places behind the last free page
   if (gt == 0) {
     if (back > room) report_error(p.err, kErrInput);
-    p.new_queue[0] = (int)(((int64_t)head + taken) % p.ring_cap);
+    p.new_queue[0] = plan_ring(head, taken, p.ring_cap);
     p.new_queue[1] = count - taken + min(back, room);
     p.new_queue[2] = asked - taken;
   }
   // ---- pages taken, and pages returned
   for (int a = gt; a < taken; a += gn) {
     const int b = plan_find(s.need, B, a);
-    const int page = p.ring[((int64_t)head + a) % p.ring_cap];
+    const int page = p.ring[plan_ring(head, a, p.ring_cap)];
     const bool bad = page < 0 || page >= kPlanMaxPage;
     if (bad) report_error(p.err, kErrInput);
     p.table[(int64_t)b * p.max_blocks + s.len[b] / 64 + (a - s.need[b])] = bad ? -1 : page;
   }
   for (int a = gt; a < min(back, room); a += gn) {
     const int b = plan_find(s.back, B, a);
-    p.ring[((int64_t)head + count + a) % p.ring_cap] = p.table[(int64_t)b * p.max_blocks + (a - s.back[b])];
+    p.ring[plan_ring(plan_ring(head, count, p.ring_cap), a, p.ring_cap)] = p.table[(int64_t)b * p.max_blocks + (a - s.back[b])];
   }
   // ---- rows
   for (int r = gt; r < p.rows; r += gn) {
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
       p.src_rows[i] = r;
       int slot = -1 - pos % 64;
       if (pos / 64 < (len + cnt) / 64) {
-        const int page = p.ring[((int64_t)head + s.need[b] + (pos / 64 - len / 64)) % p.ring_cap];
+        const int page = p.ring[plan_ring(head, s.need[b] + (pos / 64 - len / 64), p.ring_cap)];
         slot = page < 0 || page >= kPlanMaxPage ? INT_MIN : page * 64 + pos % 64;
       }
       p.slots[i] = slot;
@@ -265,7 +269,7 @@ cudaError_t launch_block_plan(const int32_t* lens, const int32_t* tails, const i
                              err};
   const int work = rows > B ? rows : B;
   const int threads = work <= 1024 ? 256 : 1024;
-  const int ctas = (work + threads * 4 - 1) / (threads * 4);
+  const int ctas = (work + threads - 1) / threads;
   const size_t smem = block_plan_smem(B, node != nullptr);
   if (smem > 48 * 1024) {
     const cudaError_t e =

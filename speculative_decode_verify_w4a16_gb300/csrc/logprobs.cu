@@ -6,16 +6,20 @@
 // over parts of the row (each part against its own maximum, then scaled by
 // exp(m_part - m)), so the logits are read once.
 //
-// token_stats_kernel: a warp takes a window of 1024 logits in registers and
-// leaves its (m, S, W) and the maxima of its four 256-logit quarters.
+// token_stats_kernel: a warp takes a window of 1024 logits in registers (the
+// next one's loads in flight) and leaves its (m, S, W) and the maxima of its
+// four 256-logit quarters as ordered integers (one reduction instruction each;
+// a NaN is above all numbers, so it reaches m and with it every result).
 // token_report_kernel, one CTA per row: merges the windows; the `top`-th
-// largest quarter maximum is a lower bound of the `top`-th largest logit, so
-// only quarters that reach it are read again (at most `top` of them unless
+// largest window maximum is a lower bound of the `top`-th largest logit, so
+// only quarters that reach it are read again (few more than `top`, unless
 // maxima tie), and the few logits at or above it are ranked in shared memory.
+// Ranks are counted (each of up to 1025 values against all), two orders of
+// magnitude less latency than a sort of the row.
 //
 // Bound: HBM for the first kernel (one pass, 16-byte loads); the second reads
-// about 1.5 % of the row's bytes in statistics and top x 256 logits, mostly
-// from L2. Windows start at 16-byte boundaries of memory, not of the row, so
+// 3 % of the row's bytes (bf16; fp32 1.6 %) in statistics and some top x 256
+// logits, mostly from L2: its latency counts. Windows start at 16-byte boundaries of memory, not of the row, so
 // that rows of any length load 16 bytes at a time.
 #include <math.h>
 
@@ -27,7 +31,7 @@ namespace w4a16 {
 constexpr int kLpWindow = 1024;
 constexpr int kLpQuarter = 256;
 constexpr int kLpStatWarps = 8;
-constexpr int kLpRepThreads = 256;
+constexpr int kLpRepThreads = 128;
 constexpr int kLpCand = 1024;    // logits ranked in shared memory
 constexpr float kLpLog2e = 1.4426950408889634f;
 
@@ -39,8 +43,8 @@ struct LogprobParams {
   float *logp, *entropy;
   int32_t* top_ids;
   float* top_logp;
-  float* win;      // [R][windows][4]: m, S, W, unused
-  float* quarter;  // [R][windows][4]: maxima
+  float4* win;     // [R][windows]: m, S, W (in powers of two: sum of log2 terms), unused
+  uint4* quarter;  // [R][windows]: the quarters' maxima (lp_key)
   unsigned* err;
 };
 
@@ -56,29 +60,62 @@ __device__ __forceinline__ int lp_shift(const T* row) {
   return (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
 }
 
-// the E = 16 / sizeof(T) elements at index e (a multiple of E less the shift)
-// of the row as floats, -inf outside [0, V)
+__device__ __forceinline__ uint64_t lp_2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void lp_un2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t lp_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t lp_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t lp_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// the 16 bytes at index e of the row (a multiple of 16 bytes less the shift),
+// elements outside [0, V) set to -inf
 template <typename T>
-__device__ __forceinline__ void lp_load(const T* row, int e, int V, float* x) {
+__device__ __forceinline__ uint4 lp_load(const T* row, int e, int V) {
   constexpr int E = 16 / sizeof(T);
-  if (e >= 0 && e + E <= V) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + e));
+  if (e >= 0 && e + E <= V) return __ldg(reinterpret_cast<const uint4*>(row + e));
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     if constexpr (sizeof(T) == 4) {
-      x[0] = __uint_as_float(w.x);
-      x[1] = __uint_as_float(w.y);
-      x[2] = __uint_as_float(w.z);
-      x[3] = __uint_as_float(w.w);
+      w[k] = e + k >= 0 && e + k < V ? reinterpret_cast<const uint32_t*>(row)[e + k] : 0xFF800000u;
     } else {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(u[k] << 16);
-        x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-      }
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(row);
+      const uint32_t lo = e + 2 * k >= 0 && e + 2 * k < V ? h[e + 2 * k] : 0xFF80u;
+      const uint32_t hi = e + 2 * k + 1 >= 0 && e + 2 * k + 1 < V ? h[e + 2 * k + 1] : 0xFF80u;
+      w[k] = lo | (hi << 16);
     }
-  } else {
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// ... as floats
+template <typename T>
+__device__ __forceinline__ void lp_floats(uint4 v, float* x) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < E; ++k) x[k] = e + k >= 0 && e + k < V ? (float)row[e + k] : -INFINITY;
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      x[k] = __uint_as_float(u[k]);
+    } else {
+      x[2 * k] = __uint_as_float(u[k] << 16);
+      x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    }
   }
 }
 
@@ -89,10 +126,8 @@ __device__ __forceinline__ unsigned lp_key(float x) {
   const unsigned b = __float_as_uint(x + 0.0f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ float lp_warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
+__device__ __forceinline__ float lp_unkey(unsigned k) {
+  return k == 0xFFFFFFFFu ? NAN : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 __device__ __forceinline__ float lp_warp_sum(float v) {
 #pragma unroll
@@ -101,59 +136,63 @@ __device__ __forceinline__ float lp_warp_sum(float v) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kLpStatWarps) token_stats_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(32 * kLpStatWarps, sizeof(T) == 2 ? 4 : 2) token_stats_kernel(const LogprobParams p) {
   constexpr int E = 16 / sizeof(T), L = 32 / E;  // loads of E elements a lane
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kLpStatWarps + (threadIdx.x >> 5);
-  if (id >= (int64_t)p.R * p.windows) return;
-  const int r = (int)(id / p.windows), w = (int)(id % p.windows);
-  const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
-  const int e0 = w * kLpWindow - lp_shift(row) + lane * E;
-  float x[32];
+  const int total = p.R * p.windows, step = gridDim.x * kLpStatWarps;
+  int id = blockIdx.x * kLpStatWarps + (threadIdx.x >> 5);
+  uint4 next[L];
+  auto load = [&](int i) {
+    const int r = i / p.windows, w = i - r * p.windows;
+    const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
+    const int e0 = w * kLpWindow - lp_shift(row) + lane * E;
 #pragma unroll
-  for (int k = 0; k < L; ++k) lp_load<T>(row, e0 + k * 32 * E, p.V, x + k * E);
-  // quarter q: loads q L / 4 .. ; a NaN is carried apart (fmaxf drops it)
-  float q[4];
-  bool nan = false;
+    for (int k = 0; k < L; ++k) next[k] = lp_load<T>(row, e0 + k * 32 * E, p.V);
+  };
+  if (id < total) load(id);
+  for (; id < total; id += step) {
+    float x[32];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    q[k] = -INFINITY;
+    for (int k = 0; k < L; ++k) lp_floats<T>(next[k], x + k * E);
+    if (id + step < total) load(id + step);
+    unsigned key[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q[k] = fmaxf(q[k], x[8 * k + j]);
-      nan |= x[8 * k + j] != x[8 * k + j];
+    for (int q = 0; q < 4; ++q) {
+      // the largest as a float, unless a NaN (which compares false) is among them
+      float m = x[8 * q];
+      bool nan = x[8 * q] != x[8 * q];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        m = fmaxf(m, x[8 * q + j]);
+        nan |= x[8 * q + j] != x[8 * q + j];
+      }
+      key[q] = __reduce_max_sync(0xffffffffu, nan ? 0xFFFFFFFFu : lp_key(m));
     }
-    q[k] = lp_warp_max(q[k]);
-  }
-  const float mx = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
-  // exp(x - m) = 2^((x - m) log2 e); x - m is exact or rounded once. z is kept
-  // off -inf so that a masked logit adds 0 * finite to W.
-  float s0 = 0.0f, s1 = 0.0f, w0 = 0.0f, w1 = 0.0f;
-  if (mx > -INFINITY || nan) {
+    const float mx = lp_unkey(max(max(key[0], key[1]), max(key[2], key[3])));
+    // z = (x - m) log2 e (kept off -inf, and off NaN: m carries that), S = sum
+    // 2^z, W = sum z 2^z, two logits an instruction
+    const uint64_t nm = lp_2(-mx, -mx), l2 = lp_2(kLpLog2e, kLpLog2e);
+    uint64_t s2[2] = {0ull, 0ull}, w2[2] = {0ull, 0ull};
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
-      const float z0 = x[j] - mx, z1 = x[j + 1] - mx;
-      const float t0 = lp_ex2(z0 * kLpLog2e), t1 = lp_ex2(z1 * kLpLog2e);
-      s0 += t0;
-      s1 += t1;
-      w0 = fmaf(fmaxf(z0, -1e30f), t0, w0);
-      w1 = fmaf(fmaxf(z1, -1e30f), t1, w1);
+      float z0, z1;
+      lp_un2(lp_mul2(lp_add2(lp_2(x[j], x[j + 1]), nm), l2), z0, z1);
+      z0 = fmaxf(z0, -1e30f);
+      z1 = fmaxf(z1, -1e30f);
+      const uint64_t t = lp_2(lp_ex2(z0), lp_ex2(z1));
+      s2[(j >> 1) & 1] = lp_add2(s2[(j >> 1) & 1], t);
+      w2[(j >> 1) & 1] = lp_fma2(lp_2(z0, z1), t, w2[(j >> 1) & 1]);
     }
-  }
-  const float S = lp_warp_sum(s0 + s1), W = lp_warp_sum(w0 + w1);
-  // a quarter with a NaN holds the row's largest key
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    bool n = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) n |= x[8 * k + j] != x[8 * k + j];
-    if (__any_sync(0xffffffffu, nan) && __any_sync(0xffffffffu, n)) q[k] = NAN;
-  }
-  if (lane == 0) {
-    reinterpret_cast<float4*>(p.win)[id] = make_float4(mx, S, W, 0.0f);
-    if (p.top > 0) reinterpret_cast<float4*>(p.quarter)[id] = make_float4(q[0], q[1], q[2], q[3]);
+    float a, b, c, d;
+    lp_un2(lp_add2(s2[0], s2[1]), a, b);
+    lp_un2(lp_add2(w2[0], w2[1]), c, d);
+    const float S = lp_warp_sum(a + b), W = lp_warp_sum(c + d);
+    if (lane == 0) {
+      p.win[id] = make_float4(mx, S, W, 0.0f);
+      if (p.top > 0) p.quarter[id] = make_uint4(key[0], key[1], key[2], key[3]);
+    }
   }
 }
 
@@ -208,78 +247,113 @@ template <typename T>
 __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const LogprobParams p) {
   __shared__ int hist[256];
   __shared__ unsigned sel[2];
-  __shared__ float red[3][kLpRepThreads / 32];
+  __shared__ float red[2][kLpRepThreads / 32];
+  __shared__ unsigned red_k[kLpRepThreads / 32];
   __shared__ unsigned ckey[kLpCand];
   __shared__ int cidx[kLpCand];
-  __shared__ int s_count, s_ties;
+  __shared__ int s_count, s_ties, s_quarters;
+  __shared__ unsigned s_bound;
+  extern __shared__ __align__(16) unsigned lp_smem[];
   grid_launch_dependents();
   grid_dependency_wait();
   const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
-  const float4* win = reinterpret_cast<const float4*>(p.win) + (int64_t)r * p.windows;
-  // ---- the windows merged: every sum against the row's maximum
-  float m = -INFINITY;
-  for (int w = tid; w < p.windows; w += kLpRepThreads) m = fmaxf(m, __ldcg(&win[w]).x);
-  m = lp_warp_max(m);
-  if (lane == 0) red[0][warp] = m;
+  const float4* win = p.win + (int64_t)r * p.windows;
+  const int nq = p.windows * 4, shift = lp_shift(row), wpad = (p.windows + 3) / 4 * 4;
+  unsigned* wkey = lp_smem;                                // [wpad] keys of the windows' maxima
+  unsigned* qkey = wkey + wpad;                            // [nq] ... of the quarters' (top > 0)
+  int* quarters = reinterpret_cast<int*>(qkey + nq);       // [nq] those to read again
+  // ---- the given tokens' logits asked for (their ids come first), then the
+  // statistics; thread tid's first window stays in registers
+  const int id0 = tid < p.m ? p.ids[(int64_t)r * p.m + tid] : -1;
+  const float x0 = id0 >= 0 && id0 < p.V ? (float)row[id0] : 0.0f;
+  float4 v0 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  unsigned mk = 0u;
+  for (int w = tid; w < wpad; w += kLpRepThreads) {
+    unsigned k = 0u;
+    if (w < p.windows) {
+      const float4 v = __ldcg(&win[w]);
+      if (w == tid) v0 = v;
+      k = lp_key(v.x);
+      if (p.top > 0) reinterpret_cast<uint4*>(qkey)[w] = __ldcg(p.quarter + (int64_t)r * p.windows + w);
+    }
+    wkey[w] = k;
+    mk = max(mk, k);
+  }
+  mk = __reduce_max_sync(0xffffffffu, mk);
+  if (lane == 0) red_k[warp] = mk;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kLpRepThreads / 32; ++k) m = fmaxf(m, red[0][k]);
+  for (int k = 0; k < kLpRepThreads / 32; ++k) mk = max(mk, red_k[k]);
+  const float m = lp_unkey(mk);
+  // ---- the windows merged: every sum against the row's maximum
   float S = 0.0f, W = 0.0f;
   for (int w = tid; w < p.windows; w += kLpRepThreads) {
-    const float4 v = __ldcg(&win[w]);
-    const float d = v.x - m, t = v.x == -INFINITY && v.y == 0.0f ? 0.0f : expf(d);
+    const float4 v = w == tid ? v0 : __ldcg(&win[w]);
+    const float d = fmaxf(v.x - m, -1e30f), t = expf(d);
     S = fmaf(v.y, t, S);
-    W += t * fmaf(fmaxf(d, -1e30f), v.y, v.z);
+    W += t * fmaf(d, v.y, v.z * 0.69314718056f);
   }
   S = lp_warp_sum(S);
   W = lp_warp_sum(W);
   if (lane == 0) {
-    red[1][warp] = S;
-    red[2][warp] = W;
+    red[0][warp] = S;
+    red[1][warp] = W;
   }
   __syncthreads();
   S = W = 0.0f;
 #pragma unroll
   for (int k = 0; k < kLpRepThreads / 32; ++k) {
-    S += red[1][k];
-    W += red[2][k];
+    S += red[0][k];
+    W += red[1][k];
   }
-  const float ls = S > 0.0f ? logf(S) : NAN;  // -inf alone, or a NaN
+  // a NaN, +inf or -inf alone: no distribution
+  const float ls = S > 0.0f && m < INFINITY && m > -INFINITY ? logf(S) : NAN;
   if (tid == 0 && p.entropy) p.entropy[r] = ls - W / S;
-  for (int i = tid; i < p.m; i += kLpRepThreads) {
-    const int id = p.ids[(int64_t)r * p.m + i];
-    float v = 0.0f;
-    if (id >= 0 && id < p.V) {
-      v = ((float)row[id] - m) - ls;
-    } else if (id != -1) {
-      report_error(p.err, kErrInput);
-      v = NAN;
-    }
-    p.logp[(int64_t)r * p.m + i] = v;
+  if (tid < p.m) {  // m <= 64 of them
+    if (id0 < -1 || id0 >= p.V) report_error(p.err, kErrInput);
+    p.logp[(int64_t)r * p.m + tid] = id0 == -1 ? 0.0f : id0 >= 0 && id0 < p.V ? (x0 - m) - ls : NAN;
   }
   if (p.top == 0) return;
 
-  // ---- the lower bound from the quarters' maxima (with fewer quarters than
-  // `top`, every logit is a candidate)
-  const float* qmax = p.quarter + (int64_t)r * p.windows * 4;
-  const int nq = p.windows * 4, shift = lp_shift(row);
-  unsigned bound = 0;
-  if (nq >= p.top)
-    bound = lp_select(p.top, hist, sel, [&](auto f) {
-      for (int i = tid; i < nq; i += kLpRepThreads) f(lp_key(__ldcg(&qmax[i])));
-    });
-  if (tid == 0) s_count = 0;
+  // ---- the lower bound: the `top`-th largest maximum of the windows, or of
+  // the quarters where there are fewer windows (with fewer quarters than `top`,
+  // every logit is a candidate)
+  if (tid == 0) {
+    s_count = s_quarters = 0;
+    s_bound = 0u;
+  }
   __syncthreads();
+  {
+    const bool by_window = p.windows >= p.top;
+    const int n = by_window ? p.windows : nq;
+    const unsigned* key = by_window ? wkey : qkey;
+    if (n >= p.top)
+      for (int i = tid; i < n; i += kLpRepThreads) {
+        const unsigned mine = key[i];
+        int rank = 0;  // of value i, the earlier of equal ones first (a key of 0 past the end counts for nothing)
+        for (int j = 0; j < n; j += 4) {
+          const uint4 k = reinterpret_cast<const uint4*>(key)[j >> 2];
+          rank += (k.x > mine || (k.x == mine && j < i)) + (k.y > mine || (k.y == mine && j + 1 < i)) +
+                  (k.z > mine || (k.z == mine && j + 2 < i)) + (k.w > mine || (k.w == mine && j + 3 < i));
+        }
+        if (rank == p.top - 1) s_bound = mine;
+      }
+  }
+  __syncthreads();
+  const unsigned bound = s_bound;
+  for (int i = tid; i < nq; i += kLpRepThreads)
+    if (qkey[i] >= bound) quarters[atomicAdd(&s_quarters, 1)] = i;
+  __syncthreads();
+  const int again = s_quarters;
   // every logit of a quarter that reaches the bound, a warp a quarter
   auto scan = [&](auto f) {
     constexpr int E = 16 / sizeof(T), L = 8 / E;
-    for (int i = warp; i < nq; i += kLpRepThreads / 32) {
-      if (lp_key(__ldcg(&qmax[i])) < bound) continue;
-      const int e0 = i * kLpQuarter - shift + lane * E;
+    for (int i = warp; i < again; i += kLpRepThreads / 32) {
+      const int e0 = quarters[i] * kLpQuarter - shift + lane * E;
       float x[8];
 #pragma unroll
-      for (int k = 0; k < L; ++k) lp_load<T>(row, e0 + k * 32 * E, p.V, x + k * E);
+      for (int k = 0; k < L; ++k) lp_floats<T>(lp_load<T>(row, e0 + k * 32 * E, p.V), x + k * E);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int e = e0 + (j / E) * 32 * E + j % E;
@@ -318,7 +392,7 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
     });
     __syncthreads();
     const int above = s_count, want = p.top - above;
-    // the ties in index order, 256 logits at a time
+    // the ties in index order, a logit a thread at a time
     for (int e0 = 0; e0 < p.V; e0 += kLpRepThreads) {
       const int e = e0 + tid;
       const bool hit = e < p.V && lp_key((float)row[e]) == kth;
@@ -360,7 +434,7 @@ size_t token_logprobs_ws(int R, int V) { return (size_t)R * lp_windows(V, false)
 
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* ids, int R, int V, int m, int top,
                                   float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
-                                  unsigned* err, cudaStream_t stream) {
+                                  int num_sms, unsigned* err, cudaStream_t stream) {
   LogprobParams p;
   p.logits = logits;
   p.ids = ids;
@@ -373,17 +447,22 @@ cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* 
   p.entropy = entropy;
   p.top_ids = top_ids;
   p.top_logp = top_logp;
-  p.win = static_cast<float*>(workspace);
-  p.quarter = p.win + (size_t)R * p.windows * 4;
+  p.win = static_cast<float4*>(workspace);
+  p.quarter = reinterpret_cast<uint4*>(p.win + (size_t)R * p.windows);
   p.err = err;
-  const int64_t warps = (int64_t)R * p.windows;
-  const dim3 grid((unsigned)((warps + kLpStatWarps - 1) / kLpStatWarps));
+  // every SM's resident CTAs (4, or 2 of fp32: see the kernel's bounds), fewer
+  // when there are fewer windows
+  const int64_t warps = (int64_t)R * p.windows, most = (int64_t)num_sms * (bf16 ? 4 : 2);
+  const int64_t ctas = (warps + kLpStatWarps - 1) / kLpStatWarps;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
   const dim3 block(32 * kLpStatWarps);
   cudaError_t e = bf16 ? launch_pdl(token_stats_kernel<__nv_bfloat16>, grid, block, 0, stream, p)
                        : launch_pdl(token_stats_kernel<float>, grid, block, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return bf16 ? launch_pdl(token_report_kernel<__nv_bfloat16>, dim3((unsigned)R), dim3(kLpRepThreads), 0, stream, p)
-              : launch_pdl(token_report_kernel<float>, dim3((unsigned)R), dim3(kLpRepThreads), 0, stream, p);
+  // window keys, quarter keys, quarter numbers (37 KB for 2^20 logits)
+  const size_t smem = ((size_t)p.windows * (top > 0 ? 8 : 0) + (p.windows + 3) / 4 * 4) * 4;
+  return bf16 ? launch_pdl(token_report_kernel<__nv_bfloat16>, dim3((unsigned)R), dim3(kLpRepThreads), smem, stream, p)
+              : launch_pdl(token_report_kernel<float>, dim3((unsigned)R), dim3(kLpRepThreads), smem, stream, p);
 }
 
 }  // namespace w4a16
