@@ -379,7 +379,7 @@ w4a16_status kv8_append(const void* k_new, const void* v_new, int64_t row_stride
   if (B < 1 || rows < 1 || layers < 1 || !kv8_cache_ok(Hkv, pages, tail_pages) || fmt < 0 || fmt > 1 ||
       row_stride < (int64_t)Hkv * D || row_stride % 8 != 0 || layer_stride < 0 || layer_stride % 8 != 0)
     return W4A16_ERR_INVALID_ARG;
-  if (D != 128 || B > kPlanMaxB || rows > (1 << 28) || (int64_t)layers * Hkv > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+  if (D != 128 || B > kPlanMaxB || rows > (1 << 24) || (int64_t)layers * Hkv > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
   const void* wide[] = {k_new, v_new, k, v, k_tail, v_tail};
   for (const void* a : wide)
     if (!aligned(a, 16)) return W4A16_ERR_INVALID_ARG;

@@ -12,10 +12,12 @@
 // pieces copy their rows.
 //
 // Bound: HBM (each row read and written once) for prompts; for the few rows
-// of a draft step over many layers the chain of dependent loads (piece ->
-// source rows -> values) per CTA. A CTA therefore takes one piece and walks
-// over `heads` (layer, head) pairs of it: the piece is found once, and a copy
-// deals all of the pairs' rows over its threads at once.
+// of a draft step over many layers latency. Which pieces there are is known on
+// the device alone, so the CTAs (four an SM) first sum up the requests' pages
+// from the plan, each for itself, and then take (page, layer, head) items in
+// turn, and after them the tail rows, (request, group of layer-heads) by
+// (request, group): no CTA is launched for work that is not there (one CTA for
+// every piece that might exist took 33 us for 80 layers of 16 drafts).
 #include <cuda_fp8.h>
 #include <limits.h>
 
@@ -36,7 +38,7 @@ struct AppendParams {
   float *k_scale, *v_scale;
   __nv_bfloat16 *k_tail, *v_tail;
   unsigned* err;
-  int heads;  // (layer, head) pairs per CTA
+  int group;   // (layer, head) pairs of a tail item
 };
 
 // exponent k of the scale for the largest finite magnitude's bf16 bits
@@ -69,129 +71,187 @@ __device__ __forceinline__ unsigned kv8_mag(uint32_t w) {
 
 template <int FMT>
 __global__ void __launch_bounds__(kAppThreads, 4) kv8_append_kernel(const AppendParams p) {
-  __shared__ int s_src[64];
+  extern __shared__ int app_smem[];
   __shared__ unsigned s_max[2][kAppThreads / 32];
+  __shared__ int s_src[2][64];
+  __shared__ int2 s_at[2][2];
+  __shared__ int s_sum[kAppThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B;
+  int* pre = app_smem;          // [B + 1] pages completed by the requests before
+  int* first = pre + B + 1;     // [B] first kept row
+  int* count = first + B;       // [B] kept rows, times 64, plus the block's rows before this step
   grid_launch_dependents();
   grid_dependency_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // ---- the request: piece numbers from new_start[b] / 64 + 2 b on are b's
-  // (it has at most kept / 64 + 2 of them). Every warp searches, 32 requests
-  // a step.
-  const int f = blockIdx.x;
-  int lo = 0, hi = p.B;  // the last b of lo .. hi - 1 whose first number is <= f
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int b = lo + lane * step;
-    const bool le = b < hi && p.new_start[b] / 64 + 2 * b <= f;
-    const int c = __popc(__ballot_sync(0xffffffffu, le));  // a prefix of the lanes
-    const int at = lo + max(c - 1, 0) * step;
-    hi = min(hi, at + step);
-    lo = at;
-  }
-  const int b = lo;
-  const int i0 = p.new_start[b], i1 = p.new_start[b + 1];
-  if (i0 < 0 || i1 > p.rows || i1 < i0) {
-    if (tid == 0) report_error(p.err, kErrInput);
-    return;
-  }
-  if (i1 == i0) return;
-  const int piece = f - (i0 / 64 + 2 * b);
-  const int first = p.slots[i0];
-  const int t = first >= 0 ? first & 63 : -1 - first;  // the block's rows before this step
-  if (t > 63) {  // no slot (INT_MIN: its page was bad)
-    if (tid == 0) report_error(p.err, kErrInput);
-    return;
-  }
-  const int cnt = i1 - i0;
-  if (piece >= (t + cnt + 63) / 64) return;
-  const int r0 = piece == 0 ? t : 0;              // the piece's new rows: r0 .. r1 - 1 of the block
-  const int r1 = min(64, t + cnt - piece * 64);
-  const int base = i0 + piece * 64 - t;            // kept row at block row r: base + r
-  // ---- source rows and slots: all new rows agree on the page (or the tail)
-  const int s0 = p.slots[base + r0];
-  const bool page_piece = s0 >= 0;
-  bool bad = page_piece ? r1 != 64 || (s0 >> 6) >= p.pages : false;
-  if (tid < 64) {
-    int src = -1;
-    if (tid >= r0 && tid < r1) {
-      src = p.src_rows[base + tid];
-      bad = bad || src < 0 || src >= p.rows || p.slots[base + tid] != (page_piece ? (s0 & ~63) + tid : -1 - tid);
+  // ---- the requests: rows, the open block's fill, pages. Thread tid sums a
+  // run of them
+  const int per = (B + kAppThreads - 1) / kAppThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int i0 = p.new_start[b], i1 = p.new_start[b + 1];
+    int n = i1 - i0, t = 0, full = 0;
+    if (i0 < 0 || i1 > p.rows || n < 0) {
+      if (blockIdx.x == 0) report_error(p.err, kErrInput);
+      n = 0;
     }
-    s_src[tid] = src;
-  }
-  const int tail_old = p.tails[b], tail_new = p.new_tails[b];
-  if (page_piece ? r0 > 0 && (tail_old < 0 || tail_old >= p.tail_pages) : (tail_new < 0 || tail_new >= p.tail_pages))
-    bad = true;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) report_error(p.err, kErrInput);
-    return;
-  }
-  const int lh0 = blockIdx.y * p.heads, lh1 = min(p.layers * p.Hkv, lh0 + p.heads);
-  if (!page_piece) {
-    // ---- copy: rows r0 .. r1 - 1, 16 words of 16 bytes each, keys and values
-    const int per = (r1 - r0) * 32, total = (lh1 - lh0) * per;
-    constexpr int kBatch = 4;  // words a thread holds: their loads are in flight together
-    for (int w0 = tid; w0 < total; w0 += kBatch * kAppThreads) {
-      uint4 x[kBatch];
-      int64_t to[kBatch];
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int w = w0 + k * kAppThreads;
-        if (w < total) {
-          const int lh = lh0 + w / per, rest = w % per;
-          const int r = r0 + (rest >> 5), c = rest & 31;  // c: 0 .. 15 keys, 16 .. 31 values
-          const int layer = lh / p.Hkv, h = lh % p.Hkv;
-          x[k] = __ldg(reinterpret_cast<const uint4*>((c < 16 ? p.k_new : p.v_new) + layer * p.layer_stride +
-                                                      (int64_t)s_src[r] * p.row_stride + h * kAppD + (c & 15) * 8));
-          to[k] = ((((int64_t)layer * p.tail_pages + tail_new) * p.Hkv + h) * 64 + r) * kAppD + (c & 15) * 8;
-        }
+    if (n > 0) {
+      const int s = p.slots[i0];
+      t = s >= 0 ? s & 63 : -1 - s;
+      if (t > 63) {  // no slot (INT_MIN: its page was bad)
+        if (blockIdx.x == 0) report_error(p.err, kErrInput);
+        n = t = 0;
       }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (w0 + k * kAppThreads < total &&
-            in_bounds(p.err, to[k] + 7, (int64_t)p.layers * p.tail_pages * p.Hkv * 64 * kAppD))
-          *reinterpret_cast<uint4*>((((w0 + k * kAppThreads) & 31) < 16 ? p.k_tail : p.v_tail) + to[k]) = x[k];
+      full = s >= 0 ? (t + n) / 64 : 0;
     }
-    return;
+    first[b] = i0;
+    count[b] = n * 64 + t;
+    pre[b] = full;
+    mine += full;
   }
-  // ---- a page: 128 threads each for the keys and the values, thread (row
+  int x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  int at = x - mine, pages = 0;
+#pragma unroll
+  for (int w = 0; w < kAppThreads / 32; ++w) {
+    at += w < warp ? s_sum[w] : 0;
+    pages += s_sum[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int full = pre[b];
+    pre[b] = at;
+    at += full;
+  }
+  if (tid == 0) pre[B] = pages;
+  __syncthreads();
+  const int pairs = p.layers * p.Hkv;
+
+  // ---- pages: 128 threads each for the keys and the values, thread (row
   // group, 8 columns): rows g, g + 8, .. of the block in registers
   const int half = tid >> 7, u = tid & 127, g = u >> 4, c = (u & 15) * 8;
   const __nv_bfloat16* src_new = half ? p.v_new : p.k_new;
   const __nv_bfloat16* src_tail = half ? p.v_tail : p.k_tail;
   uint8_t* codes = half ? p.v : p.k;
   float* scales = half ? p.v_scale : p.k_scale;
-  const int page = s0 >> 6;
-  int buf = 0;
-  for (int lh = lh0; lh < lh1; ++lh, buf ^= 1) {
-    const int layer = lh / p.Hkv, h = lh - layer * p.Hkv;
-    const __nv_bfloat16* a = src_new + layer * p.layer_stride + h * kAppD + c;
-    const __nv_bfloat16* o = src_tail + (((int64_t)layer * p.tail_pages + tail_old) * p.Hkv + h) * 64 * kAppD + c;
-    uint4 x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 8 * k + g;
-      x[k] = *reinterpret_cast<const uint4*>(r < r0 ? o + r * kAppD : a + (int64_t)s_src[r] * p.row_stride);
+  const int64_t items = (int64_t)pages * pairs;
+  // Two warps find an item's rows (a thread a row) one item ahead of the CTA:
+  // source rows, -1 - block row for those in the tail page; the page, -1 if
+  // anything fits no plan
+  auto find = [&](int64_t item, int to) {
+    const int pc = (int)(item / pairs);
+    int b = 0;  // the request: the last one with pre[b] <= pc
+    for (int hi = B - 1; b < hi;) {
+      const int mid = (b + hi + 1) >> 1;
+      if (pre[mid] <= pc)
+        b = mid;
+      else
+        hi = mid - 1;
     }
+    const int k0 = pc - pre[b], t = count[b] & 63;
+    const int r0 = k0 == 0 ? t : 0;           // the block's new rows: r0 .. 63
+    const int base = first[b] + k0 * 64 - t;  // kept row at block row r: base + r
+    const int slot = p.slots[base + r0], page = slot >> 6, tail = p.tails[b];
+    bool bad = slot < 0 || page >= p.pages || (r0 > 0 && (tail < 0 || tail >= p.tail_pages));
+    int src = -1 - tid;
+    if (tid >= r0) {
+      src = p.src_rows[base + tid];
+      bad = bad || src < 0 || src >= p.rows || p.slots[base + tid] != page * 64 + tid;
+    }
+    s_src[to][tid] = src;
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) s_at[to][warp] = make_int2(bad ? -1 : page, tail);
+  };
+  int buf = 0;
+  if (blockIdx.x < items && tid < 64) find(blockIdx.x, 0);
+  __syncthreads();
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
+    const int lh = (int)(item % pairs), layer = lh / p.Hkv, h = lh - layer * p.Hkv;
+    const int page = min(s_at[buf][0].x, s_at[buf][1].x), tail = s_at[buf][0].y;
+    const __nv_bfloat16* a = src_new + layer * p.layer_stride + h * kAppD + c;
+    const __nv_bfloat16* o = src_tail + (((int64_t)layer * p.tail_pages + tail) * p.Hkv + h) * 64 * kAppD + c;
+    uint4 v[8];
     unsigned m = 0;
+    if (page >= 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      m = max(m, max(max(kv8_mag(x[k].x), kv8_mag(x[k].y)), max(kv8_mag(x[k].z), kv8_mag(x[k].w))));
+      for (int k = 0; k < 8; ++k) {
+        const int src = s_src[buf][8 * k + g];
+        v[k] = __ldg(reinterpret_cast<const uint4*>(src < 0 ? o + (-1 - src) * kAppD : a + (int64_t)src * p.row_stride));
+      }
+    }
+    if (item + gridDim.x < items && tid < 64) find(item + gridDim.x, buf ^ 1);
+    if (page >= 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        m = max(m, max(max(kv8_mag(v[k].x), kv8_mag(v[k].y)), max(kv8_mag(v[k].z), kv8_mag(v[k].w))));
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) s_max[buf][warp] = m;
-    __syncthreads();  // one a pair: the next one writes the other buffer
+    __syncthreads();  // one an item: the next one writes the other buffers
+    if (page < 0) {
+      if (tid == 0) report_error(p.err, kErrInput);
+      continue;
+    }
 #pragma unroll
     for (int w = 0; w < 4; ++w) m = max(m, s_max[buf][half * 4 + w]);
     const int k2 = kv8_exponent<FMT>(m);
-    const float inv = __uint_as_float((unsigned)(127 - k2) << 23);  // 2^-k2, k2 in -100 .. 119
-    const int64_t at = (((int64_t)layer * p.pages + page) * p.Hkv + h);
-    if (u == 0) scales[at] = __uint_as_float((unsigned)(127 + k2) << 23);
+    const float inv = __uint_as_float((unsigned)(127 - k2) << 23);  // 2^-k2, k2 in -100 .. 120
+    const int64_t to = (((int64_t)layer * p.pages + page) * p.Hkv + h);
+    if (!in_bounds(p.err, to, (int64_t)p.layers * p.pages * p.Hkv)) continue;
+    if (u == 0) scales[to] = __uint_as_float((unsigned)(127 + k2) << 23);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 8 * k + g;
-      if (in_bounds(p.err, at, (int64_t)p.layers * p.pages * p.Hkv))
-        *reinterpret_cast<uint2*>(codes + (at * 64 + r) * kAppD + c) =
-            make_uint2(kv8_pack4<FMT>(x[k].x, x[k].y, inv), kv8_pack4<FMT>(x[k].z, x[k].w, inv));
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint2*>(codes + (to * 64 + 8 * k + g) * kAppD + c) =
+          make_uint2(kv8_pack4<FMT>(v[k].x, v[k].y, inv), kv8_pack4<FMT>(v[k].z, v[k].w, inv));
+  }
+
+  // ---- tail rows: the request's last (t + n) % 64 block rows, those of them
+  // that are new; 16 words of 16 bytes a row, keys and values. The last CTAs
+  // first (the first ones may have had a page more).
+  const int groups = (pairs + p.group - 1) / p.group;
+  const int64_t tails = (int64_t)B * groups;
+  for (int64_t item = gridDim.x - 1 - blockIdx.x; item < tails; item += gridDim.x) {
+    const int b = (int)(item / groups), lh0 = (int)(item - (int64_t)b * groups) * p.group;
+    const int n = count[b] >> 6, t = count[b] & 63, full = pre[b + 1] - pre[b];
+    const int r0 = full > 0 ? 0 : t, r1 = t + n - full * 64;  // block rows
+    if (n == 0 || r1 <= r0) continue;
+    const int base = first[b] + full * 64 - t, tail = p.new_tails[b];
+    bool bad = r1 > 64 || tail < 0 || tail >= p.tail_pages;
+    if (!bad && tid >= r0 && tid < r1) {
+      const int src = p.src_rows[base + tid];
+      bad = src < 0 || src >= p.rows || p.slots[base + tid] != -1 - tid;
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0) report_error(p.err, kErrInput);
+      continue;
+    }
+    const int total = (r1 - r0) * 32 * min(p.group, pairs - lh0);
+    constexpr int kBatch = 4;  // words a thread holds: their loads are in flight together
+    for (int w0 = tid; w0 < total; w0 += kBatch * kAppThreads) {
+      uint4 v[kBatch];
+      int64_t to[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int w = w0 + k * kAppThreads;
+        if (w < total) {
+          const int q = w >> 5, d = w & 31;  // d: 0 .. 15 keys, 16 .. 31 values
+          const int dl = q / (r1 - r0), r = r0 + q - dl * (r1 - r0);
+          const int lh = lh0 + dl, layer = lh / p.Hkv, h = lh - layer * p.Hkv;
+          v[k] = __ldg(reinterpret_cast<const uint4*>((d < 16 ? p.k_new : p.v_new) + layer * p.layer_stride +
+                                                      (int64_t)p.src_rows[base + r] * p.row_stride + h * kAppD +
+                                                      (d & 15) * 8));
+          to[k] = ((((int64_t)layer * p.tail_pages + tail) * p.Hkv + h) * 64 + r) * kAppD + (d & 15) * 8;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (w0 + k * kAppThreads < total &&
+            in_bounds(p.err, to[k] + 7, (int64_t)p.layers * p.tail_pages * p.Hkv * 64 * kAppD))
+          *reinterpret_cast<uint4*>(((tid & 31) < 16 ? p.k_tail : p.v_tail) + to[k]) = v[k];
     }
   }
 }
@@ -224,18 +284,22 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, int64_t row_
   p.k_tail = static_cast<__nv_bfloat16*>(k_tail);
   p.v_tail = static_cast<__nv_bfloat16*>(v_tail);
   p.err = err;
-  // piece numbers: see the search in the kernel
-  const int64_t numbers = rows / 64 + 2 * (int64_t)B;
-  // pairs per CTA: all of a layer's heads as long as that leaves every SM
-  // eight CTAs' worth of pieces, else fewer
-  const int64_t pairs = (int64_t)layers * Hkv;
-  int64_t heads = Hkv;
-  while (heads > 1 && numbers * ((pairs + heads - 1) / heads) < 8 * (int64_t)num_sms) heads = (heads + 1) / 2;
-  while ((pairs + heads - 1) / heads > 65535) heads *= 2;
-  p.heads = (int)heads;
-  const dim3 grid((unsigned)numbers, (unsigned)((pairs + heads - 1) / heads));
-  return fmt == 0 ? launch_pdl(kv8_append_kernel<0>, grid, dim3(kAppThreads), 0, stream, p)
-                  : launch_pdl(kv8_append_kernel<1>, grid, dim3(kAppThreads), 0, stream, p);
+  // four CTAs an SM (their registers), fewer where there is less that could be
+  // done: pages (one a request at most, and one for every 64 rows) and tails
+  const int64_t pairs = (int64_t)layers * Hkv, most = (int64_t)num_sms * 4;
+  int64_t group = (int64_t)B * pairs / (2 * most);  // tail items of two CTAs' turns, 1 .. 16 pairs each
+  group = group < 1 ? 1 : group > 16 ? 16 : group;
+  p.group = (int)group;
+  const int64_t items = (rows / 64 + (int64_t)B) * pairs, tail_items = B * ((pairs + group - 1) / group);
+  const int64_t ctas = items > tail_items ? items : tail_items;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  const size_t smem = ((size_t)3 * B + 1) * sizeof(int);
+  auto kernel = fmt == 0 ? kv8_append_kernel<0> : kv8_append_kernel<1>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kernel, grid, dim3(kAppThreads), smem, stream, p);
 }
 
 }  // namespace w4a16
