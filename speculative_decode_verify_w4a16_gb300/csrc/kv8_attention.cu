@@ -28,8 +28,8 @@
 // Online softmax: m is a reference per row, 7 below the maximum of s + log2 sv
 // when it was last set; it is raised again only when a weight would pass 2^15
 // (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is 2^-21
-// of the largest). One vote per tile over the four warps finds that; the
-// maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
+// of the largest). One vote per tile over the four warps (an mbarrier, whose
+// latency the exponentials cover) finds that; the maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
 // the first tile of a part, and seldom after it).
 //
 // Code that runs once per part (the query rows, the first maximum, the end) is
@@ -94,20 +94,8 @@ __device__ __forceinline__ void ka_widen(uint32_t in, uint32_t& lo, uint32_t& hi
       : "=r"(lo), "=r"(hi)
       : "r"(in));
 }
-// named barrier over one softmax warpgroup, and the same with a vote
+// named barrier over one softmax warpgroup
 __device__ __forceinline__ void ka_bar(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool ka_bar_any(int id, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\t"
-      "setp.ne.u32 a, %1, 0;\n\t"
-      "barrier.cta.red.or.pred b, %2, 128, a;\n\t"
-      "selp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(id)
-      : "memory");
-  return r != 0;
-}
 // two fp32 lanes in one 64-bit register, for the paired fp32 instructions
 __device__ __forceinline__ uint64_t ka_2(float lo, float hi) {
   uint64_t r;
@@ -246,8 +234,9 @@ struct KaCfg {
   static constexpr int kGmOff = kMaskOff + NP * 8;            // float4 [NP / 2]: g, g, -m, -m of two rows
   static constexpr int kPartOff = kGmOff + NP * 8;            // float [4][NP]
   static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
-  static constexpr int kBarOff = kRowOff + NP * 4;
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 14;
+  static constexpr int kScaleOff = kRowOff + NP * 4;          // float4 [16][2]: a tile's blocks
+  static constexpr int kBarOff = kScaleOff + 16 * 2 * 16;
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 12 + 2 * kGroups;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
   // TMEM columns: scores (two terms) of two tiles, O^T, then V^T of two tiles
   // (fp16 pairs along the keys: 64 columns)
@@ -347,20 +336,22 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint64_t* pv_done = p_full + 2;  // [2]
   uint64_t* q_ready = pv_done + 2;
   uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
-  uint64_t* s_free = x_full + 1;   // [2] scores read
-  uint64_t* mma_fin = s_free + 2;  // [2]
+  uint64_t* mma_fin = x_full + 1;  // [2]
+  uint64_t* votes = mma_fin + 2;   // [softmax warpgroup][2]
+  float4* scale_s = reinterpret_cast<float4*>(smem + C::kScaleOff);  // tile tc, block half: 2 (tc % 16) + half
   __shared__ uint32_t tmem_s;
   __shared__ unsigned scan_s[32];
   __shared__ unsigned s_pre;
   __shared__ int s_b, s_last;
   __shared__ int par_s[64];
   __shared__ unsigned long long bad_s[4];
+  __shared__ int over_s[4][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   grid_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&k_full[s], 1);
+      mbar_init(&k_full[s], 2);  // the copies, and the scales (or nothing)
       mbar_init(&k_free[s], 1);
     }
     for (int s = 0; s < SV; ++s) {
@@ -372,8 +363,11 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       mbar_init(&s_full[k], 1);
       mbar_init(&p_full[k], 4 * C::kGroups);
       mbar_init(&pv_done[k], 1);
-      mbar_init(&s_free[k], 4 * C::kGroups);
       mbar_init(&mma_fin[k], 1);
+      for (int g = 0; g < C::kGroups; ++g) {
+        mbar_init(&votes[2 * g + k], 4);
+        over_s[g][k] = -1;
+      }
     }
     mbar_init(q_ready, 4 * C::kGroups);
     mbar_init(x_full, 1);
@@ -455,7 +449,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   }
   KaSeg sg;
   int issued = 0;
-
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     // K stages are used in order; a bf16 tile takes two neighbours (32 KB), and
@@ -463,7 +456,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     // passed one too, completes a phase of its full and its free barrier.
     // (A bf16 tile's values have a buffer of their own: the widening warps ask
     // for them.)
-    int kc = 0, vc = 0;  // uses of the K and V stages
+    int kc = 0, vc = 0, tc = 0;  // uses of the K and V stages, tiles so far
     int k_more = 0;      // a use of K whose tile was given up
     bool ok = true;
     auto k_wait = [&](int use) {
@@ -475,7 +468,10 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         const int t = sg.len & 63;
         const bool pass = kc % S == S - 1;
         if (lane == 0) {
-          if (pass && (ok = k_wait(kc))) mbar_arrive(&k_full[S - 1]);
+          if (pass && (ok = k_wait(kc))) {
+            mbar_arrive(&k_full[S - 1]);
+            mbar_arrive(&k_full[S - 1]);
+          }
           const int use = kc + (pass ? 1 : 0), s = use % S;
           ok = ok && k_wait(use) && k_wait(use + 1);
           if (ok) {
@@ -483,7 +479,10 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
             if (t > 0 && !tok) report_error(p.err, kErrInput);
             uint8_t* kd = smem + C::kKOff + s * C::kTileBytes;
+            scale_s[2 * (tc & 15)] = scale_s[2 * (tc & 15) + 1] = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
             mbar_arrive(&k_full[s + 1]);
+            mbar_arrive(&k_full[s + 1]);
+            mbar_arrive(&k_full[s]);
             mbar_arrive_expect_tx(&k_full[s], (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
             for (int h = 0; h < 2; ++h) {
               if (tok) tma_load_3d(kd + h * C::kTileBytes, &maps.k_tail, 64 * h, 0, tail * p.Hkv + kvh, &k_full[s]);
@@ -493,35 +492,64 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         if (ok) kc += pass ? 3 : 2;
+        ++tc;
       }
-      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1; the page
-      // ids of 16 tiles at a time in the lanes
-      const int full = sg.len / 64;
+      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1. Lane 2 k + h
+      // has block h of the k-th of 16 tiles, its page and scales; the next 16
+      // tiles' are asked for ahead.
+      const int full = sg.len / 64, i0 = max(sg.lo, 1);
       const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
-      const int i0 = max(sg.lo, 1);
-      int page = 0;
-      for (int i = i0; ok && i < sg.hi; ++i) {
+      auto page_of = [&](int i) {  // of the 16 tiles from i on; -2: no such block
+        const int blk = 2 * (i - 1) + lane;
+        return blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
+      };
+      int page = -2, page_n = page_of(i0);
+      float sk = 0.0f, lsv = 0.0f, isv = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
+      auto scales_of = [&]() {  // of the pages asked for earlier
+        sk_n = 0.0f;
+        sv_n = 1.0f;
+        if (page_n >= 0 && page_n < p.pages) {
+          sk_n = p.k_scale[(int64_t)page_n * p.Hkv + kvh];
+          sv_n = p.v_scale[(int64_t)page_n * p.Hkv + kvh];
+        } else if (page_n != -2) {
+          report_error(p.err, kErrInput);
+          page_n = -1;
+        }
+      };
+      scales_of();
+#pragma unroll 1
+      for (int i = i0; ok && i < sg.hi; ++i, ++tc) {
         const int k = (i - i0) & 15;
         if (k == 0) {
-          const int blk = 2 * (i - 1) + lane;
-          page = blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
-          if (page != -2 && (page < 0 || page >= p.pages)) {
-            report_error(p.err, kErrInput);
-            page = -2;
-          }
+          page = page_n;
+          page_n = page_of(i + 16);
+        } else if (k == 8) {
+          scales_of();
         }
         const int pa = __shfl_sync(0xffffffffu, page, 2 * k), pb = __shfl_sync(0xffffffffu, page, 2 * k + 1);
+        // a page that is not there: past the tensor's end, filled with zeros
+        const int none = p.pages * p.Hkv, ks = kc % S, vs = vc % SV;
+        const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
         if (lane == 0) {
-          // a page that is not there: past the tensor's end, filled with zeros
-          const int none = p.pages * p.Hkv;
-          const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
-          const int ks = kc % S, vs = vc % SV;
           ok = k_wait(kc);
           if (ok) {
             uint8_t* kd = smem + C::kKOff + ks * C::kTileBytes;
             mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
             tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
             tma_load_3d(kd + 8192, &maps.k, 0, 0, zb, &k_full[ks]);
+          }
+        }
+        // key scale, log2 of the value scale, its inverse, 1 for no block
+        if (k == 0) {
+          sk = sk_n;
+          lsv = log2f(sv_n);
+          isv = 1.0f / sv_n;
+        }
+        if ((lane >> 1) == k) scale_s[2 * (tc & 15) + (lane & 1)] = make_float4(sk, lsv, isv, page == -2 ? 1.0f : 0.0f);
+        __syncwarp();
+        if (lane == 0) {
+          if (ok) {
+            mbar_arrive(&k_full[ks]);
             k_more = 1;
             if (vc >= SV) ok = ka_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
           }
@@ -585,8 +613,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     if (issued) umma_commit_warp(&mma_fin[0]);
   } else if (warp == 3) {
     // ------------------------------------------------------------ S^T MMAs
-    // (a warp of its own: a tile's scores go out as soon as the scores two
-    // tiles before have been read, whatever P V waits for)
+    // (a warp of its own: a tile's scores go out when P V of two tiles before
+    // is complete, so that a tile whose scores are there also has its P buffer)
     constexpr uint32_t id_s8 = umma_idesc(2 * NP, (uint32_t)FMT, 0u, 0u, 0u);
     constexpr uint32_t id_s16 = umma_idesc(NP, 1u, 1u, 0u, 0u);
     const uint32_t kb = smem_u32(smem + C::kKOff);
@@ -599,7 +627,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
 #pragma unroll 1
       for (int i = sg.lo; ok && i < sg.hi; ++i, ++tc) {
         const uint32_t d = tmem + (uint32_t)(tc & 1) * 2u * NP;
-        if (tc >= 2) ok = ka_wait(&s_free[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err);
+        if (tc >= 2) ok = ka_wait(&pv_done[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err);
         if (i == 0 && kc % S == S - 1) {  // the stage that the producer passed over
           ok = ka_wait(&k_full[S - 1], (uint32_t)(kc / S) & 1u, p.err, ok);
           umma_commit_warp(&k_free[S - 1]);
@@ -845,59 +873,30 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       uint64_t l[Q / 2];
 #pragma unroll
       for (int q = 0; q < Q / 2; ++q) l[q] = 0ull;
-      // ---- scales of this warp's block of each tile, 32 tiles at a time (a
-      // lane a tile), the next ones asked for ahead
-      const int half = qd >> 1, full = sg.len / 64, i1 = max(sg.lo, 1);
-      const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
-      auto page_of = [&](int base) {
-        const int i = base + lane, blk = 2 * (i - 1) + half;
-        if (i >= sg.hi || blk >= full) return -2;
-        const int pg = tab[blk];
-        return pg < 0 || pg >= p.pages ? -1 : pg;
-      };
-      int pg = 0, pg_n = page_of(i1);
-      float sk_l = 0.0f, lsv_l = 0.0f, isv_l = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
-      if (pg_n >= 0) {
-        sk_n = p.k_scale[(int64_t)pg_n * p.Hkv + kvh];
-        sv_n = p.v_scale[(int64_t)pg_n * p.Hkv + kvh];
-      }
+      const int half = qd >> 1;
 #pragma unroll 1
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
         const int buf = tc & 1;
         const bool bf = i == 0;
-        float sk = 1.0f, lsv = 0.0f, isv = 1.0f;
         uint32_t see = 0xFFFFu;  // rows for which the thread's key counts
-        if (!bf) {
-          const int k = (i - i1) & 31;
-          if (k == 0) {
-            pg = pg_n;
-            sk_l = sk_n;
-            lsv_l = log2f(sv_n);
-            isv_l = 1.0f / sv_n;
-          }
-          if (k == 8) pg_n = page_of(i + 24);
-          if (k == 20) {
-            sk_n = pg_n >= 0 ? p.k_scale[(int64_t)pg_n * p.Hkv + kvh] : 0.0f;
-            sv_n = pg_n >= 0 ? p.v_scale[(int64_t)pg_n * p.Hkv + kvh] : 1.0f;
-          }
-          sk = __shfl_sync(0xffffffffu, sk_l, k);
-          lsv = __shfl_sync(0xffffffffu, lsv_l, k);
-          isv = __shfl_sync(0xffffffffu, isv_l, k);
-          if (__shfl_sync(0xffffffffu, pg, k) == -2) see = 0u;  // no such block
-        } else if (key < 64) {
-          const int tail = p.tails[sg.b];
-          if (key >= (sg.len & 63) || tail < 0 || tail >= p.tail_pages) see = 0u;
-        } else {
-          see = 0u;
+        if (bf) {
+          if (key < 64) {
+            const int tail = p.tails[sg.b];
+            if (key >= (sg.len & 63) || tail < 0 || tail >= p.tail_pages) see = 0u;
+          } else {
+            see = 0u;
 #pragma unroll 1
-          for (int q = 0; q < Q; ++q) see |= (uint32_t)((mask_s[qa + q] >> (key - 64)) & 1ull) << q;
+            for (int q = 0; q < Q; ++q) see |= (uint32_t)((mask_s[qa + q] >> (key - 64)) & 1ull) << q;
+          }
         }
         ok = ka_wait(&s_full[buf], (uint32_t)(tc >> 1) & 1u, p.err, ok);
         tc_fence_after();
         // ---- t = s + log2 sv - m, two rows an instruction
         float t[Q];
         const uint32_t sc = trow + (uint32_t)buf * 2u * NP + (uint32_t)qa;
-        const uint64_t sk2 = ka_2(sk, sk), lsv2 = ka_2(lsv, lsv), c32 = ka_2(0.03125f, 0.03125f);
+        const float4 blk = scale_s[2 * (tc & 15) + half];  // key scale, log2 value scale, its inverse
+        if (blk.w != 0.0f) see = 0u;                       // no such block
+        const uint64_t sk2 = ka_2(blk.x, blk.x), lsv2 = ka_2(blk.y, blk.y), c32 = ka_2(0.03125f, 0.03125f);
 #pragma unroll
         for (int q0 = 0; q0 < Q; q0 += 8) {
           uint32_t u1[8], u2[8];
@@ -912,28 +911,30 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             ka_un2(ka_fma2(x, ka_mul2(ka_2(w.x, w.y), sk2), ka_add2(ka_2(w.z, w.w), lsv2)), t[q0 + q], t[q0 + q + 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[buf]);
         if (__any_sync(0xffffffffu, see != 0xFFFFu)) {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
             if (!((see >> q) & 1u)) t[q] = -INFINITY;
         }
         // ---- is m to be set, or does a weight pass the limit?
-        bool raise = i == sg.lo;
-        if (!raise) {
-          float over = -INFINITY;
+        float over = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
-          raise = ka_bar_any(bar, over > kKaLimit);
-        }
+        for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
+        uint64_t* vote = &votes[2 * wg + buf];
+        if (__any_sync(0xffffffffu, over > kKaLimit) && lane == 0) over_s[wg][buf] = tc;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vote);
+        // the weights, in case; the vote's latency is theirs
+        float e[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) e[q] = ka_ex2(t[q]);
+        ok = ka_wait(vote, (uint32_t)(tc >> 1) & 1u, p.err, ok);
+        const bool raise = i == sg.lo || over_s[wg][buf] == tc;
         if (raise) {
           {
-            float x[Q];
 #pragma unroll
-            for (int q = 0; q < Q; ++q) x[q] = t[q];
-            const float mx = ka_reduce16<true>(x, lane);
+            for (int q = 0; q < Q; ++q) e[q] = t[q];
+            const float mx = ka_reduce16<true>(e, lane);
             if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = mx;
           }
           ka_bar(bar);
@@ -944,7 +945,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           const float f = ka_ex2(-d);
           if (qd == 0 && lane < 16) gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
 #pragma unroll
-          for (int q = 0; q < Q; ++q) t[q] -= __shfl_sync(0xffffffffu, d, q);
+          for (int q = 0; q < Q; ++q) e[q] = ka_ex2(t[q] - __shfl_sync(0xffffffffu, d, q));
           if (i > sg.lo) {
 #pragma unroll
             for (int q = 0; q < Q; q += 2)
@@ -966,26 +967,21 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           }
           ka_bar(bar);  // the new m, and part_s read
         }
-        // ---- P, into the buffer that P V (i - 2) has left
-        if (tc >= 2) ok = ka_wait(&pv_done[buf], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
+        // ---- P (P V (i - 2) has left its buffer)
         uint4* pd = reinterpret_cast<uint4*>(smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16);
-        const uint64_t isv2 = ka_2(isv, isv);
+        const uint64_t isv2 = ka_2(blk.z, blk.z);
 #pragma unroll
-        for (int q = 0; q < Q; q += 2) {
-          t[q] = ka_ex2(t[q]);
-          t[q + 1] = ka_ex2(t[q + 1]);
-          l[q / 2] = ka_fma2(ka_2(t[q], t[q + 1]), isv2, l[q / 2]);
-        }
+        for (int q = 0; q < Q; q += 2) l[q / 2] = ka_fma2(ka_2(e[q], e[q + 1]), isv2, l[q / 2]);
         if (bf) {
 #pragma unroll
           for (int q = 0; q < Q; q += 8)
-            pd[q * 16] = make_uint4(ka_bf162(t[q], t[q + 1]), ka_bf162(t[q + 2], t[q + 3]), ka_bf162(t[q + 4], t[q + 5]),
-                                    ka_bf162(t[q + 6], t[q + 7]));
+            pd[q * 16] = make_uint4(ka_bf162(e[q], e[q + 1]), ka_bf162(e[q + 2], e[q + 3]), ka_bf162(e[q + 4], e[q + 5]),
+                                    ka_bf162(e[q + 6], e[q + 7]));
         } else {
 #pragma unroll
           for (int q = 0; q < Q; q += 8)
-            pd[q * 16] = make_uint4(ka_half2(t[q], t[q + 1]), ka_half2(t[q + 2], t[q + 3]), ka_half2(t[q + 4], t[q + 5]),
-                                    ka_half2(t[q + 6], t[q + 7]));
+            pd[q * 16] = make_uint4(ka_half2(e[q], e[q + 1]), ka_half2(e[q + 2], e[q + 3]), ka_half2(e[q + 4], e[q + 5]),
+                                    ka_half2(e[q + 6], e[q + 7]));
         }
         fence_proxy_async_smem();
         tc_fence_before();
