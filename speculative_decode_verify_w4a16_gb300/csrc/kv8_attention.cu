@@ -287,21 +287,23 @@ __device__ __noinline__ void ka_merge(const Kv8AttnParams& p, const KaWork& wk, 
 #pragma unroll 4
   for (unsigned k = 0; k < parts; ++k)
     M = fmaxf(M, __ldcg(&wk.part_ml[(k ? 2u * (c0 + k) : s0) * NP + r]).x);
-  float l = 0.0f, o[16];
+  float l = 0.0f, o[16], x[16];
+  auto load = [&](unsigned k) {
+    const float* src = wk.part_o + ((size_t)(k ? 2u * (c0 + k) : s0) * NP + qa) * kKaD + d;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) x[q] = __ldcg(src + q * kKaD);
+  };
+  load(0u);
 #pragma unroll
   for (int q = 0; q < 16; ++q) o[q] = 0.0f;
 #pragma unroll 1
   for (unsigned k = 0; k < parts; ++k) {
-    const unsigned slot = k ? 2u * (c0 + k) : s0;
-    const float* src = wk.part_o + ((size_t)slot * NP + qa) * kKaD + d;
-    float x[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) x[q] = __ldcg(src + q * kKaD);
-    const float2 ml = __ldcg(&wk.part_ml[slot * NP + r]);
+    const float2 ml = __ldcg(&wk.part_ml[(k ? 2u * (c0 + k) : s0) * NP + r]);
     const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);
     l = fmaf(w, ml.y, l);
 #pragma unroll
     for (int q = 0; q < 16; ++q) o[q] = fmaf(__shfl_sync(0xffffffffu, w, q), x[q], o[q]);
+    if (k + 1 < parts) load(k + 1);
   }
   const float inv = 1.0f / l;
 #pragma unroll
@@ -781,24 +783,25 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     const int bar = 1 + wg;
     const int G = p.H / p.Hkv, rows = p.n * G;
     const float4* gm = reinterpret_cast<const float4*>(gm_s) + (qa >> 1);
-    // the query row of a part that the thread loads: eight lanes a row, 16
-    // columns each
-    auto load_q = [&](const KaSeg& g, uint4 (&v)[2]) {
+    // where the thread's 16 columns of a part's query row are (eight lanes a
+    // row); null for a row that does not exist
+    auto q_at = [&](const KaSeg& g) {
       const int kvh = g.u / wk.row_blocks, R = (g.u - kvh * wk.row_blocks) * NP + qa + (st >> 3), j = R / G;
-      v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
-      if (R < rows) {
-        const uint4* at = reinterpret_cast<const uint4*>(p.q + ((int64_t)g.b * p.n + j) * p.q_stride +
-                                                         (kvh * G + R - j * G) * kKaD) + 2 * (st & 7);
-        v[0] = at[0];
-        v[1] = at[1];
-      }
+      return R < rows ? p.q + ((int64_t)g.b * p.n + j) * p.q_stride + (kvh * G + R - j * G) * kKaD + 16 * (st & 7)
+                      : nullptr;
     };
     int tc = 0, seg = 0;
     bool ok = true;
-    uint4 v[2];
-    bool more = ka_next(p, it, sg);
-    if (more) load_q(sg, v);
+    KaSeg nx;
+    bool more = ka_next(p, it, nx);
     while (more) {
+      sg = nx;
+      const uint4* q_now = reinterpret_cast<const uint4*>(q_at(sg));
+      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      if (q_now) {
+        v[0] = q_now[0];
+        v[1] = q_now[1];
+      }
       const int kvh = sg.u / wk.row_blocks, rb = sg.u - kvh * wk.row_blocks;
       // ---- Q: x = q 2^ex, |x| < 256, as bf16 and as two e4m3 terms
       {
@@ -869,6 +872,12 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           }
           ka_bar(bar);
         }
+      }
+      // the next part's query rows on their way to L2
+      more = ka_next(p, it, nx);
+      if (more) {
+        const __nv_bfloat16* next = q_at(nx);
+        if (next && !(st & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(next));
       }
       uint64_t l[Q / 2];
 #pragma unroll
@@ -988,11 +997,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // ---- the end of the unit's part: the rows' sums over the keys, then
-      // O^T. The next part's query rows are asked for first.
-      KaSeg nx;
-      more = ka_next(p, it, nx);
-      if (more) load_q(nx, v);
+      // ---- the end of the unit's part: the rows' sums over the keys, then O^T
       {
         float x[Q];
 #pragma unroll
@@ -1015,30 +1020,40 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       tc_fence_after();
       const unsigned long long bad = sg.lo == 0 ? bad_s[seg & 3] : 0ull;
       if (bad) ka_add_bad<Q>(p, sg.b, kvh, bad, mask_s + qa, trow + C::kOCol + (uint32_t)qa, key);
+      // whole: the rows as bf16 through the warpgroup's chunk of a P buffer (no
+      // MMA reads it any more), 256 bytes each, and out 16 bytes a thread
+      __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem + C::kPOff + (qa >> 3) * 2048);
 #pragma unroll 1
       for (int q0 = 0; q0 < Q; q0 += 8) {
         uint32_t o[8];
         tmem_ld_32x32b<8>(trow + C::kOCol + (uint32_t)(qa + q0), o);
         tmem_wait_ld();
-        const int r = qa + q0;
         if (whole) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float x = __uint_as_float(o[q]) * __shfl_sync(0xffffffffu, inv, q0 + q);
-            if (row_s[r + q] >= 0) p.out[(int64_t)row_s[r + q] * kKaD + key] = __float2bfloat16_rn(x);
-          }
+          for (int q = 0; q < 8; ++q)
+            stage[(q0 + q) * kKaD + key] =
+                __float2bfloat16_rn(__uint_as_float(o[q]) * __shfl_sync(0xffffffffu, inv, q0 + q));
         } else {
-          float* dst = wk.part_o + ((size_t)slot * NP + r) * kKaD + key;
+          float* dst = wk.part_o + ((size_t)slot * NP + qa + q0) * kKaD + key;
 #pragma unroll
           for (int q = 0; q < 8; ++q) dst[q * kKaD] = __uint_as_float(o[q]);
+        }
+      }
+      if (whole) {
+        ka_bar(bar);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int q = (st >> 4) + 8 * k;
+          if (row_s[qa + q] >= 0)
+            reinterpret_cast<uint4*>(p.out + (int64_t)row_s[qa + q] * kKaD)[st & 15] =
+                reinterpret_cast<const uint4*>(stage)[q * 16 + (st & 15)];
         }
       }
       if (!whole) {
         // ---- the last of the unit's CTAs merges the parts
         const unsigned u0 = sg.at - (unsigned)sg.lo;  // the unit's first tile
         const unsigned c0 = runs.owner(u0), parts = runs.owner(u0 + (unsigned)sg.nt - 1u) - c0 + 1u;
-        __threadfence();
-        ka_bar_all<C::kGroups>();
+        ka_bar_all<C::kGroups>();  // (the counter's release covers what the barrier has gathered)
         if (warp == C::kSoft0 && lane == 0) {
           s_last = atomic_add_acq_rel(&wk.done[c0], 1) == (int)parts - 1;
           if (s_last) wk.done[c0] = 0;
@@ -1051,7 +1066,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       }
       tc_fence_before();
       ka_bar(bar);  // the small arrays are free for the next part
-      sg = nx;
       ++seg;
     }
   }
