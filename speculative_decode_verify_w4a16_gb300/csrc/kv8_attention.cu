@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   using C = KaCfg<NP>;
   constexpr int S = C::kStages, SV = C::kVStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the next 1024-byte boundary, by an offset: through an integer the compiler
+  // would lose sight of the address space and load and store generically
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* mask_s = reinterpret_cast<uint64_t*>(smem + C::kMaskOff);
   float* gm_s = reinterpret_cast<float*>(smem + C::kGmOff);  // row r: g at 4 (r / 2) + r % 2, -m two on
   float* part_s = reinterpret_cast<float*>(smem + C::kPartOff);
