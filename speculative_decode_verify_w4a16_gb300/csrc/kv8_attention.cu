@@ -28,8 +28,8 @@
 // Online softmax: m is a reference per row, 7 below the maximum of s + log2 sv
 // when it was last set; it is raised again only when a weight would pass 2^15
 // (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is 2^-21
-// of the largest). One vote per tile over the four warps (an mbarrier, whose
-// latency the exponentials cover) finds that; the maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
+// of the largest). One vote per tile over the four warps finds that; the
+// maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
 // the first tile of a part, and seldom after it).
 //
 // Code that runs once per part (the query rows, the first maximum, the end) is
@@ -96,6 +96,19 @@ __device__ __forceinline__ void ka_widen(uint32_t in, uint32_t& lo, uint32_t& hi
 }
 // named barrier over one softmax warpgroup
 __device__ __forceinline__ void ka_bar(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+// ... and with a vote: whether p holds in any of its threads
+__device__ __forceinline__ bool ka_bar_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, %2, 128, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return r != 0;
+}
 // two fp32 lanes in one 64-bit register, for the paired fp32 instructions
 __device__ __forceinline__ uint64_t ka_2(float lo, float hi) {
   uint64_t r;
@@ -129,17 +142,14 @@ __device__ __noinline__ bool ka_wait_long(uint64_t* bar, uint32_t parity, unsign
   return mbar_wait(bar, parity, err);
 }
 // Bounded wait by a whole warp, or by one thread: every lane tests the same
-// barrier. The first tests do not ask the hardware to suspend (these hand-offs
-// are short, and a suspended thread wakes up late). Once a wait has run out
-// (still false) the later ones return at once: the warps that meet at named
-// barriers then walk through the rest of their work, on garbage and in bounds,
-// instead of leaving the others waiting.
+// barrier (a hint of a microsecond: the hardware wakes the warp when the phase
+// completes, and a polling loop takes issue slots from the other warps). Once a
+// wait has run out (still false) the later ones return at once: the warps that
+// meet at named barriers then walk through the rest of their work, on garbage
+// and in bounds, instead of leaving the others waiting.
 __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, unsigned* err, bool still = true) {
-  if (!still) return false;
-#pragma unroll 1
-  for (int k = 0; k < 64; ++k)
-    if (mbar_try_wait(bar, parity)) return true;
-  return ka_wait_long(bar, parity, err);
+  if (still && !mbar_try_wait(bar, parity, 1000u)) still = ka_wait_long(bar, parity, err);
+  return still;
 }
 
 __device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
@@ -236,7 +246,7 @@ struct KaCfg {
   static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
   static constexpr int kScaleOff = kRowOff + NP * 4;          // float4 [16][2]: a tile's blocks
   static constexpr int kBarOff = kScaleOff + 16 * 2 * 16;
-  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 12 + 2 * kGroups;
+  static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 12;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
   // TMEM columns: scores (two terms) of two tiles, O^T, then V^T of two tiles
   // (fp16 pairs along the keys: 64 columns)
@@ -341,7 +351,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint64_t* q_ready = pv_done + 2;
   uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
   uint64_t* mma_fin = x_full + 1;  // [2]
-  uint64_t* votes = mma_fin + 2;   // [softmax warpgroup][2]
   float4* scale_s = reinterpret_cast<float4*>(smem + C::kScaleOff);  // tile tc, block half: 2 (tc % 16) + half
   __shared__ uint32_t tmem_s;
   __shared__ unsigned scan_s[32];
@@ -349,7 +358,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   __shared__ int s_b, s_last;
   __shared__ int par_s[64];
   __shared__ unsigned long long bad_s[4];
-  __shared__ int over_s[4][2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   grid_launch_dependents();
@@ -368,10 +376,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       mbar_init(&p_full[k], 4 * C::kGroups);
       mbar_init(&pv_done[k], 1);
       mbar_init(&mma_fin[k], 1);
-      for (int g = 0; g < C::kGroups; ++g) {
-        mbar_init(&votes[2 * g + k], 4);
-        over_s[g][k] = -1;
-      }
     }
     mbar_init(q_ready, 4 * C::kGroups);
     mbar_init(x_full, 1);
@@ -906,7 +910,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         float t[Q];
         const uint32_t sc = trow + (uint32_t)buf * 2u * NP + (uint32_t)qa;
         const float4 blk = scale_s[2 * (tc & 15) + half];  // key scale, log2 value scale, its inverse
-        if (blk.w != 0.0f) see = 0u;                       // no such block
         const uint64_t sk2 = ka_2(blk.x, blk.x), lsv2 = ka_2(blk.y, blk.y), c32 = ka_2(0.03125f, 0.03125f);
 #pragma unroll
         for (int q0 = 0; q0 < Q; q0 += 8) {
@@ -922,30 +925,29 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
             ka_un2(ka_fma2(x, ka_mul2(ka_2(w.x, w.y), sk2), ka_add2(ka_2(w.z, w.w), lsv2)), t[q0 + q], t[q0 + q + 1]);
           }
         }
-        if (__any_sync(0xffffffffu, see != 0xFFFFu)) {
+        if (blk.w != 0.0f) {  // no such block
+#pragma unroll
+          for (int q = 0; q < Q; ++q) t[q] = -INFINITY;
+        }
+        if (bf) {
 #pragma unroll
           for (int q = 0; q < Q; ++q)
             if (!((see >> q) & 1u)) t[q] = -INFINITY;
         }
         // ---- is m to be set, or does a weight pass the limit?
-        float over = -INFINITY;
+        bool raise = i == sg.lo;
+        if (!raise) {
+          float over = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
-        uint64_t* vote = &votes[2 * wg + buf];
-        if (__any_sync(0xffffffffu, over > kKaLimit) && lane == 0) over_s[wg][buf] = tc;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vote);
-        // the weights, in case; the vote's latency is theirs
-        float e[Q];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) e[q] = ka_ex2(t[q]);
-        ok = ka_wait(vote, (uint32_t)(tc >> 1) & 1u, p.err, ok);
-        const bool raise = i == sg.lo || over_s[wg][buf] == tc;
+          for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
+          raise = ka_bar_any(bar, over > kKaLimit);
+        }
         if (raise) {
           {
+            float x[Q];
 #pragma unroll
-            for (int q = 0; q < Q; ++q) e[q] = t[q];
-            const float mx = ka_reduce16<true>(e, lane);
+            for (int q = 0; q < Q; ++q) x[q] = t[q];
+            const float mx = ka_reduce16<true>(x, lane);
             if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = mx;
           }
           ka_bar(bar);
@@ -956,7 +958,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           const float f = ka_ex2(-d);
           if (qd == 0 && lane < 16) gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
 #pragma unroll
-          for (int q = 0; q < Q; ++q) e[q] = ka_ex2(t[q] - __shfl_sync(0xffffffffu, d, q));
+          for (int q = 0; q < Q; ++q) t[q] -= __shfl_sync(0xffffffffu, d, q);
           if (i > sg.lo) {
 #pragma unroll
             for (int q = 0; q < Q; q += 2)
@@ -982,17 +984,21 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         uint4* pd = reinterpret_cast<uint4*>(smem + C::kPOff + buf * C::kPBytes + (qa >> 3) * 2048 + key * 16);
         const uint64_t isv2 = ka_2(blk.z, blk.z);
 #pragma unroll
-        for (int q = 0; q < Q; q += 2) l[q / 2] = ka_fma2(ka_2(e[q], e[q + 1]), isv2, l[q / 2]);
+        for (int q = 0; q < Q; q += 2) {
+          t[q] = ka_ex2(t[q]);
+          t[q + 1] = ka_ex2(t[q + 1]);
+          l[q / 2] = ka_fma2(ka_2(t[q], t[q + 1]), isv2, l[q / 2]);
+        }
         if (bf) {
 #pragma unroll
           for (int q = 0; q < Q; q += 8)
-            pd[q * 16] = make_uint4(ka_bf162(e[q], e[q + 1]), ka_bf162(e[q + 2], e[q + 3]), ka_bf162(e[q + 4], e[q + 5]),
-                                    ka_bf162(e[q + 6], e[q + 7]));
+            pd[q * 16] = make_uint4(ka_bf162(t[q], t[q + 1]), ka_bf162(t[q + 2], t[q + 3]), ka_bf162(t[q + 4], t[q + 5]),
+                                    ka_bf162(t[q + 6], t[q + 7]));
         } else {
 #pragma unroll
           for (int q = 0; q < Q; q += 8)
-            pd[q * 16] = make_uint4(ka_half2(e[q], e[q + 1]), ka_half2(e[q + 2], e[q + 3]), ka_half2(e[q + 4], e[q + 5]),
-                                    ka_half2(e[q + 6], e[q + 7]));
+            pd[q * 16] = make_uint4(ka_half2(t[q], t[q + 1]), ka_half2(t[q + 2], t[q + 3]), ka_half2(t[q + 4], t[q + 5]),
+                                    ka_half2(t[q + 6], t[q + 7]));
         }
         fence_proxy_async_smem();
         tc_fence_before();
