@@ -379,8 +379,14 @@ def kv8_cache(layers: int, pages: int, B: int, Hkv: int, D: int = 128, dtype: to
     return KV8Cache(*codes, *scales, *tails)
 
 
-def _need_cache(c: KV8Cache):
-    k = c.k
+def _is(t: torch.Tensor, dtype: torch.dtype, dev: int, shape) -> bool:
+    """What _need accepts, for the calls of a decode step: _need says what is
+    wrong with the rest."""
+    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
+
+
+def _need_cache(c: KV8Cache, dev: int):
+    k, k_tail = c.k, c.k_tail
     shape = k.shape
     layers, pages, Hkv, block, D = shape
     dtype = k.dtype
@@ -388,26 +394,26 @@ def _need_cache(c: KV8Cache):
         raise ValueError("the cache's codes must be torch.float8_e4m3fn or torch.float8_e5m2")
     if block != KV_BLOCK:
         raise ValueError(f"a page holds {KV_BLOCK} tokens, the cache has {block}")
-    _need(k, "cache.k", dtype)
-    _need(c.v, "cache.v", dtype, shape)
-    _need(c.k_scale, "cache.k_scale", torch.float32, shape[:3])
-    _need(c.v_scale, "cache.v_scale", torch.float32, shape[:3])
-    tail_pages = c.k_tail.shape[1]
-    tail = (layers, tail_pages, Hkv, KV_BLOCK, D)
-    _need(c.k_tail, "cache.k_tail", torch.bfloat16, tail)
-    _need(c.v_tail, "cache.v_tail", torch.bfloat16, tail)
+    tail_pages = k_tail.shape[1]
+    f32, bf16 = torch.float32, torch.bfloat16
+    heads, tail = (layers, pages, Hkv), (layers, tail_pages, Hkv, KV_BLOCK, D)
+    if not (_is(k, dtype, dev, shape) and _is(c.v, dtype, dev, shape) and _is(c.k_scale, f32, dev, heads)
+            and _is(c.v_scale, f32, dev, heads) and _is(k_tail, bf16, dev, tail) and _is(c.v_tail, bf16, dev, tail)):
+        for name, dt, sh in (("k", dtype, shape), ("v", dtype, shape), ("k_scale", f32, heads),
+                             ("v_scale", f32, heads), ("k_tail", bf16, tail), ("v_tail", bf16, tail)):
+            _need(getattr(c, name), f"cache.{name}", dt, sh)
     return layers, pages, tail_pages, Hkv, D
 
 
-def _need_rows(t: torch.Tensor, name: str, shape) -> int:
+def _need_rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """A bf16 tensor [.., tokens, heads, D] whose heads are dense and whose
     tokens are evenly apart, over all leading dimensions but a layer's (a
     slice of a fused projection); returns the tokens' stride."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_cuda or t.get_device() != _device():
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != shape:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.get_device() != _device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
         if t.dtype is not torch.bfloat16:
             raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -433,28 +439,24 @@ def kv_block_plan(lens: torch.Tensor, tails: torch.Tensor, block_table: torch.Te
     tree_parents int32 [B, n] or None for the chain). block_table int32
     [B, max_blocks] and free_ring int32 [cap] are updated in place; lens,
     tails and queue are not (the plan holds their next values)."""
-    i32 = torch.int32
+    i32, dev = torch.int32, _device()
     B = lens.shape[0] if lens.dim() == 1 else lens.numel()
-    vec = (B,)
-    _need(lens, "lens", i32, vec)
-    _need(tails, "tails", i32, vec)
-    _need(block_table, "block_table", i32)
+    vec, cap = (B,), free_ring.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
-    cap = free_ring.numel()
-    _need(free_ring, "free_ring", i32, (cap,))
-    _need(queue, "queue", i32, (3,))
     if (row_start is None) == (accepted_node is None):
         raise ValueError("give row_start (ragged rows) or accepted_node (a draft's accepted path)")
     if row_start is not None:
-        _need(row_start, "row_start", i32, (B + 1,))
+        if not _is(row_start, i32, dev, (B + 1,)):
+            _need(row_start, "row_start", i32, (B + 1,))
         if rows is None:
             raise ValueError("rows (an upper bound of row_start[B]) is required with row_start")
         if tree_parents is not None:
             raise ValueError("tree_parents goes with accepted_node")
         rows, n = int(rows), 0
     else:
-        _need(accepted_node, "accepted_node", i32, vec)
+        if not _is(accepted_node, i32, dev, vec):
+            _need(accepted_node, "accepted_node", i32, vec)
         if tree_parents is not None:
             n = tree_parents.shape[-1] if n is None else n
             _need(tree_parents, "tree_parents", i32, (B, n))
@@ -467,11 +469,16 @@ def kv_block_plan(lens: torch.Tensor, tails: torch.Tensor, block_table: torch.Te
     if plan is None:
         sizes = (B, B, B + 1, 3, max(rows, 1), max(rows, 1))
         plan = BlockPlan(*(torch.empty(s, dtype=i32, device=lens.device) for s in sizes))
-    _need(plan.new_lens, "plan.new_lens", i32, vec)
-    _need(plan.new_tails, "plan.new_tails", i32, vec)
-    _need(plan.new_start, "plan.new_start", i32, (B + 1,))
-    _need(plan.queue, "plan.queue", i32, (3,))
-    _need_plan_rows(plan, rows)
+    if not (_is(lens, i32, dev, vec) and _is(tails, i32, dev, vec) and _is(block_table, i32, dev, block_table.shape)
+            and _is(free_ring, i32, dev, (cap,)) and _is(queue, i32, dev, (3,)) and _is(plan.new_lens, i32, dev, vec)
+            and _is(plan.new_tails, i32, dev, vec) and _is(plan.new_start, i32, dev, (B + 1,))
+            and _is(plan.queue, i32, dev, (3,))):
+        for t, name, shape in ((lens, "lens", vec), (tails, "tails", vec), (block_table, "block_table", None),
+                               (free_ring, "free_ring", (cap,)), (queue, "queue", (3,)),
+                               (plan.new_lens, "plan.new_lens", vec), (plan.new_tails, "plan.new_tails", vec),
+                               (plan.new_start, "plan.new_start", (B + 1,)), (plan.queue, "plan.queue", (3,))):
+            _need(t, name, i32, shape)
+    _need_plan_rows(plan, rows, dev)
     check(lib().kv_block_plan(lens.data_ptr(), tails.data_ptr(), _ptr(row_start), _ptr(tree_parents),
                               _ptr(accepted_node), _ptr(release), B, n, rows, block_table.shape[1], cap,
                               block_table.data_ptr(), free_ring.data_ptr(), queue.data_ptr(),
@@ -481,9 +488,10 @@ def kv_block_plan(lens: torch.Tensor, tails: torch.Tensor, block_table: torch.Te
     return plan
 
 
-def _need_plan_rows(plan: BlockPlan, rows: int):
+def _need_plan_rows(plan: BlockPlan, rows: int, dev: int):
     for t, name in ((plan.src_rows, "plan.src_rows"), (plan.slots, "plan.slots")):
-        _need(t, name, torch.int32)
+        if not _is(t, torch.int32, dev, t.shape):
+            _need(t, name, torch.int32)
         if t.numel() < rows:
             raise ValueError(f"{name} must hold {rows} rows, has {t.numel()}")
 
@@ -493,21 +501,24 @@ def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails:
     """The step's kept rows into the cache, every layer at once. k_new, v_new
     bf16 [layers, rows, Hkv, D] (rows evenly apart, heads dense; [rows, Hkv, D]
     for one layer); tails: the tail pages before the step."""
-    layers, pages, tail_pages, Hkv, D = _need_cache(cache)
+    dev, i32 = _device(), torch.int32
+    layers, pages, tail_pages, Hkv, D = _need_cache(cache, dev)
     if k_new.dim() == 3:
         k_new, v_new = k_new.unsqueeze(0), v_new.unsqueeze(0)
     rows = k_new.shape[1]
     shape = (layers, rows, Hkv, D)
-    stride = _need_rows(k_new, "k_new", shape)
-    _need_rows(v_new, "v_new", shape)
+    stride = _need_rows(k_new, "k_new", shape, dev)
+    _need_rows(v_new, "v_new", shape, dev)
     if layers * rows > 1 and k_new.stride() != v_new.stride():
         raise ValueError("k_new and v_new must have the same strides")
     layer_stride = k_new.stride(0) if layers > 1 else 0
     B = tails.numel()
-    _need(tails, "tails", torch.int32, (B,))
-    _need(plan.new_tails, "plan.new_tails", torch.int32, (B,))
-    _need(plan.new_start, "plan.new_start", torch.int32, (B + 1,))
-    _need_plan_rows(plan, rows)
+    if not (_is(tails, i32, dev, (B,)) and _is(plan.new_tails, i32, dev, (B,))
+            and _is(plan.new_start, i32, dev, (B + 1,))):
+        _need(tails, "tails", i32, (B,))
+        _need(plan.new_tails, "plan.new_tails", i32, (B,))
+        _need(plan.new_start, "plan.new_start", i32, (B + 1,))
+    _need_plan_rows(plan, rows, dev)
     check(lib().kv8_append(k_new.data_ptr(), v_new.data_ptr(), stride, layer_stride, tails.data_ptr(),
                            plan.new_tails.data_ptr(), plan.new_start.data_ptr(), plan.src_rows.data_ptr(),
                            plan.slots.data_ptr(), B, rows, Hkv, D, layers, pages, tail_pages,
@@ -540,29 +551,31 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     slices of one fused projection (heads dense, tokens evenly apart); lens,
     tails int32 [B]; block_table int32 [B, max_blocks]; max_len: an upper bound
     of lens (default: what the table holds). Returns bf16 [B, n, H, D]."""
-    layers, pages, tail_pages, Hkv, D = _need_cache(cache)
+    dev, i32 = _device(), torch.int32
+    layers, pages, tail_pages, Hkv, D = _need_cache(cache, dev)
     if not 0 <= layer < layers:
         raise ValueError(f"layer {layer} is not one of the cache's {layers}")
     if q.dim() != 4:
         raise ValueError(f"q must have 4 dimensions, got {tuple(q.shape)}")
     B, n, H, _ = q.shape
-    q_stride = _need_rows(q, "q", (B, n, H, D))
+    q_stride = _need_rows(q, "q", (B, n, H, D), dev)
     new = (B, n, Hkv, D)
-    kv_stride = _need_rows(k_new, "k_new", new)
-    v_stride = _need_rows(v_new, "v_new", new)
+    kv_stride = _need_rows(k_new, "k_new", new, dev)
+    v_stride = _need_rows(v_new, "v_new", new, dev)
     if B > 1 and n > 1:
         for t, name, s in ((q, "q", q_stride), (k_new, "k_new", kv_stride), (v_new, "v_new", v_stride)):
             if t.stride(0) != n * s:
                 raise ValueError(f"{name}: the tokens of all requests must be evenly apart")
     if B * n > 1 and kv_stride != v_stride:
         raise ValueError("k_new and v_new must have the same strides")
-    _need(lens, "lens", torch.int32, (B,))
-    _need(tails, "tails", torch.int32, (B,))
-    _need(block_table, "block_table", torch.int32)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
-    if tree_parents is not None:
-        _need(tree_parents, "tree_parents", torch.int32, (B, n))
+    if not (_is(lens, i32, dev, (B,)) and _is(tails, i32, dev, (B,)) and _is(block_table, i32, dev, block_table.shape)):
+        _need(lens, "lens", i32, (B,))
+        _need(tails, "tails", i32, (B,))
+        _need(block_table, "block_table", i32)
+    if tree_parents is not None and not _is(tree_parents, i32, dev, (B, n)):
+        _need(tree_parents, "tree_parents", i32, (B, n))
     max_blocks = block_table.shape[1]
     max_len = max_blocks * KV_BLOCK + KV_BLOCK - 1 if max_len is None else int(max_len)
     scale = D ** -0.5 if scale is None else float(scale)
@@ -571,7 +584,7 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     else:
         _need(out, "out", torch.bfloat16, (B, n, H, D))
     if ws is None:
-        ws = workspace(_attention_ws(q.get_device(), B, n, H, Hkv, D, max_len), q.device,
+        ws = workspace(_attention_ws(dev, B, n, H, Hkv, D, max_len), q.device,
                        "kv8_attention")  # apart from those that need no zeros
     codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
     tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
