@@ -1,26 +1,31 @@
 // Log probabilities of given tokens, entropy and the top alternatives of
 // logit rows (contract in w4a16sv.h).
 //
-// For a row x: m = max x, S = sum exp(x - m), W = sum (x - m) exp(x - m);
-// ln p(i) = (x_i - m) - ln S, entropy = ln S - W / S. All three sums merge
-// over parts of the row (each part against its own maximum, then scaled by
-// exp(m_part - m)), so the logits are read once.
+// Everything in powers of two, with l = log2 e: for a row x and a reference
+// c = rn(l max x), S = sum 2^z and W = sum z 2^z over z = l x - c (one fused
+// multiply-add, so c's rounding does not matter); then
+//   log2 p(i) = (l x_i - c) - log2 S,   entropy = (log2 S - W / S) ln 2.
+// Sums over parts of the row, each against its own c, merge by 2^(c_part - c).
+// So the logits are read once.
 //
-// token_stats_kernel: a warp takes a window of 1024 logits in registers (the
-// next one's loads in flight) and leaves its (m, S, W) and the maxima of its
-// four 256-logit quarters as ordered integers (one reduction instruction each;
-// a NaN is above all numbers, so it reaches m and with it every result).
-// token_report_kernel, one CTA per row: merges the windows; the `top`-th
-// largest window maximum is a lower bound of the `top`-th largest logit, so
-// only quarters that reach it are read again (few more than `top`, unless
-// maxima tie), and the few logits at or above it are ranked in shared memory.
-// Ranks are counted (each of up to 1025 values against all), two orders of
-// magnitude less latency than a sort of the row.
+// A warp takes a window of 1024 logits in registers (the next one's loads in
+// flight): its (c, S, W) and the maxima of its four 256-logit quarters as
+// ordered integers (one reduction instruction each; a NaN is above all numbers,
+// so it reaches the maximum and with it every result). The report then merges
+// the windows; the `top`-th largest window maximum is a lower bound of the
+// `top`-th largest logit, so only quarters that reach it are read again (few
+// more than `top`, unless maxima tie), and the few logits at or above it are
+// ranked in shared memory. Ranks are counted, each of the maxima against all:
+// two orders of magnitude less latency than a sort of the row.
 //
-// Bound: HBM for the first kernel (one pass, 16-byte loads); the second reads
-// 3 % of the row's bytes (bf16; fp32 1.6 %) in statistics and some top x 256
-// logits, mostly from L2: its latency counts. Windows start at 16-byte boundaries of memory, not of the row, so
-// that rows of any length load 16 bytes at a time.
+// Bound: HBM (one pass, 16-byte loads), next to it the instruction issue: some
+// 240 a window and warp (bf16), so pairs of logits go through packed
+// instructions wherever there are any. With at least four rows an SM a CTA takes
+// a row from its first load to its report (token_logprobs_kernel); with fewer,
+// the windows are spread over all SMs and a second kernel reports
+// (token_stats_kernel, token_report_kernel).
+// Windows start at 16-byte boundaries of memory, not of the row, so that rows of
+// any length load 16 bytes at a time.
 #include <math.h>
 
 #include "common.cuh"
@@ -31,9 +36,9 @@ namespace w4a16 {
 constexpr int kLpWindow = 1024;
 constexpr int kLpQuarter = 256;
 constexpr int kLpStatWarps = 8;
-constexpr int kLpRepThreads = 128;
-constexpr int kLpCand = 1024;    // logits ranked in shared memory
-constexpr float kLpLog2e = 1.4426950408889634f;
+constexpr int kLpRowThreads = 128;  // of a row's report (and its windows, in one kernel)
+constexpr int kLpCand = 1024;       // logits ranked in shared memory
+constexpr float kLpLog2e = 1.4426950408889634f, kLpLn2 = 0.69314718055994531f;
 
 struct LogprobParams {
   const void* logits;
@@ -43,7 +48,7 @@ struct LogprobParams {
   float *logp, *entropy;
   int32_t* top_ids;
   float* top_logp;
-  float4* win;     // [R][windows]: m, S, W (in powers of two: sum of log2 terms), unused
+  float4* win;     // [R][windows]: c, S, W, unused
   uint4* quarter;  // [R][windows]: the quarters' maxima (lp_key)
   unsigned* err;
 };
@@ -135,63 +140,133 @@ __device__ __forceinline__ float lp_warp_sum(float v) {
   return v;
 }
 
+// the largest, NaN if any is
+__device__ __forceinline__ float lp_max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t lp_maxh2(uint32_t a, uint32_t b) {  // of two bf16 pairs
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// One window of a warp from its raw words: quarter maxima (the same in every
+// lane), and c, S, W (valid in lane 0)
+template <typename T>
+__device__ __forceinline__ void lp_window(uint4 (&raw)[32 * sizeof(T) / 16], int lane, unsigned (&key)[4], float& c,
+                                          float& S, float& W) {
+  constexpr int L = 32 * sizeof(T) / 16;
+  uint32_t* u = reinterpret_cast<uint32_t*>(raw);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float m;
+    if constexpr (sizeof(T) == 4) {
+      const float* x = reinterpret_cast<const float*>(raw) + 8 * q;
+      m = lp_max3(lp_max3(lp_max3(x[0], x[1], x[2]), x[3], x[4]), lp_max3(x[5], x[6], x[7]), x[7]);
+    } else {
+      const uint32_t h = lp_maxh2(lp_maxh2(u[4 * q], u[4 * q + 1]), lp_maxh2(u[4 * q + 2], u[4 * q + 3]));
+      const float lo = __uint_as_float(h << 16), hi = __uint_as_float(h & 0xFFFF0000u);
+      m = lp_max3(lo, hi, hi);
+    }
+    key[q] = __reduce_max_sync(0xffffffffu, lp_key(m));
+  }
+  const float mx = lp_unkey(max(max(key[0], key[1]), max(key[2], key[3])));
+  c = mx * kLpLog2e;
+  uint64_t s2[2] = {0ull, 0ull}, w2[2] = {0ull, 0ull};
+  if (fabsf(mx) < 1e30f) {
+    // logits below -1e30 (masks) as -1e30: their 2^z is 0 either way, and z 2^z
+    // is 0 and not -inf * 0
+    const uint64_t nc = lp_2(-c, -c), l2 = lp_2(kLpLog2e, kLpLog2e);
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
+#pragma unroll
+      for (int k = 0; k < 4 * L; ++k) u[k] = lp_maxh2(u[k], *reinterpret_cast<const uint32_t*>(&low));
+    }
+#pragma unroll
+    for (int k = 0; k < L; ++k) {
+      constexpr int E = 16 / sizeof(T);
+      float x[E];
+      lp_floats<T>(raw[k], x);
+#pragma unroll
+      for (int j = 0; j < E; j += 2) {
+        if constexpr (sizeof(T) == 4) {
+          x[j] = fmaxf(x[j], -1e30f);
+          x[j + 1] = fmaxf(x[j + 1], -1e30f);
+        }
+        const uint64_t z = lp_fma2(lp_2(x[j], x[j + 1]), l2, nc);
+        float z0, z1;
+        lp_un2(z, z0, z1);
+        const uint64_t t = lp_2(lp_ex2(z0), lp_ex2(z1));
+        s2[(j >> 1) & 1] = lp_add2(s2[(j >> 1) & 1], t);
+        w2[(j >> 1) & 1] = lp_fma2(z, t, w2[(j >> 1) & 1]);
+      }
+    }
+  } else if (mx == mx && fabsf(mx) < INFINITY) {
+    // a maximum beyond that: the differences first, then their powers
+#pragma unroll
+    for (int k = 0; k < L; ++k) {
+      constexpr int E = 16 / sizeof(T);
+      float x[E];
+      lp_floats<T>(raw[k], x);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float z = fmaxf((x[j] - mx) * kLpLog2e, -1e30f), t = lp_ex2(z);
+        float a, b;
+        lp_un2(s2[0], a, b);
+        s2[0] = lp_2(a + t, b);
+        lp_un2(w2[0], a, b);
+        w2[0] = lp_2(fmaf(z, t, a), b);
+      }
+    }
+  }
+  float a, b, d, e;
+  lp_un2(lp_add2(s2[0], s2[1]), a, b);
+  lp_un2(lp_add2(w2[0], w2[1]), d, e);
+  // both sums over the warp: S in the lower lanes, W in the upper ones
+  const float sl = a + b, wl = d + e;
+  float v = (lane & 16 ? wl : sl) + __shfl_xor_sync(0xffffffffu, lane & 16 ? sl : wl, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  S = v;
+  W = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// the raw words of a window: lane's 16-byte pieces, 512 bytes apart
+template <typename T>
+__device__ __forceinline__ void lp_fetch(const T* row, int w, int V, int lane, uint4 (&raw)[32 * sizeof(T) / 16]) {
+  constexpr int E = 16 / sizeof(T), L = 32 / E;
+  const int e0 = w * kLpWindow - lp_shift(row) + lane * E;
+#pragma unroll
+  for (int k = 0; k < L; ++k) raw[k] = lp_load<T>(row, e0 + k * 32 * E, V);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(32 * kLpStatWarps, sizeof(T) == 2 ? 4 : 2) token_stats_kernel(const LogprobParams p) {
-  constexpr int E = 16 / sizeof(T), L = 32 / E;  // loads of E elements a lane
+  constexpr int L = 32 * sizeof(T) / 16;
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int total = p.R * p.windows, step = gridDim.x * kLpStatWarps;
   int id = blockIdx.x * kLpStatWarps + (threadIdx.x >> 5);
   uint4 next[L];
-  auto load = [&](int i) {
-    const int r = i / p.windows, w = i - r * p.windows;
-    const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
-    const int e0 = w * kLpWindow - lp_shift(row) + lane * E;
-#pragma unroll
-    for (int k = 0; k < L; ++k) next[k] = lp_load<T>(row, e0 + k * 32 * E, p.V);
+  auto fetch = [&](int i) {
+    const int r = i / p.windows;
+    lp_fetch<T>(static_cast<const T*>(p.logits) + (int64_t)r * p.V, i - r * p.windows, p.V, lane, next);
   };
-  if (id < total) load(id);
+  if (id < total) fetch(id);
   for (; id < total; id += step) {
-    float x[32];
+    uint4 raw[L];
 #pragma unroll
-    for (int k = 0; k < L; ++k) lp_floats<T>(next[k], x + k * E);
-    if (id + step < total) load(id + step);
+    for (int k = 0; k < L; ++k) raw[k] = next[k];
+    if (id + step < total) fetch(id + step);
     unsigned key[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      // the largest as a float, unless a NaN (which compares false) is among them
-      float m = x[8 * q];
-      bool nan = x[8 * q] != x[8 * q];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) {
-        m = fmaxf(m, x[8 * q + j]);
-        nan |= x[8 * q + j] != x[8 * q + j];
-      }
-      key[q] = __reduce_max_sync(0xffffffffu, nan ? 0xFFFFFFFFu : lp_key(m));
-    }
-    const float mx = lp_unkey(max(max(key[0], key[1]), max(key[2], key[3])));
-    // z = (x - m) log2 e (kept off -inf, and off NaN: m carries that), S = sum
-    // 2^z, W = sum z 2^z, two logits an instruction
-    const uint64_t nm = lp_2(-mx, -mx), l2 = lp_2(kLpLog2e, kLpLog2e);
-    uint64_t s2[2] = {0ull, 0ull}, w2[2] = {0ull, 0ull};
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      float z0, z1;
-      lp_un2(lp_mul2(lp_add2(lp_2(x[j], x[j + 1]), nm), l2), z0, z1);
-      z0 = fmaxf(z0, -1e30f);
-      z1 = fmaxf(z1, -1e30f);
-      const uint64_t t = lp_2(lp_ex2(z0), lp_ex2(z1));
-      s2[(j >> 1) & 1] = lp_add2(s2[(j >> 1) & 1], t);
-      w2[(j >> 1) & 1] = lp_fma2(lp_2(z0, z1), t, w2[(j >> 1) & 1]);
-    }
-    float a, b, c, d;
-    lp_un2(lp_add2(s2[0], s2[1]), a, b);
-    lp_un2(lp_add2(w2[0], w2[1]), c, d);
-    const float S = lp_warp_sum(a + b), W = lp_warp_sum(c + d);
+    float c, S, W;
+    lp_window<T>(raw, lane, key, c, S, W);
     if (lane == 0) {
-      p.win[id] = make_float4(mx, S, W, 0.0f);
-      if (p.top > 0) p.quarter[id] = make_uint4(key[0], key[1], key[2], key[3]);
+      p.win[id] = make_float4(c, S, W, 0.0f);
+      p.quarter[id] = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
 }
@@ -204,7 +279,7 @@ __device__ unsigned lp_select(int k, int* hist, unsigned* out, Each each) {
   unsigned prefix = 0;
   int left = k;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kLpRepThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += kLpRowThreads) hist[i] = 0;
     __syncthreads();
     each([&](unsigned key) {
       if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
@@ -243,57 +318,70 @@ __device__ unsigned lp_select(int k, int* hist, unsigned* out, Each each) {
   return prefix;
 }
 
+// A row's shared arrays: every window's statistics and quarter keys, the
+// windows' keys (up to a multiple of 4, zeros behind), the quarters to read again
+struct LpRow {
+  float4* win;
+  uint4* quarter;
+  unsigned* wkey;
+  int* quarters;
+  __device__ __forceinline__ LpRow(uint4* mem, int windows)
+      : win(reinterpret_cast<float4*>(mem)), quarter(mem + windows),
+        wkey(reinterpret_cast<unsigned*>(mem + 2 * windows)),
+        quarters(reinterpret_cast<int*>(wkey + (windows + 3) / 4 * 4)) {}
+};
+static size_t lp_row_bytes(int windows, int top) {
+  return (size_t)windows * 32 + (windows + 3) / 4 * 16 + (top > 0 ? (size_t)windows * 16 : 0);
+}
+
+// The report of row r by the CTA. Thread i < m has its token's id and logit;
+// win and quarter are filled (and synchronised).
 template <typename T>
-__global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const LogprobParams p) {
+__device__ void lp_report(const LogprobParams& p, int r, const T* row, const LpRow& s, int id0, float x0) {
   __shared__ int hist[256];
   __shared__ unsigned sel[2];
-  __shared__ float red[2][kLpRepThreads / 32];
-  __shared__ unsigned red_k[kLpRepThreads / 32];
+  __shared__ float red[2][kLpRowThreads / 32];
+  __shared__ unsigned red_k[kLpRowThreads / 32];
   __shared__ unsigned ckey[kLpCand];
   __shared__ int cidx[kLpCand];
   __shared__ int s_count, s_ties, s_quarters;
   __shared__ unsigned s_bound;
-  extern __shared__ __align__(16) unsigned lp_smem[];
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
-  const float4* win = p.win + (int64_t)r * p.windows;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nq = p.windows * 4, shift = lp_shift(row), wpad = (p.windows + 3) / 4 * 4;
-  unsigned* wkey = lp_smem;                                // [wpad] keys of the windows' maxima
-  unsigned* qkey = wkey + wpad;                            // [nq] ... of the quarters' (top > 0)
-  int* quarters = reinterpret_cast<int*>(qkey + nq);       // [nq] those to read again
-  // ---- the given tokens' logits asked for (their ids come first), then the
-  // statistics; thread tid's first window stays in registers
-  const int id0 = tid < p.m ? p.ids[(int64_t)r * p.m + tid] : -1;
-  const float x0 = id0 >= 0 && id0 < p.V ? (float)row[id0] : 0.0f;
-  float4 v0 = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  const unsigned* qkey = reinterpret_cast<const unsigned*>(s.quarter);
+  const unsigned* wkey = s.wkey;
+  int* quarters = s.quarters;
   unsigned mk = 0u;
-  for (int w = tid; w < wpad; w += kLpRepThreads) {
-    unsigned k = 0u;
-    if (w < p.windows) {
-      const float4 v = __ldcg(&win[w]);
-      if (w == tid) v0 = v;
-      k = lp_key(v.x);
-      if (p.top > 0) reinterpret_cast<uint4*>(qkey)[w] = __ldcg(p.quarter + (int64_t)r * p.windows + w);
-    }
-    wkey[w] = k;
-    mk = max(mk, k);
+  for (int w = tid; w < wpad; w += kLpRowThreads) {
+    uint4 k = make_uint4(0u, 0u, 0u, 0u);
+    if (w < p.windows) k = s.quarter[w];
+    const unsigned most = max(max(k.x, k.y), max(k.z, k.w));
+    s.wkey[w] = most;
+    mk = max(mk, most);
   }
   mk = __reduce_max_sync(0xffffffffu, mk);
   if (lane == 0) red_k[warp] = mk;
+  if (tid == 0) {
+    s_count = s_quarters = 0;
+    s_bound = 0u;
+  }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kLpRepThreads / 32; ++k) mk = max(mk, red_k[k]);
-  const float m = lp_unkey(mk);
-  // ---- the windows merged: every sum against the row's maximum
+  for (int k = 0; k < kLpRowThreads / 32; ++k) mk = max(mk, red_k[k]);
+  const float m = lp_unkey(mk), c = m * kLpLog2e;
+  // ---- the windows merged: every sum against the row's reference
+  const bool fine = fabsf(m) < INFINITY, huge = fabsf(c) == INFINITY;
   float S = 0.0f, W = 0.0f;
-  for (int w = tid; w < p.windows; w += kLpRepThreads) {
-    const float4 v = w == tid ? v0 : __ldcg(&win[w]);
-    const float d = fmaxf(v.x - m, -1e30f), t = expf(d);
-    S = fmaf(v.y, t, S);
-    W += t * fmaf(d, v.y, v.z * 0.69314718056f);
-  }
+  if (fine)
+    for (int w = tid; w < p.windows; w += kLpRowThreads) {
+      const float4 v = s.win[w];
+      // (where l max passes the largest float, from the maxima themselves)
+      float d = huge ? (lp_unkey(wkey[w]) - m) * kLpLog2e : v.x - c;
+      d = fmaxf(d, -1e30f);
+      const float t = exp2f(d);
+      S = fmaf(v.y, t, S);
+      W += t * fmaf(d, v.y, v.z);
+    }
   S = lp_warp_sum(S);
   W = lp_warp_sum(W);
   if (lane == 0) {
@@ -303,33 +391,33 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
   __syncthreads();
   S = W = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kLpRepThreads / 32; ++k) {
+  for (int k = 0; k < kLpRowThreads / 32; ++k) {
     S += red[0][k];
     W += red[1][k];
   }
   // a NaN, +inf or -inf alone: no distribution
-  const float ls = S > 0.0f && m < INFINITY && m > -INFINITY ? logf(S) : NAN;
-  if (tid == 0 && p.entropy) p.entropy[r] = ls - W / S;
+  const float ls = fine ? log2f(S) : NAN;
+  auto logp = [&](float x) {
+    // by the same product as the sums; beyond 1e30 (a mask of the type's lowest
+    // value) by the difference, which does not overflow
+    return fabsf(m) < 1e30f && fabsf(x) < 1e30f ? (fmaf(x, kLpLog2e, -c) - ls) * kLpLn2 : (x - m) - ls * kLpLn2;
+  };
+  if (tid == 0 && p.entropy) p.entropy[r] = (ls - W / S) * kLpLn2;
   if (tid < p.m) {  // m <= 64 of them
     if (id0 < -1 || id0 >= p.V) report_error(p.err, kErrInput);
-    p.logp[(int64_t)r * p.m + tid] = id0 == -1 ? 0.0f : id0 >= 0 && id0 < p.V ? (x0 - m) - ls : NAN;
+    p.logp[(int64_t)r * p.m + tid] = id0 == -1 ? 0.0f : id0 >= 0 && id0 < p.V ? logp(x0) : NAN;
   }
   if (p.top == 0) return;
 
   // ---- the lower bound: the `top`-th largest maximum of the windows, or of
   // the quarters where there are fewer windows (with fewer quarters than `top`,
   // every logit is a candidate)
-  if (tid == 0) {
-    s_count = s_quarters = 0;
-    s_bound = 0u;
-  }
-  __syncthreads();
   {
     const bool by_window = p.windows >= p.top;
     const int n = by_window ? p.windows : nq;
     const unsigned* key = by_window ? wkey : qkey;
     if (n >= p.top)
-      for (int i = tid; i < n; i += kLpRepThreads) {
+      for (int i = tid; i < n; i += kLpRowThreads) {
         const unsigned mine = key[i];
         int rank = 0;  // of value i, the earlier of equal ones first (a key of 0 past the end counts for nothing)
         for (int j = 0; j < n; j += 4) {
@@ -342,14 +430,14 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
   }
   __syncthreads();
   const unsigned bound = s_bound;
-  for (int i = tid; i < nq; i += kLpRepThreads)
+  for (int i = tid; i < nq; i += kLpRowThreads)
     if (qkey[i] >= bound) quarters[atomicAdd(&s_quarters, 1)] = i;
   __syncthreads();
   const int again = s_quarters;
   // every logit of a quarter that reaches the bound, a warp a quarter
   auto scan = [&](auto f) {
     constexpr int E = 16 / sizeof(T), L = 8 / E;
-    for (int i = warp; i < again; i += kLpRepThreads / 32) {
+    for (int i = warp; i < again; i += kLpRowThreads / 32) {
       const int e0 = quarters[i] * kLpQuarter - shift + lane * E;
       float x[8];
 #pragma unroll
@@ -393,7 +481,7 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
     __syncthreads();
     const int above = s_count, want = p.top - above;
     // the ties in index order, a logit a thread at a time
-    for (int e0 = 0; e0 < p.V; e0 += kLpRepThreads) {
+    for (int e0 = 0; e0 < p.V; e0 += kLpRowThreads) {
       const int e = e0 + tid;
       const bool hit = e < p.V && lp_key((float)row[e]) == kth;
       const unsigned ball = __ballot_sync(0xffffffffu, hit);
@@ -408,7 +496,7 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
       }
       __syncthreads();
       if (tid == 0)
-        for (int k = 0; k < kLpRepThreads / 32; ++k) s_ties += hist[k];
+        for (int k = 0; k < kLpRowThreads / 32; ++k) s_ties += hist[k];
       __syncthreads();
       if (s_ties >= want) break;
     }
@@ -416,21 +504,98 @@ __global__ void __launch_bounds__(kLpRepThreads) token_report_kernel(const Logpr
     __syncthreads();
   }
   // ---- ranks: larger key first, then the lower index
-  for (int i = tid; i < n; i += kLpRepThreads) {
+  for (int i = tid; i < n; i += kLpRowThreads) {
     const unsigned key = ckey[i];
     const int e = cidx[i];
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += ckey[j] > key || (ckey[j] == key && cidx[j] < e);
     if (rank < p.top) {
       p.top_ids[(int64_t)r * p.top + rank] = e;
-      p.top_logp[(int64_t)r * p.top + rank] = ((float)row[e] - m) - ls;
+      p.top_logp[(int64_t)r * p.top + rank] = logp((float)row[e]);
     }
   }
+}
+
+// The report of rows whose windows another kernel has summed up.
+template <typename T>
+__global__ void __launch_bounds__(kLpRowThreads) token_report_kernel(const LogprobParams p) {
+  extern __shared__ uint4 lp_smem[];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int r = blockIdx.x, tid = threadIdx.x;
+  const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
+  const LpRow s(lp_smem, p.windows);
+  const int id0 = tid < p.m ? p.ids[(int64_t)r * p.m + tid] : -1;
+  const float x0 = id0 >= 0 && id0 < p.V ? (float)row[id0] : 0.0f;
+  for (int w = tid; w < p.windows; w += kLpRowThreads) {
+    s.win[w] = __ldcg(&p.win[(int64_t)r * p.windows + w]);
+    s.quarter[w] = __ldcg(&p.quarter[(int64_t)r * p.windows + w]);
+  }
+  __syncthreads();
+  lp_report<T>(p, r, row, s, id0, x0);
+}
+
+// A CTA a row, from the windows to the report.
+template <typename T>
+__global__ void __launch_bounds__(kLpRowThreads, sizeof(T) == 2 ? 8 : 5) token_logprobs_kernel(const LogprobParams p) {
+  extern __shared__ uint4 lp_smem[];
+  constexpr int L = 32 * sizeof(T) / 16, kWarps = kLpRowThreads / 32;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* row = static_cast<const T*>(p.logits) + (int64_t)r * p.V;
+  const LpRow s(lp_smem, p.windows);
+  const int id0 = tid < p.m ? p.ids[(int64_t)r * p.m + tid] : -1;
+  uint4 next[L];
+  if (warp < p.windows) lp_fetch<T>(row, warp, p.V, lane, next);
+  const float x0 = id0 >= 0 && id0 < p.V ? (float)row[id0] : 0.0f;
+  for (int w = warp; w < p.windows; w += kWarps) {
+    uint4 raw[L];
+#pragma unroll
+    for (int k = 0; k < L; ++k) raw[k] = next[k];
+    if (w + kWarps < p.windows) lp_fetch<T>(row, w + kWarps, p.V, lane, next);
+    unsigned key[4];
+    float c, S, W;
+    lp_window<T>(raw, lane, key, c, S, W);
+    if (lane == 0) {
+      s.win[w] = make_float4(c, S, W, 0.0f);
+      s.quarter[w] = make_uint4(key[0], key[1], key[2], key[3]);
+    }
+  }
+  __syncthreads();
+  lp_report<T>(p, r, row, s, id0, x0);
 }
 
 static int lp_windows(int V, bool wide) { return (V + (wide ? 3 : 7) + kLpWindow - 1) / kLpWindow; }
 
 size_t token_logprobs_ws(int R, int V) { return (size_t)R * lp_windows(V, false) * 32; }
+
+template <typename T>
+static cudaError_t launch_lp(const LogprobParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = lp_row_bytes(p.windows, p.top);  // 6 KB for 128 K logits, 49 KB for 2^20
+  cudaError_t e;
+  // a CTA a row when that gives every SM four of them (1024 rows of 128256 bf16
+  // logits: 68 us, 79 us with two kernels; 16 rows: 10 us with two)
+  if (p.R >= 4 * num_sms) {
+    if (smem > 32 * 1024) {
+      e = cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(token_logprobs_kernel<T>, dim3((unsigned)p.R), dim3(kLpRowThreads), smem, stream, p);
+  }
+  // every SM's resident CTAs (4, or 2 of fp32: see the kernel's bounds), fewer
+  // when there are fewer windows
+  const int64_t warps = (int64_t)p.R * p.windows, most = (int64_t)num_sms * (sizeof(T) == 2 ? 4 : 2);
+  const int64_t ctas = (warps + kLpStatWarps - 1) / kLpStatWarps;
+  e = launch_pdl(token_stats_kernel<T>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(32 * kLpStatWarps), 0, stream,
+                 p);
+  if (e != cudaSuccess) return e;
+  if (smem > 32 * 1024) {
+    e = cudaFuncSetAttribute(token_report_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(token_report_kernel<T>, dim3((unsigned)p.R), dim3(kLpRowThreads), smem, stream, p);
+}
 
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* ids, int R, int V, int m, int top,
                                   float* logp, float* entropy, int32_t* top_ids, float* top_logp, void* workspace,
@@ -450,19 +615,7 @@ cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* 
   p.win = static_cast<float4*>(workspace);
   p.quarter = reinterpret_cast<uint4*>(p.win + (size_t)R * p.windows);
   p.err = err;
-  // every SM's resident CTAs (4, or 2 of fp32: see the kernel's bounds), fewer
-  // when there are fewer windows
-  const int64_t warps = (int64_t)R * p.windows, most = (int64_t)num_sms * (bf16 ? 4 : 2);
-  const int64_t ctas = (warps + kLpStatWarps - 1) / kLpStatWarps;
-  const dim3 grid((unsigned)(ctas < most ? ctas : most));
-  const dim3 block(32 * kLpStatWarps);
-  cudaError_t e = bf16 ? launch_pdl(token_stats_kernel<__nv_bfloat16>, grid, block, 0, stream, p)
-                       : launch_pdl(token_stats_kernel<float>, grid, block, 0, stream, p);
-  if (e != cudaSuccess) return e;
-  // window keys, quarter keys, quarter numbers (37 KB for 2^20 logits)
-  const size_t smem = ((size_t)p.windows * (top > 0 ? 8 : 0) + (p.windows + 3) / 4 * 4) * 4;
-  return bf16 ? launch_pdl(token_report_kernel<__nv_bfloat16>, dim3((unsigned)R), dim3(kLpRepThreads), smem, stream, p)
-              : launch_pdl(token_report_kernel<float>, dim3((unsigned)R), dim3(kLpRepThreads), smem, stream, p);
+  return bf16 ? launch_lp<__nv_bfloat16>(p, num_sms, stream) : launch_lp<float>(p, num_sms, stream);
 }
 
 }  // namespace w4a16
