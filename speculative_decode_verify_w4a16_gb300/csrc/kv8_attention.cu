@@ -319,7 +319,8 @@ __device__ __noinline__ void ka_merge(const Kv8AttnParams& p, const KaWork& wk, 
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
     const float x = o[q] * __shfl_sync(0xffffffffu, inv, q);
-    if (row[qa + q] >= 0) p.out[(int64_t)row[qa + q] * kKaD + d] = __float2bfloat16_rn(x);
+    if (row[qa + q] >= 0 && in_bounds(p.err, row[qa + q], (int64_t)p.B * p.n * p.H))
+      p.out[(int64_t)row[qa + q] * kKaD + d] = __float2bfloat16_rn(x);
   }
 }
 
@@ -1044,7 +1045,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         } else {
           float* dst = wk.part_o + ((size_t)slot * NP + qa + q0) * kKaD + key;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q * kKaD] = __uint_as_float(o[q]);
+          for (int q = 0; q < 8; ++q)
+            if (in_bounds(p.err, (int64_t)slot * NP + qa + q0 + q, (int64_t)2 * wk.ctas * NP))
+              dst[q * kKaD] = __uint_as_float(o[q]);
         }
       }
       if (whole) {
@@ -1052,7 +1055,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int q = (st >> 4) + 8 * k;
-          if (row_s[qa + q] >= 0)
+          if (row_s[qa + q] >= 0 && in_bounds(p.err, row_s[qa + q], (int64_t)p.B * p.n * p.H))
             reinterpret_cast<uint4*>(p.out + (int64_t)row_s[qa + q] * kKaD)[st & 15] =
                 reinterpret_cast<const uint4*>(stage)[q * 16 + (st & 15)];
         }

@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     const int page = p.ring[plan_ring(head, a, p.ring_cap)];
     const bool bad = page < 0 || page >= kPlanMaxPage;
     if (bad) report_error(p.err, kErrInput);
-    p.table[(int64_t)b * p.max_blocks + s.len[b] / 64 + (a - s.need[b])] = bad ? -1 : page;
+    const int64_t at = (int64_t)b * p.max_blocks + s.len[b] / 64 + (a - s.need[b]);
+    if (in_bounds(p.err, at, (int64_t)(b + 1) * p.max_blocks)) p.table[at] = bad ? -1 : page;
   }
   for (int a = gt; a < min(back, room); a += gn) {
     const int b = plan_find(s.back, B, a);

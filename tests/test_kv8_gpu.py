@@ -306,6 +306,7 @@ ATTN = [  # B, n, H, Hkv, lens, tree, dtype
     (1, 64, 64, 8, [1000], True, E5M2),                   # 512 rows
     (2, 24, 48, 3, [300, 77], True, E4M3),                # 16 query heads a head
     (70, 2, 4, 2, [(i * 37) % 261 for i in range(70)], False, E4M3),
+    (900, 1, 1, 1, [(i * 61) % 331 for i in range(900)], False, E5M2),  # more requests than a CTA has threads
 ]
 
 
