@@ -3,7 +3,8 @@
 //
 // Everything in powers of two, with l = log2 e: for a row x and a reference
 // c = rn(l max x), S = sum 2^z and W = sum z 2^z over z = l x - c (one fused
-// multiply-add, so c's rounding does not matter); then
+// multiply-add, so c's rounding cancels; it moves the largest z by up to
+// 2^-24 |c|, so from |max x| = 2^20 on z = l (x - max x) instead); then
 //   log2 p(i) = (l x_i - c) - log2 S,   entropy = (log2 S - W / S) ln 2.
 // Sums over parts of the row, each against its own c, merge by 2^(c_part - c).
 // So the logits are read once.
@@ -39,6 +40,7 @@ constexpr int kLpStatWarps = 8;
 constexpr int kLpRowThreads = 128;  // of a row's report (and its windows, in one kernel)
 constexpr int kLpCand = 1024;       // logits ranked in shared memory
 constexpr float kLpLog2e = 1.4426950408889634f, kLpLn2 = 0.69314718055994531f;
+constexpr float kLpNear = 1048576.0f;  // maxima below it: c is the reference, else l max x itself
 
 struct LogprobParams {
   const void* logits;
@@ -175,7 +177,7 @@ __device__ __forceinline__ void lp_window(uint4 (&raw)[32 * sizeof(T) / 16], int
   const float mx = lp_unkey(max(max(key[0], key[1]), max(key[2], key[3])));
   c = mx * kLpLog2e;
   uint64_t s2[2] = {0ull, 0ull}, w2[2] = {0ull, 0ull};
-  if (fabsf(mx) < 1e30f) {
+  if (fabsf(mx) < kLpNear) {
     // logits below -1e30 (masks) as -1e30: their 2^z is 0 either way, and z 2^z
     // is 0 and not -inf * 0
     const uint64_t nc = lp_2(-c, -c), l2 = lp_2(kLpLog2e, kLpLog2e);
@@ -204,7 +206,7 @@ __device__ __forceinline__ void lp_window(uint4 (&raw)[32 * sizeof(T) / 16], int
       }
     }
   } else if (mx == mx && fabsf(mx) < INFINITY) {
-    // a maximum beyond that: the differences first, then their powers
+    // a maximum beyond: the differences first, then their powers
 #pragma unroll
     for (int k = 0; k < L; ++k) {
       constexpr int E = 16 / sizeof(T);
@@ -370,13 +372,18 @@ __device__ void lp_report(const LogprobParams& p, int r, const T* row, const LpR
   for (int k = 0; k < kLpRowThreads / 32; ++k) mk = max(mk, red_k[k]);
   const float m = lp_unkey(mk), c = m * kLpLog2e;
   // ---- the windows merged: every sum against the row's reference
-  const bool fine = fabsf(m) < INFINITY, huge = fabsf(c) == INFINITY;
+  const bool fine = fabsf(m) < INFINITY, near = fabsf(m) < kLpNear;
   float S = 0.0f, W = 0.0f;
   if (fine)
     for (int w = tid; w < p.windows; w += kLpRowThreads) {
       const float4 v = s.win[w];
-      // (where l max passes the largest float, from the maxima themselves)
-      float d = huge ? (lp_unkey(wkey[w]) - m) * kLpLog2e : v.x - c;
+      const float mx = lp_unkey(wkey[w]);
+      // the window's reference less the row's, whichever form each has
+      float d;
+      if (fabsf(mx) < kLpNear)
+        d = near ? v.x - c : -fmaf(m, kLpLog2e, -v.x);
+      else
+        d = near ? fmaf(mx, kLpLog2e, -c) : (mx - m) * kLpLog2e;
       d = fmaxf(d, -1e30f);
       const float t = exp2f(d);
       S = fmaf(v.y, t, S);
@@ -398,9 +405,9 @@ __device__ void lp_report(const LogprobParams& p, int r, const T* row, const LpR
   // a NaN, +inf or -inf alone: no distribution
   const float ls = fine ? log2f(S) : NAN;
   auto logp = [&](float x) {
-    // by the same product as the sums; beyond 1e30 (a mask of the type's lowest
-    // value) by the difference, which does not overflow
-    return fabsf(m) < 1e30f && fabsf(x) < 1e30f ? (fmaf(x, kLpLog2e, -c) - ls) * kLpLn2 : (x - m) - ls * kLpLn2;
+    // by the same form as the sums; for a mask near the type's lowest value by
+    // the difference, which does not overflow
+    return near && fabsf(x) < 1e30f ? (fmaf(x, kLpLog2e, -c) - ls) * kLpLn2 : (x - m) - ls * kLpLn2;
   };
   if (tid == 0 && p.entropy) p.entropy[r] = (ls - W / S) * kLpLn2;
   if (tid < p.m) {  // m <= 64 of them

@@ -87,6 +87,42 @@ def test_masked_tokens():
     _check(x, torch.tensor([[0, 1], [4999, 0], [5, 3000], [0, 1], [2, 3], [7, 8]], dtype=torch.int32), 20)
 
 
+def _extremes():
+    """Rows whose maximum is far from zero, in every window or in some."""
+    f32 = np.float32
+    rows = [torch.full((5003,), v) for v in (-1e4, -1e9, -1e10, -1e20, 1e10, 5e29, 2e38, -2.0 ** 20, 2.0 ** 20 - 1)]
+    for top in (f32(2.0 ** 20), f32(1e9), f32(1.9000001e30)):  # neighbours, in windows of their own
+        r = torch.full((5003,), -1e9)
+        r[4000], r[10], r[2500] = float(np.nextafter(top, f32(3e38))), float(top), float(np.nextafter(top, f32(0)))
+        rows.append(r)
+    r = torch.full((5003,), -2.0 ** 21)  # windows far away from a maximum that is near
+    r[17] = 3.0
+    rows.append(r)
+    r = torch.full((5003,), -torch.inf)
+    r[3000:] = 1048575.9375
+    r[2] = 1048576.0
+    rows.append(r)
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", [1, 50])  # 700 of them: more than a few an SM
+def test_maxima_far_from_zero(dtype, rows):
+    x = _extremes().repeat(rows, 1).to(dtype)
+    ids = torch.tensor([[10, 4000, 2500, 2, 17]], dtype=torch.int32).repeat(x.shape[0], 1)
+    _check(x, ids, 3)
+
+
+def test_many_rows_with_masks_and_ties():
+    g = torch.Generator().manual_seed(8)
+    x = torch.randint(-3, 4, (640, 4099), generator=g).float()
+    x[::3, 2000:] = -torch.inf
+    x[1::3, :4000] = torch.finfo(torch.float32).min
+    x[2::6] = torch.randn(x[2::6].shape, generator=g) * 4
+    ids = torch.randint(-1, 4099, (640, 2), generator=g, dtype=torch.int32)
+    _check(x, ids, 33)
+
+
 def test_rows_without_a_distribution_are_nan():
     x = torch.randn(4, 3000)
     x[0, :] = -torch.inf
