@@ -52,11 +52,19 @@ __device__ __forceinline__ int kv8_exponent(unsigned amax_bits) {
   return k < -100 ? -100 : k;
 }
 
+__device__ __forceinline__ void kv8_mul2(float a, float b, float inv, float& x, float& y) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmul.rn.f32x2 v, v, s;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(inv));
+}
+
 template <int FMT>
 __device__ __forceinline__ uint32_t kv8_pack4(uint32_t a, uint32_t b, float inv) {
   // four bf16 (two words) -> four codes
-  const float x0 = __uint_as_float(a << 16) * inv, x1 = __uint_as_float(a & 0xFFFF0000u) * inv;
-  const float x2 = __uint_as_float(b << 16) * inv, x3 = __uint_as_float(b & 0xFFFF0000u) * inv;
+  float x0, x1, x2, x3;
+  kv8_mul2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), inv, x0, x1);
+  kv8_mul2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u), inv, x2, x3);
   constexpr __nv_fp8_interpretation_t t = FMT == 0 ? __NV_E4M3 : __NV_E5M2;
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, t);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2, x3), __NV_SATFINITE, t);
@@ -138,12 +146,25 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv8_append_kernel(const Append
   const __nv_bfloat16* src_tail = half ? p.v_tail : p.k_tail;
   uint8_t* codes = half ? p.v : p.k;
   float* scales = half ? p.v_scale : p.k_scale;
-  const int64_t items = (int64_t)pages * pairs;
+  // item i is page i / pairs and layer-head i % pairs; a CTA's items are step
+  // apart, kept as both parts
+  struct Item {
+    int pc, lh;
+  };
+  const int step_pc = (int)gridDim.x / pairs, step_lh = (int)gridDim.x - step_pc * pairs;
+  auto after = [&](Item i) {
+    i.pc += step_pc;
+    i.lh += step_lh;
+    if (i.lh >= pairs) {
+      i.lh -= pairs;
+      ++i.pc;
+    }
+    return i;
+  };
   // Two warps find an item's rows (a thread a row) one item ahead of the CTA:
   // source rows, -1 - block row for those in the tail page; the page, -1 if
   // anything fits no plan
-  auto find = [&](int64_t item, int to) {
-    const int pc = (int)(item / pairs);
+  auto find = [&](int pc, int to) {
     int b = 0;  // the request: the last one with pre[b] <= pc
     for (int hi = B - 1; b < hi;) {
       const int mid = (b + hi + 1) >> 1;
@@ -167,10 +188,13 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv8_append_kernel(const Append
     if (lane == 0) s_at[to][warp] = make_int2(bad ? -1 : page, tail);
   };
   int buf = 0;
-  if (blockIdx.x < items && tid < 64) find(blockIdx.x, 0);
+  Item item;
+  item.pc = (int)blockIdx.x / pairs;
+  item.lh = (int)blockIdx.x - item.pc * pairs;
+  if (item.pc < pages && tid < 64) find(item.pc, 0);
   __syncthreads();
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
-    const int lh = (int)(item % pairs), layer = lh / p.Hkv, h = lh - layer * p.Hkv;
+  for (Item next = item; item.pc < pages; item = next, buf ^= 1) {
+    const int lh = item.lh, layer = lh / p.Hkv, h = lh - layer * p.Hkv;
     const int page = min(s_at[buf][0].x, s_at[buf][1].x), tail = s_at[buf][0].y;
     const __nv_bfloat16* a = src_new + layer * p.layer_stride + h * kAppD + c;
     const __nv_bfloat16* o = src_tail + (((int64_t)layer * p.tail_pages + tail) * p.Hkv + h) * 64 * kAppD + c;
@@ -183,11 +207,24 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv8_append_kernel(const Append
         v[k] = __ldg(reinterpret_cast<const uint4*>(src < 0 ? o + (-1 - src) * kAppD : a + (int64_t)src * p.row_stride));
       }
     }
-    if (item + gridDim.x < items && tid < 64) find(item + gridDim.x, buf ^ 1);
+    next = after(item);
+    if (next.pc < pages && tid < 64) find(next.pc, buf ^ 1);
     if (page >= 0) {
+      // the two halves of the words side by side; where anything is not finite
+      // again, without that
+      unsigned m2 = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        m = max(m, max(max(kv8_mag(v[k].x), kv8_mag(v[k].y)), max(kv8_mag(v[k].z), kv8_mag(v[k].w))));
+      for (int k = 0; k < 8; ++k) {
+        m2 = __vimax3_u16x2(m2, v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu);
+        m2 = __vimax3_u16x2(m2, v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu);
+      }
+      m = max(m2 & 0xFFFFu, m2 >> 16);
+      if (m >= 0x7F80u) {
+        m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          m = max(m, max(max(kv8_mag(v[k].x), kv8_mag(v[k].y)), max(kv8_mag(v[k].z), kv8_mag(v[k].w))));
+      }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) s_max[buf][warp] = m;
