@@ -24,7 +24,13 @@
 // instructions wherever there are any. With at least four rows an SM a CTA takes
 // a row from its first load to its report (token_logprobs_kernel); with fewer,
 // the windows are spread over all SMs and a second kernel reports
-// (token_stats_kernel, token_report_kernel).
+// (token_stats_kernel, token_report_kernel). Rows of 128256 logits, both ways,
+// in us: 64 rows 16 and 13, 228 27 and 22, 608 33 and 40 (fp32 55 and 58), 912
+// 51 and 58 (bf16).
+// A row's CTA has 256 threads, four CTAs an SM: with 1024 rows the later rows
+// stream while the first ones report (58 us, 263 MB: 0.67 of the HBM copy rate);
+// 128 threads and eight CTAs take them all at once and then report all at once,
+// 68 us; 512 threads 63 us. 16 rows of fp32 (8.2 MB) take 8.4 us, latency.
 // Windows start at 16-byte boundaries of memory, not of the row, so that rows of
 // any length load 16 bytes at a time.
 #include <math.h>
@@ -37,7 +43,7 @@ namespace w4a16 {
 constexpr int kLpWindow = 1024;
 constexpr int kLpQuarter = 256;
 constexpr int kLpStatWarps = 8;
-constexpr int kLpRowThreads = 128;  // of a row's report (and its windows, in one kernel)
+constexpr int kLpRowThreads = 256;  // of a row's report (and its windows, in one kernel)
 constexpr int kLpCand = 1024;       // logits ranked in shared memory
 constexpr float kLpLog2e = 1.4426950408889634f, kLpLn2 = 0.69314718055994531f;
 constexpr float kLpNear = 1048576.0f;  // maxima below it: c is the reference, else l max x itself
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kLpRowThreads) token_report_kernel(const Logpr
 
 // A CTA a row, from the windows to the report.
 template <typename T>
-__global__ void __launch_bounds__(kLpRowThreads, sizeof(T) == 2 ? 8 : 5) token_logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpRowThreads, sizeof(T) == 2 ? 4 : 2) token_logprobs_kernel(const LogprobParams p) {
   extern __shared__ uint4 lp_smem[];
   constexpr int L = 32 * sizeof(T) / 16, kWarps = kLpRowThreads / 32;
   grid_launch_dependents();
@@ -581,8 +587,7 @@ template <typename T>
 static cudaError_t launch_lp(const LogprobParams& p, int num_sms, cudaStream_t stream) {
   const size_t smem = lp_row_bytes(p.windows, p.top);  // 6 KB for 128 K logits, 49 KB for 2^20
   cudaError_t e;
-  // a CTA a row when that gives every SM four of them (1024 rows of 128256 bf16
-  // logits: 68 us, 79 us with two kernels; 16 rows: 10 us with two)
+  // a CTA a row when that gives every SM four of them (measured above)
   if (p.R >= 4 * num_sms) {
     if (smem > 32 * 1024) {
       e = cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
