@@ -85,6 +85,20 @@ __device__ __forceinline__ uint32_t ka_bf162(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// two fp16 x as e4m3 terms: x = c1 + c2 / 32 (the difference is exact)
+__device__ __forceinline__ void ka_terms(uint32_t x, uint32_t& c1, uint32_t& c2) {
+  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 y, k;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, a;\n\t"
+      "sub.f16x2 y, %2, y;\n\t"
+      "mov.b32 k, 0x50005000;\n\t"  // 32, twice
+      "mul.f16x2 y, y, k;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, y;\n\t"
+      "cvt.u32.u16 %0, a;\n\t"
+      "cvt.u32.u16 %1, b;\n\t}"
+      : "=r"(c1), "=r"(c2)
+      : "r"(x));
+}
 // four e4m3 codes widened to fp16 (exact)
 __device__ __forceinline__ void ka_widen(uint32_t in, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\t"
@@ -801,14 +815,17 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     bool ok = true;
     KaSeg nx;
     bool more = ka_next(p, it, nx);
+    uint4 v[2];  // the thread's 16 columns of a part's query row
+    auto q_load = [&](const __nv_bfloat16* at) {
+      v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (at) {
+        v[0] = reinterpret_cast<const uint4*>(at)[0];
+        v[1] = reinterpret_cast<const uint4*>(at)[1];
+      }
+    };
+    if (more) q_load(q_at(nx));
     while (more) {
       sg = nx;
-      const uint4* q_now = reinterpret_cast<const uint4*>(q_at(sg));
-      uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      if (q_now) {
-        v[0] = q_now[0];
-        v[1] = q_now[1];
-      }
       const int kvh = sg.u / wk.row_blocks, rb = sg.u - kvh * wk.row_blocks;
       // ---- Q: x = q 2^ex, |x| < 256, as bf16 and as two e4m3 terms
       {
@@ -823,28 +840,34 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           par_s[st] = up;
         }
         const int r = qa + (st >> 3), c = st & 7, sw = r & 7;
-        const uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-        unsigned m = 0;
+        uint32_t in[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        // the largest magnitude (two side by side); without what is not finite
+        unsigned m2 = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
-          m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        for (int e = 0; e < 8; e += 2) m2 = __vimax3_u16x2(m2, in[e] & 0x7FFF7FFFu, in[e + 1] & 0x7FFF7FFFu);
+        unsigned m = max(m2 & 0xFFFFu, m2 >> 16);
+        if (m >= 0x7F80u) {  // an infinity becomes a NaN, which e4m3 has; the row is NaN either way
+          m = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const unsigned lo = in[e] & 0x7FFFu, hi = (in[e] >> 16) & 0x7FFFu;
+            if (lo >= 0x7F80u) in[e] |= 0x7FFFu;
+            if (hi >= 0x7F80u) in[e] |= 0x7FFF0000u;
+            m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+          }
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int ex = min(134 - (int)(m >> 7), 120);  // |q| 2^ex in [128, 256)
         const float up = __uint_as_float((unsigned)(127 + ex) << 23);
+        // x in fp16: its 8 bits are exact above 2^-16 (2^-24 of the maximum)
         uint32_t t1[4], t2[4], w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float x0 = __uint_as_float(in[e] << 16) * up, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * up;
-          if (!(fabsf(x0) < INFINITY)) x0 = NAN;  // e4m3 has no infinity; the row is NaN either way
-          if (!(fabsf(x1) < INFINITY)) x1 = NAN;
+          const float x0 = __uint_as_float(in[e] << 16) * up, x1 = __uint_as_float(in[e] & 0xFFFF0000u) * up;
           w[e] = ka_bf162(x0, x1);
-          const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-          const float2 b1 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c1, __NV_E4M3)));
-          const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2((x0 - b1.x) * 32.0f, (x1 - b1.y) * 32.0f),
-                                                       __NV_SATFINITE, __NV_E4M3);
+          uint32_t c1, c2;
+          ka_terms(ka_half2(x0, x1), c1, c2);
           t1[e >> 1] = (e & 1) ? t1[e >> 1] | (c1 << 16) : c1;
           t2[e >> 1] = (e & 1) ? t2[e >> 1] | (c2 << 16) : c2;
         }
@@ -882,10 +905,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       }
       // the next part's query rows on their way to L2
       more = ka_next(p, it, nx);
-      if (more) {
-        const __nv_bfloat16* next = q_at(nx);
-        if (next && !(st & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(next));
-      }
+      const __nv_bfloat16* q_next = more ? q_at(nx) : nullptr;
+      if (q_next && !(st & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_next));
       uint64_t l[Q / 2];
 #pragma unroll
       for (int q = 0; q < Q / 2; ++q) l[q] = 0ull;
@@ -1007,6 +1028,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // ---- the end of the unit's part: the rows' sums over the keys, then O^T
+      q_load(q_next);
       {
         float x[Q];
 #pragma unroll
