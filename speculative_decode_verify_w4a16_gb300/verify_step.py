@@ -29,6 +29,7 @@ import torch
 from . import api
 
 D = 128
+MAX_ROWS = 80  # of one linear
 
 
 def _weight(N: int, K: int, gen: torch.Generator) -> api.PackedWeight:
@@ -123,18 +124,24 @@ def verify_step(target: Target, cache: api.KV8Cache, state: Requests, last: torc
     return Emitted(tokens, report.logp.view(B, K + 1), report.top_ids, report.top_logp)
 
 
-def decode(target: Target, prompts: List[List[int]], steps: int, K: int, draft_of, pages: int = 256) -> List[list]:
+def decode(target: Target, prompts: List[List[int]], steps: int, K: int, draft_of) -> List[list]:
     """Greedy decoding with drafts: draft_of(b, tokens, K) gives K token ids to
     try after request b's tokens (a drafter's place). Returns each request's
     (token, log probability) pairs."""
     B = len(prompts)
+    if not B or not all(prompts):
+        raise ValueError("decode needs prompts of at least one token")
+    if B * (K + 1) > MAX_ROWS:
+        raise ValueError(f"{B} requests with drafts of {K} are more than the linear's {MAX_ROWS} rows")
     longest = max(map(len, prompts)) + steps * (K + 1)
-    state = Requests.empty(B, longest // api.KV_BLOCK + 1, pages)
+    blocks = longest // api.KV_BLOCK + 1
+    pages = B * blocks  # no request is ever refused one
+    state = Requests.empty(B, blocks, pages)
     cache = api.kv8_cache(len(target.layers), pages, B, target.kv_heads)
-    # the prompts, all but their last tokens, one chain of up to 16 rows at a time
-    done = [0] * B
+    # the prompts, all but their last tokens, chains of as many rows as the linear takes
+    done, at_once = [0] * B, min(MAX_ROWS // B, 64)
     while any(done[b] < len(p) - 1 for b, p in enumerate(prompts)):
-        rows = [p[done[b]:min(done[b] + 16, len(p) - 1)] for b, p in enumerate(prompts)]
+        rows = [p[done[b]:min(done[b] + at_once, len(p) - 1)] for b, p in enumerate(prompts)]
         n = max(map(len, rows))
         ids = torch.tensor([r + [0] * (n - len(r)) for r in rows], dtype=torch.int32, device="cuda")
         _, k, v = target.forward(ids, cache, state, longest)

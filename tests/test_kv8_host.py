@@ -119,3 +119,14 @@ def test_reference_attention_by_hand():
     v = torch.tensor([[[5.0] * 4], [[7.0] * 4], [[11.0] * 4]])
     out, mag = ref.attention(values, torch.ones(3, 2, 4), torch.zeros(3, 1, 4), v, [-1, 0, 0])
     assert out[:, 0, 0].tolist() == [3.0, 4.0, 5.0] and torch.equal(out, mag)
+
+
+def test_the_verify_loop_refuses_what_it_cannot_run():
+    from speculative_decode_verify_w4a16_gb300 import verify_step
+
+    with pytest.raises(ValueError):
+        verify_step.decode(None, [], 1, 1, None)
+    with pytest.raises(ValueError):
+        verify_step.decode(None, [[1], []], 1, 1, None)
+    with pytest.raises(ValueError):
+        verify_step.decode(None, [[1]] * 17, 1, 4, None)
