@@ -375,12 +375,13 @@ w4a16_status w4a16_linear_noalloc(const void* x, int M, int64_t K, const void* q
  *               step completes, -1 - r for row r of the tail page; INT32_MIN
  *               behind the last
  * No output may overlap an input. The same call again, on the same inputs,
- * gives the same results. B <= 4096, ring_cap <= 2^25, B * max_blocks < 2^31.
- * Bad input (a length outside the table, falling row_start, a bad node or
- * parent, a page id outside [0, 2^25), a full ring, a queue outside the ring)
- * sets W4A16_ERR_DEVICE_INPUT in the device error word; the request then
- * keeps nothing (a bad node or parent: its root alone; a falling row_start:
- * any of the rows; a bad page: the
+ * gives the same results. B <= 4096, rows <= 2^30, ring_cap <= 2^25,
+ * B * max_blocks < 2^31.
+ * Bad input (a length outside the table, a row_start that falls or passes
+ * `rows`, a bad node or parent, a page id outside [0, 2^25), a full ring, a
+ * queue outside the ring) sets W4A16_ERR_DEVICE_INPUT in the device error
+ * word; the request then keeps nothing (a bad row_start: no request does; a
+ * bad node or parent: the request keeps its root alone; a bad page: the
  * block's slots are INT32_MIN), and nothing is written out of bounds.
  * ---------------------------------------------------------------------- */
 w4a16_status kv_block_plan(const int32_t* lens, const int32_t* tails, const int32_t* row_start,

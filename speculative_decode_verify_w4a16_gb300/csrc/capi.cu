@@ -346,7 +346,7 @@ w4a16_status kv_block_plan(const int32_t* lens, const int32_t* tails, const int3
     return W4A16_ERR_INVALID_ARG;
   if (accepted_node && (n < 1 || (int64_t)B * n != rows)) return W4A16_ERR_INVALID_ARG;
   if (B > kPlanMaxB || (accepted_node && n > 64) || ring_cap > (1 << 25) || (int64_t)B * max_blocks > INT32_MAX ||
-      max_blocks > (INT32_MAX - 63) / 64)
+      max_blocks > (INT32_MAX - 63) / 64 || rows > (1 << 30))
     return W4A16_ERR_UNSUPPORTED;
   const void* all[] = {lens,  tails,    row_start, tree_parents, accepted_node, release,  block_table, free_ring,
                        queue, new_lens, new_tails, new_start,    new_queue,     src_rows, slots};

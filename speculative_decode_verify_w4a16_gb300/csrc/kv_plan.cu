@@ -139,7 +139,16 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
       s.path[b] = j == 63 ? ~0ull : (1ull << (j + 1)) - 1ull;
     }
   }
-  __syncthreads();
+  bool bad_rows = false;
+  if (p.row_start)
+    for (int b = tid; b < B; b += nt) {
+      const int first = p.row_start[b], next = p.row_start[b + 1];
+      bad_rows |= first < 0 || next > p.rows || next < first;
+    }
+  // ranges that are not one after the other: whose a row is cannot be told, so
+  // nobody keeps any
+  bad_rows = __syncthreads_or(bad_rows);
+  if (bad_rows && say && tid == 0) report_error(p.err, kErrInput);
   const int64_t cap_tokens = (int64_t)p.max_blocks * 64 + 63;
   for (int b = tid; b < B; b += nt) {
     int len = p.lens[b], first = 0;
@@ -148,13 +157,7 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
       cnt = __popcll(s.path[b]);
     } else {
       first = p.row_start[b];
-      const int next = p.row_start[b + 1];
-      cnt = (int64_t)next - first;
-      if (first < 0 || next > p.rows || cnt < 0) {
-        if (say) report_error(p.err, kErrInput);
-        cnt = 0;
-        first = 0;
-      }
+      cnt = bad_rows ? 0 : p.row_start[b + 1] - first;
     }
     const bool ended = p.release && p.release[b] != 0;
     if (len < 0 || len > cap_tokens) {  // a length the table cannot hold
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     const int tail = p.tails[b];
     p.new_tails[b] = filled ? tail ^ 1 : tail;
   }
-  for (int b = gt; b <= B; b += gn) p.new_start[b] = max(0, min(s.start[b], p.rows));
+  for (int b = gt; b <= B; b += gn) p.new_start[b] = s.start[b];
   const int room = p.ring_cap - count;  // ring places behind the last free page
   if (gt == 0) {
     if (back > room) report_error(p.err, kErrInput);
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     const int cnt = s.start[b + 1] - s.start[b];
     if (keep && off < cnt) {
       const int len = s.len[b], i = s.start[b] + off, pos = len + off;
-      if ((unsigned)i >= (unsigned)p.rows) continue;  // overlapping ranges of a falling row_start
+      if (!in_bounds(p.err, i, p.rows)) continue;
       p.src_rows[i] = r;
       int slot = -1 - pos % 64;
       if (pos / 64 < (len + cnt) / 64) {

@@ -138,6 +138,24 @@ def test_plan_reports_bad_input():
     assert s == 5 and set(p["slots"][:B]) == {ref.SKIP}
 
 
+@pytest.mark.parametrize("start,rows", [([0, 5, 3, 9], 9), ([0, 4, 12, 12], 9), ([-2, 4, 6, 9], 9), ([0, 9, 0, 9], 9),
+                                        ([0, 4, 6, 10], 9)])
+def test_plan_with_bad_row_ranges_keeps_nothing(start, rows):
+    """And leaves nothing of an earlier plan in its outputs."""
+    rng = np.random.default_rng(4)
+    lens, tails, table, ring, queue = _plan_case(3, 200, rng, 8, 5)
+    args = [_i32(x) for x in (lens, tails, table, ring, queue)]
+    plan = sv.kv_block_plan(*args, row_start=_i32([0, 3, 6, 9]), rows=rows)
+    assert sv.check_device_status() == 0
+    args = [_i32(x) for x in (lens, tails, table, ring, queue)]
+    plan = sv.kv_block_plan(*args, row_start=_i32(start), rows=rows, plan=plan)
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 5
+    assert np.array_equal(plan.new_lens.cpu(), lens) and np.array_equal(plan.new_tails.cpu(), tails)
+    assert not plan.new_start.any() and (plan.src_rows[:rows] == -1).all() and (plan.slots[:rows] == ref.SKIP).all()
+    assert plan.queue[:2].tolist() == list(queue[:2]) and np.array_equal(args[2].cpu(), table)
+
+
 # ----------------------------------------------------------------- append
 
 def _history(rng, Hkv, tokens, D=128, scale=1.0):

@@ -38,6 +38,7 @@ def test_plan_refuses(L):
     assert plan(lens=ODD) == BAD and plan(slots=ODD) == BAD
     assert plan(B=5000, rows=25000) == UNSUPPORTED and plan(n=65, rows=260) == UNSUPPORTED
     assert plan(cap=(1 << 25) + 1) == UNSUPPORTED and plan(max_blocks=1 << 30) == UNSUPPORTED
+    assert plan(node=None, row_start=P, rows=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_append_refuses(L):
