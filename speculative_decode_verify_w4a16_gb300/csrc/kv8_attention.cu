@@ -81,8 +81,34 @@ constexpr int kKaTile = 128;      // keys per tile
 constexpr float kKaRoom = 7.0f;    // log2 of the largest weight when m is set
 constexpr float kKaLimit = 15.0f;  // ... and where m is raised
 
+// Quotients. Code that runs once is met with cold instruction caches, and an
+// integer division is some 25 instructions.
+// a / d for a < 2^31, d known to the host: with 2^(l-1) < d <= 2^l and
+// m = floor(2^(31+l) / d) + 1, m d = 2^(31+l) + e, 0 < e <= 2^l, so a m / 2^(31+l)
+// is a / d and less than 1 / d more: its integer part is the quotient.
+struct KaDiv {
+  uint32_t d, m, shift;
+  __device__ __forceinline__ int operator()(int a) const { return (int)(((uint64_t)(uint32_t)a * m) >> shift); }
+};
+static KaDiv ka_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return KaDiv{d, (uint32_t)((uint64_t(1) << (31 + l)) / d + 1), 31 + l};
+}
+// a / b, a < 2^31, from the quotient of floats: a few units off at most, then exact
+__device__ __forceinline__ unsigned ka_quot(unsigned a, unsigned b) {
+  unsigned q = (unsigned)__fdividef((float)a, (float)b);
+  int r = (int)(a - q * b);
+#pragma unroll 1
+  for (; r < 0; r += (int)b) --q;
+#pragma unroll 1
+  for (; r >= (int)b; r -= (int)b) ++q;
+  return q;
+}
+
 struct KaWork {  // the cut of the tiles into runs
-  int row_blocks, np, ctas, min_tiles;
+  int row_blocks, np, G;  // G query heads a head
+  KaDiv by_g, by_blocks, by_units, by_ctas;
   int* done;        // [ctas]: finished parts of the cut unit that begins in a run; zero at rest
   float2* part_ml;  // [2 ctas][np]
   float* part_o;    // [2 ctas][np][D]
@@ -217,20 +243,21 @@ __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSe
   return true;
 }
 
-// As many runs of the T tiles as leave min_tiles tiles each; run c of them
-// begins at c (T / runs) + min(c, T % runs). (T < 2^31: the host checks.)
+// As many runs of the T tiles as leave two tiles each, one an SM at most; run c
+// of them begins at c per + min(c, rest). (1 <= T < 2^31: the host checks.)
 struct KaCut {
   unsigned runs, per, rest;
-  __device__ __forceinline__ KaCut(unsigned T, unsigned ctas, unsigned min_tiles) {
-    runs = T / min_tiles;
-    runs = runs < 1u ? 1u : runs > ctas ? ctas : runs;
-    per = T / runs;
+  KaCut() = default;
+  __device__ __forceinline__ KaCut(unsigned T, const KaDiv& by_ctas) {
+    const bool all = T / 2 >= by_ctas.d;
+    runs = all ? by_ctas.d : max(T / 2, 1u);
+    per = all ? (unsigned)by_ctas((int)T) : min(T, 2u);
     rest = T - per * runs;
   }
   __device__ __forceinline__ unsigned begin(unsigned c) const { return c * per + min(c, rest); }
   __device__ __forceinline__ unsigned owner(unsigned f) const {  // the run that holds tile f
     const unsigned big = rest * (per + 1u);
-    return f < big ? f / (per + 1u) : rest + (f - big) / per;
+    return f < big ? ka_quot(f, per + 1u) : rest + ka_quot(f - big, per);
   }
 };
 
@@ -316,41 +343,78 @@ __device__ __forceinline__ void ka_bar_all() {
   asm volatile("barrier.cta.sync 9, %0;" ::"n"(128 * GROUPS) : "memory");
 }
 
-// The parts of a cut unit merged: the first in slot s0, that of run c0 + k in
-// slot 2 (c0 + k). A thread takes column d of its warpgroup's 16 rows; lane l
-// holds the maxima and sums of row l % 16.
+// A cut unit whose parts are all there, for this CTA to merge
+struct KaMerge {
+  int b, u;
+  unsigned s0, c0, parts;  // the first part in slot s0, that of run c0 + k in slot 2 (c0 + k)
+};
+
+// By the whole CTA, at its end: a warp takes 4 rows, a lane 4 columns of each;
+// lane 4 k + i has (m, l) of the k-th of 8 parts in row r + i. The loads of
+// kAhead parts are in flight together, the first ones' next to the (m, l): what
+// costs here is the latency of L2.
 template <int NP>
-__device__ __noinline__ void ka_merge(const Kv8AttnParams& p, const KaWork& wk, unsigned s0, unsigned c0,
-                                      unsigned parts, int qa, int d, int lane, const int* row) {
-  const int r = qa + (lane & 15);
-  float M = -INFINITY;
-#pragma unroll 4
-  for (unsigned k = 0; k < parts; ++k)
-    M = fmaxf(M, __ldcg(&wk.part_ml[(k ? 2u * (c0 + k) : s0) * NP + r]).x);
-  float l = 0.0f, o[16], x[16];
-  auto load = [&](unsigned k) {
-    const float* src = wk.part_o + ((size_t)(k ? 2u * (c0 + k) : s0) * NP + qa) * kKaD + d;
+__device__ __forceinline__ void ka_merge(const Kv8AttnParams& p, const KaWork& wk, const KaMerge& mg, int r, int lane) {
+  constexpr int kAhead = NP <= 32 ? 4 : 2;
+  const unsigned parts = mg.parts;
+  auto slot = [&](unsigned k) { return (size_t)(k ? 2u * (mg.c0 + k) : mg.s0) * NP + r; };
+  float4 x[kAhead][4], o[4];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) x[q] = __ldcg(src + q * kKaD);
+  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto load = [&](unsigned k0) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (k0 + a < parts) {
+        const float4* src = reinterpret_cast<const float4*>(wk.part_o + slot(k0 + a) * kKaD) + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[a][i] = __ldcg(src + i * (kKaD / 4));
+      }
+  };
+  auto stat = [&](unsigned k0) {
+    const unsigned k = k0 + (lane >> 2);
+    return k < parts ? __ldcg(&wk.part_ml[slot(k) + (lane & 3)]) : make_float2(-INFINITY, 0.0f);
   };
   load(0u);
-#pragma unroll
-  for (int q = 0; q < 16; ++q) o[q] = 0.0f;
+  float2 ml = stat(0u);
+  float M = ml.x;
 #pragma unroll 1
-  for (unsigned k = 0; k < parts; ++k) {
-    const float2 ml = __ldcg(&wk.part_ml[(k ? 2u * (c0 + k) : s0) * NP + r]);
-    const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);
+  for (unsigned k = 8; k < parts; k += 8) M = fmaxf(M, stat(k).x);
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float l = 0.0f;
+#pragma unroll 1
+  for (unsigned k8 = 0; k8 < parts; k8 += 8) {
+    if (k8) ml = stat(k8);
+    const float w = ml.x == M ? 1.0f : ka_ex2(ml.x - M);  // 0 for a part that is not there
     l = fmaf(w, ml.y, l);
+#pragma unroll 1
+    for (unsigned k = k8; k < min(k8 + 8u, parts); k += kAhead) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) o[q] = fmaf(__shfl_sync(0xffffffffu, w, q), x[q], o[q]);
-    if (k + 1 < parts) load(k + 1);
+      for (int a = 0; a < kAhead; ++a)
+        if (k + a < parts) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, (int)(4u * (k - k8 + a)) + i);
+            o[i].x = fmaf(wi, x[a][i].x, o[i].x);
+            o[i].y = fmaf(wi, x[a][i].y, o[i].y);
+            o[i].z = fmaf(wi, x[a][i].z, o[i].z);
+            o[i].w = fmaf(wi, x[a][i].w, o[i].w);
+          }
+        }
+      if (k + kAhead < parts) load(k + kAhead);
+    }
   }
-  const float inv = 1.0f / l;
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const float x = o[q] * __shfl_sync(0xffffffffu, inv, q);
-    if (row[qa + q] >= 0 && in_bounds(p.err, row[qa + q], (int64_t)p.B * p.n * p.H))
-      p.out[(int64_t)row[qa + q] * kKaD + d] = __float2bfloat16_rn(x);
+  for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const float inv = 1.0f / l;
+  const int G = wk.G, kvh = wk.by_blocks(mg.u), R0 = (mg.u - kvh * wk.row_blocks) * NP + r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float v = __shfl_sync(0xffffffffu, inv, i);
+    const int R = R0 + i, j = wk.by_g(R), row = (mg.b * p.n + j) * p.H + kvh * G + R - j * G;
+    if (R < p.n * G && in_bounds(p.err, row, (int64_t)p.B * p.n * p.H))
+      reinterpret_cast<uint2*>(p.out + (int64_t)row * kKaD)[lane] =
+          make_uint2(ka_bf162(o[i].x * v, o[i].y * v), ka_bf162(o[i].z * v, o[i].w * v));
   }
 }
 
@@ -386,7 +450,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   __shared__ uint32_t tmem_s;
   __shared__ unsigned scan_s[32];
   __shared__ unsigned s_pre;
-  __shared__ int s_b, s_last;
+  __shared__ int s_b;
+  __shared__ KaCut cut_s;
+  __shared__ KaMerge merge_s[2];  // a run's first and last unit
   __shared__ int par_s[64];
   __shared__ unsigned long long bad_s[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -411,6 +477,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     mbar_init(q_ready, 4 * C::kGroups);
     mbar_init(x_full, 1);
     fence_mbarrier_init();
+    merge_s[0].parts = merge_s[1].parts = 0u;
   }
   if (warp == 2) {
     tmem_alloc(&tmem_s, C::kCols);
@@ -443,10 +510,15 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     x = lane < C::kThreads / 32 ? scan_s[lane] : 0u;
     T = __reduce_add_sync(0xffffffffu, x) * (unsigned)units;
   }
-  const KaCut runs(T, (unsigned)wk.ctas, (unsigned)wk.min_tiles);
-  const unsigned f0 = runs.begin(blockIdx.x), f1 = runs.begin(blockIdx.x + 1u);
+  unsigned f0, f1;
   {
-    const unsigned target = f0 / (unsigned)units;  // tiles of one unit of the requests before b <= target
+    const KaCut runs(T, wk.by_ctas);
+    f0 = runs.begin(blockIdx.x);
+    f1 = blockIdx.x < runs.runs ? runs.begin(blockIdx.x + 1u) : f0;
+    if (tid == 0) cut_s = runs;
+  }
+  {
+    const unsigned target = (unsigned)wk.by_units((int)f0);  // tiles of one unit of the requests before b <= target
     unsigned before = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B && before <= target; b0 += C::kThreads) {
@@ -477,13 +549,13 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   KaIter it;
   {
     it.at = f0;
-    it.left = blockIdx.x < runs.runs ? f1 - f0 : 0u;
+    it.left = f1 - f0;
     it.units = units;
     it.b = it.left > 0 ? s_b : 0;
     it.len = ka_len(p, it.b);
     it.nt = ka_tiles(it.len);
     const unsigned rel = it.left > 0 ? f0 - (unsigned)units * s_pre : 0u;
-    it.u = (int)(rel / (unsigned)it.nt);
+    it.u = (int)ka_quot(rel, (unsigned)it.nt);
     it.tile = (int)rel - it.u * it.nt;
   }
   KaSeg sg;
@@ -502,7 +574,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       return use < S || ka_wait(&k_free[use % S], (uint32_t)(use / S - 1) & 1u, p.err);
     };
     while (ok && ka_next(p, it, sg)) {
-      const int kvh = sg.u / wk.row_blocks;
+      const int kvh = wk.by_blocks(sg.u);
       if (sg.lo == 0) {
         const int t = sg.len & 63;
         const bool pass = kc % S == S - 1;
@@ -726,7 +798,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           if (ct == 0) bad_s[seg & 3] = 0ull;
           asm volatile("barrier.cta.sync 8, 128;" ::: "memory");  // (ids 1 .. 4 and 9: the softmax)
           if (ct == 0 && ok) {  // (all four warps are past the last such tile)
-            const int kvh = sg.u / wk.row_blocks;
+            const int kvh = wk.by_blocks(sg.u);
             mbar_arrive_expect_tx(x_full, (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
             for (int h = 0; h < 2; ++h) {
               if (tok) tma_load_3d(w + h * C::kTileBytes, &maps.v_tail, 64 * h, 0, tail * p.Hkv + kvh, x_full);
@@ -818,19 +890,17 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     const int qa = wg * Q;                           // its first row
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
     const int bar = 1 + wg;
-    const int G = p.H / p.Hkv, rows = p.n * G;
+    const int G = wk.G, rows = p.n * G;
     const float4* gm = reinterpret_cast<const float4*>(gm_s) + (qa >> 1);
     // where the thread's 16 columns of a part's query row are (eight lanes a
     // row); null for a row that does not exist
     auto q_at = [&](const KaSeg& g) {
-      const int kvh = g.u / wk.row_blocks, R = (g.u - kvh * wk.row_blocks) * NP + qa + (st >> 3), j = R / G;
+      const int kvh = wk.by_blocks(g.u), R = (g.u - kvh * wk.row_blocks) * NP + qa + (st >> 3), j = wk.by_g(R);
       return R < rows ? p.q + ((int64_t)g.b * p.n + j) * p.q_stride + (kvh * G + R - j * G) * kKaD + 16 * (st & 7)
                       : nullptr;
     };
     int tc = 0, seg = 0;
     bool ok = true;
-    KaSeg nx;
-    bool more = ka_next(p, it, nx);
     uint4 v[2];  // the thread's 16 columns of a part's query row
     auto q_load = [&](const __nv_bfloat16* at) {
       v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
@@ -839,10 +909,12 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         v[1] = reinterpret_cast<const uint4*>(at)[1];
       }
     };
-    if (more) q_load(q_at(nx));
-    while (more) {
-      sg = nx;
-      const int kvh = sg.u / wk.row_blocks, rb = sg.u - kvh * wk.row_blocks;
+    {
+      KaIter first = it;
+      if (ka_next(p, first, sg)) q_load(q_at(sg));
+    }
+    while (ka_next(p, it, sg)) {
+      const int kvh = wk.by_blocks(sg.u), rb = sg.u - kvh * wk.row_blocks;
       // ---- Q: x = q 2^ex, |x| < 256, as bf16 and as two e4m3 terms
       {
         if (sg.lo == 0 && p.parents && st < p.n) {
@@ -897,7 +969,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
         if (c == 0) {
-          const int R = rb * NP + r, j = R / G;
+          const int R = rb * NP + r, j = wk.by_g(R);
           gm_s[4 * (r >> 1) + (r & 1)] = __uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2;
           gm_s[4 * (r >> 1) + 2 + (r & 1)] = 0.0f;
           row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + R - j * G : -1;
@@ -905,7 +977,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         ka_bar(bar);
         if (sg.lo == 0) {
           if (st < Q) {
-            const int R = rb * NP + qa + st, j = R / G;
+            const int R = rb * NP + qa + st, j = wk.by_g(R);
             uint64_t mk = 0;
             if (R < rows) {
               if (p.parents)
@@ -920,8 +992,12 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         }
       }
       // the next part's query rows on their way to L2
-      more = ka_next(p, it, nx);
-      const __nv_bfloat16* q_next = more ? q_at(nx) : nullptr;
+      const __nv_bfloat16* q_next = nullptr;
+      {
+        KaIter after = it;
+        KaSeg next;
+        if (ka_next(p, after, next)) q_next = q_at(next);
+      }
       if (q_next && !(st & 1)) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_next));
       uint64_t l[Q / 2];
 #pragma unroll
@@ -1084,7 +1160,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           float* dst = wk.part_o + ((size_t)slot * NP + qa + q0) * kKaD + key;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (in_bounds(p.err, (int64_t)slot * NP + qa + q0 + q, (int64_t)2 * wk.ctas * NP))
+            if (in_bounds(p.err, (int64_t)slot * NP + qa + q0 + q, (int64_t)2 * wk.by_ctas.d * NP))
               dst[q * kKaD] = __uint_as_float(o[q]);
         }
       }
@@ -1099,19 +1175,18 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         }
       }
       if (!whole) {
-        // ---- the last of the unit's CTAs merges the parts
-        const unsigned u0 = sg.at - (unsigned)sg.lo;  // the unit's first tile
-        const unsigned c0 = runs.owner(u0), parts = runs.owner(u0 + (unsigned)sg.nt - 1u) - c0 + 1u;
+        // ---- the last of the unit's CTAs is to merge the parts, at its end
         ka_bar_all<C::kGroups>();  // (the counter's release covers what the barrier has gathered)
         if (warp == C::kSoft0 && lane == 0) {
-          s_last = atomic_add_acq_rel(&wk.done[c0], 1) == (int)parts - 1;
-          if (s_last) wk.done[c0] = 0;
+          const KaCut runs = cut_s;
+          const unsigned u0 = sg.at - (unsigned)sg.lo;  // the unit's first tile
+          const unsigned c0 = runs.owner(u0), parts = runs.owner(u0 + (unsigned)sg.nt - 1u) - c0 + 1u;
+          if (atomic_add_acq_rel(&wk.done[c0], 1) == (int)parts - 1) {
+            wk.done[c0] = 0;
+            // the first part is its run's first only if the run begins with it
+            merge_s[seg == 0 ? 0 : 1] = KaMerge{sg.b, sg.u, 2u * c0 + (runs.begin(c0) == u0 ? 0u : 1u), c0, parts};
+          }
         }
-        ka_bar_all<C::kGroups>();
-        // the first part is its run's first only if the run begins with it
-        if (s_last)
-          ka_merge<NP>(p, wk, 2u * c0 + (runs.begin(c0) == u0 ? 0u : 1u), c0, parts, qa, key, lane, row_s);
-        ka_bar_all<C::kGroups>();
       }
       tc_fence_before();
       ka_bar(bar);  // the small arrays are free for the next part
@@ -1130,6 +1205,9 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k)
+    if (merge_s[k].parts > 0u && 4 * warp < NP) ka_merge<NP>(p, wk, merge_s[k], 4 * warp, lane);
 }
 
 // ------------------------------------------------------------------ host
@@ -1164,7 +1242,7 @@ static cudaError_t launch_ka(const KaMaps& maps, const Kv8AttnParams& p, const K
   const cudaError_t e =
       cudaFuncSetAttribute(kv8_attention_kernel<NP, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_attention_kernel<NP, FMT>, dim3((unsigned)wk.ctas), dim3(KaCfg<NP>::kThreads), (size_t)smem,
+  return launch_pdl(kv8_attention_kernel<NP, FMT>, dim3(wk.by_ctas.d), dim3(KaCfg<NP>::kThreads), (size_t)smem,
                     stream, maps, p, wk);
 }
 
@@ -1204,8 +1282,11 @@ cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspac
   KaWork wk;
   wk.row_blocks = k.row_blocks;
   wk.np = k.np;
-  wk.ctas = k.ctas;
-  wk.min_tiles = 2;
+  wk.G = p.H / p.Hkv;
+  wk.by_g = ka_div((uint32_t)wk.G);
+  wk.by_blocks = ka_div((uint32_t)wk.row_blocks);
+  wk.by_units = ka_div((uint32_t)(p.Hkv * wk.row_blocks));
+  wk.by_ctas = ka_div((uint32_t)k.ctas);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   wk.done = reinterpret_cast<int*>(ws);
   wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
