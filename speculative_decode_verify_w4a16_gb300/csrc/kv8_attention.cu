@@ -257,7 +257,8 @@ struct KaCut {
   __device__ __forceinline__ unsigned begin(unsigned c) const { return c * per + min(c, rest); }
   __device__ __forceinline__ unsigned owner(unsigned f) const {  // the run that holds tile f
     const unsigned big = rest * (per + 1u);
-    return f < big ? ka_quot(f, per + 1u) : rest + ka_quot(f - big, per);
+    const bool low = f < big;
+    return (low ? 0u : rest) + ka_quot(low ? f : f - big, low ? per + 1u : per);
   }
 };
 
@@ -575,8 +576,18 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     };
     while (ok && ka_next(p, it, sg)) {
       const int kvh = wk.by_blocks(sg.u);
+      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1. Lane 2 k + h
+      // has block h of the k-th of 16 tiles, its page and scales; the next 16
+      // tiles' are asked for ahead.
+      const int full = sg.len / 64, i0 = max(sg.lo, 1);
+      const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
+      auto page_of = [&](int i) {  // of the 16 tiles from i on; -2: no such block
+        const int blk = 2 * (i - 1) + lane;
+        return blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
+      };
+      int page_n = page_of(i0);  // (asked for before the bf16 tile: its latency then passes beside that)
       if (sg.lo == 0) {
-        const int t = sg.len & 63;
+        const int t = sg.len & 63, tail = lane == 0 ? p.tails[sg.b] : 0;
         const bool pass = kc % S == S - 1;
         if (lane == 0) {
           if (pass && (ok = k_wait(kc))) {
@@ -586,7 +597,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           const int use = kc + (pass ? 1 : 0), s = use % S;
           ok = ok && k_wait(use) && k_wait(use + 1);
           if (ok) {
-            const int tail = p.tails[sg.b];
             const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
             if (t > 0 && !tok) report_error(p.err, kErrInput);
             uint8_t* kd = smem + C::kKOff + s * C::kTileBytes;
@@ -605,16 +615,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         if (ok) kc += pass ? 3 : 2;
         ++tc;
       }
-      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1. Lane 2 k + h
-      // has block h of the k-th of 16 tiles, its page and scales; the next 16
-      // tiles' are asked for ahead.
-      const int full = sg.len / 64, i0 = max(sg.lo, 1);
-      const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
-      auto page_of = [&](int i) {  // of the 16 tiles from i on; -2: no such block
-        const int blk = 2 * (i - 1) + lane;
-        return blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
-      };
-      int page = -2, page_n = page_of(i0);
+      int page = -2;
       float sk = 0.0f, lsv = 0.0f, isv = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
       auto scales_of = [&]() {  // of the pages asked for earlier
         sk_n = 0.0f;
@@ -1180,7 +1181,14 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         if (warp == C::kSoft0 && lane == 0) {
           const KaCut runs = cut_s;
           const unsigned u0 = sg.at - (unsigned)sg.lo;  // the unit's first tile
-          const unsigned c0 = runs.owner(u0), parts = runs.owner(u0 + (unsigned)sg.nt - 1u) - c0 + 1u;
+          unsigned c0 = blockIdx.x, c1 = blockIdx.x;    // the runs of its first and last
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e)
+            if (e ? sg.hi < sg.nt : sg.lo > 0) {
+              const unsigned c = runs.owner(e ? u0 + (unsigned)sg.nt - 1u : u0);
+              e ? c1 = c : c0 = c;
+            }
+          const unsigned parts = c1 - c0 + 1u;
           if (atomic_add_acq_rel(&wk.done[c0], 1) == (int)parts - 1) {
             wk.done[c0] = 0;
             // the first part is its run's first only if the run begins with it
