@@ -139,16 +139,8 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
       s.path[b] = j == 63 ? ~0ull : (1ull << (j + 1)) - 1ull;
     }
   }
+  __syncthreads();
   bool bad_rows = false;
-  if (p.row_start)
-    for (int b = tid; b < B; b += nt) {
-      const int first = p.row_start[b], next = p.row_start[b + 1];
-      bad_rows |= first < 0 || next > p.rows || next < first;
-    }
-  // ranges that are not one after the other: whose a row is cannot be told, so
-  // nobody keeps any
-  bad_rows = __syncthreads_or(bad_rows);
-  if (bad_rows && say && tid == 0) report_error(p.err, kErrInput);
   const int64_t cap_tokens = (int64_t)p.max_blocks * 64 + 63;
   for (int b = tid; b < B; b += nt) {
     int len = p.lens[b], first = 0;
@@ -157,7 +149,9 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
       cnt = __popcll(s.path[b]);
     } else {
       first = p.row_start[b];
-      cnt = bad_rows ? 0 : p.row_start[b + 1] - first;
+      const int next = p.row_start[b + 1];
+      cnt = (int64_t)next - first;
+      bad_rows |= first < 0 || next > p.rows || cnt < 0;
     }
     const bool ended = p.release && p.release[b] != 0;
     if (len < 0 || len > cap_tokens) {  // a length the table cannot hold
@@ -177,6 +171,12 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     s.need[b] = (int)((len + cnt) / 64 - len / 64);
     s.back[b] = ended ? len / 64 : 0;
     s.start[b] = (int)cnt;
+  }
+  // ranges that are not one after the other: whose a row is cannot be told, so
+  // nobody keeps any
+  if (__syncthreads_or(bad_rows)) {
+    if (say && tid == 0) report_error(p.err, kErrInput);
+    for (int b = tid; b < B; b += nt) s.start[b] = s.need[b] = 0;
   }
   plan_scan(s.need, B, scratch);
   plan_scan(s.back, B, scratch);
