@@ -37,32 +37,40 @@ struct PlanArrays {
   uint64_t* path;
 };
 
-// Exclusive sum over the requests, in place: a[0 .. B - 1] holds the counts on
-// entry, a[B] the total on return. Every thread of the CTA calls it.
-__device__ void plan_scan(int* a, int B, int* scratch) {
+// Exclusive sums over the requests, in place, of N arrays at once (the barriers
+// are what costs): a[k][0 .. B - 1] hold the counts on entry, a[k][B] the total
+// on return. Every thread of the CTA calls it.
+template <int N>
+__device__ __forceinline__ void plan_scan(int* const (&a)[N], int B, int2* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int per = (B + blockDim.x - 1) / blockDim.x;
   const int i0 = min(B, (int)threadIdx.x * per), i1 = min(B, i0 + per);
   __syncthreads();  // the counts are written, and scratch is free
-  int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += a[i];
-  int x = sum;
+  int sum[2] = {0, 0}, x[2];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
+  for (int k = 0; k < N; ++k) {
+    for (int i = i0; i < i1; ++i) sum[k] += a[k][i];
+    x[k] = sum[k];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], d);
+      if (lane >= d) x[k] += y;
+    }
   }
-  if (lane == 31) scratch[warp] = x;
+  if (lane == 31) scratch[warp] = make_int2(x[0], N > 1 ? x[N - 1] : 0);
   __syncthreads();
-  const int w = lane < nw ? scratch[lane] : 0;
-  const int total = __reduce_add_sync(0xffffffffu, w);
-  int o = x - sum + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
-  for (int i = i0; i < i1; ++i) {
-    const int c = a[i];
-    a[i] = o;
-    o += c;
+  const int2 w2 = lane < nw ? scratch[lane] : make_int2(0, 0);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int w = k ? w2.y : w2.x, total = __reduce_add_sync(0xffffffffu, w);
+    int o = x[k] - sum[k] + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    for (int i = i0; i < i1; ++i) {
+      const int c = a[k][i];
+      a[k][i] = o;
+      o += c;
+    }
+    if (threadIdx.x == 0) a[k][B] = total;
   }
-  if (threadIdx.x == 0) a[B] = total;
   __syncthreads();
 }
 
@@ -87,7 +95,7 @@ __device__ __forceinline__ int plan_ring(int head, int a, int cap) {
 
 __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanParams p) {
   extern __shared__ uint64_t plan_smem[];
-  __shared__ int scratch[32];
+  __shared__ int2 scratch[32];
   const int B = p.B, tid = threadIdx.x, nt = blockDim.x;
   PlanArrays s;
   s.path = plan_smem;
@@ -178,8 +186,10 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     if (say && tid == 0) report_error(p.err, kErrInput);
     for (int b = tid; b < B; b += nt) s.start[b] = s.need[b] = 0;
   }
-  plan_scan(s.need, B, scratch);
-  plan_scan(s.back, B, scratch);
+  {
+    int* const pages[2] = {s.need, s.back};
+    plan_scan(pages, B, scratch);
+  }
   // ---- grants: need[] and back[] are sums before each request now
   __shared__ int taken_s;
   if (tid == 0) taken_s = 0;
@@ -195,7 +205,8 @@ __global__ void __launch_bounds__(1024) kv_block_plan_kernel(const BlockPlanPara
     }
   }
   if (most) atomicMax(&taken_s, most);
-  plan_scan(s.start, B, scratch);  // the rows of granted requests
+  int* const granted[1] = {s.start};
+  plan_scan(granted, B, scratch);  // the rows of granted requests
   const int taken = taken_s, asked = s.need[B], back = s.back[B], kept = s.start[B];
   const int gt = blockIdx.x * nt + tid, gn = gridDim.x * nt;
 
