@@ -33,8 +33,11 @@
 // the first tile of a part, and seldom after it).
 //
 // Code that runs once per part (the query rows, the first maximum, the end) is
-// kept short, in rolled loops: a CTA meets it with cold instruction caches, and
-// straight-line code then costs some 300 cycles per eight instructions.
+// kept short: a CTA meets it with cold instruction caches, and straight-line
+// code then costs some 20 to 40 cycles an instruction. Hence the quotients without
+// integer divisions and the merge of cut units after everything else, where
+// all warps take part and no registers have to be kept (both together: the
+// trees 225 -> 201 us, one request of one node 14.0 -> 12.6).
 //
 // The last tile of bf16 rows, the tail page's (rows 0 .. 63 of the tile) and
 // the tree's own (64 .. 127), comes first in a request's tiles, with bf16
@@ -51,20 +54,21 @@
 // per run, and the CTA that finishes last of them (a counter) merges them.
 //
 // Measured (one layer of 64 query heads on 8, e4m3): four requests of 120 to
-// 131 K tokens, one node each (1.02 GB) 161 us, 0.94 of the HBM copy rate, which
-// bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 51 us, 0.58 of
-// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 225 us, 0.24 of
-// the bf16 rate; one request of 1003 tokens and one node 14 us. The chains and
-// trees are bound by the softmax warps' latency: a tile takes 1600 cycles at 48
-// rows and 2000 at 64 (the products take 460 and 600 of them, the warps issue in
-// 40 to 50 % of the cycles), and a part's start and end another 10000. Measured
+// 131 K tokens, one node each (1.02 GB) 158 us, 0.96 of the HBM copy rate, which
+// bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 48 us, 0.61 of
+// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 201 us, 0.27 of
+// the bf16 rate; one request of 1003 tokens and one node 12.5 us. The chains and
+// trees are bound by the softmax warps' latency: a tile takes some 1600 cycles at
+// 48 rows and 1800 at 64 (the products take 460 and 600 of them, the warps issue
+// in 40 to 50 % of the cycles), and a part's start and end some 8000. Measured
 // and not kept, against what there was at the time: 128 rows a block with 32 a
 // warpgroup, the trees in 563 us (registers); 32 rows a warpgroup at 64, no gain
 // (fewer warps to hide latency with); the two terms' products added up in TMEM,
 // 272 against 240; the next part's query rows prepared by a warp of its own,
 // 273 against 232 (it takes 2500 cycles for four rows; their loads before the
-// part's end: 225); scores given back when read and fetched a tile ahead, 249
-// against 225, the chains 52 against 51.
+// part's end: 225); scores given back when read, and fetched a tile ahead where
+// registers allow, 208 against 201 and the chains 50 against 48; cut units
+// announced at the CTA's end only, 206.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
