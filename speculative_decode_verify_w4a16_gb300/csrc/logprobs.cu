@@ -25,12 +25,14 @@
 // a row from its first load to its report (token_logprobs_kernel); with fewer,
 // the windows are spread over all SMs and a second kernel reports
 // (token_stats_kernel, token_report_kernel). Rows of 128256 logits, both ways,
-// in us: 64 rows 16 and 13, 228 27 and 22, 608 33 and 40 (fp32 55 and 58), 912
-// 51 and 58 (bf16).
+// in us (before the last steps): 64 rows 16 and 13, 228 27 and 22, 608 33 and 40
+// (fp32 55 and 58), 912 51 and 58 (bf16).
 // A row's CTA has 256 threads, four CTAs an SM: with 1024 rows the later rows
-// stream while the first ones report (58 us, 263 MB: 0.67 of the HBM copy rate);
-// 128 threads and eight CTAs take them all at once and then report all at once,
-// 68 us; 512 threads 63 us. 16 rows of fp32 (8.2 MB) take 7.7 us, latency.
+// stream while the first ones report (56 us, 263 MB: 0.70 of the HBM copy rate;
+// 58 us with every load's bounds looked at, not only those of a row's ends); 128
+// threads and eight CTAs take them all at once and then report all at once, 68
+// against 58; 512 threads 63; the maxima by the reduction instruction for floats
+// 58 against 56. 16 rows of fp32 (8.2 MB) take 7.7 us, latency.
 // Windows start at 16-byte boundaries of memory, not of the row, so that rows of
 // any length load 16 bytes at a time.
 #include <math.h>
@@ -245,9 +247,15 @@ __device__ __forceinline__ void lp_window(uint4 (&raw)[32 * sizeof(T) / 16], int
 template <typename T>
 __device__ __forceinline__ void lp_fetch(const T* row, int w, int V, int lane, uint4 (&raw)[32 * sizeof(T) / 16]) {
   constexpr int E = 16 / sizeof(T), L = 32 / E;
-  const int e0 = w * kLpWindow - lp_shift(row) + lane * E;
+  const int first = w * kLpWindow - lp_shift(row), e0 = first + lane * E;
+  if (first >= 0 && first + kLpWindow <= V) {  // all but the row's ends
+    const uint4* p = reinterpret_cast<const uint4*>(row + e0);
 #pragma unroll
-  for (int k = 0; k < L; ++k) raw[k] = lp_load<T>(row, e0 + k * 32 * E, V);
+    for (int k = 0; k < L; ++k) raw[k] = __ldg(p + k * 32);
+  } else {
+#pragma unroll
+    for (int k = 0; k < L; ++k) raw[k] = lp_load<T>(row, e0 + k * 32 * E, V);
+  }
 }
 
 template <typename T>
