@@ -253,4 +253,18 @@ __device__ __forceinline__ float ldg_stream_f(const float* p) {
   return v;
 }
 
+// ------------------------------------------------------------ quotients
+// a / d for a < 2^31, d known to the host: with 2^(l-1) < d <= 2^l and
+// m = floor(2^(31+l) / d) + 1, m d = 2^(31+l) + e, 0 < e <= 2^l, so a m / 2^(31+l)
+// is a / d and less than 1 / d more: its integer part is the quotient.
+struct FastDiv {
+  uint32_t d, m, shift;
+  __device__ __forceinline__ int operator()(int a) const { return (int)(((uint64_t)(uint32_t)a * m) >> shift); }
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return FastDiv{d, (uint32_t)((uint64_t(1) << (31 + l)) / d + 1), 31 + l};
+}
+
 }  // namespace w4a16

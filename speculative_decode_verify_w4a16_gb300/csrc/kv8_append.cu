@@ -19,12 +19,14 @@
 // tail rows, (request, group of layer-heads) by (request, group): no CTA is
 // launched for work that is not there (one CTA for every piece that might exist
 // took 33 us for 80 layers of 16 drafts).
-// Measured: prompts of 32767 rows (8 heads, 182 MB) 37.9 us, 0.71 of the HBM
-// copy rate; 80 rows of 16 drafts in 80 layers (60 MB, most of it blocks that
-// complete) 16.4 us, 0.54; 64 rows of one layer 3.8 us. Keys and values by the
-// same CTA (256 threads, four an SM): 37.3, 16.8 and 4.4 us. The next item's
-// words on their way meanwhile (in registers, or copied to shared memory
-// asynchronously): 41 to 45 us for the prompts.
+// Measured: prompts of 32767 rows (8 heads, 182 MB) 36 us, 0.75 of the HBM copy
+// rate; 80 rows of 16 drafts in 80 layers (60 MB, most of it blocks that
+// complete) 14.9 us, 0.60; 64 rows of one layer 3.7 us. Against what there was at
+// the time: keys and values by the same CTA (256 threads, four an SM) 37.3, 16.8
+// and 4.4 us against 37.9, 16.4 and 3.8; the next item's words on their way
+// meanwhile (in registers, or copied to shared memory asynchronously) 41 to 45 us
+// for the prompts against 40; integer divisions for layers and tail rows 37.9 and
+// 16.4 us against 36.0 and 14.9.
 #include <cuda_fp8.h>
 #include <limits.h>
 
@@ -46,6 +48,7 @@ struct AppendParams {
   __nv_bfloat16 *k_tail, *v_tail;
   unsigned* err;
   int group;   // (layer, head) pairs of a tail item
+  FastDiv by_heads;
 };
 
 // exponent k of the scale for the largest finite magnitude's bf16 bits
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kAppThreads, 8) kv8_append_kernel(const Append
   if (item.pc < pages && tid < 64) find(item.pc, 0);
   __syncthreads();
   for (Item next = item; item.pc < pages; item = next, buf ^= 1) {
-    const int lh = item.lh, layer = lh / p.Hkv, h = lh - layer * p.Hkv;
+    const int lh = item.lh, layer = p.by_heads(lh), h = lh - layer * p.Hkv;
     const int page = min(s_at[buf][0].x, s_at[buf][1].x), tail = s_at[buf][0].y;
     const __nv_bfloat16* a = src_new + layer * p.layer_stride + h * kAppD + c;
     const __nv_bfloat16* o = src_tail + (((int64_t)layer * p.tail_pages + tail) * p.Hkv + h) * 64 * kAppD + c;
@@ -274,6 +277,8 @@ __global__ void __launch_bounds__(kAppThreads, 8) kv8_append_kernel(const Append
       continue;
     }
     const int total = (r1 - r0) * 32 * min(p.group, pairs - lh0);
+    // q / rows for q < 1024 by 2^20 / rows rounded up (1 to 64 rows, 16 pairs)
+    const int rows = r1 - r0, inv = (1 << 20) / rows + 1;
     constexpr int kBatch = 4;  // words a thread holds: their loads are in flight together
     for (int w0 = tid; w0 < total; w0 += kBatch * kAppThreads) {
       uint4 v[kBatch];
@@ -283,8 +288,8 @@ __global__ void __launch_bounds__(kAppThreads, 8) kv8_append_kernel(const Append
         const int w = w0 + k * kAppThreads;
         if (w < total) {
           const int q = w >> 5, d = w & 31;  // d: 0 .. 15 keys, 16 .. 31 values
-          const int dl = q / (r1 - r0), r = r0 + q - dl * (r1 - r0);
-          const int lh = lh0 + dl, layer = lh / p.Hkv, h = lh - layer * p.Hkv;
+          const int dl = (q * inv) >> 20, r = r0 + q - dl * rows;
+          const int lh = lh0 + dl, layer = p.by_heads(lh), h = lh - layer * p.Hkv;
           v[k] = __ldg(reinterpret_cast<const uint4*>((d < 16 ? p.k_new : p.v_new) + layer * p.layer_stride +
                                                       (int64_t)p.src_rows[base + r] * p.row_stride + h * kAppD +
                                                       (d & 15) * 8));
@@ -334,6 +339,7 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, int64_t row_
   int64_t group = (int64_t)B * pairs / (2 * most);  // tail items of two CTAs' turns, 1 .. 16 pairs each
   group = group < 1 ? 1 : group > 16 ? 16 : group;
   p.group = (int)group;
+  p.by_heads = fast_div((uint32_t)Hkv);
   const int64_t items = 2 * (rows / 64 + (int64_t)B) * pairs, tail_items = B * ((pairs + group - 1) / group);
   const int64_t ctas = items > tail_items ? items : tail_items;
   const dim3 grid((unsigned)(ctas < most ? ctas + (ctas & 1) : most));

@@ -85,20 +85,8 @@ constexpr int kKaTile = 128;      // keys per tile
 constexpr float kKaRoom = 7.0f;    // log2 of the largest weight when m is set
 constexpr float kKaLimit = 15.0f;  // ... and where m is raised
 
-// Quotients. Code that runs once is met with cold instruction caches, and an
-// integer division is some 25 instructions.
-// a / d for a < 2^31, d known to the host: with 2^(l-1) < d <= 2^l and
-// m = floor(2^(31+l) / d) + 1, m d = 2^(31+l) + e, 0 < e <= 2^l, so a m / 2^(31+l)
-// is a / d and less than 1 / d more: its integer part is the quotient.
-struct KaDiv {
-  uint32_t d, m, shift;
-  __device__ __forceinline__ int operator()(int a) const { return (int)(((uint64_t)(uint32_t)a * m) >> shift); }
-};
-static KaDiv ka_div(uint32_t d) {
-  uint32_t l = 0;
-  while ((uint64_t(1) << l) < d) ++l;
-  return KaDiv{d, (uint32_t)((uint64_t(1) << (31 + l)) / d + 1), 31 + l};
-}
+// Quotients without integer divisions (FastDiv, and this): code that runs once is
+// met with cold instruction caches, and a division is some 25 instructions.
 // a / b, a < 2^31, from the quotient of floats: a few units off at most, then exact
 __device__ __forceinline__ unsigned ka_quot(unsigned a, unsigned b) {
   unsigned q = (unsigned)__fdividef((float)a, (float)b);
@@ -112,7 +100,7 @@ __device__ __forceinline__ unsigned ka_quot(unsigned a, unsigned b) {
 
 struct KaWork {  // the cut of the tiles into runs
   int row_blocks, np, G;  // G query heads a head
-  KaDiv by_g, by_blocks, by_units, by_ctas;
+  FastDiv by_g, by_blocks, by_units, by_ctas;
   int* done;        // [ctas]: finished parts of the cut unit that begins in a run; zero at rest
   float2* part_ml;  // [2 ctas][np]
   float* part_o;    // [2 ctas][np][D]
@@ -252,7 +240,7 @@ __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSe
 struct KaCut {
   unsigned runs, per, rest;
   KaCut() = default;
-  __device__ __forceinline__ KaCut(unsigned T, const KaDiv& by_ctas) {
+  __device__ __forceinline__ KaCut(unsigned T, const FastDiv& by_ctas) {
     const bool all = T / 2 >= by_ctas.d;
     runs = all ? by_ctas.d : max(T / 2, 1u);
     per = all ? (unsigned)by_ctas((int)T) : min(T, 2u);
@@ -1295,10 +1283,10 @@ cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspac
   wk.row_blocks = k.row_blocks;
   wk.np = k.np;
   wk.G = p.H / p.Hkv;
-  wk.by_g = ka_div((uint32_t)wk.G);
-  wk.by_blocks = ka_div((uint32_t)wk.row_blocks);
-  wk.by_units = ka_div((uint32_t)(p.Hkv * wk.row_blocks));
-  wk.by_ctas = ka_div((uint32_t)k.ctas);
+  wk.by_g = fast_div((uint32_t)wk.G);
+  wk.by_blocks = fast_div((uint32_t)wk.row_blocks);
+  wk.by_units = fast_div((uint32_t)(p.Hkv * wk.row_blocks));
+  wk.by_ctas = fast_div((uint32_t)k.ctas);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   wk.done = reinterpret_cast<int*>(ws);
   wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
