@@ -57,7 +57,7 @@
 // 131 K tokens, one node each (1.02 GB) 158 us, 0.95 of the HBM copy rate, which
 // bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 48 us, 0.61 of
 // it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 201 us, 0.27 of
-// the bf16 rate; one request of 1003 tokens and one node 12.4 us. The chains and
+// the bf16 rate; one request of 1003 tokens and one node 10.8 us. The chains and
 // trees are bound by the softmax warps' latency: a tile takes some 1600 cycles at
 // 48 rows and 1800 at 64 (the products take 460 and 600 of them, the warps issue
 // in 40 to 50 % of the cycles), and a part's start and end some 8000. Measured
@@ -235,15 +235,21 @@ __device__ __forceinline__ bool ka_next(const Kv8AttnParams& p, KaIter& it, KaSe
   return true;
 }
 
-// As many runs of the T tiles as leave two tiles each, one an SM at most; run c
-// of them begins at c per + min(c, rest). (1 <= T < 2^31: the host checks.)
+// As many runs of the T tiles as leave `least` (1 or 2) tiles each, one an SM at
+// most; run c of them begins at c per + min(c, rest). (1 <= T < 2^31: the host
+// checks.)
+// Single tiles where the units have 16 or fewer on average: a tile costs more
+// than the merge of twice the parts (8 units of 3 tiles 8.9 us against 11.0, of
+// 9 tiles 10.8 against 12.4; of 33 tiles, though, 15.3 against 12.4, and one unit
+// of 33 13.9 against 10.8).
 struct KaCut {
   unsigned runs, per, rest;
   KaCut() = default;
-  __device__ __forceinline__ KaCut(unsigned T, const FastDiv& by_ctas) {
-    const bool all = T / 2 >= by_ctas.d;
-    runs = all ? by_ctas.d : max(T / 2, 1u);
-    per = all ? (unsigned)by_ctas((int)T) : min(T, 2u);
+  __device__ __forceinline__ KaCut(unsigned T, unsigned units, const FastDiv& by_ctas) {
+    const unsigned least = (uint64_t)T > (uint64_t)16u * units ? 2u : 1u, most = least == 2u ? T / 2 : T;
+    const bool all = most >= by_ctas.d;
+    runs = all ? by_ctas.d : max(most, 1u);
+    per = all ? (unsigned)by_ctas((int)T) : min(T, least);
     rest = T - per * runs;
   }
   __device__ __forceinline__ unsigned begin(unsigned c) const { return c * per + min(c, rest); }
@@ -505,7 +511,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   }
   unsigned f0, f1;
   {
-    const KaCut runs(T, wk.by_ctas);
+    const KaCut runs(T, (unsigned)(p.B * units), wk.by_ctas);
     f0 = runs.begin(blockIdx.x);
     f1 = blockIdx.x < runs.runs ? runs.begin(blockIdx.x + 1u) : f0;
     if (tid == 0) cut_s = runs;
