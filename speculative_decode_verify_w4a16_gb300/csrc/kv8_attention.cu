@@ -56,14 +56,15 @@
 // Measured (one layer of 64 query heads on 8, e4m3): four requests of 120 to
 // 131 K tokens, one node each (1.02 GB) 158 us, 0.95 of the HBM copy rate, which
 // bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 48 us, 0.61 of
-// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 201 us, 0.27 of
+// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 196 us, 0.27 of
 // the bf16 rate; one request of 1003 tokens and one node 10.8 us. The chains and
 // trees are bound by the softmax warps' latency: a tile takes some 1600 cycles at
 // 48 rows and 1800 at 64 (the products take 460 and 600 of them, the warps issue
 // in 40 to 50 % of the cycles), and a part's start and end some 8000. Measured
 // and not kept, against what there was at the time: 128 rows a block with 32 a
 // warpgroup, the trees in 563 us (registers); 32 rows a warpgroup at 64, no gain
-// (fewer warps to hide latency with); the two terms' products added up in TMEM,
+// (fewer warps to hide latency with), 8 rows at 48, the chains in 55 against 48
+// (64 registers); the two terms' products added up in TMEM,
 // 272 against 240; the next part's query rows prepared by a warp of its own,
 // 273 against 232 (it takes 2500 cycles for four rows; their loads before the
 // part's end: 225); scores given back when read, and fetched a tile ahead where
@@ -261,7 +262,7 @@ struct KaCut {
 };
 
 // Sixteen rows, a value each in every lane: reduced over the warp by halving
-// the rows at each exchange; lanes 2 i and 2 i + 1 return row ka_row(lane).
+// the rows at each exchange; lanes 2 r and 2 r + 1 return row r.
 template <bool MAX>
 __device__ __forceinline__ float ka_reduce16(float (&v)[16], int lane) {
 #pragma unroll
@@ -275,9 +276,6 @@ __device__ __forceinline__ float ka_reduce16(float (&v)[16], int lane) {
   }
   const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
   return MAX ? fmaxf(v[0], got) : v[0] + got;
-}
-__device__ __forceinline__ int ka_row(int lane) {
-  return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
 }
 
 template <int NP>
@@ -964,15 +962,15 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         *reinterpret_cast<uint4*>(q8 + NP * 128) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
         *reinterpret_cast<uint4*>(q16 + (((2 * (c & 3)) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(q16 + (((2 * (c & 3) + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
         if (c == 0) {
           const int R = rb * NP + r, j = wk.by_g(R);
           gm_s[4 * (r >> 1) + (r & 1)] = __uint_as_float((unsigned)(127 - ex) << 23) * p.scale_log2;
           gm_s[4 * (r >> 1) + 2 + (r & 1)] = 0.0f;
           row_s[r] = R < rows ? (sg.b * p.n + j) * p.H + kvh * G + R - j * G : -1;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
         ka_bar(bar);
         if (sg.lo == 0) {
           if (st < Q) {
@@ -1061,7 +1059,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < Q; ++q) x[q] = t[q];
             const float mx = ka_reduce16<true>(x, lane);
-            if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = mx;
+            if (!(lane & 1)) part_s[qd * NP + qa + (lane >> 1)] = mx;
           }
           ka_bar(bar);
           const int r = qa + (lane & 15);  // a lane's row from here on
@@ -1125,7 +1123,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < Q; q += 2) ka_un2(l[q / 2], x[q], x[q + 1]);
         const float y = ka_reduce16<false>(x, lane);
-        if (!(lane & 1)) part_s[qd * NP + qa + ka_row(lane)] = y;
+        if (!(lane & 1)) part_s[qd * NP + qa + (lane >> 1)] = y;
       }
       ka_bar(bar);
       float inv;  // of a lane's row
