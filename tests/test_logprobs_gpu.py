@@ -113,6 +113,17 @@ def test_maxima_far_from_zero(dtype, rows):
     _check(x, ids, 3)
 
 
+@pytest.mark.parametrize("R", [3, 640])
+@pytest.mark.parametrize("V,top", [(257, 5), (300, 64), (1000, 32), (1023, 1), (2000, 20), (8000, 33)])
+def test_short_rows(R, V, top):
+    """Fewer quarters than alternatives, or not many more: other ways to the candidates."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(R, V, generator=g) * 3
+    x[1::3] = torch.randint(-4, 5, x[1::3].shape, generator=g).float()
+    x[2::3, V // 3:] = -torch.inf
+    _check(x, torch.randint(0, V // 3, (R, 1), generator=g, dtype=torch.int32), top)
+
+
 def test_many_rows_with_masks_and_ties():
     g = torch.Generator().manual_seed(8)
     x = torch.randint(-3, 4, (640, 4099), generator=g).float()
