@@ -535,12 +535,21 @@ __device__ void lp_report(const LogprobParams& p, int r, const T* row, const LpR
     n = p.top;
     __syncthreads();
   }
-  if (n > 4 * p.top) {
-    // few quarters and so many candidates: all against all costs n^2, so only
-    // those that reach the `top`-th key (1000 rows of 1000 logits with 32
-    // alternatives: 36 us, 834 with all of them)
-    const unsigned kth = lp_select(p.top, hist, sel, [&](auto f) {
-      for (int i = tid; i < n; i += kLpRowThreads) f(ckey[i]);
+  // few quarters, and so many candidates: all against all costs n^2, so first
+  // only those that reach the `top`-th key, and of many equal to it the first ones
+  // (1000 rows of 1000 logits with 32 alternatives: 36 us, 834 with all of them)
+#pragma unroll 1
+  for (int round = 0; round < 2 && n > 4 * p.top; ++round) {
+    const unsigned kth = round == 0 ? 0u : sel[0];
+    const int ties = (int)sel[1];  // of the `top` largest, those equal to the last
+    __syncthreads();
+    const unsigned least = lp_select(round == 0 ? p.top : ties, hist, sel, [&](auto f) {
+      for (int i = tid; i < n; i += kLpRowThreads) {
+        if (round == 0)
+          f(ckey[i]);
+        else if (ckey[i] == kth)
+          f(~(unsigned)cidx[i]);
+      }
     });
     constexpr int kEach = kLpCand / kLpRowThreads;
     unsigned key[kEach];
@@ -556,7 +565,8 @@ __device__ void lp_report(const LogprobParams& p, int r, const T* row, const LpR
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (tid + j * kLpRowThreads < n && key[j] >= kth) {
+      if (tid + j * kLpRowThreads < n &&
+          (round == 0 ? key[j] >= least : key[j] > kth || ~(unsigned)e[j] >= least)) {
         const int at = atomicAdd(&s_count, 1);
         ckey[at] = key[j];
         cidx[at] = e[j];
