@@ -30,7 +30,9 @@
 // (fp16 holds 2^15.99; weights down to 2^-14 keep all 11 bits, that is 2^-21
 // of the largest). One vote per tile over the four warps finds that; the
 // maximum itself, and the rescaling of O^T in TMEM, are computed only then (at
-// the first tile of a part, and seldom after it).
+// the first tile of a part, and seldom after it). Blocks of zeros have scale 1,
+// whatever their neighbours have: they, and pages that are not there, count as
+// 2^-64, so that they do not raise m.
 //
 // Code that runs once per part (the query rows, the first maximum, the end) is
 // kept short: a CTA meets it with cold instruction caches, and straight-line
@@ -39,13 +41,18 @@
 // all warps take part and no registers have to be kept (both together: the
 // trees 225 -> 201 us, one request of one node 14.0 -> 12.6).
 //
-// The last tile of bf16 rows, the tail page's (rows 0 .. 63 of the tile) and
-// the tree's own (64 .. 127), comes first in a request's tiles, with bf16
-// operands (kind::f16) and the mask: tail row r for r < lens % 64, node j for
-// the rows of j and its descendants. Rows that hold nothing are zeroed in
-// shared memory, and so are values that are not finite in a node (a node does
-// not see its siblings, and 0 * NaN is NaN); they are added at the end to the
-// rows that do see the node.
+// The tile of bf16 rows, the tail page's (rows 0 .. 63 of the tile) and the
+// tree's own (64 .. 127), comes last in a request's tiles, with bf16 operands
+// (kind::f16) and the mask: tail row r for r < lens % 64, node j for the rows of
+// j and its descendants. Last, because m is then what the 8-bit tiles' weights
+// need, in fp16 and in units of their own value scales; the bf16 weights and the
+// fp32 sums have range for any such m (raised only past 2^64). With that tile
+// first, m came from it, and of small values the cached ones' weights were lost
+// (what the order costs: the trees 197 -> 199 us, 3 requests with trees of 17
+// nodes 15.4 -> 16.6, the others nothing).
+// Rows that hold nothing are zeroed in shared memory, and so are values that are
+// not finite in a node (a node does not see its siblings, and 0 * NaN is NaN);
+// they are added at the end to the rows that do see the node.
 //
 // Work: every (request, KV head, row block) unit has 1 + ceil(full blocks / 2)
 // tiles. The tiles of all units are laid end to end and cut into one run per
@@ -56,8 +63,8 @@
 // Measured (one layer of 64 query heads on 8, e4m3): four requests of 120 to
 // 131 K tokens, one node each (1.02 GB) 158 us, 0.95 of the HBM copy rate, which
 // bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 48 us, 0.61 of
-// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 196 us, 0.27 of
-// the bf16 rate; one request of 1003 tokens and one node 10.8 us. The chains and
+// it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 199 us, 0.27 of
+// the bf16 rate; one request of 1003 tokens and one node 10.7 us. The chains and
 // trees are bound by the softmax warps' latency: a tile takes some 1600 cycles at
 // 48 rows and 1800 at 64 (the products take 460 and 600 of them, the warps issue
 // in 40 to 50 % of the cycles), and a part's start and end some 8000. Measured
@@ -85,6 +92,7 @@ constexpr int kKaD = 128;
 constexpr int kKaTile = 128;      // keys per tile
 constexpr float kKaRoom = 7.0f;    // log2 of the largest weight when m is set
 constexpr float kKaLimit = 15.0f;  // ... and where m is raised
+constexpr float kKaLimit16 = 64.0f;  // ... and by the bf16 tile
 
 // Quotients without integer divisions (FastDiv, and this): code that runs once is
 // met with cold instruction caches, and a division is some 25 instructions.
@@ -201,6 +209,31 @@ __device__ __forceinline__ bool ka_wait(uint64_t* bar, uint32_t parity, unsigned
   return still;
 }
 
+// By a whole warp: whether the lane's block of codes (8 KB at v) holds zeros
+// alone, for the lanes that ask. One load tells for nearly every block.
+__device__ __noinline__ bool ka_zero_block(const uint8_t* v, bool ask) {
+  constexpr uint32_t kMag = 0x7F7F7F7Fu;  // (a zero may have a sign)
+  const int lane = threadIdx.x & 31;
+  bool zero = false;
+  if (ask) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(v));
+    zero = ((x.x | x.y | x.z | x.w) & kMag) == 0u;
+  }
+#pragma unroll 1
+  for (unsigned left = __ballot_sync(0xffffffffu, zero); left; left &= left - 1) {
+    const int of = __ffs((int)left) - 1;
+    const uint4* at = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, (unsigned long long)v, of)) + lane;
+    uint32_t any = 0u;
+#pragma unroll 4
+    for (int i = 0; i < 64 * kKaD / 512; ++i) {
+      const uint4 x = __ldg(at + 32 * i);
+      any |= x.x | x.y | x.z | x.w;
+    }
+    if (__any_sync(0xffffffffu, (any & kMag) != 0u) && lane == of) zero = false;
+  }
+  return zero;
+}
+
 __device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
   const int l = p.lens[b];
   return l < 0 ? 0 : l > p.max_len ? p.max_len : l;
@@ -208,10 +241,13 @@ __device__ __forceinline__ int ka_len(const Kv8AttnParams& p, int b) {
 __device__ __forceinline__ int ka_tiles(int len) { return 1 + (len / 64 + 1) / 2; }
 
 // One part of a run: tiles lo .. hi - 1 of the nt tiles of unit u of request
-// b; tile lo is tile at of all
+// b; tile lo is tile at of all. Tile i holds blocks 2 i and 2 i + 1, the last
+// one the bf16 rows.
 struct KaSeg {
   int b, u, lo, hi, nt, len;
   unsigned at;
+  __device__ __forceinline__ bool ends() const { return hi == nt; }       // holds the bf16 tile
+  __device__ __forceinline__ bool bf16(int i) const { return i + 1 == nt; }
 };
 struct KaIter {
   unsigned at, left;
@@ -299,7 +335,8 @@ struct KaCfg {
   static constexpr int kPartOff = kGmOff + NP * 8;            // float [4][NP]
   static constexpr int kRowOff = kPartOff + NP * 16;          // int [NP]
   static constexpr int kScaleOff = kRowOff + NP * 4;          // float4 [16][2]: a tile's blocks
-  static constexpr int kBarOff = kScaleOff + 16 * 2 * 16;
+  static constexpr int kSeeOff = kScaleOff + 16 * 2 * 16;     // u16 [groups][128]
+  static constexpr int kBarOff = kSeeOff + kGroups * 256;
   static constexpr int kNumBars = 2 * kStages + 2 * kVStages + 12;
   static constexpr int kTotal = kBarOff + kNumBars * 8 + 1024;
   // TMEM columns: scores (two terms) of two tiles, O^T, then V^T of two tiles
@@ -444,6 +481,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
   uint64_t* x_full = q_ready + 1;  // a bf16 tile's values
   uint64_t* mma_fin = x_full + 1;  // [2]
   float4* scale_s = reinterpret_cast<float4*>(smem + C::kScaleOff);  // tile tc, block half: 2 (tc % 16) + half
+  uint16_t* see_s = reinterpret_cast<uint16_t*>(smem + C::kSeeOff);
   __shared__ uint32_t tmem_s;
   __shared__ unsigned scan_s[32];
   __shared__ unsigned s_pre;
@@ -572,20 +610,87 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     };
     while (ok && ka_next(p, it, sg)) {
       const int kvh = wk.by_blocks(sg.u);
-      // 8-bit tiles: tile i holds blocks 2 (i - 1), 2 (i - 1) + 1. Lane 2 k + h
-      // has block h of the k-th of 16 tiles, its page and scales; the next 16
-      // tiles' are asked for ahead.
-      const int full = sg.len / 64, i0 = max(sg.lo, 1);
+      // 8-bit tiles: lane 2 k + h has block h of the k-th of 16 tiles, its page and
+      // scales; the next 16 tiles' are asked for ahead.
+      const int full = sg.len / 64, end8 = min(sg.hi, sg.nt - 1);
       const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
       auto page_of = [&](int i) {  // of the 16 tiles from i on; -2: no such block
-        const int blk = 2 * (i - 1) + lane;
-        return blk < full && blk < 2 * (sg.hi - 1) ? tab[blk] : -2;
+        const int blk = 2 * i + lane;
+        return blk < full && blk < 2 * end8 ? tab[blk] : -2;
       };
-      int page_n = page_of(i0);  // (asked for before the bf16 tile: its latency then passes beside that)
-      if (sg.lo == 0) {
-        const int t = sg.len & 63, tail = lane == 0 ? p.tails[sg.b] : 0;
+      int page_n = page_of(sg.lo), page = -2;
+      float sk = 0.0f, lsv = 0.0f, isv = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
+      auto scales_of = [&]() {  // of the pages asked for earlier
+        sk_n = 0.0f;
+        sv_n = 1.0f;
+        if (page_n >= 0 && page_n < p.pages) {
+          sk_n = p.k_scale[(int64_t)page_n * p.Hkv + kvh];
+          sv_n = p.v_scale[(int64_t)page_n * p.Hkv + kvh];
+        } else if (page_n != -2) {
+          report_error(p.err, kErrInput);
+          page_n = -1;
+        }
+      };
+      scales_of();
+#pragma unroll 1
+      for (int i = sg.lo; ok && i < end8; ++i, ++tc) {
+        const int k = (i - sg.lo) & 15;
+        if (k == 0) {
+          page = page_n;
+          page_n = page_of(i + 16);
+        } else if (k == 8) {
+          scales_of();
+        }
+        const int pa = __shfl_sync(0xffffffffu, page, 2 * k), pb = __shfl_sync(0xffffffffu, page, 2 * k + 1);
+        // a page that is not there: past the tensor's end, filled with zeros
+        const int none = p.pages * p.Hkv, ks = kc % S, vs = vc % SV;
+        const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
+        if (lane == 0) {
+          ok = k_wait(kc);
+          if (ok) {
+            uint8_t* kd = smem + C::kKOff + ks * C::kTileBytes;
+            mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+            tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
+            tma_load_3d(kd + 8192, &maps.k, 0, 0, zb, &k_full[ks]);
+          }
+        }
+        // key scale, log2 of the value scale, its inverse, 1 for no block
+        if (k == 0) {
+          sk = sk_n;
+          const bool one = page >= 0 && sv_n == 1.0f;  // perhaps a block of zeros
+          bool nothing = page == -1;
+          if (__any_sync(0xffffffffu, one))
+            nothing |= ka_zero_block(p.v + ((int64_t)(one ? page : 0) * p.Hkv + kvh) * (64 * kKaD), one);
+          lsv = nothing ? -64.0f : log2f(sv_n);
+          isv = nothing ? 18446744073709551616.0f : 1.0f / sv_n;
+        }
+        if ((lane >> 1) == k) scale_s[2 * (tc & 15) + (lane & 1)] = make_float4(sk, lsv, isv, page == -2 ? 1.0f : 0.0f);
+        __syncwarp();
+        if (lane == 0) {
+          if (ok) {
+            mbar_arrive(&k_full[ks]);
+            k_more = 1;
+            if (vc >= SV) ok = ka_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
+          }
+          if (ok) {
+            uint8_t* vd = smem + C::kVOff + vs * C::kTileBytes;
+            mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+            tma_load_3d(vd, &maps.v, 0, 0, za, &v_full[vs]);
+            tma_load_3d(vd + 8192, &maps.v, 0, 0, zb, &v_full[vs]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (ok) {
+          ++kc;
+          ++vc;
+          k_more = 0;
+        }
+      }
+      if (ok && sg.ends()) {
+        const int t = sg.len & 63;
         const bool pass = kc % S == S - 1;
         if (lane == 0) {
+          const int tail = p.tails[sg.b];
           if (pass && (ok = k_wait(kc))) {
             mbar_arrive(&k_full[S - 1]);
             mbar_arrive(&k_full[S - 1]);
@@ -610,70 +715,6 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         if (ok) kc += pass ? 3 : 2;
         ++tc;
-      }
-      int page = -2;
-      float sk = 0.0f, lsv = 0.0f, isv = 1.0f, sk_n = 0.0f, sv_n = 1.0f;
-      auto scales_of = [&]() {  // of the pages asked for earlier
-        sk_n = 0.0f;
-        sv_n = 1.0f;
-        if (page_n >= 0 && page_n < p.pages) {
-          sk_n = p.k_scale[(int64_t)page_n * p.Hkv + kvh];
-          sv_n = p.v_scale[(int64_t)page_n * p.Hkv + kvh];
-        } else if (page_n != -2) {
-          report_error(p.err, kErrInput);
-          page_n = -1;
-        }
-      };
-      scales_of();
-#pragma unroll 1
-      for (int i = i0; ok && i < sg.hi; ++i, ++tc) {
-        const int k = (i - i0) & 15;
-        if (k == 0) {
-          page = page_n;
-          page_n = page_of(i + 16);
-        } else if (k == 8) {
-          scales_of();
-        }
-        const int pa = __shfl_sync(0xffffffffu, page, 2 * k), pb = __shfl_sync(0xffffffffu, page, 2 * k + 1);
-        // a page that is not there: past the tensor's end, filled with zeros
-        const int none = p.pages * p.Hkv, ks = kc % S, vs = vc % SV;
-        const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
-        if (lane == 0) {
-          ok = k_wait(kc);
-          if (ok) {
-            uint8_t* kd = smem + C::kKOff + ks * C::kTileBytes;
-            mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
-            tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
-            tma_load_3d(kd + 8192, &maps.k, 0, 0, zb, &k_full[ks]);
-          }
-        }
-        // key scale, log2 of the value scale, its inverse, 1 for no block
-        if (k == 0) {
-          sk = sk_n;
-          lsv = log2f(sv_n);
-          isv = 1.0f / sv_n;
-        }
-        if ((lane >> 1) == k) scale_s[2 * (tc & 15) + (lane & 1)] = make_float4(sk, lsv, isv, page == -2 ? 1.0f : 0.0f);
-        __syncwarp();
-        if (lane == 0) {
-          if (ok) {
-            mbar_arrive(&k_full[ks]);
-            k_more = 1;
-            if (vc >= SV) ok = ka_wait(&v_free[vs], (uint32_t)(vc / SV - 1) & 1u, p.err);
-          }
-          if (ok) {
-            uint8_t* vd = smem + C::kVOff + vs * C::kTileBytes;
-            mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
-            tma_load_3d(vd, &maps.v, 0, 0, za, &v_full[vs]);
-            tma_load_3d(vd + 8192, &maps.v, 0, 0, zb, &v_full[vs]);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        if (ok) {
-          ++kc;
-          ++vc;
-          k_more = 0;
-        }
       }
     }
     // every copy has landed before the CTA exits (it has, unless a wait ran
@@ -701,12 +742,13 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         // or a bf16 tile's from shared memory: 128-byte rows of 64 columns a
         // key, the other 64 columns a half on
         const uint32_t bp = pb + (uint32_t)(w * C::kPBytes);
-        if (i == 0) {
-#pragma unroll
+        if (sg.bf16(i)) {
+#pragma unroll 1
           for (int k = 0; k < 8; ++k)
             umma_bf16_ss_warp(tmem + C::kOCol,
                               umma_desc_sw128_mnmajor(xb + 2048u * (uint32_t)k, (uint32_t)C::kTileBytes, 1024u),
-                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o16, k > 0 ? 1u : 0u);
+                              umma_desc_flat_mnmajor(bp + 256u * (uint32_t)k, 128u, 2048u), id_o16,
+                              (i > sg.lo || k > 0) ? 1u : 0u);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -736,19 +778,19 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       for (int i = sg.lo; ok && i < sg.hi; ++i, ++tc) {
         const uint32_t d = tmem + (uint32_t)(tc & 1) * 2u * NP;
         if (tc >= 2) ok = ka_wait(&pv_done[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err);
-        if (i == 0 && kc % S == S - 1) {  // the stage that the producer passed over
+        if (sg.bf16(i) && kc % S == S - 1) {  // the stage that the producer passed over
           ok = ka_wait(&k_full[S - 1], (uint32_t)(kc / S) & 1u, p.err, ok);
           umma_commit_warp(&k_free[S - 1]);
           ++kc;
         }
         const int s = kc % S;
         ok = ka_wait(&k_full[s], (uint32_t)(kc / S) & 1u, p.err, ok);
-        if (i == 0) ok = ka_wait(&k_full[s + 1], (uint32_t)((kc + 1) / S) & 1u, p.err, ok);
+        if (sg.bf16(i)) ok = ka_wait(&k_full[s + 1], (uint32_t)((kc + 1) / S) & 1u, p.err, ok);
         issued = 1;
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = kb + (uint32_t)s * C::kTileBytes;
-        if (i == 0) {
+        if (sg.bf16(i)) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             umma_bf16_ss_warp(d, umma_desc_sw128_kmajor(a + (uint32_t)((k >> 2) * C::kTileBytes + 32 * (k & 3))),
@@ -783,26 +825,35 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
     int vc = 0, tc = 0, xc = 0, seg = 0, last = -2;  // last: the latest bf16 tile
     bool ok = true;
     while (ka_next(p, it, sg)) {
+      // The bf16 tile's values: fetched and made ready at the part's start, while
+      // the softmax warps are at the last part's end and at this one's query rows,
+      // once P V of the last such tile has left their buffer (and so all four warps
+      // are past it)
+      bool to_do = sg.ends();
+      const int t = sg.len & 63, tail = p.tails[sg.b];
+      const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
+      if (to_do) {
+        if (last >= 0 && last >= tc - 2) ok = ka_wait(&pv_done[last & 1], (uint32_t)(last >> 1) & 1u, p.err, ok);
+        last = tc + sg.hi - sg.lo - 1;
+        if (ct == 0) bad_s[seg & 3] = 0ull;
+        if (ct == 0 && ok) {
+          const int kvh = wk.by_blocks(sg.u);
+          uint8_t* w = smem + C::kXOff;
+          mbar_arrive_expect_tx(x_full, (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
+          for (int h = 0; h < 2; ++h) {
+            if (tok) tma_load_3d(w + h * C::kTileBytes, &maps.v_tail, 64 * h, 0, tail * p.Hkv + kvh, x_full);
+            tma_load_4d(w + h * C::kTileBytes + 8192, &maps.v_new, 64 * h, kvh, 0, sg.b, x_full);
+          }
+        }
+        __syncwarp();
+      }
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
         // P V (tc - 2) has left the TMEM buffer
         if (tc >= 2) ok = ka_wait(&pv_done[tc & 1], (uint32_t)((tc - 2) >> 1) & 1u, p.err, ok);
-        if (i == 0) {
-          const int t = sg.len & 63, tail = p.tails[sg.b];
-          const bool tok = t > 0 && tail >= 0 && tail < p.tail_pages;
+        if (to_do) {
+          to_do = false;
           uint8_t* w = smem + C::kXOff;
-          if (last == tc - 1) ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
-          last = tc;
-          if (ct == 0) bad_s[seg & 3] = 0ull;
           asm volatile("barrier.cta.sync 8, 128;" ::: "memory");  // (ids 1 .. 4 and 9: the softmax)
-          if (ct == 0 && ok) {  // (all four warps are past the last such tile)
-            const int kvh = wk.by_blocks(sg.u);
-            mbar_arrive_expect_tx(x_full, (uint32_t)((tok ? 64 : 0) + p.n) * 256u);
-            for (int h = 0; h < 2; ++h) {
-              if (tok) tma_load_3d(w + h * C::kTileBytes, &maps.v_tail, 64 * h, 0, tail * p.Hkv + kvh, x_full);
-              tma_load_4d(w + h * C::kTileBytes + 8192, &maps.v_new, 64 * h, kvh, 0, sg.b, x_full);
-            }
-          }
-          __syncwarp();
           ok = ka_wait(x_full, (uint32_t)xc & 1u, p.err, ok);
           ++xc;
           // thread = row of the tile: its 256 bytes, both halves
@@ -837,7 +888,8 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           }
           if (bad) atomicOr(&bad_s[seg & 3], 1ull << (ct - 64));
           fence_proxy_async_smem();
-        } else {
+        }
+        if (!sg.bf16(i)) {
           const int s = vc % SV;
           ok = ka_wait(&v_full[s], (uint32_t)(vc / SV) & 1u, p.err, ok);
           ++vc;
@@ -914,7 +966,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       const int kvh = wk.by_blocks(sg.u), rb = sg.u - kvh * wk.row_blocks;
       // ---- Q: x = q 2^ex, |x| < 256, as bf16 and as two e4m3 terms
       {
-        if (sg.lo == 0 && p.parents && st < p.n) {
+        if (sg.ends() && p.parents && st < p.n) {
           // the parents (bad ones reported and cut off), for the masks; every
           // warpgroup writes the same
           int up = p.parents[(int64_t)sg.b * p.n + st];
@@ -972,7 +1024,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready);
         ka_bar(bar);
-        if (sg.lo == 0) {
+        if (sg.ends()) {
           if (st < Q) {
             const int R = rb * NP + qa + st, j = wk.by_g(R);
             uint64_t mk = 0;
@@ -987,6 +1039,18 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           }
           ka_bar(bar);
         }
+      }
+      if (sg.ends()) {
+        uint32_t see = 0xFFFFu;
+        if (key < 64) {
+          const int tail = p.tails[sg.b];
+          if (key >= (sg.len & 63) || tail < 0 || tail >= p.tail_pages) see = 0u;
+        } else {
+          see = 0u;
+#pragma unroll 1
+          for (int q = 0; q < Q; ++q) see |= (uint32_t)((mask_s[qa + q] >> (key - 64)) & 1ull) << q;
+        }
+        see_s[wg * 128 + key] = (uint16_t)see;
       }
       // the next part's query rows on their way to L2
       const __nv_bfloat16* q_next = nullptr;
@@ -1003,18 +1067,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
 #pragma unroll 1
       for (int i = sg.lo; i < sg.hi; ++i, ++tc) {
         const int buf = tc & 1;
-        const bool bf = i == 0;
-        uint32_t see = 0xFFFFu;  // rows for which the thread's key counts
-        if (bf) {
-          if (key < 64) {
-            const int tail = p.tails[sg.b];
-            if (key >= (sg.len & 63) || tail < 0 || tail >= p.tail_pages) see = 0u;
-          } else {
-            see = 0u;
-#pragma unroll 1
-            for (int q = 0; q < Q; ++q) see |= (uint32_t)((mask_s[qa + q] >> (key - 64)) & 1ull) << q;
-          }
-        }
+        const bool bf = sg.bf16(i);
         ok = ka_wait(&s_full[buf], (uint32_t)(tc >> 1) & 1u, p.err, ok);
         tc_fence_after();
         // ---- t = s + log2 sv - m, two rows an instruction
@@ -1041,17 +1094,19 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           for (int q = 0; q < Q; ++q) t[q] = -INFINITY;
         }
         if (bf) {
+          const uint32_t see = see_s[wg * 128 + key];
 #pragma unroll
           for (int q = 0; q < Q; ++q)
             if (!((see >> q) & 1u)) t[q] = -INFINITY;
         }
         // ---- is m to be set, or does a weight pass the limit?
+        const float limit = bf ? kKaLimit16 : kKaLimit;
         bool raise = i == sg.lo;
         if (!raise) {
           float over = -INFINITY;
 #pragma unroll
           for (int q = 0; q < Q; q += 2) over = ka_max3(over, t[q], t[q + 1]);
-          raise = ka_bar_any(bar, over > kKaLimit);
+          raise = ka_bar_any(bar, over > limit);
         }
         if (raise) {
           {
@@ -1065,7 +1120,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
           const int r = qa + (lane & 15);  // a lane's row from here on
           const float mx = fmaxf(fmaxf(part_s[r], part_s[NP + r]), fmaxf(part_s[2 * NP + r], part_s[3 * NP + r]));
           float d = 0.0f;
-          if (i == sg.lo ? mx > -INFINITY : mx > kKaLimit) d = mx - kKaRoom;
+          if (i == sg.lo ? mx > -INFINITY : mx > limit) d = mx - kKaRoom;
           const float f = ka_ex2(-d);
           if (qd == 0 && lane < 16) gm_s[4 * (r >> 1) + 2 + (r & 1)] -= d;
 #pragma unroll
@@ -1138,7 +1193,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       }
       ok = ka_wait(&pv_done[(tc - 1) & 1], (uint32_t)((tc - 1) >> 1) & 1u, p.err, ok);
       tc_fence_after();
-      const unsigned long long bad = sg.lo == 0 ? bad_s[seg & 3] : 0ull;
+      const unsigned long long bad = sg.ends() ? bad_s[seg & 3] : 0ull;
       if (bad) ka_add_bad<Q>(p, sg.b, kvh, bad, mask_s + qa, trow + C::kOCol + (uint32_t)qa, key);
       // whole: the rows as bf16 through the warpgroup's chunk of a P buffer (no
       // MMA reads it any more), 256 bytes each, and out 16 bytes a thread
