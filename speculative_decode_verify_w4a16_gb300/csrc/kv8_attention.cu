@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
       const int32_t* tab = p.table + (int64_t)sg.b * p.max_blocks;
       auto page_of = [&](int i) {  // of the 16 tiles from i on; -2: no such block
         const int blk = 2 * i + lane;
-        return blk < full && blk < 2 * end8 ? tab[blk] : -2;
+        return blk < full && blk < 2 * end8 ? max(tab[blk], -1) : -2;  // (any negative entry is a bad page)
       };
       int page_n = page_of(sg.lo), page = -2;
       float sk = 0.0f, lsv = 0.0f, isv = 1.0f, sk_n = 0.0f, sv_n = 1.0f;

@@ -1,0 +1,48 @@
+"""Edges of the paged 8-bit cache operators."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_reference as ref
+import speculative_decode_verify_w4a16_gb300 as sv
+from helpers import dev
+from test_kv8_gpu import E4M3, _attn_inputs, _history, _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decode_verify_w4a16_gb300 import build
+    build.build()
+
+
+def test_a_negative_table_entry_is_a_bad_page():
+    """Whatever its value: it is reported and reads as zeros."""
+    rng = np.random.default_rng(1)
+    B, n, H, Hkv, D = 3, 3, 8, 2, 128
+    cache = ref.Cache([_history(rng, Hkv, L) for L in (130, 300, 70)], E4M3, rng, 320)
+    c, table, lens, tails = cache.to(sv, dev())
+    qkv, cols = _attn_inputs(rng, B, n, H, Hkv)
+    dq = [qkv.to(dev())[:, :, s].unflatten(2, (-1, D)) for s in cols]
+
+    def run(value=None):
+        t = table.clone()
+        if value is not None:
+            t[1, 2] = value
+        out = sv.kv8_tree_attention(*dq, c, 0, t, lens, tails, max_len=320)
+        torch.cuda.synchronize()
+        return out.cpu(), sv.check_device_status()
+
+    good, status = run()
+    assert status == 0
+    zeros = cache.values[1]
+    for x in zeros:
+        x[:, 128:192] = 0.0
+    q, k, v = (qkv[:, :, s].unflatten(2, (-1, D)) for s in cols)
+    want, mag = ref.attention(zeros, q[1], k[1], v[1], ref.chain(n))
+    for value in (-1, -2, -3, -(2 ** 31)):
+        out, status = run(value)
+        assert status == 5 and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]), value
+        # test_kv8_gpu's bound
+        assert ((out[1].double() - want).abs() <= 1.05 * 2.0 ** -8 * (mag + want.abs()) + 1e-6).all(), value
