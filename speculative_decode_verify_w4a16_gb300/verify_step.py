@@ -27,6 +27,7 @@ from typing import List
 import torch
 
 from . import api
+from ._lib import check
 
 D = 128
 MAX_ROWS = 80  # of one linear
@@ -127,7 +128,8 @@ def verify_step(target: Target, cache: api.KV8Cache, state: Requests, last: torc
 def decode(target: Target, prompts: List[List[int]], steps: int, K: int, draft_of) -> List[list]:
     """Greedy decoding with drafts: draft_of(b, tokens, K) gives K token ids to
     try after request b's tokens (a drafter's place). Returns each request's
-    (token, log probability) pairs."""
+    (token, log probability) pairs; raises W4A16Error for whatever the kernels
+    reported in the device error word."""
     B = len(prompts)
     if not B or not all(prompts):
         raise ValueError("decode needs prompts of at least one token")
@@ -163,7 +165,7 @@ def decode(target: Target, prompts: List[List[int]], steps: int, K: int, draft_o
             new = [(t, lp) for t, lp in zip(ids, lps) if t >= 0]
             out[b] += new
             tokens[b] += [t for t, _ in new]
-    api.check_device_status()
+    check(api.check_device_status(), "decode")
     return out
 
 
