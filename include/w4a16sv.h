@@ -475,6 +475,11 @@ w4a16_status token_logprobs(const void* logits, int bf16, const int32_t* ids, in
  * ---------------------------------------------------------------------- */
 w4a16_status w4a16_check_device_status(void* stream);
 
+/* The id of the graph capture that `stream` is in, 0 if it is in none: a
+ * workspace that is zeroed in a capture is that capture's own, since it is the
+ * graph that zeroes it. */
+unsigned long long w4a16_stream_capture_id(void* stream);
+
 /* ------------------------------------------------------------------------
  * Host-side planning helpers (no GPU needed; exported so tests can check
  * the work split of the linear).

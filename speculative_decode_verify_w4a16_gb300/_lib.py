@@ -41,6 +41,7 @@ SIGNATURES = {
     "spec_accept_workspace_bytes": (_sz, [_i32, _i32, _i32]),
     "spec_accept": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
     "w4a16_check_device_status": (_i32, [_vp]),
+    "w4a16_stream_capture_id": (ctypes.c_ulonglong, [_vp]),
     "w4a16_item_rounds": (ctypes.c_int, [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
     "w4a16_item_begin": (_i64, [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     "w4a16_item_owner": (_i64, [_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64]),

@@ -4,6 +4,7 @@ CUDA stream; every step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from functools import lru_cache
 from typing import Optional
@@ -51,7 +52,9 @@ _ws_cache: dict = {}
 
 def workspace(nbytes: int, device: Optional[torch.device] = None, key: str = "default") -> torch.Tensor:
     """A zero-filled scratch buffer of at least nbytes on `device`, cached per
-    (device, key). The kernels leave it zeroed after every call."""
+    (device, key). The kernels leave it zeroed after every call. The linears,
+    the accept step and tree_attention take theirs from here by default: calls
+    that may overlap, on several streams, need a `ws` each."""
     index = None if device is None else (device if isinstance(device, torch.device) else torch.device(device)).index
     k = (_device() if index is None else index, key)
     buf = _ws_cache.get(k)
@@ -59,6 +62,27 @@ def workspace(nbytes: int, device: Optional[torch.device] = None, key: str = "de
         dev = torch.device("cuda", k[0])
         buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
         _ws_cache[k] = buf
+    return buf
+
+
+_stream_ws: dict = {}
+
+
+def _stream_workspace(nbytes: int, key: str, stream=None) -> torch.Tensor:
+    """The default workspace of a call on `stream` (default: the current one):
+    zero-filled on that stream, and kept for it, so that calls on several
+    streams share nothing. Within a graph capture it is the capture's own,
+    zeroed by the graph: a captured graph holds no address of a buffer that a
+    later call might replace, and an eager call none that only a graph zeroes."""
+    raw = _stream(stream)
+    capture = lib().w4a16_stream_capture_id(raw)
+    k = (_device(), raw, key, capture != 0)
+    kept = _stream_ws.get(k)
+    if kept is not None and kept[0] == capture and kept[1].numel() >= nbytes:
+        return kept[1]
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", k[0]))
+    _stream_ws[k] = (capture, buf)
     return buf
 
 
@@ -550,7 +574,9 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     [B, n, H, D] and the tree's own k_new, v_new bf16 [B, n, Hkv, D] may be
     slices of one fused projection (heads dense, tokens evenly apart); lens,
     tails int32 [B]; block_table int32 [B, max_blocks]; max_len: an upper bound
-    of lens (default: what the table holds). Returns bf16 [B, n, H, D]."""
+    of lens (default: what the table holds); ws: zeroed before its first use, and
+    used by no two calls at once (default: one for each stream and capture).
+    Returns bf16 [B, n, H, D]."""
     dev, i32 = _device(), torch.int32
     layers, pages, tail_pages, Hkv, D = _need_cache(cache, dev)
     if not 0 <= layer < layers:
@@ -584,8 +610,7 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     else:
         _need(out, "out", torch.bfloat16, (B, n, H, D))
     if ws is None:
-        ws = workspace(_attention_ws(dev, B, n, H, Hkv, D, max_len), q.device,
-                       "kv8_attention")  # apart from those that need no zeros
+        ws = _stream_workspace(_attention_ws(dev, B, n, H, Hkv, D, max_len), "kv8_attention", stream)
     codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
     tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
     check(lib().kv8_tree_attention(
@@ -616,7 +641,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top: int = 0, ws: Op
                    stream=None) -> TokenLogprobs:
     """Log probabilities of given tokens under logit rows (fp32 or bf16 [R, V];
     ids int32 [R, m] or [R], -1 for none), each row's entropy, and its `top`
-    most probable tokens (ties to the lower index)."""
+    most probable tokens (ties to the lower index). ws: used by no two calls at
+    once (default: one for each stream and capture)."""
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"logits must be {torch.float32} or {torch.bfloat16}, got {logits.dtype}")
     _need(logits, "logits", logits.dtype)
@@ -632,7 +658,7 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top: int = 0, ws: Op
                         torch.empty((R, top), dtype=torch.int32, device=dev),
                         torch.empty((R, top), dtype=f32, device=dev))
     if ws is None:
-        ws = workspace(_logprobs_ws(R, V, top), dev, "logprobs")
+        ws = _stream_workspace(_logprobs_ws(R, V, top), "logprobs", stream)
     check(lib().token_logprobs(logits.data_ptr(), int(logits.dtype is torch.bfloat16), ids.data_ptr(), R, V, m, top,
                                out.logp.data_ptr(), out.entropy.data_ptr(), out.top_ids.data_ptr(),
                                out.top_logp.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),

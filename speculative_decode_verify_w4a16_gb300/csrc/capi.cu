@@ -492,6 +492,16 @@ w4a16_status token_logprobs(const void* logits, int bf16, const int32_t* ids, in
              : W4A16_ERR_CUDA;
 }
 
+unsigned long long w4a16_stream_capture_id(void* stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream while another one captures: not in a capture itself)
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusNone ? 0 : id;
+}
+
 w4a16_status w4a16_check_device_status(void* stream) {
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
