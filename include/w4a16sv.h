@@ -400,7 +400,7 @@ w4a16_status kv_block_plan(const int32_t* lens, const int32_t* tails, const int3
  * page in bf16.
  *   k_new, v_new  device bf16 [layers][rows][Hkv][D]: `row_stride` elements
  *                 from row to row and `layer_stride` from layer to layer
- *                 (multiples of 8), heads D apart; 16-byte aligned
+ *                 (multiples of 8), heads D apart; 16-byte aligned; rows >= 1
  *   tails         the tail pages before the step (kv_block_plan's input);
  *                 new_tails, new_start, src_rows, slots: kv_block_plan's outputs
  * Slots or rows that fit no such plan, or ids outside the cache, set

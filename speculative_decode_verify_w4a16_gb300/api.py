@@ -442,6 +442,8 @@ def _need_rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
             raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     outer, tokens, H, D = shape
+    if tokens == 0:
+        return H * D
     so, stride, sh, sd = t.stride()
     if tokens == 1:
         stride = so if outer > 1 else H * D
@@ -524,7 +526,7 @@ def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails:
                stream=None) -> None:
     """The step's kept rows into the cache, every layer at once. k_new, v_new
     bf16 [layers, rows, Hkv, D] (rows evenly apart, heads dense; [rows, Hkv, D]
-    for one layer); tails: the tail pages before the step."""
+    for one layer; no rows: nothing to do); tails: the tail pages before the step."""
     dev, i32 = _device(), torch.int32
     layers, pages, tail_pages, Hkv, D = _need_cache(cache, dev)
     if k_new.dim() == 3:
@@ -543,6 +545,8 @@ def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails:
         _need(plan.new_tails, "plan.new_tails", i32, (B,))
         _need(plan.new_start, "plan.new_start", i32, (B + 1,))
     _need_plan_rows(plan, rows, dev)
+    if rows == 0:  # a step that keeps nothing, as kv_block_plan has it
+        return
     check(lib().kv8_append(k_new.data_ptr(), v_new.data_ptr(), stride, layer_stride, tails.data_ptr(),
                            plan.new_tails.data_ptr(), plan.new_start.data_ptr(), plan.src_rows.data_ptr(),
                            plan.slots.data_ptr(), B, rows, Hkv, D, layers, pages, tail_pages,

@@ -46,3 +46,30 @@ def test_a_negative_table_entry_is_a_bad_page():
         assert status == 5 and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2]), value
         # test_kv8_gpu's bound
         assert ((out[1].double() - want).abs() <= 1.05 * 2.0 ** -8 * (mag + want.abs()) + 1e-6).all(), value
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_a_step_of_no_rows(layers):
+    """The plan allows it (all requests ended, or none brought a row); the append
+    has nothing to do, and refuses what it always refuses."""
+    B, Hkv, D = 3, 2, 128
+    cache = sv.kv8_cache(layers, 4, B, Hkv, device=dev())
+    tails = _i32(2 * np.arange(B))
+    plan = sv.kv_block_plan(_i32([5, 64, 0]), tails, _i32([[-1], [0], [-1]]), _i32([1, 2, 3, 0]), _i32([0, 3, 0]),
+                            row_start=_i32(np.zeros(B + 1)), rows=0, release=_i32([0, 1, 0]))
+    assert plan.new_lens.tolist() == [5, 0, 0] and plan.queue.tolist() == [0, 4, 0]
+    none = torch.empty(layers, 0, Hkv, D, dtype=torch.bfloat16, device=dev())
+    before = [x.view(torch.uint8).clone() for x in (cache.k, cache.v, cache.k_tail, cache.v_tail)]
+    sv.kv8_append(cache, none, none, tails, plan)
+    keep = torch.zeros(0, dtype=torch.int64, device=dev())
+    some = torch.ones(layers, 7, Hkv, D, dtype=torch.bfloat16, device=dev())
+    sv.kv8_append(cache, some[:, keep], some[:, :0], tails, plan)
+    if layers == 1:
+        sv.kv8_append(cache, none[0], none[0], tails, plan)
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 0
+    for x, y in zip((cache.k, cache.v, cache.k_tail, cache.v_tail), before):
+        assert torch.equal(x.view(torch.uint8), y)
+    for bad in (none.float(), none.cpu(), none[:, :, :1], none.transpose(2, 3)):
+        with pytest.raises(ValueError):
+            sv.kv8_append(cache, bad, bad, tails, plan)
