@@ -534,10 +534,10 @@ def kv8_append(cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor, tails:
     rows = k_new.shape[1]
     shape = (layers, rows, Hkv, D)
     stride = _need_rows(k_new, "k_new", shape, dev)
-    _need_rows(v_new, "v_new", shape, dev)
-    if layers * rows > 1 and k_new.stride() != v_new.stride():
+    v_stride = _need_rows(v_new, "v_new", shape, dev)
+    layer_stride, v_layer = (k_new.stride(0), v_new.stride(0)) if layers > 1 else (0, 0)
+    if rows > 0 and (layer_stride != v_layer or (rows > 1 and stride != v_stride)):
         raise ValueError("k_new and v_new must have the same strides")
-    layer_stride = k_new.stride(0) if layers > 1 else 0
     B = tails.numel()
     if not (_is(tails, i32, dev, (B,)) and _is(plan.new_tails, i32, dev, (B,))
             and _is(plan.new_start, i32, dev, (B + 1,))):

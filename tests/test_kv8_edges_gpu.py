@@ -73,3 +73,36 @@ def test_a_step_of_no_rows(layers):
     for bad in (none.float(), none.cpu(), none[:, :, :1], none.transpose(2, 3)):
         with pytest.raises(ValueError):
             sv.kv8_append(cache, bad, bad, tails, plan)
+
+
+@pytest.mark.parametrize("layers,rows,Hkv", [(1, 70, 2), (1, 70, 1), (2, 70, 1), (2, 1, 2), (1, 1, 3)])
+def test_append_looks_at_the_strides_that_matter(layers, rows, Hkv):
+    """Keys and values whose strides differ in dimensions of size one are the
+    same call; ones whose rows or layers lie differently are refused."""
+    B, D = 1, 128
+    rng = np.random.default_rng(6)
+    data = [torch.from_numpy(rng.standard_normal((layers, rows, Hkv, D))).bfloat16().to(dev()) for _ in range(2)]
+    tails = _i32([0])
+    plan = sv.kv_block_plan(_i32([0]), tails, _i32([[-1, -1]]), _i32([1, 0]), _i32([0, 2, 0]),
+                            row_start=_i32([0, rows]), rows=rows)
+
+    def run(k, v):
+        cache = sv.kv8_cache(layers, 2, B, Hkv, device=dev())
+        sv.kv8_append(cache, k, v, tails, plan)
+        torch.cuda.synchronize()
+        assert sv.check_device_status() == 0
+        return [x.view(torch.uint8) for x in (cache.k, cache.v, cache.k_tail, cache.v_tail)]
+
+    def laid(x, *strides):
+        y = torch.zeros(8 * layers * rows * Hkv * D, dtype=torch.bfloat16, device=dev())
+        return y.as_strided(x.shape, strides).copy_(x)
+
+    want = run(*data)
+    row, layer = Hkv * D + 8, rows * (Hkv * D + 8) + 64
+    k = laid(data[0], layer, row, D, 1)
+    odd = [layer if layers > 1 else 7 * layer, row if rows > 1 else layer, D if Hkv > 1 else 16, 1]
+    assert all(torch.equal(a, b) for a, b in zip(run(k, laid(data[1], *odd)), want))
+    for bad in ([layer + 8, row, D, 1] if layers > 1 else None, [layer, row + 8, D, 1] if rows > 1 else None):
+        if bad:
+            with pytest.raises(ValueError):
+                run(k, laid(data[1], *bad))
