@@ -107,15 +107,19 @@ class Emitted:
 def verify_step(target: Target, cache: api.KV8Cache, state: Requests, last: torch.Tensor, draft: torch.Tensor,
                 max_len: int, top: int = 3) -> Emitted:
     """One greedy step: `last` int32 [B], the last emitted token of each
-    request (not yet in the cache), and its draft int32 [B, K]. The state and
-    the cache move on."""
+    request (not yet in the cache), and its draft int32 [B, K], K = 0 for plain
+    decoding. The state and the cache move on."""
     B, K = draft.shape
     ids = torch.cat([last[:, None], draft], 1)  # row i gives the token after draft i - 1
     logits, k, v = target.forward(ids, cache, state, max_len)
-    accepted, token, node = api.spec_accept_node(logits, draft)
+    if K:
+        accepted, token, node = api.spec_accept_node(logits, draft)
+    else:  # nothing to accept: the most probable token
+        token = api.token_logprobs(logits.view(B, -1), ids[:, :0], top=1).top_ids[:, 0]
+        accepted = node = torch.zeros_like(token)
     # the emitted tokens, row by row: drafts as far as they were accepted, then the target's
     row = torch.arange(K + 1, device=ids.device)[None]
-    tokens = torch.where(row < accepted[:, None], torch.cat([draft, draft[:, :1]], 1), token[:, None])
+    tokens = torch.where(row < accepted[:, None], torch.cat([draft, token[:, None]], 1), token[:, None])
     tokens = torch.where(row <= accepted[:, None], tokens, -1).int()
     report = api.token_logprobs(logits.view(B * (K + 1), -1), tokens.view(-1), top=top)
     # rows 0 .. accepted (the last token and the accepted drafts) go into the cache
@@ -181,7 +185,7 @@ def main():
     prompts = [torch.randint(0, target.vocab, (20 + 37 * b,), generator=g).tolist() for b in range(a.requests)]
     # plain greedy decoding first; its tokens, every third one wrong, then serve as drafts
     need = a.steps * (a.draft + 1)
-    plain = decode(target, prompts, need, 1, lambda b, t, K: [0] * K)
+    plain = decode(target, prompts, need, 0, lambda b, t, K: [])
     known = [p + [t for t, _ in o] for p, o in zip(prompts, plain)]
 
     def draft_of(b, tokens, K):
