@@ -15,8 +15,10 @@ from ._lib import W4A16Error, check, lib
 
 GROUP = 128
 
-_device = torch._C._cuda_getDevice  # the current device's index
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the current device's index, and its current stream's handle, without the
+# lookups that the public functions add (a torch without CUDA has neither)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
