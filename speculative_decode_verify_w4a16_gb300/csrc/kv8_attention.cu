@@ -88,6 +88,18 @@
 
 namespace w4a16 {
 
+#if W4A16_TEST_HOOKS
+// Debug builds only: the producer of CTA 0 leaves out the keys of the 8-bit tile
+// with this index in its run (no copy, no arrival for it), so that the bounded
+// waits run out and the kernel reports a timeout. -1: off.
+__device__ int g_test_skip_tile = -1;
+__device__ __forceinline__ bool test_skip_tile(int tile) {
+  return blockIdx.x == 0 && tile == *(volatile int*)&g_test_skip_tile;
+}
+#else
+__device__ __forceinline__ bool test_skip_tile(int) { return false; }
+#endif
+
 constexpr int kKaD = 128;
 constexpr int kKaTile = 128;      // keys per tile
 constexpr float kKaRoom = 7.0f;    // log2 of the largest weight when m is set
@@ -647,7 +659,7 @@ __global__ void __launch_bounds__(KaCfg<NP>::kThreads, 1)
         const int za = pa < 0 ? none : pa * p.Hkv + kvh, zb = pb < 0 ? none : pb * p.Hkv + kvh;
         if (lane == 0) {
           ok = k_wait(kc);
-          if (ok) {
+          if (ok && !test_skip_tile(tc)) {
             uint8_t* kd = smem + C::kKOff + ks * C::kTileBytes;
             mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
             tma_load_3d(kd, &maps.k, 0, 0, za, &k_full[ks]);
@@ -1359,3 +1371,10 @@ cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspac
 }
 
 }  // namespace w4a16
+
+#if W4A16_TEST_HOOKS
+// Debug builds only (not part of the C ABI header): see g_test_skip_tile.
+extern "C" int w4a16_test_set_skip_tile(int tile) {
+  return (int)cudaMemcpyToSymbol(w4a16::g_test_skip_tile, &tile, sizeof(int));
+}
+#endif
