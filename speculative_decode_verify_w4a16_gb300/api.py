@@ -411,6 +411,11 @@ def _is(t: torch.Tensor, dtype: torch.dtype, dev: int, shape) -> bool:
     return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
 
 
+def _need_ws(ws: torch.Tensor, dev: int):
+    if ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
+
+
 def _need_cache(c: KV8Cache, dev: int):
     k, k_tail = c.k, c.k_tail
     shape = k.shape
@@ -617,6 +622,8 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
         _need(out, "out", torch.bfloat16, (B, n, H, D))
     if ws is None:
         ws = _stream_workspace(_attention_ws(dev, B, n, H, Hkv, D, max_len), "kv8_attention", stream)
+    else:
+        _need_ws(ws, dev)
     codes, heads = pages * Hkv * KV_BLOCK * D * layer, pages * Hkv * layer * 4
     tail = tail_pages * Hkv * KV_BLOCK * D * layer * 2
     check(lib().kv8_tree_attention(
@@ -665,6 +672,8 @@ def token_logprobs(logits: torch.Tensor, ids: torch.Tensor, top: int = 0, ws: Op
                         torch.empty((R, top), dtype=f32, device=dev))
     if ws is None:
         ws = _stream_workspace(_logprobs_ws(R, V, top), "logprobs", stream)
+    else:
+        _need_ws(ws, _device())
     check(lib().token_logprobs(logits.data_ptr(), int(logits.dtype is torch.bfloat16), ids.data_ptr(), R, V, m, top,
                                out.logp.data_ptr(), out.entropy.data_ptr(), out.top_ids.data_ptr(),
                                out.top_logp.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),

@@ -109,3 +109,16 @@ def test_a_graph_has_its_own(make, larger):
     torch.cuda.synchronize()
     assert torch.equal(out_2, want_f) and torch.equal(out_f, want_f) and torch.equal(out_g, want_g)
     assert sv.check_device_status() == 0
+
+
+@pytest.mark.parametrize("make", CALLS)
+def test_a_workspace_that_is_not_on_the_device_is_refused(make):
+    f = make(6)
+    f()
+    with pytest.raises(ValueError):
+        f(ws=torch.zeros(1 << 26, dtype=torch.uint8))
+    with pytest.raises(sv.W4A16Error) as e:
+        f(ws=torch.zeros(256, dtype=torch.uint8, device=dev()))
+    assert e.value.status == 6  # W4A16_ERR_WORKSPACE
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 0
