@@ -25,6 +25,7 @@ __all__ = [
     "check_device_status", "kv8_append", "kv8_cache", "kv8_tree_attention", "kv8_tree_attention_workspace_bytes",
     "kv_block_plan", "kv_compact", "linear", "linear_logits", "linear_logits_workspace_bytes", "linear_noalloc",
     "linear_workspace_bytes", "packed_scale_bytes", "packed_weight_bytes", "prepack", "quantize", "spec_accept",
-    "spec_accept_node", "spec_accept_prestat", "token_logprobs", "token_logprobs_workspace_bytes", "tree_attention", "tree_attention_workspace_bytes", "workspace",
+    "spec_accept_node", "spec_accept_prestat", "token_logprobs", "token_logprobs_workspace_bytes", "tree_attention",
+    "tree_attention_workspace_bytes", "workspace",
     "LIB_PATH", "W4A16Error", "lib", "status_string",
 ]

@@ -19,9 +19,11 @@
 // tail rows, (request, group of layer-heads) by (request, group): no CTA is
 // launched for work that is not there (one CTA for every piece that might exist
 // took 33 us for 80 layers of 16 drafts).
-// Measured: prompts of 32767 rows (8 heads, 182 MB) 36 us, 0.75 of the HBM copy
-// rate; 80 rows of 16 drafts in 80 layers (60 MB, most of it blocks that
-// complete) 14.9 us, 0.60; 64 rows of one layer 3.7 us. Against what there was at
+// Measured: prompts of 29364 rows (8 heads, 182 MB; 7344 page items, six in turn
+// a CTA) 36 us, 0.74 of the HBM copy rate; 46 rows of 16 drafts in 80 layers (60
+// MB, half of it the one block that completes: 1280 page items, a second one for
+// 64 of the 1216 CTAs, then the tail rows) 14.9 us, 0.60; 64 rows of one layer
+// 3.7 us. Against what there was at
 // the time: keys and values by the same CTA (256 threads, four an SM) 37.3, 16.8
 // and 4.4 us against 37.9, 16.4 and 3.8; the next item's words on their way
 // meanwhile (in registers, or copied to shared memory asynchronously) 41 to 45 us

@@ -61,13 +61,13 @@
 // per run, and the CTA that finishes last of them (a counter) merges them.
 //
 // Measured (one layer of 64 query heads on 8, e4m3): four requests of 120 to
-// 131 K tokens, one node each (1.02 GB) 158 us, 0.95 of the HBM copy rate, which
+// 131 K tokens, one node each (1.02 GB) 159 us, 0.95 of the HBM copy rate, which
 // bounds it; 16 requests of 4 to 8 K tokens, chains of 5 (198 MB) 48 us, 0.61 of
 // it; 16 of 2 to 4 K tokens with trees of 64 nodes (102 GFLOP) 199 us, 0.27 of
-// the bf16 rate; one request of 1003 tokens and one node 10.7 us. The chains and
+// the bf16 rate; one request of 1003 tokens and one node 10.6 us. The chains and
 // trees are bound by the softmax warps' latency: a tile takes some 1600 cycles at
 // 48 rows and 1800 at 64 (the products take 460 and 600 of them, the warps issue
-// in 40 to 50 % of the cycles), and a part's start and end some 8000. Measured
+// in 45 to 55 % of the cycles), and a part's start and end some 8000. Measured
 // and not kept, against what there was at the time: 128 rows a block with 32 a
 // warpgroup, the trees in 563 us (registers); 32 rows a warpgroup at 64, no gain
 // (fewer warps to hide latency with), 8 rows at 48, the chains in 55 against 48

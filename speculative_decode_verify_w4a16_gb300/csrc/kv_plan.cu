@@ -11,7 +11,7 @@
 // 64 K rows of 1021 requests, moves 0.55 MB. So every CTA computes the sums
 // over all requests itself (a few KB from L2) instead of waiting for another
 // kernel or CTA, and the rows and pages are dealt over the grid. Measured: 16
-// requests with a draft each 4.5 us, 1021 requests with 63 rows each 7.4 us;
+// requests with a draft each 4.5 us, 1021 requests with 0 to 126 rows each 7.4 us;
 // nearly all of it is the launch and the chain of loads and scans.
 #include <limits.h>
 

@@ -24,15 +24,19 @@
 // instructions wherever there are any. With at least four rows an SM a CTA takes
 // a row from its first load to its report (token_logprobs_kernel); with fewer,
 // the windows are spread over all SMs and a second kernel reports
-// (token_stats_kernel, token_report_kernel). Rows of 128256 logits, both ways,
-// in us (before the last steps): 64 rows 16 and 13, 228 27 and 22, 608 33 and 40
-// (fp32 55 and 58), 912 51 and 58 (bf16).
+// (token_stats_kernel, token_report_kernel). Rows of 128256 logits with 20
+// alternatives, both ways, in us: bf16, 16 rows 15.7 and 11.5, 64 rows 16.0 and
+// 17.1, 228 29.1 and 26.0, 456 34.5 and 36.5, 608 35.1 and 43.3, 1024 57.5 and
+// 66.9; fp32, 16 rows 16.1 and 12.7, 228 27.4 and 32.2, 456 51.4 and 50.1, 608
+// 60.3 and 61.5, 1024 105 and 97: nowhere does the rule lose more than 18 %.
 // A row's CTA has 256 threads, four CTAs an SM: with 1024 rows the later rows
-// stream while the first ones report (56 us, 263 MB: 0.70 of the HBM copy rate;
+// stream while the first ones report (57 us, 263 MB: 0.68 of the HBM copy rate;
 // 58 us with every load's bounds looked at, not only those of a row's ends); 128
 // threads and eight CTAs take them all at once and then report all at once, 68
 // against 58; 512 threads 63; the maxima by the reduction instruction for floats
-// 58 against 56. 16 rows of fp32 (8.2 MB) take 7.7 us, latency.
+// 58 against 56. 16 rows of fp32 (8.2 MB) take 8.2 us, latency. Rows where fewer
+// than `top` logits are above all others (all but a few masked, or flat) take 0.3
+// ms, 1024 of them 0.9 (bf16) and 1.7 ms: every logit is then a candidate.
 // Windows start at 16-byte boundaries of memory, not of the row, so that rows of
 // any length load 16 bytes at a time.
 #include <math.h>
