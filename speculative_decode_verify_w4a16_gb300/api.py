@@ -15,9 +15,11 @@ from ._lib import W4A16Error, check, lib
 
 GROUP = 128
 
-# the current device's index, and its current stream's handle, without the
-# lookups that the public functions add (a torch without CUDA has neither)
+# the current device's index, its current stream's handle, and whether that is
+# being captured, without the lookups that the public functions add (a torch
+# without CUDA has none of them)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: True)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
@@ -77,7 +79,7 @@ def _stream_workspace(nbytes: int, key: str, stream=None) -> torch.Tensor:
     zeroed by the graph: a captured graph holds no address of a buffer that a
     later call might replace, and an eager call none that only a graph zeroes."""
     raw = _stream(stream)
-    capture = lib().w4a16_stream_capture_id(raw)
+    capture = lib().w4a16_stream_capture_id(raw) if stream is not None or _capturing() else 0
     k = (_device(), raw, key, capture != 0)
     kept = _stream_ws.get(k)
     if kept is not None and kept[0] == capture and kept[1].numel() >= nbytes:
