@@ -431,8 +431,9 @@ w4a16_status kv8_append(const void* k_new, const void* v_new, int64_t row_stride
  * as they are; q as the sum of two 8-bit terms, exact down to 2^-14 of the
  * row's largest element), the softmax weights rounded to fp16 for the 8-bit
  * values (times the block's value scale: 11 bits down to 2^-21 of the row's
- * largest such product, fewer below) and to bf16 for the tail's and the tree's
- * own, out to bf16.
+ * largest such product, fewer below; a block of zeros, with kv8_append's scale
+ * of 1 for it, does not count) and to bf16 for the tail's and the tree's own, out
+ * to bf16.
  * A length outside [0, max_len], a bad parent, or a page or tail id outside
  * the cache sets W4A16_ERR_DEVICE_INPUT (length clamped; the node attends to
  * itself and the prefix; a bad page reads as zeros). Launch rules as for

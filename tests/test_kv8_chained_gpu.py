@@ -38,7 +38,7 @@ def test_log_probabilities_right_after_the_logits(M):
     for _ in range(5):
         for x, exp in zip(xs, want):
             sv.linear_logits(x, w, logits=logits, stats=stats)
-            r = sv.token_logprobs(logits, ids, top=7)  # of the buffer that the last round's logits were in
+            r = sv.token_logprobs(logits, ids, top=7)  # of the buffer that the last pass's logits were in
             assert all(torch.equal(a, b) for a, b in zip((r.logp, r.entropy, r.top_ids, r.top_logp), exp))
     assert sv.check_device_status() == 0
 
@@ -46,20 +46,20 @@ def test_log_probabilities_right_after_the_logits(M):
 @pytest.mark.parametrize("dtype", [E4M3, E5M2])
 def test_plan_append_and_attention_one_after_the_other(dtype):
     """Prompts into an empty cache, and attention over them at once; the pages
-    hold another round's tokens until then."""
+    hold another pass's tokens until then."""
     rng = np.random.default_rng(12)
-    B, Hkv, H, n, D, rounds = 6, 4, 16, 3, 128, 5
+    B, Hkv, H, n, D, passes = 6, 4, 16, 3, 128, 5
     counts = np.array([700, 64, 1300, 1, 129, 400])
     rows, pages = int(counts.sum()), int((counts // 64).sum())
     start = _i32(np.concatenate([[0], np.cumsum(counts)]))
     cache = sv.kv8_cache(1, pages, B, Hkv, dtype=dtype, device=dev())
     lens, tails, queue = _i32(np.zeros(B)), _i32(2 * np.arange(B)), _i32([0, pages, 0])
     data = []
-    for _ in range(rounds):
+    for _ in range(passes):
         k, v = (torch.from_numpy(rng.standard_normal((rows, Hkv, D))).bfloat16().to(dev()) for _ in range(2))
         q, own_k, own_v = (torch.from_numpy(rng.standard_normal((B, n, h, D))).bfloat16().to(dev()) for h in (H, Hkv, Hkv))
         data.append((k, v, q, own_k, own_v))
-    rings = [_i32(rng.permutation(pages)) for _ in range(rounds)]
+    rings = [_i32(rng.permutation(pages)) for _ in range(passes)]
 
     def run(i, between):
         k, v, q, own_k, own_v = data[i]
@@ -71,10 +71,10 @@ def test_plan_append_and_attention_one_after_the_other(dtype):
         between()
         return sv.kv8_tree_attention(q, own_k, own_v, cache, 0, table, plan.new_lens, plan.new_tails)
 
-    want = [run(i, torch.cuda.synchronize).clone() for i in range(rounds)]
+    want = [run(i, torch.cuda.synchronize).clone() for i in range(passes)]
     assert all(torch.isfinite(w).all() for w in want)
     for _ in range(4):
-        got = [run(i, lambda: None) for i in range(rounds)]
+        got = [run(i, lambda: None) for i in range(passes)]
         torch.cuda.synchronize()
         assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert sv.check_device_status() == 0
