@@ -449,6 +449,89 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions: the rows of queries and keys turned by their positions.
+ * Pair i = 0 .. rot / 2 - 1 of a head's first `rot` elements is (i, i + rot / 2),
+ * or (2 i, 2 i + 1) with `interleaved`; the row at position p takes it from
+ * (u, v) to factor (u cos a - v sin a, v cos a + u sin a), a = p f_i; with
+ * `inverse` a = -p f_i (the gradient of the other direction; with factor 1 its
+ * undoing). The elements from `rot` on are copied.
+ *   x, y       device [T][heads][D] of type 0 (bf16), 1 (fp16) or 2 (fp32): rows
+ *              x_stride, y_stride elements apart (multiples of 8), heads D
+ *              apart; 16-byte aligned. y may be x (with the same stride), and
+ *              overlaps it in no other way
+ *   positions  device int32 [T], any value
+ *   turns      device uint64 [rot / 2]: f_i / 2 pi in units of 2^-64 (angles are
+ *              exact to 2^-32 turns and positions * 2^-65)
+ *   D a multiple of 8, <= 1024; rot a multiple of 16, <= D; T 1 .. 2^31 - 1
+ * Arithmetic: sines, cosines and the rotation in fp32, rounded once to the
+ * type. Launch rules as for w4a16_linear.
+ * ---------------------------------------------------------------------- */
+w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positions, const uint64_t* turns, int T,
+                         int heads, int D, int rot, int interleaved, float factor, int inverse, int type, void* y,
+                         int64_t y_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 16-bit key/value cache: a request's token p sits in row p % 64 of the
+ * page that its block table names for block p / 64. A step brings T rows, some
+ * for each request: the rows row_start[b] .. row_start[b + 1] - 1 of request b
+ * (none, one, or thousands) take the positions lens[b] onwards. The step's own
+ * keys and values are appended first, and attention reads them from the pages;
+ * rows that a verify step rejects are written over by the next step, which
+ * starts at the accepted length.
+ *   k, v         device [pages][Hkv][64][D] of one layer, type 0 (bf16) or 1
+ *                (fp16); D 64 or 128; 16-byte aligned
+ *   block_table  device int32 [B][max_blocks]: the pages of the blocks
+ *                0 .. (lens[b] + rows - 1) / 64 (other entries unread)
+ *   lens         device int32 [B]: tokens of request b before the step
+ *   row_start    device int32 [B + 1], not falling, row_start[B] <= T; NULL:
+ *                T / B rows each. Rows of no request are neither read nor written
+ *   T 1 .. 2^24, B <= 4096, pages * Hkv <= 2^25, B * max_blocks < 2^31
+ * A request whose rows or positions lie outside (row_start falling or past T, a
+ * negative length, a position past the table) sets W4A16_ERR_DEVICE_INPUT in
+ * the device error word and is left out: none of its rows is written. A page id
+ * outside the cache sets it too: nothing is written there, and it reads as
+ * zeros.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * A step's keys and values into the pages, the keys rotated by their positions
+ * on the way (rope_rotate's rotation; turns NULL with rot 0: none), and the
+ * rotated queries of the same rows (q, q_out NULL: none).
+ *   k_new, v_new  device [T][Hkv][D]; q, q_out device [T][H][D]; rows their
+ *                 strides apart, as in rope_rotate; q_out may be q
+ * Launch rules as for w4a16_linear.
+ * ---------------------------------------------------------------------- */
+w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride, const void* q,
+                         int64_t q_stride, const uint64_t* turns, int rot, int interleaved, float factor,
+                         const int32_t* block_table, const int32_t* lens, const int32_t* row_start, int T, int B,
+                         int H, int Hkv, int D, int max_blocks, int pages, int type, void* k, void* v, void* q_out,
+                         int64_t q_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Causal attention of a step's rows over the paged 16-bit cache, one layer: the
+ * row at position p of its request sees that request's keys 0 .. p, with a
+ * window the last `window` of them (max(0, p - window + 1) .. p); out =
+ * softmax(scale q . k) . v over those, query head h with key/value head
+ * h / (H / Hkv). What a row does not see does not touch it, NaN or infinite as
+ * it may be.
+ *   q, out     device [T][H][D] of the cache's type (16-byte aligned), rows of q
+ *              q_stride elements apart (a multiple of 8), out dense; the rows
+ *              of no request are left as they were
+ *   window     0: none
+ *   workspace  kv16_attention_workspace_bytes() bytes (256-byte aligned), zero
+ *              before its first use; every call leaves the counters at its
+ *              start zero. May be NULL when that is 0
+ * Arithmetic: scores and sums in fp32, the softmax weights rounded to the
+ * cache's type for the sum of the values, out rounded once. T * H < 2^31.
+ * Launch rules as for w4a16_linear.
+ * ---------------------------------------------------------------------- */
+size_t kv16_attention_workspace_bytes(int T, int H, int Hkv, int D);
+w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, const void* v, const int32_t* block_table,
+                            const int32_t* lens, const int32_t* row_start, int T, int B, int H, int Hkv, int D,
+                            int max_blocks, int pages, int window, float scale, int type, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Log probabilities of given tokens, entropy and the most probable tokens of
  * logit rows (what a serving step reports beside the tokens it emits).
  *   logits     device [R][V], fp32 (bf16 = 0) or bf16 (bf16 = 1), dense

@@ -5,9 +5,11 @@ CUDA stream; every step of the computation runs in the library's kernels.
 from __future__ import annotations
 
 import contextlib
+import math
 from dataclasses import dataclass
+from fractions import Fraction
 from functools import lru_cache
-from typing import Optional
+from typing import List, Optional, Tuple
 
 import torch
 
@@ -635,6 +637,328 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
         tails.data_ptr(), _ptr(tree_parents), B, n, H, Hkv, D, max_blocks, pages, tail_pages, max_len,
         _KV8_FORMATS[cache.k.dtype], scale, out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
         "kv8_tree_attention")
+    return out
+
+
+# ------------------------------------------------------ rotary positions
+
+_TURN = 2 * Fraction(31415926535897932384626433832795028841972, 10 ** 40)  # radians of a turn
+_ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+@dataclass
+class Rope:
+    """A rotation by position: the frequencies of its pairs, and how they lie."""
+    turns: torch.Tensor  # int64 [rot / 2], holding uint64: turns a position, in 2^-64
+    factor: float        # on what is rotated
+    interleaved: bool    # pairs (2i, 2i + 1), else (i, i + rot / 2)
+
+    @property
+    def rot(self) -> int:
+        return 2 * self.turns.numel()
+
+
+def rope_angles(rot: int, base: float = 10000.0, scaling: Optional[dict] = None) -> Tuple[List[float], float]:
+    """Radians a position of each of the rot / 2 pairs, base^(-2i / rot), and
+    the factor on what is rotated. `scaling` stretches them for contexts longer
+    than the trained ones ("kind", and what it needs):
+      none
+      linear  factor                    all positions divided
+      ntk     factor                    a larger base: base * factor^(rot / (rot - 2))
+      bands   factor, low, high, trained   pairs that turn `high` times or more over the `trained`
+                                        positions are kept, those that turn `low` times or less
+                                        divided, a blend between
+      yarn    factor, trained, fast (32), slow (1), attention   the same with a ramp over the pairs
+                                        (Peng et al. 2023), and what is rotated times `attention`
+                                        (0.1 ln factor + 1)"""
+    rot, base = int(rot), float(base)
+    if rot < 2 or rot % 2 or not (base > 0 and math.isfinite(base)):
+        raise ValueError("rot must be even and positive, base positive")
+    scaling = dict(scaling or {"kind": "none"})
+    kind = scaling.pop("kind", None)
+    needs = {"none": (), "linear": ("factor",), "ntk": ("factor",), "bands": ("factor", "low", "high", "trained"),
+             "yarn": ("factor", "trained")}
+    may = {"yarn": ("fast", "slow", "attention")}
+    if kind not in needs:
+        raise ValueError(f"scaling kind {kind!r} is not one of {', '.join(needs)}")
+    missing = [x for x in needs[kind] if x not in scaling]
+    unknown = [x for x in scaling if x not in needs[kind] + may.get(kind, ())]
+    if missing or unknown:
+        raise ValueError(f"scaling {kind}: " + (f"{missing[0]} is missing" if missing else f"unknown {unknown[0]}"))
+    v = {x: float(y) for x, y in scaling.items()}
+    if not all(y > 0 and math.isfinite(y) for y in v.values()):
+        raise ValueError(f"scaling {kind}: values must be positive")
+    factor = v.get("factor", 1.0)
+    if kind == "ntk":
+        if rot < 4:
+            raise ValueError("scaling ntk: rot must be 4 or more")
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    attention = 1.0
+    if kind == "linear":
+        f = [x / factor for x in f]
+    elif kind == "bands":
+        if not v["high"] > v["low"]:
+            raise ValueError("scaling bands: high must be above low")
+        for i, x in enumerate(f):
+            keep = (v["trained"] * x / (2 * math.pi) - v["low"]) / (v["high"] - v["low"])
+            keep = min(max(keep, 0.0), 1.0)
+            f[i] = x * keep + x / factor * (1 - keep)
+    elif kind == "yarn":
+        fast, slow = v.get("fast", 32.0), v.get("slow", 1.0)
+        if not fast >= slow or base == 1.0:
+            raise ValueError("scaling yarn: fast must not be below slow, base not 1")
+        first, last = (rot * math.log(v["trained"] / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow))
+        first, last = max(math.floor(first), 0), min(math.ceil(last), rot - 1)
+        for i, x in enumerate(f):
+            ramp = min(max((i - first) / max(last - first, 1e-3), 0.0), 1.0)
+            f[i] = x / factor * ramp + x * (1 - ramp)
+        attention = v.get("attention", 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0)
+    return f, attention
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[dict] = None, interleaved: bool = False,
+                     device=None) -> Rope:
+    """The rotation of the first `rot` elements of a head; see rope_angles for
+    base and scaling. rot is a multiple of 16."""
+    if rot % 16 != 0:
+        raise ValueError("rot must be a multiple of 16")
+    angles, factor = rope_angles(rot, base, scaling)
+    turns = []
+    for x in angles:  # the nearest whole number to x / 2 pi * 2^64, modulo 2^64, as an int64
+        n, d = x.as_integer_ratio()
+        t = (2 * (n << 64) * _TURN.denominator + d * _TURN.numerator) // (2 * d * _TURN.numerator) % 2 ** 64
+        turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    turns = torch.tensor(turns, dtype=torch.int64)
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    return Rope(turns.to(dev), factor, bool(interleaved))
+
+
+def _rows(t: torch.Tensor, name: str, dev: int):
+    """(rows, heads, D, elements from row to row) of a tensor [rows, heads, D]
+    or [B, n, heads, D] whose heads are dense and whose rows are evenly apart
+    (a slice of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        rows, heads, D = shape
+        stride, sh, sd = strides
+    elif len(shape) == 4:
+        B, n, heads, D = shape
+        rows = B * n
+        outer, stride, sh, sd = strides
+        if n == 1:
+            stride = outer
+        elif B > 1 and outer != n * stride:
+            raise ValueError(f"{name}: its rows must be evenly apart")
+    else:
+        raise ValueError(f"{name} must have 3 or 4 dimensions, got {tuple(shape)}")
+    if rows <= 1:
+        stride = heads * D + -(heads * D) % 8
+    if (D > 1 and sd != 1) or (heads > 1 and sh != D):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    if rows > 1 and (stride < heads * D or stride % 8 != 0):
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
+    return rows, heads, D, stride
+
+
+def _need_rope(r: Rope, D: int, dev: int) -> int:
+    t = r.turns
+    if t.dtype is not torch.int64 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous():
+        _need(t, "the rotation's turns", torch.int64, (t.numel(),))
+    rot = 2 * t.numel()
+    if rot > D:
+        raise ValueError(f"the rotation takes {rot} elements, a head has {D}")
+    return rot
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, freqs: Rope, out: Optional[torch.Tensor] = None,
+         inverse: bool = False, stream=None) -> torch.Tensor:
+    """Rows turned by their positions. x bf16, fp16 or fp32 [T, heads, D] or
+    [B, n, heads, D], possibly a slice of a fused projection (heads dense, rows
+    evenly apart); positions int32 of x's leading shape; out: like x (x itself:
+    in place; it overlaps x in no other way). inverse: by the opposite angle,
+    which also takes a gradient with respect to the result to one with respect
+    to x."""
+    dev = _device()
+    kind = _ROW_TYPES.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"x must be {torch.bfloat16}, {torch.float16} or {torch.float32}, got {x.dtype}")
+    T, heads, D, stride = _rows(x, "x", dev)
+    lead = x.shape[:-2]
+    if not _is(positions, torch.int32, dev, lead):
+        _need(positions, "positions", torch.int32, lead)
+    rot = _need_rope(freqs, D, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out_stride = heads * D
+    elif out is x:
+        out_stride = stride
+    else:
+        if out.dtype is not x.dtype or out.shape != x.shape:
+            raise ValueError(f"out must be {x.dtype} of shape {tuple(x.shape)}, got {out.dtype} {tuple(out.shape)}")
+        out_stride = _rows(out, "out", dev)[3]
+    if T == 0 or heads == 0:
+        return out
+    check(lib().rope_rotate(x.data_ptr(), stride, positions.data_ptr(), freqs.turns.data_ptr(), T, heads, D, rot,
+                            freqs.interleaved, freqs.factor, inverse, kind, out.data_ptr(), out_stride,
+                            _stream(stream)), "rope_rotate")
+    return out
+
+
+# ------------------------------------------------------ paged 16-bit cache
+
+@dataclass
+class KV16Cache:
+    """Keys and values in 16 bits, in pages of 64 tokens. The leading dimension is the layer."""
+    k: torch.Tensor  # bf16 or fp16 [layers, pages, Hkv, 64, D]
+    v: torch.Tensor
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k, self.v))
+
+
+def kv16_cache(layers: int, pages: int, Hkv: int, D: int = 128, dtype: torch.dtype = torch.bfloat16,
+               device=None) -> KV16Cache:
+    """An empty cache of `pages` pages."""
+    if _ROW_TYPES.get(dtype, 2) > 1:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    return KV16Cache(*(torch.zeros((layers, pages, Hkv, KV_BLOCK, D), dtype=dtype, device=dev) for _ in range(2)))
+
+
+def _need_kv16(c: KV16Cache, layer: int, dev: int):
+    """(type, pages, Hkv, D, bytes before the layer) of a cache's layer."""
+    k, shape, dtype = c.k, c.k.shape, c.k.dtype
+    kind = _ROW_TYPES.get(dtype, 2)
+    if kind > 1:
+        raise ValueError("the cache must be torch.bfloat16 or torch.float16")
+    if len(shape) != 5 or shape[3] != KV_BLOCK:
+        raise ValueError(f"the cache must have shape (layers, pages, Hkv, {KV_BLOCK}, D), got {tuple(shape)}")
+    if not (_is(k, dtype, dev, shape) and _is(c.v, dtype, dev, shape)):
+        _need(k, "cache.k", dtype, shape)
+        _need(c.v, "cache.v", dtype, shape)
+    layers, pages, Hkv, _, D = shape
+    if not 0 <= layer < layers:
+        raise ValueError(f"layer {layer} is not one of the cache's {layers}")
+    return kind, pages, Hkv, D, 2 * layer * pages * Hkv * KV_BLOCK * D
+
+
+def _need_step(block_table: torch.Tensor, lens: torch.Tensor, row_start: Optional[torch.Tensor], rows: int, dev: int):
+    """(B, max_blocks) of a step's requests."""
+    i32 = torch.int32
+    B = lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
+    if not (_is(lens, i32, dev, (B,)) and _is(block_table, i32, dev, block_table.shape)):
+        _need(lens, "lens", i32, (B,))
+        _need(block_table, "block_table", i32)
+    if row_start is None:
+        if B == 0 or rows % B:
+            raise ValueError(f"{rows} rows are not the same number for each of {B} requests: row_start is required")
+    elif not _is(row_start, i32, dev, (B + 1,)):
+        _need(row_start, "row_start", i32, (B + 1,))
+    return B, block_table.shape[1]
+
+
+def kv16_append(cache: KV16Cache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
+                lens: torch.Tensor, *, row_start: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                stream=None) -> Optional[torch.Tensor]:
+    """A step's keys and values of one layer into the cache's pages, the keys
+    rotated by their positions on the way, and the queries of the same rows
+    with them. k_new, v_new [T, Hkv, D] and q [T, H, D] (or [B, n, .., D]) of the
+    cache's type may be slices of one fused projection. Request b's rows are
+    row_start[b] .. row_start[b + 1] - 1 (int32 [B + 1]; default: T / B each), at
+    positions lens[b] onwards; block_table int32 [B, max_blocks] names their
+    pages. Rows behind the last request's are left alone. Returns the rotated
+    queries (q_out, which may be q; a new tensor by default), None without q."""
+    dev = _device()
+    kind, pages, Hkv, D, at = _need_kv16(cache, layer, dev)
+    dtype = cache.k.dtype
+    T, heads, width, k_stride = _rows(k_new, "k_new", dev)
+    v_rows, v_heads, v_width, v_stride = _rows(v_new, "v_new", dev)
+    if (heads, width) != (Hkv, D) or (v_rows, v_heads, v_width) != (T, Hkv, D):
+        raise ValueError(f"k_new and v_new must have rows of ({Hkv}, {D}), got {tuple(k_new.shape)} and "
+                         f"{tuple(v_new.shape)}")
+    if k_new.dtype is not dtype or v_new.dtype is not dtype:
+        raise ValueError(f"k_new and v_new must be {dtype}, as the cache, got {k_new.dtype} and {v_new.dtype}")
+    B, max_blocks = _need_step(block_table, lens, row_start, T, dev)
+    rot = 0 if rope is None else _need_rope(rope, D, dev)
+    H, q_stride, out_stride = 0, 0, 0
+    if q is not None:
+        q_rows, H, q_width, q_stride = _rows(q, "q", dev)
+        if q_rows != T or q_width != D or q.dtype is not dtype:
+            raise ValueError(f"q must be {dtype} with {T} rows of heads of {D}, got {q.dtype} {tuple(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            out_stride = H * D
+        elif q_out is q:
+            out_stride = q_stride
+        else:
+            if q_out.dtype is not dtype or q_out.shape != q.shape:
+                raise ValueError(f"q_out must be {dtype} of shape {tuple(q.shape)}, got {q_out.dtype} "
+                                 f"{tuple(q_out.shape)}")
+            out_stride = _rows(q_out, "q_out", dev)[3]
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    if T == 0:
+        return q_out
+    check(lib().kv16_append(k_new.data_ptr(), v_new.data_ptr(), k_stride, v_stride, _ptr(q), q_stride,
+                            None if rope is None else rope.turns.data_ptr(), rot,
+                            False if rope is None else rope.interleaved, 1.0 if rope is None else rope.factor,
+                            block_table.data_ptr(), lens.data_ptr(), _ptr(row_start), T, B, H, Hkv, D, max_blocks, pages,
+                            kind, cache.k.data_ptr() + at, cache.v.data_ptr() + at, _ptr(q_out), out_stride,
+                            _stream(stream)), "kv16_append")
+    return q_out
+
+
+def kv16_attention_workspace_bytes(T: int, H: int, Hkv: int, D: int) -> int:
+    return int(lib().kv16_attention_workspace_bytes(T, H, Hkv, D))
+
+
+@lru_cache(maxsize=256)
+def _kv16_ws(device: int, T: int, H: int, Hkv: int, D: int) -> int:
+    return kv16_attention_workspace_bytes(T, H, Hkv, D)
+
+
+def kv16_attention(q: torch.Tensor, cache: KV16Cache, layer: int, block_table: torch.Tensor, lens: torch.Tensor, *,
+                   row_start: Optional[torch.Tensor] = None, window: int = 0, scale: Optional[float] = None,
+                   out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of a step's rows, whose keys and values kv16_append has
+    put into the cache: decoding rows, sequence drafts, chunks of prompts, or all
+    of them in one call. q [T, H, D] (or [B, n, H, D]) of the cache's type may be
+    a slice of a fused projection; block_table, lens and row_start as for
+    kv16_append (lens: tokens before the step). The row at position p sees the
+    keys 0 .. p, with a window the last `window` of them. ws: zeroed before its
+    first use, and used by no two calls at once (default: one for each stream
+    and capture). Returns out, dense and of q's shape; its rows behind the last
+    request's are left as they were (undefined in a new tensor)."""
+    dev = _device()
+    kind, pages, Hkv, D, at = _need_kv16(cache, layer, dev)
+    T, H, width, q_stride = _rows(q, "q", dev)
+    if width != D or q.dtype is not cache.k.dtype:
+        raise ValueError(f"q must be {cache.k.dtype} with heads of {D}, got {q.dtype} {tuple(q.shape)}")
+    B, max_blocks = _need_step(block_table, lens, row_start, T, dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif not _is(out, q.dtype, dev, q.shape):
+        _need(out, "out", q.dtype, q.shape)
+    if T == 0:
+        return out
+    if ws is None:
+        ws = _stream_workspace(_kv16_ws(dev, T, H, Hkv, D), "kv16_attention", stream)
+    else:
+        _need_ws(ws, dev)
+    check(lib().kv16_attention(q.data_ptr(), q_stride, cache.k.data_ptr() + at, cache.v.data_ptr() + at,
+                               block_table.data_ptr(), lens.data_ptr(), _ptr(row_start), T, B, H, Hkv, D, max_blocks,
+                               pages, window, scale, kind, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _stream(stream)), "kv16_attention")
     return out
 
 

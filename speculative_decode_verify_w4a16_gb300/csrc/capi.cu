@@ -465,6 +465,150 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
              : W4A16_ERR_CUDA;
 }
 
+// ------------------------------------------------- rotary positions
+// rows of a tensor [T][heads][D]: `stride` elements apart
+static bool rows_ok(const void* p, int64_t stride, int64_t heads, int D) {
+  return aligned(p, 16) && stride >= heads * D && stride % 8 == 0;
+}
+
+static bool rotation_ok(const uint64_t* turns, int D, int rot, float factor) {
+  return rot >= 0 && rot <= D && (rot == 0 || turns) && aligned(turns, 8) && factor > 0.0f && factor < INFINITY;
+}
+
+w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positions, const uint64_t* turns, int T,
+                         int heads, int D, int rot, int interleaved, float factor, int inverse, int type, void* y,
+                         int64_t y_stride, void* stream) {
+  if (!x || !positions || !turns || !y || T < 1 || heads < 1 || D < 1 || rot < 2 || type < 0 || type > 2)
+    return W4A16_ERR_INVALID_ARG;
+  if (!rotation_ok(turns, D, rot, factor) || !rows_ok(x, x_stride, heads, D) || !rows_ok(y, y_stride, heads, D) ||
+      !aligned(positions, 4) || (x == y && x_stride != y_stride))
+    return W4A16_ERR_INVALID_ARG;
+  if (D % 8 != 0 || rot % 16 != 0 || D > 1024 || heads > (1 << 20)) return W4A16_ERR_UNSUPPORTED;
+  RowParams p = {};
+  p.q = x;
+  p.q_stride = x_stride;
+  p.q_out = y;
+  p.out_stride = y_stride;
+  p.positions = positions;
+  p.turns = turns;
+  p.factor = factor;
+  p.T = T;
+  p.Hq = heads;
+  p.D = D;
+  p.rot = rot;
+  p.inter = interleaved != 0;
+  p.inverse = inverse != 0;
+  return launch_rope(p, type, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+}
+
+// ------------------------------------------------- paged 16-bit cache
+// a step's rows and the cache that they go to
+static bool kv16_step_ok(const int32_t* row_start, int T, int B, int Hkv, int max_blocks, int pages) {
+  return T >= 1 && B >= 1 && Hkv >= 1 && Hkv <= 65535 && pages >= 1 && max_blocks >= 1 &&
+         max_blocks <= (INT32_MAX - 63) / 64 && (int64_t)B * max_blocks <= INT32_MAX &&
+         (int64_t)pages * Hkv <= (1 << 25) && (row_start || T % B == 0);
+}
+
+w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride, const void* q,
+                         int64_t q_stride, const uint64_t* turns, int rot, int interleaved, float factor,
+                         const int32_t* block_table, const int32_t* lens, const int32_t* row_start, int T, int B,
+                         int H, int Hkv, int D, int max_blocks, int pages, int type, void* k, void* v, void* q_out,
+                         int64_t q_out_stride, void* stream) {
+  if (!k_new || !v_new || !block_table || !lens || !k || !v || (q != nullptr) != (q_out != nullptr))
+    return W4A16_ERR_INVALID_ARG;
+  if (!kv16_step_ok(row_start, T, B, Hkv, max_blocks, pages) || D < 1 || type < 0 || type > 1 ||
+      (q && (H < 1 || !rows_ok(q, q_stride, H, D) || !rows_ok(q_out, q_out_stride, H, D))) ||
+      (q == q_out && q_stride != q_out_stride))
+    return W4A16_ERR_INVALID_ARG;
+  if (!rows_ok(k_new, k_stride, Hkv, D) || !rows_ok(v_new, v_stride, Hkv, D) ||
+      !rotation_ok(turns, D, rot, factor) || !aligned(k, 16) || !aligned(v, 16) || !aligned(block_table, 4) ||
+      !aligned(lens, 4) || !aligned(row_start, 4))
+    return W4A16_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || rot % 16 != 0 || B > kPlanMaxB || T > (1 << 24) || (q && H > (1 << 20)))
+    return W4A16_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  RowParams p = {};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.q_out = q_out;
+  p.out_stride = q_out_stride;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.turns = turns;
+  p.factor = factor;
+  p.T = T;
+  p.Hq = q ? H : 0;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.rot = rot;
+  p.inter = interleaved != 0;
+  p.start = row_start;
+  p.lens = lens;
+  p.table = block_table;
+  p.B = B;
+  p.per = T / B;
+  p.max_blocks = max_blocks;
+  p.pages = pages;
+  p.k = k;
+  p.v = v;
+  p.err = dev.err;
+  return launch_kv16_append(p, type, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
+}
+
+static bool kv16_attn_shape_ok(int T, int H, int Hkv) {
+  return T >= 1 && H >= 1 && Hkv >= 1 && Hkv <= 65535 && H % Hkv == 0 && (int64_t)T * H <= INT32_MAX;
+}
+
+size_t kv16_attention_workspace_bytes(int T, int H, int Hkv, int D) {
+  if (!kv16_attn_shape_ok(T, H, Hkv) || (D != 64 && D != 128) || T > (1 << 24)) return 0;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return 0;
+  return kv16_attention_ws(T, H, Hkv, D, dev.num_sms);
+}
+
+w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, const void* v, const int32_t* block_table,
+                            const int32_t* lens, const int32_t* row_start, int T, int B, int H, int Hkv, int D,
+                            int max_blocks, int pages, int window, float scale, int type, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!q || !k || !v || !block_table || !lens || !out) return W4A16_ERR_INVALID_ARG;
+  if (!kv16_attn_shape_ok(T, H, Hkv) || !kv16_step_ok(row_start, T, B, Hkv, max_blocks, pages) || D < 1 || type < 0 ||
+      type > 1 || window < 0 || !rows_ok(q, q_stride, H, D) || !(scale > 0.0f) || !(scale < INFINITY))
+    return W4A16_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
+      !aligned(row_start, 4))
+    return W4A16_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || B > kPlanMaxB || T > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
+  const size_t need = kv16_attention_ws(T, H, Hkv, D, dev.num_sms);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  Kv16AttnParams p = {};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.k = k;
+  p.v = v;
+  p.start = row_start;
+  p.lens = lens;
+  p.table = block_table;
+  p.T = T;
+  p.B = B;
+  p.per = T / B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.max_blocks = max_blocks;
+  p.pages = pages;
+  p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out;
+  p.err = dev.err;
+  return launch_kv16_attention(p, type, D, workspace, dev.num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? W4A16_OK
+             : W4A16_ERR_CUDA;
+}
+
 // ------------------------------------------------- log probabilities
 static bool logprobs_shape_ok(int R, int V, int m, int top) {
   return R >= 1 && R <= (1 << 20) && V >= 1 && V <= (1 << 20) && m >= 0 && m <= 64 && top >= 0 && top <= 64 &&

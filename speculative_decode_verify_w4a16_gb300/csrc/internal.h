@@ -161,6 +161,38 @@ size_t kv8_attention_ws(int n, int H, int Hkv, int num_sms);
 bool kv8_attention_fits(int B, int n, int H, int Hkv, int max_len);
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, int fmt, void* workspace, int num_sms, cudaStream_t stream);
 
+// ---- rotary positions, paged 16-bit cache
+struct RowParams {
+  const void* q;  // [T][Hq][D], rows q_stride elements apart (rope: the rows themselves)
+  void* q_out;    // [T][Hq][D], rows out_stride apart
+  const void *k_new, *v_new;  // [T][Hkv][D]
+  int64_t q_stride, out_stride, k_stride, v_stride;
+  const int32_t* positions;  // rope: [T]
+  const uint64_t* turns;     // [rot / 2]: turns a position, in 2^-64
+  float factor;
+  int T, Hq, Hkv, D, rot, inter, inverse;
+  // append: row i of request b (start[b] .. start[b + 1] - 1, or `per` rows each) at position lens[b] + i - start[b]
+  const int32_t *start, *lens, *table;
+  int B, per, max_blocks, pages;
+  void *k, *v;  // [pages][Hkv][64][D]
+  unsigned* err;
+};
+cudaError_t launch_rope(const RowParams& p, int type, cudaStream_t stream);
+cudaError_t launch_kv16_append(const RowParams& p, int type, cudaStream_t stream);
+struct Kv16AttnParams {
+  const void* q;  // [T][H][D], rows q_stride elements apart
+  int64_t q_stride;
+  const void *k, *v;  // [pages][Hkv][64][D]
+  const int32_t *start, *lens, *table;
+  int T, B, per, H, Hkv, max_blocks, pages, window;
+  float scale_log2;  // softmax scale * log2(e)
+  void* out;  // [T][H][D]
+  unsigned* err;
+};
+size_t kv16_attention_ws(int rows, int H, int Hkv, int D, int num_sms);
+cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void* workspace, int num_sms,
+                                  cudaStream_t stream);
+
 // ---- log probabilities of logit rows
 size_t token_logprobs_ws(int R, int V);
 cudaError_t launch_token_logprobs(const void* logits, bool bf16, const int32_t* ids, int R, int V, int m, int top,
