@@ -580,7 +580,8 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4))
     return W4A16_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || B > kPlanMaxB || T > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || B > kPlanMaxB || T > (1 << 24) || !kv16_attention_fits(T, B, H, Hkv, max_blocks))
+    return W4A16_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
   const size_t need = kv16_attention_ws(T, H, Hkv, D, dev.num_sms);

@@ -189,7 +189,8 @@ struct Kv16AttnParams {
   void* out;  // [T][H][D]
   unsigned* err;
 };
-size_t kv16_attention_ws(int rows, int H, int Hkv, int D, int num_sms);
+size_t kv16_attention_ws(int T, int H, int Hkv, int D, int num_sms);
+bool kv16_attention_fits(int T, int B, int H, int Hkv, int max_blocks);
 cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void* workspace, int num_sms,
                                   cudaStream_t stream);
 

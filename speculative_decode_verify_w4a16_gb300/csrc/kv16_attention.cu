@@ -1,101 +1,1039 @@
 // Causal attention of a step's new rows over the paged 16-bit cache (contract in w4a16sv.h).
 //
 // A row at position p of its request sees the keys max(0, p - window + 1) .. p:
-// out = sum_j softmax_j(scale q . k_j) v_j, a warp a row and query head, the
-// running maximum and sum of the softmax in fp32.
+// out = sum_j softmax_j(scale q . k_j) v_j. The query rows of a key/value head
+// are its G = H / Hkv query heads at every new token, row r = token * G +
+// head-in-group, so that keys and values are read once for the group. A unit
+// is 256 of those rows of one request and head, against 128-key tiles (two
+// pages) from the first key that any of its rows sees to the last.
+//
+// Split: the units of all requests end to end, by their estimated work, cut into
+// one run a CTA (a CTA an SM), at tile boundaries. A unit that is cut leaves
+// its pieces' maxima, sums and unnormalised outputs in the workspace, and the
+// CTA that finishes last merges them, in the order of the keys: every CTA gets
+// the same work whatever the lengths are, decoding rows and prompts share a
+// launch, the host needs no length, and no CTA waits for another.
+//
+// In a CTA (tcgen05, TMEM, TMA):
+//   warp 0        the run's parts (a unit or a piece of one), published in a
+//                 ring of descriptors; TMA copies of K and V tiles into a ring
+//   warps 1, 2    the MMAs of slot 0 and 1: S = Q K^T (128 x 128 x D, both from
+//                 shared memory) and O += P V (P from TMEM, V as it was loaded:
+//                 the MN-major operand)
+//   warp 3        the guard: looks through the values of tiles that some row
+//                 sees in part, and takes out NaN and infinities, which a weight
+//                 of zero would not hide; rows that do see them get them added
+//                 at the end
+//   warps 4 - 11  the softmax of slot 0 and 1, one row a thread: scores from
+//                 TMEM, running maximum and sum in fp32, weights rounded to the
+//                 cache's type back into TMEM over the scores
+// With more than 128 rows the two slots are two row tiles, which share every
+// key tile; with fewer they take the key tiles in turn and are merged at the
+// part's end. While one slot's softmax runs, the tensor pipe works for the other.
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
-#include "common.cuh"
 #include "internal.h"
+#include "softmax.cuh"
+#include "tcgen05.cuh"
 
 namespace w4a16 {
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) {
-  return __bfloat162float(x);
+constexpr int kCaThreads = 384;
+constexpr int kCaKeys = 128;  // keys of a tile: two pages
+constexpr int kCaDesc = 4;    // parts described ahead
+constexpr int kCaOk = 8;      // guarded tiles that the guard may be ahead: more than the ring holds
+constexpr int kCaSpecial = 10;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
+
+// The weights a key tile has in the split: two row tiles, or one.
+constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
+constexpr int kCaOverhead = 128;  // keys that a unit's start and end are worth
+
+// Weights are taken against a reference that is raised only by a maximum more
+// than `lazy` (log2) above it, so that the sums in TMEM are seldom rescaled. In
+// fp16 the reference itself stands for 2^8: weights up to 2^14 fit, and those
+// down to 2^-22 of the reference keep all their bits (2^-32: some).
+template <int TYPE>
+constexpr float kCaLazy = TYPE == 0 ? 8.0f : 6.0f;
+template <int TYPE>
+constexpr float kCaUp = TYPE == 0 ? 0.0f : 8.0f;
+
+struct CaMaps {
+  CUtensorMap k, v;  // [pages * Hkv][64][D]
+};
+struct CaWork {
+  FastDiv by_g;
+  int ctas, rows_cap;  // rows of a workspace slot
+  int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
+  float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain
+  float* part_o;       // [2 * ctas][rows_cap][D] unnormalised sums
+};
+
+// One part of a CTA's run: tiles lo .. hi - 1 of the nt tiles of a unit.
+struct CaPart {
+  int b, at, past, kvh;
+  int row0, rows;    // the unit's rows (packed): row0 .. row0 + rows - 1
+  int tile0, nt;     // the unit's first tile and their number
+  int lo, hi;        // hi = 0: no more parts
+  int gw, gc;        // tiles gw .. gc - 1 of the part are seen whole by every row; the others are masked and guarded
+  int first_cut;     // cut units: the first CTA that begins inside this unit
+  int last_key;      // the last key that any row sees
+  int64_t u0, v;     // cut units: begin and extent in the split
+};
+struct CaSpecial {
+  int key0;
+  uint32_t keys[4];  // of the tile's 128: those with a value that is not finite
+};
+struct CaShared {
+  uint64_t full[12], free[12];
+  uint64_t s_full[2], p_full[2], o_full[2], fin[2];
+  uint64_t stat, read, stored, told;
+  uint64_t landed[kCaOk], ok[kCaOk];  // guarded values: in shared memory, looked through
+  uint64_t desc_full[kCaDesc], desc_free[kCaDesc], q_ready[kCaDesc];
+  CaPart part[kCaDesc];
+  int specials[kCaDesc];
+  CaSpecial special[kCaDesc][kCaSpecial];
+  uint32_t tmem;
+  int last;
+};
+
+template <int D>
+struct CaLayout {
+  static constexpr int kHalf = 128 * 128;  // 128 rows of 64 columns
+  static constexpr int kTile = D / 64 * kHalf;
+  static constexpr int kBufs = D == 128 ? 5 : 12;
+  static constexpr int kRingOff = 2 * kTile;
+  static constexpr int kSharedOff = kRingOff + kBufs * kTile;
+  static constexpr int kTotal = kSharedOff + (int)sizeof(CaShared) + 1024;  // + alignment
+  static_assert(kTotal <= 227 * 1024, "shared memory");
+  static_assert(kBufs <= 12 && kBufs / 2 < kCaOk, "rings");
+};
+
+// TMEM columns: the slots' scores (their weights over the first half) and sums
+__device__ __forceinline__ uint32_t ca_s_col(int t) { return 128u * (uint32_t)t; }
+__device__ __forceinline__ uint32_t ca_o_col(int t) { return 256u + 128u * (uint32_t)t; }
+
+// Bounded wait by a whole warp; false once it has run out.
+__device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
+  return mbar_wait(bar, parity, err);
 }
-template <>
-__device__ __forceinline__ float to_float(__half x) {
-  return __half2float(x);
-}
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half from_float(float x) {
-  return __float2half_rn(x);
+__device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
+  return mbar_try_wait(bar, parity, 1000u) || ca_wait_long(bar, parity, err);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kv16_attention_rows_kernel(const Kv16AttnParams p) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= (int64_t)p.T * p.H) return;
-  if (item == 0 && p.start)  // rows out of order are found wherever they are
-    for (int i = lane; i < p.B; i += 32)
-      if (p.start[i + 1] < p.start[i]) report_error(p.err, kErrInput);
-  const int row = (int)(item / p.H), h = (int)(item % p.H);
-  int b = 0, first = 0, last = 0;
-  for (; b < p.B; ++b) {
-    first = p.start ? p.start[b] : b * p.per;
-    last = p.start ? p.start[b + 1] : first + p.per;
-    if (row >= first && row < last) break;
+#if W4A16_TEST_HOOKS
+// Debug builds only: the producer of CTA 0 leaves out this buffer of its run (no
+// copy, no arrival), so that the bounded waits run out. -1: off.
+__device__ int g_test_skip_copy = -1;
+__device__ __forceinline__ bool test_skip_copy(uint32_t buf) {
+  return blockIdx.x == 0 && (int)buf == *(volatile int*)&g_test_skip_copy;
+}
+#else
+__device__ __forceinline__ bool test_skip_copy(uint32_t) { return false; }
+#endif
+
+// ------------------------------------------------------------------ the split
+
+// A request's rows: the first, their number (0 where it brings none or is not
+// valid), and the tokens before them.
+struct CaRequest {
+  int at, cnt, past;
+};
+__device__ __forceinline__ CaRequest ca_request(const Kv16AttnParams& p, int b, bool report) {
+  CaRequest r;
+  r.at = p.start ? p.start[b] : b * p.per;
+  const int end = p.start ? p.start[b + 1] : r.at + p.per;
+  r.cnt = 0;
+  r.past = 0;
+  if (r.at < 0 || end < r.at || end > p.T) {
+    if (report) report_error(p.err, kErrInput);
+    return r;
   }
-  if (b == p.B) return;
-  const int len = p.lens[b];
-  if (first < 0 || last > p.T || len < 0 || (int64_t)len + (last - first) > (int64_t)p.max_blocks * 64) {
-    if (lane == 0) report_error(p.err, kErrInput);
-    return;
+  if (end == r.at) return r;
+  r.past = p.lens[b];
+  if (r.past < 0 || (int64_t)r.past + (end - r.at) > (int64_t)p.max_blocks * 64) {
+    if (report) report_error(p.err, kErrInput);
+    return r;
   }
-  constexpr int E = D / 32;
-  const int pos = len + row - first, kvh = h / (p.H / p.Hkv);
-  const T* qr = static_cast<const T*>(p.q) + (int64_t)row * p.q_stride + (int64_t)h * D;
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_float<T>(qr[lane + 32 * e]) * p.scale_log2;
-    o[e] = 0.0f;
-  }
-  for (int j = p.window > 0 ? max(0, pos - p.window + 1) : 0; j <= pos; ++j) {
-    const int page = p.table[(int64_t)b * p.max_blocks + j / 64];
-    const bool there = page >= 0 && page < p.pages;
-    if (!there && lane == 0) report_error(p.err, kErrInput);
-    const int64_t at = (((int64_t)page * p.Hkv + kvh) * 64 + j % 64) * D;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      s += q[e] * (there ? to_float<T>(static_cast<const T*>(p.k)[at + lane + 32 * e]) : 0.0f);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    const float mx = fmaxf(m, s), c = exp2f(m - mx), w = exp2f(s - mx);
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * c + w * (there ? to_float<T>(static_cast<const T*>(p.v)[at + lane + 32 * e]) : 0.0f);
-    m = mx;
-  }
-  T* out = static_cast<T*>(p.out) + ((int64_t)row * p.H + h) * D;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = from_float<T>(o[e] / l);
+  r.cnt = end - r.at;
+  return r;
 }
 
-size_t kv16_attention_ws(int rows, int H, int Hkv, int D, int num_sms) { return 0; }
+// Estimated work of a request's units, per head: unit i has G (past + overhead) +
+// 256 (i + 1), the keys of its last row times G, times a weight, and no more
+// than a window's. Sums in closed form; every CTA computes the same numbers.
+struct CaLoad {
+  int64_t base, cap, overhead;
+  int units, weight, capped;  // from unit `capped` on the window's extent
+  __device__ __forceinline__ int64_t before(int i) const {  // units 0 .. i - 1
+    const int64_t m = i < capped ? i : capped;
+    return weight * (i * overhead + m * base + 128 * m * (m + 1) + (i - m) * cap);
+  }
+};
+__device__ __forceinline__ CaLoad ca_load(const Kv16AttnParams& p, const CaWork& wk, const CaRequest& r) {
+  const int G = (int)wk.by_g.d;
+  CaLoad w;
+  const int64_t rows = (int64_t)r.cnt * G;
+  w.units = (int)((rows + 255) / 256);
+  w.weight = rows > 128 ? kCaWeight2 : kCaWeight1;
+  w.base = (int64_t)G * r.past;
+  w.overhead = (int64_t)G * kCaOverhead;
+  w.cap = 0;
+  w.capped = w.units;
+  if (p.window > 0) {
+    w.cap = (int64_t)G * p.window + 256;
+    const int64_t n = w.cap > w.base ? (w.cap - w.base + 255) / 256 - 1 : 0;  // units below the cap
+    w.capped = n < w.units ? (int)n : w.units;
+  }
+  return w;
+}
+
+// The key tiles of a unit.
+struct CaTiles {
+  int first_pos, last_pos, tile0, nt;
+};
+__device__ __forceinline__ CaTiles ca_tiles(const Kv16AttnParams& p, const CaWork& wk, const CaRequest& r, int unit) {
+  const int row0 = unit * 256, rows = r.cnt * (int)wk.by_g.d;
+  CaTiles t;
+  t.first_pos = r.past + wk.by_g(row0);
+  t.last_pos = r.past + wk.by_g(min(row0 + 255, rows - 1));
+  t.tile0 = p.window > 0 ? max(0, t.first_pos - p.window + 1) / kCaKeys : 0;
+  t.nt = t.last_pos / kCaKeys + 1 - t.tile0;
+  return t;
+}
+
+// Where a run begins: tile `cut` of a unit.
+struct CaPlace {
+  int b, kvh, unit, cut;
+  int64_t u0, v;
+};
+// The place of x in request b, whose work begins at `at` (at <= x < its end).
+__device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, const CaRequest& r, int64_t at, int64_t x) {
+  const CaLoad w = ca_load(p, wk, r);
+  const int64_t head = w.before(w.units);
+  CaPlace o;
+  o.b = b;
+  o.kvh = (int)((x - at) / head);
+  at += o.kvh * head;
+  int lo = 0, hi = w.units;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w.before(mid) <= x - at)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  o.unit = lo;
+  o.u0 = at + w.before(lo);
+  o.v = w.before(lo + 1) - w.before(lo);
+  o.cut = (int)((x - o.u0) * ca_tiles(p, wk, r, lo).nt / o.v);
+  return o;
+}
+
+template <int TYPE>
+__device__ __forceinline__ uint32_t ca_pack(float lo, float hi) {
+  if constexpr (TYPE == 0) return pack_bf16_rn(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int TYPE>
+constexpr uint32_t kCaExp = TYPE == 0 ? 0x7F807F80u : 0x7C007C00u;
+template <int TYPE>
+constexpr uint32_t kCaExpUnit = TYPE == 0 ? 0x00800080u : 0x04000400u;
+// bit 15 and 31: the half's exponent is all ones (NaN or infinite)
+template <int TYPE>
+__device__ __forceinline__ uint32_t ca_not_finite(uint32_t w) {
+  return ((w & kCaExp<TYPE>)+kCaExpUnit<TYPE>)&0x80008000u;
+}
+
+// The values at `at` (D elements) that are not finite, added to an output row's columns c0 .. c0 + 31.
+template <int TYPE>
+__device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaShared* sh, int slot, int b, int kvh, int D,
+                                            int pos, int c0, uint32_t* ov) {
+  const int n = min(*(volatile const int*)&sh->specials[slot], kCaSpecial);
+  for (int e = 0; e < n; ++e) {
+    const CaSpecial& s = sh->special[slot][e];
+    for (int r = 0; r < kCaKeys; ++r) {
+      const int key = s.key0 + r;
+      if (!((s.keys[r >> 5] >> (r & 31)) & 1u) || key > pos || (p.window > 0 && key <= pos - p.window)) continue;
+      const int page = p.table[(int64_t)b * p.max_blocks + key / 64];
+      if (page < 0 || page >= p.pages) continue;
+      const uint16_t* v =
+          static_cast<const uint16_t*>(p.v) + (((int64_t)page * p.Hkv + kvh) * 64 + key % 64) * D + c0;
+      for (int c = 0; c < 32; ++c) {
+        const uint32_t bits = v[c];
+        if (!(ca_not_finite<TYPE>(bits) & 0x8000u)) continue;
+        const float x = TYPE == 0 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half((unsigned short)bits));
+        ov[c] = __float_as_uint(__uint_as_float(ov[c]) + x);
+      }
+    }
+  }
+}
+
+// The last position of slot t's rows, where the slots are row tiles.
+__device__ __forceinline__ int ca_slot_last(const CaWork& wk, const CaPart& d, int t) {
+  return d.past + wk.by_g(d.row0 + min(d.rows - 1, 128 * t + 127));
+}
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kCaThreads, 1)
+    kv16_attention_kernel(const __grid_constant__ CaMaps maps, const Kv16AttnParams p, const CaWork wk) {
+  using L = CaLayout<D>;
+  constexpr int NB = L::kBufs;
+  extern __shared__ uint8_t ca_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ca_smem) + 1023) & ~uintptr_t(1023));
+  CaShared* sh = reinterpret_cast<CaShared*>(smem + L::kSharedOff);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = (int)wk.by_g.d, C = wk.ctas, cta = (int)blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->free[i], 2);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->p_full[t], 4);
+      mbar_init(&sh->o_full[t], 1);
+      mbar_init(&sh->fin[t], 1);
+    }
+    mbar_init(&sh->stat, 4);
+    mbar_init(&sh->read, 4);
+    mbar_init(&sh->stored, 8);
+    mbar_init(&sh->told, 1);
+    for (int i = 0; i < kCaOk; ++i) {
+      mbar_init(&sh->landed[i], 1);
+      mbar_init(&sh->ok[i], 1);
+    }
+    for (int i = 0; i < kCaDesc; ++i) {
+      mbar_init(&sh->q_ready[i], 8);
+      mbar_init(&sh->desc_full[i], 1);
+      mbar_init(&sh->desc_free[i], 11);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem, 512u);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&maps.k);
+    tma_prefetch_map(&maps.v);
+  }
+  grid_dependency_wait();  // everything else in global memory may come from the kernels before
+
+  // ---- the run: CTA c takes the work from floor(W c / C) to floor(W (c + 1) / C).
+  // Each thread sums a row of requests; the scratch lies where Q will
+  struct Scratch {
+    int64_t sums[kCaThreads / 32];
+    CaPlace place[2];
+  };
+  Scratch* scr = reinterpret_cast<Scratch*>(smem);
+  const int per = (p.B + kCaThreads - 1) / kCaThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const CaRequest r = ca_request(p, b, cta == 0);
+    if (r.cnt > 0) {
+      const CaLoad w = ca_load(p, wk, r);
+      mine += p.Hkv * w.before(w.units);
+    }
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, upto, k);
+    if (lane >= k) upto += o;
+  }
+  if (lane == 31) scr->sums[warp] = upto;
+  if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1};
+  __syncthreads();
+  grid_launch_dependents();  // (TMEM is allocated: no later kernel can hold it while this one waits for it)
+  int64_t W = 0, at = upto - mine;
+  for (int w = 0; w < kCaThreads / 32; ++w) {
+    if (w < warp) at += scr->sums[w];
+    W += scr->sums[w];
+  }
+  auto bound = [&](int c) { return W * c / C; };
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    const int64_t x = bound(cta + e);
+    if (x < at || x >= at + mine) continue;
+    int64_t a = at;
+    for (int b = b0; b < b1; ++b) {
+      const CaRequest r = ca_request(p, b, false);
+      if (r.cnt == 0) continue;
+      const CaLoad w = ca_load(p, wk, r);
+      const int64_t n = p.Hkv * w.before(w.units);
+      if (x < a + n) {
+        scr->place[e] = ca_locate(p, wk, b, r, a, x);
+        break;
+      }
+      a += n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const CaPlace begin = scr->place[0], end = scr->place[1];
+  const uint32_t tmem = sh->tmem;
+  __syncthreads();  // the scratch becomes Q
+  // what part of a cut unit falls to CTA c: tiles cut_at(c) .. cut_at(c + 1) - 1
+  auto cut_at = [&](int c, int64_t u0, int64_t v, int nt) {
+    const int64_t x = bound(c);
+    return x <= u0 ? 0 : x >= u0 + v ? nt : (int)((x - u0) * nt / v);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------- parts and copies
+    uint32_t buf = 0, guarded = 0;
+    int seq = 0;
+    bool ok = true;
+    int b = begin.b, kvh = begin.kvh, unit = begin.unit;
+    bool first = true;
+    CaRequest r{0, 0, 0};
+    CaLoad w;
+    if (b < p.B) {
+      r = ca_request(p, b, false);
+      w = ca_load(p, wk, r);
+    }
+    while (ok && b < p.B) {
+      const bool at_end = b == end.b && kvh == end.kvh && unit == end.unit;
+      const CaTiles t = ca_tiles(p, wk, r, unit);
+      const int lo = first ? begin.cut : 0, hi = at_end ? end.cut : t.nt;
+      if (hi > lo) {
+        const int ds = seq % kCaDesc;
+        if (seq >= kCaDesc && !ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        // key tiles t with 128 t + 127 <= first_pos, and 128 t > last_pos - window, are seen whole by every row
+        const int whole = (t.first_pos + 1) / kCaKeys - t.tile0 - lo;
+        const int in_window =
+            p.window > 0 && t.last_pos >= p.window ? (t.last_pos - p.window) / kCaKeys + 1 - t.tile0 - lo : 0;
+        const int gw = min(max(in_window, 0), hi - lo), gc = max(min(whole, hi - lo), gw);
+        if (lane == 0) {
+          CaPart& d = sh->part[ds];
+          d.b = b;
+          d.at = r.at;
+          d.past = r.past;
+          d.kvh = kvh;
+          d.row0 = unit * 256;
+          d.rows = min(256, r.cnt * G - unit * 256);
+          d.tile0 = t.tile0;
+          d.nt = t.nt;
+          d.lo = lo;
+          d.hi = hi;
+          d.gw = gw;
+          d.gc = gc;
+          d.last_key = t.last_pos;
+          d.first_cut = 0;
+          if (lo > 0 || hi < t.nt) {
+            const CaPlace& c = first ? begin : end;
+            d.u0 = c.u0;
+            d.v = c.v;
+            int cs = (int)(c.u0 * C / W) + 1;  // the first CTA that begins after the unit's begin
+            while (bound(cs) <= c.u0) ++cs;
+            d.first_cut = cs;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->desc_full[ds]);
+        ++seq;
+        // the pages of 16 tiles at a time, a lane an entry; entries outside first .. last key are not read
+        const int blk_lo = (p.window > 0 ? max(0, t.first_pos - p.window + 1) : 0) / 64, blk_hi = t.last_pos / 64;
+        const int32_t* row = p.table + (int64_t)b * p.max_blocks;
+        int base = 2 * (t.tile0 + lo);
+        auto entry = [&](int blk) {
+          if (blk < blk_lo || blk > blk_hi) return -1;
+          const int page = in_bounds(p.err, blk, p.max_blocks) ? row[blk] : -1;
+          if (page >= 0 && page < p.pages) return page;
+          report_error(p.err, kErrInput);
+          return -1;
+        };
+        int now = base + lane < 2 * (t.tile0 + hi) ? entry(base + lane) : -1;
+        for (int i = lo; ok && i < hi; ++i) {
+          const int blk = 2 * (t.tile0 + i);
+          if (blk - base >= 32) {
+            base += 32;
+            now = base + lane < 2 * (t.tile0 + hi) ? entry(base + lane) : -1;
+          }
+          int z[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int page = __shfl_sync(0xffffffffu, now, blk - base + k);
+            z[k] = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++buf) {
+            const uint32_t s = buf % NB, use = buf / NB;
+            if (use > 0 && !ca_wait(&sh->free[s], (use - 1) & 1u, p.err)) {
+              ok = false;
+              break;
+            }
+            // guarded values land at a barrier of their own: the guard tells when they may be used
+            const bool guard = kv == 1 && (i - lo < gw || i - lo >= gc);
+            if (lane == 0 && !test_skip_copy(buf)) {
+              uint8_t* st = smem + L::kRingOff + s * L::kTile;
+              uint64_t* bar = guard ? &sh->landed[guarded % kCaOk] : &sh->full[s];
+              if (guard) mbar_arrive(&sh->full[s]);
+              mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(st + h * L::kHalf + k * 64 * 128, kv ? &maps.v : &maps.k, 64 * h, 0, z[k], bar);
+            }
+            guarded += guard;
+            __syncwarp();
+          }
+        }
+      }
+      if (at_end) break;
+      first = false;
+      if (++unit == w.units) {
+        unit = 0;
+        if (++kvh == p.Hkv) {
+          kvh = 0;
+          do {
+            if (++b == p.B) break;
+            r = ca_request(p, b, false);
+          } while (r.cnt == 0);
+          if (b < p.B) w = ca_load(p, wk, r);
+        }
+      }
+    }
+    // no more parts
+    const int ds = seq % kCaDesc;
+    if (ok && seq >= kCaDesc) ok = ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err);
+    if (ok && lane == 0) {
+      sh->part[ds].lo = 0;
+      sh->part[ds].hi = 0;
+      mbar_arrive(&sh->desc_full[ds]);
+    }
+    // the copies in flight land before the CTA exits (some may be, if a wait of another warp ran out)
+    for (uint32_t k = buf > NB ? buf - NB : 0; k < buf; ++k)
+      if (!test_skip_copy(k)) ca_wait(&sh->full[k % NB], (k / NB) & 1u, p.err);
+    for (uint32_t k = guarded > kCaOk ? guarded - kCaOk : 0; k < guarded; ++k)
+      ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err);
+  } else if (warp <= 2) {
+    // ------------------------------------------------------ MMA, slot t
+    const int t = warp - 1;
+    constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
+    const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
+    uint32_t buf = 0, pc = 0, oks = 0;
+    bool ok = true, issued = false;
+    for (int seq = 0; ok; ++seq) {
+      const int ds = seq % kCaDesc;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      const CaPart& d = sh->part[ds];
+      const int n = d.hi - d.lo, gw = d.gw, gc = d.gc;
+      if (n <= 0) break;
+      const bool two = d.rows > 128;
+      // this slot's tiles: as far as its rows see where the slots are row tiles, every other one where they share the rows
+      int upto = n;
+      if (two) upto = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
+      const int step = two ? 1 : 2;
+      int i = two ? 0 : t, at = 0;
+      const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kTile);
+      // Each slot releases every buffer once, in order: those it does not use as soon as they are there.
+      auto pass = [&](int to) {
+        for (; at < to; ++at)
+          for (uint32_t x = buf + 2u * (uint32_t)at, e = x + 2u; x < e; ++x) {
+            if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+            if (lane == 0) mbar_arrive(&sh->free[x % NB]);
+            __syncwarp();
+          }
+        return true;
+      };
+      auto scores = [&]() {
+        if (!pass(i)) return false;
+        const uint32_t x = buf + 2u * (uint32_t)i;
+        if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+        tc_fence_after();
+        const uint32_t k0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3));
+          umma_bf16_ss_warp(tmem + ca_s_col(t), umma_desc_sw128_kmajor(q0 + off), umma_desc_sw128_kmajor(k0 + off),
+                            idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_warp(&sh->s_full[t]);
+        umma_commit_warp(&sh->free[x % NB]);
+        issued = true;
+        return true;
+      };
+      if (i < upto) ok = ca_wait(&sh->q_ready[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
+      for (bool first = true; ok && i < upto; first = false) {
+        const uint32_t x = buf + 2u * (uint32_t)i + 1u;
+        if (!ca_wait(&sh->p_full[t], pc++ & 1u, p.err) || !ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        if (i < gw || i >= gc) {  // the guard has looked through the values
+          const uint32_t g = oks + (uint32_t)(i < gw ? i : gw + i - gc);
+          if (!ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+        }
+        tc_fence_after();
+        const uint32_t v0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kCaKeys / 16; ++kk)
+          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t) + 8u * (uint32_t)kk,
+                            umma_desc_sw128_mnmajor(v0 + 2048u * (uint32_t)kk, (uint32_t)L::kHalf, 1024u), idesc_o,
+                            (!first || kk > 0) ? 1u : 0u);
+        umma_commit_warp(&sh->free[x % NB]);
+        at = i + 1;
+        i += step;
+        if (i < upto)
+          ok = scores();
+        else
+          umma_commit_warp(&sh->o_full[t]);
+      }
+      ok = ok && pass(n);
+      buf += 2u * (uint32_t)n;
+      oks += (uint32_t)(gw + n - gc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
+    }
+    if (issued) {
+      umma_commit_warp(&sh->fin[t]);  // tracks all of this warp's MMAs
+      ca_wait(&sh->fin[t], 0u, p.err);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ guard
+    uint32_t buf = 0, oks = 0;
+    bool ok = true;
+    for (int seq = 0; ok; ++seq) {
+      const int ds = seq % kCaDesc;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      const CaPart& d = sh->part[ds];
+      const int lo = d.lo, n = d.hi - lo, gw = d.gw, gc = d.gc, tile0 = d.tile0, last_key = d.last_key;
+      if (n <= 0) break;
+      if (lane == 0) *(volatile int*)&sh->specials[ds] = 0;
+      __syncwarp();
+      for (int i = gw > 0 ? 0 : gc; ok && i < n; i = i + 1 < gw || i + 1 >= gc ? i + 1 : gc) {
+        const uint32_t x = buf + 2u * (uint32_t)i + 1u;
+        if (!ca_wait(&sh->landed[oks % kCaOk], (oks / kCaOk) & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        uint8_t* v0 = smem + L::kRingOff + (x % NB) * L::kTile;
+        uint32_t any = 0;
+#pragma unroll 8
+        for (int o = lane * 16; o < L::kTile; o += 512) {
+          const uint4 w = *reinterpret_cast<const uint4*>(v0 + o);
+          any |= ca_not_finite<TYPE>(w.x) | ca_not_finite<TYPE>(w.y) | ca_not_finite<TYPE>(w.z) |
+                 ca_not_finite<TYPE>(w.w);
+        }
+        if (__any_sync(0xffffffffu, any != 0u)) {
+          const int e = *(volatile int*)&sh->specials[ds];
+          CaSpecial& sp = sh->special[ds][min(e, kCaSpecial - 1)];
+          if (lane < 4) sp.keys[lane] = 0u;
+          if (lane == 4) sp.key0 = (tile0 + lo + i) * kCaKeys;
+          __syncwarp();
+          for (int o = lane * 4; o < L::kTile; o += 128) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(v0 + o);
+            const uint32_t bad = ca_not_finite<TYPE>(*w);
+            if (!bad) continue;
+            const int r = (o % L::kHalf) / 128;
+            if ((tile0 + lo + i) * kCaKeys + r <= last_key) atomicOr(&sp.keys[r >> 5], 1u << (r & 31));
+            *w &= ~((bad >> 15) * 0xFFFFu);
+          }
+          fence_proxy_async_smem();
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) *(volatile int*)&sh->specials[ds] = min(e + 1, kCaSpecial);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ok[oks % kCaOk]);
+        ++oks;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
+      buf += 2u * (uint32_t)n;
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    const int t = (warp - 4) >> 2, qd = warp & 3, rl = qd * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
+    uint32_t sc = 0, oc = 0, shared_parts = 0, cut_parts = 0;
+    bool ok = true;
+    for (int seq = 0; ok; ++seq) {
+      const int ds = seq % kCaDesc;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      const CaPart& d = sh->part[ds];
+      const int lo = d.lo, n = d.hi - lo, rows = d.rows, past = d.past;
+      if (n <= 0) break;
+      const bool two = rows > 128;
+      const int ur = (two ? 128 * t : 0) + rl;  // row of the unit
+      const bool valid = ur < rows;
+      const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = past + j;
+      const int head = d.kvh * G + R - j * G;
+      if (two || t == 0) {  // this row of Q: 128-byte swizzle, K-major, halves of 64 columns
+        uint8_t* qt = smem + t * L::kTile;
+        const int64_t qi = (int64_t)(d.at + j) * p.q_stride + (int64_t)head * D;
+        const bool qok = valid && in_bounds(p.err, d.at + j, p.T);
+        uint4 v[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          v[c] = qok ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + qi + c * 8)
+                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * L::kHalf + rl * 128 + (((c & 7) ^ (rl & 7)) << 4)) = v[c];
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_ready[ds]);
+      int nt = (n - t + 1) / 2;
+      if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - lo, 0), n);
+      const int gw = d.gw, gc = d.gc, key_base = (d.tile0 + lo) * kCaKeys;
+      const bool any_row = __any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.0f;
+      for (int jt = 0; ok && jt < nt; ++jt) {
+        const int i = two ? jt : 2 * jt + t;
+        if (!ca_wait(&sh->s_full[t], sc++ & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        if (!any_row) {  // (what the weights of these rows are does not matter)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[t]);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(trow + ca_s_col(t) + 32u * (uint32_t)h, sv[h]);
+        tmem_wait_ld();
+        if (i < gw || i >= gc) {
+          const int key0 = key_base + i * kCaKeys;
+          const int top = pos - key0, bottom = p.window > 0 ? top - p.window : -1;  // seen: bottom < c <= top
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (32 * h + c > top || 32 * h + c <= bottom) sv[h][c] = __float_as_uint(-INFINITY);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        float cf = 1.0f;
+        if (mx > m + kCaLazy<TYPE>) {
+          cf = m == -INFINITY ? 0.0f : ex2(m - mx);
+          m = mx;
+          l *= cf;
+        }
+        if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
+          // O holds the sums of the tiles before: the commit that announced these scores covers their MMAs
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * cf);
+            tmem_st_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+          }
+        }
+        const float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nu2 = f2_pack(-u, -u);
+        uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pr[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t* s2 = &sv[2 * h + (c >> 4)][2 * (c & 15)];
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, nu2), x0, x1);
+            const float e0 = ex2(x0), e1 = ex2(x1);
+            pr[c] = ca_pack<TYPE>(e0, e1);
+            const uint64_t r2 = f2_pack(e0, e1);
+            if (c & 1)
+              lb = f2_add(lb, r2);
+            else
+              la = f2_add(la, r2);
+          }
+          tmem_st_32x32b_x32(trow + ca_s_col(t) + 32u * (uint32_t)h, pr);
+        }
+        {
+          float a0, a1, c0, c1;
+          f2_unpack(la, a0, a1);
+          f2_unpack(lb, c0, c1);
+          l += (a0 + a1) + (c0 + c1);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[t]);
+      }
+      // ---- the part's end
+      if (ok && nt > 0) ok = ca_wait(&sh->o_full[t], oc++ & 1u, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
+      if (!two) {
+        if (t == 1) {  // hand over the reference and the sum through TMEM; the sums are there
+          uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
+          tmem_st_32x32b_x8(trow + ca_s_col(1), st);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->stat);
+        } else {
+          if (!ca_wait(&sh->stat, shared_parts & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t st[8];
+          tmem_ld_32x32b_x8(trow + ca_s_col(1), st);
+          tmem_wait_ld();
+          const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
+          if (n > 1 && !(l1 == 0.0f)) {
+            const float M = fmaxf(m, m1);
+            a0 = l == 0.0f ? 0.0f : ex2(m - M);
+            a1 = ex2(m1 - M);
+            l = l * a0 + l1 * a1;
+            m = M;
+          }
+        }
+      }
+      const bool mine_to_store = two || t == 0;
+      const bool cut = n < d.nt;
+      const int64_t slot = 2 * cta + (lo > 0 ? 0 : 1);
+      if (mine_to_store && any_row) {
+        const float il = 1.0f / l;
+        const int64_t oi = ((int64_t)(d.at + j) * p.H + head) * D;
+        const int64_t pi = slot * wk.rows_cap + ur;
+        const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
+        const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
+        const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
+        const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32];
+          if (nt > 0) {
+            tmem_ld_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] = 0u;
+          }
+          if (other) {
+            uint32_t ow[32];
+            tmem_ld_32x32b_x32(trow + ca_o_col(1) + (uint32_t)c0, ow);
+            tmem_wait_ld();
+            if (a1 != 0.0f) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                ov[c] = __float_as_uint(__uint_as_float(ov[c]) * a0 + __uint_as_float(ow[c]) * a1);
+            }
+          }
+          if (specials && valid) {
+            uint32_t tmp[32];  // (not ov itself: its address would put it in memory)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) tmp[c] = ov[c];
+            ca_add_special<TYPE>(p, sh, ds, d.b, d.kvh, D, pos, c0, tmp);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] = tmp[c];
+          }
+          if (!st_ok) continue;
+          if (cut) {
+            float* dst = wk.part_o + pi * D + c0;
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<float4*>(dst + c) = make_float4(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1]),
+                                                                __uint_as_float(ov[c + 2]), __uint_as_float(ov[c + 3]));
+          } else {
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + oi + c0;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              uint4 w;
+              w.x = ca_pack<TYPE>(__uint_as_float(ov[c]) * il, __uint_as_float(ov[c + 1]) * il);
+              w.y = ca_pack<TYPE>(__uint_as_float(ov[c + 2]) * il, __uint_as_float(ov[c + 3]) * il);
+              w.z = ca_pack<TYPE>(__uint_as_float(ov[c + 4]) * il, __uint_as_float(ov[c + 5]) * il);
+              w.w = ca_pack<TYPE>(__uint_as_float(ov[c + 6]) * il, __uint_as_float(ov[c + 7]) * il);
+              *reinterpret_cast<uint4*>(dst + c) = w;
+            }
+          }
+        }
+        if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
+      }
+      if (!two) {  // slot 1's scores and sums may be written again
+        if (t == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->read);
+        } else if (!ca_wait(&sh->read, shared_parts & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        ++shared_parts;
+      }
+      tc_fence_before();
+      if (cut) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->stored);
+        if (warp == 4) {
+          if (!ca_wait(&sh->stored, cut_parts & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            int* done = wk.done + (in_bounds(p.err, d.first_cut, C) ? d.first_cut : 0);
+            const bool last = atomic_add_acq_rel(done, n) + n == d.nt;
+            if (last) *done = 0;
+            *(volatile int*)&sh->last = last ? 1 : 0;
+            mbar_arrive(&sh->told);
+          }
+          __syncwarp();
+        }
+        if (!ca_wait(&sh->told, cut_parts & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        ++cut_parts;
+        if (*(volatile int*)&sh->last) {
+          // the unit's pieces, merged in the order of the keys: a row's D / 4 quads of columns by as many threads
+          __threadfence();
+          constexpr int Q = D / 4;
+          const int c_first = d.first_cut - 1;
+          for (int item = tid - 128; item < (rows * Q + 31) / 32 * 32; item += 256) {
+            const int rr = item / Q, col = 4 * (item % Q);
+            const bool live = rr < rows;
+            float M = -INFINITY, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+              for (int cb = c_first; cb < C && bound(cb) < d.u0 + d.v; cb += 32) {
+                const int c = cb + lane;
+                const int from = cut_at(min(c, C), d.u0, d.v, d.nt), to = cut_at(min(c + 1, C), d.u0, d.v, d.nt);
+                unsigned list = __ballot_sync(0xffffffffu, to > from);
+                const unsigned heads = __ballot_sync(0xffffffffu, from == 0);
+                for (; list; list &= list - 1) {
+                  const int k = __ffs(list) - 1;
+                  const int64_t row = (int64_t)(2 * (cb + k) + (int)((heads >> k) & 1u)) * wk.rows_cap + rr;
+                  if (!live) continue;
+                  const float2 ml = __ldcg(&wk.part_ml[row]);
+                  if (ml.y == 0.0f) continue;  // none of the piece's keys is seen
+                  if (pass == 0) {
+                    M = fmaxf(M, ml.x);
+                  } else {
+                    const float f = ex2(ml.x - M);
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(wk.part_o + row * D + col));
+                    sum += f * ml.y;
+                    acc[0] += f * o.x;
+                    acc[1] += f * o.y;
+                    acc[2] += f * o.z;
+                    acc[3] += f * o.w;
+                  }
+                }
+              }
+            }
+            if (!live) continue;
+            const int R2 = d.row0 + rr, j2 = wk.by_g(R2);
+            const float inv = 1.0f / sum;
+            if (in_bounds(p.err, d.at + j2, p.T)) {
+              uint2 w;
+              w.x = ca_pack<TYPE>(acc[0] * inv, acc[1] * inv);
+              w.y = ca_pack<TYPE>(acc[2] * inv, acc[3] * inv);
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                        ((int64_t)(d.at + j2) * p.H + d.kvh * G + R2 - j2 * G) * D + col) = w;
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
+    }
+  }
+
+  // ---------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512u);
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct CaPlan {
+  int ctas, rows_cap;
+  size_t done_bytes, ml_bytes, total;
+};
+static CaPlan ca_plan(int T, int H, int Hkv, int D, int num_sms) {
+  CaPlan k;
+  k.ctas = num_sms > 0 ? num_sms : 1;
+  const int64_t rows = (int64_t)T * (H / Hkv);
+  k.rows_cap = rows < 256 ? (int)rows : 256;
+  k.done_bytes = ((size_t)k.ctas * 4 + 255) / 256 * 256;
+  k.ml_bytes = ((size_t)2 * k.ctas * k.rows_cap * 8 + 255) / 256 * 256;
+  k.total = k.done_bytes + k.ml_bytes + (size_t)2 * k.ctas * k.rows_cap * D * 4;
+  return k;
+}
+
+size_t kv16_attention_ws(int T, int H, int Hkv, int D, int num_sms) { return ca_plan(T, H, Hkv, D, num_sms).total; }
+
+// The split's numbers stay below 2^55 (times the CTAs: 2^63), a unit's work times its tiles too.
+bool kv16_attention_fits(int T, int B, int H, int Hkv, int max_blocks) {
+  const double G = H / Hkv, units = (double)T * H / 256 + (double)B * Hkv;
+  return G <= 1024 && max_blocks <= (1 << 21) &&
+         units * kCaWeight2 * (G * (64.0 * max_blocks + kCaOverhead) + 256.0) < 36028797018963968.0;
+}
+
+template <int TYPE, int D>
+static cudaError_t launch_ca(const CaMaps& maps, const Kv16AttnParams& p, const CaWork& wk, cudaStream_t stream) {
+  constexpr int smem = CaLayout<D>::kTotal;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv16_attention_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv16_attention_kernel<TYPE, D>, dim3((unsigned)wk.ctas), dim3(kCaThreads), (size_t)smem, stream, maps,
+                    p, wk);
+}
 
 cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void* workspace, int num_sms,
                                   cudaStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)p.T * p.H + 3) / 4)), block(128);
-  if (type == 0)
-    return D == 128 ? launch_pdl(kv16_attention_rows_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, p)
-                    : launch_pdl(kv16_attention_rows_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, p);
-  return D == 128 ? launch_pdl(kv16_attention_rows_kernel<__half, 128>, grid, block, 0, stream, p)
-                  : launch_pdl(kv16_attention_rows_kernel<__half, 64>, grid, block, 0, stream, p);
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+  if (!encode) return cudaErrorNotSupported;
+  const CaPlan k = ca_plan(p.T, p.H, p.Hkv, D, num_sms);
+  CaMaps maps;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, 64, (cuuint64_t)p.pages * p.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 128};
+  const cuuint32_t box[3] = {64u, 64u, 1u}, es[3] = {1u, 1u, 1u};
+  for (int c = 0; c < 2; ++c)
+    if (encode(c ? &maps.v : &maps.k, type == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void*>(c ? p.v : p.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  CaWork wk;
+  wk.by_g = fast_div((uint32_t)(p.H / p.Hkv));
+  wk.ctas = k.ctas;
+  wk.rows_cap = k.rows_cap;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  wk.done = reinterpret_cast<int*>(ws);
+  wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
+  wk.part_o = reinterpret_cast<float*>(ws + k.done_bytes + k.ml_bytes);
+  if (D == 128)
+    return type == 0 ? launch_ca<0, 128>(maps, p, wk, stream) : launch_ca<1, 128>(maps, p, wk, stream);
+  return type == 0 ? launch_ca<0, 64>(maps, p, wk, stream) : launch_ca<1, 64>(maps, p, wk, stream);
 }
 
 }  // namespace w4a16
+
+#if W4A16_TEST_HOOKS
+// Debug builds only (not part of the C ABI header): see g_test_skip_copy.
+extern "C" int w4a16_test_set_skip_copy(int buf) {
+  return (int)cudaMemcpyToSymbol(w4a16::g_test_skip_copy, &buf, sizeof(int));
+}
+#endif
