@@ -40,10 +40,10 @@
 namespace w4a16 {
 
 constexpr int kCaThreads = 384;
-constexpr int kCaKeys = 128;  // keys of a tile: two pages
+constexpr int kCaKeys = 64;   // keys of a tile: a page
 constexpr int kCaDesc = 4;    // parts described ahead
-constexpr int kCaOk = 8;      // guarded tiles that the guard may be ahead: more than the ring holds
-constexpr int kCaSpecial = 10;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
+constexpr int kCaOk = 16;     // guarded tiles that the guard may be ahead: more than the ring holds
+constexpr int kCaSpecial = 12;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
 
 // The weights a key tile has in the split: two row tiles, or one.
 constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
@@ -64,6 +64,7 @@ struct CaMaps {
 struct CaWork {
   FastDiv by_g;
   int ctas, rows_cap;  // rows of a workspace slot
+  uint64_t ctas_inv;   // floor(2^64 / ctas)
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
   float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain
   float* part_o;       // [2 * ctas][rows_cap][D] unnormalised sums
@@ -82,14 +83,14 @@ struct CaPart {
 };
 struct CaSpecial {
   int key0;
-  uint32_t keys[4];  // of the tile's 128: those with a value that is not finite
+  uint32_t keys[2];  // of the tile's 64: those with a value that is not finite
 };
 struct CaShared {
-  uint64_t full[12], free[12];
-  uint64_t s_full[2], p_full[2], o_full[2], fin[2];
+  uint64_t full[20], free[20];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], fin[2];
   uint64_t stat, read, stored, told;
   uint64_t landed[kCaOk], ok[kCaOk];  // guarded values: in shared memory, looked through
-  uint64_t desc_full[kCaDesc], desc_free[kCaDesc], q_ready[kCaDesc];
+  uint64_t desc_full[kCaDesc], desc_free[kCaDesc], q_ready[2][kCaDesc];
   CaPart part[kCaDesc];
   int specials[kCaDesc];
   CaSpecial special[kCaDesc][kCaSpecial];
@@ -99,19 +100,33 @@ struct CaShared {
 
 template <int D>
 struct CaLayout {
-  static constexpr int kHalf = 128 * 128;  // 128 rows of 64 columns
+  static constexpr int kQHalf = 128 * 128;  // 128 rows of 64 columns
+  static constexpr int kQ = D / 64 * kQHalf;
+  static constexpr int kHalf = kCaKeys * 128;  // 64 keys of 64 columns
   static constexpr int kTile = D / 64 * kHalf;
-  static constexpr int kBufs = D == 128 ? 5 : 12;
-  static constexpr int kRingOff = 2 * kTile;
+  static constexpr int kBufs = D == 128 ? 10 : 20;
+  static constexpr int kRingOff = 2 * kQ;
   static constexpr int kSharedOff = kRingOff + kBufs * kTile;
   static constexpr int kTotal = kSharedOff + (int)sizeof(CaShared) + 1024;  // + alignment
   static_assert(kTotal <= 227 * 1024, "shared memory");
-  static_assert(kBufs <= 12 && kBufs / 2 < kCaOk, "rings");
+  static_assert(kBufs <= 20 && kBufs / 2 < kCaOk, "rings");
 };
 
-// TMEM columns: the slots' scores (their weights over the first half) and sums
-__device__ __forceinline__ uint32_t ca_s_col(int t) { return 128u * (uint32_t)t; }
+// TMEM columns: a slot's two score buffers (the weights over the first half of one) and its sums
+__device__ __forceinline__ uint32_t ca_s_col(int t, int sb) { return 128u * (uint32_t)t + 64u * (uint32_t)sb; }
 __device__ __forceinline__ uint32_t ca_o_col(int t) { return 256u + 128u * (uint32_t)t; }
+
+// 16 bytes to shared memory, asynchronously; zeros where there are none.
+__device__ __forceinline__ void ca_copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void ca_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int N>
+struct CaInt {
+  static constexpr int value = N;
+};
 
 // Bounded wait by a whole warp; false once it has run out.
 __device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
@@ -133,6 +148,19 @@ __device__ __forceinline__ bool test_skip_copy(uint32_t) { return false; }
 #endif
 
 // ------------------------------------------------------------------ the split
+
+// floor(a / b) for 0 <= a, b > 0 and a quotient below 2^22 (the fp32 estimate is
+// off by less than one half then, and put right), and of a * n / b for a < b.
+__device__ __forceinline__ int ca_fix(int q, int64_t a, int64_t b) {
+  int64_t r = a - q * b;
+  while (r < 0) r += b, --q;
+  while (r >= b) r -= b, ++q;
+  return q;
+}
+__device__ __forceinline__ int ca_quotient(int64_t a, int64_t b) { return ca_fix((int)((float)a / (float)b), a, b); }
+__device__ __forceinline__ int ca_share(int64_t a, int n, int64_t b) {
+  return ca_fix((int)((float)a / (float)b * (float)n), a * n, b);
+}
 
 // A request's rows: the first, their number (0 where it brings none or is not
 // valid), and the tokens before them.
@@ -213,7 +241,7 @@ __device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, c
   const int64_t head = w.before(w.units);
   CaPlace o;
   o.b = b;
-  o.kvh = (int)((x - at) / head);
+  o.kvh = ca_quotient(x - at, head);
   at += o.kvh * head;
   int lo = 0, hi = w.units;
   while (hi - lo > 1) {
@@ -226,7 +254,7 @@ __device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, c
   o.unit = lo;
   o.u0 = at + w.before(lo);
   o.v = w.before(lo + 1) - w.before(lo);
-  o.cut = (int)((x - o.u0) * ca_tiles(p, wk, r, lo).nt / o.v);
+  o.cut = ca_share(x - o.u0, ca_tiles(p, wk, r, lo).nt, o.v);
   return o;
 }
 
@@ -292,9 +320,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       mbar_init(&sh->free[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh->s_full[t], 1);
-      mbar_init(&sh->p_full[t], 4);
-      mbar_init(&sh->o_full[t], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&sh->s_full[t][k], 1);
+        mbar_init(&sh->p_full[t][k], 4);
+        mbar_init(&sh->pv_done[t][k], 1);
+      }
       mbar_init(&sh->fin[t], 1);
     }
     mbar_init(&sh->stat, 4);
@@ -306,7 +336,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       mbar_init(&sh->ok[i], 1);
     }
     for (int i = 0; i < kCaDesc; ++i) {
-      mbar_init(&sh->q_ready[i], 8);
+      for (int t = 0; t < 2; ++t) mbar_init(&sh->q_ready[t][i], 4);
       mbar_init(&sh->desc_full[i], 1);
       mbar_init(&sh->desc_free[i], 11);
     }
@@ -322,7 +352,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   }
   grid_dependency_wait();  // everything else in global memory may come from the kernels before
 
-  // ---- the run: CTA c takes the work from floor(W c / C) to floor(W (c + 1) / C).
+  // ---- the run: CTA c of C takes the work from about W c / C to W (c + 1) / C.
   // Each thread sums a row of requests; the scratch lies where Q will
   struct Scratch {
     int64_t sums[kCaThreads / 32];
@@ -354,7 +384,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (w < warp) at += scr->sums[w];
     W += scr->sums[w];
   }
-  auto bound = [&](int c) { return W * c / C; };
+  auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, wk.ctas_inv * (uint64_t)c); };
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const int64_t x = bound(cta + e);
@@ -381,7 +411,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // what part of a cut unit falls to CTA c: tiles cut_at(c) .. cut_at(c + 1) - 1
   auto cut_at = [&](int c, int64_t u0, int64_t v, int nt) {
     const int64_t x = bound(c);
-    return x <= u0 ? 0 : x >= u0 + v ? nt : (int)((x - u0) * nt / v);
+    return x <= u0 ? 0 : x >= u0 + v ? nt : ca_share(x - u0, nt, v);
   };
 
   if (warp == 0) {
@@ -407,7 +437,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           ok = false;
           break;
         }
-        // key tiles t with 128 t + 127 <= first_pos, and 128 t > last_pos - window, are seen whole by every row
+        // key tiles t with 64 t + 63 <= first_pos, and 64 t > last_pos - window, are seen whole by every row
         const int whole = (t.first_pos + 1) / kCaKeys - t.tile0 - lo;
         const int in_window =
             p.window > 0 && t.last_pos >= p.window ? (t.last_pos - p.window) / kCaKeys + 1 - t.tile0 - lo : 0;
@@ -428,42 +458,40 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           d.gc = gc;
           d.last_key = t.last_pos;
           d.first_cut = 0;
-          if (lo > 0 || hi < t.nt) {
-            const CaPlace& c = first ? begin : end;
-            d.u0 = c.u0;
-            d.v = c.v;
-            int cs = (int)(c.u0 * C / W) + 1;  // the first CTA that begins after the unit's begin
-            while (bound(cs) <= c.u0) ++cs;
-            d.first_cut = cs;
+          d.u0 = first ? begin.u0 : end.u0;
+          d.v = first ? begin.v : end.v;
+        }
+        if (lo > 0 || hi < t.nt) {  // the first CTA that begins after the unit's begin, looked for from here downwards
+          int cs = cta + 1;
+          while (true) {
+            const unsigned later = __ballot_sync(0xffffffffu, cs - lane >= 1 && bound(cs - lane) > (first ? begin.u0 : end.u0));
+            const int n = later == 0xffffffffu ? 32 : __ffs(~later) - 1;
+            cs -= n;
+            if (n < 32) break;
           }
+          if (lane == 0) sh->part[ds].first_cut = cs + 1;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->desc_full[ds]);
         ++seq;
-        // the pages of 16 tiles at a time, a lane an entry; entries outside first .. last key are not read
-        const int blk_lo = (p.window > 0 ? max(0, t.first_pos - p.window + 1) : 0) / 64, blk_hi = t.last_pos / 64;
+        // the pages of 32 tiles at a time, a lane an entry
         const int32_t* row = p.table + (int64_t)b * p.max_blocks;
-        int base = 2 * (t.tile0 + lo);
-        auto entry = [&](int blk) {
-          if (blk < blk_lo || blk > blk_hi) return -1;
-          const int page = in_bounds(p.err, blk, p.max_blocks) ? row[blk] : -1;
+        int base = t.tile0 + lo;
+        auto entries = [&]() {
+          if (base + lane >= t.tile0 + hi || !in_bounds(p.err, base + lane, p.max_blocks)) return -1;
+          const int page = row[base + lane];
           if (page >= 0 && page < p.pages) return page;
           report_error(p.err, kErrInput);
           return -1;
         };
-        int now = base + lane < 2 * (t.tile0 + hi) ? entry(base + lane) : -1;
+        int now = entries();
         for (int i = lo; ok && i < hi; ++i) {
-          const int blk = 2 * (t.tile0 + i);
-          if (blk - base >= 32) {
+          if (t.tile0 + i - base >= 32) {
             base += 32;
-            now = base + lane < 2 * (t.tile0 + hi) ? entry(base + lane) : -1;
+            now = entries();
           }
-          int z[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int page = __shfl_sync(0xffffffffu, now, blk - base + k);
-            z[k] = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
-          }
+          const int page = __shfl_sync(0xffffffffu, now, t.tile0 + i - base);
+          const int z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++buf) {
             const uint32_t s = buf % NB, use = buf / NB;
@@ -479,10 +507,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
               if (guard) mbar_arrive(&sh->full[s]);
               mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                  tma_load_3d(st + h * L::kHalf + k * 64 * 128, kv ? &maps.v : &maps.k, 64 * h, 0, z[k], bar);
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(st + h * L::kHalf, kv ? &maps.v : &maps.k, 64 * h, 0, z, bar);
             }
             guarded += guard;
             __syncwarp();
@@ -521,7 +547,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const int t = warp - 1;
     constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
     const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
-    uint32_t buf = 0, pc = 0, oks = 0;
+    uint32_t buf = 0, oks = 0;
+    uint32_t sc = 0, pc = 0;  // score tiles issued and weights used so far: buffer and phase
     bool ok = true, issued = false;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -534,9 +561,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       int upto = n;
       if (two) upto = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
       const int step = two ? 1 : 2;
-      int i = two ? 0 : t, at = 0;
-      const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kTile);
-      // Each slot releases every buffer once, in order: those it does not use as soon as they are there.
+      int i = two ? 0 : t;  // the tile whose scores come next
+      int at = 0;           // tiles before it are used or passed over
+      const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kQ);
+      // Each slot releases every buffer once: those it does not use as soon as they are there.
       auto pass = [&](int to) {
         for (; at < to; ++at)
           for (uint32_t x = buf + 2u * (uint32_t)at, e = x + 2u; x < e; ++x) {
@@ -552,26 +580,33 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
         tc_fence_after();
         const uint32_t k0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
+        const int sb = (int)(sc & 1u);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3));
-          umma_bf16_ss_warp(tmem + ca_s_col(t), umma_desc_sw128_kmajor(q0 + off), umma_desc_sw128_kmajor(k0 + off),
-                            idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_warp(&sh->s_full[t]);
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_ss_warp(tmem + ca_s_col(t, sb),
+                            umma_desc_sw128_kmajor(q0 + (uint32_t)((kk >> 2) * L::kQHalf + 32 * (kk & 3))),
+                            umma_desc_sw128_kmajor(k0 + (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3))), idesc_s,
+                            kk > 0 ? 1u : 0u);
+        umma_commit_warp(&sh->s_full[t][sb]);
         umma_commit_warp(&sh->free[x % NB]);
         issued = true;
+        ++sc;
+        at = i + 1;
+        i += step;
         return true;
       };
-      if (i < upto) ok = ca_wait(&sh->q_ready[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
-      for (bool first = true; ok && i < upto; first = false) {
-        const uint32_t x = buf + 2u * (uint32_t)i + 1u;
-        if (!ca_wait(&sh->p_full[t], pc++ & 1u, p.err) || !ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) {
+      if (i < upto) ok = ca_wait(&sh->q_ready[two ? t : 0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
+      if (ok && i < upto) ok = scores();
+      // the scores two tiles on go out once the weights of a tile, which lie in their buffer, are used
+      for (int v = two ? 0 : t; ok && v < upto; v += step) {
+        const uint32_t x = buf + 2u * (uint32_t)v + 1u;
+        const int sb = (int)(pc & 1u);
+        if (!ca_wait(&sh->p_full[t][sb], (pc >> 1) & 1u, p.err) || !ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) {
           ok = false;
           break;
         }
-        if (i < gw || i >= gc) {  // the guard has looked through the values
-          const uint32_t g = oks + (uint32_t)(i < gw ? i : gw + i - gc);
+        if (v < gw || v >= gc) {  // the guard has looked through the values
+          const uint32_t g = oks + (uint32_t)(v < gw ? v : gw + v - gc);
           if (!ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err)) {
             ok = false;
             break;
@@ -581,16 +616,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const uint32_t v0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < kCaKeys / 16; ++kk)
-          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t) + 8u * (uint32_t)kk,
+          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, sb) + 8u * (uint32_t)kk,
                             umma_desc_sw128_mnmajor(v0 + 2048u * (uint32_t)kk, (uint32_t)L::kHalf, 1024u), idesc_o,
-                            (!first || kk > 0) ? 1u : 0u);
+                            (v >= step || kk > 0) ? 1u : 0u);
+        umma_commit_warp(&sh->pv_done[t][sb]);
         umma_commit_warp(&sh->free[x % NB]);
-        at = i + 1;
-        i += step;
-        if (i < upto)
-          ok = scores();
-        else
-          umma_commit_warp(&sh->o_full[t]);
+        ++pc;
+        if (i < upto) ok = scores();
       }
       ok = ok && pass(n);
       buf += 2u * (uint32_t)n;
@@ -631,8 +663,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (__any_sync(0xffffffffu, any != 0u)) {
           const int e = *(volatile int*)&sh->specials[ds];
           CaSpecial& sp = sh->special[ds][min(e, kCaSpecial - 1)];
-          if (lane < 4) sp.keys[lane] = 0u;
-          if (lane == 4) sp.key0 = (tile0 + lo + i) * kCaKeys;
+          if (lane < 2) sp.keys[lane] = 0u;
+          if (lane == 2) sp.key0 = (tile0 + lo + i) * kCaKeys;
           __syncwarp();
           for (int o = lane * 4; o < L::kTile; o += 128) {
             uint32_t* w = reinterpret_cast<uint32_t*>(v0 + o);
@@ -659,68 +691,71 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     // ---------------------------------------------------------- softmax
     const int t = (warp - 4) >> 2, qd = warp & 3, rl = qd * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
-    uint32_t sc = 0, oc = 0, shared_parts = 0, cut_parts = 0;
+    uint32_t sc = 0, shared_parts = 0, cut_parts = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
       if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
       const CaPart& d = sh->part[ds];
-      const int lo = d.lo, n = d.hi - lo, rows = d.rows, past = d.past;
+      const int lo = d.lo, n = d.hi - lo, rows = d.rows;
       if (n <= 0) break;
       const bool two = rows > 128;
-      const int ur = (two ? 128 * t : 0) + rl;  // row of the unit
+      const int slot_row = two ? 128 * t : 0, ur = slot_row + rl;  // the slot's first row, this thread's row of the unit
       const bool valid = ur < rows;
-      const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = past + j;
+      const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = d.past + j;
       const int head = d.kvh * G + R - j * G;
-      if (two || t == 0) {  // this row of Q: 128-byte swizzle, K-major, halves of 64 columns
-        uint8_t* qt = smem + t * L::kTile;
-        const int64_t qi = (int64_t)(d.at + j) * p.q_stride + (int64_t)head * D;
-        const bool qok = valid && in_bounds(p.err, d.at + j, p.T);
-        uint4 v[D / 8];
+      uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;  // this warp's rows of Q (and its buffer for the results)
+      if (two || t == 0) {  // 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
+        const int c = lane & 7;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          v[c] = qok ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + qi + c * 8)
-                     : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3), u = slot_row + qd * 32 + r;
+          const int R2 = d.row0 + (u < rows ? u : 0), j2 = wk.by_g(R2);
+          const bool there = u < rows && in_bounds(p.err, d.at + j2, p.T);
+          const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(d.at + j2) * p.q_stride +
+                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + c * 8;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * L::kHalf + rl * 128 + (((c & 7) ^ (rl & 7)) << 4)) = v[c];
+          for (int h = 0; h < D / 64; ++h)
+            ca_copy16(qt + h * L::kQHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src + h * 64 : p.q, there);
+        }
+        ca_copy_wait();
         fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->q_ready[ds]);
+      if (lane == 0) mbar_arrive(&sh->q_ready[t][ds]);
       int nt = (n - t + 1) / 2;
       if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - lo, 0), n);
       const int gw = d.gw, gc = d.gc, key_base = (d.tile0 + lo) * kCaKeys;
       const bool any_row = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.0f;
-      for (int jt = 0; ok && jt < nt; ++jt) {
-        const int i = two ? jt : 2 * jt + t;
-        if (!ca_wait(&sh->s_full[t], sc++ & 1u, p.err)) {
+      for (int jt = 0; jt < nt; ++jt, ++sc) {
+        const int i = two ? jt : 2 * jt + t, sb = (int)(sc & 1u);
+        if (!ca_wait(&sh->s_full[t][sb], (sc >> 1) & 1u, p.err)) {
           ok = false;
           break;
         }
         if (!any_row) {  // (what the weights of these rows are does not matter)
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->p_full[t]);
+          if (lane == 0) mbar_arrive(&sh->p_full[t][sb]);
           continue;
         }
         tc_fence_after();
-        uint32_t sv[4][32];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) tmem_ld_32x32b_x32(trow + ca_s_col(t) + 32u * (uint32_t)h, sv[h]);
+        uint32_t sv[2][32];
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, sb), sv[0]);
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, sb) + 32u, sv[1]);
         tmem_wait_ld();
         if (i < gw || i >= gc) {
-          const int key0 = key_base + i * kCaKeys;
-          const int top = pos - key0, bottom = p.window > 0 ? top - p.window : -1;  // seen: bottom < c <= top
+          const int top = pos - key_base - i * kCaKeys;                   // seen: bottom < c <= top
+          const int bottom = p.window > 0 ? top - p.window : -1;
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (32 * h + c > top || 32 * h + c <= bottom) sv[h][c] = __float_as_uint(-INFINITY);
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int c = 0; c < 16; ++c)
             m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1]));
@@ -732,7 +767,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           l *= cf;
         }
         if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
-          // O holds the sums of the tiles before: the commit that announced these scores covers their MMAs
+          // O holds the sums of the tiles before: wait for the last of them
+          if (!ca_wait(&sh->pv_done[t][sb ^ 1], ((sc - 1) >> 1) & 1u, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t ov[32];
@@ -746,24 +786,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nu2 = f2_pack(-u, -u);
         uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
+        uint32_t pr[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pr[32];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t* s2 = &sv[2 * h + (c >> 4)][2 * (c & 15)];
+          for (int c = 0; c < 16; ++c) {
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s2[0]), __uint_as_float(s2[1])), sc2, nu2), x0, x1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1])), sc2, nu2), x0, x1);
             const float e0 = ex2(x0), e1 = ex2(x1);
-            pr[c] = ca_pack<TYPE>(e0, e1);
+            pr[16 * h + c] = ca_pack<TYPE>(e0, e1);
             const uint64_t r2 = f2_pack(e0, e1);
             if (c & 1)
               lb = f2_add(lb, r2);
             else
               la = f2_add(la, r2);
           }
-          tmem_st_32x32b_x32(trow + ca_s_col(t) + 32u * (uint32_t)h, pr);
-        }
+        tmem_st_32x32b_x32(trow + ca_s_col(t, sb), pr);
         {
           float a0, a1, c0, c1;
           f2_unpack(la, a0, a1);
@@ -773,17 +811,17 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[t]);
+        if (lane == 0) mbar_arrive(&sh->p_full[t][sb]);
       }
       // ---- the part's end
-      if (ok && nt > 0) ok = ca_wait(&sh->o_full[t], oc++ & 1u, p.err);
+      if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
       if (!ok) break;
       tc_fence_after();
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
         if (t == 1) {  // hand over the reference and the sum through TMEM; the sums are there
           uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-          tmem_st_32x32b_x8(trow + ca_s_col(1), st);
+          tmem_st_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -795,7 +833,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           tc_fence_after();
           uint32_t st[8];
-          tmem_ld_32x32b_x8(trow + ca_s_col(1), st);
+          tmem_ld_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_ld();
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
           if (n > 1 && !(l1 == 0.0f)) {
@@ -811,10 +849,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const bool cut = n < d.nt;
       const int64_t slot = 2 * cta + (lo > 0 ? 0 : 1);
       if (mine_to_store && any_row) {
-        const float il = 1.0f / l;
-        const int64_t oi = ((int64_t)(d.at + j) * p.H + head) * D;
+        const float il = cut ? 1.0f : 1.0f / l;
         const int64_t pi = slot * wk.rows_cap + ur;
+        // the row's place, in 16-byte words: the result's, or the piece's in the workspace
+        const int64_t place = cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8;
+        uint4* dst = cut ? reinterpret_cast<uint4*>(wk.part_o) : static_cast<uint4*>(p.out);
         const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
+        const unsigned rows_ok = __ballot_sync(0xffffffffu, st_ok);
         const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
         const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
         const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
@@ -846,25 +887,34 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = tmp[c];
           }
-          if (!st_ok) continue;
+          // through the warp's rows of Q (whose products are complete), so that lanes write whole lines
+          uint4* mine = reinterpret_cast<uint4*>(qt + lane * 128);
+          const int words = cut ? 8 : 4, from = cut ? 0 : (c0 >> 3) & 4;
           if (cut) {
-            float* dst = wk.part_o + pi * D + c0;
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(dst + c) = make_float4(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1]),
-                                                                __uint_as_float(ov[c + 2]), __uint_as_float(ov[c + 3]));
+            for (int c = 0; c < 8; ++c)
+              mine[c ^ (lane & 7)] = make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
           } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + oi + c0;
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
+            for (int c = 0; c < 4; ++c) {
               uint4 w;
-              w.x = ca_pack<TYPE>(__uint_as_float(ov[c]) * il, __uint_as_float(ov[c + 1]) * il);
-              w.y = ca_pack<TYPE>(__uint_as_float(ov[c + 2]) * il, __uint_as_float(ov[c + 3]) * il);
-              w.z = ca_pack<TYPE>(__uint_as_float(ov[c + 4]) * il, __uint_as_float(ov[c + 5]) * il);
-              w.w = ca_pack<TYPE>(__uint_as_float(ov[c + 6]) * il, __uint_as_float(ov[c + 7]) * il);
-              *reinterpret_cast<uint4*>(dst + c) = w;
+              w.x = ca_pack<TYPE>(__uint_as_float(ov[8 * c]) * il, __uint_as_float(ov[8 * c + 1]) * il);
+              w.y = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 2]) * il, __uint_as_float(ov[8 * c + 3]) * il);
+              w.z = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 4]) * il, __uint_as_float(ov[8 * c + 5]) * il);
+              w.w = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 6]) * il, __uint_as_float(ov[8 * c + 7]) * il);
+              mine[(from + c) ^ (lane & 7)] = w;
             }
           }
+          if (from + words < 8) continue;  // half a line
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3), c = lane & 7;
+            const int64_t to = __shfl_sync(0xffffffffu, place, r);
+            if ((rows_ok >> r) & 1u)
+              dst[to + (cut ? c0 / 4 : (c0 & ~63) / 8) + c] = *reinterpret_cast<const uint4*>(qt + r * 128 + ((c ^ (r & 7)) << 4));
+          }
+          __syncwarp();
         }
         if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
       }
@@ -904,51 +954,99 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         ++cut_parts;
         if (*(volatile int*)&sh->last) {
-          // the unit's pieces, merged in the order of the keys: a row's D / 4 quads of columns by as many threads
+          // the unit's pieces, merged in the order of the keys. Warp w of the eight takes the
+          // rows w, w + 8, ..; lane i keeps the reference and the sum of the i-th of them
           __threadfence();
-          constexpr int Q = D / 4;
+          constexpr int V = D / 32;  // columns a lane
+          const int w8 = warp - 4, mine8 = rows > w8 ? (rows - w8 + 7) / 8 : 0;
           const int c_first = d.first_cut - 1;
-          for (int item = tid - 128; item < (rows * Q + 31) / 32 * 32; item += 256) {
-            const int rr = item / Q, col = 4 * (item % Q);
-            const bool live = rr < rows;
-            float M = -INFINITY, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          int c_last = c_first;  // the last CTA with a piece
+          {
+            int c = c_first + 1 + lane;
+            unsigned in;
+            while ((in = __ballot_sync(0xffffffffu, c < C && bound(c) < d.u0 + d.v)) == 0xffffffffu) c += 32;
+            c_last = c - lane - 1 + __popc(in);
+          }
+          // the place of CTA c's piece in the workspace (rows), -1 where it has none; lane k of a round: c = cb + k
+          auto piece = [&](int c) {
+            if (c > c_last) return int64_t(-1);
+            const int from = cut_at(c, d.u0, d.v, d.nt), to = cut_at(c + 1, d.u0, d.v, d.nt);
+            return to > from ? (int64_t)(2 * c + (from == 0 ? 1 : 0)) * wk.rows_cap : int64_t(-1);
+          };
+          const int row_i = w8 + 8 * min(lane, max(mine8 - 1, 0));
+          float M = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
-              for (int cb = c_first; cb < C && bound(cb) < d.u0 + d.v; cb += 32) {
-                const int c = cb + lane;
-                const int from = cut_at(min(c, C), d.u0, d.v, d.nt), to = cut_at(min(c + 1, C), d.u0, d.v, d.nt);
-                unsigned list = __ballot_sync(0xffffffffu, to > from);
-                const unsigned heads = __ballot_sync(0xffffffffu, from == 0);
-                for (; list; list &= list - 1) {
-                  const int k = __ffs(list) - 1;
-                  const int64_t row = (int64_t)(2 * (cb + k) + (int)((heads >> k) & 1u)) * wk.rows_cap + rr;
-                  if (!live) continue;
+          for (int turn = 0; turn < 2; ++turn)
+            for (int cb = c_first; cb <= c_last; cb += 32) {
+              const int64_t place = piece(cb + lane);
+#pragma unroll 4
+              for (int k = 0; k < min(32, c_last - cb + 1); ++k) {
+                const int64_t at = __shfl_sync(0xffffffffu, place, k);
+                const float2 ml = at >= 0 ? __ldcg(&wk.part_ml[at + row_i]) : make_float2(-INFINITY, 0.0f);
+                if (ml.y == 0.0f) continue;  // none of the piece's keys is seen
+                if (turn == 0)
+                  M = fmaxf(M, ml.x);
+                else
+                  sum += ex2(ml.x - M) * ml.y;
+              }
+            }
+          const float inv = 1.0f / sum;
+          auto merge = [&](int first_i, auto count) {  // that many rows at once
+            constexpr int N = decltype(count)::value;
+            float acc[N][V];
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+              for (int v = 0; v < V; ++v) acc[q][v] = 0.0f;
+            for (int cb = c_first; cb <= c_last; cb += 32) {
+              const int64_t place = piece(cb + lane);
+#pragma unroll(N == 1 ? 8 : 1)
+              for (int k = 0; k < min(32, c_last - cb + 1); ++k) {
+                const int64_t at = __shfl_sync(0xffffffffu, place, k);
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                  const int i8 = first_i + q;
+                  const float Mq = __shfl_sync(0xffffffffu, M, i8);
+                  if (at < 0 || i8 >= mine8) continue;
+                  const int64_t row = at + w8 + 8 * i8;
                   const float2 ml = __ldcg(&wk.part_ml[row]);
-                  if (ml.y == 0.0f) continue;  // none of the piece's keys is seen
-                  if (pass == 0) {
-                    M = fmaxf(M, ml.x);
+                  const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - Mq);  // (a piece without visible keys has zeros)
+                  const float* o = wk.part_o + row * D + V * lane;
+                  if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
+                    acc[q][0] += f * x.x;
+                    acc[q][1] += f * x.y;
+                    acc[q][2] += f * x.z;
+                    acc[q][3] += f * x.w;
                   } else {
-                    const float f = ex2(ml.x - M);
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(wk.part_o + row * D + col));
-                    sum += f * ml.y;
-                    acc[0] += f * o.x;
-                    acc[1] += f * o.y;
-                    acc[2] += f * o.z;
-                    acc[3] += f * o.w;
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
+                    acc[q][0] += f * x.x;
+                    acc[q][1] += f * x.y;
                   }
                 }
               }
             }
-            if (!live) continue;
-            const int R2 = d.row0 + rr, j2 = wk.by_g(R2);
-            const float inv = 1.0f / sum;
-            if (in_bounds(p.err, d.at + j2, p.T)) {
-              uint2 w;
-              w.x = ca_pack<TYPE>(acc[0] * inv, acc[1] * inv);
-              w.y = ca_pack<TYPE>(acc[2] * inv, acc[3] * inv);
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                                        ((int64_t)(d.at + j2) * p.H + d.kvh * G + R2 - j2 * G) * D + col) = w;
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+              const int i8 = first_i + q;
+              const float iq = __shfl_sync(0xffffffffu, inv, i8 & 31);
+              if (i8 >= mine8) continue;
+              const int R2 = d.row0 + w8 + 8 * i8, j2 = wk.by_g(R2);
+              if (!in_bounds(p.err, d.at + j2, p.T)) continue;
+              uint32_t* to = reinterpret_cast<uint32_t*>(
+                  static_cast<uint16_t*>(p.out) + ((int64_t)(d.at + j2) * p.H + d.kvh * G + R2 - j2 * G) * D + V * lane);
+              if constexpr (V == 4)
+                *reinterpret_cast<uint2*>(to) = make_uint2(ca_pack<TYPE>(acc[q][0] * iq, acc[q][1] * iq),
+                                                           ca_pack<TYPE>(acc[q][2] * iq, acc[q][3] * iq));
+              else
+                *to = ca_pack<TYPE>(acc[q][0] * iq, acc[q][1] * iq);
             }
+          };
+          // many rows have few pieces, many pieces few rows: loads in flight along the one or the other
+          if (mine8 > 4) {
+            for (int i8 = 0; i8 < mine8; i8 += 4) merge(i8, CaInt<4>());
+          } else {
+            for (int i8 = 0; i8 < mine8; ++i8) merge(i8, CaInt<1>());
           }
         }
       }
@@ -1019,6 +1117,7 @@ cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void
   CaWork wk;
   wk.by_g = fast_div((uint32_t)(p.H / p.Hkv));
   wk.ctas = k.ctas;
+  wk.ctas_inv = k.ctas > 1 ? ~uint64_t(0) / (uint64_t)k.ctas : ~uint64_t(0);
   wk.rows_cap = k.rows_cap;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   wk.done = reinterpret_cast<int*>(ws);
