@@ -17,16 +17,17 @@
 // In a CTA (tcgen05, TMEM, TMA):
 //   warp 0        the run's parts (a unit or a piece of one), published in a
 //                 ring of descriptors; TMA copies of K and V tiles into a ring
-//   warps 1, 2    the MMAs of slot 0 and 1: S = Q K^T (128 x 128 x D, both from
-//                 shared memory) and O += P V (P from TMEM, V as it was loaded:
-//                 the MN-major operand)
+//   warp 1        the MMAs of both slots, in turn: S = Q K^T (128 x 128 x D, both
+//                 from shared memory) and O += P V (P from TMEM, V as it was
+//                 loaded: the MN-major operand)
 //   warp 3        the guard: looks through the values of tiles that some row
 //                 sees in part, and takes out NaN and infinities, which a weight
 //                 of zero would not hide; rows that do see them get them added
 //                 at the end
-//   warps 4 - 11  the softmax of slot 0 and 1, one row a thread: scores from
-//                 TMEM, running maximum and sum in fp32, weights rounded to the
-//                 cache's type back into TMEM over the scores
+//   warps 4 - 19  the softmax, two warpgroups a slot that take its tiles in turn,
+//                 one row a thread: scores from TMEM, running maximum and sum in
+//                 fp32, weights rounded to the cache's type back into TMEM over
+//                 the scores
 // With more than 128 rows the two slots are two row tiles, which share every
 // key tile; with fewer they take the key tiles in turn and are merged at the
 // part's end. While one slot's softmax runs, the tensor pipe works for the other.
@@ -39,15 +40,17 @@
 
 namespace w4a16 {
 
-constexpr int kCaThreads = 384;
-constexpr int kCaKeys = 64;   // keys of a tile: a page
-constexpr int kCaDesc = 4;    // parts described ahead
-constexpr int kCaOk = 16;     // guarded tiles that the guard may be ahead: more than the ring holds
-constexpr int kCaSpecial = 12;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
+constexpr int kCaThreads = 640;
+constexpr int kCaKeys = 128;  // keys of a tile: two pages
+constexpr int kCaDesc = 2;    // parts described ahead
+constexpr int kCaOk = 8;      // guarded tiles that the guard may be ahead: more than the ring holds
+constexpr int kCaSpecial = 6;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
 
 // The weights a key tile has in the split: two row tiles, or one.
 constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
-constexpr int kCaOverhead = 128;  // keys that a unit's start and end are worth
+constexpr int kCaOverhead = 256;  // keys that a unit's start and end are worth
+constexpr int kCaLeast = 4;       // tiles a CTA has at least, where units are cut
+constexpr int kCaMerge = 6;       // tiles that a cut is worth
 
 // Weights are taken against a reference that is raised only by a maximum more
 // than `lazy` (log2) above it, so that the sums in TMEM are seldom rescaled. In
@@ -83,15 +86,16 @@ struct CaPart {
 };
 struct CaSpecial {
   int key0;
-  uint32_t keys[2];  // of the tile's 64: those with a value that is not finite
+  uint32_t keys[4];  // of the tile's 128: those with a value that is not finite
 };
 struct CaShared {
-  uint64_t full[20], free[20];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], fin[2];
-  uint64_t stat, read, stored, told;
+  uint64_t full[10], free[10];
+  uint64_t s_full[2], p_full[2][2], o_full[2], fin;
+  uint64_t mark[2][2][4], sums[2], stat, read, stored, told;
   uint64_t landed[kCaOk], ok[kCaOk];  // guarded values: in shared memory, looked through
   uint64_t desc_full[kCaDesc], desc_free[kCaDesc], q_ready[2][kCaDesc];
   CaPart part[kCaDesc];
+  float top[2][2][128];  // the largest score of each row in a warpgroup's half of a tile
   int specials[kCaDesc];
   CaSpecial special[kCaDesc][kCaSpecial];
   uint32_t tmem;
@@ -100,20 +104,18 @@ struct CaShared {
 
 template <int D>
 struct CaLayout {
-  static constexpr int kQHalf = 128 * 128;  // 128 rows of 64 columns
-  static constexpr int kQ = D / 64 * kQHalf;
-  static constexpr int kHalf = kCaKeys * 128;  // 64 keys of 64 columns
+  static constexpr int kHalf = 128 * 128;  // 128 rows of 64 columns
   static constexpr int kTile = D / 64 * kHalf;
-  static constexpr int kBufs = D == 128 ? 10 : 20;
-  static constexpr int kRingOff = 2 * kQ;
+  static constexpr int kBufs = D == 128 ? 5 : 10;
+  static constexpr int kRingOff = 2 * kTile;
   static constexpr int kSharedOff = kRingOff + kBufs * kTile;
-  static constexpr int kTotal = kSharedOff + (int)sizeof(CaShared) + 1024;  // + alignment
+  static constexpr int kTotal = kSharedOff + (int)sizeof(CaShared);
   static_assert(kTotal <= 227 * 1024, "shared memory");
-  static_assert(kBufs <= 20 && kBufs / 2 < kCaOk, "rings");
+  static_assert(kBufs <= 10 && kBufs / 2 < kCaOk, "rings");
 };
 
-// TMEM columns: a slot's two score buffers (the weights over the first half of one) and its sums
-__device__ __forceinline__ uint32_t ca_s_col(int t, int sb) { return 128u * (uint32_t)t + 64u * (uint32_t)sb; }
+// TMEM columns: a slot's scores, each half's weights over the first half of them, and its sums
+__device__ __forceinline__ uint32_t ca_s_col(int t, int hb) { return 128u * (uint32_t)t + 64u * (uint32_t)hb; }
 __device__ __forceinline__ uint32_t ca_o_col(int t) { return 256u + 128u * (uint32_t)t; }
 
 // 16 bytes to shared memory, asynchronously; zeros where there are none.
@@ -122,11 +124,6 @@ __device__ __forceinline__ void ca_copy16(void* dst, const void* src, bool there
                : "memory");
 }
 __device__ __forceinline__ void ca_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-template <int N>
-struct CaInt {
-  static constexpr int value = N;
-};
 
 // Bounded wait by a whole warp; false once it has run out.
 __device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
@@ -150,7 +147,8 @@ __device__ __forceinline__ bool test_skip_copy(uint32_t) { return false; }
 // ------------------------------------------------------------------ the split
 
 // floor(a / b) for 0 <= a, b > 0 and a quotient below 2^22 (the fp32 estimate is
-// off by less than one half then, and put right), and of a * n / b for a < b.
+// off by less than one half then, and put right); the whole number next to a * n / b
+// for a < b.
 __device__ __forceinline__ int ca_fix(int q, int64_t a, int64_t b) {
   int64_t r = a - q * b;
   while (r < 0) r += b, --q;
@@ -159,7 +157,7 @@ __device__ __forceinline__ int ca_fix(int q, int64_t a, int64_t b) {
 }
 __device__ __forceinline__ int ca_quotient(int64_t a, int64_t b) { return ca_fix((int)((float)a / (float)b), a, b); }
 __device__ __forceinline__ int ca_share(int64_t a, int n, int64_t b) {
-  return ca_fix((int)((float)a / (float)b * (float)n), a * n, b);
+  return ca_fix((int)((float)a / (float)b * (float)n + 0.5f), 2 * a * n + b, 2 * b);
 }
 
 // A request's rows: the first, their number (0 where it brings none or is not
@@ -274,6 +272,17 @@ __device__ __forceinline__ uint32_t ca_not_finite(uint32_t w) {
   return ((w & kCaExp<TYPE>)+kCaExpUnit<TYPE>)&0x80008000u;
 }
 
+// two values times zero, added to acc
+template <int TYPE>
+__device__ __forceinline__ uint32_t ca_times_zero(uint32_t w, uint32_t acc) {
+  uint32_t r;
+  if constexpr (TYPE == 0)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+  return r;
+}
+
 // The values at `at` (D elements) that are not finite, added to an output row's columns c0 .. c0 + 31.
 template <int TYPE>
 __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaShared* sh, int slot, int b, int kvh, int D,
@@ -298,6 +307,86 @@ __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaSha
   }
 }
 
+// A cut unit's rows from its np pieces, by sixteen warps: warp w has the rows w, w +
+// 16, .., a lane D / 32 columns; N rows and K pieces at a time, whose loads go out
+// together.
+template <int TYPE, int D, int N, int K>
+__device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk, const CaPart& d, const int* list, int np,
+                                      int w, int lane) {
+  constexpr int V = D / 32;
+  const int G = (int)wk.by_g.d, rows = d.rows;
+  for (int r0 = w; r0 < rows; r0 += 16 * N) {
+    float acc[N][V], M[N], S[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      M[q] = -INFINITY;
+      S[q] = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[q][v] = 0.0f;
+    }
+    for (int k0 = 0; k0 < np; k0 += K) {
+      float2 ml[N][K];
+      float o[N][K][V];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int at = k0 + k < np ? list[k0 + k] : 0;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const bool there = k0 + k < np && r0 + 16 * q < rows;
+          const int64_t row = (int64_t)at + (there ? r0 + 16 * q : 0);
+          ml[q][k] = there ? __ldcg(&wk.part_ml[row]) : make_float2(-INFINITY, 0.0f);
+          const float* x = wk.part_o + row * D + V * lane;
+          if constexpr (V == 4) {
+            const float4 y = there ? __ldcg(reinterpret_cast<const float4*>(x)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            o[q][k][0] = y.x;
+            o[q][k][1] = y.y;
+            o[q][k][2] = y.z;
+            o[q][k][3] = y.w;
+          } else {
+            const float2 y = there ? __ldcg(reinterpret_cast<const float2*>(x)) : make_float2(0.0f, 0.0f);
+            o[q][k][0] = y.x;
+            o[q][k][1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        float top = M[q];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (ml[q][k].y != 0.0f) top = fmaxf(top, ml[q][k].x);  // (a sum of zero: the piece's keys are not seen)
+        const float f0 = S[q] == 0.0f ? 0.0f : ex2(M[q] - top);
+        S[q] *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[q][v] *= f0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float f = ml[q][k].y == 0.0f ? 0.0f : ex2(ml[q][k].x - top);
+          S[q] += f * ml[q][k].y;
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[q][v] += f * o[q][k][v];
+        }
+        M[q] = top;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int r = r0 + 16 * q;
+      if (r >= rows) continue;
+      const float inv = 1.0f / S[q];
+      const int R = d.row0 + r, j = wk.by_g(R);
+      if (!in_bounds(p.err, d.at + j, p.T)) continue;
+      uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                 ((int64_t)(d.at + j) * p.H + d.kvh * G + R - j * G) * D + V * lane);
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(to) =
+            make_uint2(ca_pack<TYPE>(acc[q][0] * inv, acc[q][1] * inv), ca_pack<TYPE>(acc[q][2] * inv, acc[q][3] * inv));
+      else
+        *to = ca_pack<TYPE>(acc[q][0] * inv, acc[q][1] * inv);
+    }
+  }
+}
+
 // The last position of slot t's rows, where the slots are row tiles.
 __device__ __forceinline__ int ca_slot_last(const CaWork& wk, const CaPart& d, int t) {
   return d.past + wk.by_g(d.row0 + min(d.rows - 1, 128 * t + 127));
@@ -308,37 +397,38 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     kv16_attention_kernel(const __grid_constant__ CaMaps maps, const Kv16AttnParams p, const CaWork wk) {
   using L = CaLayout<D>;
   constexpr int NB = L::kBufs;
-  extern __shared__ uint8_t ca_smem[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ca_smem) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
   CaShared* sh = reinterpret_cast<CaShared*>(smem + L::kSharedOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = (int)wk.by_g.d, C = wk.ctas, cta = (int)blockIdx.x;
+  const int G = (int)wk.by_g.d, cta = (int)blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < NB; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->free[i], 2);
+      mbar_init(&sh->free[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->o_full[t], 1);
       for (int k = 0; k < 2; ++k) {
-        mbar_init(&sh->s_full[t][k], 1);
         mbar_init(&sh->p_full[t][k], 4);
-        mbar_init(&sh->pv_done[t][k], 1);
+        for (int q = 0; q < 4; ++q) mbar_init(&sh->mark[t][k][q], 1);
       }
-      mbar_init(&sh->fin[t], 1);
+      mbar_init(&sh->sums[t], 8);
     }
+    mbar_init(&sh->fin, 1);
     mbar_init(&sh->stat, 4);
-    mbar_init(&sh->read, 4);
-    mbar_init(&sh->stored, 8);
+    mbar_init(&sh->read, 8);
+    mbar_init(&sh->stored, 16);
     mbar_init(&sh->told, 1);
     for (int i = 0; i < kCaOk; ++i) {
       mbar_init(&sh->landed[i], 1);
       mbar_init(&sh->ok[i], 1);
     }
     for (int i = 0; i < kCaDesc; ++i) {
-      for (int t = 0; t < 2; ++t) mbar_init(&sh->q_ready[t][i], 4);
+      for (int t = 0; t < 2; ++t) mbar_init(&sh->q_ready[t][i], 8);
       mbar_init(&sh->desc_full[i], 1);
-      mbar_init(&sh->desc_free[i], 11);
+      mbar_init(&sh->desc_free[i], 18);
     }
     fence_mbarrier_init();
   }
@@ -356,19 +446,23 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // Each thread sums a row of requests; the scratch lies where Q will
   struct Scratch {
     int64_t sums[kCaThreads / 32];
+    int units[kCaThreads / 32];
     CaPlace place[2];
   };
   Scratch* scr = reinterpret_cast<Scratch*>(smem);
   const int per = (p.B + kCaThreads - 1) / kCaThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int64_t mine = 0;
+  int units = 0;
   for (int b = b0; b < b1; ++b) {
     const CaRequest r = ca_request(p, b, cta == 0);
     if (r.cnt > 0) {
       const CaLoad w = ca_load(p, wk, r);
       mine += p.Hkv * w.before(w.units);
+      units = min(units + p.Hkv * w.units, 65535);  // (more than any number of CTAs will do)
     }
   }
+  units = __reduce_add_sync(0xffffffffu, units);
   int64_t upto = mine;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
@@ -376,15 +470,30 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (lane >= k) upto += o;
   }
   if (lane == 31) scr->sums[warp] = upto;
+  if (lane == 31) scr->units[warp] = units;
   if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1};
   __syncthreads();
   grid_launch_dependents();  // (TMEM is allocated: no later kernel can hold it while this one waits for it)
   int64_t W = 0, at = upto - mine;
+  units = 0;
   for (int w = 0; w < kCaThreads / 32; ++w) {
     if (w < warp) at += scr->sums[w];
     W += scr->sums[w];
+    units += scr->units[w];
   }
-  auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, wk.ctas_inv * (uint64_t)c); };
+  // Fewer units than CTAs: as many CTAs as give each unit a whole number of pieces of at least kCaLeast tiles, unless
+  // all of them would be done sooner although nearly every one then has to merge.
+  int C = wk.ctas;
+  uint64_t inv = wk.ctas_inv;
+  if (units > 0 && units < C) {
+    const float tile = (float)(kCaWeight1 * G * kCaKeys), w = (float)W;
+    const int even = units * max(1, min(C / units, (int)(w / (tile * kCaLeast * (float)units))));
+    if (w / (float)even <= w / (float)C + tile * kCaMerge) {
+      C = even;
+      inv = ~uint64_t(0) / (uint64_t)C;
+    }
+  }
+  auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, inv * (uint64_t)c); };
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     const int64_t x = bound(cta + e);
@@ -416,7 +525,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------- parts and copies
-    uint32_t buf = 0, guarded = 0;
+    uint32_t buf = 0, guarded = 0, issued = 0;
     int seq = 0;
     bool ok = true;
     int b = begin.b, kvh = begin.kvh, unit = begin.unit;
@@ -437,7 +546,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           ok = false;
           break;
         }
-        // key tiles t with 64 t + 63 <= first_pos, and 64 t > last_pos - window, are seen whole by every row
+        // key tiles t with 128 t + 127 <= first_pos, and 128 t > last_pos - window, are seen whole by every row
         const int whole = (t.first_pos + 1) / kCaKeys - t.tile0 - lo;
         const int in_window =
             p.window > 0 && t.last_pos >= p.window ? (t.last_pos - p.window) / kCaKeys + 1 - t.tile0 - lo : 0;
@@ -474,45 +583,59 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->desc_full[ds]);
         ++seq;
-        // the pages of 32 tiles at a time, a lane an entry
+        // the pages of 16 tiles at a time, a lane an entry; those that no row sees any key of are not read
+        const int blk_lo = (p.window > 0 ? max(0, t.first_pos - p.window + 1) : 0) / 64, blk_hi = t.last_pos / 64;
         const int32_t* row = p.table + (int64_t)b * p.max_blocks;
-        int base = t.tile0 + lo;
+        int base = 2 * (t.tile0 + lo);
         auto entries = [&]() {
-          if (base + lane >= t.tile0 + hi || !in_bounds(p.err, base + lane, p.max_blocks)) return -1;
-          const int page = row[base + lane];
+          const int blk = base + lane;
+          if (blk < blk_lo || blk > blk_hi || blk >= 2 * (t.tile0 + hi) || !in_bounds(p.err, blk, p.max_blocks)) return -1;
+          const int page = row[blk];
           if (page >= 0 && page < p.pages) return page;
           report_error(p.err, kErrInput);
           return -1;
         };
         int now = entries();
         for (int i = lo; ok && i < hi; ++i) {
-          if (t.tile0 + i - base >= 32) {
+          if (2 * (t.tile0 + i) - base >= 32) {
             base += 32;
             now = entries();
           }
-          const int page = __shfl_sync(0xffffffffu, now, t.tile0 + i - base);
-          const int z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++buf) {
-            const uint32_t s = buf % NB, use = buf / NB;
-            if (use > 0 && !ca_wait(&sh->free[s], (use - 1) & 1u, p.err)) {
-              ok = false;
-              break;
-            }
-            // guarded values land at a barrier of their own: the guard tells when they may be used
-            const bool guard = kv == 1 && (i - lo < gw || i - lo >= gc);
-            if (lane == 0 && !test_skip_copy(buf)) {
-              uint8_t* st = smem + L::kRingOff + s * L::kTile;
-              uint64_t* bar = guard ? &sh->landed[guarded % kCaOk] : &sh->full[s];
-              if (guard) mbar_arrive(&sh->full[s]);
+          int z[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int page = __shfl_sync(0xffffffffu, now, 2 * (t.tile0 + i) - base + k);
+            z[k] = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
+          }
+          // guarded values land at a barrier of their own: the guard tells when they may be used
+          const bool guard = i - lo < gw || i - lo >= gc;
+          if (lane == 0) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t x = buf + (uint32_t)kv, s = x % NB, use = x / NB;
+              ok = ok && (use == 0 || ca_wait(&sh->free[s], (use - 1) & 1u, p.err));
+              if (!ok || test_skip_copy(x)) continue;
+              uint64_t* bar = &sh->full[s];
+              if (kv == 1 && guard) {
+                mbar_arrive(bar);
+                bar = &sh->landed[guarded % kCaOk];
+              }
               mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
 #pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tma_load_3d(st + h * L::kHalf, kv ? &maps.v : &maps.k, 64 * h, 0, z, bar);
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(smem + L::kRingOff + s * L::kTile + h * L::kHalf + k * 64 * 128, kv ? &maps.v : &maps.k, 64 * h,
+                              0, z[k], bar);
+              issued = (uint32_t)kv + 1u;  // (of this tile, where a wait runs out)
             }
-            guarded += guard;
-            __syncwarp();
           }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          issued = __shfl_sync(0xffffffffu, issued, 0);
+          if (!ok) break;
+          issued = 0;
+          buf += 2u;
+          guarded += guard;
         }
       }
       if (at_end) break;
@@ -538,17 +661,17 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       mbar_arrive(&sh->desc_full[ds]);
     }
     // the copies in flight land before the CTA exits (some may be, if a wait of another warp ran out)
-    for (uint32_t k = buf > NB ? buf - NB : 0; k < buf; ++k)
+    for (uint32_t k = buf > NB ? buf - NB : 0; k < buf + issued; ++k)
       if (!test_skip_copy(k)) ca_wait(&sh->full[k % NB], (k / NB) & 1u, p.err);
     for (uint32_t k = guarded > kCaOk ? guarded - kCaOk : 0; k < guarded; ++k)
       ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err);
-  } else if (warp <= 2) {
-    // ------------------------------------------------------ MMA, slot t
-    const int t = warp - 1;
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA
+    // One warp for both slots, in turn: what a slot waits for is then done while the other slot's softmax runs. (A warp a
+    // slot: both slots' products end up side by side on the tensor pipe, and then both wait for their softmax.)
     constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
     const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
-    uint32_t buf = 0, oks = 0;
-    uint32_t sc = 0, pc = 0;  // score tiles issued and weights used so far: buffer and phase
+    uint32_t buf = 0, oks = 0, pc[2] = {0u, 0u};  // buffers, guarded tiles and each slot's weights so far
     bool ok = true, issued = false;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -557,83 +680,86 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int n = d.hi - d.lo, gw = d.gw, gc = d.gc;
       if (n <= 0) break;
       const bool two = d.rows > 128;
-      // this slot's tiles: as far as its rows see where the slots are row tiles, every other one where they share the rows
-      int upto = n;
-      if (two) upto = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
-      const int step = two ? 1 : 2;
-      int i = two ? 0 : t;  // the tile whose scores come next
-      int at = 0;           // tiles before it are used or passed over
-      const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kQ);
-      // Each slot releases every buffer once: those it does not use as soon as they are there.
-      auto pass = [&](int to) {
-        for (; at < to; ++at)
-          for (uint32_t x = buf + 2u * (uint32_t)at, e = x + 2u; x < e; ++x) {
-            if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
-            if (lane == 0) mbar_arrive(&sh->free[x % NB]);
-            __syncwarp();
-          }
-        return true;
-      };
-      auto scores = [&]() {
-        if (!pass(i)) return false;
-        const uint32_t x = buf + 2u * (uint32_t)i;
-        if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+      // row tiles: slot 0's rows may see fewer tiles than slot 1's, which see them all
+      const int upto0 = two ? min(max(ca_slot_last(wk, d, 0) / kCaKeys + 1 - d.tile0 - d.lo, 0), n) : n;
+      auto at = [&](uint32_t x) { return smem_u32(smem + L::kRingOff + (x % NB) * L::kTile); };
+      auto landed = [&](uint32_t x) { return ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err); };
+      // S = Q K^T of slot t and tile i, and the barriers that it arrives at: the scores', the buffer's after its last use
+      auto scores = [&](int t, int i, bool last_use) {
+        const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kTile), k0 = at(buf + 2u * (uint32_t)i);
         tc_fence_after();
-        const uint32_t k0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
-        const int sb = (int)(sc & 1u);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_ss_warp(tmem + ca_s_col(t, sb),
-                            umma_desc_sw128_kmajor(q0 + (uint32_t)((kk >> 2) * L::kQHalf + 32 * (kk & 3))),
-                            umma_desc_sw128_kmajor(k0 + (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3))), idesc_s,
-                            kk > 0 ? 1u : 0u);
-        umma_commit_warp(&sh->s_full[t][sb]);
-        umma_commit_warp(&sh->free[x % NB]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3));
+          umma_bf16_ss_warp(tmem + ca_s_col(t, 0), umma_desc_sw128_kmajor(q0 + off), umma_desc_sw128_kmajor(k0 + off),
+                            idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_warp(&sh->s_full[t]);
+        if (last_use) umma_commit_warp(&sh->free[(buf + 2u * (uint32_t)i) % NB]);
         issued = true;
-        ++sc;
-        at = i + 1;
-        i += step;
+      };
+      // O += P V, each half of the keys once its weights are there
+      auto sums = [&](int t, int i, bool first, bool last_use) {
+        const uint32_t v0 = at(buf + 2u * (uint32_t)i + 1u);
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          if (!ca_wait(&sh->p_full[t][hb], pc[t] & 1u, p.err)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, hb) + 8u * (uint32_t)kk,
+                              umma_desc_sw128_mnmajor(v0 + 2048u * (uint32_t)(4 * hb + kk), (uint32_t)L::kHalf, 1024u),
+                              idesc_o, (!first || hb > 0 || kk > 0) ? 1u : 0u);
+        }
+        ++pc[t];
+        if (last_use) umma_commit_warp(&sh->free[(buf + 2u * (uint32_t)i + 1u) % NB]);
         return true;
       };
-      if (i < upto) ok = ca_wait(&sh->q_ready[two ? t : 0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
-      if (ok && i < upto) ok = scores();
-      // the scores two tiles on go out once the weights of a tile, which lie in their buffer, are used
-      for (int v = two ? 0 : t; ok && v < upto; v += step) {
-        const uint32_t x = buf + 2u * (uint32_t)v + 1u;
-        const int sb = (int)(pc & 1u);
-        if (!ca_wait(&sh->p_full[t][sb], (pc >> 1) & 1u, p.err) || !ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        if (v < gw || v >= gc) {  // the guard has looked through the values
-          const uint32_t g = oks + (uint32_t)(v < gw ? v : gw + v - gc);
-          if (!ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-        }
-        tc_fence_after();
-        const uint32_t v0 = smem_u32(smem + L::kRingOff + (x % NB) * L::kTile);
-#pragma unroll
-        for (int kk = 0; kk < kCaKeys / 16; ++kk)
-          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, sb) + 8u * (uint32_t)kk,
-                            umma_desc_sw128_mnmajor(v0 + 2048u * (uint32_t)kk, (uint32_t)L::kHalf, 1024u), idesc_o,
-                            (v >= step || kk > 0) ? 1u : 0u);
-        umma_commit_warp(&sh->pv_done[t][sb]);
-        umma_commit_warp(&sh->free[x % NB]);
-        ++pc;
-        if (i < upto) ok = scores();
+      const uint32_t phase = (uint32_t)(seq / kCaDesc) & 1u;
+      // the first scores (both slots' warps are done with the part before; where they share the rows slot 0's load them)
+      ok = landed(buf) && ca_wait(&sh->q_ready[0][ds], phase, p.err);
+      if (ok && upto0 > 0) scores(0, 0, !two);
+      ok = ok && ca_wait(&sh->q_ready[1][ds], phase, p.err);
+      if (ok && two) scores(1, 0, true);
+      if (ok && !two && n > 1) {
+        ok = landed(buf + 2u);
+        if (ok) scores(1, 1, true);
       }
-      ok = ok && pass(n);
+      for (int i = 0; ok && i < n; ++i) {
+        ok = landed(buf + 2u * (uint32_t)i + 1u);
+        if (ok && (i < gw || i >= gc)) {  // the guard has looked through the values
+          const uint32_t g = oks + (uint32_t)(i < gw ? i : gw + i - gc);
+          ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err);
+        }
+        const int next = i + (two ? 1 : 2);  // the tile whose scores go out behind these sums
+        if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
+        if (two) {
+          if (ok && i < upto0) {
+            ok = sums(0, i, i == 0, false);
+            if (ok && next < upto0) scores(0, next, false);
+            if (ok && next >= upto0) umma_commit_warp(&sh->o_full[0]);
+          }
+          ok = ok && sums(1, i, i == 0, true);
+          if (ok && next < n) scores(1, next, true);
+          if (ok && next >= n) umma_commit_warp(&sh->o_full[1]);
+        } else {
+          const int t = i & 1;
+          ok = ok && sums(t, i, i == t, true);
+          if (ok && next < n) scores(t, next, true);
+          if (ok && next >= n) umma_commit_warp(&sh->o_full[t]);
+        }
+      }
       buf += 2u * (uint32_t)n;
       oks += (uint32_t)(gw + n - gc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
     }
     if (issued) {
-      umma_commit_warp(&sh->fin[t]);  // tracks all of this warp's MMAs
-      ca_wait(&sh->fin[t], 0u, p.err);
+      umma_commit_warp(&sh->fin);  // tracks all of this warp's MMAs
+      ca_wait(&sh->fin, 0u, p.err);
     }
+  } else if (warp == 2) {
+    // (no work)
   } else if (warp == 3) {
     // ------------------------------------------------------------ guard
     uint32_t buf = 0, oks = 0;
@@ -653,18 +779,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           break;
         }
         uint8_t* v0 = smem + L::kRingOff + (x % NB) * L::kTile;
-        uint32_t any = 0;
+        uint32_t nil[4] = {0u, 0u, 0u, 0u};  // 0 times each value, summed up: NaN where one is not finite
 #pragma unroll 8
         for (int o = lane * 16; o < L::kTile; o += 512) {
           const uint4 w = *reinterpret_cast<const uint4*>(v0 + o);
-          any |= ca_not_finite<TYPE>(w.x) | ca_not_finite<TYPE>(w.y) | ca_not_finite<TYPE>(w.z) |
-                 ca_not_finite<TYPE>(w.w);
+          nil[0] = ca_times_zero<TYPE>(w.x, nil[0]);
+          nil[1] = ca_times_zero<TYPE>(w.y, nil[1]);
+          nil[2] = ca_times_zero<TYPE>(w.z, nil[2]);
+          nil[3] = ca_times_zero<TYPE>(w.w, nil[3]);
         }
-        if (__any_sync(0xffffffffu, any != 0u)) {
+        if (__any_sync(0xffffffffu, ((nil[0] | nil[1] | nil[2] | nil[3]) & 0x7FFF7FFFu) != 0u)) {
           const int e = *(volatile int*)&sh->specials[ds];
           CaSpecial& sp = sh->special[ds][min(e, kCaSpecial - 1)];
-          if (lane < 2) sp.keys[lane] = 0u;
-          if (lane == 2) sp.key0 = (tile0 + lo + i) * kCaKeys;
+          if (lane < 4) sp.keys[lane] = 0u;
+          if (lane == 4) sp.key0 = (tile0 + lo + i) * kCaKeys;
           __syncwarp();
           for (int o = lane * 4; o < L::kTile; o += 128) {
             uint32_t* w = reinterpret_cast<uint32_t*>(v0 + o);
@@ -689,9 +817,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- softmax
-    const int t = (warp - 4) >> 2, qd = warp & 3, rl = qd * 32 + lane;
+    const int t = (warp - 4) >> 3, hb = ((warp - 4) >> 2) & 1, qd = warp & 3, rl = qd * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
-    uint32_t sc = 0, shared_parts = 0, cut_parts = 0;
+    uint32_t sc = 0, oc = 0, marks = 0, parts = 0, shared_parts = 0, cut_parts = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -704,19 +832,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const bool valid = ur < rows;
       const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = d.past + j;
       const int head = d.kvh * G + R - j * G;
-      uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;  // this warp's rows of Q (and its buffer for the results)
+      // this warp's part of the slot's Q (half the columns, or half the rows), and its buffer for the results
+      uint8_t* qt = smem + t * L::kTile + qd * 32 * 128;
       if (two || t == 0) {  // 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
         const int c = lane & 7;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int k = D == 128 ? kk : 4 * hb + kk, h = D == 128 ? hb : 0;
           const int r = 4 * k + (lane >> 3), u = slot_row + qd * 32 + r;
           const int R2 = d.row0 + (u < rows ? u : 0), j2 = wk.by_g(R2);
           const bool there = u < rows && in_bounds(p.err, d.at + j2, p.T);
           const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(d.at + j2) * p.q_stride +
-                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + c * 8;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            ca_copy16(qt + h * L::kQHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src + h * 64 : p.q, there);
+                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + h * 64 + c * 8;
+          ca_copy16(qt + h * L::kHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src : p.q, there);
         }
         ca_copy_wait();
         fence_proxy_async_smem();
@@ -729,23 +857,23 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const bool any_row = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.0f;
       for (int jt = 0; jt < nt; ++jt, ++sc) {
-        const int i = two ? jt : 2 * jt + t, sb = (int)(sc & 1u);
-        if (!ca_wait(&sh->s_full[t][sb], (sc >> 1) & 1u, p.err)) {
+        const int i = two ? jt : 2 * jt + t;
+        if (!ca_wait(&sh->s_full[t], sc & 1u, p.err)) {
           ok = false;
           break;
         }
         if (!any_row) {  // (what the weights of these rows are does not matter)
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->p_full[t][sb]);
+          if (lane == 0) mbar_arrive(&sh->p_full[t][hb]);
           continue;
         }
         tc_fence_after();
         uint32_t sv[2][32];
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, sb), sv[0]);
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, sb) + 32u, sv[1]);
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb), sv[0]);
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb) + 32u, sv[1]);
         tmem_wait_ld();
         if (i < gw || i >= gc) {
-          const int top = pos - key_base - i * kCaKeys;                   // seen: bottom < c <= top
+          const int top = pos - key_base - i * kCaKeys - 64 * hb;  // seen: bottom < c <= top
           const int bottom = p.window > 0 ? top - p.window : -1;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -759,7 +887,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
           for (int c = 0; c < 16; ++c)
             m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1]));
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // the row's largest score, from both halves (the next tile's is written when both have read this one)
+        *(volatile float*)&sh->top[t][hb][rl] = mx;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->mark[t][hb][qd]);
+        if (!ca_wait(&sh->mark[t][hb ^ 1][qd], marks++ & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        mx = fmaxf(mx, *(volatile float*)&sh->top[t][hb ^ 1][rl]) * p.scale_log2;
         float cf = 1.0f;
         if (mx > m + kCaLazy<TYPE>) {
           cf = m == -INFINITY ? 0.0f : ex2(m - mx);
@@ -767,41 +904,37 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           l *= cf;
         }
         if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
-          // O holds the sums of the tiles before: wait for the last of them
-          if (!ca_wait(&sh->pv_done[t][sb ^ 1], ((sc - 1) >> 1) & 1u, p.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+          // O holds the sums of the tiles before (the commit that announced these scores covers them); half the columns each
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+          for (int c0 = hb * (D / 2); c0 < (hb + 1) * (D / 2); c0 += 16) {
+            uint32_t ov[16];
+            tmem_ld_32x32b<16>(trow + ca_o_col(t) + (uint32_t)c0, ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * cf);
-            tmem_st_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+            for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * cf);
+            tmem_st_32x32b_x16(trow + ca_o_col(t) + (uint32_t)c0, ov);
           }
         }
         const float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nu2 = f2_pack(-u, -u);
         uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
-        uint32_t pr[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pr[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             float x0, x1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1])), sc2, nu2), x0, x1);
             const float e0 = ex2(x0), e1 = ex2(x1);
-            pr[16 * h + c] = ca_pack<TYPE>(e0, e1);
+            pr[c] = ca_pack<TYPE>(e0, e1);
             const uint64_t r2 = f2_pack(e0, e1);
             if (c & 1)
               lb = f2_add(lb, r2);
             else
               la = f2_add(la, r2);
           }
-        tmem_st_32x32b_x32(trow + ca_s_col(t, sb), pr);
+          tmem_st_32x32b_x16(trow + ca_s_col(t, hb) + 16u * (uint32_t)h, pr);
+        }
         {
           float a0, a1, c0, c1;
           f2_unpack(la, a0, a1);
@@ -811,21 +944,39 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[t][sb]);
+        if (lane == 0) mbar_arrive(&sh->p_full[t][hb]);
       }
-      // ---- the part's end
-      if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
+      // ---- the part's end: the warpgroups of a slot add up their sums, over TMEM; each then has half of the columns
+      if (ok && nt > 0) ok = ca_wait(&sh->o_full[t], oc++ & 1u, p.err);
       if (!ok) break;
       tc_fence_after();
+      {
+        uint32_t st[8] = {__float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        tmem_st_32x32b_x8(trow + ca_s_col(t, hb), st);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->sums[t]);
+        if (!ca_wait(&sh->sums[t], parts++ & 1u, p.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_ld_32x32b_x8(trow + ca_s_col(t, hb ^ 1), st);
+        tmem_wait_ld();
+        l += __uint_as_float(st[0]);
+      }
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
-        if (t == 1) {  // hand over the reference and the sum through TMEM; the sums are there
-          uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-          tmem_st_32x32b_x8(trow + ca_s_col(1, 0), st);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->stat);
+        if (t == 1) {  // hand over the reference and the sum through TMEM; the sums of values are there
+          if (hb == 0) {
+            uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_st_32x32b_x8(trow + ca_s_col(1, 0) + 8u, st);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->stat);
+          }
         } else {
           if (!ca_wait(&sh->stat, shared_parts & 1u, p.err)) {
             ok = false;
@@ -833,7 +984,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           tc_fence_after();
           uint32_t st[8];
-          tmem_ld_32x32b_x8(trow + ca_s_col(1, 0), st);
+          tmem_ld_32x32b_x8(trow + ca_s_col(1, 0) + 8u, st);
           tmem_wait_ld();
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
           if (n > 1 && !(l1 == 0.0f)) {
@@ -845,55 +996,75 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
         }
       }
-      const bool mine_to_store = two || t == 0;
       const bool cut = n < d.nt;
       const int64_t slot = 2 * cta + (lo > 0 ? 0 : 1);
-      if (mine_to_store && any_row) {
+      constexpr int LW = D / 16;  // 16-byte words of a row in the buffer: half a row's columns, rounded
+      uint8_t* stage = D == 128 ? qt + hb * L::kHalf : qt + hb * 2048;
+      if ((two || t == 0) && any_row) {
         const float il = cut ? 1.0f : 1.0f / l;
         const int64_t pi = slot * wk.rows_cap + ur;
         // the row's place, in 16-byte words: the result's, or the piece's in the workspace
-        const int64_t place = cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8;
+        const int64_t place = (cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8) + hb * (cut ? D / 8 : LW);
         uint4* dst = cut ? reinterpret_cast<uint4*>(wk.part_o) : static_cast<uint4*>(p.out);
         const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
         const unsigned rows_ok = __ballot_sync(0xffffffffu, st_ok);
         const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
         const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
         const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
+        // through the warp's part of Q (whose products are complete), so that lanes write whole lines
+        auto put = [&](int word, uint4 w) {
+          *reinterpret_cast<uint4*>(stage + lane * (16 * LW) + ((word ^ (lane & (LW - 1))) << 4)) = w;
+        };
+        auto flush = [&](int word) {  // LW words of each row, from this one on
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < LW; ++k) {
+            const int r = (32 / LW) * k + lane / LW, c = lane % LW;
+            const int64_t to = __shfl_sync(0xffffffffu, place, r);
+            if ((rows_ok >> r) & 1u)
+              dst[to + word + c] =
+                  *reinterpret_cast<const uint4*>(stage + r * (16 * LW) + ((c ^ (r & (LW - 1))) << 4));
+          }
+          __syncwarp();
+        };
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          const uint32_t col = (uint32_t)(hb * (D / 2) + c0);
           uint32_t ov[32];
           if (nt > 0) {
-            tmem_ld_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, ov);
+            tmem_ld_32x32b_x32(trow + ca_o_col(t) + col, ov);
             tmem_wait_ld();
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
           }
           if (other) {
-            uint32_t ow[32];
-            tmem_ld_32x32b_x32(trow + ca_o_col(1) + (uint32_t)c0, ow);
-            tmem_wait_ld();
-            if (a1 != 0.0f) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                ov[c] = __float_as_uint(__uint_as_float(ov[c]) * a0 + __uint_as_float(ow[c]) * a1);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t ow[16];
+              tmem_ld_32x32b<16>(trow + ca_o_col(1) + col + 16u * (uint32_t)h, ow);
+              tmem_wait_ld();
+              if (a1 != 0.0f) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  ov[16 * h + c] = __float_as_uint(__uint_as_float(ov[16 * h + c]) * a0 + __uint_as_float(ow[c]) * a1);
+              }
             }
           }
           if (specials && valid) {
             uint32_t tmp[32];  // (not ov itself: its address would put it in memory)
 #pragma unroll
             for (int c = 0; c < 32; ++c) tmp[c] = ov[c];
-            ca_add_special<TYPE>(p, sh, ds, d.b, d.kvh, D, pos, c0, tmp);
+            ca_add_special<TYPE>(p, sh, ds, d.b, d.kvh, D, pos, (int)col, tmp);
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = tmp[c];
           }
-          // through the warp's rows of Q (whose products are complete), so that lanes write whole lines
-          uint4* mine = reinterpret_cast<uint4*>(qt + lane * 128);
-          const int words = cut ? 8 : 4, from = cut ? 0 : (c0 >> 3) & 4;
           if (cut) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              mine[c ^ (lane & 7)] = make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]);
+            for (int c = 0; c < 8; ++c) {
+              put(c & (LW - 1), make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]));
+              if ((c & (LW - 1)) == LW - 1) flush(c0 / 4 + c - (LW - 1));
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -902,21 +1073,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
               w.y = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 2]) * il, __uint_as_float(ov[8 * c + 3]) * il);
               w.z = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 4]) * il, __uint_as_float(ov[8 * c + 5]) * il);
               w.w = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 6]) * il, __uint_as_float(ov[8 * c + 7]) * il);
-              mine[(from + c) ^ (lane & 7)] = w;
+              put(c0 / 8 + c, w);
             }
+            if (c0 / 8 + 4 == LW) flush(0);
           }
-          if (from + words < 8) continue;  // half a line
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + (lane >> 3), c = lane & 7;
-            const int64_t to = __shfl_sync(0xffffffffu, place, r);
-            if ((rows_ok >> r) & 1u)
-              dst[to + (cut ? c0 / 4 : (c0 & ~63) / 8) + c] = *reinterpret_cast<const uint4*>(qt + r * 128 + ((c ^ (r & 7)) << 4));
-          }
-          __syncwarp();
         }
-        if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
+        if (cut && st_ok && hb == 0) wk.part_ml[pi] = make_float2(m, l);
       }
       if (!two) {  // slot 1's scores and sums may be written again
         if (t == 0) {
@@ -940,7 +1102,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             break;
           }
           if (lane == 0) {
-            int* done = wk.done + (in_bounds(p.err, d.first_cut, C) ? d.first_cut : 0);
+            int* done = wk.done + (in_bounds(p.err, d.first_cut, wk.ctas) ? d.first_cut : 0);
             const bool last = atomic_add_acq_rel(done, n) + n == d.nt;
             if (last) *done = 0;
             *(volatile int*)&sh->last = last ? 1 : 0;
@@ -954,100 +1116,25 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         ++cut_parts;
         if (*(volatile int*)&sh->last) {
-          // the unit's pieces, merged in the order of the keys. Warp w of the eight takes the
-          // rows w, w + 8, ..; lane i keeps the reference and the sum of the i-th of them
+          // the unit's pieces, merged in the order of the keys: their places first, each warp for itself
           __threadfence();
-          constexpr int V = D / 32;  // columns a lane
-          const int w8 = warp - 4, mine8 = rows > w8 ? (rows - w8 + 7) / 8 : 0;
-          const int c_first = d.first_cut - 1;
-          int c_last = c_first;  // the last CTA with a piece
-          {
-            int c = c_first + 1 + lane;
-            unsigned in;
-            while ((in = __ballot_sync(0xffffffffu, c < C && bound(c) < d.u0 + d.v)) == 0xffffffffu) c += 32;
-            c_last = c - lane - 1 + __popc(in);
+          int* list = reinterpret_cast<int*>(stage);
+          int np = 0;
+          for (int cb = d.first_cut - 1;; cb += 32) {
+            const int c = cb + lane;
+            const bool in = c < C && bound(c) < d.u0 + d.v;
+            const int from = in ? cut_at(c, d.u0, d.v, d.nt) : 0, to = in ? cut_at(c + 1, d.u0, d.v, d.nt) : 0;
+            const unsigned has = __ballot_sync(0xffffffffu, to > from);
+            if (to > from) list[np + __popc(has & ((1u << lane) - 1u))] = (2 * c + (from == 0 ? 1 : 0)) * wk.rows_cap;
+            np += __popc(has);
+            if (!__all_sync(0xffffffffu, in)) break;
           }
-          // the place of CTA c's piece in the workspace (rows), -1 where it has none; lane k of a round: c = cb + k
-          auto piece = [&](int c) {
-            if (c > c_last) return int64_t(-1);
-            const int from = cut_at(c, d.u0, d.v, d.nt), to = cut_at(c + 1, d.u0, d.v, d.nt);
-            return to > from ? (int64_t)(2 * c + (from == 0 ? 1 : 0)) * wk.rows_cap : int64_t(-1);
-          };
-          const int row_i = w8 + 8 * min(lane, max(mine8 - 1, 0));
-          float M = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-          for (int turn = 0; turn < 2; ++turn)
-            for (int cb = c_first; cb <= c_last; cb += 32) {
-              const int64_t place = piece(cb + lane);
-#pragma unroll 4
-              for (int k = 0; k < min(32, c_last - cb + 1); ++k) {
-                const int64_t at = __shfl_sync(0xffffffffu, place, k);
-                const float2 ml = at >= 0 ? __ldcg(&wk.part_ml[at + row_i]) : make_float2(-INFINITY, 0.0f);
-                if (ml.y == 0.0f) continue;  // none of the piece's keys is seen
-                if (turn == 0)
-                  M = fmaxf(M, ml.x);
-                else
-                  sum += ex2(ml.x - M) * ml.y;
-              }
-            }
-          const float inv = 1.0f / sum;
-          auto merge = [&](int first_i, auto count) {  // that many rows at once
-            constexpr int N = decltype(count)::value;
-            float acc[N][V];
-#pragma unroll
-            for (int q = 0; q < N; ++q)
-#pragma unroll
-              for (int v = 0; v < V; ++v) acc[q][v] = 0.0f;
-            for (int cb = c_first; cb <= c_last; cb += 32) {
-              const int64_t place = piece(cb + lane);
-#pragma unroll(N == 1 ? 8 : 1)
-              for (int k = 0; k < min(32, c_last - cb + 1); ++k) {
-                const int64_t at = __shfl_sync(0xffffffffu, place, k);
-#pragma unroll
-                for (int q = 0; q < N; ++q) {
-                  const int i8 = first_i + q;
-                  const float Mq = __shfl_sync(0xffffffffu, M, i8);
-                  if (at < 0 || i8 >= mine8) continue;
-                  const int64_t row = at + w8 + 8 * i8;
-                  const float2 ml = __ldcg(&wk.part_ml[row]);
-                  const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - Mq);  // (a piece without visible keys has zeros)
-                  const float* o = wk.part_o + row * D + V * lane;
-                  if constexpr (V == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
-                    acc[q][0] += f * x.x;
-                    acc[q][1] += f * x.y;
-                    acc[q][2] += f * x.z;
-                    acc[q][3] += f * x.w;
-                  } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
-                    acc[q][0] += f * x.x;
-                    acc[q][1] += f * x.y;
-                  }
-                }
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < N; ++q) {
-              const int i8 = first_i + q;
-              const float iq = __shfl_sync(0xffffffffu, inv, i8 & 31);
-              if (i8 >= mine8) continue;
-              const int R2 = d.row0 + w8 + 8 * i8, j2 = wk.by_g(R2);
-              if (!in_bounds(p.err, d.at + j2, p.T)) continue;
-              uint32_t* to = reinterpret_cast<uint32_t*>(
-                  static_cast<uint16_t*>(p.out) + ((int64_t)(d.at + j2) * p.H + d.kvh * G + R2 - j2 * G) * D + V * lane);
-              if constexpr (V == 4)
-                *reinterpret_cast<uint2*>(to) = make_uint2(ca_pack<TYPE>(acc[q][0] * iq, acc[q][1] * iq),
-                                                           ca_pack<TYPE>(acc[q][2] * iq, acc[q][3] * iq));
-              else
-                *to = ca_pack<TYPE>(acc[q][0] * iq, acc[q][1] * iq);
-            }
-          };
+          __syncwarp();
           // many rows have few pieces, many pieces few rows: loads in flight along the one or the other
-          if (mine8 > 4) {
-            for (int i8 = 0; i8 < mine8; i8 += 4) merge(i8, CaInt<4>());
-          } else {
-            for (int i8 = 0; i8 < mine8; ++i8) merge(i8, CaInt<1>());
-          }
+          if (np <= 2)
+            ca_merge<TYPE, D, 4, 2>(p, wk, d, list, np, warp - 4, lane);
+          else
+            ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane);
         }
       }
       __syncwarp();

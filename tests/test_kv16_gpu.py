@@ -259,15 +259,16 @@ def test_bad_pages_and_lengths():
         torch.cuda.synchronize()
         assert sv.check_device_status() == INPUT, (lens, starts)
         at = _starts(c.counts)
-        for b in range(3):
-            part = out[at[b]:at[b + 1]]
-            assert (part == 7).all() if b in left else torch.equal(part, good[at[b]:at[b + 1]]), (lens, starts, b)
+        assert all((out[at[b]:at[b + 1]] == 7).all() for b in left), (lens, starts)
+        # the others' rows, by the bound: where a request's keys are cut depends on the batch, and so the sums' order
+        c.check(out, requests=[b for b in range(3) if b not in left])
     # a request that brings nothing may have any length
     out = torch.full_like(good, 7.0)
     sv.kv16_attention(c.q, c.cache, 1, c.table.to(dev()), _i32([200, -5, 100]), row_start=_i32([0, 5, 5, 5]), out=out)
     torch.cuda.synchronize()
     assert sv.check_device_status() == 0
-    assert torch.equal(out[:5], good[:5]) and (out[5:] == 7).all()
+    c.check(out, requests=[0])
+    assert (out[5:] == 7).all()
     # falling rows: reported, nothing out of bounds
     sv.kv16_attention(c.q, c.cache, 1, c.table.to(dev()), _i32(c.lens), row_start=_i32([0, 12, 5, 18]), out=out)
     torch.cuda.synchronize()
