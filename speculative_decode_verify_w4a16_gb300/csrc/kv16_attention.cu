@@ -732,12 +732,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err);
         }
         const int next = i + (two ? 1 : 2);  // the tile whose scores go out behind these sums
-        if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
         if (two) {
           if (ok && i < upto0) {
             ok = sums(0, i, i == 0, false);
+            if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
             if (ok && next < upto0) scores(0, next, false);
             if (ok && next >= upto0) umma_commit_warp(&sh->o_full[0]);
+          } else if (ok && next < n) {
+            ok = landed(buf + 2u * (uint32_t)next);
           }
           ok = ok && sums(1, i, i == 0, true);
           if (ok && next < n) scores(1, next, true);
@@ -745,6 +747,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         } else {
           const int t = i & 1;
           ok = ok && sums(t, i, i == t, true);
+          if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
           if (ok && next < n) scores(t, next, true);
           if (ok && next >= n) umma_commit_warp(&sh->o_full[t]);
         }
@@ -825,23 +828,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int ds = seq % kCaDesc;
       if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
       const CaPart& d = sh->part[ds];
-      const int lo = d.lo, n = d.hi - lo, rows = d.rows;
+      const int n = d.hi - d.lo;
       if (n <= 0) break;
-      const bool two = rows > 128;
-      const int slot_row = two ? 128 * t : 0, ur = slot_row + rl;  // the slot's first row, this thread's row of the unit
-      const bool valid = ur < rows;
-      const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = d.past + j;
-      const int head = d.kvh * G + R - j * G;
+      const bool two = d.rows > 128;
       // this warp's part of the slot's Q (half the columns, or half the rows), and its buffer for the results
       uint8_t* qt = smem + t * L::kTile + qd * 32 * 128;
       if (two || t == 0) {  // 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
-        const int c = lane & 7;
+        const int c = lane & 7, u0 = (two ? 128 * t : 0) + qd * 32;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int k = D == 128 ? kk : 4 * hb + kk, h = D == 128 ? hb : 0;
-          const int r = 4 * k + (lane >> 3), u = slot_row + qd * 32 + r;
-          const int R2 = d.row0 + (u < rows ? u : 0), j2 = wk.by_g(R2);
-          const bool there = u < rows && in_bounds(p.err, d.at + j2, p.T);
+          const int r = 4 * k + (lane >> 3), u = u0 + r;
+          const int R2 = d.row0 + (u < d.rows ? u : 0), j2 = wk.by_g(R2);
+          const bool there = u < d.rows && in_bounds(p.err, d.at + j2, p.T);
           const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(d.at + j2) * p.q_stride +
                                 (int64_t)(d.kvh * G + R2 - j2 * G) * D + h * 64 + c * 8;
           ca_copy16(qt + h * L::kHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src : p.q, there);
@@ -852,9 +851,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_ready[t][ds]);
       int nt = (n - t + 1) / 2;
-      if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - lo, 0), n);
-      const int gw = d.gw, gc = d.gc, key_base = (d.tile0 + lo) * kCaKeys;
-      const bool any_row = __any_sync(0xffffffffu, valid);
+      if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
+      const int gw = d.gw, gc = d.gc;
+      bool any_row;
+      int rel;  // the row's position, from the first key of the part's first tile and this half on
+      {
+        const int u = (two ? 128 * t : 0) + rl;
+        any_row = __any_sync(0xffffffffu, u < d.rows);
+        rel = d.past + wk.by_g(d.row0 + (u < d.rows ? u : 0)) - (d.tile0 + d.lo) * kCaKeys - 64 * hb;
+      }
       float m = -INFINITY, l = 0.0f;
       for (int jt = 0; jt < nt; ++jt, ++sc) {
         const int i = two ? jt : 2 * jt + t;
@@ -868,26 +873,34 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           continue;
         }
         tc_fence_after();
-        uint32_t sv[2][32];
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb), sv[0]);
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb) + 32u, sv[1]);
-        tmem_wait_ld();
-        if (i < gw || i >= gc) {
-          const int top = pos - key_base - i * kCaKeys - 64 * hb;  // seen: bottom < c <= top
-          const int bottom = p.window > 0 ? top - p.window : -1;
+        // The scores pass through the registers 32 columns at a time, the last ones twice: all 64 beside what the loop keeps
+        // do not fit the 96 registers that 640 threads have (spilled, a tile took a fifth longer)
+        const bool masked = i < gw || i >= gc;
+        auto mask = [&](uint32_t* x, int first, int count) {
+          const int top = rel - i * kCaKeys - first;  // seen: bottom < c <= top
+          const int bottom = p.window > 0 ? top - p.window : -1 - first;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < 32; ++c)
+            if (c < count && (c > top || c <= bottom)) x[c] = __float_as_uint(-INFINITY);
+        };
+        auto largest = [&](const uint32_t* x) {
+          float m4[4];
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (32 * h + c > top || 32 * h + c <= bottom) sv[h][c] = __float_as_uint(-INFINITY);
-        }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int c = 0; c < 4; ++c) m4[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1]));
-        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int c = 4; c < 16; ++c)
+            m4[c & 3] = max3f(m4[c & 3], __uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        };
+        uint32_t sv[32];
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb) + 32u, sv);
+        tmem_wait_ld(sv);
+        if (masked) mask(sv, 32, 32);
+        float mx = largest(sv);
+        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb), sv);
+        tmem_wait_ld(sv);
+        if (masked) mask(sv, 0, 32);
+        mx = fmaxf(mx, largest(sv));
         // the row's largest score, from both halves (the next tile's is written when both have read this one)
         *(volatile float*)&sh->top[t][hb][rl] = mx;
         __syncwarp();
@@ -909,7 +922,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           for (int c0 = hb * (D / 2); c0 < (hb + 1) * (D / 2); c0 += 16) {
             uint32_t ov[16];
             tmem_ld_32x32b<16>(trow + ca_o_col(t) + (uint32_t)c0, ov);
-            tmem_wait_ld();
+            tmem_wait_ld(ov);
 #pragma unroll
             for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * cf);
             tmem_st_32x32b_x16(trow + ca_o_col(t) + (uint32_t)c0, ov);
@@ -918,13 +931,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nu2 = f2_pack(-u, -u);
         uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
+        auto weigh = [&](const uint32_t* x, int first) {  // 16 columns
+          uint32_t pr[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pr[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 8; ++c) {
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[h][2 * c]), __uint_as_float(sv[h][2 * c + 1])), sc2, nu2), x0, x1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2), x0, x1);
             const float e0 = ex2(x0), e1 = ex2(x1);
             pr[c] = ca_pack<TYPE>(e0, e1);
             const uint64_t r2 = f2_pack(e0, e1);
@@ -933,8 +945,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             else
               la = f2_add(la, r2);
           }
-          tmem_st_32x32b_x16(trow + ca_s_col(t, hb) + 16u * (uint32_t)h, pr);
-        }
+          tmem_st_32x32b_x8(trow + ca_s_col(t, hb) + (uint32_t)(first / 2), pr);
+        };
+        uint32_t s2[16], s3[16];
+        weigh(sv, 0);
+        tmem_ld_32x32b<16>(trow + ca_s_col(t, hb) + 32u, s2);
+        weigh(sv + 16, 16);
+        tmem_wait_ld(s2);
+        if (masked) mask(s2, 32, 16);
+        tmem_ld_32x32b<16>(trow + ca_s_col(t, hb) + 48u, s3);
+        weigh(s2, 32);
+        tmem_wait_ld(s3);
+        if (masked) mask(s3, 48, 16);
+        weigh(s3, 48);
         {
           float a0, a1, c0, c1;
           f2_unpack(la, a0, a1);
@@ -963,7 +986,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         tc_fence_after();
         tmem_ld_32x32b_x8(trow + ca_s_col(t, hb ^ 1), st);
-        tmem_wait_ld();
+        tmem_wait_ld(st);
         l += __uint_as_float(st[0]);
       }
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
@@ -985,7 +1008,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           tc_fence_after();
           uint32_t st[8];
           tmem_ld_32x32b_x8(trow + ca_s_col(1, 0) + 8u, st);
-          tmem_wait_ld();
+          tmem_wait_ld(st);
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
           if (n > 1 && !(l1 == 0.0f)) {
             const float M = fmaxf(m, m1);
@@ -996,8 +1019,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
         }
       }
-      const bool cut = n < d.nt;
-      const int64_t slot = 2 * cta + (lo > 0 ? 0 : 1);
+      // the row again, from the descriptor (kept over the tiles it would cost registers there)
+      const volatile CaPart& e = sh->part[ds];
+      const int rows = e.rows, ur = (two ? 128 * t : 0) + rl;
+      const bool valid = ur < rows;
+      const int R = e.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = e.past + j;
+      const int head = e.kvh * G + R - j * G;
+      const bool cut = n < e.nt;
+      const int64_t slot = 2 * cta + (e.lo > 0 ? 0 : 1);
       constexpr int LW = D / 16;  // 16-byte words of a row in the buffer: half a row's columns, rounded
       uint8_t* stage = D == 128 ? qt + hb * L::kHalf : qt + hb * 2048;
       if ((two || t == 0) && any_row) {
@@ -1033,7 +1062,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           uint32_t ov[32];
           if (nt > 0) {
             tmem_ld_32x32b_x32(trow + ca_o_col(t) + col, ov);
-            tmem_wait_ld();
+            tmem_wait_ld(ov);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = 0u;
@@ -1043,7 +1072,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             for (int h = 0; h < 2; ++h) {
               uint32_t ow[16];
               tmem_ld_32x32b<16>(trow + ca_o_col(1) + col + 16u * (uint32_t)h, ow);
-              tmem_wait_ld();
+              tmem_wait_ld(ow);
               if (a1 != 0.0f) {
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
