@@ -24,10 +24,9 @@
 //                 sees in part, and takes out NaN and infinities, which a weight
 //                 of zero would not hide; rows that do see them get them added
 //                 at the end
-//   warps 4 - 19  the softmax, two warpgroups a slot that take its tiles in turn,
-//                 one row a thread: scores from TMEM, running maximum and sum in
-//                 fp32, weights rounded to the cache's type back into TMEM over
-//                 the scores
+//   warps 4 - 11  the softmax of slot 0 and 1, one row a thread: scores from TMEM,
+//                 weights and their sum in fp32, the weights rounded to the
+//                 cache's type back into TMEM over the scores
 // With more than 128 rows the two slots are two row tiles, which share every
 // key tile; with fewer they take the key tiles in turn and are merged at the
 // part's end. While one slot's softmax runs, the tensor pipe works for the other.
@@ -40,29 +39,31 @@
 
 namespace w4a16 {
 
-constexpr int kCaThreads = 640;
-constexpr int kCaKeys = 128;  // keys of a tile: two pages
-constexpr int kCaDesc = 2;    // parts described ahead
-constexpr int kCaOk = 8;      // guarded tiles that the guard may be ahead: more than the ring holds
-constexpr int kCaSpecial = 6;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
+constexpr int kCaThreads = 384;
+constexpr int kCaKeys = 64;   // keys of a tile: a page
+constexpr int kCaDesc = 4;    // parts described ahead
+constexpr int kCaOk = 16;     // guarded tiles that the guard may be ahead: more than the ring holds
+constexpr int kCaSpecial = 12;  // guarded tiles of a part, at most (256 tokens' own keys, and as many where a window ends)
 
 // The weights a key tile has in the split: two row tiles, or one.
 constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
 constexpr int kCaOverhead = 256;  // keys that a unit's start and end are worth
-constexpr int kCaLeast = 4;       // tiles a CTA has at least, where units are cut
-constexpr int kCaMerge = 6;       // tiles that a cut is worth
+constexpr int kCaLeast = 8;       // tiles a CTA has at least, where units are cut
+constexpr int kCaMerge = 12;      // tiles that a cut is worth
 
-// Weights are taken against a reference that is raised only by a maximum more
-// than `lazy` (log2) above it, so that the sums in TMEM are seldom rescaled. In
-// fp16 the reference itself stands for 2^8: weights up to 2^14 fit, and those
-// down to 2^-22 of the reference keep all their bits (2^-32: some).
+// Weights are taken against a reference: the largest score of the first tile that
+// the row sees keys of. It is raised (and the sums so far, in TMEM, rescaled) by a
+// tile whose weights, 64 at a time, add up to more than this; no weight is then
+// larger, and no tile's maximum has to be found otherwise. In fp16 the reference
+// itself stands for 2^8: weights fit up to 2^15, and down to 2^-22 of the
+// reference they keep all their bits (2^-32: some).
 template <int TYPE>
-constexpr float kCaLazy = TYPE == 0 ? 8.0f : 6.0f;
+constexpr float kCaMost = TYPE == 0 ? 256.0f : 32768.0f;
 template <int TYPE>
 constexpr float kCaUp = TYPE == 0 ? 0.0f : 8.0f;
 
 struct CaMaps {
-  CUtensorMap k, v;  // [pages * Hkv][64][D]
+  CUtensorMap k, v;  // [pages * Hkv][D / 64][64][64]: halves of 64 columns apart, as they lie in shared memory
 };
 struct CaWork {
   FastDiv by_g;
@@ -86,16 +87,15 @@ struct CaPart {
 };
 struct CaSpecial {
   int key0;
-  uint32_t keys[4];  // of the tile's 128: those with a value that is not finite
+  uint32_t keys[2];  // of the tile's 64: those with a value that is not finite
 };
 struct CaShared {
-  uint64_t full[10], free[10];
-  uint64_t s_full[2], p_full[2][2], o_full[2], fin;
-  uint64_t mark[2][2][4], sums[2], stat, read, stored, told;
+  uint64_t full[20], free[20];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], fin[2];
+  uint64_t stat, read, stored, told;
   uint64_t landed[kCaOk], ok[kCaOk];  // guarded values: in shared memory, looked through
   uint64_t desc_full[kCaDesc], desc_free[kCaDesc], q_ready[2][kCaDesc];
   CaPart part[kCaDesc];
-  float top[2][2][128];  // the largest score of each row in a warpgroup's half of a tile
   int specials[kCaDesc];
   CaSpecial special[kCaDesc][kCaSpecial];
   uint32_t tmem;
@@ -104,18 +104,20 @@ struct CaShared {
 
 template <int D>
 struct CaLayout {
-  static constexpr int kHalf = 128 * 128;  // 128 rows of 64 columns
+  static constexpr int kQHalf = 128 * 128;  // 128 rows of 64 columns
+  static constexpr int kQ = D / 64 * kQHalf;
+  static constexpr int kHalf = kCaKeys * 128;  // 64 keys of 64 columns
   static constexpr int kTile = D / 64 * kHalf;
-  static constexpr int kBufs = D == 128 ? 5 : 10;
-  static constexpr int kRingOff = 2 * kTile;
+  static constexpr int kBufs = D == 128 ? 10 : 20;
+  static constexpr int kRingOff = 2 * kQ;
   static constexpr int kSharedOff = kRingOff + kBufs * kTile;
   static constexpr int kTotal = kSharedOff + (int)sizeof(CaShared);
   static_assert(kTotal <= 227 * 1024, "shared memory");
-  static_assert(kBufs <= 10 && kBufs / 2 < kCaOk, "rings");
+  static_assert(kBufs <= 20 && kBufs / 2 < kCaOk, "rings");
 };
 
-// TMEM columns: a slot's scores, each half's weights over the first half of them, and its sums
-__device__ __forceinline__ uint32_t ca_s_col(int t, int hb) { return 128u * (uint32_t)t + 64u * (uint32_t)hb; }
+// TMEM columns: a slot's two score buffers (a tile's weights over the first half of its scores), and its sums
+__device__ __forceinline__ uint32_t ca_s_col(int t, int sb) { return 128u * (uint32_t)t + 64u * (uint32_t)sb; }
 __device__ __forceinline__ uint32_t ca_o_col(int t) { return 256u + 128u * (uint32_t)t; }
 
 // 16 bytes to shared memory, asynchronously; zeros where there are none.
@@ -307,15 +309,15 @@ __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaSha
   }
 }
 
-// A cut unit's rows from its np pieces, by sixteen warps: warp w has the rows w, w +
-// 16, .., a lane D / 32 columns; N rows and K pieces at a time, whose loads go out
+// A cut unit's rows from its np pieces, by eight warps: warp w has the rows w, w +
+// 8, .., a lane D / 32 columns; N rows and K pieces at a time, whose loads go out
 // together.
 template <int TYPE, int D, int N, int K>
 __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk, const CaPart& d, const int* list, int np,
                                       int w, int lane) {
   constexpr int V = D / 32;
   const int G = (int)wk.by_g.d, rows = d.rows;
-  for (int r0 = w; r0 < rows; r0 += 16 * N) {
+  for (int r0 = w; r0 < rows; r0 += 8 * N) {
     float acc[N][V], M[N], S[N];
 #pragma unroll
     for (int q = 0; q < N; ++q) {
@@ -332,8 +334,8 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
         const int at = k0 + k < np ? list[k0 + k] : 0;
 #pragma unroll
         for (int q = 0; q < N; ++q) {
-          const bool there = k0 + k < np && r0 + 16 * q < rows;
-          const int64_t row = (int64_t)at + (there ? r0 + 16 * q : 0);
+          const bool there = k0 + k < np && r0 + 8 * q < rows;
+          const int64_t row = (int64_t)at + (there ? r0 + 8 * q : 0);
           ml[q][k] = there ? __ldcg(&wk.part_ml[row]) : make_float2(-INFINITY, 0.0f);
           const float* x = wk.part_o + row * D + V * lane;
           if constexpr (V == 4) {
@@ -371,7 +373,7 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) {
-      const int r = r0 + 16 * q;
+      const int r = r0 + 8 * q;
       if (r >= rows) continue;
       const float inv = 1.0f / S[q];
       const int R = d.row0 + r, j = wk.by_g(R);
@@ -405,30 +407,28 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NB; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->free[i], 1);
+      mbar_init(&sh->free[i], 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh->s_full[t], 1);
-      mbar_init(&sh->o_full[t], 1);
+      mbar_init(&sh->fin[t], 1);
       for (int k = 0; k < 2; ++k) {
+        mbar_init(&sh->s_full[t][k], 1);
         mbar_init(&sh->p_full[t][k], 4);
-        for (int q = 0; q < 4; ++q) mbar_init(&sh->mark[t][k][q], 1);
+        mbar_init(&sh->pv_done[t][k], 1);
       }
-      mbar_init(&sh->sums[t], 8);
     }
-    mbar_init(&sh->fin, 1);
     mbar_init(&sh->stat, 4);
-    mbar_init(&sh->read, 8);
-    mbar_init(&sh->stored, 16);
+    mbar_init(&sh->read, 4);
+    mbar_init(&sh->stored, 8);
     mbar_init(&sh->told, 1);
     for (int i = 0; i < kCaOk; ++i) {
       mbar_init(&sh->landed[i], 1);
       mbar_init(&sh->ok[i], 1);
     }
     for (int i = 0; i < kCaDesc; ++i) {
-      for (int t = 0; t < 2; ++t) mbar_init(&sh->q_ready[t][i], 8);
+      for (int t = 0; t < 2; ++t) mbar_init(&sh->q_ready[t][i], 4);
       mbar_init(&sh->desc_full[i], 1);
-      mbar_init(&sh->desc_free[i], 18);
+      mbar_init(&sh->desc_free[i], 11);
     }
     fence_mbarrier_init();
   }
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           ok = false;
           break;
         }
-        // key tiles t with 128 t + 127 <= first_pos, and 128 t > last_pos - window, are seen whole by every row
+        // key tiles t with 64 t + 63 <= first_pos, and 64 t > last_pos - window, are seen whole by every row
         const int whole = (t.first_pos + 1) / kCaKeys - t.tile0 - lo;
         const int in_window =
             p.window > 0 && t.last_pos >= p.window ? (t.last_pos - p.window) / kCaKeys + 1 - t.tile0 - lo : 0;
@@ -583,30 +583,24 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->desc_full[ds]);
         ++seq;
-        // the pages of 16 tiles at a time, a lane an entry; those that no row sees any key of are not read
-        const int blk_lo = (p.window > 0 ? max(0, t.first_pos - p.window + 1) : 0) / 64, blk_hi = t.last_pos / 64;
+        // the pages of 32 tiles at a time, a lane an entry
         const int32_t* row = p.table + (int64_t)b * p.max_blocks;
-        int base = 2 * (t.tile0 + lo);
+        int base = t.tile0 + lo;
         auto entries = [&]() {
-          const int blk = base + lane;
-          if (blk < blk_lo || blk > blk_hi || blk >= 2 * (t.tile0 + hi) || !in_bounds(p.err, blk, p.max_blocks)) return -1;
-          const int page = row[blk];
+          if (base + lane >= t.tile0 + hi || !in_bounds(p.err, base + lane, p.max_blocks)) return -1;
+          const int page = row[base + lane];
           if (page >= 0 && page < p.pages) return page;
           report_error(p.err, kErrInput);
           return -1;
         };
         int now = entries();
         for (int i = lo; ok && i < hi; ++i) {
-          if (2 * (t.tile0 + i) - base >= 32) {
+          if (t.tile0 + i - base >= 32) {
             base += 32;
             now = entries();
           }
-          int z[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int page = __shfl_sync(0xffffffffu, now, 2 * (t.tile0 + i) - base + k);
-            z[k] = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
-          }
+          const int page = __shfl_sync(0xffffffffu, now, t.tile0 + i - base);
+          const int z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
           // guarded values land at a barrier of their own: the guard tells when they may be used
           const bool guard = i - lo < gw || i - lo >= gc;
           if (lane == 0) {
@@ -621,12 +615,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 bar = &sh->landed[guarded % kCaOk];
               }
               mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                  tma_load_3d(smem + L::kRingOff + s * L::kTile + h * L::kHalf + k * 64 * 128, kv ? &maps.v : &maps.k, 64 * h,
-                              0, z[k], bar);
+              tma_load_4d(smem + L::kRingOff + s * L::kTile, kv ? &maps.v : &maps.k, 0, 0, 0, z, bar);
               issued = (uint32_t)kv + 1u;  // (of this tile, where a wait runs out)
             }
           }
@@ -665,13 +654,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       if (!test_skip_copy(k)) ca_wait(&sh->full[k % NB], (k / NB) & 1u, p.err);
     for (uint32_t k = guarded > kCaOk ? guarded - kCaOk : 0; k < guarded; ++k)
       ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err);
-  } else if (warp == 1) {
-    // --------------------------------------------------------------- MMA
-    // One warp for both slots, in turn: what a slot waits for is then done while the other slot's softmax runs. (A warp a
-    // slot: both slots' products end up side by side on the tensor pipe, and then both wait for their softmax.)
+  } else if (warp <= 2) {
+    // ------------------------------------------------------ MMA, slot t
+    // The scores are a tile ahead of the weights, so that neither side waits for the other's latency.
+    const int t = warp - 1;
     constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
     const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
-    uint32_t buf = 0, oks = 0, pc[2] = {0u, 0u};  // buffers, guarded tiles and each slot's weights so far
+    uint32_t buf = 0, oks = 0, sc = 0, pc = 0;  // buffers, guarded tiles, scores issued and weights used so far
     bool ok = true, issued = false;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -680,89 +669,77 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int n = d.hi - d.lo, gw = d.gw, gc = d.gc;
       if (n <= 0) break;
       const bool two = d.rows > 128;
-      // row tiles: slot 0's rows may see fewer tiles than slot 1's, which see them all
-      const int upto0 = two ? min(max(ca_slot_last(wk, d, 0) / kCaKeys + 1 - d.tile0 - d.lo, 0), n) : n;
-      auto at = [&](uint32_t x) { return smem_u32(smem + L::kRingOff + (x % NB) * L::kTile); };
-      auto landed = [&](uint32_t x) { return ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err); };
-      // S = Q K^T of slot t and tile i, and the barriers that it arrives at: the scores', the buffer's after its last use
-      auto scores = [&](int t, int i, bool last_use) {
-        const uint32_t q0 = smem_u32(smem + (two ? t : 0) * L::kTile), k0 = at(buf + 2u * (uint32_t)i);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * L::kHalf + 32 * (kk & 3));
-          umma_bf16_ss_warp(tmem + ca_s_col(t, 0), umma_desc_sw128_kmajor(q0 + off), umma_desc_sw128_kmajor(k0 + off),
-                            idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_warp(&sh->s_full[t]);
-        if (last_use) umma_commit_warp(&sh->free[(buf + 2u * (uint32_t)i) % NB]);
-        issued = true;
-      };
-      // O += P V, each half of the keys once its weights are there
-      auto sums = [&](int t, int i, bool first, bool last_use) {
-        const uint32_t v0 = at(buf + 2u * (uint32_t)i + 1u);
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          if (!ca_wait(&sh->p_full[t][hb], pc[t] & 1u, p.err)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, hb) + 8u * (uint32_t)kk,
-                              umma_desc_sw128_mnmajor(v0 + 2048u * (uint32_t)(4 * hb + kk), (uint32_t)L::kHalf, 1024u),
-                              idesc_o, (!first || hb > 0 || kk > 0) ? 1u : 0u);
-        }
-        ++pc[t];
-        if (last_use) umma_commit_warp(&sh->free[(buf + 2u * (uint32_t)i + 1u) % NB]);
+      // this slot's tiles: as far as its rows see where the slots are row tiles, every other one where they share the rows
+      const int upto = two ? min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n) : n;
+      const int step = two ? 1 : 2;
+      int i = two ? 0 : t;  // the tile whose scores come next
+      int at = 0;           // tiles before it are used or passed over
+      const uint64_t q0 = umma_desc_sw128_kmajor(smem_u32(smem + (two ? t : 0) * L::kQ));
+      // Each slot releases every buffer once: those it does not use as soon as they are there (a phase is never skipped).
+      auto pass = [&](int to) {
+        for (; at < to; ++at)
+          for (uint32_t x = buf + 2u * (uint32_t)at, e = x + 2u; x < e; ++x) {
+            if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+            if (lane == 0) mbar_arrive(&sh->free[x % NB]);
+            __syncwarp();
+          }
         return true;
       };
-      const uint32_t phase = (uint32_t)(seq / kCaDesc) & 1u;
-      // the first scores (both slots' warps are done with the part before; where they share the rows slot 0's load them)
-      ok = landed(buf) && ca_wait(&sh->q_ready[0][ds], phase, p.err);
-      if (ok && upto0 > 0) scores(0, 0, !two);
-      ok = ok && ca_wait(&sh->q_ready[1][ds], phase, p.err);
-      if (ok && two) scores(1, 0, true);
-      if (ok && !two && n > 1) {
-        ok = landed(buf + 2u);
-        if (ok) scores(1, 1, true);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        ok = landed(buf + 2u * (uint32_t)i + 1u);
-        if (ok && (i < gw || i >= gc)) {  // the guard has looked through the values
-          const uint32_t g = oks + (uint32_t)(i < gw ? i : gw + i - gc);
+      auto scores = [&]() {  // S = Q K^T
+        if (!pass(i)) return false;
+        const uint32_t x = buf + 2u * (uint32_t)i;
+        if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+        tc_fence_after();
+        const uint64_t k0 = umma_desc_sw128_kmajor(smem_u32(smem + L::kRingOff + (x % NB) * L::kTile));
+        const int sb = (int)(sc & 1u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)  // (the descriptors count in 16 bytes)
+          umma_bf16_ss_warp(tmem + ca_s_col(t, sb), q0 + (uint64_t)((kk >> 2) * L::kQHalf / 16 + 2 * (kk & 3)),
+                            k0 + (uint64_t)((kk >> 2) * L::kHalf / 16 + 2 * (kk & 3)), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit_warp(&sh->s_full[t][sb]);
+        umma_commit_warp(&sh->free[x % NB]);
+        issued = true;
+        ++sc;
+        at = i + 1;
+        i += step;
+        return true;
+      };
+      // (slot 1's warps are done with the part before, and where the slots share the rows slot 0's have loaded them)
+      if (i < upto && t == 1 && !two) ok = ca_wait(&sh->q_ready[0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err);
+      if (ok && i < upto) ok = ca_wait(&sh->q_ready[t][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
+      if (ok && i < upto) ok = scores();
+      // the scores two tiles on go out behind the product of the weights that lie in their buffer
+      for (int v = two ? 0 : t; ok && v < upto; v += step, ++pc) {
+        const uint32_t x = buf + 2u * (uint32_t)v + 1u;
+        const int sb = (int)(pc & 1u);
+        ok = ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err);
+        if (ok && (v < gw || v >= gc)) {  // the guard has looked through the values
+          const uint32_t g = oks + (uint32_t)(v < gw ? v : gw + v - gc);
           ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err);
         }
-        const int next = i + (two ? 1 : 2);  // the tile whose scores go out behind these sums
-        if (two) {
-          if (ok && i < upto0) {
-            ok = sums(0, i, i == 0, false);
-            if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
-            if (ok && next < upto0) scores(0, next, false);
-            if (ok && next >= upto0) umma_commit_warp(&sh->o_full[0]);
-          } else if (ok && next < n) {
-            ok = landed(buf + 2u * (uint32_t)next);
-          }
-          ok = ok && sums(1, i, i == 0, true);
-          if (ok && next < n) scores(1, next, true);
-          if (ok && next >= n) umma_commit_warp(&sh->o_full[1]);
-        } else {
-          const int t = i & 1;
-          ok = ok && sums(t, i, i == t, true);
-          if (ok && next < n) ok = landed(buf + 2u * (uint32_t)next);
-          if (ok && next < n) scores(t, next, true);
-          if (ok && next >= n) umma_commit_warp(&sh->o_full[t]);
-        }
+        ok = ok && ca_wait(&sh->p_full[t][sb], (pc >> 1) & 1u, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v0 =
+            umma_desc_sw128_mnmajor(smem_u32(smem + L::kRingOff + (x % NB) * L::kTile), (uint32_t)L::kHalf, 1024u);
+#pragma unroll
+        for (int kk = 0; kk < kCaKeys / 16; ++kk)  // O += P V
+          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, sb) + 8u * (uint32_t)kk, v0 + (uint64_t)(128 * kk),
+                            idesc_o, (v >= step || kk > 0) ? 1u : 0u);
+        umma_commit_warp(&sh->pv_done[t][sb]);
+        umma_commit_warp(&sh->free[x % NB]);
+        if (i < upto) ok = scores();
       }
+      ok = ok && pass(n);
       buf += 2u * (uint32_t)n;
       oks += (uint32_t)(gw + n - gc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
     }
     if (issued) {
-      umma_commit_warp(&sh->fin);  // tracks all of this warp's MMAs
-      ca_wait(&sh->fin, 0u, p.err);
+      umma_commit_warp(&sh->fin[t]);  // tracks all of this warp's MMAs
+      ca_wait(&sh->fin[t], 0u, p.err);
     }
-  } else if (warp == 2) {
-    // (no work)
   } else if (warp == 3) {
     // ------------------------------------------------------------ guard
     uint32_t buf = 0, oks = 0;
@@ -794,8 +771,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (__any_sync(0xffffffffu, ((nil[0] | nil[1] | nil[2] | nil[3]) & 0x7FFF7FFFu) != 0u)) {
           const int e = *(volatile int*)&sh->specials[ds];
           CaSpecial& sp = sh->special[ds][min(e, kCaSpecial - 1)];
-          if (lane < 4) sp.keys[lane] = 0u;
-          if (lane == 4) sp.key0 = (tile0 + lo + i) * kCaKeys;
+          if (lane < 2) sp.keys[lane] = 0u;
+          if (lane == 2) sp.key0 = (tile0 + lo + i) * kCaKeys;
           __syncwarp();
           for (int o = lane * 4; o < L::kTile; o += 128) {
             uint32_t* w = reinterpret_cast<uint32_t*>(v0 + o);
@@ -820,9 +797,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
   } else {
     // ---------------------------------------------------------- softmax
-    const int t = (warp - 4) >> 3, hb = ((warp - 4) >> 2) & 1, qd = warp & 3, rl = qd * 32 + lane;
+    const int t = (warp - 4) >> 2, qd = warp & 3, rl = qd * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
-    uint32_t sc = 0, oc = 0, marks = 0, parts = 0, shared_parts = 0, cut_parts = 0;
+    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    uint32_t sc = 0, shared_parts = 0, cut_parts = 0;
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -831,19 +809,25 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int n = d.hi - d.lo;
       if (n <= 0) break;
       const bool two = d.rows > 128;
-      // this warp's part of the slot's Q (half the columns, or half the rows), and its buffer for the results
-      uint8_t* qt = smem + t * L::kTile + qd * 32 * 128;
+      const int ur = (two ? 128 * t : 0) + rl;  // this thread's row of the unit
+      const bool valid = ur < d.rows;
+      const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = d.past + j;
+      const int head = d.kvh * G + R - j * G;
+      const bool any_row = __any_sync(0xffffffffu, valid);
+      // this warp's rows of the slot's Q, and its buffer for the results
+      uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;
       if (two || t == 0) {  // 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
-        const int c = lane & 7, u0 = (two ? 128 * t : 0) + qd * 32;
+        const int c = lane & 7;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int k = D == 128 ? kk : 4 * hb + kk, h = D == 128 ? hb : 0;
-          const int r = 4 * k + (lane >> 3), u = u0 + r;
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3), u = ur - lane + r;
           const int R2 = d.row0 + (u < d.rows ? u : 0), j2 = wk.by_g(R2);
           const bool there = u < d.rows && in_bounds(p.err, d.at + j2, p.T);
           const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(d.at + j2) * p.q_stride +
-                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + h * 64 + c * 8;
-          ca_copy16(qt + h * L::kHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src : p.q, there);
+                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + c * 8;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            ca_copy16(qt + h * L::kQHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src + 64 * h : p.q, there);
         }
         ca_copy_wait();
         fence_proxy_async_smem();
@@ -853,88 +837,34 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       int nt = (n - t + 1) / 2;
       if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
       const int gw = d.gw, gc = d.gc;
-      bool any_row;
-      int rel;  // the row's position, from the first key of the part's first tile and this half on
-      {
-        const int u = (two ? 128 * t : 0) + rl;
-        any_row = __any_sync(0xffffffffu, u < d.rows);
-        rel = d.past + wk.by_g(d.row0 + (u < d.rows ? u : 0)) - (d.tile0 + d.lo) * kCaKeys - 64 * hb;
-      }
+      const int rel = pos - (d.tile0 + d.lo) * kCaKeys;  // the row's position, from the part's first key on
       float m = -INFINITY, l = 0.0f;
       for (int jt = 0; jt < nt; ++jt, ++sc) {
-        const int i = two ? jt : 2 * jt + t;
-        if (!ca_wait(&sh->s_full[t], sc & 1u, p.err)) {
+        const int i = two ? jt : 2 * jt + t, buf = (int)(sc & 1u);
+        if (!ca_wait(&sh->s_full[t][buf], (sc >> 1) & 1u, p.err)) {
           ok = false;
           break;
         }
         if (!any_row) {  // (what the weights of these rows are does not matter)
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->p_full[t][hb]);
+          if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
           continue;
         }
         tc_fence_after();
-        // The scores pass through the registers 32 columns at a time, the last ones twice: all 64 beside what the loop keeps
-        // do not fit the 96 registers that 640 threads have (spilled, a tile took a fifth longer)
         const bool masked = i < gw || i >= gc;
-        auto mask = [&](uint32_t* x, int first, int count) {
-          const int top = rel - i * kCaKeys - first;  // seen: bottom < c <= top
-          const int bottom = p.window > 0 ? top - p.window : -1 - first;
+        auto mask = [&](uint32_t (&x)[32], int first) {  // columns first .. first + 31
+          const int top = rel - i * kCaKeys - first;    // seen: bottom < c <= top
+          const int bottom = p.window > 0 ? top - p.window : -1;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (c < count && (c > top || c <= bottom)) x[c] = __float_as_uint(-INFINITY);
+            if (c > top || c <= bottom) x[c] = __float_as_uint(-INFINITY);
         };
-        auto largest = [&](const uint32_t* x) {
-          float m4[4];
+        // the weights of 32 columns, as pairs of the cache's type, and their sum
+        auto weigh = [&](const uint32_t (&x)[32], uint32_t* pr, float u) {
+          const uint64_t nu2 = f2_pack(-u, -u);
+          uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) m4[c] = fmaxf(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-#pragma unroll
-          for (int c = 4; c < 16; ++c)
-            m4[c & 3] = max3f(m4[c & 3], __uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
-          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        };
-        uint32_t sv[32];
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb) + 32u, sv);
-        tmem_wait_ld(sv);
-        if (masked) mask(sv, 32, 32);
-        float mx = largest(sv);
-        tmem_ld_32x32b_x32(trow + ca_s_col(t, hb), sv);
-        tmem_wait_ld(sv);
-        if (masked) mask(sv, 0, 32);
-        mx = fmaxf(mx, largest(sv));
-        // the row's largest score, from both halves (the next tile's is written when both have read this one)
-        *(volatile float*)&sh->top[t][hb][rl] = mx;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->mark[t][hb][qd]);
-        if (!ca_wait(&sh->mark[t][hb ^ 1][qd], marks++ & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        mx = fmaxf(mx, *(volatile float*)&sh->top[t][hb ^ 1][rl]) * p.scale_log2;
-        float cf = 1.0f;
-        if (mx > m + kCaLazy<TYPE>) {
-          cf = m == -INFINITY ? 0.0f : ex2(m - mx);
-          m = mx;
-          l *= cf;
-        }
-        if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
-          // O holds the sums of the tiles before (the commit that announced these scores covers them); half the columns each
-#pragma unroll 1
-          for (int c0 = hb * (D / 2); c0 < (hb + 1) * (D / 2); c0 += 16) {
-            uint32_t ov[16];
-            tmem_ld_32x32b<16>(trow + ca_o_col(t) + (uint32_t)c0, ov);
-            tmem_wait_ld(ov);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * cf);
-            tmem_st_32x32b_x16(trow + ca_o_col(t) + (uint32_t)c0, ov);
-          }
-        }
-        const float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
-        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), nu2 = f2_pack(-u, -u);
-        uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
-        auto weigh = [&](const uint32_t* x, int first) {  // 16 columns
-          uint32_t pr[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 16; ++c) {
             float x0, x1;
             f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nu2), x0, x1);
             const float e0 = ex2(x0), e1 = ex2(x1);
@@ -945,61 +875,82 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             else
               la = f2_add(la, r2);
           }
-          tmem_st_32x32b_x8(trow + ca_s_col(t, hb) + (uint32_t)(first / 2), pr);
+          float a0, a1;
+          f2_unpack(f2_add(la, lb), a0, a1);
+          return a0 + a1;
         };
-        uint32_t s2[16], s3[16];
-        weigh(sv, 0);
-        tmem_ld_32x32b<16>(trow + ca_s_col(t, hb) + 32u, s2);
-        weigh(sv + 16, 16);
-        tmem_wait_ld(s2);
-        if (masked) mask(s2, 32, 16);
-        tmem_ld_32x32b<16>(trow + ca_s_col(t, hb) + 48u, s3);
-        weigh(s2, 32);
-        tmem_wait_ld(s3);
-        if (masked) mask(s3, 48, 16);
-        weigh(s3, 48);
-        {
-          float a0, a1, c0, c1;
-          f2_unpack(la, a0, a1);
-          f2_unpack(lb, c0, c1);
-          l += (a0 + a1) + (c0 + c1);
+        const uint32_t col = trow + ca_s_col(t, buf);
+        uint32_t sa[32], sb[32], pr[32];
+        auto load = [&]() {
+          tmem_ld_32x32b_x32(col, sa);
+          tmem_ld_32x32b_x32(col + 32u, sb);
+          tmem_wait_ld(sa);
+          tmem_wait_ld(sb);
+          if (masked) {
+            mask(sa, 0);
+            mask(sb, 32);
+          }
+        };
+        load();
+        float u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
+        float sum = weigh(sa, pr, u);
+        sum += weigh(sb, pr + 16, u);
+        const bool raise = m == -INFINITY || !(sum <= kCaMost<TYPE>);
+        if (__any_sync(0xffffffffu, raise)) {
+          // the reference becomes the largest score where it has to; the sums so far follow
+          load();
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sa[2 * c]), __uint_as_float(sa[2 * c + 1]));
+            m4[(c + 2) & 3] = max3f(m4[(c + 2) & 3], __uint_as_float(sb[2 * c]), __uint_as_float(sb[2 * c + 1]));
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          float cf = 1.0f;
+          if (raise && mx > m) {
+            cf = m == -INFINITY ? 0.0f : ex2(m - mx);
+            m = mx;
+            l *= cf;
+          }
+          if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
+            if (!ca_wait(&sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err)) {  // the sums of the tile before
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              tmem_ld_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, pr);
+              tmem_wait_ld(pr);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pr[c] = __float_as_uint(__uint_as_float(pr[c]) * cf);
+              tmem_st_32x32b_x32(trow + ca_o_col(t) + (uint32_t)c0, pr);
+            }
+          }
+          u = (m == -INFINITY ? 0.0f : m) - kCaUp<TYPE>;
+          sum = weigh(sa, pr, u);
+          sum += weigh(sb, pr + 16, u);
         }
+        l += sum;
+        tmem_st_32x32b_x32(col, pr);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[t][hb]);
+        if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
       }
-      // ---- the part's end: the warpgroups of a slot add up their sums, over TMEM; each then has half of the columns
-      if (ok && nt > 0) ok = ca_wait(&sh->o_full[t], oc++ & 1u, p.err);
+      // ---- the part's end
+      if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
       if (!ok) break;
       tc_fence_after();
-      {
-        uint32_t st[8] = {__float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        tmem_st_32x32b_x8(trow + ca_s_col(t, hb), st);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->sums[t]);
-        if (!ca_wait(&sh->sums[t], parts++ & 1u, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_ld_32x32b_x8(trow + ca_s_col(t, hb ^ 1), st);
-        tmem_wait_ld(st);
-        l += __uint_as_float(st[0]);
-      }
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
         if (t == 1) {  // hand over the reference and the sum through TMEM; the sums of values are there
-          if (hb == 0) {
-            uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_st_32x32b_x8(trow + ca_s_col(1, 0) + 8u, st);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->stat);
-          }
+          uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
+          tmem_st_32x32b_x8(trow + ca_s_col(1, 0), st);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->stat);
         } else {
           if (!ca_wait(&sh->stat, shared_parts & 1u, p.err)) {
             ok = false;
@@ -1007,7 +958,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           tc_fence_after();
           uint32_t st[8];
-          tmem_ld_32x32b_x8(trow + ca_s_col(1, 0) + 8u, st);
+          tmem_ld_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_ld(st);
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
           if (n > 1 && !(l1 == 0.0f)) {
@@ -1019,46 +970,37 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
         }
       }
-      // the row again, from the descriptor (kept over the tiles it would cost registers there)
-      const volatile CaPart& e = sh->part[ds];
-      const int rows = e.rows, ur = (two ? 128 * t : 0) + rl;
-      const bool valid = ur < rows;
-      const int R = e.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = e.past + j;
-      const int head = e.kvh * G + R - j * G;
-      const bool cut = n < e.nt;
-      const int64_t slot = 2 * cta + (e.lo > 0 ? 0 : 1);
-      constexpr int LW = D / 16;  // 16-byte words of a row in the buffer: half a row's columns, rounded
-      uint8_t* stage = D == 128 ? qt + hb * L::kHalf : qt + hb * 2048;
+      const bool cut = n < d.nt;
+      const int64_t slot = 2 * cta + (d.lo > 0 ? 0 : 1);
       if ((two || t == 0) && any_row) {
         const float il = cut ? 1.0f : 1.0f / l;
         const int64_t pi = slot * wk.rows_cap + ur;
         // the row's place, in 16-byte words: the result's, or the piece's in the workspace
-        const int64_t place = (cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8) + hb * (cut ? D / 8 : LW);
+        const int64_t place = (cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8) ;
         uint4* dst = cut ? reinterpret_cast<uint4*>(wk.part_o) : static_cast<uint4*>(p.out);
         const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
         const unsigned rows_ok = __ballot_sync(0xffffffffu, st_ok);
         const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
         const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
         const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
-        // through the warp's part of Q (whose products are complete), so that lanes write whole lines
+        // through the warp's rows of Q (whose products are complete), so that lanes write whole lines of 128 bytes
         auto put = [&](int word, uint4 w) {
-          *reinterpret_cast<uint4*>(stage + lane * (16 * LW) + ((word ^ (lane & (LW - 1))) << 4)) = w;
+          *reinterpret_cast<uint4*>(qt + lane * 128 + ((word ^ (lane & 7)) << 4)) = w;
         };
-        auto flush = [&](int word) {  // LW words of each row, from this one on
+        auto flush = [&](int word) {  // eight words of each row, from this one on
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < LW; ++k) {
-            const int r = (32 / LW) * k + lane / LW, c = lane % LW;
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3), c = lane & 7;
             const int64_t to = __shfl_sync(0xffffffffu, place, r);
             if ((rows_ok >> r) & 1u)
-              dst[to + word + c] =
-                  *reinterpret_cast<const uint4*>(stage + r * (16 * LW) + ((c ^ (r & (LW - 1))) << 4));
+              dst[to + word + c] = *reinterpret_cast<const uint4*>(qt + r * 128 + ((c ^ (r & 7)) << 4));
           }
           __syncwarp();
         };
 #pragma unroll 1
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          const uint32_t col = (uint32_t)(hb * (D / 2) + c0);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          const uint32_t col = (uint32_t)c0;
           uint32_t ov[32];
           if (nt > 0) {
             tmem_ld_32x32b_x32(trow + ca_o_col(t) + col, ov);
@@ -1090,10 +1032,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           if (cut) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              put(c & (LW - 1), make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]));
-              if ((c & (LW - 1)) == LW - 1) flush(c0 / 4 + c - (LW - 1));
-            }
+            for (int c = 0; c < 8; ++c) put(c, make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]));
+            flush(c0 / 4);
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -1102,12 +1042,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
               w.y = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 2]) * il, __uint_as_float(ov[8 * c + 3]) * il);
               w.z = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 4]) * il, __uint_as_float(ov[8 * c + 5]) * il);
               w.w = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 6]) * il, __uint_as_float(ov[8 * c + 7]) * il);
-              put(c0 / 8 + c, w);
+              put((c0 >> 3 & 4) + c, w);
             }
-            if (c0 / 8 + 4 == LW) flush(0);
+            if (c0 & 32) flush((c0 & ~63) / 8);
           }
         }
-        if (cut && st_ok && hb == 0) wk.part_ml[pi] = make_float2(m, l);
+        if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
       }
       if (!two) {  // slot 1's scores and sums may be written again
         if (t == 0) {
@@ -1147,7 +1087,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (*(volatile int*)&sh->last) {
           // the unit's pieces, merged in the order of the keys: their places first, each warp for itself
           __threadfence();
-          int* list = reinterpret_cast<int*>(stage);
+          int* list = reinterpret_cast<int*>(qt);
           int np = 0;
           for (int cb = d.first_cut - 1;; cb += 32) {
             const int c = cb + lane;
@@ -1221,11 +1161,11 @@ cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void
   if (!encode) return cudaErrorNotSupported;
   const CaPlan k = ca_plan(p.T, p.H, p.Hkv, D, num_sms);
   CaMaps maps;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, 64, (cuuint64_t)p.pages * p.Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 128};
-  const cuuint32_t box[3] = {64u, 64u, 1u}, es[3] = {1u, 1u, 1u};
+  const cuuint64_t dims[4] = {64, 64, (cuuint64_t)D / 64, (cuuint64_t)p.pages * p.Hkv};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 128};
+  const cuuint32_t box[4] = {64u, 64u, (cuuint32_t)D / 64, 1u}, es[4] = {1u, 1u, 1u, 1u};
   for (int c = 0; c < 2; ++c)
-    if (encode(c ? &maps.v : &maps.k, type == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+    if (encode(c ? &maps.v : &maps.k, type == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                const_cast<void*>(c ? p.v : p.k), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
