@@ -50,6 +50,7 @@ constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
 constexpr int kCaOverhead = 256;  // keys that a unit's start and end are worth
 constexpr int kCaLeast = 8;       // tiles a CTA has at least, where units are cut
 constexpr int kCaMerge = 12;      // tiles that a cut is worth
+constexpr int kCaSnap = 16;       // tiles that a cut may move to the unit's begin or end
 
 // Weights are taken against a reference: the largest score of the first tile that
 // the row sees keys of. It is raised (and the sums so far, in TMEM, rescaled) by a
@@ -127,6 +128,19 @@ __device__ __forceinline__ void ca_copy16(void* dst, const void* src, bool there
 }
 __device__ __forceinline__ void ca_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// The page's head z by TMA, counted on bar; by a whole warp, whose elected lane
+// issues (from code that one lane alone runs, an issue takes several times as long).
+__device__ __forceinline__ void ca_copy_tile(void* dst, const CUtensorMap* map, int32_t z, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%2], %4;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%5, %5, %5, %3}], "
+      "[%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(z), "r"(bytes), "r"(0)
+      : "memory");
+}
+
 // Bounded wait by a whole warp; false once it has run out.
 __device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
   return mbar_wait(bar, parity, err);
@@ -149,17 +163,19 @@ __device__ __forceinline__ bool test_skip_copy(uint32_t) { return false; }
 // ------------------------------------------------------------------ the split
 
 // floor(a / b) for 0 <= a, b > 0 and a quotient below 2^22 (the fp32 estimate is
-// off by less than one half then, and put right); the whole number next to a * n / b
-// for a < b.
+// off by less than one then, and put right); the whole number next to a * n / b for
+// a < b, or one of the ends, if it is no more than `snap` from it. __fdividef: b
+// below 2^126.
 __device__ __forceinline__ int ca_fix(int q, int64_t a, int64_t b) {
   int64_t r = a - q * b;
   while (r < 0) r += b, --q;
   while (r >= b) r -= b, ++q;
   return q;
 }
-__device__ __forceinline__ int ca_quotient(int64_t a, int64_t b) { return ca_fix((int)((float)a / (float)b), a, b); }
-__device__ __forceinline__ int ca_share(int64_t a, int n, int64_t b) {
-  return ca_fix((int)((float)a / (float)b * (float)n + 0.5f), 2 * a * n + b, 2 * b);
+__device__ __forceinline__ int ca_quotient(int64_t a, int64_t b) { return ca_fix((int)__fdividef((float)a, (float)b), a, b); }
+__device__ __forceinline__ int ca_share(int64_t a, int n, int64_t b, int snap) {
+  const int q = ca_fix((int)(__fdividef((float)a, (float)b) * (float)n + 0.5f), 2 * a * n + b, 2 * b);
+  return q <= min(snap, n / 2) ? 0 : n - q <= snap ? n : q;
 }
 
 // A request's rows: the first, their number (0 where it brings none or is not
@@ -234,9 +250,11 @@ __device__ __forceinline__ CaTiles ca_tiles(const Kv16AttnParams& p, const CaWor
 struct CaPlace {
   int b, kvh, unit, cut;
   int64_t u0, v;
+  CaRequest r;
 };
 // The place of x in request b, whose work begins at `at` (at <= x < its end).
-__device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, const CaRequest& r, int64_t at, int64_t x) {
+__device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, const CaRequest& r, int64_t at, int64_t x,
+                             int snap) {
   const CaLoad w = ca_load(p, wk, r);
   const int64_t head = w.before(w.units);
   CaPlace o;
@@ -254,7 +272,8 @@ __device__ CaPlace ca_locate(const Kv16AttnParams& p, const CaWork& wk, int b, c
   o.unit = lo;
   o.u0 = at + w.before(lo);
   o.v = w.before(lo + 1) - w.before(lo);
-  o.cut = ca_share(x - o.u0, ca_tiles(p, wk, r, lo).nt, o.v);
+  o.r = r;
+  o.cut = ca_share(x - o.u0, ca_tiles(p, wk, r, lo).nt, o.v, snap);
   return o;
 }
 
@@ -447,6 +466,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   struct Scratch {
     int64_t sums[kCaThreads / 32];
     int units[kCaThreads / 32];
+    int64_t at[2];  // the work before the requests that the run begins and ends in
     CaPlace place[2];
   };
   Scratch* scr = reinterpret_cast<Scratch*>(smem);
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   }
   if (lane == 31) scr->sums[warp] = upto;
   if (lane == 31) scr->units[warp] = units;
-  if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1};
+  if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1, CaRequest{0, 0, 0}};
   __syncthreads();
   grid_launch_dependents();  // (TMEM is allocated: no later kernel can hold it while this one waits for it)
   int64_t W = 0, at = upto - mine;
@@ -485,6 +505,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // all of them would be done sooner although nearly every one then has to merge.
   int C = wk.ctas;
   uint64_t inv = wk.ctas_inv;
+  const int snap = units < C ? 1 : kCaSnap;  // (few units: nearly every cut is meant)
   if (units > 0 && units < C) {
     const float tile = (float)(kCaWeight1 * G * kCaKeys), w = (float)W;
     const int even = units * max(1, min(C / units, (int)(w / (tile * kCaLeast * (float)units))));
@@ -502,14 +523,24 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     for (int b = b0; b < b1; ++b) {
       const CaRequest r = ca_request(p, b, false);
       if (r.cnt == 0) continue;
-      const CaLoad w = ca_load(p, wk, r);
-      const int64_t n = p.Hkv * w.before(w.units);
+      int64_t n = mine;  // (a thread with one request knows its work)
+      if (per > 1) {
+        const CaLoad w = ca_load(p, wk, r);
+        n = p.Hkv * w.before(w.units);
+      }
       if (x < a + n) {
-        scr->place[e] = ca_locate(p, wk, b, r, a, x);
+        scr->place[e].b = b;
+        scr->place[e].r = r;
+        scr->at[e] = a;
         break;
       }
       a += n;
     }
+  }
+  __syncthreads();
+  if ((tid == 0 || tid == 32) && scr->place[tid >> 5].b < p.B) {  // both ends at once
+    const int e = tid >> 5;
+    scr->place[e] = ca_locate(p, wk, scr->place[e].b, scr->place[e].r, scr->at[e], bound(cta + e), snap);
   }
   tc_fence_before();
   __syncthreads();
@@ -520,7 +551,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // what part of a cut unit falls to CTA c: tiles cut_at(c) .. cut_at(c + 1) - 1
   auto cut_at = [&](int c, int64_t u0, int64_t v, int nt) {
     const int64_t x = bound(c);
-    return x <= u0 ? 0 : x >= u0 + v ? nt : ca_share(x - u0, nt, v);
+    return x <= u0 ? 0 : x >= u0 + v ? nt : ca_share(x - u0, nt, v, snap);
   };
 
   if (warp == 0) {
@@ -530,12 +561,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     bool ok = true;
     int b = begin.b, kvh = begin.kvh, unit = begin.unit;
     bool first = true;
-    CaRequest r{0, 0, 0};
+    CaRequest r = begin.r;
     CaLoad w;
-    if (b < p.B) {
-      r = ca_request(p, b, false);
-      w = ca_load(p, wk, r);
-    }
+    if (b < p.B) w = ca_load(p, wk, r);
     while (ok && b < p.B) {
       const bool at_end = b == end.b && kvh == end.kvh && unit == end.unit;
       const CaTiles t = ca_tiles(p, wk, r, unit);
@@ -603,24 +631,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const int z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
           // guarded values land at a barrier of their own: the guard tells when they may be used
           const bool guard = i - lo < gw || i - lo >= gc;
-          if (lane == 0) {
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              const uint32_t x = buf + (uint32_t)kv, s = x % NB, use = x / NB;
-              ok = ok && (use == 0 || ca_wait(&sh->free[s], (use - 1) & 1u, p.err));
-              if (!ok || test_skip_copy(x)) continue;
-              uint64_t* bar = &sh->full[s];
-              if (kv == 1 && guard) {
-                mbar_arrive(bar);
-                bar = &sh->landed[guarded % kCaOk];
-              }
-              mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
-              tma_load_4d(smem + L::kRingOff + s * L::kTile, kv ? &maps.v : &maps.k, 0, 0, 0, z, bar);
-              issued = (uint32_t)kv + 1u;  // (of this tile, where a wait runs out)
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t x = buf + (uint32_t)kv, s = x % NB, use = x / NB;
+            ok = ok && (use == 0 || ca_wait(&sh->free[s], (use - 1) & 1u, p.err));
+            if (!ok || test_skip_copy(x)) continue;
+            uint64_t* bar = &sh->full[s];
+            if (kv == 1 && guard) {
+              if (lane == 0) mbar_arrive(bar);
+              bar = &sh->landed[guarded % kCaOk];
             }
+            ca_copy_tile(smem + L::kRingOff + s * L::kTile, kv ? &maps.v : &maps.k, z, bar, (uint32_t)L::kTile);
+            issued = (uint32_t)kv + 1u;  // (of this tile, where a wait runs out)
           }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          issued = __shfl_sync(0xffffffffu, issued, 0);
           if (!ok) break;
           issued = 0;
           buf += 2u;
@@ -987,15 +1010,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         auto put = [&](int word, uint4 w) {
           *reinterpret_cast<uint4*>(qt + lane * 128 + ((word ^ (lane & 7)) << 4)) = w;
         };
+        uint4* to[8];  // where this lane's share of the rows 4 k + lane / 8 goes
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[k] = dst + __shfl_sync(0xffffffffu, place, 4 * k + (lane >> 3)) + (lane & 7);
         auto flush = [&](int word) {  // eight words of each row, from this one on
           __syncwarp();
+          uint4 w[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + (lane >> 3), c = lane & 7;
-            const int64_t to = __shfl_sync(0xffffffffu, place, r);
-            if ((rows_ok >> r) & 1u)
-              dst[to + word + c] = *reinterpret_cast<const uint4*>(qt + r * 128 + ((c ^ (r & 7)) << 4));
+            const int r = 4 * k + (lane >> 3);
+            w[k] = *reinterpret_cast<const uint4*>(qt + r * 128 + (((lane ^ r) & 7) << 4));
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if ((rows_ok >> (4 * k + (lane >> 3))) & 1u) to[k][word] = w[k];
           __syncwarp();
         };
 #pragma unroll 1
@@ -1101,7 +1129,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           __syncwarp();
           // many rows have few pieces, many pieces few rows: loads in flight along the one or the other
           if (np <= 2)
-            ca_merge<TYPE, D, 4, 2>(p, wk, d, list, np, warp - 4, lane);
+            ca_merge<TYPE, D, 8, 2>(p, wk, d, list, np, warp - 4, lane);
           else
             ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane);
         }
