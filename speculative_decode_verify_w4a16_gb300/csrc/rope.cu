@@ -14,6 +14,14 @@
 // latency for the rows of a step. A CTA takes a row: its loads go out first, the
 // row's sines and cosines (one pair a thread, for all heads) are computed
 // meanwhile and handed over through shared memory.
+// Measured: 16381 rows of 72 heads 92 us (604 MB: 0.97 of the HBM copy rate),
+// 4093 rows of 40 heads, half of each turned in pairs, 10.4 us (84 MB, in part in
+// the L2), 12.0 K rows of 64 + 16 heads into pages 104 us (655 MB, 0.93); 80 rows
+// 3.1 us, 64 rows into pages 5.1. What keeps the memory busy is bytes in flight and
+// CTAs at once: 128 threads, five items each, eight CTAs an SM; against 92, 104 us
+// there were 96, 110 with 192 threads (5 CTAs), 105, 110 with 256 and three items
+// (5), 95, 101 with 256 and one (8), 130, 142 with ten CTAs (registers spilled), and
+// 104, 123 with the loads behind the sines.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -21,7 +29,11 @@
 
 namespace w4a16 {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
+constexpr int kRowBlocks = 8;  // CTAs an SM
+// items whose loads a thread has in flight (fp32: what the registers hold)
+template <int TYPE>
+constexpr int kRowFlight = TYPE == 2 ? 2 : 5;
 
 // eight elements as fp32, and back: 16 bytes of bf16 or fp16, 32 of fp32
 template <int TYPE>
@@ -36,7 +48,8 @@ __device__ __forceinline__ Eight<TYPE> load8(const void* p, int64_t at) {
   Eight<TYPE> e;
   const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * kElt<TYPE>);
 #pragma unroll
-  for (int i = 0; i < (TYPE == 2 ? 2 : 1); ++i) e.w[i] = s[i];
+  for (int i = 0; i < (TYPE == 2 ? 2 : 1); ++i)
+    e.w[i] = s[i];
   return e;
 }
 template <int TYPE>
@@ -98,35 +111,35 @@ __device__ __forceinline__ float2 cos_sin(uint32_t turn, float factor) {
                      quarter >= 2u ? -sn * factor : sn * factor);
 }
 
-// The rotated (u, v) of unit `u` of a head: pairs 8 u .. 8 u + 7. Half layout:
-// eight elements at 8 u and eight at rot / 2 + 8 u; interleaved: sixteen at 16 u.
+// Half layout: the pairs 8 u .. 8 u + 7, a their first elements, b their second ones.
 template <int TYPE>
-__device__ __forceinline__ void turn_unit(Eight<TYPE>& a, Eight<TYPE>& b, const float2* cs, int u, bool inter) {
+__device__ __forceinline__ void turn_halves(Eight<TYPE>& a, Eight<TYPE>& b, const float2* cs) {
   float x[8], y[8];
   widen<TYPE>(a, x);
   widen<TYPE>(b, y);
-  const float2* c = cs + 8 * u;
-  if (inter) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 c0 = c[i], c1 = c[4 + i];
-      const float u0 = x[2 * i], v0 = x[2 * i + 1], u1 = y[2 * i], v1 = y[2 * i + 1];
-      x[2 * i] = u0 * c0.x - v0 * c0.y;
-      x[2 * i + 1] = v0 * c0.x + u0 * c0.y;
-      y[2 * i] = u1 * c1.x - v1 * c1.y;
-      y[2 * i + 1] = v1 * c1.x + u1 * c1.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 ci = c[i];
-      const float p = x[i], q = y[i];
-      x[i] = p * ci.x - q * ci.y;
-      y[i] = q * ci.x + p * ci.y;
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float2 c = cs[i];
+    const float u = x[i], v = y[i];
+    x[i] = u * c.x - v * c.y;
+    y[i] = v * c.x + u * c.y;
   }
   a = narrow<TYPE>(x);
   b = narrow<TYPE>(y);
+}
+// Interleaved: four pairs side by side.
+template <int TYPE>
+__device__ __forceinline__ void turn_pairs(Eight<TYPE>& a, const float2* cs) {
+  float x[8];
+  widen<TYPE>(a, x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = cs[i];
+    const float u = x[2 * i], v = x[2 * i + 1];
+    x[2 * i] = u * c.x - v * c.y;
+    x[2 * i + 1] = v * c.x + u * c.y;
+  }
+  a = narrow<TYPE>(x);
 }
 
 // Where row i of a step goes: the request b with start[b] <= i < start[b + 1]
@@ -176,20 +189,67 @@ __device__ RowPlace find_row(const RowParams& p, int i, int lane) {
   return {pos, page};
 }
 
-// One row a CTA. Rotated heads: x (rope) or q, then k (append); copied: v.
-template <int TYPE, bool APPEND>
-__global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const RowParams p) {
+// One row a CTA. Rotated heads: x (rope) or q, then k (append); copied: v. A head
+// is so many items: eight pairs (half layout) or eight elements (interleaved) to
+// turn, then eight elements to copy. A thread takes every 128th item, kRowFlight at
+// a time, and loads the first ones before it waits for the sines.
+template <int TYPE, bool APPEND, bool INTER>
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks) rope_rows_kernel(const RowParams p, const FastDiv by_items,
+                                                                const FastDiv by_eighths) {
   extern __shared__ float2 row_cs[];  // [rot / 2]
   __shared__ RowPlace s_place;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, row = blockIdx.x;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int row = blockIdx.x;
-  RowPlace place{0, 0};
+  const int D = p.D, half = p.rot / 2, turns = INTER ? p.rot / 8 : p.rot / 16, items = (int)by_items.d;
+  const int turned = (p.Hq + (APPEND ? p.Hkv : 0)) * items, total = turned + (APPEND ? p.Hkv * (D / 8) : 0);
+  struct Item {
+    int head, at;  // head of the row (q's, then k's, then v's), first element
+    bool turn;
+  };
+  auto item = [&](int i) {
+    Item t;
+    if (!APPEND || i < turned) {
+      t.head = by_items(i);
+      const int u = i - t.head * items;
+      t.turn = u < turns;
+      t.at = t.turn ? 8 * u : p.rot + 8 * (u - turns);
+    } else {
+      const int h = by_eighths(i - turned);
+      t.head = p.Hq + p.Hkv + h;
+      t.turn = false;
+      t.at = 8 * (i - turned - h * (D / 8));
+    }
+    return t;
+  };
+  Eight<TYPE> a[kRowFlight<TYPE>], b[kRowFlight<TYPE>];
+  auto load = [&](int first) {
+#pragma unroll
+    for (int k = 0; k < kRowFlight<TYPE>; ++k) {
+      const int i = first + k * kRowThreads;
+      if (i >= total) break;
+      const Item t = item(i);
+      const void* src = p.q;
+      int64_t from = (int64_t)row * p.q_stride + (int64_t)t.head * D;
+      if (APPEND && t.head >= p.Hq) {
+        const bool key = t.head < p.Hq + p.Hkv;
+        src = key ? p.k_new : p.v_new;
+        from = (int64_t)row * (key ? p.k_stride : p.v_stride) + (int64_t)(t.head - p.Hq - (key ? 0 : p.Hkv)) * D;
+      }
+      a[k] = load8<TYPE>(src, from + t.at);
+      if (!INTER && t.turn) b[k] = load8<TYPE>(src, from + t.at + half);
+    }
+  };
+  bool taken = true;  // (append: a row of no request is not read)
   if constexpr (APPEND) {
     if (row == 0 && p.start)  // rows out of order are found wherever they are
       for (int b = tid; b < p.B; b += kRowThreads)
         if (p.start[b + 1] < p.start[b]) report_error(p.err, kErrInput);
+    taken = !p.start || row < p.start[p.B];
+  }
+  if (taken) load(tid);
+  RowPlace place{0, 0};
+  if constexpr (APPEND) {
     if (tid < 32) {
       const RowPlace r = find_row(p, row, tid);
       if (tid == 0) s_place = r;
@@ -200,84 +260,57 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const RowParams 
   } else {
     place.pos = p.positions[row];
   }
-  for (int i = tid; i < p.rot / 2; i += kRowThreads) {
-    const uint64_t turns = p.turns[i] * (uint64_t)(int64_t)(p.inverse ? -(int64_t)place.pos : (int64_t)place.pos);
-    row_cs[i] = cos_sin((uint32_t)(turns >> 32), p.factor);
+  for (int i = tid; i < half; i += kRowThreads) {
+    const uint64_t turn = p.turns[i] * (uint64_t)(int64_t)(p.inverse ? -(int64_t)place.pos : (int64_t)place.pos);
+    row_cs[i] = cos_sin((uint32_t)(turn >> 32), p.factor);
   }
   __syncthreads();
-  const int D = p.D, units = p.rot / 16, rest = (D - p.rot) / 8;
   const int64_t page_row = ((int64_t)place.page * p.Hkv * 64 + place.pos % 64) * D;
-  const bool stored = !APPEND || place.page >= 0;
-  // head h's source and destination (null: none)
-  auto head = [&](int h, const void*& src, int64_t& from, void*& dst, int64_t& to) {
-    if (h < p.Hq) {
-      src = p.q;
-      from = (int64_t)row * p.q_stride + (int64_t)h * D;
-      dst = p.q_out;
-      to = (int64_t)row * p.out_stride + (int64_t)h * D;
-    } else {
-      const bool key = h < p.Hq + p.Hkv;
-      const int g = h - p.Hq - (key ? 0 : p.Hkv);
-      src = key ? p.k_new : p.v_new;
-      from = (int64_t)row * (key ? p.k_stride : p.v_stride) + (int64_t)g * D;
-      dst = stored ? (key ? p.k : p.v) : nullptr;
-      to = page_row + (int64_t)g * 64 * D;
+  for (int first = tid; first < total; first += kRowFlight<TYPE> * kRowThreads) {
+    if (first != tid || !taken) load(first);
+#pragma unroll
+    for (int k = 0; k < kRowFlight<TYPE>; ++k) {
+      const int i = first + k * kRowThreads;
+      if (i >= total) break;
+      const Item t = item(i);
+      if (t.turn) {
+        if constexpr (INTER)
+          turn_pairs<TYPE>(a[k], row_cs + t.at / 2);
+        else
+          turn_halves<TYPE>(a[k], b[k], row_cs + t.at);
+      }
+      void* dst = p.q_out;
+      int64_t to = (int64_t)row * p.out_stride + (int64_t)t.head * D;
+      if (APPEND && t.head >= p.Hq) {
+        const bool key = t.head < p.Hq + p.Hkv;
+        dst = key ? p.k : p.v;
+        to = page_row + (int64_t)(t.head - p.Hq - (key ? 0 : p.Hkv)) * 64 * D;
+        if (place.page < 0 || !in_bounds(p.err, to + t.at + (t.turn && !INTER ? half : 0) + 7,
+                                         (int64_t)p.pages * p.Hkv * 64 * D))
+          continue;
+      }
+      store8<TYPE>(dst, to + t.at, a[k]);
+      if (!INTER && t.turn) store8<TYPE>(dst, to + t.at + half, b[k]);
     }
-  };
-  const int turned = p.Hq + (APPEND ? p.Hkv : 0);
-  const int second = p.inter ? 8 : p.rot / 2, width = p.inter ? 16 : 8;
-  for (int i = tid; i < turned * units; i += kRowThreads) {
-    const int h = i / units, u = i - h * units;
-    const void* src;
-    void* dst;
-    int64_t from, to;
-    head(h, src, from, dst, to);
-    if (!dst) continue;
-    Eight<TYPE> a = load8<TYPE>(src, from + width * u), b = load8<TYPE>(src, from + width * u + second);
-    turn_unit<TYPE>(a, b, row_cs, u, p.inter != 0);
-    store8<TYPE>(dst, to + width * u, a);
-    store8<TYPE>(dst, to + width * u + second, b);
-  }
-  const int copies = turned * rest + (APPEND ? p.Hkv * (D / 8) : 0);
-  for (int i = tid; i < copies; i += kRowThreads) {
-    int h, at;
-    if (i < turned * rest) {
-      h = i / rest;
-      at = p.rot + 8 * (i - h * rest);
-    } else {
-      const int j = i - turned * rest;
-      h = j / (D / 8);
-      at = 8 * (j - h * (D / 8));
-      h += turned;
-    }
-    const void* src;
-    void* dst;
-    int64_t from, to;
-    head(h, src, from, dst, to);
-    if (dst) store8<TYPE>(dst, to + at, load8<TYPE>(src, from + at));
   }
 }
 
-template <bool APPEND>
-static cudaError_t launch_rows(const RowParams& p, int type, cudaStream_t stream) {
+template <int TYPE, bool APPEND>
+static cudaError_t launch_rows_t(const RowParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.T), block(kRowThreads);
   const size_t smem = (size_t)p.rot / 2 * sizeof(float2);
-  switch (type) {
-    case 0: return launch_pdl(rope_rows_kernel<0, APPEND>, grid, block, smem, stream, p);
-    case 1: return launch_pdl(rope_rows_kernel<1, APPEND>, grid, block, smem, stream, p);
-    default:
-      if constexpr (APPEND)
-        return cudaErrorInvalidValue;
-      else
-        return launch_pdl(rope_rows_kernel<2, false>, grid, block, smem, stream, p);
-  }
+  const int items = p.inter ? p.D / 8 : p.rot / 16 + (p.D - p.rot) / 8;
+  const FastDiv by_items = fast_div((uint32_t)items), by_eighths = fast_div((uint32_t)(p.D / 8));
+  if (p.inter) return launch_pdl(rope_rows_kernel<TYPE, APPEND, true>, grid, block, smem, stream, p, by_items, by_eighths);
+  return launch_pdl(rope_rows_kernel<TYPE, APPEND, false>, grid, block, smem, stream, p, by_items, by_eighths);
 }
 
 cudaError_t launch_rope(const RowParams& p, int type, cudaStream_t stream) {
-  return launch_rows<false>(p, type, stream);
+  return type == 0 ? launch_rows_t<0, false>(p, stream)
+                   : type == 1 ? launch_rows_t<1, false>(p, stream) : launch_rows_t<2, false>(p, stream);
 }
 cudaError_t launch_kv16_append(const RowParams& p, int type, cudaStream_t stream) {
-  return launch_rows<true>(p, type, stream);
+  return type == 0 ? launch_rows_t<0, true>(p, stream) : launch_rows_t<1, true>(p, stream);
 }
 
 }  // namespace w4a16
