@@ -69,6 +69,7 @@ struct CaMaps {
 struct CaWork {
   FastDiv by_g;
   int ctas, rows_cap;  // rows of a workspace slot
+  int wide;            // out lies on 32 bytes
   uint64_t ctas_inv;   // floor(2^64 / ctas)
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
   float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain
@@ -139,6 +140,18 @@ __device__ __forceinline__ void ca_copy_tile(void* dst, const CUtensorMap* map, 
       "[%2];\n\t}" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(z), "r"(bytes), "r"(0)
       : "memory");
+}
+
+// 32 bytes to global memory, at once where they lie on 32.
+__device__ __forceinline__ void ca_store32(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // Bounded wait by a whole warp; false once it has run out.
@@ -824,39 +837,47 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)(32 * qd) << 16);
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t sc = 0, shared_parts = 0, cut_parts = 0;
-    bool ok = true;
+    bool ok = true, have_q = false;
+    // this warp's rows of a part's Q: 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
+    auto load_q = [&](const CaPart& e) {
+      const int u0 = (e.rows > 128 ? 128 * t : 0) + qd * 32, c = lane & 7;
+      if (e.rows <= 128 && t == 1) return;  // (slot 0's rows)
+      uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + (lane >> 3), u = u0 + r;
+        const int R2 = e.row0 + (u < e.rows ? u : 0), j2 = wk.by_g(R2);
+        const bool there = u < e.rows && in_bounds(p.err, e.at + j2, p.T);
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(e.at + j2) * p.q_stride +
+                              (int64_t)(e.kvh * G + R2 - j2 * G) * D + c * 8;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          ca_copy16(qt + h * L::kQHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src + 64 * h : p.q, there);
+      }
+    };
+    auto hand_q = [&](int ds) {
+      ca_copy_wait();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_ready[t][ds]);
+    };
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
       if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
       const CaPart& d = sh->part[ds];
       const int n = d.hi - d.lo;
       if (n <= 0) break;
-      const bool two = d.rows > 128;
+      if (!have_q) {
+        load_q(d);
+        hand_q(ds);
+      }
+      have_q = false;
+      const bool two = d.rows > 128, cut = n < d.nt;
       const int ur = (two ? 128 * t : 0) + rl;  // this thread's row of the unit
       const bool valid = ur < d.rows;
       const int R = d.row0 + (valid ? ur : 0), j = wk.by_g(R), pos = d.past + j;
       const int head = d.kvh * G + R - j * G;
       const bool any_row = __any_sync(0xffffffffu, valid);
-      // this warp's rows of the slot's Q, and its buffer for the results
-      uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;
-      if (two || t == 0) {  // 128-byte swizzle, K-major, halves of 64 columns; eight lanes a row
-        const int c = lane & 7;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + (lane >> 3), u = ur - lane + r;
-          const int R2 = d.row0 + (u < d.rows ? u : 0), j2 = wk.by_g(R2);
-          const bool there = u < d.rows && in_bounds(p.err, d.at + j2, p.T);
-          const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(d.at + j2) * p.q_stride +
-                                (int64_t)(d.kvh * G + R2 - j2 * G) * D + c * 8;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            ca_copy16(qt + h * L::kQHalf + r * 128 + ((c ^ (r & 7)) << 4), there ? src + 64 * h : p.q, there);
-        }
-        ca_copy_wait();
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->q_ready[t][ds]);
       int nt = (n - t + 1) / 2;
       if (two) nt = min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n);
       const int gw = d.gw, gc = d.gc;
@@ -874,6 +895,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           continue;
         }
         tc_fence_after();
+        // With the last scores this slot's Q is done with (row tiles: it is this slot's alone): the next part's comes in
+        // behind the last tile's weights. (A cut part's end needs the place.)
+        if (jt + 1 == nt && two && !cut) {
+          const int dn = (seq + 1) % kCaDesc;
+          if (__all_sync(0xffffffffu, mbar_test(&sh->desc_full[dn], (uint32_t)((seq + 1) / kCaDesc) & 1u)) &&
+              sh->part[dn].hi > 0) {
+            load_q(sh->part[dn]);
+            have_q = true;
+          }
+        }
         const bool masked = i < gw || i >= gc;
         auto mask = [&](uint32_t (&x)[32], int first) {  // columns first .. first + 31
           const int top = rel - i * kCaKeys - first;    // seen: bottom < c <= top
@@ -961,6 +992,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
       }
+      if (have_q) hand_q((seq + 1) % kCaDesc);
       // ---- the part's end
       if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
       if (!ok) break;
@@ -993,39 +1025,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
         }
       }
-      const bool cut = n < d.nt;
       const int64_t slot = 2 * cta + (d.lo > 0 ? 0 : 1);
       if ((two || t == 0) && any_row) {
-        const float il = cut ? 1.0f : 1.0f / l;
+        const float il = 1.0f / l;
         const int64_t pi = slot * wk.rows_cap + ur;
-        // the row's place, in 16-byte words: the result's, or the piece's in the workspace
-        const int64_t place = (cut ? pi * (D / 4) : (((int64_t)(d.at + j) * p.H + head) * D) / 8) ;
-        uint4* dst = cut ? reinterpret_cast<uint4*>(wk.part_o) : static_cast<uint4*>(p.out);
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)(d.at + j) * p.H + head) * D;
+        float* part = wk.part_o + pi * D;
         const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
-        const unsigned rows_ok = __ballot_sync(0xffffffffu, st_ok);
         const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
         const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
         const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
-        // through the warp's rows of Q (whose products are complete), so that lanes write whole lines of 128 bytes
-        auto put = [&](int word, uint4 w) {
-          *reinterpret_cast<uint4*>(qt + lane * 128 + ((word ^ (lane & 7)) << 4)) = w;
-        };
-        uint4* to[8];  // where this lane's share of the rows 4 k + lane / 8 goes
-#pragma unroll
-        for (int k = 0; k < 8; ++k) to[k] = dst + __shfl_sync(0xffffffffu, place, 4 * k + (lane >> 3)) + (lane & 7);
-        auto flush = [&](int word) {  // eight words of each row, from this one on
-          __syncwarp();
-          uint4 w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + (lane >> 3);
-            w[k] = *reinterpret_cast<const uint4*>(qt + r * 128 + (((lane ^ r) & 7) << 4));
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if ((rows_ok >> (4 * k + (lane >> 3))) & 1u) to[k][word] = w[k];
-          __syncwarp();
-        };
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           const uint32_t col = (uint32_t)c0;
@@ -1058,21 +1067,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) ov[c] = tmp[c];
           }
+          if (!st_ok) continue;
+          // a lane its own row, in whole sectors (through shared memory, whole lines at once: slower by the round trip)
           if (cut) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) put(c, make_uint4(ov[4 * c], ov[4 * c + 1], ov[4 * c + 2], ov[4 * c + 3]));
-            flush(c0 / 4);
+            for (int c = 0; c < 32; c += 8) ca_store32(part + c0 + c, ov + c, true);
           } else {
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 w;
-              w.x = ca_pack<TYPE>(__uint_as_float(ov[8 * c]) * il, __uint_as_float(ov[8 * c + 1]) * il);
-              w.y = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 2]) * il, __uint_as_float(ov[8 * c + 3]) * il);
-              w.z = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 4]) * il, __uint_as_float(ov[8 * c + 5]) * il);
-              w.w = ca_pack<TYPE>(__uint_as_float(ov[8 * c + 6]) * il, __uint_as_float(ov[8 * c + 7]) * il);
-              put((c0 >> 3 & 4) + c, w);
-            }
-            if (c0 & 32) flush((c0 & ~63) / 8);
+            for (int c = 0; c < 16; ++c)
+              w[c] = ca_pack<TYPE>(__uint_as_float(ov[2 * c]) * il, __uint_as_float(ov[2 * c + 1]) * il);
+            ca_store32(dst + c0, w, wk.wide != 0);
+            ca_store32(dst + c0 + 16, w + 8, wk.wide != 0);
           }
         }
         if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
@@ -1115,7 +1121,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (*(volatile int*)&sh->last) {
           // the unit's pieces, merged in the order of the keys: their places first, each warp for itself
           __threadfence();
-          int* list = reinterpret_cast<int*>(qt);
+          int* list = reinterpret_cast<int*>(smem + t * L::kQ + qd * 32 * 128);  // (this warp's rows of Q)
           int np = 0;
           for (int cb = d.first_cut - 1;; cb += 32) {
             const int c = cb + lane;
@@ -1203,6 +1209,7 @@ cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void
   wk.ctas = k.ctas;
   wk.ctas_inv = k.ctas > 1 ? ~uint64_t(0) / (uint64_t)k.ctas : ~uint64_t(0);
   wk.rows_cap = k.rows_cap;
+  wk.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   wk.done = reinterpret_cast<int*>(ws);
   wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
