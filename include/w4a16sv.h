@@ -481,7 +481,9 @@ w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positio
  *   k, v         device [pages][Hkv][64][D] of one layer, type 0 (bf16) or 1
  *                (fp16); D 64 or 128; 16-byte aligned
  *   block_table  device int32 [B][max_blocks]: the pages of the blocks
- *                0 .. (lens[b] + rows - 1) / 64 (other entries unread)
+ *                0 .. (lens[b] + rows - 1) / 64 (other entries unread). Requests
+ *                may share pages that no row of the step goes to; of two rows
+ *                for one place either may be kept
  *   lens         device int32 [B]: tokens of request b before the step
  *   row_start    device int32 [B + 1], not falling, row_start[B] <= T; NULL:
  *                T / B rows each. Rows of no request are neither read nor written
@@ -519,11 +521,16 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
  *              of no request are left as they were
  *   window     0: none
  *   workspace  kv16_attention_workspace_bytes() bytes (256-byte aligned), zero
- *              before its first use; every call leaves the counters at its
- *              start zero. May be NULL when that is 0
+ *              before its first use, and again after
+ *              W4A16_ERR_DEVICE_TIMEOUT; every other call leaves the counters
+ *              at its start zero
  * Arithmetic: scores and sums in fp32, the softmax weights rounded to the
- * cache's type for the sum of the values, out rounded once. T * H < 2^31.
- * Launch rules as for w4a16_linear.
+ * cache's type for the sum of the values, out rounded once. The order of the
+ * sums depends on the whole batch (it is cut into equal shares of work), not on
+ * timing: the same call gives the same bits.
+ * T * H < 2^31, H / Hkv <= 1024, max_blocks <= 2^21 (W4A16_ERR_UNSUPPORTED
+ * beyond, and for T, B, H and max_blocks whose estimated work passes 2^55 in
+ * all). Launch rules as for w4a16_linear.
  * ---------------------------------------------------------------------- */
 size_t kv16_attention_workspace_bytes(int T, int H, int Hkv, int D);
 w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, const void* v, const int32_t* block_table,

@@ -601,7 +601,7 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
   p.Hkv = Hkv;
   p.max_blocks = max_blocks;
   p.pages = pages;
-  p.window = window;
+  p.window = window >= (int64_t)max_blocks * 64 ? 0 : window;  // (a window past every position is none)
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
   p.err = dev.err;
