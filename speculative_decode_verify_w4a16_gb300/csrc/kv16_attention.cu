@@ -154,12 +154,45 @@ __device__ __forceinline__ void ca_store32(void* dst, const uint32_t* w, bool wi
   }
 }
 
-// Bounded wait by a whole warp; false once it has run out.
+// Four MMAs of a k-step each, issued by one elected lane of a converged warp; the first adds to what is there if
+// `accumulate`. SS: both operands from shared memory, K-major (32 bytes a step); TS: A from TMEM (8 columns a step), B
+// MN-major (16 rows of 128 bytes).
+__device__ __forceinline__ void ca_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 b2, %2, 4;\n\t"
+      "add.s64 a3, %1, 6;\n\tadd.s64 b3, %2, 6;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void ca_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\tadd.u32 a2, %1, 16;\n\tadd.s64 b2, %2, 256;\n\t"
+      "add.u32 a3, %1, 24;\n\tadd.s64 b3, %2, 384;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Bounded wait by a whole warp; false once it has run out. (A test without a time answers in 45 cycles, and several
+// at once in little more; one with a time takes 80, each for itself.)
 __device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
   return mbar_wait(bar, parity, err);
 }
 __device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
-  return mbar_try_wait(bar, parity, 1000u) || ca_wait_long(bar, parity, err);
+  return mbar_try_wait(bar, parity) || ca_wait_long(bar, parity, err);
 }
 
 #if W4A16_TEST_HOOKS
@@ -696,7 +729,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const int t = warp - 1;
     constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
     const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
-    uint32_t buf = 0, oks = 0, sc = 0, pc = 0;  // buffers, guarded tiles, scores issued and weights used so far
+    // Tile i of a part has the buffers 2 r (keys) and 2 r + 1 (values) of the ring, r its place among kPairs, and the
+    // phase ph. (A slot's turn is a chain of instructions that both slots' pace hangs on: places are stepped, not divided
+    // out.)
+    constexpr uint32_t kPairs = NB / 2;
+    struct Place {
+      uint32_t r, ph;
+      __device__ __forceinline__ void step(uint32_t by) {
+        r += by;
+        if (r >= kPairs) r -= kPairs, ph ^= 1u;
+      }
+    };
+    Place part0 = {0u, 0u};             // the part's first tile
+    uint32_t oks = 0, sc = 0, pc = 0;   // guarded tiles, scores issued and weights used so far
+    const uint32_t s_col = tmem + ca_s_col(t, 0), o_col = tmem + ca_o_col(t);
+    const uint64_t ring_k = umma_desc_sw128_kmajor(smem_u32(smem + L::kRingOff));
+    const uint64_t ring_v = umma_desc_sw128_mnmajor(smem_u32(smem + L::kRingOff + L::kTile), (uint32_t)L::kHalf, 1024u);
     bool ok = true, issued = false;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
@@ -707,67 +755,69 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const bool two = d.rows > 128;
       // this slot's tiles: as far as its rows see where the slots are row tiles, every other one where they share the rows
       const int upto = two ? min(max(ca_slot_last(wk, d, t) / kCaKeys + 1 - d.tile0 - d.lo, 0), n) : n;
-      const int step = two ? 1 : 2;
-      int i = two ? 0 : t;  // the tile whose scores come next
-      int at = 0;           // tiles before it are used or passed over
+      const int step = two ? 1 : 2, first = two ? 0 : t;
+      int i = first;  // the tile whose scores come next
+      int at = 0;     // tiles before it are used or passed over
+      Place pi = part0, pv;
       const uint64_t q0 = umma_desc_sw128_kmajor(smem_u32(smem + (two ? t : 0) * L::kQ));
       // Each slot releases every buffer once: those it does not use as soon as they are there (a phase is never skipped).
       auto pass = [&](int to) {
-        for (; at < to; ++at)
-          for (uint32_t x = buf + 2u * (uint32_t)at, e = x + 2u; x < e; ++x) {
-            if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
-            if (lane == 0) mbar_arrive(&sh->free[x % NB]);
+        for (; at < to; ++at, pi.step(1u))
+          for (uint32_t x = 2u * pi.r, e = x + 2u; x < e; ++x) {
+            if (!ca_wait(&sh->full[x], pi.ph, p.err)) return false;
+            if (lane == 0) mbar_arrive(&sh->free[x]);
             __syncwarp();
           }
         return true;
       };
-      auto scores = [&]() {  // S = Q K^T
-        if (!pass(i)) return false;
-        const uint32_t x = buf + 2u * (uint32_t)i;
-        if (!ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err)) return false;
+      auto scores = [&](bool there) {  // S = Q K^T
+        if (at < i) {
+          if (!pass(i)) return false;
+          there = false;
+        }
+        if (!there && !ca_wait(&sh->full[2u * pi.r], pi.ph, p.err)) return false;
         tc_fence_after();
-        const uint64_t k0 = umma_desc_sw128_kmajor(smem_u32(smem + L::kRingOff + (x % NB) * L::kTile));
-        const int sb = (int)(sc & 1u);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)  // (the descriptors count in 16 bytes)
-          umma_bf16_ss_warp(tmem + ca_s_col(t, sb), q0 + (uint64_t)((kk >> 2) * L::kQHalf / 16 + 2 * (kk & 3)),
-                            k0 + (uint64_t)((kk >> 2) * L::kHalf / 16 + 2 * (kk & 3)), idesc_s, kk > 0 ? 1u : 0u);
+        const uint32_t sb = sc & 1u;
+        const uint64_t k0 = ring_k + (uint64_t)(pi.r * (2u * L::kTile / 16));  // (the descriptors count in 16 bytes)
+        ca_mma4_ss(s_col + 64u * sb, q0, k0, idesc_s, 0u);
+        if constexpr (D == 128) ca_mma4_ss(s_col + 64u * sb, q0 + L::kQHalf / 16, k0 + L::kHalf / 16, idesc_s, 1u);
         umma_commit_warp(&sh->s_full[t][sb]);
-        umma_commit_warp(&sh->free[x % NB]);
+        umma_commit_warp(&sh->free[2u * pi.r]);
         issued = true;
         ++sc;
         at = i + 1;
         i += step;
+        pi.step(1u);
         return true;
       };
       // (slot 1's warps are done with the part before, and where the slots share the rows slot 0's have loaded them)
       if (i < upto && t == 1 && !two) ok = ca_wait(&sh->q_ready[0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err);
-      if (ok && i < upto) ok = ca_wait(&sh->q_ready[t][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores();
-      if (ok && i < upto) ok = scores();
+      if (ok && i < upto) ok = ca_wait(&sh->q_ready[t][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores(false);
+      if (ok && i < upto) ok = scores(false);
       // the scores two tiles on go out behind the product of the weights that lie in their buffer
-      for (int v = two ? 0 : t; ok && v < upto; v += step, ++pc) {
-        const uint32_t x = buf + 2u * (uint32_t)v + 1u;
-        const int sb = (int)(pc & 1u);
-        ok = ca_wait(&sh->full[x % NB], (x / NB) & 1u, p.err);
+      pv = part0;
+      pv.step((uint32_t)first);
+      for (int v = first; ok && v < upto; v += step, ++pc, pv.step((uint32_t)step)) {
+        const uint32_t sb = pc & 1u;
+        uint64_t *values = &sh->full[2u * pv.r + 1u], *weights = &sh->p_full[t][sb];
+        const bool v_there = mbar_test(values, pv.ph), p_there = mbar_test(weights, (pc >> 1) & 1u);
+        const bool k_there = mbar_test(&sh->full[2u * pi.r], pi.ph);  // (the tile `at`, whose last phase is waited for)
+        if (!v_there) ok = ca_wait(values, pv.ph, p.err);
         if (ok && (v < gw || v >= gc)) {  // the guard has looked through the values
           const uint32_t g = oks + (uint32_t)(v < gw ? v : gw + v - gc);
           ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err);
         }
-        ok = ok && ca_wait(&sh->p_full[t][sb], (pc >> 1) & 1u, p.err);
+        if (ok && !p_there) ok = ca_wait(weights, (pc >> 1) & 1u, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t v0 =
-            umma_desc_sw128_mnmajor(smem_u32(smem + L::kRingOff + (x % NB) * L::kTile), (uint32_t)L::kHalf, 1024u);
-#pragma unroll
-        for (int kk = 0; kk < kCaKeys / 16; ++kk)  // O += P V
-          umma_bf16_ts_warp(tmem + ca_o_col(t), tmem + ca_s_col(t, sb) + 8u * (uint32_t)kk, v0 + (uint64_t)(128 * kk),
-                            idesc_o, (v >= step || kk > 0) ? 1u : 0u);
+        // O += P V
+        ca_mma4_ts(o_col, s_col + 64u * sb, ring_v + (uint64_t)(pv.r * (2u * L::kTile / 16)), idesc_o, v >= step ? 1u : 0u);
         umma_commit_warp(&sh->pv_done[t][sb]);
-        umma_commit_warp(&sh->free[x % NB]);
-        if (i < upto) ok = scores();
+        umma_commit_warp(&sh->free[2u * pv.r + 1u]);
+        if (i < upto) ok = scores(k_there);
       }
       ok = ok && pass(n);
-      buf += 2u * (uint32_t)n;
+      part0 = pi;
       oks += (uint32_t)(gw + n - gc);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->desc_free[ds]);
