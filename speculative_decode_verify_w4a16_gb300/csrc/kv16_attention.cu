@@ -594,6 +594,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const CaPlace begin = scr->place[0], end = scr->place[1];
   const uint32_t tmem = sh->tmem;
   __syncthreads();  // the scratch becomes Q
+  // A tile has the buffers 2 r (keys) and 2 r + 1 (values) of the ring, r its place among kPairs, and the phase ph.
+  // (Places are stepped, not divided out: the pace hangs on these chains of instructions.)
+  constexpr uint32_t kPairs = NB / 2;
+  struct Place {
+    uint32_t r, ph;
+    __device__ __forceinline__ void step(uint32_t by) {
+      r += by;
+      if (r >= kPairs) r -= kPairs, ph ^= 1u;
+    }
+  };
   // what part of a cut unit falls to CTA c: tiles cut_at(c) .. cut_at(c + 1) - 1
   auto cut_at = [&](int c, int64_t u0, int64_t v, int nt) {
     const int64_t x = bound(c);
@@ -602,7 +612,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------- parts and copies
-    uint32_t buf = 0, guarded = 0, issued = 0;
+    uint32_t keys = 0, values = 0, guarded = 0;  // tiles copied so far, and guarded ones
+    Place pk = {0u, 0u}, pv = {0u, 0u};
     int seq = 0;
     bool ok = true;
     int b = begin.b, kvh = begin.kvh, unit = begin.unit;
@@ -668,32 +679,40 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           return -1;
         };
         int now = entries();
-        for (int i = lo; ok && i < hi; ++i) {
-          if (t.tile0 + i - base >= 32) {
-            base += 32;
-            now = entries();
-          }
-          const int page = __shfl_sync(0xffffffffu, now, t.tile0 + i - base);
-          const int z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
-          // guarded values land at a barrier of their own: the guard tells when they may be used
-          const bool guard = i - lo < gw || i - lo >= gc;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t x = buf + (uint32_t)kv, s = x % NB, use = x / NB;
-            ok = ok && (use == 0 || ca_wait(&sh->free[s], (use - 1) & 1u, p.err));
-            if (!ok || test_skip_copy(x)) continue;
-            uint64_t* bar = &sh->full[s];
-            if (kv == 1 && guard) {
-              if (lane == 0) mbar_arrive(bar);
-              bar = &sh->landed[guarded % kCaOk];
+        // keys two tiles before values, as they are used: a buffer is in use for no longer than it has to be
+        int z1 = 0, z2 = 0;
+        for (int k = lo; ok && k < hi + 2; ++k) {
+          int z = 0;
+          if (k < hi) {
+            if (t.tile0 + k - base >= 32) {
+              base += 32;
+              now = entries();
             }
-            ca_copy_tile(smem + L::kRingOff + s * L::kTile, kv ? &maps.v : &maps.k, z, bar, (uint32_t)L::kTile);
-            issued = (uint32_t)kv + 1u;  // (of this tile, where a wait runs out)
+            const int page = __shfl_sync(0xffffffffu, now, t.tile0 + k - base);
+            z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
+            ok = keys < kPairs || ca_wait(&sh->free[2u * pk.r], pk.ph ^ 1u, p.err);
+            if (ok && !test_skip_copy(2u * keys))
+              ca_copy_tile(smem + L::kRingOff + 2u * pk.r * L::kTile, &maps.k, z, &sh->full[2u * pk.r], (uint32_t)L::kTile);
+            if (ok) ++keys, pk.step(1u);
           }
-          if (!ok) break;
-          issued = 0;
-          buf += 2u;
-          guarded += guard;
+          const int v = k - 2;
+          if (ok && v >= lo) {
+            const uint32_t x = 2u * pv.r + 1u;
+            ok = values < kPairs || ca_wait(&sh->free[x], pv.ph ^ 1u, p.err);
+            // guarded values land at a barrier of their own: the guard tells when they may be used
+            const bool guard = v - lo < gw || v - lo >= gc;
+            if (ok && !test_skip_copy(2u * values + 1u)) {
+              uint64_t* bar = &sh->full[x];
+              if (guard) {
+                if (lane == 0) mbar_arrive(bar);
+                bar = &sh->landed[guarded % kCaOk];
+              }
+              ca_copy_tile(smem + L::kRingOff + x * L::kTile, &maps.v, z2, bar, (uint32_t)L::kTile);
+            }
+            if (ok) ++values, guarded += guard, pv.step(1u);
+          }
+          z2 = z1;
+          z1 = z;
         }
       }
       if (at_end) break;
@@ -719,8 +738,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       mbar_arrive(&sh->desc_full[ds]);
     }
     // the copies in flight land before the CTA exits (some may be, if a wait of another warp ran out)
-    for (uint32_t k = buf > NB ? buf - NB : 0; k < buf + issued; ++k)
-      if (!test_skip_copy(k)) ca_wait(&sh->full[k % NB], (k / NB) & 1u, p.err);
+    for (uint32_t k = keys > kPairs ? keys - kPairs : 0; k < keys; ++k)
+      if (!test_skip_copy(2u * k)) ca_wait(&sh->full[2u * (k % kPairs)], (k / kPairs) & 1u, p.err);
+    for (uint32_t k = values > kPairs ? values - kPairs : 0; k < values; ++k)
+      if (!test_skip_copy(2u * k + 1u)) ca_wait(&sh->full[2u * (k % kPairs) + 1u], (k / kPairs) & 1u, p.err);
     for (uint32_t k = guarded > kCaOk ? guarded - kCaOk : 0; k < guarded; ++k)
       ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err);
   } else if (warp <= 2) {
@@ -729,17 +750,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const int t = warp - 1;
     constexpr uint32_t fmt = TYPE == 0 ? 1u : 0u;
     const uint32_t idesc_s = umma_idesc(kCaKeys, fmt, fmt, 0u, 0u), idesc_o = umma_idesc(D, fmt, fmt, 0u, 1u);
-    // Tile i of a part has the buffers 2 r (keys) and 2 r + 1 (values) of the ring, r its place among kPairs, and the
-    // phase ph. (A slot's turn is a chain of instructions that both slots' pace hangs on: places are stepped, not divided
-    // out.)
-    constexpr uint32_t kPairs = NB / 2;
-    struct Place {
-      uint32_t r, ph;
-      __device__ __forceinline__ void step(uint32_t by) {
-        r += by;
-        if (r >= kPairs) r -= kPairs, ph ^= 1u;
-      }
-    };
     Place part0 = {0u, 0u};             // the part's first tile
     uint32_t oks = 0, sc = 0, pc = 0;   // guarded tiles, scores issued and weights used so far
     const uint32_t s_col = tmem + ca_s_col(t, 0), o_col = tmem + ca_o_col(t);
