@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int u0 = (e.rows > 128 ? 128 * t : 0) + qd * 32, c = lane & 7;
       if (e.rows <= 128 && t == 1) return;  // (slot 0's rows)
       uint8_t* qt = smem + t * L::kQ + qd * 32 * 128;
-#pragma unroll
+#pragma unroll 1  // (a part runs it once: the shorter code is sooner there)
       for (int k = 0; k < 8; ++k) {
         const int r = 4 * k + (lane >> 3), u = u0 + r;
         const int R2 = e.row0 + (u < e.rows ? u : 0), j2 = wk.by_g(R2);
@@ -955,16 +955,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           continue;
         }
         tc_fence_after();
-        // With the last scores this slot's Q is done with (row tiles: it is this slot's alone): the next part's comes in
-        // behind the last tile's weights. (A cut part's end needs the place.)
-        if (jt + 1 == nt && two && !cut) {
-          const int dn = (seq + 1) % kCaDesc;
-          if (__all_sync(0xffffffffu, mbar_test(&sh->desc_full[dn], (uint32_t)((seq + 1) / kCaDesc) & 1u)) &&
-              sh->part[dn].hi > 0) {
-            load_q(sh->part[dn]);
-            have_q = true;
-          }
-        }
         const bool masked = i < gw || i >= gc;
         auto mask = [&](uint32_t (&x)[32], int first) {  // columns first .. first + 31
           const int top = rel - i * kCaKeys - first;    // seen: bottom < c <= top
@@ -1052,9 +1042,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
       }
-      if (have_q) hand_q((seq + 1) % kCaDesc);
+      // With its last scores this slot is done with its Q (row tiles: it is this slot's alone), and the next part's comes
+      // in beside the last product of the weights, its scores beside this part's end. (A cut part's end needs the place.)
+      if (ok && nt > 0 && two && !cut) {
+        const int dn = (seq + 1) % kCaDesc;
+        if (__all_sync(0xffffffffu, mbar_test(&sh->desc_full[dn], (uint32_t)((seq + 1) / kCaDesc) & 1u)) &&
+            sh->part[dn].hi > 0) {
+          load_q(sh->part[dn]);
+          have_q = true;
+        }
+      }
       // ---- the part's end
       if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
+      if (have_q) hand_q((seq + 1) % kCaDesc);
       if (!ok) break;
       tc_fence_after();
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
