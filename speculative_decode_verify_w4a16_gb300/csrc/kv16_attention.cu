@@ -955,13 +955,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           continue;
         }
         tc_fence_after();
-        const bool masked = i < gw || i >= gc;
+        // seen: the columns bottom < c <= top (where a whole warp sees all of them, there is nothing to mask)
+        const int top = rel - i * kCaKeys, bottom = p.window > 0 ? top - p.window : -1;
+        bool masked = i < gw || i >= gc;
+        if (masked) masked = __any_sync(0xffffffffu, top < kCaKeys - 1 || bottom >= 0);
         auto mask = [&](uint32_t (&x)[32], int first) {  // columns first .. first + 31
-          const int top = rel - i * kCaKeys - first;    // seen: bottom < c <= top
-          const int bottom = p.window > 0 ? top - p.window : -1;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
-            if (c > top || c <= bottom) x[c] = __float_as_uint(-INFINITY);
+            if (first + c > top || first + c <= bottom) x[c] = __float_as_uint(-INFINITY);
         };
         // the weights of 32 columns, as pairs of the cache's type, and their sum
         auto weigh = [&](const uint32_t (&x)[32], uint32_t* pr, float u) {
@@ -1054,8 +1055,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       }
       // ---- the part's end
       if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
-      if (have_q) hand_q((seq + 1) % kCaDesc);
-      if (!ok) break;
+      if (!ok) {
+        if (have_q) ca_copy_wait();
+        break;
+      }
+      bool to_hand = have_q;
       tc_fence_after();
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
@@ -1098,6 +1102,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           const uint32_t col = (uint32_t)c0;
+          if (to_hand && c0 > 0) {  // (behind the first columns: the rows are there by now)
+            hand_q((seq + 1) % kCaDesc);
+            to_hand = false;
+          }
           uint32_t ov[32];
           if (nt > 0) {
             tmem_ld_32x32b_x32(trow + ca_o_col(t) + col, ov);
@@ -1143,6 +1151,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
       }
+      if (to_hand) hand_q((seq + 1) % kCaDesc);
       if (!two) {  // slot 1's scores and sums may be written again
         if (t == 0) {
           tc_fence_before();
