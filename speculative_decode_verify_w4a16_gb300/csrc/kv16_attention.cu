@@ -9,17 +9,21 @@
 //
 // Split: the units of all requests end to end, by their estimated work, cut into
 // one run a CTA (a CTA an SM), at tile boundaries. A unit that is cut leaves
-// its pieces' maxima, sums and unnormalised outputs in the workspace, and the
+// its pieces' references, sums and unnormalised outputs in the workspace, and the
 // CTA that finishes last merges them, in the order of the keys: every CTA gets
-// the same work whatever the lengths are, decoding rows and prompts share a
-// launch, the host needs no length, and no CTA waits for another.
+// much the same work whatever the lengths are, decoding rows and prompts share a
+// launch, the host needs no length, and no CTA waits for another. A cut costs some
+// 10 to 18 thousand cycles (a part's start and end 3 to 9 thousand, a tile of two
+// row tiles 1400, of one 600 to 800), so it moves to a unit's end where that is
+// near, and few units get few CTAs.
 //
 // In a CTA (tcgen05, TMEM, TMA):
 //   warp 0        the run's parts (a unit or a piece of one), published in a
-//                 ring of descriptors; TMA copies of K and V tiles into a ring
-//   warp 1        the MMAs of both slots, in turn: S = Q K^T (128 x 128 x D, both
-//                 from shared memory) and O += P V (P from TMEM, V as it was
-//                 loaded: the MN-major operand)
+//                 ring of descriptors; TMA copies of K and V tiles into a ring,
+//                 K two tiles ahead of V, as they are used
+//   warps 1, 2    the MMAs of slot 0 and 1: S = Q K^T (128 x 64 x D, both from
+//                 shared memory) two tiles ahead of O += P V (P from TMEM, V as
+//                 it was loaded: the MN-major operand)
 //   warp 3        the guard: looks through the values of tiles that some row
 //                 sees in part, and takes out NaN and infinities, which a weight
 //                 of zero would not hide; rows that do see them get them added
@@ -30,6 +34,30 @@
 // With more than 128 rows the two slots are two row tiles, which share every
 // key tile; with fewer they take the key tiles in turn and are merged at the
 // part's end. While one slot's softmax runs, the tensor pipe works for the other.
+//
+// Bound and measured (bf16, D 128, 64 heads over 8, unless said; times by events):
+//   long contexts, 4 requests of 120 to 131 K, one row each: HBM, 297 us for 2.04 GB
+//     (1.01 of a plain copy's rate)
+//   16 requests of 4 to 8 K, 5 rows each: 79 us for 392 MB (0.73); a run is some 79
+//     tiles, its start, end and merge a third of it
+//   a chunk of 2048 rows after 30720: the tensor pipe, 1.42 ms cold to 1.57 ms in a
+//     row (the clock falls): 1.5 to 1.36 PFLOP/s, 0.79 to 0.71 of the bf16 peak. Of
+//     some 1640 cycles a tile the MMAs take 1370: with N = 64 S takes 52 cycles a k-step
+//     for 32 of arithmetic (shared memory: 6 KB a step at 128 bytes a cycle); with
+//     one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
+//     arithmetic no less than with it
+//   7 prompts of up to 1501 rows, 16 heads of their own: 94 us, 0.38 of the peak; the
+//     longest run has 1.3 times the mean's work (a unit of up to 24 tiles is the
+//     grain), and parts of 4 to 24 tiles start and end in 7000 cycles
+//   49 requests, one in 8 a prompt, fp16, D 64, window 4096: 412 to 426 us, 0.35 of the
+//     peak; softmax and hand-offs, some 1250 cycles a tile (the MMAs 700, the
+//     exponentials 512)
+// Tried and slower, or no better: 128-key tiles with one score buffer (chunk 1586 us
+// when this form took 1500), a row's columns over two warpgroups, two warpgroups a
+// slot taking its tiles in turn, one MMA warp for both slots (in turn, or whichever is
+// ready), the next scores loaded beside the store of the weights (mixed 429 -> 477),
+// outputs through shared memory in whole lines (prompts 100 -> 105), tiles that a warp
+// does not see at all passed over (mixed 423 -> 435: the branch lengthens the others).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
