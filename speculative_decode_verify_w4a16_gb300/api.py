@@ -358,7 +358,11 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
 
 def check_device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error status."""
-    return int(lib().w4a16_check_device_status(_stream(stream)))
+    status = int(lib().w4a16_check_device_status(_stream(stream)))
+    if status:  # a wait that ran out may have left a count in a default workspace of kv16_attention: new ones from here on
+        for k in [k for k in _stream_ws if k[2] == "kv16_attention"]:
+            _stream_ws.pop(k, None)
+    return status
 
 
 # ------------------------------------------------------ paged 8-bit cache

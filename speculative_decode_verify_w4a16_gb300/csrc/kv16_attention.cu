@@ -4,8 +4,8 @@
 // out = sum_j softmax_j(scale q . k_j) v_j. The query rows of a key/value head
 // are its G = H / Hkv query heads at every new token, row r = token * G +
 // head-in-group, so that keys and values are read once for the group. A unit
-// is 256 of those rows of one request and head, against 128-key tiles (two
-// pages) from the first key that any of its rows sees to the last.
+// is 256 of those rows of one request and head, against 64-key tiles (pages)
+// from the first key that any of its rows sees to the last.
 //
 // Split: the units of all requests end to end, by their estimated work, cut into
 // one run a CTA (a CTA an SM), at tile boundaries. A unit that is cut leaves

@@ -67,3 +67,24 @@ def test_a_wait_that_runs_out(hook, dtype, D, n, H, Hkv, first, skip):
             for x in (cache.k, cache.v))
     want, mag = ref.attention(q[0], k, v, first)
     assert ((out[0].to(dev()).double() - want).abs() <= ref.attention_bound(want, mag, v, dtype)).all()
+
+
+def test_default_workspaces_are_renewed(hook):
+    """The same without a workspace of one's own: after the report the next calls give what the first one gave."""
+    g = torch.Generator(device=dev())
+    g.manual_seed(1)
+    cache = sv.KV16Cache(*(torch.randn(1, 9, 1, 64, 128, generator=g, device=dev()).bfloat16() for _ in range(2)))
+    q = torch.randn(1, 3, 4, 128, generator=g, device=dev()).bfloat16()
+    lens = torch.tensor([60000], dtype=torch.int32, device=dev())
+    table = (torch.arange(940, dtype=torch.int32, device=dev()) % 9).view(1, 940)
+    good = sv.kv16_attention(q, cache, 0, table, lens)
+    assert sv.check_device_status() == 0
+    assert hook(2) == 0
+    try:
+        sv.kv16_attention(q, cache, 0, table, lens)
+        assert sv.check_device_status() == 4
+    finally:
+        assert hook(-1) == 0
+    for _ in range(2):
+        assert torch.equal(sv.kv16_attention(q, cache, 0, table, lens), good)
+    assert sv.check_device_status() == 0
