@@ -742,24 +742,26 @@ def _rows(t: torch.Tensor, name: str, dev: int):
     """(rows, heads, D, elements from row to row) of a tensor [rows, heads, D]
     or [B, n, heads, D] whose heads are dense and whose rows are evenly apart
     (a slice of a fused projection)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     shape, strides = t.shape, t.stride()
     if len(shape) == 3:
         rows, heads, D = shape
         stride, sh, sd = strides
+        if sd == 1 and sh == D and rows > 1 and stride % 8 == 0 and stride >= heads * D and t.get_device() == dev:
+            return rows, heads, D, stride
     elif len(shape) == 4:
         B, n, heads, D = shape
         rows = B * n
         outer, stride, sh, sd = strides
         if n == 1:
             stride = outer
-        elif B > 1 and outer != n * stride:
-            raise ValueError(f"{name}: its rows must be evenly apart")
-    else:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if len(shape) not in (3, 4):
         raise ValueError(f"{name} must have 3 or 4 dimensions, got {tuple(shape)}")
+    if len(shape) == 4 and n > 1 and B > 1 and outer != n * stride:
+        raise ValueError(f"{name}: its rows must be evenly apart")
     if rows <= 1:
         stride = heads * D + -(heads * D) % 8
     if (D > 1 and sd != 1) or (heads > 1 and sh != D):
@@ -797,7 +799,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: Rope, out: Optional[to
         _need(positions, "positions", torch.int32, lead)
     rot = _need_rope(freqs, D, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         out_stride = heads * D
     elif out is x:
         out_stride = stride
@@ -843,9 +845,11 @@ def _need_kv16(c: KV16Cache, layer: int, dev: int):
         raise ValueError("the cache must be torch.bfloat16 or torch.float16")
     if len(shape) != 5 or shape[3] != KV_BLOCK:
         raise ValueError(f"the cache must have shape (layers, pages, Hkv, {KV_BLOCK}, D), got {tuple(shape)}")
-    if not (_is(k, dtype, dev, shape) and _is(c.v, dtype, dev, shape)):
+    v = c.v
+    if not (k.get_device() == dev == v.get_device() and v.dtype is dtype and v.shape == shape and k.is_contiguous()
+            and v.is_contiguous()):
         _need(k, "cache.k", dtype, shape)
-        _need(c.v, "cache.v", dtype, shape)
+        _need(v, "cache.v", dtype, shape)
     layers, pages, Hkv, _, D = shape
     if not 0 <= layer < layers:
         raise ValueError(f"layer {layer} is not one of the cache's {layers}")
@@ -885,8 +889,11 @@ def kv16_append(cache: KV16Cache, layer: int, k_new: torch.Tensor, v_new: torch.
     kind, pages, Hkv, D, at = _need_kv16(cache, layer, dev)
     dtype = cache.k.dtype
     T, heads, width, k_stride = _rows(k_new, "k_new", dev)
-    v_rows, v_heads, v_width, v_stride = _rows(v_new, "v_new", dev)
-    if (heads, width) != (Hkv, D) or (v_rows, v_heads, v_width) != (T, Hkv, D):
+    if v_new.shape == k_new.shape and v_new.stride() == k_new.stride() and v_new.get_device() == dev:
+        v_rows, v_heads, v_width, v_stride = T, heads, width, k_stride
+    else:
+        v_rows, v_heads, v_width, v_stride = _rows(v_new, "v_new", dev)
+    if heads != Hkv or width != D or v_rows != T or v_heads != Hkv or v_width != D:
         raise ValueError(f"k_new and v_new must have rows of ({Hkv}, {D}), got {tuple(k_new.shape)} and "
                          f"{tuple(v_new.shape)}")
     if k_new.dtype is not dtype or v_new.dtype is not dtype:
@@ -899,7 +906,7 @@ def kv16_append(cache: KV16Cache, layer: int, k_new: torch.Tensor, v_new: torch.
         if q_rows != T or q_width != D or q.dtype is not dtype:
             raise ValueError(f"q must be {dtype} with {T} rows of heads of {D}, got {q.dtype} {tuple(q.shape)}")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             out_stride = H * D
         elif q_out is q:
             out_stride = q_stride
