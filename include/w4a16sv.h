@@ -526,8 +526,8 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
  *              at its start zero
  * Arithmetic: scores and sums in fp32, the softmax weights rounded to the
  * cache's type for the sum of the values, out rounded once. The order of the
- * sums depends on the whole batch (it is cut into equal shares of work), not on
- * timing: the same call gives the same bits.
+ * sums depends on the whole batch (how its work is shared out), not on timing:
+ * the same call gives the same bits.
  * T * H < 2^31, H / Hkv <= 1024, max_blocks <= 2^21 (W4A16_ERR_UNSUPPORTED
  * beyond, and for T, B, H and max_blocks whose estimated work passes 2^55 in
  * all). Launch rules as for w4a16_linear.

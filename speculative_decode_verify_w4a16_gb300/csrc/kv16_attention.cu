@@ -15,7 +15,8 @@
 // launch, the host needs no length, and no CTA waits for another. A cut costs some
 // 10 to 18 thousand cycles (a part's start and end 3 to 9 thousand, a tile of two
 // row tiles 1400, of one 600 to 800), so it moves to a unit's end where that is
-// near, and few units get few CTAs.
+// near, and few units get few CTAs. Many short units are taken whole from a queue
+// instead; which CTA has a unit does not show in its rows.
 //
 // In a CTA (tcgen05, TMEM, TMA):
 //   warp 0        the run's parts (a unit or a piece of one), published in a
@@ -46,17 +47,16 @@
 //     for 32 of arithmetic (shared memory: 6 KB a step at 128 bytes a cycle); with
 //     one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
 //     arithmetic no less than with it
-//   7 prompts of up to 1501 rows, 16 heads of their own: 94 us, 0.38 of the peak; the
-//     longest run has 1.3 times the mean's work (a unit of up to 24 tiles is the
-//     grain), and parts of 4 to 24 tiles start and end in 7000 cycles
-//   49 requests, one in 8 a prompt, fp16, D 64, window 4096: 412 to 426 us, 0.35 of the
+//   7 prompts of up to 3002 rows, 16 heads of their own: 81 us, 0.45 of the peak;
+//     parts of 4 to 47 tiles start and end in 7000 cycles, and masked tiles take more
+//   49 requests, one in 8 a prompt, fp16, D 64, window 4096: 406 us, 0.36 of the
 //     peak; softmax and hand-offs, some 1250 cycles a tile (the MMAs 700, the
 //     exponentials 512)
 // Tried and slower, or no better: 128-key tiles with one score buffer (chunk 1586 us
 // when this form took 1500), a row's columns over two warpgroups, two warpgroups a
 // slot taking its tiles in turn, one MMA warp for both slots (in turn, or whichever is
 // ready), the next scores loaded beside the store of the weights (mixed 429 -> 477),
-// outputs through shared memory in whole lines (prompts 100 -> 105), tiles that a warp
+// outputs through shared memory in whole lines (5 us of 100 for prompts), tiles that a warp
 // does not see at all passed over (mixed 423 -> 435: the branch lengthens the others).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -80,6 +80,14 @@ constexpr int kCaLeast = 8;       // tiles a CTA has at least, where units are c
 constexpr int kCaMerge = 12;      // tiles that a cut is worth
 constexpr int kCaSnap = 16;       // tiles that a cut may move to the unit's begin or end
 
+// Many short units are not cut into runs but taken from a queue, whole ones, a request's longest first: where no unit has
+// more than kCaQueueTiles tiles and there are twice as many as CTAs, or four times the tiles and four times as many units.
+// Measured, cut / queue, us: 7 prompts of up to 3002 rows 94 / 81, 64 requests of up to 2000 tokens 60 / 53.5, 32 prompts of
+// up to 512 rows 122 / 114, 4 of 4000 rows 821 / 770, 49 requests with a window of 4096 421 / 406; fewer and longer units, 64
+// requests of up to 4000 tokens (3.4 units of 32 tiles a CTA): 101.5 / 104; 256 of up to 6000 (13.5 of 47): 300 / 301.
+constexpr int kCaQueueTiles = 32;
+constexpr int kCaMany = 65535;  // units that are too many to be counted (more than any number of CTAs wants)
+
 // Weights are taken against a reference: the largest score of the first tile that
 // the row sees keys of. It is raised (and the sums so far, in TMEM, rescaled) by a
 // tile whose weights, 64 at a time, add up to more than this; no weight is then
@@ -100,6 +108,7 @@ struct CaWork {
   int wide;            // out lies on 32 bytes
   uint64_t ctas_inv;   // floor(2^64 / ctas)
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
+  int* queue;          // units taken, CTAs finished
   float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain
   float* part_o;       // [2 * ctas][rows_cap][D] unnormalised sums
 };
@@ -539,7 +548,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // Each thread sums a row of requests; the scratch lies where Q will
   struct Scratch {
     int64_t sums[kCaThreads / 32];
-    int units[kCaThreads / 32];
+    int units[kCaThreads / 32], longest[kCaThreads / 32];
     int64_t at[2];  // the work before the requests that the run begins and ends in
     CaPlace place[2];
   };
@@ -547,16 +556,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const int per = (p.B + kCaThreads - 1) / kCaThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int64_t mine = 0;
-  int units = 0;
+  int units = 0, longest = 0;
   for (int b = b0; b < b1; ++b) {
     const CaRequest r = ca_request(p, b, cta == 0);
     if (r.cnt > 0) {
       const CaLoad w = ca_load(p, wk, r);
       mine += p.Hkv * w.before(w.units);
-      units = min(units + p.Hkv * w.units, 65535);  // (more than any number of CTAs will do)
+      units = (int)min((int64_t)units + (int64_t)p.Hkv * w.units, (int64_t)kCaMany);
+      longest = max(longest, ca_tiles(p, wk, r, w.units - 1).nt);
     }
   }
   units = __reduce_add_sync(0xffffffffu, units);
+  longest = __reduce_max_sync(0xffffffffu, longest);
   int64_t upto = mine;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
@@ -564,7 +575,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (lane >= k) upto += o;
   }
   if (lane == 31) scr->sums[warp] = upto;
-  if (lane == 31) scr->units[warp] = units;
+  if (lane == 31) {
+    scr->units[warp] = units;
+    scr->longest[warp] = longest;
+  }
   if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1, CaRequest{0, 0, 0}};
   __syncthreads();
   grid_launch_dependents();  // (TMEM is allocated: no later kernel can hold it while this one waits for it)
@@ -574,7 +588,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (w < warp) at += scr->sums[w];
     W += scr->sums[w];
     units += scr->units[w];
+    longest = max(longest, scr->longest[w]);
   }
+  const bool queue = units < kCaMany && ((units >= 2 * wk.ctas && longest <= kCaQueueTiles) ||
+                                         (units >= 4 * wk.ctas && longest <= 4 * kCaQueueTiles));
   // Fewer units than CTAs: as many CTAs as give each unit a whole number of pieces of at least kCaLeast tiles, unless
   // all of them would be done sooner although nearly every one then has to merge.
   int C = wk.ctas;
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   }
   auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, inv * (uint64_t)c); };
 #pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < 2 && !queue; ++e) {
     const int64_t x = bound(cta + e);
     if (x < at || x >= at + mine) continue;
     int64_t a = at;
@@ -649,10 +666,48 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     CaRequest r = begin.r;
     CaLoad w;
     if (b < p.B) w = ca_load(p, wk, r);
-    while (ok && b < p.B) {
-      const bool at_end = b == end.b && kvh == end.kvh && unit == end.unit;
+    // the queue: 32 requests at a time, a lane each, of which the first has the units from `from` on
+    int group = 0, from = 0, mine_units = 0, mine_upto = 0;
+    CaRequest mine_r;
+    auto look = [&]() {
+      mine_r = group + lane < p.B ? ca_request(p, group + lane, false) : CaRequest{0, 0, 0};
+      mine_units = mine_r.cnt > 0 ? ca_load(p, wk, mine_r).units * p.Hkv : 0;
+      mine_upto = mine_units;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, mine_upto, k);
+        if (lane >= k) mine_upto += o;
+      }
+    };
+    if (queue) look();
+    while (ok) {
+      bool at_end = false;
+      if (queue) {
+        int u = lane == 0 ? atomicAdd(wk.queue, 1) : 0;
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (u >= units) break;
+        int in_group;
+        while (u - from >= (in_group = __shfl_sync(0xffffffffu, mine_upto, 31)) && group + 32 < p.B) {
+          from += in_group;
+          group += 32;
+          look();
+        }
+        const int l = __ffs(__ballot_sync(0xffffffffu, mine_upto > u - from)) - 1;
+        if (l < 0) break;
+        b = group + l;
+        r.at = __shfl_sync(0xffffffffu, mine_r.at, l);
+        r.cnt = __shfl_sync(0xffffffffu, mine_r.cnt, l);
+        r.past = __shfl_sync(0xffffffffu, mine_r.past, l);
+        const int n = __shfl_sync(0xffffffffu, mine_units, l);
+        const int k = u - from - (__shfl_sync(0xffffffffu, mine_upto, l) - n);  // the last rows first, all heads of them
+        kvh = k % p.Hkv;
+        unit = n / p.Hkv - 1 - k / p.Hkv;
+      } else {
+        if (b >= p.B) break;
+        at_end = b == end.b && kvh == end.kvh && unit == end.unit;
+      }
       const CaTiles t = ca_tiles(p, wk, r, unit);
-      const int lo = first ? begin.cut : 0, hi = at_end ? end.cut : t.nt;
+      const int lo = !queue && first ? begin.cut : 0, hi = at_end ? end.cut : t.nt;
       if (hi > lo) {
         const int ds = seq % kCaDesc;
         if (seq >= kCaDesc && !ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err)) {
@@ -743,6 +798,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           z1 = z;
         }
       }
+      if (queue) continue;
       if (at_end) break;
       first = false;
       if (++unit == w.units) {
@@ -1245,6 +1301,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // ---------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
+  if (queue && tid == 0 && atomic_add_acq_rel(wk.queue + 1, 1) == wk.ctas - 1) wk.queue[0] = wk.queue[1] = 0;
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512u);
@@ -1261,7 +1318,7 @@ static CaPlan ca_plan(int T, int H, int Hkv, int D, int num_sms) {
   k.ctas = num_sms > 0 ? num_sms : 1;
   const int64_t rows = (int64_t)T * (H / Hkv);
   k.rows_cap = rows < 256 ? (int)rows : 256;
-  k.done_bytes = ((size_t)k.ctas * 4 + 255) / 256 * 256;
+  k.done_bytes = ((size_t)(k.ctas + 2) * 4 + 255) / 256 * 256;
   k.ml_bytes = ((size_t)2 * k.ctas * k.rows_cap * 8 + 255) / 256 * 256;
   k.total = k.done_bytes + k.ml_bytes + (size_t)2 * k.ctas * k.rows_cap * D * 4;
   return k;
@@ -1309,6 +1366,7 @@ cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void
   wk.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   wk.done = reinterpret_cast<int*>(ws);
+  wk.queue = wk.done + k.ctas;
   wk.part_ml = reinterpret_cast<float2*>(ws + k.done_bytes);
   wk.part_o = reinterpret_cast<float*>(ws + k.done_bytes + k.ml_bytes);
   if (D == 128)

@@ -146,3 +146,50 @@ def test_rows_of_every_width(dtype, interleaved):
         want, mag = ref.rotate(x, cos, sin, interleaved)
         assert ((got.double() - want).abs() <= ref.rotation_bound(want, mag, dtype)).all(), (heads, D, rot)
     assert sv.check_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,D,H,Hkv", [(BF16, 128, 16, 8), (F16, 64, 24, 8)])
+@pytest.mark.parametrize("lens,counts,window", [
+    ([int(x) for x in np.random.default_rng(5).integers(0, 1900, 60)], [1 + b % 5 * (b % 2) for b in range(60)], 0),
+    ([0] * 12, [900, 0, 1, 64, 65, 300, 1500, 2, 128, 129, 700, 33], 0),
+    ([int(x) for x in np.random.default_rng(6).integers(0, 5000, 40)], [b * 13 % 700 for b in range(40)], 500),
+    ([5] * 300, [b % 3 for b in range(300)], 0),
+])
+def test_many_short_units(dtype, D, H, Hkv, lens, counts, window):
+    """More units than CTAs several times over: taken whole, from a queue that every call leaves as it was."""
+    c = Case(8, dtype, D, H, Hkv, lens, counts, pad=2)
+    ws = torch.zeros(sv.kv16_attention_workspace_bytes(c.T, H, Hkv, D), dtype=torch.uint8, device=dev())
+    first = None
+    for _ in range(4):
+        out = torch.full((c.T, H, D), 7.0, dtype=dtype, device=dev())
+        c.run(out=out, window=window, ws=ws)
+        first = out if first is None else first
+        assert torch.equal(out, first)  # whichever CTA has a unit
+    assert sv.check_device_status() == 0
+    assert (first[sum(counts):] == 7).all()
+    c.check(first, window=window, requests=[b for b in range(len(lens)) if counts[b]][::3])
+    # a request alone, cut or not, is the same within the bound: and a batch of them is again whole afterwards
+    alone = Case(9, dtype, D, H, Hkv, [3000], [2])
+    alone.check(alone.run(ws=ws))
+    assert torch.equal(c.run(window=window, ws=ws)[:sum(counts)], first[:sum(counts)])
+
+
+def test_many_short_units_with_bad_requests():
+    """Requests that are left out, and pages that are none, among many: the others are served."""
+    lens, counts = [100 + b for b in range(80)], [1 + b % 4 for b in range(80)]
+    c = Case(10, BF16, 128, 8, 8, lens, counts)
+    good = c.run()
+    assert sv.check_device_status() == 0
+    bad = list(lens)
+    bad[7], bad[40] = -1, 1 << 20
+    table = c.table.clone()
+    table[79, 0] = 1 << 20
+    out = sv.kv16_attention(c.q, c.cache, c.layer, table.to(dev()), _i32(bad), row_start=_i32(_starts(counts)))
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 5  # W4A16_ERR_DEVICE_INPUT
+    at = _starts(counts)
+    for b in range(79):
+        if b not in (7, 40):
+            assert torch.equal(out[at[b]:at[b + 1]], good[at[b]:at[b + 1]]), b
+    assert torch.equal(c.run(), good)
+    assert sv.check_device_status() == 0
