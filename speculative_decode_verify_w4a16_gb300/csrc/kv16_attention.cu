@@ -270,6 +270,7 @@ __device__ __forceinline__ CaRequest ca_request(const Kv16AttnParams& p, int b, 
   CaRequest r;
   r.at = p.start ? p.start[b] : b * p.per;
   const int end = p.start ? p.start[b + 1] : r.at + p.per;
+  const int len = p.lens[b];  // (fetched with the others)
   r.cnt = 0;
   r.past = 0;
   if (r.at < 0 || end < r.at || end > p.T) {
@@ -277,7 +278,7 @@ __device__ __forceinline__ CaRequest ca_request(const Kv16AttnParams& p, int b, 
     return r;
   }
   if (end == r.at) return r;
-  r.past = p.lens[b];
+  r.past = len;
   if (r.past < 0 || (int64_t)r.past + (end - r.at) > (int64_t)p.max_blocks * 64) {
     if (report) report_error(p.err, kErrInput);
     return r;
@@ -557,8 +558,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int64_t mine = 0;
   int units = 0, longest = 0;
+  CaRequest r = {0, 0, 0};
   for (int b = b0; b < b1; ++b) {
-    const CaRequest r = ca_request(p, b, cta == 0);
+    r = ca_request(p, b, cta == 0);
     if (r.cnt > 0) {
       const CaLoad w = ca_load(p, wk, r);
       mine += p.Hkv * w.before(w.units);
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const int even = units * max(1, min(C / units, (int)(w / (tile * kCaLeast * (float)units))));
     if (w / (float)even <= w / (float)C + tile * kCaMerge) {
       C = even;
-      inv = ~uint64_t(0) / (uint64_t)C;
+      inv = (uint64_t)(0xFFFFFFFFu / (uint32_t)C) << 32;  // (2^64 / C less 2^-32 C of it: a short division)
     }
   }
   auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, inv * (uint64_t)c); };
@@ -612,10 +614,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (x < at || x >= at + mine) continue;
     int64_t a = at;
     for (int b = b0; b < b1; ++b) {
-      const CaRequest r = ca_request(p, b, false);
-      if (r.cnt == 0) continue;
-      int64_t n = mine;  // (a thread with one request knows its work)
+      int64_t n = mine;  // (a thread with one request knows it, and its work)
       if (per > 1) {
+        r = ca_request(p, b, false);
+        if (r.cnt == 0) continue;
         const CaLoad w = ca_load(p, wk, r);
         n = p.Hkv * w.before(w.units);
       }
@@ -1287,7 +1289,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           __syncwarp();
           // many rows have few pieces, many pieces few rows: loads in flight along the one or the other
-          if (np <= 2)
+          if (np <= 2 && d.rows > 32)
             ca_merge<TYPE, D, 8, 2>(p, wk, d, list, np, warp - 4, lane);
           else
             ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane);
