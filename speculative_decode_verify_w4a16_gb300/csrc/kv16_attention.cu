@@ -76,9 +76,13 @@ constexpr int kCaSpecial = 12;  // guarded tiles of a part, at most (256 tokens'
 // The weights a key tile has in the split: two row tiles, or one.
 constexpr int kCaWeight2 = 8, kCaWeight1 = 5;
 constexpr int kCaOverhead = 256;  // keys that a unit's start and end are worth
-constexpr int kCaLeast = 8;       // tiles a CTA has at least, where units are cut
-constexpr int kCaMerge = 12;      // tiles that a cut is worth
-constexpr int kCaSnap = 16;       // tiles that a cut may move to the unit's begin or end
+constexpr int kCaSnap = 16;       // tiles that a cut may move to the unit's begin or end,
+constexpr int kCaSnapFew = 4;     // and where there are fewer units than CTAs
+// What a cut is worth, in tiles of one row tile: by itself, and for each row of each piece (stored, fetched and added); and
+// the tiles that a piece has at least. Measured: one row after 1003 tokens, units in 2 pieces 14.3 us, in 3 13.6, in 19
+// 15.9; 300 rows of 32 heads over 8 after 1000, whole 27.6 us, in 3 pieces 64; the same after 8000 in 3 pieces 75 us, and 82
+// where cuts lay a tile or two beside the units' ends.
+constexpr float kCaCut = 8.0f, kCaRowPiece = 0.056f, kCaLeast = 6.0f;
 
 // Many short units are not cut into runs but taken from a queue, whole ones, a request's longest first: where no unit has
 // more than kCaQueueTiles tiles and there are twice as many as CTAs, or four times the tiles and four times as many units.
@@ -594,17 +598,27 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   }
   const bool queue = units < kCaMany && ((units >= 2 * wk.ctas && longest <= kCaQueueTiles) ||
                                          (units >= 4 * wk.ctas && longest <= 4 * kCaQueueTiles));
-  // Fewer units than CTAs: as many CTAs as give each unit a whole number of pieces of at least kCaLeast tiles, unless
-  // all of them would be done sooner although nearly every one then has to merge.
+  // Fewer units than CTAs: each in a whole number of pieces, as many as pay, unless it is done sooner with a run for every
+  // CTA, nearly all of which then merge.
   int C = wk.ctas;
   uint64_t inv = wk.ctas_inv;
-  const int snap = units < C ? 1 : kCaSnap;  // (few units: nearly every cut is meant)
+  int snap = kCaSnap;
   if (units > 0 && units < C) {
-    const float tile = (float)(kCaWeight1 * G * kCaKeys), w = (float)W;
-    const int even = units * max(1, min(C / units, (int)(w / (tile * kCaLeast * (float)units))));
-    if (w / (float)even <= w / (float)C + tile * kCaMerge) {
-      C = even;
+    const float all = (float)W / (float)(kCaWeight1 * G * kCaKeys), per_unit = all / (float)units;
+    const float row = kCaRowPiece * fminf(256.0f, (float)p.T * (float)p.H / (float)units);
+    int k = max(1, min(C / units, (int)fminf(sqrtf(per_unit / row), per_unit / kCaLeast)));
+    float even = per_unit / (float)k + kCaCut + (float)k * row;
+    if (k == 1 || per_unit <= even) {
+      k = 1;
+      even = per_unit + kCaCut;  // (units of different lengths are cut all the same)
+    }
+    // (a run for every CTA: most have a second part to start)
+    if (even <= all / (float)C + 1.5f * kCaCut + ((float)C / (float)units + 2.0f) * row) {
+      C = units * k;
+      snap = max(1, min(kCaSnap, (int)(per_unit / (float)(4 * k))));
       inv = (uint64_t)(0xFFFFFFFFu / (uint32_t)C) << 32;  // (2^64 / C less 2^-32 C of it: a short division)
+    } else {
+      snap = kCaSnapFew;  // (nearly every cut is meant)
     }
   }
   auto bound = [&](int c) { return c >= C ? W : (int64_t)__umul64hi((uint64_t)W, inv * (uint64_t)c); };
@@ -1288,8 +1302,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             if (!__all_sync(0xffffffffu, in)) break;
           }
           __syncwarp();
-          // many rows have few pieces, many pieces few rows: loads in flight along the one or the other
-          if (np <= 2 && d.rows > 32)
+          // loads in flight along rows or along pieces: whichever takes fewer turns, each of them a load's latency
+          if ((d.rows + 63) / 64 * ((np + 1) / 2) < (d.rows + 7) / 8 * ((np + 7) / 8))
             ca_merge<TYPE, D, 8, 2>(p, wk, d, list, np, warp - 4, lane);
           else
             ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane);
