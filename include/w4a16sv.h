@@ -518,7 +518,8 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
  * it may be.
  *   q, out     device [T][H][D] of the cache's type (16-byte aligned), rows of q
  *              q_stride elements apart (a multiple of 8), out dense; the rows
- *              of no request are left as they were
+ *              of no request are left as they were. out may be a dense q, and
+ *              overlaps it in no other way
  *   window     0: none
  *   workspace  kv16_attention_workspace_bytes() bytes (256-byte aligned), zero
  *              before its first use, and again after

@@ -360,8 +360,9 @@ def check_device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error status."""
     status = int(lib().w4a16_check_device_status(_stream(stream)))
     if status:  # a wait that ran out may have left a count in a default workspace of kv16_attention: new ones from here on
-        for k in [k for k in _stream_ws if k[2] == "kv16_attention"]:
-            _stream_ws.pop(k, None)
+        for k in list(_stream_ws):
+            if k[2] == "kv16_attention":
+                _stream_ws.pop(k, None)
     return status
 
 
@@ -947,8 +948,9 @@ def kv16_attention(q: torch.Tensor, cache: KV16Cache, layer: int, block_table: t
     kv16_append (lens: tokens before the step). The row at position p sees the
     keys 0 .. p, with a window the last `window` of them. ws: zeroed before its
     first use, and used by no two calls at once (default: one for each stream
-    and capture). Returns out, dense and of q's shape; its rows behind the last
-    request's are left as they were (undefined in a new tensor)."""
+    and capture). Returns out, dense and of q's shape (a dense q itself: in
+    place); its rows behind the last request's are left as they were (undefined
+    in a new tensor)."""
     dev = _device()
     kind, pages, Hkv, D, at = _need_kv16(cache, layer, dev)
     T, H, width, q_stride = _rows(q, "q", dev)

@@ -193,3 +193,30 @@ def test_many_short_units_with_bad_requests():
             assert torch.equal(out[at[b]:at[b + 1]], good[at[b]:at[b + 1]]), b
     assert torch.equal(c.run(), good)
     assert sv.check_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,counts", [([0, 700, 90], [300, 3, 70]), ([20000], [40]), ([9000], [300]),
+                                         ([50 + b for b in range(80)], [1 + b % 4 for b in range(80)])])
+def test_out_in_place_of_the_queries(lens, counts):
+    """Whole units, cut ones and the queue's."""
+    c = Case(11, BF16, 128, 16, 8, lens, counts)
+    want, before = c.run(), c.q.clone()
+    assert c.run(out=c.q) is c.q
+    assert sv.check_device_status() == 0
+    assert torch.equal(c.q, want)
+    c.q = before
+    c.check(want)
+
+
+def test_queries_that_are_not_finite_stay_with_their_rows():
+    c = Case(12, BF16, 128, 8, 2, [300, 2000], [130, 5])
+    want = c.run().clone()
+    for row, head, x in ((0, 0, torch.nan), (77, 3, torch.inf), (131, 7, -torch.inf), (134, 1, torch.nan)):
+        c.q[row, head, 5] = x
+    got = c.run()
+    hit = torch.zeros(c.T, 8, dtype=torch.bool, device=dev())
+    for row, head in ((0, 0), (77, 3), (131, 7), (134, 1)):
+        hit[row, head] = True
+    assert torch.equal(got[~hit], want[~hit])
+    assert not got[hit].isfinite().any()
+    assert sv.check_device_status() == 0
