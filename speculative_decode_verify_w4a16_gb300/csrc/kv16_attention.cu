@@ -41,10 +41,11 @@
 //     (1.01 of a plain copy's rate)
 //   16 requests of 4 to 8 K, 5 rows each: 79 us for 392 MB (0.73); a run is some 79
 //     tiles, its start, end and merge a third of it
-//   a chunk of 2048 rows after 30720: the tensor pipe, 1.42 ms cold to 1.57 ms in a
-//     row (the clock falls): 1.5 to 1.36 PFLOP/s, 0.79 to 0.71 of the bf16 peak. Of
-//     some 1640 cycles a tile the MMAs take 1370: with N = 64 S takes 52 cycles a k-step
-//     for 32 of arithmetic (shared memory: 6 KB a step at 128 bytes a cycle); with
+//   a chunk of 2048 rows after 30720: the tensor pipe and the softmax, 1.42 ms cold to
+//     1.57 ms in a row (the clock falls): 1.5 to 1.36 PFLOP/s, 0.79 to 0.71 of the bf16
+//     peak. Of some 1640 cycles a tile the MMAs of both slots take 1250 (626 each, 392
+//     of it S: with N = 64 a k-step takes 49 cycles for 32 of arithmetic, as shared
+//     memory gives 128 bytes a cycle), a slot's softmax 1000 and its hand-offs 400; with
 //     one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
 //     arithmetic no less than with it
 //   7 prompts of up to 3002 rows, 16 heads of their own: 81 us, 0.45 of the peak;
@@ -55,7 +56,7 @@
 // Tried and slower, or no better: 128-key tiles with one score buffer (chunk 1586 us
 // when this form took 1500), a row's columns over two warpgroups, two warpgroups a
 // slot taking its tiles in turn, one MMA warp for both slots (in turn, or whichever is
-// ready), the next scores loaded beside the store of the weights (mixed 429 -> 477),
+// ready), a slot's MMAs kept together (chunk 1500 -> 2010), the next scores loaded beside the store of the weights (mixed 429 -> 477),
 // outputs through shared memory in whole lines (5 us of 100 for prompts), tiles that a warp
 // does not see at all passed over (mixed 423 -> 435: the branch lengthens the others).
 #include <cudaTypedefs.h>
