@@ -220,3 +220,34 @@ def test_queries_that_are_not_finite_stay_with_their_rows():
     assert torch.equal(got[~hit], want[~hit])
     assert not got[hit].isfinite().any()
     assert sv.check_device_status() == 0
+
+
+def test_as_many_requests_as_are_taken():
+    """4096 requests (a CTA looks through them 32 at a time), some without rows."""
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(0, 130, 4096)]
+    counts = [int(x) for x in rng.integers(0, 3, 4096)]
+    c = Case(13, BF16, 128, 4, 1, lens, counts, pad=5)
+    out = torch.full((c.T, 4, 128), 7.0, dtype=BF16, device=dev())
+    c.run(out=out)
+    assert sv.check_device_status() == 0
+    assert (out[sum(counts):] == 7).all()
+    c.check(out, requests=[*range(0, 4096, 61), 4094, 4095])
+
+
+@pytest.mark.parametrize("lens,counts,window", [([50 + 7 * b for b in range(90)], [1 + b % 4 for b in range(90)], 0),
+                                                ([0] * 9, [700, 3, 128, 129, 0, 65, 300, 900, 1], 200),
+                                                ([1003], [1], 0), ([1000], [300], 0), ([40000, 3], [70, 1], 0)])
+def test_in_the_bounds_checked_build(lens, counts, window):
+    """The queue, whole units, pieces and their merges: nothing out of bounds, and the same bits."""
+    from speculative_decode_verify_w4a16_gb300 import _lib, build
+
+    c = Case(14, BF16, 128, 16, 8, lens, counts, pad=1)
+    want = c.run(window=window)
+    with _lib.use_library(build.build_bounds()):
+        got = c.run(window=window)
+        torch.cuda.synchronize()
+        assert sv.check_device_status() == 0  # W4A16_ERR_BOUNDS would be 7
+    n = sum(counts)
+    assert torch.equal(got[:n], want[:n])
+    c.check(want, window=window)
