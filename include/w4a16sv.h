@@ -525,8 +525,9 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
  *              before its first use, and again after
  *              W4A16_ERR_DEVICE_TIMEOUT; every other call leaves the counters
  *              at its start zero
- * Arithmetic: scores and sums in fp32, the softmax weights rounded to the
- * cache's type for the sum of the values, out rounded once. The order of the
+ * Arithmetic: scores and sums in fp32 (the scores may have any size that fp32
+ * holds), the softmax weights rounded to the cache's type for the sum of the
+ * values, out rounded once. The order of the
  * sums depends on the whole batch (how its work is shared out), not on timing:
  * the same call gives the same bits.
  * T * H < 2^31, H / Hkv <= 1024, max_blocks <= 2^21 (W4A16_ERR_UNSUPPORTED

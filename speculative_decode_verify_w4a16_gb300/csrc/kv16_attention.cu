@@ -103,6 +103,11 @@ template <int TYPE>
 constexpr float kCaMost = TYPE == 0 ? 256.0f : 32768.0f;
 template <int TYPE>
 constexpr float kCaUp = TYPE == 0 ? 0.0f : 8.0f;
+// A weight is 2^(s c - m), c the scale and m the reference times c, rounded, in one multiplication and addition: off by
+// the rounding of m, up to 2^-24 |m| powers of two, by the same for all of a row's keys. From this size of m on (the rounding
+// passes what the type holds from 2^28 on in fp16, 2^32 in bf16) the reference is kept as a score r, before the scale, and a
+// weight is 2^((s - r) c), the difference first (ca_far_tile, which such rows come to at every tile).
+constexpr float kCaFar = 1024.0f;
 
 struct CaMaps {
   CUtensorMap k, v;  // [pages * Hkv][D / 64][64][64]: halves of 64 columns apart, as they lie in shared memory
@@ -114,7 +119,7 @@ struct CaWork {
   uint64_t ctas_inv;   // floor(2^64 / ctas)
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
   int* queue;          // units taken, CTAs finished
-  float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain
+  float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain; or a score as CaRef
   float* part_o;       // [2 * ctas][rows_cap][D] unnormalised sums
 };
 
@@ -417,6 +422,107 @@ __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaSha
   }
 }
 
+// A reference and the sum against it, as they are handed over: (m, l), or (r, -l) where the reference is kept as a score.
+struct CaRef {
+  float ref, sum;
+  __device__ __forceinline__ bool far() const { return sum < 0.0f; }
+};
+// The larger reference of a and b, and what sums against each are worth against it, where one of them is kept as a score.
+// (One kept, one not: they lie far apart, or both where the rounding of r c is 2^-14.)
+__device__ __noinline__ float2 ca_factors(CaRef a, CaRef b, float c, CaRef* top) {
+  const float x = a.far() ? a.ref * c : a.ref, y = b.far() ? b.ref * c : b.ref;
+  if (a.far() && b.far()) {
+    *top = a.ref >= b.ref ? a : b;
+    return make_float2(ex2((a.ref - top->ref) * c), ex2((b.ref - top->ref) * c));
+  }
+  *top = x >= y ? a : b;
+  return make_float2(x >= y ? 1.0f : ex2(x - y), x >= y ? ex2(y - x) : 1.0f);
+}
+
+// A tile of a warp's rows, of which one at least keeps its reference as a score or will: its weights over its scores, the
+// largest score the reference where it is to be raised, the sums so far (not with the first tile, `more`) rescaled. The
+// warp's other rows get what they get without it, to the bit.
+struct CaRow {
+  float m, r, l;
+  bool ok;
+};
+template <int TYPE, int D>
+__device__ __noinline__ CaRow ca_far_tile(CaRow w, uint32_t col, uint32_t o_col, int top, int bottom, float c, bool raise,
+                                          bool more, uint64_t* before, uint32_t parity, unsigned* err) {
+  uint32_t x[16];
+  auto load = [&](int first) {
+    tmem_ld_32x32b<16>(col + (uint32_t)first, x);
+    tmem_wait_ld(x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (first + k > top || first + k <= bottom) x[k] = __float_as_uint(-INFINITY);
+  };
+  float raw = -INFINITY;
+#pragma unroll 1
+  for (int first = 0; first < kCaKeys; first += 16) {
+    load(first);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) raw = fmaxf(raw, __uint_as_float(x[k]));
+  }
+  float cf = 1.0f;
+  if (raw > -INFINITY) {
+    const bool was = w.r > -INFINITY, far = fabsf(raw * c) >= kCaFar;
+    if (was ? raw > w.r : raise && raw * c > w.m) {
+      cf = was ? ex2(far ? (w.r - raw) * c : w.r * c - raw * c) : w.m == -INFINITY ? 0.0f : ex2(w.m - raw * c);
+      w.l *= cf;
+      w.r = far ? raw : -INFINITY;
+      w.m = far ? -INFINITY : raw * c;
+    }
+  }
+  if (more && __any_sync(0xffffffffu, cf < 1.0f)) {
+    if (!ca_wait(before, parity, err)) return {0.0f, 0.0f, 0.0f, false};  // the sums of the tile before
+    tc_fence_after();
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 16) {
+      tmem_ld_32x32b<16>(o_col + (uint32_t)c0, x);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * cf);
+      tmem_st_32x32b_x16(o_col + (uint32_t)c0, x);
+    }
+  }
+  const bool far = w.r > -INFINITY;
+  const float off = far ? w.r : 0.0f, u = (far || w.m == -INFINITY ? 0.0f : w.m) - kCaUp<TYPE>;
+  const uint64_t c2 = f2_pack(c, c), nu2 = f2_pack(-u, -u);
+  float half[2];  // the sums of 32 columns each
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
+#pragma unroll 1
+    for (int first = 32 * h; first < 32 * h + 32; first += 16) {  // (16 columns of weights lie over scores that are used)
+      load(first);
+      uint32_t pr[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]) - off, __uint_as_float(x[2 * k + 1]) - off), c2, nu2), x0, x1);
+        const float e0 = ex2(x0), e1 = ex2(x1);
+        pr[k] = ca_pack<TYPE>(e0, e1);
+        const uint64_t r2 = f2_pack(e0, e1);
+        if (k & 1)
+          lb = f2_add(lb, r2);
+        else
+          la = f2_add(la, r2);
+      }
+      tmem_st_32x32b_x8(col + (uint32_t)first / 2u, pr);
+    }
+    float a0, a1;
+    f2_unpack(f2_add(la, lb), a0, a1);
+    if (h == 0)
+      half[0] = a0 + a1;
+    else
+      half[1] = a0 + a1;
+  }
+  w.l += half[0] + half[1];
+  tmem_wait_st();
+  return w;
+}
+
 // A cut unit's rows from its np pieces, by eight warps: warp w has the rows w, w +
 // 8, .., a lane D / 32 columns; N rows and K pieces at a time, whose loads go out
 // together.
@@ -461,6 +567,25 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
       }
 #pragma unroll
       for (int q = 0; q < N; ++q) {
+        bool far = S[q] < 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) far = far || ml[q][k].y < 0.0f;
+        if (far) {  // (S < 0: M is kept as a score)
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (ml[q][k].y == 0.0f) continue;
+            const CaRef a = {M[q], S[q]}, b = {ml[q][k].x, ml[q][k].y};
+            CaRef top = b;
+            float2 f = make_float2(0.0f, 1.0f);
+            if (S[q] != 0.0f) f = ca_factors(a, b, p.scale_log2, &top);
+            const float sum = f.x * fabsf(a.sum) + f.y * fabsf(b.sum);
+            M[q] = top.ref;
+            S[q] = top.far() ? -sum : sum;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[q][v] = f.x * acc[q][v] + f.y * o[q][k][v];
+          }
+          continue;
+        }
         float top = M[q];
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -483,7 +608,7 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
     for (int q = 0; q < N; ++q) {
       const int r = r0 + 8 * q;
       if (r >= rows) continue;
-      const float inv = 1.0f / S[q];
+      const float inv = 1.0f / fabsf(S[q]);
       const int R = d.row0 + r, j = wk.by_g(R);
       if (!in_bounds(p.err, d.at + j, p.T)) continue;
       uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
@@ -1044,6 +1169,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int gw = d.gw, gc = d.gc;
       const int rel = pos - (d.tile0 + d.lo) * kCaKeys;  // the row's position, from the part's first key on
       float m = -INFINITY, l = 0.0f;
+      float r = -INFINITY;  // the reference where it is kept as a score (m is -infinity then)
       for (int jt = 0; jt < nt; ++jt, ++sc) {
         const int i = two ? jt : 2 * jt + t, buf = (int)(sc & 1u);
         if (!ca_wait(&sh->s_full[t][buf], (sc >> 1) & 1u, p.err)) {
@@ -1111,7 +1237,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             m4[c & 3] = max3f(m4[c & 3], __uint_as_float(sa[2 * c]), __uint_as_float(sa[2 * c + 1]));
             m4[(c + 2) & 3] = max3f(m4[(c + 2) & 3], __uint_as_float(sb[2 * c]), __uint_as_float(sb[2 * c + 1]));
           }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          const float raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx = raw * p.scale_log2;
+          if (__any_sync(0xffffffffu, r > -INFINITY || (fabsf(mx) >= kCaFar && raw > -INFINITY))) {
+            const CaRow w = ca_far_tile<TYPE, D>({m, r, l, true}, col, trow + ca_o_col(t), top, bottom, p.scale_log2, raise,
+                                                 jt > 0, &sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err);
+            if (!w.ok) {
+              ok = false;
+              break;
+            }
+            m = w.m;
+            r = w.r;
+            l = w.l;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
+            continue;
+          }
           float cf = 1.0f;
           if (raise && mx > m) {
             cf = m == -INFINITY ? 0.0f : ex2(m - mx);
@@ -1165,7 +1306,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
         if (t == 1) {  // hand over the reference and the sum through TMEM; the sums of values are there
-          uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
+          const bool far = r > -INFINITY;
+          uint32_t st[8] = {__float_as_uint(far ? r : m), __float_as_uint(far ? -l : l), 0u, 0u, 0u, 0u, 0u, 0u};
           tmem_st_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_st();
           tc_fence_before();
@@ -1181,7 +1323,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           tmem_ld_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_ld(st);
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
-          if (n > 1 && !(l1 == 0.0f)) {
+          if (n > 1 && (r > -INFINITY ? !(l1 == 0.0f) : l1 < 0.0f)) {
+            const bool far = r > -INFINITY;
+            const CaRef a = {far ? r : m, far ? -l : l}, b = {m1, l1};
+            CaRef top = b;
+            float2 f = make_float2(0.0f, 1.0f);
+            if (!(l == 0.0f)) f = ca_factors(a, b, p.scale_log2, &top);
+            a0 = f.x;
+            a1 = f.y;
+            l = l * a0 + fabsf(l1) * a1;
+            r = top.far() ? top.ref : -INFINITY;
+            m = top.far() ? -INFINITY : top.ref;
+          } else if (n > 1 && !(l1 == 0.0f)) {
             const float M = fmaxf(m, m1);
             a0 = l == 0.0f ? 0.0f : ex2(m - M);
             a1 = ex2(m1 - M);
@@ -1250,7 +1403,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             ca_store32(dst + c0 + 16, w + 8, wk.wide != 0);
           }
         }
-        if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
+        if (cut && st_ok) wk.part_ml[pi] = r > -INFINITY ? make_float2(r, -l) : make_float2(m, l);
       }
       if (to_hand) hand_q((seq + 1) % kCaDesc);
       if (!two) {  // slot 1's scores and sums may be written again

@@ -1,0 +1,100 @@
+"""The paged 16-bit attention with scores far from zero: finite scores give what
+the definition gives, however large they are. But for the last test the scores
+are whole numbers that fp32 holds, so that the weights depend on their
+differences alone."""
+import numpy as np
+import pytest
+import torch
+
+import kv16_reference as ref
+import speculative_decode_verify_w4a16_gb300 as sv
+from helpers import dev
+from test_kv16_gpu import BF16, F16, Case, _starts
+
+pytestmark = pytest.mark.gpu
+
+# one row, slots that share the rows and ones that do not, cut units, the queue's
+SHAPES = [([5], [1]), ([1003], [1]), ([900], [40]), ([0], [300]), ([20000], [3]), ([9000], [200]),
+          ([100 + b for b in range(80)], [1 + b % 3 for b in range(80)])]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from speculative_decode_verify_w4a16_gb300 import build
+    build.build()
+
+
+def _run(c, **kw):
+    for b in range(len(c.lens)):
+        c.put(b)
+    out = c.run(**kw)
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 0
+    return out
+
+
+@pytest.mark.parametrize("dtype,D,dims,first,second", [
+    (F16, 128, 4, 32752.0, 61408.0), (F16, 64, 4, 32752.0, 61408.0), (F16, 64, 1, 32752.0, 44704.0),
+    (BF16, 128, 128, 1.9296875 * 2.0 ** 45, 1.8046875 * 2.0 ** 45), (BF16, 64, 1, 1.9296875 * 2.0 ** 20, 1.8046875 * 2.0 ** 20),
+])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("lens,counts", SHAPES)
+def test_the_largest_scores_share_the_row(dtype, D, dims, first, second, sign, lens, counts):
+    """Scores dims * first * second * 2^-a, a = 0 .. 5 by the key: those that are largest of what a row sees weigh the
+    same, the others nothing. fp16: up to 2^33, 2^30 in powers of two; bf16: up to 2^99. The products have 22 bits (fp16)
+    or 16, and so up to 24 for four of them, or 128: fp32 holds every sum."""
+    rng = np.random.default_rng(len(lens) + int(sign))
+    c = Case(1, dtype, D, 8, 4, lens, counts)
+    c.q.zero_()
+    c.q[..., :dims] = sign * first
+    for k, v in c.kv:
+        keys = torch.from_numpy(second * 2.0 ** -rng.integers(0, 6, k.shape[:2]).astype(np.float64)).to(dev())
+        k.zero_()
+        k[..., :dims] = keys[..., None]
+        assert (k[..., 0].double() == keys).all() and c.q[0, 0, 0].double() == sign * first
+    out = _run(c)
+    assert out.isfinite().all()
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype,D", [(F16, 128), (BF16, 64), (BF16, 128)])
+@pytest.mark.parametrize("first,second", [(64, 125), (8, 125), (64, 512), (512, 2048), (-64, 125), (-512, 2048)])
+@pytest.mark.parametrize("lens,counts", SHAPES)
+def test_differences_of_large_scores(dtype, D, first, second, lens, counts):
+    """Scores first * second + j, j = 0 .. 255 by the key: on both sides of where the weights are taken another way (8000
+    is 1020 powers of two at D 128), and beyond it."""
+    rng = np.random.default_rng(len(lens) + abs(first))
+    c = Case(2, dtype, D, 8, 4, lens, counts)
+    c.q.zero_()
+    c.q[..., 0], c.q[..., 1] = first, 1
+    for k, v in c.kv:
+        k.zero_()
+        k[..., 0] = second
+        k[..., 1] = torch.from_numpy(rng.integers(0, 256, k.shape[:2])).to(dev())
+    c.check(_run(c))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens,counts", SHAPES)
+def test_scores_that_leave_and_come_back(dtype, lens, counts):
+    """A few keys far above the others, and rows that see none of them yet.
+
+    A far score is 2^15 and some tens, a sum of D = 128 products in fp32: it is off by at most D 2^-24 times the products'
+    magnitudes, which are below 2^15 + 2^11 (by Cauchy's inequality, norms of less than 45 each for the other 127, which is
+    asserted). So the weights are off by the factor exp(2 e), e that times the scale, in the worst case, and a row by
+    exp(2 e) - 1 times the weighted magnitudes and itself."""
+    rng = np.random.default_rng(3)
+    c = Case(3, dtype, 128, 8, 4, lens, counts)
+    c.q[..., 0] = 64
+    for k, v in c.kv:
+        far = torch.from_numpy(rng.integers(0, 50, k.shape[:2]) == 0).to(dev())
+        k[..., 0] = torch.where(far, 512.0, 0.0).to(dtype)
+        assert k[..., 1:].double().norm(dim=-1).max() < 45
+    assert c.q[..., 1:].double().norm(dim=-1).max() < 45
+    out = _run(c)
+    factor = np.expm1(2 * 128 * 2.0 ** -24 * (2 ** 15 + 2 ** 11) * 128 ** -0.5)
+    at = _starts(counts)
+    for b, (k, v) in enumerate(c.kv):
+        want, mag = ref.attention(c.q[at[b]:at[b + 1]], k, v, lens[b])
+        bound = ref.attention_bound(want, mag, v, dtype) + factor * (mag + want.abs())
+        assert ((out[at[b]:at[b + 1]].double() - want).abs() <= bound).all(), b
