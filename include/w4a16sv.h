@@ -490,8 +490,10 @@ w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positio
  *   T 1 .. 2^24, B <= 4096, pages * Hkv <= 2^25, B * max_blocks < 2^31
  * A request whose rows or positions lie outside (row_start falling or past T, a
  * negative length, a position past the table) sets W4A16_ERR_DEVICE_INPUT in
- * the device error word and is left out: none of its rows is written. A page id
- * outside the cache sets it too: nothing is written there, and it reads as
+ * the device error word and is left out: none of its rows is written. (Where
+ * row_start falls, rows may lie in several requests' ranges: which of those
+ * requests they are taken for is not defined then, nor whether they are.) A page
+ * id outside the cache sets it too: nothing is written there, and it reads as
  * zeros.
  * ---------------------------------------------------------------------- */
 

@@ -242,9 +242,11 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) rope_rows_kernel(cons
   };
   bool taken = true;  // (append: a row of no request is not read)
   if constexpr (APPEND) {
-    if (row == 0 && p.start)  // rows out of order are found wherever they are
-      for (int b = tid; b < p.B; b += kRowThreads)
-        if (p.start[b + 1] < p.start[b]) report_error(p.err, kErrInput);
+    if (row == 0 && p.start)  // rows out of order or outside are found wherever they are: no row of the step may lead to them
+      for (int b = tid; b < p.B; b += kRowThreads) {
+        const int first = p.start[b], last = p.start[b + 1];
+        if (first < 0 || last < first || last > p.T) report_error(p.err, kErrInput);
+      }
     taken = !p.start || row < p.start[p.B];
   }
   if (taken) load(tid);
