@@ -462,7 +462,8 @@ w4a16_status kv8_tree_attention(const void* q, const void* k_new, const void* v_
  *   positions  device int32 [T], any value
  *   turns      device uint64 [rot / 2]: f_i / 2 pi in units of 2^-64 (angles are
  *              exact to 2^-32 turns and positions * 2^-65)
- *   D a multiple of 8, <= 1024; rot a multiple of 16, <= D; T 1 .. 2^31 - 1
+ *   T 1 .. 2^31 - 1, rot 2 .. D (else W4A16_ERR_INVALID_ARG); D a multiple of 8,
+ *   <= 1024, rot of 16, heads <= 2^20 (else W4A16_ERR_UNSUPPORTED)
  * Arithmetic: sines, cosines and the rotation in fp32, rounded once to the
  * type. Launch rules as for w4a16_linear.
  * ---------------------------------------------------------------------- */
@@ -487,7 +488,9 @@ w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positio
  *   lens         device int32 [B]: tokens of request b before the step
  *   row_start    device int32 [B + 1], not falling, row_start[B] <= T; NULL:
  *                T / B rows each. Rows of no request are neither read nor written
- *   T 1 .. 2^24, B <= 4096, pages * Hkv <= 2^25, B * max_blocks < 2^31
+ *   Hkv 1 .. 65535, pages * Hkv <= 2^25, max_blocks < 2^25, B * max_blocks < 2^31
+ *   (else W4A16_ERR_INVALID_ARG); T 1 .. 2^24, B <= 4096 (more:
+ *   W4A16_ERR_UNSUPPORTED, as any other D)
  * A request whose rows or positions lie outside (row_start falling or past T, a
  * negative length, a position past the table) sets W4A16_ERR_DEVICE_INPUT in
  * the device error word and is left out: none of its rows is written. (Where
@@ -502,7 +505,8 @@ w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positio
  * on the way (rope_rotate's rotation; turns NULL with rot 0: none), and the
  * rotated queries of the same rows (q, q_out NULL: none).
  *   k_new, v_new  device [T][Hkv][D]; q, q_out device [T][H][D]; rows their
- *                 strides apart, as in rope_rotate; q_out may be q
+ *                 strides apart, as in rope_rotate; q_out may be q; H <= 2^20
+ *                 (else W4A16_ERR_UNSUPPORTED)
  * Launch rules as for w4a16_linear.
  * ---------------------------------------------------------------------- */
 w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride, const void* q,

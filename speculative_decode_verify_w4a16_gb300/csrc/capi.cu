@@ -559,11 +559,14 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
 }
 
 static bool kv16_attn_shape_ok(int T, int H, int Hkv) {
-  return T >= 1 && H >= 1 && Hkv >= 1 && Hkv <= 65535 && H % Hkv == 0 && (int64_t)T * H <= INT32_MAX;
+  return T >= 1 && H >= 1 && Hkv >= 1 && Hkv <= 65535 && H % Hkv == 0;
+}
+static bool kv16_attn_size_ok(int T, int H, int D) {
+  return (D == 64 || D == 128) && T <= (1 << 24) && (int64_t)T * H <= INT32_MAX;
 }
 
 size_t kv16_attention_workspace_bytes(int T, int H, int Hkv, int D) {
-  if (!kv16_attn_shape_ok(T, H, Hkv) || (D != 64 && D != 128) || T > (1 << 24)) return 0;
+  if (!kv16_attn_shape_ok(T, H, Hkv) || !kv16_attn_size_ok(T, H, D)) return 0;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return 0;
   return kv16_attention_ws(T, H, Hkv, D, dev.num_sms);
@@ -580,7 +583,7 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4))
     return W4A16_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || B > kPlanMaxB || T > (1 << 24) || !kv16_attention_fits(T, B, H, Hkv, max_blocks))
+  if (!kv16_attn_size_ok(T, H, D) || B > kPlanMaxB || !kv16_attention_fits(T, B, H, Hkv, max_blocks))
     return W4A16_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
