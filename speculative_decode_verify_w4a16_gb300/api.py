@@ -13,7 +13,7 @@ from typing import List, Optional, Tuple
 
 import torch
 
-from ._lib import W4A16Error, check, lib
+from ._lib import ERR_DEVICE_TIMEOUT, W4A16Error, check, lib
 
 GROUP = 128
 
@@ -359,9 +359,12 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
 def check_device_status(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error status."""
     status = int(lib().w4a16_check_device_status(_stream(stream)))
-    if status:  # a wait that ran out may have left a count in a default workspace of kv16_attention: new ones from here on
+    if status == ERR_DEVICE_TIMEOUT:
+        # a wait that ran out may have left a count in one of the device's default workspaces of kv16_attention: new ones
+        # from here on (whatever else is reported, the counts are zero)
+        dev = _device()
         for k in list(_stream_ws):
-            if k[2] == "kv16_attention":
+            if k[0] == dev and k[2] == "kv16_attention":
                 _stream_ws.pop(k, None)
     return status
 
