@@ -652,6 +652,7 @@ def kv8_tree_attention(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
 
 _TURN = 2 * Fraction(31415926535897932384626433832795028841972, 10 ** 40)  # radians of a turn
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_INT_MAX = 2 ** 31 - 1  # (ctypes passes a larger int on without its upper bits)
 
 
 @dataclass
@@ -750,7 +751,8 @@ def _rows(t: torch.Tensor, name: str, dev: int):
     if len(shape) == 3:
         rows, heads, D = shape
         stride, sh, sd = strides
-        if sd == 1 and sh == D and rows > 1 and stride % 8 == 0 and stride >= heads * D and t.get_device() == dev:
+        if (sd == 1 and sh == D and rows > 1 and stride % 8 == 0 and stride >= heads * D and rows | heads | D <= _INT_MAX
+                and t.get_device() == dev):
             return rows, heads, D, stride
     elif len(shape) == 4:
         B, n, heads, D = shape
@@ -764,6 +766,8 @@ def _rows(t: torch.Tensor, name: str, dev: int):
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if len(shape) not in (3, 4):
         raise ValueError(f"{name} must have 3 or 4 dimensions, got {tuple(shape)}")
+    if rows | heads | D > _INT_MAX:
+        raise ValueError(f"{name}: {rows} rows of ({heads}, {D}) are too many")
     if len(shape) == 4 and n > 1 and B > 1 and outer != n * stride:
         raise ValueError(f"{name}: its rows must be evenly apart")
     if rows <= 1:
@@ -866,6 +870,8 @@ def _need_step(block_table: torch.Tensor, lens: torch.Tensor, row_start: Optiona
     B = lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, max_blocks), got {tuple(block_table.shape)}")
+    if B | block_table.shape[1] > _INT_MAX:
+        raise ValueError(f"block_table of shape {tuple(block_table.shape)} is too large")
     if not (_is(lens, i32, dev, (B,)) and _is(block_table, i32, dev, block_table.shape)):
         _need(lens, "lens", i32, (B,))
         _need(block_table, "block_table", i32)
@@ -933,6 +939,8 @@ def kv16_append(cache: KV16Cache, layer: int, k_new: torch.Tensor, v_new: torch.
 
 
 def kv16_attention_workspace_bytes(T: int, H: int, Hkv: int, D: int) -> int:
+    if max(T, H, Hkv, D) > _INT_MAX:
+        return 0
     return int(lib().kv16_attention_workspace_bytes(T, H, Hkv, D))
 
 
@@ -961,6 +969,8 @@ def kv16_attention(q: torch.Tensor, cache: KV16Cache, layer: int, block_table: t
         raise ValueError(f"q must be {cache.k.dtype} with heads of {D}, got {q.dtype} {tuple(q.shape)}")
     B, max_blocks = _need_step(block_table, lens, row_start, T, dev)
     scale = D ** -0.5 if scale is None else float(scale)
+    if not -1 <= window <= _INT_MAX:  # (past every position it is none)
+        window = _INT_MAX if window > 0 else -1
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     elif not _is(out, q.dtype, dev, q.shape):
