@@ -523,6 +523,31 @@ __device__ __noinline__ CaRow ca_far_tile(CaRow w, uint32_t col, uint32_t o_col,
   return w;
 }
 
+// Row r of a cut unit from its pieces where some reference is kept as a score, by a warp: D / 32 columns a lane, to `to`.
+template <int TYPE, int D>
+__device__ __noinline__ void ca_merge_far(const Kv16AttnParams& p, const CaWork& wk, const int* list, int np, int r, uint32_t* to,
+                                          int lane) {
+  constexpr int V = D / 32;
+  float acc[V] = {};
+  CaRef a = {0.0f, 0.0f};
+  for (int k = 0; k < np; ++k) {
+    const int64_t row = (int64_t)list[k] + r;
+    const float2 ml = __ldcg(&wk.part_ml[row]);
+    const CaRef b = {ml.x, ml.y};
+    if (b.sum == 0.0f) continue;
+    CaRef top = b;
+    float2 f = make_float2(0.0f, 1.0f);
+    if (a.sum != 0.0f) f = ca_factors(a, b, p.scale_log2, &top);
+    const float sum = f.x * fabsf(a.sum) + f.y * fabsf(b.sum);
+    a = {top.ref, top.far() ? -sum : sum};
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = f.x * acc[v] + f.y * __ldcg(wk.part_o + row * D + V * lane + v);
+  }
+  const float inv = 1.0f / fabsf(a.sum);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) to[v / 2] = ca_pack<TYPE>(acc[v] * inv, acc[v + 1] * inv);
+}
+
 // A cut unit's rows from its np pieces, by eight warps: warp w has the rows w, w +
 // 8, .., a lane D / 32 columns; N rows and K pieces at a time, whose loads go out
 // together.
@@ -533,8 +558,10 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
   const int G = (int)wk.by_g.d, rows = d.rows;
   for (int r0 = w; r0 < rows; r0 += 8 * N) {
     float acc[N][V], M[N], S[N];
+    bool far[N];  // some reference is kept as a score: what is summed here does not count
 #pragma unroll
     for (int q = 0; q < N; ++q) {
+      far[q] = false;
       M[q] = -INFINITY;
       S[q] = 0.0f;
 #pragma unroll
@@ -567,29 +594,12 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
       }
 #pragma unroll
       for (int q = 0; q < N; ++q) {
-        bool far = S[q] < 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) far = far || ml[q][k].y < 0.0f;
-        if (far) {  // (S < 0: M is kept as a score)
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            if (ml[q][k].y == 0.0f) continue;
-            const CaRef a = {M[q], S[q]}, b = {ml[q][k].x, ml[q][k].y};
-            CaRef top = b;
-            float2 f = make_float2(0.0f, 1.0f);
-            if (S[q] != 0.0f) f = ca_factors(a, b, p.scale_log2, &top);
-            const float sum = f.x * fabsf(a.sum) + f.y * fabsf(b.sum);
-            M[q] = top.ref;
-            S[q] = top.far() ? -sum : sum;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[q][v] = f.x * acc[q][v] + f.y * o[q][k][v];
-          }
-          continue;
-        }
         float top = M[q];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+          far[q] = far[q] || ml[q][k].y < 0.0f;
           if (ml[q][k].y != 0.0f) top = fmaxf(top, ml[q][k].x);  // (a sum of zero: the piece's keys are not seen)
+        }
         const float f0 = S[q] == 0.0f ? 0.0f : ex2(M[q] - top);
         S[q] *= f0;
 #pragma unroll
@@ -608,12 +618,14 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
     for (int q = 0; q < N; ++q) {
       const int r = r0 + 8 * q;
       if (r >= rows) continue;
-      const float inv = 1.0f / fabsf(S[q]);
+      const float inv = 1.0f / S[q];
       const int R = d.row0 + r, j = wk.by_g(R);
       if (!in_bounds(p.err, d.at + j, p.T)) continue;
       uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                  ((int64_t)(d.at + j) * p.H + d.kvh * G + R - j * G) * D + V * lane);
-      if constexpr (V == 4)
+      if (far[q])
+        ca_merge_far<TYPE, D>(p, wk, list, np, r, to, lane);
+      else if constexpr (V == 4)
         *reinterpret_cast<uint2*>(to) =
             make_uint2(ca_pack<TYPE>(acc[q][0] * inv, acc[q][1] * inv), ca_pack<TYPE>(acc[q][2] * inv, acc[q][3] * inv));
       else
