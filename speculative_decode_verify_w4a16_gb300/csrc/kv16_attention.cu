@@ -149,6 +149,7 @@ struct CaShared {
   CaSpecial special[kCaDesc][kCaSpecial];
   uint32_t tmem;
   int last;
+  unsigned beat;  // counts on as the producer does
 };
 
 template <int D>
@@ -233,13 +234,28 @@ __device__ __forceinline__ void ca_mma4_ts(uint32_t d, uint32_t a, uint64_t b, u
       : "memory");
 }
 
-// Bounded wait by a whole warp; false once it has run out. (A test without a time answers in 45 cycles, and several
-// at once in little more; one with a time takes 80, each for itself.)
-__device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err) {
-  return mbar_wait(bar, parity, err);
+// Bounded wait by a whole warp; false once it has run out: when kWaitLimitNs have passed in which the CTA's producer got no
+// further. (It is not the wait itself that is bounded: the guard has nothing to do while a part's unmasked tiles pass by, which
+// may be two million of them.) A test without a time answers in 45 cycles, and several at once in little more; one with a
+// time takes 80, each for itself.
+__device__ __noinline__ bool ca_wait_long(uint64_t* bar, uint32_t parity, unsigned* err, const unsigned* beat) {
+  unsigned long long t0 = globaltimer_ns();
+  unsigned last = *(volatile const unsigned*)beat;
+  while (!mbar_try_wait(bar, parity, 1000000u)) {
+    const unsigned long long t = globaltimer_ns();
+    const unsigned now = *(volatile const unsigned*)beat;
+    if (now != last) {
+      last = now;
+      t0 = t;
+    } else if (t - t0 > kWaitLimitNs) {
+      report_error(err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
 }
-__device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, unsigned* err) {
-  return mbar_try_wait(bar, parity) || ca_wait_long(bar, parity, err);
+__device__ __forceinline__ bool ca_wait(uint64_t* bar, uint32_t parity, unsigned* err, const unsigned* beat) {
+  return mbar_try_wait(bar, parity) || ca_wait_long(bar, parity, err, beat);
 }
 
 #if W4A16_TEST_HOOKS
@@ -448,7 +464,8 @@ struct CaRow {
 };
 template <int TYPE, int D>
 __device__ __noinline__ CaRow ca_far_tile(CaRow w, uint32_t col, uint32_t o_col, int top, int bottom, float c, bool raise,
-                                          bool more, uint64_t* before, uint32_t parity, unsigned* err) {
+                                          bool more, uint64_t* before, uint32_t parity, unsigned* err,
+                                          const unsigned* beat) {
   uint32_t x[16];
   auto load = [&](int first) {
     tmem_ld_32x32b<16>(col + (uint32_t)first, x);
@@ -475,7 +492,7 @@ __device__ __noinline__ CaRow ca_far_tile(CaRow w, uint32_t col, uint32_t o_col,
     }
   }
   if (more && __any_sync(0xffffffffu, cf < 1.0f)) {
-    if (!ca_wait(before, parity, err)) return {0.0f, 0.0f, 0.0f, false};  // the sums of the tile before
+    if (!ca_wait(before, parity, err, beat)) return {0.0f, 0.0f, 0.0f, false};  // the sums of the tile before
     tc_fence_after();
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 16) {
@@ -650,6 +667,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const int G = (int)wk.by_g.d, cta = (int)blockIdx.x;
 
   if (tid == 0) {
+    sh->beat = 0u;
     for (int i = 0; i < NB; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->free[i], 2);
@@ -864,7 +882,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int lo = !queue && first ? begin.cut : 0, hi = at_end ? end.cut : t.nt;
       if (hi > lo) {
         const int ds = seq % kCaDesc;
-        if (seq >= kCaDesc && !ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err)) {
+        if (seq >= kCaDesc && !ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err, &sh->beat)) {
           ok = false;
           break;
         }
@@ -924,10 +942,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             if (t.tile0 + k - base >= 32) {
               base += 32;
               now = entries();
+              if (lane == 0) *(volatile unsigned*)&sh->beat = sh->beat + 1u;
             }
             const int page = __shfl_sync(0xffffffffu, now, t.tile0 + k - base);
             z = page >= 0 ? page * p.Hkv + kvh : p.pages * p.Hkv;  // past the last page: zeros
-            ok = keys < kPairs || ca_wait(&sh->free[2u * pk.r], pk.ph ^ 1u, p.err);
+            ok = keys < kPairs || ca_wait(&sh->free[2u * pk.r], pk.ph ^ 1u, p.err, &sh->beat);
             if (ok && !test_skip_copy(2u * keys))
               ca_copy_tile(smem + L::kRingOff + 2u * pk.r * L::kTile, &maps.k, z, &sh->full[2u * pk.r], (uint32_t)L::kTile);
             if (ok) ++keys, pk.step(1u);
@@ -935,7 +954,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const int v = k - 2;
           if (ok && v >= lo) {
             const uint32_t x = 2u * pv.r + 1u;
-            ok = values < kPairs || ca_wait(&sh->free[x], pv.ph ^ 1u, p.err);
+            ok = values < kPairs || ca_wait(&sh->free[x], pv.ph ^ 1u, p.err, &sh->beat);
             // guarded values land at a barrier of their own: the guard tells when they may be used
             const bool guard = v - lo < gw || v - lo >= gc;
             if (ok && !test_skip_copy(2u * values + 1u)) {
@@ -969,7 +988,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
     // no more parts
     const int ds = seq % kCaDesc;
-    if (ok && seq >= kCaDesc) ok = ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err);
+    if (ok && seq >= kCaDesc) ok = ca_wait(&sh->desc_free[ds], (uint32_t)(seq / kCaDesc - 1) & 1u, p.err, &sh->beat);
     if (ok && lane == 0) {
       sh->part[ds].lo = 0;
       sh->part[ds].hi = 0;
@@ -977,11 +996,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
     // the copies in flight land before the CTA exits (some may be, if a wait of another warp ran out)
     for (uint32_t k = keys > kPairs ? keys - kPairs : 0; k < keys; ++k)
-      if (!test_skip_copy(2u * k)) ca_wait(&sh->full[2u * (k % kPairs)], (k / kPairs) & 1u, p.err);
+      if (!test_skip_copy(2u * k)) ca_wait(&sh->full[2u * (k % kPairs)], (k / kPairs) & 1u, p.err, &sh->beat);
     for (uint32_t k = values > kPairs ? values - kPairs : 0; k < values; ++k)
-      if (!test_skip_copy(2u * k + 1u)) ca_wait(&sh->full[2u * (k % kPairs) + 1u], (k / kPairs) & 1u, p.err);
+      if (!test_skip_copy(2u * k + 1u)) ca_wait(&sh->full[2u * (k % kPairs) + 1u], (k / kPairs) & 1u, p.err, &sh->beat);
     for (uint32_t k = guarded > kCaOk ? guarded - kCaOk : 0; k < guarded; ++k)
-      ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err);
+      ca_wait(&sh->landed[k % kCaOk], (k / kCaOk) & 1u, p.err, &sh->beat);
   } else if (warp <= 2) {
     // ------------------------------------------------------ MMA, slot t
     // The scores are a tile ahead of the weights, so that neither side waits for the other's latency.
@@ -996,7 +1015,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     bool ok = true, issued = false;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
-      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err, &sh->beat)) break;
       const CaPart& d = sh->part[ds];
       const int n = d.hi - d.lo, gw = d.gw, gc = d.gc;
       if (n <= 0) break;
@@ -1012,7 +1031,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       auto pass = [&](int to) {
         for (; at < to; ++at, pi.step(1u))
           for (uint32_t x = 2u * pi.r, e = x + 2u; x < e; ++x) {
-            if (!ca_wait(&sh->full[x], pi.ph, p.err)) return false;
+            if (!ca_wait(&sh->full[x], pi.ph, p.err, &sh->beat)) return false;
             if (lane == 0) mbar_arrive(&sh->free[x]);
             __syncwarp();
           }
@@ -1023,7 +1042,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           if (!pass(i)) return false;
           there = false;
         }
-        if (!there && !ca_wait(&sh->full[2u * pi.r], pi.ph, p.err)) return false;
+        if (!there && !ca_wait(&sh->full[2u * pi.r], pi.ph, p.err, &sh->beat)) return false;
         tc_fence_after();
         const uint32_t sb = sc & 1u;
         const uint64_t k0 = ring_k + (uint64_t)(pi.r * (2u * L::kTile / 16));  // (the descriptors count in 16 bytes)
@@ -1039,8 +1058,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         return true;
       };
       // (slot 1's warps are done with the part before, and where the slots share the rows slot 0's have loaded them)
-      if (i < upto && t == 1 && !two) ok = ca_wait(&sh->q_ready[0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err);
-      if (ok && i < upto) ok = ca_wait(&sh->q_ready[t][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err) && scores(false);
+      if (i < upto && t == 1 && !two) ok = ca_wait(&sh->q_ready[0][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err, &sh->beat);
+      if (ok && i < upto) ok = ca_wait(&sh->q_ready[t][ds], (uint32_t)(seq / kCaDesc) & 1u, p.err, &sh->beat) && scores(false);
       if (ok && i < upto) ok = scores(false);
       // the scores two tiles on go out behind the product of the weights that lie in their buffer
       pv = part0;
@@ -1050,12 +1069,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         uint64_t *values = &sh->full[2u * pv.r + 1u], *weights = &sh->p_full[t][sb];
         const bool v_there = mbar_test(values, pv.ph), p_there = mbar_test(weights, (pc >> 1) & 1u);
         const bool k_there = mbar_test(&sh->full[2u * pi.r], pi.ph);  // (the tile `at`, whose last phase is waited for)
-        if (!v_there) ok = ca_wait(values, pv.ph, p.err);
+        if (!v_there) ok = ca_wait(values, pv.ph, p.err, &sh->beat);
         if (ok && (v < gw || v >= gc)) {  // the guard has looked through the values
           const uint32_t g = oks + (uint32_t)(v < gw ? v : gw + v - gc);
-          ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err);
+          ok = ca_wait(&sh->ok[g % kCaOk], (g / kCaOk) & 1u, p.err, &sh->beat);
         }
-        if (ok && !p_there) ok = ca_wait(weights, (pc >> 1) & 1u, p.err);
+        if (ok && !p_there) ok = ca_wait(weights, (pc >> 1) & 1u, p.err, &sh->beat);
         if (!ok) break;
         tc_fence_after();
         // O += P V
@@ -1072,7 +1091,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
     if (issued) {
       umma_commit_warp(&sh->fin[t]);  // tracks all of this warp's MMAs
-      ca_wait(&sh->fin[t], 0u, p.err);
+      ca_wait(&sh->fin[t], 0u, p.err, &sh->beat);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ guard
@@ -1080,7 +1099,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     bool ok = true;
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
-      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err, &sh->beat)) break;
       const CaPart& d = sh->part[ds];
       const int lo = d.lo, n = d.hi - lo, gw = d.gw, gc = d.gc, tile0 = d.tile0, last_key = d.last_key;
       if (n <= 0) break;
@@ -1088,7 +1107,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       __syncwarp();
       for (int i = gw > 0 ? 0 : gc; ok && i < n; i = i + 1 < gw || i + 1 >= gc ? i + 1 : gc) {
         const uint32_t x = buf + 2u * (uint32_t)i + 1u;
-        if (!ca_wait(&sh->landed[oks % kCaOk], (oks / kCaOk) & 1u, p.err)) {
+        if (!ca_wait(&sh->landed[oks % kCaOk], (oks / kCaOk) & 1u, p.err, &sh->beat)) {
           ok = false;
           break;
         }
@@ -1161,7 +1180,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     };
     for (int seq = 0; ok; ++seq) {
       const int ds = seq % kCaDesc;
-      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err)) break;
+      if (!ca_wait(&sh->desc_full[ds], (uint32_t)(seq / kCaDesc) & 1u, p.err, &sh->beat)) break;
       const CaPart& d = sh->part[ds];
       const int n = d.hi - d.lo;
       if (n <= 0) break;
@@ -1184,7 +1203,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       float r = -INFINITY;  // the reference where it is kept as a score (m is -infinity then)
       for (int jt = 0; jt < nt; ++jt, ++sc) {
         const int i = two ? jt : 2 * jt + t, buf = (int)(sc & 1u);
-        if (!ca_wait(&sh->s_full[t][buf], (sc >> 1) & 1u, p.err)) {
+        if (!ca_wait(&sh->s_full[t][buf], (sc >> 1) & 1u, p.err, &sh->beat)) {
           ok = false;
           break;
         }
@@ -1252,7 +1271,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           const float raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx = raw * p.scale_log2;
           if (__any_sync(0xffffffffu, r > -INFINITY || (fabsf(mx) >= kCaFar && raw > -INFINITY))) {
             const CaRow w = ca_far_tile<TYPE, D>({m, r, l, true}, col, trow + ca_o_col(t), top, bottom, p.scale_log2, raise,
-                                                 jt > 0, &sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err);
+                                                 jt > 0, &sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err, &sh->beat);
             if (!w.ok) {
               ok = false;
               break;
@@ -1272,7 +1291,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             l *= cf;
           }
           if (jt > 0 && __any_sync(0xffffffffu, cf < 1.0f)) {
-            if (!ca_wait(&sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err)) {  // the sums of the tile before
+            if (!ca_wait(&sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err, &sh->beat)) {  // the sums of the tile before
               ok = false;
               break;
             }
@@ -1308,7 +1327,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
       }
       // ---- the part's end
-      if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err);
+      if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err, &sh->beat);
       if (!ok) {
         if (have_q) ca_copy_wait();
         break;
@@ -1326,7 +1345,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->stat);
         } else {
-          if (!ca_wait(&sh->stat, shared_parts & 1u, p.err)) {
+          if (!ca_wait(&sh->stat, shared_parts & 1u, p.err, &sh->beat)) {
             ok = false;
             break;
           }
@@ -1423,7 +1442,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->read);
-        } else if (!ca_wait(&sh->read, shared_parts & 1u, p.err)) {
+        } else if (!ca_wait(&sh->read, shared_parts & 1u, p.err, &sh->beat)) {
           ok = false;
           break;
         }
@@ -1435,7 +1454,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->stored);
         if (warp == 4) {
-          if (!ca_wait(&sh->stored, cut_parts & 1u, p.err)) {
+          if (!ca_wait(&sh->stored, cut_parts & 1u, p.err, &sh->beat)) {
             ok = false;
             break;
           }
@@ -1448,7 +1467,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           }
           __syncwarp();
         }
-        if (!ca_wait(&sh->told, cut_parts & 1u, p.err)) {
+        if (!ca_wait(&sh->told, cut_parts & 1u, p.err, &sh->beat)) {
           ok = false;
           break;
         }
