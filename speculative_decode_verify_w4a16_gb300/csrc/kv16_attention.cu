@@ -104,10 +104,10 @@ constexpr float kCaMost = TYPE == 0 ? 256.0f : 32768.0f;
 template <int TYPE>
 constexpr float kCaUp = TYPE == 0 ? 0.0f : 8.0f;
 // A weight is 2^(s c - m), c the scale and m the reference times c, rounded, in one multiplication and addition: off by
-// the rounding of m, up to 2^-24 |m| powers of two, by the same for all of a row's keys. From this size of m on (the rounding
-// passes what the type holds from 2^28 on in fp16, 2^32 in bf16) the reference is kept as a score r, before the scale, and a
-// weight is 2^((s - r) c), the difference first (ca_far_tile, which such rows come to at every tile).
-constexpr float kCaFar = 1024.0f;
+// the rounding of m, 2^-24 |m| powers of two at most, by the same for all of a row's keys, so that it cancels. From 2^28 on in
+// fp16, 2^32 in bf16, it passes what a weight holds. Rows that had a reference of this size are done over, key by key
+// (ca_far_row): scores like that need not be fast, and the code for them in the tiles' loop cost the others 2 percent.
+constexpr float kCaFar = 16777216.0f;
 
 struct CaMaps {
   CUtensorMap k, v;  // [pages * Hkv][D / 64][64][64]: halves of 64 columns apart, as they lie in shared memory
@@ -119,7 +119,7 @@ struct CaWork {
   uint64_t ctas_inv;   // floor(2^64 / ctas)
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
   int* queue;          // units taken, CTAs finished
-  float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain; or a score as CaRef
+  float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain; a sum below zero: the row is to be done over
   float* part_o;       // [2 * ctas][rows_cap][D] unnormalised sums
 };
 
@@ -438,131 +438,77 @@ __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaSha
   }
 }
 
-// A reference and the sum against it, as they are handed over: (m, l), or (r, -l) where the reference is kept as a score.
-struct CaRef {
-  float ref, sum;
-  __device__ __forceinline__ bool far() const { return sum < 0.0f; }
-};
-// The larger reference of a and b, and what sums against each are worth against it, where one of them is kept as a score.
-// (One kept, one not: they lie far apart, or both where the rounding of r c is 2^-14.)
-__device__ __noinline__ float2 ca_factors(CaRef a, CaRef b, float c, CaRef* top) {
-  const float x = a.far() ? a.ref * c : a.ref, y = b.far() ? b.ref * c : b.ref;
-  if (a.far() && b.far()) {
-    *top = a.ref >= b.ref ? a : b;
-    return make_float2(ex2((a.ref - top->ref) * c), ex2((b.ref - top->ref) * c));
-  }
-  *top = x >= y ? a : b;
-  return make_float2(x >= y ? 1.0f : ex2(x - y), x >= y ? ex2(y - x) : 1.0f);
+// Row R of part d's request and head from the definition, by a warp, D / 32 columns a lane: differences of scores are taken
+// before the scale, against the largest so far.
+template <int TYPE>
+__device__ __forceinline__ float ca_value(uint32_t w, int half) {
+  if constexpr (TYPE == 0) return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return half ? v.y : v.x;
 }
-
-// A tile of a warp's rows, of which one at least keeps its reference as a score or will: its weights over its scores, the
-// largest score the reference where it is to be raised, the sums so far (not with the first tile, `more`) rescaled. The
-// warp's other rows get what they get without it, to the bit.
-struct CaRow {
-  float m, r, l;
-  bool ok;
-};
 template <int TYPE, int D>
-__device__ __noinline__ CaRow ca_far_tile(CaRow w, uint32_t col, uint32_t o_col, int top, int bottom, float c, bool raise,
-                                          bool more, uint64_t* before, uint32_t parity, unsigned* err,
-                                          const unsigned* beat) {
-  uint32_t x[16];
-  auto load = [&](int first) {
-    tmem_ld_32x32b<16>(col + (uint32_t)first, x);
-    tmem_wait_ld(x);
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (first + k > top || first + k <= bottom) x[k] = __float_as_uint(-INFINITY);
+__device__ __noinline__ void ca_far_row(const Kv16AttnParams& p, const CaPart& d, int G, int R, int lane, unsigned* beat) {
+  constexpr int W = D / 64;  // words a lane
+  const int j = R / G, pos = d.past + j, head = d.kvh * G + R - j * G;
+  if (!in_bounds(p.err, d.at + j, p.T)) return;
+  auto words = [&](const void* base, int64_t row, uint32_t* w) {
+    const uint32_t* at = static_cast<const uint32_t*>(base) + row / 2 + W * lane;
+    if constexpr (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(at);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+      w[0] = *at;
+    }
   };
-  float raw = -INFINITY;
+  uint32_t q[W];
+  words(p.q, (int64_t)(d.at + j) * p.q_stride + (int64_t)head * D, q);
+  float acc[2 * W] = {}, m = -INFINITY, l = 0.0f;
+  constexpr int N = 8;  // keys at a time, of one page
+  const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
 #pragma unroll 1
-  for (int first = 0; first < kCaKeys; first += 16) {
-    load(first);
+  for (int key0 = first / N * N; key0 <= pos; key0 += N) {
+    const int page = p.table[(int64_t)d.b * p.max_blocks + key0 / 64];
+    const int64_t row = (((int64_t)page * p.Hkv + d.kvh) * 64 + key0 % 64) * D;
+    uint32_t k[N][W] = {}, v[N][W] = {};
+    if (page >= 0 && page < p.pages) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) raw = fmaxf(raw, __uint_as_float(x[k]));
-  }
-  float cf = 1.0f;
-  if (raw > -INFINITY) {
-    const bool was = w.r > -INFINITY, far = fabsf(raw * c) >= kCaFar;
-    if (was ? raw > w.r : raise && raw * c > w.m) {
-      cf = was ? ex2(far ? (w.r - raw) * c : w.r * c - raw * c) : w.m == -INFINITY ? 0.0f : ex2(w.m - raw * c);
-      w.l *= cf;
-      w.r = far ? raw : -INFINITY;
-      w.m = far ? -INFINITY : raw * c;
-    }
-  }
-  if (more && __any_sync(0xffffffffu, cf < 1.0f)) {
-    if (!ca_wait(before, parity, err, beat)) return {0.0f, 0.0f, 0.0f, false};  // the sums of the tile before
-    tc_fence_after();
-#pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 16) {
-      tmem_ld_32x32b<16>(o_col + (uint32_t)c0, x);
-      tmem_wait_ld(x);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * cf);
-      tmem_st_32x32b_x16(o_col + (uint32_t)c0, x);
-    }
-  }
-  const bool far = w.r > -INFINITY;
-  const float off = far ? w.r : 0.0f, u = (far || w.m == -INFINITY ? 0.0f : w.m) - kCaUp<TYPE>;
-  const uint64_t c2 = f2_pack(c, c), nu2 = f2_pack(-u, -u);
-  float half[2];  // the sums of 32 columns each
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    uint64_t la = f2_pack(0.0f, 0.0f), lb = la;
-#pragma unroll 1
-    for (int first = 32 * h; first < 32 * h + 32; first += 16) {  // (16 columns of weights lie over scores that are used)
-      load(first);
-      uint32_t pr[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float x0, x1;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * k]) - off, __uint_as_float(x[2 * k + 1]) - off), c2, nu2), x0, x1);
-        const float e0 = ex2(x0), e1 = ex2(x1);
-        pr[k] = ca_pack<TYPE>(e0, e1);
-        const uint64_t r2 = f2_pack(e0, e1);
-        if (k & 1)
-          lb = f2_add(lb, r2);
-        else
-          la = f2_add(la, r2);
+      for (int n = 0; n < N; ++n) {
+        words(p.k, row + n * D, k[n]);
+        words(p.v, row + n * D, v[n]);
       }
-      tmem_st_32x32b_x8(col + (uint32_t)first / 2u, pr);
     }
-    float a0, a1;
-    f2_unpack(f2_add(la, lb), a0, a1);
-    if (h == 0)
-      half[0] = a0 + a1;
-    else
-      half[1] = a0 + a1;
-  }
-  w.l += half[0] + half[1];
-  tmem_wait_st();
-  return w;
-}
-
-// Row r of a cut unit from its pieces where some reference is kept as a score, by a warp: D / 32 columns a lane, to `to`.
-template <int TYPE, int D>
-__device__ __noinline__ void ca_merge_far(const Kv16AttnParams& p, const CaWork& wk, const int* list, int np, int r, uint32_t* to,
-                                          int lane) {
-  constexpr int V = D / 32;
-  float acc[V] = {};
-  CaRef a = {0.0f, 0.0f};
-  for (int k = 0; k < np; ++k) {
-    const int64_t row = (int64_t)list[k] + r;
-    const float2 ml = __ldcg(&wk.part_ml[row]);
-    const CaRef b = {ml.x, ml.y};
-    if (b.sum == 0.0f) continue;
-    CaRef top = b;
-    float2 f = make_float2(0.0f, 1.0f);
-    if (a.sum != 0.0f) f = ca_factors(a, b, p.scale_log2, &top);
-    const float sum = f.x * fabsf(a.sum) + f.y * fabsf(b.sum);
-    a = {top.ref, top.far() ? -sum : sum};
+    float s[N];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = f.x * acc[v] + f.y * __ldcg(wk.part_o + row * D + V * lane + v);
-  }
-  const float inv = 1.0f / fabsf(a.sum);
+    for (int n = 0; n < N; ++n) {
+      s[n] = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; v += 2) to[v / 2] = ca_pack<TYPE>(acc[v] * inv, acc[v + 1] * inv);
+      for (int i = 0; i < 2 * W; ++i) s[n] = fmaf(ca_value<TYPE>(q[i / 2], i & 1), ca_value<TYPE>(k[n][i / 2], i & 1), s[n]);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], x);
+    }
+    const float before = m;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (key0 + n >= first && key0 + n <= pos) m = fmaxf(m, s[n]);
+    const float f = before == -INFINITY ? 0.0f : ex2((before - m) * p.scale_log2);
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) acc[i] *= f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (key0 + n < first || key0 + n > pos) continue;
+      const float w = s[n] == -INFINITY ? 0.0f : ex2((s[n] - m) * p.scale_log2);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < 2 * W; ++i) acc[i] = fmaf(w, ca_value<TYPE>(v[n][i / 2], i & 1), acc[i]);
+    }
+    if (lane == 0 && key0 % 512 == 0) atomicAdd(beat, 1u);
+  }
+  const float inv = 1.0f / l;
+  uint32_t* to = static_cast<uint32_t*>(p.out) + ((int64_t)(d.at + j) * p.H + head) * D / 2 + W * lane;
+#pragma unroll
+  for (int i = 0; i < W; ++i) to[i] = ca_pack<TYPE>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
 }
 
 // A cut unit's rows from its np pieces, by eight warps: warp w has the rows w, w +
@@ -570,12 +516,12 @@ __device__ __noinline__ void ca_merge_far(const Kv16AttnParams& p, const CaWork&
 // together.
 template <int TYPE, int D, int N, int K>
 __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk, const CaPart& d, const int* list, int np,
-                                      int w, int lane) {
+                                      int w, int lane, unsigned* beat) {
   constexpr int V = D / 32;
   const int G = (int)wk.by_g.d, rows = d.rows;
   for (int r0 = w; r0 < rows; r0 += 8 * N) {
     float acc[N][V], M[N], S[N];
-    bool far[N];  // some reference is kept as a score: what is summed here does not count
+    bool far[N];  // the row is done over
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       far[q] = false;
@@ -641,7 +587,7 @@ __device__ __noinline__ void ca_merge(const Kv16AttnParams& p, const CaWork& wk,
       uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
                                                  ((int64_t)(d.at + j) * p.H + d.kvh * G + R - j * G) * D + V * lane);
       if (far[q])
-        ca_merge_far<TYPE, D>(p, wk, list, np, r, to, lane);
+        ca_far_row<TYPE, D>(p, d, G, R, lane, beat);
       else if constexpr (V == 4)
         *reinterpret_cast<uint2*>(to) =
             make_uint2(ca_pack<TYPE>(acc[q][0] * inv, acc[q][1] * inv), ca_pack<TYPE>(acc[q][2] * inv, acc[q][3] * inv));
@@ -1200,7 +1146,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       const int gw = d.gw, gc = d.gc;
       const int rel = pos - (d.tile0 + d.lo) * kCaKeys;  // the row's position, from the part's first key on
       float m = -INFINITY, l = 0.0f;
-      float r = -INFINITY;  // the reference where it is kept as a score (m is -infinity then)
+      bool far = false;  // the row is to be done over
       for (int jt = 0; jt < nt; ++jt, ++sc) {
         const int i = two ? jt : 2 * jt + t, buf = (int)(sc & 1u);
         if (!ca_wait(&sh->s_full[t][buf], (sc >> 1) & 1u, p.err, &sh->beat)) {
@@ -1269,21 +1215,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             m4[(c + 2) & 3] = max3f(m4[(c + 2) & 3], __uint_as_float(sb[2 * c]), __uint_as_float(sb[2 * c + 1]));
           }
           const float raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx = raw * p.scale_log2;
-          if (__any_sync(0xffffffffu, r > -INFINITY || (fabsf(mx) >= kCaFar && raw > -INFINITY))) {
-            const CaRow w = ca_far_tile<TYPE, D>({m, r, l, true}, col, trow + ca_o_col(t), top, bottom, p.scale_log2, raise,
-                                                 jt > 0, &sh->pv_done[t][buf ^ 1], ((sc - 1) >> 1) & 1u, p.err, &sh->beat);
-            if (!w.ok) {
-              ok = false;
-              break;
-            }
-            m = w.m;
-            r = w.r;
-            l = w.l;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->p_full[t][buf]);
-            continue;
-          }
+          far = far || (fabsf(mx) >= kCaFar && fabsf(raw) < INFINITY);
           float cf = 1.0f;
           if (raise && mx > m) {
             cf = m == -INFINITY ? 0.0f : ex2(m - mx);
@@ -1327,6 +1259,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
       }
       // ---- the part's end
+      if (far) l = -1.0f;
       if (ok && nt > 0) ok = ca_wait(&sh->pv_done[t][(sc - 1) & 1u], ((sc - 1) >> 1) & 1u, p.err, &sh->beat);
       if (!ok) {
         if (have_q) ca_copy_wait();
@@ -1337,8 +1270,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       float a0 = 1.0f, a1 = 0.0f;  // factors of this slot's sums and of the other's
       if (!two) {
         if (t == 1) {  // hand over the reference and the sum through TMEM; the sums of values are there
-          const bool far = r > -INFINITY;
-          uint32_t st[8] = {__float_as_uint(far ? r : m), __float_as_uint(far ? -l : l), 0u, 0u, 0u, 0u, 0u, 0u};
+          uint32_t st[8] = {__float_as_uint(m), __float_as_uint(l), 0u, 0u, 0u, 0u, 0u, 0u};
           tmem_st_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_st();
           tc_fence_before();
@@ -1354,17 +1286,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           tmem_ld_32x32b_x8(trow + ca_s_col(1, 0), st);
           tmem_wait_ld(st);
           const float m1 = __uint_as_float(st[0]), l1 = __uint_as_float(st[1]);
-          if (n > 1 && (r > -INFINITY ? !(l1 == 0.0f) : l1 < 0.0f)) {
-            const bool far = r > -INFINITY;
-            const CaRef a = {far ? r : m, far ? -l : l}, b = {m1, l1};
-            CaRef top = b;
-            float2 f = make_float2(0.0f, 1.0f);
-            if (!(l == 0.0f)) f = ca_factors(a, b, p.scale_log2, &top);
-            a0 = f.x;
-            a1 = f.y;
-            l = l * a0 + fabsf(l1) * a1;
-            r = top.far() ? top.ref : -INFINITY;
-            m = top.far() ? -INFINITY : top.ref;
+          if (n > 1 && (l < 0.0f || l1 < 0.0f)) {
+            l = -1.0f;
           } else if (n > 1 && !(l1 == 0.0f)) {
             const float M = fmaxf(m, m1);
             a0 = l == 0.0f ? 0.0f : ex2(m - M);
@@ -1380,7 +1303,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const int64_t pi = slot * wk.rows_cap + ur;
         uint16_t* dst = static_cast<uint16_t*>(p.out) + ((int64_t)(d.at + j) * p.H + head) * D;
         float* part = wk.part_o + pi * D;
-        const bool st_ok = valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : in_bounds(p.err, d.at + j, p.T));
+        const bool st_ok =
+            valid && (cut ? in_bounds(p.err, ur, wk.rows_cap) : !(l < 0.0f) && in_bounds(p.err, d.at + j, p.T));
         const bool looked = two ? (gw > 0 && nt > 0) || gc < nt : gw > 0 || gc < n;
         const bool specials = looked && *(volatile const int*)&sh->specials[ds] > 0;
         const bool other = __any_sync(0xffffffffu, a1 != 0.0f);
@@ -1434,7 +1358,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             ca_store32(dst + c0 + 16, w + 8, wk.wide != 0);
           }
         }
-        if (cut && st_ok) wk.part_ml[pi] = r > -INFINITY ? make_float2(r, -l) : make_float2(m, l);
+        if (cut && st_ok) wk.part_ml[pi] = make_float2(m, l);
+        for (unsigned over = __ballot_sync(0xffffffffu, valid && !cut && l < 0.0f); over; over &= over - 1)
+          ca_far_row<TYPE, D>(p, d, G, __shfl_sync(0xffffffffu, R, __ffs(over) - 1), lane, &sh->beat);
       }
       if (to_hand) hand_q((seq + 1) % kCaDesc);
       if (!two) {  // slot 1's scores and sums may be written again
@@ -1490,9 +1416,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           // loads in flight along rows too, or along pieces: whichever takes fewer turns, each of them a load's latency (512
           // rows of 8 heads after 30000 tokens: 115 us; with 8 rows and 2 pieces a turn 121)
           if ((d.rows + 31) / 32 * ((np + 3) / 4) < (d.rows + 7) / 8 * ((np + 7) / 8))
-            ca_merge<TYPE, D, 4, 4>(p, wk, d, list, np, warp - 4, lane);
+            ca_merge<TYPE, D, 4, 4>(p, wk, d, list, np, warp - 4, lane, &sh->beat);
           else
-            ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane);
+            ca_merge<TYPE, D, 1, 8>(p, wk, d, list, np, warp - 4, lane, &sh->beat);
         }
       }
       __syncwarp();

@@ -98,3 +98,63 @@ def test_scores_that_leave_and_come_back(dtype, lens, counts):
         want, mag = ref.attention(c.q[at[b]:at[b + 1]], k, v, lens[b])
         bound = ref.attention_bound(want, mag, v, dtype) + factor * (mag + want.abs())
         assert ((out[at[b]:at[b + 1]].double() - want).abs() <= bound).all(), b
+
+
+@pytest.mark.parametrize("dtype,big", [(F16, 32752.0), (BF16, 1.9296875 * 2.0 ** 30)])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,counts", SHAPES)
+def test_beside_ordinary_rows(dtype, big, window, in_place, lens, counts):
+    """Every third row has scores of more than 2^24 powers of two, of one element; the others have zeros there, and get what
+    they get without them, to the bit. In place of the queries, with a window and a page that is none too."""
+    rng = np.random.default_rng(len(lens))
+    c = Case(4, dtype, 128, 8, 4, lens, counts, pad=1)
+    c.q[..., 0] = 0
+    far = torch.arange(c.T, device=dev()) % 3 == 1
+    for k, v in c.kv:
+        k[..., 0] = torch.from_numpy(44704.0 * 2.0 ** -rng.integers(0, 6, k.shape[:2]).astype(np.float64)).to(dev())
+    ordinary = c.q.clone()
+    ordinary[far] = 0
+    c.q[far] = 0
+    c.q[far, :, 0] = big
+    if lens[0] == 900:  # a page that is none reads as zeros
+        for x in c.kv[0]:
+            x[:, 128:192] = 0
+    for b in range(len(lens)):
+        c.put(b)
+    if lens[0] == 900:
+        c.table[0, 2] = -1
+    q = c.q
+    out = c.run(window=window, out=c.q.clone() if not in_place else None)
+    torch.cuda.synchronize()
+    status = sv.check_device_status()
+    assert status == (5 if lens[0] == 900 and not window else 0)
+    if in_place:
+        want, c.q = out, q.clone()
+        out = c.run(window=window, out=c.q)
+        torch.cuda.synchronize()
+        assert sv.check_device_status() == status
+        assert out is c.q and torch.equal(out[:sum(counts)], want[:sum(counts)])
+    c.q = q
+    c.check(out, window)
+    c.q = ordinary
+    assert torch.equal(c.run(window=window)[:sum(counts)][~far[:sum(counts)]], out[:sum(counts)][~far[:sum(counts)]])
+    sv.check_device_status()
+
+
+def test_values_that_are_not_finite():
+    """Rows that are done over see the values of their keys alone, guarded ones among them."""
+    for lens, counts in (([100], [150]), ([20000], [40])):
+        c = Case(5, F16, 128, 4, 1, lens, counts)
+        c.q.zero_()
+        c.q[..., 0] = 32752.0
+        k, v = c.kv[0]
+        k.zero_()
+        k[..., 0] = 44704.0
+        at = lens[0] + counts[0] // 2
+        v[0, at, 5], v[0, at + 1, 6], v[0, at + 2, 7] = torch.inf, -torch.inf, torch.nan
+        out = _run(c)
+        n = counts[0] // 2
+        assert out[:n].isfinite().all() and (out[n:, :, 5] == torch.inf).all()
+        assert (out[n + 1:, :, 6] == -torch.inf).all() and out[n + 2:, :, 7].isnan().all()
+        c.check(out)
