@@ -87,10 +87,18 @@ constexpr float kCaCut = 8.0f, kCaRowPiece = 0.056f, kCaLeast = 6.0f;
 
 // Many short units are not cut into runs but taken from a queue, whole ones, a request's longest first: where no unit has
 // more than kCaQueueTiles tiles and there are twice as many as CTAs, or four times the tiles and four times as many units.
-// Measured, cut / queue, us: 7 prompts of up to 3002 rows 94 / 81, 64 requests of up to 2000 tokens 60 / 53.5, 32 prompts of
-// up to 512 rows 122 / 114, 4 of 4000 rows 821 / 770, 49 requests with a window of 4096 421 / 406; fewer and longer units, 64
-// requests of up to 4000 tokens (3.4 units of 32 tiles a CTA): 101.5 / 104; 256 of up to 6000 (13.5 of 47): 300 / 301.
+// Measured, cut / queue, us (bf16, D 128, 64 heads over 8): 7 prompts of up to 3002 rows (16 heads of their own) 96 / 81, 64
+// requests of up to 2000 tokens, one row each, 63 / 59, 32 prompts of up to 512 rows 125 / 110, 4 of 4000 rows 832 / 771, 49
+// requests with a window of 4096 434 / 417; fewer and longer units, 64 requests of up to 4000 tokens (3.4 units of 32 tiles a
+// CTA): 100.6 / 100.5; 256 of up to 6000 (13.5 of 47): 477 / 465.
+// And where none is left to the end that is far longer than the others: with what its request's units are of a CTA's share
+// taken off, the request's longest weighs no more than kCaQueueLate of them on average. (The queue has the requests in their
+// order: behind the others it is what the call waits for.) 79 requests of 100 tokens and a last one of 1000 35 / 38, of 8000
+// 42 / 87 (first 41 / 66); 200 of 100 and a last one of 4000 76 / 95 (first 76 / 71); 100 of 500 and a last one of 2000 56 / 66
+// (first 57 / 55); 40 prompts of 100 rows and a last one of 2000 (16 heads of their own) 62 / 61 (first 62 / 51), of 3000 91 /
+// 73. Sorted by length, which was tried, the queue needs no such rule, but evenly spread batches took 5 percent longer.
 constexpr int kCaQueueTiles = 32;
+constexpr float kCaQueueLate = 2.6f;
 constexpr int kCaMany = 65535;  // units that are too many to be counted (more than any number of CTAs wants)
 
 // Weights are taken against a reference: the largest score of the first tile that
@@ -117,6 +125,7 @@ struct CaWork {
   int ctas, rows_cap;  // rows of a workspace slot
   int wide;            // out lies on 32 bytes
   uint64_t ctas_inv;   // floor(2^64 / ctas)
+  float tiles_inv;     // a CTA's share of the split's work, in tiles by their weight, for 1
   int* done;           // [ctas] tiles of the unit that this CTA's first cut is in, finished
   int* queue;          // units taken, CTAs finished
   float2* part_ml;     // [2 * ctas][rows_cap] (reference, sum), log2 domain; a sum below zero: the row is to be done over
@@ -655,7 +664,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   // Each thread sums a row of requests; the scratch lies where Q will
   struct Scratch {
     int64_t sums[kCaThreads / 32];
-    int units[kCaThreads / 32], longest[kCaThreads / 32];
+    int units[kCaThreads / 32], longest[kCaThreads / 32], late[kCaThreads / 32];
     int64_t at[2];  // the work before the requests that the run begins and ends in
     CaPlace place[2];
   };
@@ -663,19 +672,23 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const int per = (p.B + kCaThreads - 1) / kCaThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   int64_t mine = 0;
-  int units = 0, longest = 0;
+  int units = 0, longest = 0, late = 0;
   CaRequest r = {0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     r = ca_request(p, b, cta == 0);
     if (r.cnt > 0) {
       const CaLoad w = ca_load(p, wk, r);
-      mine += p.Hkv * w.before(w.units);
+      const int64_t n = p.Hkv * w.before(w.units);
+      mine += n;
       units = (int)min((int64_t)units + (int64_t)p.Hkv * w.units, (int64_t)kCaMany);
-      longest = max(longest, ca_tiles(p, wk, r, w.units - 1).nt);
+      const int nt = ca_tiles(p, wk, r, w.units - 1).nt;
+      longest = max(longest, nt);
+      late = max(late, w.weight * (nt + kCaOverhead / kCaKeys) - (int)((float)n * wk.tiles_inv));
     }
   }
   units = __reduce_add_sync(0xffffffffu, units);
   longest = __reduce_max_sync(0xffffffffu, longest);
+  late = __reduce_max_sync(0xffffffffu, late);
   int64_t upto = mine;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
@@ -686,6 +699,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   if (lane == 31) {
     scr->units[warp] = units;
     scr->longest[warp] = longest;
+    scr->late[warp] = late;
   }
   if (tid < 2) scr->place[tid] = CaPlace{p.B, 0, 0, 0, 0, 1, CaRequest{0, 0, 0}};
   __syncthreads();
@@ -697,9 +711,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     W += scr->sums[w];
     units += scr->units[w];
     longest = max(longest, scr->longest[w]);
+    late = max(late, scr->late[w]);
   }
-  const bool queue = units < kCaMany && ((units >= 2 * wk.ctas && longest <= kCaQueueTiles) ||
-                                         (units >= 4 * wk.ctas && longest <= 4 * kCaQueueTiles));
+  const bool queue = units < kCaMany &&
+                     ((units >= 2 * wk.ctas && longest <= kCaQueueTiles) ||
+                      (units >= 4 * wk.ctas && longest <= 4 * kCaQueueTiles)) &&
+                     (float)late * (float)units <= kCaQueueLate * (float)W * (wk.tiles_inv * (float)wk.ctas);
   // Fewer units than CTAs: each in a whole number of pieces, as many as pay, unless it is done sooner with a run for every
   // CTA, nearly all of which then merge.
   int C = wk.ctas;
@@ -1490,6 +1507,7 @@ cudaError_t launch_kv16_attention(const Kv16AttnParams& p, int type, int D, void
   wk.by_g = fast_div((uint32_t)(p.H / p.Hkv));
   wk.ctas = k.ctas;
   wk.ctas_inv = k.ctas > 1 ? ~uint64_t(0) / (uint64_t)k.ctas : ~uint64_t(0);
+  wk.tiles_inv = 1.0f / ((float)k.ctas * (float)(p.H / p.Hkv * kCaKeys));
   wk.rows_cap = k.rows_cap;
   wk.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -1,5 +1,5 @@
 """Batches of many short requests and a few long ones: right wherever the long ones
-stand, and no unit that outweighs a CTA's share of the work is left whole."""
+stand, and a unit far longer than the others is not left whole for the end."""
 import numpy as np
 import pytest
 import torch
@@ -31,8 +31,8 @@ def _pieces(c, **kw):
                                                    (100, 200, 16000, False), (1000, 100, 1000, True)])
 @pytest.mark.parametrize("at", ["first", "middle", "last"])
 def test_a_long_request_among_short_ones_is_cut(short, many, long, whole, at):
-    """In 16 CTAs' share of the work or more there is room for a long unit; in less it is cut. 8 units a request, 152 CTAs:
-    79 requests of 2 tiles are 4 units a CTA, some 26 tiles with their starts and ends, and 8000 tokens are 126."""
+    """One row and 8 heads of their own a request. A unit of 2 or 8 tiles weighs some 12 or 18 with its start and end, one of
+    126 tiles ten or seven times as much; with 251 there are too many tiles for any batch."""
     i = {"first": 0, "middle": many // 2, "last": many}[at]
     lens = [short] * many
     lens.insert(i, long)
@@ -49,7 +49,7 @@ def test_a_long_request_among_short_ones_is_cut(short, many, long, whole, at):
     ([30] * 383 + [700], [1] * 384), ([30] * 384 + [700], [1] * 385), ([30, 0] * 500 + [700], [1, 0] * 500 + [1]),
 ])
 def test_units_far_longer_than_the_others(dtype, D, H, Hkv, lens, counts):
-    """Taken first, where a thread has a request (up to 384 of them): every row once, the same bits whoever has it."""
+    """Whole or cut, wherever they stand: every row once, the same bits in every call."""
     c = Case(2, dtype, D, H, Hkv, lens, counts, pad=2)
     first = None
     for _ in range(4):
@@ -66,7 +66,7 @@ def test_units_far_longer_than_the_others(dtype, D, H, Hkv, lens, counts):
 def test_any_order_of_the_requests():
     """The same requests in other orders: their rows do not change where no unit is cut."""
     rng = np.random.default_rng(3)
-    lens = [int(x) for x in rng.integers(0, 300, 90)] + [1200, 1500]
+    lens = [int(x) for x in rng.integers(0, 300, 90)] + [900, 1000]
     c = Case(4, BF16, 128, 8, 8, lens, [1] * 92)
     out, cut = _pieces(c)
     assert not cut
