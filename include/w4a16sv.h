@@ -527,6 +527,7 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
  *              of no request are left as they were. out may be a dense q, and
  *              overlaps it in no other way
  *   window     0: none
+ *   scale      above 0, below 2^127
  *   workspace  kv16_attention_workspace_bytes() bytes (256-byte aligned), zero
  *              before its first use, and again after
  *              W4A16_ERR_DEVICE_TIMEOUT; every other call leaves the counters

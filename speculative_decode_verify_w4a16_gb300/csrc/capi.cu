@@ -558,6 +558,7 @@ w4a16_status kv16_append(const void* k_new, const void* v_new, int64_t k_stride,
   return launch_kv16_append(p, type, static_cast<cudaStream_t>(stream)) == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;  // (weights are powers of two of the scores times the scale times this)
 static bool kv16_attn_shape_ok(int T, int H, int Hkv) {
   return T >= 1 && H >= 1 && Hkv >= 1 && Hkv <= 65535 && H % Hkv == 0;
 }
@@ -578,7 +579,8 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
                             size_t workspace_bytes, void* stream) {
   if (!q || !k || !v || !block_table || !lens || !out) return W4A16_ERR_INVALID_ARG;
   if (!kv16_attn_shape_ok(T, H, Hkv) || !kv16_step_ok(row_start, T, B, Hkv, max_blocks, pages) || D < 1 || type < 0 ||
-      type > 1 || window < 0 || !rows_ok(q, q_stride, H, D) || !(scale > 0.0f) || !(scale < INFINITY))
+      type > 1 || window < 0 || !rows_ok(q, q_stride, H, D) || !(scale > 0.0f) ||
+      !(scale * kLog2e < INFINITY))
     return W4A16_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4))
@@ -605,7 +607,7 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
   p.max_blocks = max_blocks;
   p.pages = pages;
   p.window = window >= (int64_t)max_blocks * 64 ? 0 : window;  // (a window past every position is none)
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale * kLog2e;
   p.out = out;
   p.err = dev.err;
   return launch_kv16_attention(p, type, D, workspace, dev.num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess

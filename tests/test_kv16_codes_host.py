@@ -52,3 +52,10 @@ def test_append(L, kw, status):
     T, B, H, Hkv, D = (a[x] for x in ("T", "B", "H", "Hkv", "D"))
     assert L.kv16_append(P, P, Hkv * D, Hkv * D, P, H * D, P, a["rot"], 0, 1.0, P, P, P, T, B, H, Hkv, D, a["max_blocks"],
                          a["pages"], 0, P, P, OTHER, H * D, None) == status
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, BAD), (2.4e38, BAD), (1e38, UNSUPPORTED), (1e-30, UNSUPPORTED), (0.0, BAD),
+                                          (-1.0, BAD), (float("inf"), BAD), (float("nan"), BAD)])
+def test_scales(L, scale, status):
+    """Scales whose product with log2(e) fp32 does not hold would give NaN (4097 requests, so that no good call launches)."""
+    assert L.kv16_attention(P, 1024, P, P, P, P, P, 8, 4097, 8, 2, 128, 4, 9, 0, scale, 0, P, None, 0, None) == status
