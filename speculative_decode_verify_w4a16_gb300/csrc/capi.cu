@@ -582,6 +582,7 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
       type > 1 || window < 0 || !rows_ok(q, q_stride, H, D) || !(scale > 0.0f) ||
       !(scale * kLog2e < INFINITY))
     return W4A16_ERR_INVALID_ARG;
+  if (q == out && q_stride != (int64_t)H * D && T > 1) return W4A16_ERR_INVALID_ARG;  // (rows would lie over later ones)
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4))
     return W4A16_ERR_INVALID_ARG;
