@@ -426,6 +426,8 @@ def _is(t: torch.Tensor, dtype: torch.dtype, dev: int, shape) -> bool:
 def _need_ws(ws: torch.Tensor, dev: int):
     if ws.get_device() != dev:
         raise ValueError(f"ws is on {ws.device}, the current device is cuda:{dev}")
+    if not ws.is_contiguous():  # (an expanded one has fewer bytes than elements)
+        raise ValueError("ws must be contiguous")
 
 
 def _need_cache(c: KV8Cache, dev: int):
