@@ -582,12 +582,12 @@ w4a16_status kv16_attention(const void* q, int64_t q_stride, const void* k, cons
       type > 1 || window < 0 || !rows_ok(q, q_stride, H, D) || !(scale > 0.0f) ||
       !(scale * kLog2e < INFINITY))
     return W4A16_ERR_INVALID_ARG;
-  if (q == out && q_stride != (int64_t)H * D && T > 1) return W4A16_ERR_INVALID_ARG;  // (rows would lie over later ones)
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(lens, 4) ||
       !aligned(row_start, 4))
     return W4A16_ERR_INVALID_ARG;
   if (!kv16_attn_size_ok(T, H, D) || B > kPlanMaxB || !kv16_attention_fits(T, B, H, Hkv, max_blocks))
     return W4A16_ERR_UNSUPPORTED;
+  if (q == out && q_stride != (int64_t)H * D && T > 1) return W4A16_ERR_INVALID_ARG;  // (rows would lie over later ones)
   DeviceInfo dev;
   if (device_info(&dev) != cudaSuccess) return W4A16_ERR_CUDA;
   const size_t need = kv16_attention_ws(T, H, Hkv, D, dev.num_sms);

@@ -62,9 +62,10 @@ def test_scales(L, scale, status):
 
 
 def test_out_in_place_of_queries_that_are_not_dense(L):
-    """The output is dense: over a slice of a fused projection its rows would lie on queries that are still to be read."""
-    def attn(q, stride, out, T=6, B=4097):
-        return L.kv16_attention(q, stride, P, P, P, P, P, T, B, 8, 2, 128, 4, 9, 0, 0.1, 0, out, None, 0, None)
+    """The output is dense: over a slice of a fused projection its rows would lie on queries that are still to be read.
+    (Nothing launches: the calls that are not refused for that have no workspace, where there is a GPU, or no device.)"""
+    def attn(q, stride, out, T=6):
+        return L.kv16_attention(q, stride, P, P, P, P, P, T, 2, 8, 2, 128, 4, 9, 0, 0.1, 0, out, None, 0, None)
     assert attn(P, 1536, P) == BAD
     for q, stride, out, T in ((P, 1024, P, 6), (P, 1536, OTHER, 6), (P, 1536, P, 1)):
-        assert attn(q, stride, out, T) == UNSUPPORTED  # (4097 requests: no good call launches)
+        assert attn(q, stride, out, T) in (_lib.ERR_WORKSPACE, _lib.ERR_CUDA)
