@@ -703,7 +703,12 @@ def rope_angles(rot: int, base: float = 10000.0, scaling: Optional[dict] = None)
     if kind == "ntk":
         if rot < 4:
             raise ValueError("scaling ntk: rot must be 4 or more")
-        base *= factor ** (rot / (rot - 2))
+        try:
+            base *= factor ** (rot / (rot - 2))
+        except OverflowError:
+            base = math.inf
+        if not math.isfinite(base):
+            raise ValueError(f"scaling ntk: factor {factor} takes the base past every number")
     f = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
     attention = 1.0
     if kind == "linear":
@@ -725,6 +730,8 @@ def rope_angles(rot: int, base: float = 10000.0, scaling: Optional[dict] = None)
             ramp = min(max((i - first) / max(last - first, 1e-3), 0.0), 1.0)
             f[i] = x / factor * ramp + x * (1 - ramp)
         attention = v.get("attention", 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0)
+    if not all(map(math.isfinite, f)):
+        raise ValueError("a frequency is past every number: base or factor too small")
     return f, attention
 
 

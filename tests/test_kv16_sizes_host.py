@@ -63,3 +63,18 @@ def test_windows(monkeypatch, window, passed):
     api.kv16_attention(tensors["q"], c, 0, tensors["table"], tensors["lens"], window=window, out=tensors["q"],
                        ws=tensors["ws"], stream=types.SimpleNamespace(cuda_stream=0))
     assert got == [passed]
+
+
+@pytest.mark.parametrize("scaling", [{"kind": "ntk", "factor": 1e305}, {"kind": "ntk", "factor": 1e306},
+                                     {"kind": "linear", "factor": 1e-320},
+                                     {"kind": "bands", "factor": 1e-320, "low": 1, "high": 4, "trained": 10},
+                                     {"kind": "yarn", "factor": 1e-320, "trained": 4096}])
+def test_frequencies_that_no_number_holds(scaling):
+    for f in (api.rope_angles, lambda *a, **k: api.rope_frequencies(*a, device="cpu", **k)):
+        with pytest.raises(ValueError):
+            f(64, 10000.0, scaling=scaling)
+
+
+@pytest.mark.parametrize("scaling", [{"kind": "ntk", "factor": 1e200}, {"kind": "linear", "factor": 1e-200}])
+def test_frequencies_of_any_size(scaling):
+    assert api.rope_frequencies(64, 10000.0, scaling=scaling, device="cpu").rot == 64
