@@ -484,7 +484,7 @@ w4a16_status rope_rotate(const void* x, int64_t x_stride, const int32_t* positio
  *   block_table  device int32 [B][max_blocks]: the pages of the blocks
  *                0 .. (lens[b] + rows - 1) / 64 (other entries unread). Requests
  *                may share pages that no row of the step goes to; of two rows
- *                for one place either may be kept
+ *                for one place any parts of either may be kept
  *   lens         device int32 [B]: tokens of request b before the step
  *   row_start    device int32 [B + 1], not falling, row_start[B] <= T; NULL:
  *                T / B rows each. Rows of no request are neither read nor written

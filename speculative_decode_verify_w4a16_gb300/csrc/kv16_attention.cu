@@ -31,26 +31,32 @@
 //                 at the end
 //   warps 4 - 11  the softmax of slot 0 and 1, one row a thread: scores from TMEM,
 //                 weights and their sum in fp32, the weights rounded to the
-//                 cache's type back into TMEM over the scores
+//                 cache's type back into TMEM over the scores: the product takes
+//                 both operands in one type. Each is off by half a step at most,
+//                 and a row by that of its weighted magnitudes (the sum is that of
+//                 the unrounded ones: it adds nothing)
 // With more than 128 rows the two slots are two row tiles, which share every
 // key tile; with fewer they take the key tiles in turn and are merged at the
 // part's end. While one slot's softmax runs, the tensor pipe works for the other.
 //
 // Bound and measured (bf16, D 128, 64 heads over 8, unless said; times by events):
-//   long contexts, 4 requests of 120 to 131 K, one row each: HBM, 297 us for 2.04 GB
-//     (1.01 of a plain copy's rate)
-//   16 requests of 4 to 8 K, 5 rows each: 79 us for 392 MB (0.73); a run is some 79
+//   long contexts, 4 requests of 120 to 131 K, one row each: HBM, 302 us for 2.04 GB
+//     (0.99 of a plain copy's rate)
+//   64 and 256 requests of 1 to 8 K, one row each: 192 us for 1.18 GB (0.91), 678 for
+//     4.72 (1.02); at fp16, D 64 117 and 427 (0.74, 0.81): half the bytes a tile, the
+//     same hand-offs
+//   16 requests of 4 to 8 K, 5 rows each: 80 us for 392 MB (0.72); a run is some 79
 //     tiles, its start, end and merge a third of it
 //   a chunk of 2048 rows after 30720: the tensor pipe and the softmax, 1.42 ms cold to
-//     1.57 ms in a row (the clock falls): 1.5 to 1.36 PFLOP/s, 0.79 to 0.71 of the bf16
-//     peak. Of some 1640 cycles a tile the MMAs of both slots take 1250 (626 each, 392
+//     1.6 ms in a row (the clock falls): 1.5 to 1.33 PFLOP/s, 0.79 to 0.70 of the bf16
+//     peak (fp16 1.46 ms; D 64, half the work, 1.11). Of some 1640 cycles a tile the MMAs of both slots take 1250 (626 each, 392
 //     of it S: with N = 64 a k-step takes 49 cycles for 32 of arithmetic, as shared
 //     memory gives 128 bytes a cycle), a slot's softmax 1000 and its hand-offs 400; with
 //     one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
 //     arithmetic no less than with it
 //   7 prompts of up to 3002 rows, 16 heads of their own: 81 us, 0.45 of the peak;
 //     parts of 4 to 47 tiles start and end in 7000 cycles, and masked tiles take more
-//   49 requests, one in 8 a prompt, fp16, D 64, window 4096: 406 us, 0.36 of the
+//   49 requests, one in 8 a prompt, fp16, D 64, window 4096: 410 us, 0.36 of the
 //     peak; softmax and hand-offs, some 1250 cycles a tile (the MMAs 700, the
 //     exponentials 512)
 // Tried and slower, or no better: 128-key tiles with one score buffer (chunk 1586 us
@@ -80,9 +86,9 @@ constexpr int kCaOverhead = 256;  // keys that a unit's start and end are worth
 constexpr int kCaSnap = 16;       // tiles that a cut may move to the unit's begin or end,
 constexpr int kCaSnapFew = 4;     // and where there are fewer units than CTAs
 // What a cut is worth, in tiles of one row tile: by itself, and for each row of each piece (stored, fetched and added); and
-// the tiles that a piece has at least. Measured: one row after 1003 tokens, units in 2 pieces 14.3 us, in 3 13.6, in 19
-// 15.9; 300 rows of 32 heads over 8 after 1000, whole 27.6 us, in 3 pieces 64; the same after 8000 in 3 pieces 75 us, and 82
-// where cuts lay a tile or two beside the units' ends.
+// the tiles that a piece has at least. Measured: one row of 64 heads over 8 after 1003 tokens, units in 2 pieces 14.3 us, in
+// 3 13.6, in 19 15.9; 300 rows of 32 heads over 8 after 1000, whole 27.6 us, in 3 pieces 64; the same after 8000 in 3 pieces
+// 75 us, and 82 where cuts lay a tile or two beside the units' ends.
 constexpr float kCaCut = 8.0f, kCaRowPiece = 0.056f, kCaLeast = 6.0f;
 
 // Many short units are not cut into runs but taken from a queue, whole ones, a request's longest first: where no unit has
@@ -114,7 +120,8 @@ constexpr float kCaUp = TYPE == 0 ? 0.0f : 8.0f;
 // A weight is 2^(s c - m), c the scale and m the reference times c, rounded, in one multiplication and addition: off by
 // the rounding of m, 2^-24 |m| powers of two at most, by the same for all of a row's keys, so that it cancels. From 2^28 on in
 // fp16, 2^32 in bf16, it passes what a weight holds. Rows that had a reference of this size are done over, key by key
-// (ca_far_row): scores like that need not be fast, and the code for them in the tiles' loop cost the others 2 percent.
+// (ca_far_row): scores like that need not be fast (one row of 64 heads after 8000 tokens 1.25 ms), and the code for them in
+// the tiles' loop cost the others 2 percent.
 constexpr float kCaFar = 16777216.0f;
 
 struct CaMaps {

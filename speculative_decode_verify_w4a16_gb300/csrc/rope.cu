@@ -14,10 +14,13 @@
 // latency for the rows of a step. A CTA takes a row: its loads go out first, the
 // row's sines and cosines (one pair a thread, for all heads) are computed
 // meanwhile and handed over through shared memory.
-// Measured: 16381 rows of 72 heads 92 us (604 MB: 0.97 of the HBM copy rate),
-// 4093 rows of 40 heads, half of each turned in pairs, 10.4 us (84 MB, in part in
-// the L2), 12.0 K rows of 64 + 16 heads into pages 104 us (655 MB, 0.93); 80 rows
-// 3.1 us, 64 rows into pages 5.1. What keeps the memory busy is bytes in flight and
+// Measured: 16381 rows of 72 heads 92.8 us (604 MB: 0.96 of the HBM copy rate), fp32
+// 179 (1.21 GB, 0.99), 4093 rows of 40 heads, half of each turned in pairs, 10.4 us (84
+// MB, in part in the L2), 12.0 K rows of 64 + 16 heads into pages 105 us (655 MB,
+// 0.92); 80 rows 3.1 us, 64 rows into pages 5.1. Rows of few heads leave most of a
+// CTA's threads without an item: 32768 rows of one head of 64 take 34.5 us (8.5 MB:
+// 0.04), of 8 heads of 128 40 (134 MB, 0.49), 12 K rows of 8 + 8 heads into pages
+// without queries 26 (98 MB, 0.56), of 1 + 1 18 (0.10). What keeps the memory busy is bytes in flight and
 // CTAs at once: 128 threads, five items each, eight CTAs an SM; against 92, 104 us
 // there were 96, 110 with 192 threads (5 CTAs), 105, 110 with 256 and three items
 // (5), 95, 101 with 256 and one (8), 130, 142 with ten CTAs (registers spilled), and

@@ -158,3 +158,23 @@ def test_values_that_are_not_finite():
         assert out[:n].isfinite().all() and (out[n:, :, 5] == torch.inf).all()
         assert (out[n + 1:, :, 6] == -torch.inf).all() and out[n + 2:, :, 7].isnan().all()
         c.check(out)
+
+
+@pytest.mark.parametrize("lens,counts", SHAPES + [([100] * 79 + [8000], [1] * 80)])
+def test_in_the_bounds_checked_build(lens, counts):
+    """Rows that are done over, in whole units, pieces and from the queue: nothing out of bounds, and the same bits."""
+    from speculative_decode_verify_w4a16_gb300 import _lib, build
+
+    c = Case(6, F16, 64, 8, 4, lens, counts, pad=1)
+    c.q.zero_()
+    c.q[::2, :, 0] = 32752.0
+    for k, _ in c.kv:
+        k[..., 0] = (k[..., 0].abs() * 2.0 ** 13).to(F16)
+    want = _run(c, window=150)
+    with _lib.use_library(build.build_bounds()):
+        got = c.run(window=150)
+        torch.cuda.synchronize()
+        assert sv.check_device_status() == 0  # W4A16_ERR_BOUNDS would be 7
+    n = sum(counts)  # (some keys are infinite: NaN to the rows that see them)
+    torch.testing.assert_close(got[:n], want[:n], rtol=0, atol=0, equal_nan=True)
+    c.check(want, 150)
