@@ -49,10 +49,10 @@
 //     tiles, its start, end and merge a third of it
 //   a chunk of 2048 rows after 30720: the tensor pipe and the softmax, 1.42 ms cold to
 //     1.6 ms in a row (the clock falls): 1.5 to 1.33 PFLOP/s, 0.79 to 0.70 of the bf16
-//     peak (fp16 1.46 ms; D 64, half the work, 1.11). Of some 1640 cycles a tile the MMAs of both slots take 1250 (626 each, 392
-//     of it S: with N = 64 a k-step takes 49 cycles for 32 of arithmetic, as shared
-//     memory gives 128 bytes a cycle), a slot's softmax 1000 and its hand-offs 400; with
-//     one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
+//     peak (fp16 1.46 ms; D 64, half the work, 1.11). Of some 1640 cycles a tile the
+//     MMAs of both slots take 1250 (626 each, 392 of it S: with N = 64 a k-step takes 49
+//     cycles for 32 of arithmetic, as shared memory gives 128 bytes a cycle), a slot's
+//     softmax 1000 and its hand-offs 400; with one k-step of S in place of eight the chunk took 1.11 ms, without the softmax's
 //     arithmetic no less than with it
 //   7 prompts of up to 3002 rows, 16 heads of their own: 81 us, 0.45 of the peak;
 //     parts of 4 to 47 tiles start and end in 7000 cycles, and masked tiles take more
@@ -165,7 +165,7 @@ struct CaShared {
   CaSpecial special[kCaDesc][kCaSpecial];
   uint32_t tmem;
   int last;
-  unsigned beat;  // counts on as the producer does
+  unsigned beat;  // counts on as the producer, or a row that is done over, does
 };
 
 template <int D>
@@ -454,14 +454,15 @@ __device__ __noinline__ void ca_add_special(const Kv16AttnParams& p, const CaSha
   }
 }
 
-// Row R of part d's request and head from the definition, by a warp, D / 32 columns a lane: differences of scores are taken
-// before the scale, against the largest so far.
+// the first or second value of a pair
 template <int TYPE>
 __device__ __forceinline__ float ca_value(uint32_t w, int half) {
   if constexpr (TYPE == 0) return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
   const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
   return half ? v.y : v.x;
 }
+// Row R of part d's request and head from the definition, by a warp, D / 32 columns a lane: differences of scores are taken
+// before the scale, against the largest so far.
 template <int TYPE, int D>
 __device__ __noinline__ void ca_far_row(const Kv16AttnParams& p, const CaPart& d, int G, int R, int lane, unsigned* beat) {
   constexpr int W = D / 64;  // words a lane
@@ -1239,9 +1240,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             m4[(c + 2) & 3] = max3f(m4[(c + 2) & 3], __uint_as_float(sb[2 * c]), __uint_as_float(sb[2 * c + 1]));
           }
           const float raw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mx = raw * p.scale_log2;
-          far = far || (fabsf(mx) >= kCaFar && fabsf(raw) < INFINITY);
           float cf = 1.0f;
           if (raise && mx > m) {
+            far = far || (fabsf(mx) >= kCaFar && fabsf(raw) < INFINITY);
             cf = m == -INFINITY ? 0.0f : ex2(m - mx);
             m = mx;
             l *= cf;

@@ -20,9 +20,9 @@
 // 0.92); 80 rows 3.1 us, 64 rows into pages 5.1. Rows of few heads leave most of a
 // CTA's threads without an item: 32768 rows of one head of 64 take 34.5 us (8.5 MB:
 // 0.04), of 8 heads of 128 40 (134 MB, 0.49), 12 K rows of 8 + 8 heads into pages
-// without queries 26 (98 MB, 0.56), of 1 + 1 18 (0.10). What keeps the memory busy is bytes in flight and
-// CTAs at once: 128 threads, five items each, eight CTAs an SM; against 92, 104 us
-// there were 96, 110 with 192 threads (5 CTAs), 105, 110 with 256 and three items
+// without queries 26 (98 MB, 0.56), of 1 + 1 18 (0.10). What keeps the memory busy is
+// bytes in flight and CTAs at once: 128 threads, five items each, eight CTAs an SM;
+// against 92, 104 us there were 96, 110 with 192 threads (5 CTAs), 105, 110 with 256 and three items
 // (5), 95, 101 with 256 and one (8), 130, 142 with ten CTAs (registers spilled), and
 // 104, 123 with the loads behind the sines.
 #include <cuda_fp16.h>

@@ -178,3 +178,25 @@ def test_in_the_bounds_checked_build(lens, counts):
     n = sum(counts)  # (some keys are infinite: NaN to the rows that see them)
     torch.testing.assert_close(got[:n], want[:n], rtol=0, atol=0, equal_nan=True)
     c.check(want, 150)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lens,counts", [([400], [40]), ([0], [300]), ([9000], [200])])
+def test_scores_far_below_the_others(dtype, lens, counts):
+    """Even rows see most keys 2^26 powers of two and more below the first ones: no weight, and nothing to be done over,
+    whether the other rows' references rise with those keys or not."""
+    c = Case(7, dtype, 128, 8, 4, lens, counts)
+    even = torch.arange(c.T, device=dev()) % 2 == 0
+    c.q[..., 0] = 0
+    c.q[even, :, 0] = 32752.0 if dtype is F16 else 32768.0
+    for k, _ in c.kv:
+        k[..., 0] = 0
+        k[:, 64:, 0] = -44704.0
+    low = _run(c)
+    c.check(low)
+    c.q[~even, :, 0] = -2.0 ** -8
+    raised = c.run()
+    torch.cuda.synchronize()
+    assert sv.check_device_status() == 0
+    c.check(raised)
+    assert torch.equal(raised[even], low[even])
